@@ -22,6 +22,9 @@ MK_ERR_UNSUPPORTED = -4
 MK_ERR_TIMEOUT = -5
 MK_ERR_NOMEM = -6
 MK_INSTR_WORDS = 16
+MK_F32, MK_BF16 = 0, 1
+MK_MAX_TREE = 64
+ROPE_KINDS = {"none": 0, "linear": 1, "base": 2, "wavelength": 3, "yarn": 4}
 
 
 class MKError(RuntimeError):
@@ -51,6 +54,25 @@ class mk_weights(ctypes.Structure):
 
 class mk_kv_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class mk_rope_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n", "n_heads", "n_kv_heads", "head_dim", "rot", "interleaved", "dtype",
+                                               "slots", "max_seq")]
+                + [("eps", ctypes.c_float), ("mscale", ctypes.c_float), ("qkv_stride", ctypes.c_int64),
+                   ("q_stride", ctypes.c_int64)]
+                + [(n, ctypes.c_void_p) for n in ("qkv", "q_out", "k_cache", "v_cache", "positions", "rows", "slot_of",
+                                                  "inv_freq", "q_norm", "k_norm")])
+
+
+class mk_tree_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "nodes", "n_heads", "n_kv_heads", "head_dim", "dtype", "slots",
+                                               "max_seq", "max_len")]
+                + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_int64) for n in ("q_batch_stride", "q_token_stride", "out_batch_stride",
+                                                 "out_token_stride")]
+                + [(n, ctypes.c_void_p) for n in ("q", "out", "k_cache", "v_cache", "lengths", "counts", "slot_of",
+                                                  "masks")])
 
 
 _lib = None
@@ -100,6 +122,13 @@ def load(path: str | None = None):
     L.mk_twell_ffn.argtypes = [_VP, _VP, _VP, _I32, _I32, _VP, _VP, _VP, _VP]
     L.mk_prefill.argtypes = [_VP, _VP, _I32, _I32, _VP, _VP, _VP]
     L.mk_tc_gemm.argtypes = [_VP, _I32, _I32, _VP, _VP, _I32, _VP, _VP, _VP, _VP]
+    L.mk_rope_append.argtypes = [ctypes.POINTER(mk_rope_args), _VP]
+    L.mk_rope_frequencies.argtypes = [_I32, _I32] + [ctypes.c_double] * 5 + [_VP, ctypes.POINTER(ctypes.c_float)]
+    L.mk_tree_attention.argtypes = [ctypes.POINTER(mk_tree_args), _VP]
+    L.mk_tree_masks.argtypes = [_VP, _VP, _I32, _I32, _VP, _VP, _VP]
+    L.mk_tree_accept.argtypes = [_VP, _VP, _VP, _I32, _VP]
+    L.mk_kv_compact.argtypes = [_VP, _VP] + [_I32] * 6 + [_VP] * 4
+    L.mk_kv_reorder.argtypes = [_VP, _VP] + [_I32] * 5 + [_VP] * 3
     L.mk_destroy.argtypes = [_VP]
     L.mk_destroy.restype = None
     _lib = L
@@ -253,6 +282,181 @@ def tc_gemm(w, bhi, blo, y, r=None, status=None, stream=None) -> None:
         raise MKError(rc, f"mk_tc_gemm returned {rc}")
     if status is None and int(st.item()) != 0:
         raise MKError(MK_ERR_TIMEOUT, "a bounded wait of the tensor-core contraction expired")
+
+
+def _bad(msg: str):
+    raise MKError(MK_ERR_INVALID_ARG, msg)
+
+
+def _need(t, what: str, dtype, shape, dev, dense: bool = True):
+    """Device pointer of tensor t after its type, shape (None: any extent), device and layout are checked."""
+    if t.dtype != dtype:
+        _bad(f"{what} must be {dtype}, not {t.dtype}")
+    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        _bad(f"{what} has shape {tuple(t.shape)}, not {shape}")
+    if t.device != dev:
+        _bad(f"{what} is on {t.device}, not {dev}")
+    if dense and not t.is_contiguous():
+        _bad(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _run_on(dev, stream, call) -> None:
+    """call(stream pointer) with `dev` current; without a stream, on dev's current one."""
+    import torch
+    if dev.type != "cuda":
+        _bad(f"tensors must be on a CUDA device, not {dev}")
+    if torch.cuda.current_device() == dev.index:
+        check(call((stream or torch.cuda.current_stream()).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            check(call((stream or torch.cuda.current_stream()).cuda_stream))
+
+
+def _io_dtype(t, what: str) -> int:
+    import torch
+    if t.dtype == torch.float32:
+        return MK_F32
+    if t.dtype == torch.bfloat16:
+        return MK_BF16
+    _bad(f"{what} must be float32 or bfloat16, not {t.dtype}")
+
+
+def rope_frequencies(rot: int, theta: float, kind: str = "none", factor: float = 1.0, original_len: float = 8192.0,
+                     low: float = 1.0, high: float | None = None):
+    """mk_rope_frequencies: (float64 CPU tensor [rot / 2] of radians per position, factor on the rotated
+    values). kind: "none", "linear", "base", "wavelength" (high defaults to 4) or "yarn" (32)."""
+    import torch
+    if kind not in ROPE_KINDS:
+        _bad(f"kind must be one of {sorted(ROPE_KINDS)}, not {kind!r}")
+    if high is None:
+        high = 32.0 if kind == "yarn" else 4.0
+    out = torch.empty(max(1, int(rot) // 2), dtype=torch.float64)
+    m = ctypes.c_float()
+    check(load().mk_rope_frequencies(ROPE_KINDS[kind], int(rot), float(theta), float(factor), float(original_len),
+                                     float(low), float(high), out.data_ptr(), ctypes.byref(m)))
+    return out, m.value
+
+
+def rope_append(qkv, q_out, k_cache, v_cache, positions, rows, inv_freq, slots=None, q_norm=None, k_norm=None,
+                eps: float = 1e-5, mscale: float = 1.0, interleaved: bool = False, stream=None) -> None:
+    """mk_rope_append on CUDA tensors: qkv [n][(Hq + 2 Hkv) hd] float32 or bfloat16 (rows may be strided),
+    q_out [n][Hq][hd] of the same type (token stride free), k_cache / v_cache bfloat16 [B][Hkv][max_seq][hd]
+    (one layer), positions / rows / slots int32 [n], inv_freq float64 [rot / 2], q_norm / k_norm bfloat16 [hd]."""
+    import torch
+    dev, dt = qkv.device, _io_dtype(qkv, "qkv")
+    if k_cache.dim() != 4 or q_out.dim() != 3 or qkv.dim() != 2 or inv_freq.dim() != 1:
+        _bad("qkv, q_out, k_cache, inv_freq must have 2, 3, 4, 1 dimensions")
+    B, Hkv, S, hd = k_cache.shape
+    n, Hq, _ = q_out.shape
+    half = inv_freq.shape[0]
+    bf, i32 = torch.bfloat16, torch.int32
+    a = mk_rope_args(n, Hq, Hkv, hd, 2 * half, 1 if interleaved else 0, dt, B, S, eps, mscale, qkv.stride(0),
+                     q_out.stride(0), _need(qkv, "qkv", qkv.dtype, (n, (Hq + 2 * Hkv) * hd), dev, False),
+                     _need(q_out, "q_out", qkv.dtype, (n, Hq, hd), dev, False),
+                     _need(k_cache, "k_cache", bf, (B, Hkv, S, hd), dev),
+                     _need(v_cache, "v_cache", bf, (B, Hkv, S, hd), dev),
+                     _need(positions, "positions", i32, (n,), dev), _need(rows, "rows", i32, (n,), dev),
+                     None if slots is None else _need(slots, "slots", i32, (n,), dev),
+                     _need(inv_freq, "inv_freq", torch.float64, (half,), dev),
+                     None if q_norm is None else _need(q_norm, "q_norm", bf, (hd,), dev),
+                     None if k_norm is None else _need(k_norm, "k_norm", bf, (hd,), dev))
+    if n == 0:
+        return
+    if qkv.stride(1) != 1 or q_out.stride(2) != 1 or q_out.stride(1) != hd:
+        _bad("the heads of a token must be contiguous in qkv and q_out")
+    L = load()
+    _run_on(dev, stream, lambda s: L.mk_rope_append(ctypes.byref(a), s))
+
+
+def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None = None, counts=None, slots=None,
+                   max_len: int = 0, stream=None) -> None:
+    """mk_tree_attention on CUDA tensors: q and out [B][T][Hq][hd] float32 or bfloat16 (batch and node strides
+    free), k_cache / v_cache bfloat16 [slots][Hkv][max_seq][hd] (one layer), lengths / counts / slots int32 [B],
+    masks int64 [B][T] (the 64 bits of the ancestor mask). scale defaults to 1 / sqrt(hd)."""
+    import torch
+    dev, dt = q.device, _io_dtype(q, "q")
+    if q.dim() != 4 or k_cache.dim() != 4:
+        _bad("q and k_cache must have 4 dimensions")
+    B, T, Hq, hd = q.shape
+    n_slots, Hkv, S, _ = k_cache.shape
+    bf, i32 = torch.bfloat16, torch.int32
+    qs, os = q.stride(), out.stride()
+    a = mk_tree_args(B, T, Hq, Hkv, hd, dt, n_slots, S, int(max_len), hd ** -0.5 if scale is None else scale,
+                     qs[0] if B > 1 else 0, qs[1] if T > 1 else Hq * hd, os[0] if B > 1 else 0,
+                     os[1] if T > 1 else Hq * hd, _need(q, "q", q.dtype, (B, T, Hq, hd), dev, False),
+                     _need(out, "out", q.dtype, (B, T, Hq, hd), dev, False),
+                     _need(k_cache, "k_cache", bf, (n_slots, Hkv, S, hd), dev),
+                     _need(v_cache, "v_cache", bf, (n_slots, Hkv, S, hd), dev),
+                     _need(lengths, "lengths", i32, (B,), dev),
+                     None if counts is None else _need(counts, "counts", i32, (B,), dev),
+                     None if slots is None else _need(slots, "slots", i32, (B,), dev),
+                     _need(masks, "masks", torch.int64, (B, T), dev))
+    if slots is None and B > n_slots:
+        _bad(f"{B} sequences for {n_slots} cache slots")
+    if B == 0:
+        return
+    if qs[3] != 1 or os[3] != 1 or (Hq > 1 and (qs[2] != hd or os[2] != hd)):
+        _bad("the heads of a node must be contiguous in q and out")
+    L = load()
+    _run_on(dev, stream, lambda s: L.mk_tree_attention(ctypes.byref(a), s))
+
+
+def tree_masks(parents, masks, depths=None, counts=None, stream=None) -> None:
+    """mk_tree_masks on CUDA tensors: parents int32 [B][T] -> masks int64 [B][T], depths int32 [B][T] or None."""
+    import torch
+    dev, i32 = parents.device, torch.int32
+    if parents.dim() != 2:
+        _bad("parents must have 2 dimensions")
+    B, T = parents.shape
+    p = (_need(parents, "parents", i32, (B, T), dev),
+         None if counts is None else _need(counts, "counts", i32, (B,), dev), B, T,
+         _need(masks, "masks", torch.int64, (B, T), dev),
+         None if depths is None else _need(depths, "depths", i32, (B, T), dev))
+    L = load()
+    _run_on(dev, stream, lambda s: L.mk_tree_masks(*p, s))
+
+
+def tree_accept(tokens, parents, draws):
+    """mk_tree_accept: the accepted nodes (list, node 0 first) of a verified tree; the three are host sequences of
+    n whole numbers. The next token is draws[path[-1]]."""
+    n = len(tokens)
+    if len(parents) != n or len(draws) != n:
+        _bad("tokens, parents and draws must have the same length")
+    arr = ctypes.c_int32 * max(1, n)
+    path = arr()
+    c = check(load().mk_tree_accept(arr(*map(int, tokens)), arr(*map(int, parents)), arr(*map(int, draws)), n, path))
+    return list(path[:c])
+
+
+def _caches(k, v):
+    import torch
+    if k.dim() != 5:
+        _bad("the caches must have 5 dimensions")
+    shape = tuple(k.shape)
+    return (_need(k, "k", torch.bfloat16, shape, k.device), _need(v, "v", torch.bfloat16, shape, k.device), *shape)
+
+
+def kv_compact(k, v, starts, nodes, counts, stream=None) -> None:
+    """mk_kv_compact on CUDA tensors: k / v bfloat16 [L][B][Hkv][max_seq][hd], starts / counts int32 [B], nodes
+    int32 [B][n]: rows starts[b] + nodes[b][i] move to starts[b] + i."""
+    import torch
+    c, dev, i32 = _caches(k, v), k.device, torch.int32
+    B, n = k.shape[1], nodes.shape[-1]
+    p = (_need(starts, "starts", i32, (B,), dev), _need(nodes, "nodes", i32, (B, n), dev),
+         _need(counts, "counts", i32, (B,), dev))
+    L = load()
+    _run_on(dev, stream, lambda s: L.mk_kv_compact(*c, n, *p, s))
+
+
+def kv_reorder(k, v, sources, lengths, stream=None) -> None:
+    """mk_kv_reorder on CUDA tensors: k / v bfloat16 [L][B][Hkv][max_seq][hd], sources / lengths int32 [B]: rows
+    [0, lengths[b]) of slot b become slot sources[b]'s."""
+    import torch
+    c, dev, i32 = _caches(k, v), k.device, torch.int32
+    p = (_need(sources, "sources", i32, (k.shape[1],), dev), _need(lengths, "lengths", i32, (k.shape[1],), dev))
+    L = load()
+    _run_on(dev, stream, lambda s: L.mk_kv_reorder(*c, *p, s))
 
 
 class Megakernel:

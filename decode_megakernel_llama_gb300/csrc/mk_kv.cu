@@ -1,0 +1,168 @@
+// mk_kv.cu — moves of rows inside the KV cache: mk_kv_compact (the accepted
+// path of a drafted tree, behind the committed rows) and mk_kv_reorder (slots
+// copied, forked and exchanged).
+//
+// Both are pure copies: what bounds them is the memory's rate, each moved row
+// read once and written once. The one thing to get right is that sources and
+// targets overlap, so every thread has all its loads behind it before the
+// first store that could touch another's source:
+//   compact: one CTA holds all moved rows of one (layer, K or V, slot, head)
+//     in registers, a barrier between its loads and its stores (no other CTA
+//     touches those rows);
+//   reorder: a thread owns one 16-byte column of a cache row in ALL slots;
+//     it loads what every slot will hold and then stores, so any mapping of
+//     slots, cycles too, needs no second buffer and no barrier.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mk_internal.h"
+#include "mk_ops.h"
+
+namespace mkops {
+namespace {
+
+constexpr int kMaxNodes = 64;
+constexpr int kT = 256;
+
+// grid (2 * L * Hkv, B): CTA of (layer, K or V, head) and slot.
+template <int HD>
+__global__ void __launch_bounds__(kT) kv_compact(uint16_t *kc, uint16_t *vc, int L, int B, int Hkv, int max_seq, int T,
+                                                 const int32_t *__restrict__ starts, const int32_t *__restrict__ nodes,
+                                                 const int32_t *__restrict__ counts) {
+    constexpr int CPR = HD / 8;                   // 16-byte chunks of a row
+    constexpr int NC = kMaxNodes * CPR / kT;      // chunks of a thread
+    const int b = blockIdx.y, tid = threadIdx.x;
+    const int plane = blockIdx.x % (L * Hkv), l = plane / Hkv, h = plane % Hkv;
+    uint16_t *cache = blockIdx.x < L * Hkv ? kc : vc;
+    const int start = starts[b], n = min(counts[b], T);
+    if (start < 0 || n <= 0) return;
+    uint4 *rows = reinterpret_cast<uint4 *>(cache + (((int64_t)l * B + b) * Hkv + h) * max_seq * HD);
+    uint4 v[NC];
+    bool move[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int i = (tid + c * kT) / CPR, part = tid % CPR;
+        move[c] = false;
+        if (i < n) {
+            const int node = nodes[(int64_t)b * T + i];
+            const int64_t src = (int64_t)start + node, dst = (int64_t)start + i;
+            move[c] = node >= 0 && node != i && src < max_seq && dst < max_seq;
+            if (move[c]) v[c] = rows[src * CPR + part];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int i = (tid + c * kT) / CPR, part = tid % CPR;
+        if (move[c]) rows[((int64_t)start + i) * CPR + part] = v[c];
+    }
+}
+
+// grid (blocks of a plane, 2 * L * Hkv); V = uint4 (NB <= 32) or uint2 (64).
+template <typename V, int NB>
+__global__ void __launch_bounds__(kT) kv_reorder(V *kc, V *vc, int L, int B, int Hkv, int max_seq, int cpr,
+                                                 const int32_t *__restrict__ sources,
+                                                 const int32_t *__restrict__ lengths) {
+    __shared__ int src[NB], len[NB];
+    __shared__ int most;
+    const int tid = threadIdx.x;
+    if (tid == 0) most = 0;
+    __syncthreads();
+    if (tid < NB) {
+        int s = tid < B ? sources[tid] : tid;
+        int n = tid < B ? min(max(lengths[tid], 0), max_seq) : 0;
+        if (s < 0 || s >= B || s == tid) n = 0;  // stays as it is
+        src[tid] = n ? s : 0;
+        len[tid] = n;
+        if (n) atomicMax(&most, n);
+    }
+    __syncthreads();
+    const int plane = blockIdx.y % (L * Hkv), l = plane / Hkv, h = plane % Hkv;
+    V *cache = blockIdx.y < L * Hkv ? kc : vc;
+    const int64_t slot_stride = (int64_t)Hkv * max_seq * cpr;
+    V *base = cache + ((int64_t)l * B * Hkv + h) * max_seq * cpr;
+    const int64_t total = (int64_t)most * cpr;
+    for (int64_t i = (int64_t)blockIdx.x * kT + tid; i < total; i += (int64_t)gridDim.x * kT) {
+        const int row = (int)(i / cpr);
+        V v[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            if (row < len[b]) v[b] = base[src[b] * slot_stride + i];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            if (row < len[b]) base[b * slot_stride + i] = v[b];
+    }
+}
+
+int check_cache(const char *who, const void *k, const void *v, int L, int B, int Hkv, int max_seq, int hd) {
+    using mkint::set_error;
+    if (!k || !v) return set_error(MK_ERR_INVALID_ARG, who);
+    if (L < 1 || B < 1 || Hkv < 1 || max_seq < 1) return set_error(MK_ERR_INVALID_ARG, who);
+    if (hd != 64 && hd != 128) return set_error(MK_ERR_UNSUPPORTED, who);
+    if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15u)
+        return set_error(MK_ERR_INVALID_ARG, who);
+    if ((int64_t)L * Hkv > 32767 || B > 65535) return set_error(MK_ERR_UNSUPPORTED, who);
+    return MK_OK;
+}
+
+}  // namespace
+}  // namespace mkops
+
+extern "C" int mk_kv_compact(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_kv_heads, int32_t max_seq,
+                             int32_t head_dim, int32_t nodes_per_slot, const int32_t *d_starts, const int32_t *d_nodes,
+                             const int32_t *d_counts, void *stream) {
+    using mkint::set_error;
+    const int rc = mkops::check_cache("mk_kv_compact: bad cache (pointer, alignment, size or head_dim)", k, v,
+                                      n_layers, slots, n_kv_heads, max_seq, head_dim);
+    if (rc) return rc;
+    if (!d_starts || !d_nodes || !d_counts)
+        return set_error(MK_ERR_INVALID_ARG, "mk_kv_compact: a required pointer is NULL");
+    if (nodes_per_slot < 1 || nodes_per_slot > mkops::kMaxNodes)
+        return set_error(MK_ERR_INVALID_ARG, "mk_kv_compact: nodes_per_slot outside [1, MK_MAX_TREE]");
+    const dim3 grid(2 * n_layers * n_kv_heads, slots);
+    uint16_t *kc = static_cast<uint16_t *>(k), *vc = static_cast<uint16_t *>(v);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (head_dim == 64)
+        mkops::kv_compact<64><<<grid, mkops::kT, 0, s>>>(kc, vc, n_layers, slots, n_kv_heads, max_seq, nodes_per_slot,
+                                                         d_starts, d_nodes, d_counts);
+    else
+        mkops::kv_compact<128><<<grid, mkops::kT, 0, s>>>(kc, vc, n_layers, slots, n_kv_heads, max_seq, nodes_per_slot,
+                                                          d_starts, d_nodes, d_counts);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? MK_OK : mkops::cuda_error(e, "mk_kv_compact");
+}
+
+extern "C" int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_kv_heads, int32_t max_seq,
+                             int32_t head_dim, const int32_t *d_sources, const int32_t *d_lengths, void *stream) {
+    using mkint::set_error;
+    const int rc = mkops::check_cache("mk_kv_reorder: bad cache (pointer, alignment, size or head_dim)", k, v,
+                                      n_layers, slots, n_kv_heads, max_seq, head_dim);
+    if (rc) return rc;
+    if (!d_sources || !d_lengths)
+        return set_error(MK_ERR_INVALID_ARG, "mk_kv_reorder: a required pointer is NULL");
+    if (slots > 64) return set_error(MK_ERR_UNSUPPORTED, "mk_kv_reorder: more than 64 slots");
+    const int planes = 2 * n_layers * n_kv_heads;
+    const int64_t chunks = (int64_t)max_seq * head_dim / 8;
+    int64_t per = (chunks + mkops::kT - 1) / mkops::kT;
+    const int64_t want = (152 * 16 + planes - 1) / planes;
+    if (per > want) per = want;
+    const dim3 grid((unsigned)per, planes);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int cpr = head_dim / 8;
+    auto go = [&](auto kernel, auto *kc, auto *vc, int c) {
+        kernel<<<grid, mkops::kT, 0, s>>>(kc, vc, n_layers, slots, n_kv_heads, max_seq, c, d_sources, d_lengths);
+    };
+    uint4 *k4 = static_cast<uint4 *>(k), *v4 = static_cast<uint4 *>(v);
+    if (slots <= 4)
+        go(mkops::kv_reorder<uint4, 4>, k4, v4, cpr);
+    else if (slots <= 8)
+        go(mkops::kv_reorder<uint4, 8>, k4, v4, cpr);
+    else if (slots <= 16)
+        go(mkops::kv_reorder<uint4, 16>, k4, v4, cpr);
+    else if (slots <= 32)
+        go(mkops::kv_reorder<uint4, 32>, k4, v4, cpr);
+    else
+        go(mkops::kv_reorder<uint2, 64>, static_cast<uint2 *>(k), static_cast<uint2 *>(v), 2 * cpr);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? MK_OK : mkops::cuda_error(e, "mk_kv_reorder");
+}

@@ -1,0 +1,60 @@
+// mk_ops.h — what the standalone operators' sources share (mk_rope.cu,
+// mk_tree.cu, mk_kv.cu), and their launches for the C ABI and for the paths of
+// the handle (mk_prefill.cu). Not part of the C ABI.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/mk.h"
+
+namespace mkops {
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// Two fp32 rounded to nearest even as bf16, `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t u;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+    return u;
+}
+#endif
+
+// Sets the calling thread's error text from a CUDA error; returns MK_ERR_CUDA.
+int cuda_error(cudaError_t e, const char *what);
+
+struct RopeArgs {
+    int n, Hq, Hkv, rot, interleaved, slots, max_seq;
+    float eps, mscale;
+    int64_t qkv_stride, q_stride;  // elements from one token to the next
+    const void *qkv;
+    void *q_out;
+    uint16_t *kc, *vc;
+    const int32_t *positions, *rows, *slot_of;
+    const double *inv_freq;
+    const uint16_t *q_norm, *k_norm;
+};
+
+cudaError_t rope_append_launch(const RopeArgs &a, int hd, bool f32, cudaStream_t s);
+
+// Attention of a tree of drafted tokens. Out: out (fp32 or bf16), or, with
+// hi set, the hi / lo bf16 terms of the fp32 result at out's strides.
+struct TreeArgs {
+    int B, T, Hq, Hkv, slots, max_seq;
+    float scale;
+    int64_t q_batch, q_token, o_batch, o_token;  // strides in elements
+    const void *q;
+    void *out;
+    uint16_t *hi, *lo;
+    const uint16_t *kc, *vc;
+    const int32_t *lengths, *counts, *slot_of;
+    const uint64_t *masks;
+};
+
+cudaError_t tree_attention_launch(const TreeArgs &a, int hd, bool f32, int max_len, int n_sm, cudaStream_t s);
+
+cudaError_t tree_masks_launch(const int32_t *parents, const int32_t *counts, int B, int T, uint64_t *masks,
+                              int32_t *depths, cudaStream_t s);
+
+}  // namespace mkops

@@ -1,0 +1,250 @@
+// mk_rope.cu — per-head norms, rotary positions and the append to the KV
+// cache in one pass (mk_rope_append), and the host-side frequencies of scaled
+// contexts (mk_rope_frequencies).
+//
+// Mathematics, for token t with rotary position p, head vector x [hd]:
+//   x' = x * g / sqrt(mean(x^2) + eps)              (queries, keys; optional)
+//   angle_i = p * w_i, w_i radians per position (64 bits)
+//   (a, b) -> mscale * (a cos - b sin, b cos + a sin) for the rot/2 pairs
+//   (x'_i, x'_{i + rot/2}) or, interleaved, (x'_{2i}, x'_{2i+1});
+//   the hd - rot elements behind them pass through.
+// The angle is reduced to a fraction of a turn in 64 bits before its sine and
+// cosine are taken in 32, so a far position loses nothing: a turn's fraction
+// is off by at most p * 2^-53 turns.
+//
+// What bounds it: memory. Each element is read once and written once; the
+// arithmetic is a few operations an element. A CTA takes one token: its first
+// rot/2 threads form the token's sines and cosines once for all heads
+// (shared memory) while every warp's loads are already in flight; a head is
+// held by hd/4 lanes of a warp, four elements a lane, so the norm is a
+// shuffle sum and the partner of a pair is a shuffle away.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "mk_internal.h"
+#include "mk_ops.h"
+
+namespace mkops {
+namespace {
+
+constexpr int kT = 256;  // threads per CTA
+constexpr int kW = kT / 32;
+constexpr int kMaxHalf = 64;  // rotated pairs of a head
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float *p) {
+    return *reinterpret_cast<const float4 *>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<uint16_t>(const uint16_t *p) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y));
+}
+
+__device__ __forceinline__ uint2 pack4(float4 v) { return make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)); }
+
+template <typename T>
+__device__ __forceinline__ void store4(T *p, float4 v);
+template <>
+__device__ __forceinline__ void store4<float>(float *p, float4 v) {
+    *reinterpret_cast<float4 *>(p) = v;
+}
+template <>
+__device__ __forceinline__ void store4<uint16_t>(uint16_t *p, float4 v) {
+    *reinterpret_cast<uint2 *>(p) = pack4(v);
+}
+
+// The value of element e of this lane's head, from the head's staged row.
+__device__ __forceinline__ float part(const float4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kT) rope_append(const RopeArgs a) {
+    constexpr int LPH = HD / 4;    // lanes of a head
+    constexpr int HPW = 32 / LPH;  // heads of a warp
+    __shared__ float2 cs[kMaxHalf];
+    __shared__ float4 stage[kT];  // a head's row, for pairs that are not whole lanes apart
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int sub = lane / LPH, j = lane % LPH;  // head of the warp, lane of the head
+    const int t = blockIdx.x, half = a.rot / 2;
+    const T *in = static_cast<const T *>(a.qkv) + (int64_t)t * a.qkv_stride;
+    T *qo = static_cast<T *>(a.q_out) + (int64_t)t * a.q_stride;
+    const int n_rows = a.Hq + 2 * a.Hkv;
+    const int slot = a.slot_of ? a.slot_of[t] : 0, row = a.rows[t];
+    const bool keep = slot >= 0 && slot < a.slots && row >= 0 && row < a.max_seq;
+    if (tid < half) {
+        // radians to turns in 64 bits; the fraction of a turn fits 32
+        const double turns = (double)a.positions[t] * a.inv_freq[tid] * 0.15915494309189533577;
+        float s, c;
+        sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+        cs[tid] = make_float2(c * a.mscale, s * a.mscale);
+    }
+    __syncthreads();
+    for (int h0 = blockIdx.y * kW * HPW + warp * HPW; h0 < n_rows; h0 += gridDim.y * kW * HPW) {
+        const int h = h0 + sub;
+        const bool live = h < n_rows;
+        float4 v = live ? load4<T>(in + h * HD + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
+        const uint16_t *gain = is_q ? a.q_norm : (is_k ? a.k_norm : nullptr);
+        float ss = v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        if (gain) {
+            const float r = 1.0f / sqrtf(ss * (1.0f / HD) + a.eps);
+            const float4 g = load4<uint16_t>(gain + 4 * j);
+            v = make_float4(v.x * r * g.x, v.y * r * g.y, v.z * r * g.z, v.w * r * g.w);
+        }
+        float4 y = v;
+        if (a.interleaved) {
+            if (is_q || is_k) {
+                if (2 * j < half) {
+                    const float2 c = cs[2 * j];
+                    y.x = v.x * c.x - v.y * c.y;
+                    y.y = v.y * c.x + v.x * c.y;
+                }
+                if (2 * j + 1 < half) {
+                    const float2 c = cs[2 * j + 1];
+                    y.z = v.z * c.x - v.w * c.y;
+                    y.w = v.w * c.x + v.z * c.y;
+                }
+            }
+        } else {
+            __syncwarp();
+            stage[tid] = v;
+            __syncwarp();
+            if (is_q || is_k) {
+                const float *mine = reinterpret_cast<const float *>(stage + tid - j);
+                float o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = 4 * j + i;
+                    const float x = part(v, i);
+                    if (e < half) {
+                        const float2 c = cs[e];
+                        o[i] = x * c.x - mine[e + half] * c.y;
+                    } else if (e < a.rot) {
+                        const float2 c = cs[e - half];
+                        o[i] = x * c.x + mine[e - half] * c.y;
+                    } else {
+                        o[i] = x;
+                    }
+                }
+                y = make_float4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        if (!live) continue;
+        if (is_q) {
+            store4<T>(qo + h * HD + 4 * j, y);
+        } else if (keep) {
+            const int kvh = is_k ? h - a.Hq : h - a.Hq - a.Hkv;
+            uint16_t *c = is_k ? a.kc : a.vc;
+            store4<uint16_t>(c + (((int64_t)slot * a.Hkv + kvh) * a.max_seq + row) * HD + 4 * j, y);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t rope_append_launch(const RopeArgs &a, int hd, bool f32, cudaStream_t s) {
+    const dim3 grid(a.n, 1);
+    if (f32) {
+        if (hd == 64)
+            rope_append<float, 64><<<grid, kT, 0, s>>>(a);
+        else
+            rope_append<float, 128><<<grid, kT, 0, s>>>(a);
+    } else {
+        if (hd == 64)
+            rope_append<uint16_t, 64><<<grid, kT, 0, s>>>(a);
+        else
+            rope_append<uint16_t, 128><<<grid, kT, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace mkops
+
+extern "C" int mk_rope_append(const mk_rope_args *a, void *stream) {
+    using mkint::set_error;
+    if (!a || !a->qkv || !a->q_out || !a->k_cache || !a->v_cache || !a->positions || !a->rows || !a->inv_freq)
+        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: a required pointer is NULL");
+    if (a->dtype != MK_F32 && a->dtype != MK_BF16)
+        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: dtype is neither MK_F32 nor MK_BF16");
+    if (a->head_dim != 64 && a->head_dim != 128)
+        return set_error(MK_ERR_UNSUPPORTED, "mk_rope_append: head_dim must be 64 or 128");
+    if (a->n < 0 || a->n_heads < 1 || a->n_kv_heads < 1 || a->slots < 1 || a->max_seq < 1)
+        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: bad size");
+    if (a->rot < 2 || a->rot > a->head_dim || a->rot % 2)
+        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: rot must be even, 2 .. head_dim");
+    if (!(a->eps >= 0.f) || !isfinite(a->eps) || !isfinite(a->mscale))
+        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: eps or mscale is not a finite number");
+    const int64_t q = (int64_t)a->n_heads * a->head_dim, qkv = q + 2 * (int64_t)a->n_kv_heads * a->head_dim;
+    if (qkv > INT32_MAX) return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: too many heads");
+    if (a->qkv_stride < qkv || a->q_stride < q || a->qkv_stride % 4 || a->q_stride % 4)
+        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: a stride is too small or not a multiple of 4 elements");
+    const uintptr_t io = reinterpret_cast<uintptr_t>(a->qkv) | reinterpret_cast<uintptr_t>(a->q_out);
+    const uintptr_t cache = reinterpret_cast<uintptr_t>(a->k_cache) | reinterpret_cast<uintptr_t>(a->v_cache) |
+                            reinterpret_cast<uintptr_t>(a->q_norm) | reinterpret_cast<uintptr_t>(a->k_norm);
+    if ((io & 15u) || (cache & 7u) || (reinterpret_cast<uintptr_t>(a->inv_freq) & 7u))
+        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: a pointer is not aligned");
+    if (a->n == 0) return MK_OK;
+    mkops::RopeArgs r{};
+    r.n = a->n, r.Hq = a->n_heads, r.Hkv = a->n_kv_heads, r.rot = a->rot, r.interleaved = a->interleaved;
+    r.slots = a->slots, r.max_seq = a->max_seq, r.eps = a->eps, r.mscale = a->mscale;
+    r.qkv_stride = a->qkv_stride, r.q_stride = a->q_stride;
+    r.qkv = a->qkv, r.q_out = a->q_out;
+    r.kc = static_cast<uint16_t *>(a->k_cache), r.vc = static_cast<uint16_t *>(a->v_cache);
+    r.positions = a->positions, r.rows = a->rows, r.slot_of = a->slot_of, r.inv_freq = a->inv_freq;
+    r.q_norm = static_cast<const uint16_t *>(a->q_norm), r.k_norm = static_cast<const uint16_t *>(a->k_norm);
+    const cudaError_t e =
+        mkops::rope_append_launch(r, a->head_dim, a->dtype == MK_F32, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MK_OK : mkops::cuda_error(e, "mk_rope_append");
+}
+
+extern "C" int mk_rope_frequencies(int32_t kind, int32_t rot, double theta, double factor, double original_len,
+                                   double low, double high, double *out, float *mscale) {
+    using mkint::set_error;
+    if (!out || !mscale) return set_error(MK_ERR_INVALID_ARG, "mk_rope_frequencies: NULL pointer");
+    if (rot < 2 || rot % 2 || !(theta > 1.0) || !isfinite(theta))
+        return set_error(MK_ERR_INVALID_ARG, "mk_rope_frequencies: rot must be even and >= 2, theta finite and > 1");
+    if (kind != MK_ROPE_PLAIN && (!(factor >= 1.0) || !isfinite(factor)))
+        return set_error(MK_ERR_INVALID_ARG, "mk_rope_frequencies: factor must be finite and >= 1");
+    if ((kind == MK_ROPE_WAVELENGTH || kind == MK_ROPE_YARN) &&
+        (!(original_len > 0.0) || !(low > 0.0) || !(high > low) || !isfinite(original_len) || !isfinite(high)))
+        return set_error(MK_ERR_INVALID_ARG, "mk_rope_frequencies: needs original_len > 0 and 0 < low < high");
+    const double two_pi = 6.283185307179586477;
+    double base = theta;
+    *mscale = 1.f;
+    if (kind == MK_ROPE_BASE) {
+        if (rot < 4) return set_error(MK_ERR_INVALID_ARG, "mk_rope_frequencies: MK_ROPE_BASE needs rot >= 4");
+        base = theta * pow(factor, (double)rot / (rot - 2));
+    } else if (kind < MK_ROPE_PLAIN || kind > MK_ROPE_YARN) {
+        return set_error(MK_ERR_INVALID_ARG, "mk_rope_frequencies: unknown kind");
+    }
+    double lo = 0.0, hi = 1.0;
+    if (kind == MK_ROPE_YARN) {
+        // the pair whose wave turns b times over the original context
+        auto pair_of = [&](double b) { return rot * log(original_len / (b * two_pi)) / (2.0 * log(theta)); };
+        lo = std::max(0.0, floor(pair_of(high)));
+        hi = std::min(rot - 1.0, ceil(pair_of(low)));
+        *mscale = (float)(0.1 * log(factor) + 1.0);
+    }
+    for (int i = 0; i < rot / 2; ++i) {
+        const double f = pow(base, -2.0 * i / rot);
+        double w = f;
+        if (kind == MK_ROPE_LINEAR) {
+            w = f / factor;
+        } else if (kind == MK_ROPE_WAVELENGTH) {
+            const double s = std::min(1.0, std::max(0.0, (original_len * f / two_pi - low) / (high - low)));
+            w = f * ((1.0 - s) / factor + s);
+        } else if (kind == MK_ROPE_YARN) {
+            const double r = std::min(1.0, std::max(0.0, (i - lo) / std::max(1e-3, hi - lo)));
+            w = f / factor * r + f * (1.0 - r);
+        }
+        out[i] = w;
+    }
+    return MK_OK;
+}

@@ -397,6 +397,147 @@ int mk_twell_down(const void *d_w_down_t, int32_t F, int32_t d, const float *d_h
 int mk_twell_ffn(const void *d_w_gate, const void *d_w_up, const void *d_w_down_t, int32_t F, int32_t d,
                  const float *d_x, float *d_h, float *d_y, void *stream);
 
+/* ---- Operators of a drafted tree ------------------------------------------
+ * What a step that verifies several drafted tokens at once needs beside the
+ * decode step: the tokens of a tree are appended to the cache behind the
+ * committed rows (mk_rope_append), every node attends over the committed rows
+ * and its own ancestors (mk_tree_attention), and the accepted path's rows
+ * move up behind the committed ones (mk_kv_compact); mk_kv_reorder copies,
+ * forks and exchanges whole sequences. They work on one layer's (or, the
+ * last two, all layers') cache in mk_kv_cache's layout, on the current
+ * device, with no handle and no workspace: one launch each, asynchronous on
+ * `stream`, safe in several streams at once and in captured graphs as long as
+ * the calls touch different memory. Device arrays are read when the kernel
+ * runs; what they hold is checked there, and a sequence, row or slot that
+ * lies outside the cache is left alone, never followed.
+ * The pages name no such operators; each declaration states its formula. */
+#define MK_F32 0
+#define MK_BF16 1
+#define MK_MAX_TREE 64  /* nodes of a tree */
+#define MK_MAX_GROUP 16 /* query heads per kv head of mk_tree_attention */
+
+/* Norms, rotary positions and cache append of n tokens in one pass.
+ * Row t of qkv (dtype, row stride qkv_stride elements) holds n_heads query
+ * heads, then n_kv_heads key heads, then n_kv_heads value heads of head_dim
+ * (64 or 128) elements. Per query head (and key head, with k_norm):
+ *   x' = x * q_norm / sqrt(mean(x^2) + eps)   (q_norm bf16 [head_dim], or NULL)
+ *   (a, b) -> mscale * (a cos A_i - b sin A_i, b cos A_i + a sin A_i),
+ *   A_i = positions[t] * inv_freq[i], i < rot / 2,
+ * over the pairs (x'_i, x'_{i + rot/2}), or with `interleaved` (x'_{2i},
+ * x'_{2i+1}), of the first rot elements; the others pass through. Rotated
+ * queries go to q_out (dtype, [n][n_heads][head_dim], token stride q_stride;
+ * it may be qkv itself with the same stride), rotated keys and the values,
+ * rounded to nearest bf16, to cache row rows[t] of slot slot_of[t] (0 with
+ * slot_of NULL). A row outside [0, max_seq) or slot outside [0, slots) is
+ * not written (its query still is); two tokens of one call must not name
+ * the same row. Sums, sines and cosines are fp32, angles 64-bit.
+ * k_cache, v_cache: bf16 [slots][n_kv_heads][max_seq][head_dim], one layer.
+ * positions, rows, slot_of: device int32 [n]; inv_freq: device double
+ * [rot / 2], radians per position (mk_rope_frequencies makes them).
+ * qkv and q_out 16-byte, the others naturally (caches, norms 8-byte)
+ * aligned, strides multiples of 4 elements. MK_ERR_INVALID_ARG, or
+ * MK_ERR_UNSUPPORTED for another head_dim. n = 0 does nothing. */
+typedef struct mk_rope_args {
+    int32_t n, n_heads, n_kv_heads, head_dim, rot, interleaved, dtype, slots, max_seq;
+    float eps, mscale;
+    int64_t qkv_stride, q_stride;
+    const void *qkv;
+    void *q_out;
+    void *k_cache, *v_cache;
+    const int32_t *positions, *rows, *slot_of;
+    const double *inv_freq;
+    const void *q_norm, *k_norm;
+} mk_rope_args;
+int mk_rope_append(const mk_rope_args *args, void *stream);
+
+/* Host: the frequencies of mk_rope_append for a context scaled `factor`
+ * times, out[i] (host double [rot / 2]), and the factor on the rotated values
+ * (*mscale). With f_i = theta^(-2i / rot):
+ *   MK_ROPE_PLAIN       f_i
+ *   MK_ROPE_LINEAR      f_i / factor (position interpolation)
+ *   MK_ROPE_BASE        f_i with theta * factor^(rot / (rot - 2)) as theta
+ *   MK_ROPE_WAVELENGTH  f_i ((1 - s) / factor + s), s = (turns - low) /
+ *                       (high - low) clamped to [0, 1], turns = original_len
+ *                       f_i / 2 pi (the turns over the original context)
+ *   MK_ROPE_YARN        f_i (r / factor + 1 - r), r rising from 0 at the pair
+ *                       that turns `high` times over the original context to
+ *                       1 at the one that turns `low` times (Peng et al.,
+ *                       2023); *mscale = 0.1 ln(factor) + 1
+ * *mscale is 1 for the others. MK_ERR_INVALID_ARG for values outside their
+ * meaning (factor < 1, low >= high, an odd rot, ...). */
+#define MK_ROPE_PLAIN 0
+#define MK_ROPE_LINEAR 1
+#define MK_ROPE_BASE 2
+#define MK_ROPE_WAVELENGTH 3
+#define MK_ROPE_YARN 4
+int mk_rope_frequencies(int32_t kind, int32_t rot, double theta, double factor, double original_len, double low,
+                        double high, double *out, float *mscale);
+
+/* Attention of drafted trees over the cache. For sequence b < batch, node t <
+ * counts[b] (every node with counts NULL), query head h:
+ *   out = sum_j p_j v_j / sum_j p_j, p_j = exp(scale * q . k_j - max),
+ * over the rows j of kv head h / (n_heads / n_kv_heads) of slot slot_of[b] (b
+ * with slot_of NULL) that the node sees: the committed rows j < lengths[b],
+ * and row lengths[b] + i, i < counts[b], where bit i of masks[b][t] is set
+ * (mk_tree_masks makes them of parents). What the other rows hold, NaN and
+ * infinities too, does not matter; a node that sees no row gets zeros; nodes
+ * from counts[b] on are not written. nodes = 1 is plain decode attention.
+ * q and out: dtype (fp32 or bf16), head h of node t of sequence b at b *
+ * batch_stride + t * token_stride + h * head_dim; caches bf16 [slots]
+ * [n_kv_heads][max_seq][head_dim], one layer; head_dim 64 or 128. Sums and
+ * statistics are fp32; fp32 queries and the probabilities with them enter the
+ * products as two bf16 terms each (16 bits of the value), bf16 queries as
+ * they are. max_len: a bound on lengths[b] known to the host (0: max_seq),
+ * used only to choose the launch; results are right if a length exceeds it.
+ * lengths outside [0, max_seq] and counts past the nodes or the cache's end
+ * are cut to them. out must not overlap q or the cache. Pointers 16-byte
+ * aligned, strides multiples of 8 elements. */
+typedef struct mk_tree_args {
+    int32_t batch, nodes, n_heads, n_kv_heads, head_dim, dtype, slots, max_seq, max_len;
+    float scale;
+    int64_t q_batch_stride, q_token_stride, out_batch_stride, out_token_stride;
+    const void *q;
+    void *out;
+    const void *k_cache, *v_cache;
+    const int32_t *lengths, *counts, *slot_of;
+    const uint64_t *masks;
+} mk_tree_args;
+int mk_tree_attention(const mk_tree_args *args, void *stream);
+
+/* masks[b][t] (bit i: node i is t or an ancestor of t) and, if depths is not
+ * NULL, depths[b][t] (0 for a root) of the trees d_parents (device int32
+ * [batch][nodes]: the parent's index, below the node's own; anything else
+ * makes the node a root). Nodes from d_counts[b] on (nullable) are not
+ * written. */
+int mk_tree_masks(const int32_t *d_parents, const int32_t *d_counts, int32_t batch, int32_t nodes, uint64_t *d_masks,
+                  int32_t *d_depths, void *stream);
+
+/* Host: the accepted path of a verified tree. Node 0 is the token that was
+ * already chosen; draws[t] is the model's token after node t. The walk goes
+ * from a node to its first child whose token is the draw there, until there
+ * is none. path (host int32 [n]) receives the nodes, node 0 first; returns
+ * their number c (draws[path[c - 1]] is the next token), or
+ * MK_ERR_INVALID_ARG. */
+int mk_tree_accept(const int32_t *tokens, const int32_t *parents, const int32_t *draws, int32_t n, int32_t *path);
+
+/* For every layer, kv head, slot b and i < d_counts[b]: cache row starts[b] +
+ * nodes[b][i] (keys and values) moves to row starts[b] + i, all as if at
+ * once. k, v: bf16 [n_layers][slots][n_kv_heads][max_seq][head_dim]; d_starts,
+ * d_counts device int32 [slots], d_nodes device int32 [slots][nodes_per_slot],
+ * nodes_per_slot <= MK_MAX_TREE. A negative node, or one that leads out of
+ * the cache, moves nothing; a slot with count 0 is left as it is. */
+int mk_kv_compact(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_kv_heads, int32_t max_seq,
+                  int32_t head_dim, int32_t nodes_per_slot, const int32_t *d_starts, const int32_t *d_nodes,
+                  const int32_t *d_counts, void *stream);
+
+/* For every layer, kv head and slot b: rows [0, d_lengths[b]) of slot b become
+ * what slot d_sources[b] held before the call, all slots as if at once, so
+ * slots can be forked, exchanged and rotated in place (beams, parallel
+ * samples). A slot whose source is itself or outside [0, slots), and rows
+ * from d_lengths[b] on, are left as they are. At most 64 slots. */
+int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_kv_heads, int32_t max_seq,
+                  int32_t head_dim, const int32_t *d_sources, const int32_t *d_lengths, void *stream);
+
 /* Optional per-instruction timing: when `enable` is non-zero, every step
  * records %globaltimer stamps per instruction into a device buffer that
  * mk_read_trace copies out (see mk_read_trace).
