@@ -13,7 +13,7 @@ LIB = os.path.join(BUILD, "libmk.so")
 LIB_CHECKED = os.path.join(BUILD, "libmk_checked.so")
 SOURCES = ["mk_kernel_hd64.cu", "mk_kernel_hd128.cu", "mk_kernel.cu", "mk_host.cpp", "mk_noalloc.cu", "mk_w2a8.cu",
            "mk_prefill.cu", "mk_twell.cu", "mk_rope.cu", "mk_tree.cu", "mk_kv.cu"]
-DEPS = SOURCES + ["mk_kernel.cuh", "mk_plan.h", "mk_internal.h", "mk_prefill.h", "mk_ops.h"]
+DEPS = SOURCES + ["mk_kernel.cuh", "mk_plan.h", "mk_internal.h", "mk_prefill.h", "mk_ops.h", "mk_tc.cuh", "mk_tree_attn.cuh"]
 
 
 def nvcc() -> str:

@@ -50,6 +50,7 @@ struct TreeArgs {
     const uint16_t *kc, *vc;
     const int32_t *lengths, *counts, *slot_of;
     const uint64_t *masks;
+    int *err;  // set to 1 if a bounded wait runs out (nullable)
 };
 
 cudaError_t tree_attention_launch(const TreeArgs &a, int hd, bool f32, int max_len, int n_sm, cudaStream_t s);

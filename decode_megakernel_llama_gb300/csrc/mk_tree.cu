@@ -13,92 +13,14 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <algorithm>
+
 #include "mk_internal.h"
 #include "mk_ops.h"
+#include "mk_tree_attn.cuh"
 
 namespace mkops {
 namespace {
-
-constexpr int kT = 256;
-constexpr int kW = kT / 32;
-
-// The sequence's slot, committed rows and nodes, held inside the cache
-// whatever the device arrays say.
-struct Seq {
-    int slot, len, n;
-};
-
-__device__ __forceinline__ Seq sequence(const TreeArgs &a, int b) {
-    Seq s;
-    s.slot = a.slot_of ? a.slot_of[b] : b;
-    s.len = min(max(a.lengths[b], 0), a.max_seq);
-    s.n = min(a.counts ? min(max(a.counts[b], 0), a.T) : a.T, a.max_seq - s.len);
-    if (s.slot < 0 || s.slot >= a.slots) s.n = 0;
-    return s;
-}
-
-// One CTA per (query head, node, sequence); warp w takes every 8th row, lane
-// l the dims E l .. E l + E - 1.
-template <typename TQ, int HD>
-__global__ void __launch_bounds__(kT) tree_attention_simple(const TreeArgs a) {
-    constexpr int E = HD / 32;
-    __shared__ float ms[kW], ls[kW], os[kW][HD];
-    const int h = blockIdx.x, t = blockIdx.y, b = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Seq s = sequence(a, b);
-    if (t >= s.n) return;
-    const TQ *q = static_cast<const TQ *>(a.q) + b * a.q_batch + t * a.q_token + (int64_t)h * HD + E * lane;
-    float qv[E], o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        if constexpr (sizeof(TQ) == 4)
-            qv[e] = q[e] * a.scale;
-        else
-            qv[e] = bf_lo(q[e]) * a.scale;
-        o[e] = 0.f;
-    }
-    const int64_t at = ((int64_t)s.slot * a.Hkv + h / (a.Hq / a.Hkv)) * a.max_seq * HD + E * lane;
-    const uint64_t mask = a.masks[(int64_t)b * a.T + t];
-    float m = -INFINITY, l = 0.f;
-    for (int j = warp; j < s.len + s.n; j += kW) {
-        if (j >= s.len && !((mask >> (j - s.len)) & 1)) continue;
-        const uint16_t *k = a.kc + at + (int64_t)j * HD, *v = a.vc + at + (int64_t)j * HD;
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) x = fmaf(qv[e], bf_lo(k[e]), x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-        const float mn = fmaxf(m, x), c = m == mn ? 1.f : expf(m - mn), p = expf(x - mn);
-        l = l * c + p;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(p, bf_lo(v[e]), o[e] * c);
-        m = mn;
-    }
-    if (lane == 0) ms[warp] = m, ls[warp] = l;
-#pragma unroll
-    for (int e = 0; e < E; ++e) os[warp][E * lane + e] = o[e];
-    __syncthreads();
-    for (int d = threadIdx.x; d < HD; d += kT) {
-        float M = -INFINITY, L = 0.f, O = 0.f;
-        for (int w = 0; w < kW; ++w) M = fmaxf(M, ms[w]);
-        for (int w = 0; w < kW; ++w) {
-            const float c = ms[w] == -INFINITY ? 0.f : expf(ms[w] - M);
-            L = fmaf(ls[w], c, L);
-            O = fmaf(os[w][d], c, O);
-        }
-        const float y = M == -INFINITY ? 0.f : O / L;
-        const int64_t to = b * a.o_batch + t * a.o_token + (int64_t)h * HD + d;
-        if (a.hi) {
-            const uint32_t u = pack_bf16(y, 0.f);
-            a.hi[to] = (uint16_t)u;
-            a.lo[to] = (uint16_t)pack_bf16(y - bf_lo(u), 0.f);
-        } else if constexpr (sizeof(TQ) == 4) {
-            static_cast<float *>(a.out)[to] = y;
-        } else {
-            static_cast<uint16_t *>(a.out)[to] = (uint16_t)pack_bf16(y, 0.f);
-        }
-    }
-}
 
 // One warp per sequence; lane l walks up from nodes l and l + 32.
 __global__ void __launch_bounds__(32) tree_masks(const int32_t *__restrict__ parents,
@@ -131,20 +53,82 @@ int cuda_error(cudaError_t e, const char *what) {
     return mkint::set_error(MK_ERR_CUDA, text);
 }
 
+namespace {
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// The cache of one layer as [planes][max_seq][hd], boxes of 128 rows x 64
+// dims, 128-byte swizzle. Made for each call (it holds the address).
+bool cache_map(CUtensorMap *map, const void *cache, int planes, int max_seq, int hd) {
+    const EncodeTiled enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)max_seq, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)max_seq * hd * 2};
+    const cuuint32_t box[3] = {64, kTile, 1}, one[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(cache), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int HD, int TERMS, int NR>
+cudaError_t launch(const TreeArgs &a, int max_len, int n_sm, cudaStream_t s) {
+    using C = AttnShape<HD, TERMS, NR>;
+    CUtensorMap kmap, vmap;
+    if (!cache_map(&kmap, a.kc, a.slots * a.Hkv, a.max_seq, HD) ||
+        !cache_map(&vmap, a.vc, a.slots * a.Hkv, a.max_seq, HD))
+        return cudaErrorInvalidValue;
+    const auto kernel = tree_attention<HD, TERMS, NR>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    const int row_tiles = (a.T * (a.Hq / a.Hkv) + NR - 1) / NR;
+    const int64_t units = (int64_t)a.B * a.Hkv * row_tiles;
+    const int tiles = (std::min(max_len + a.T, a.max_seq) + kTile - 1) / kTile;
+    int S = 1;
+    while (S < 16 && units * S * 2 <= n_sm * (HD == 64 ? 2 : 1) && S * 2 <= tiles) S *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(S, a.B * a.Hkv, row_tiles);
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, kmap, vmap, a);
+}
+
+}  // namespace
+
 cudaError_t tree_attention_launch(const TreeArgs &a, int hd, bool f32, int max_len, int n_sm, cudaStream_t s) {
-    const dim3 grid(a.Hq, a.T, a.B);
+    const int rows = a.T * (a.Hq / a.Hkv);
     if (f32) {
-        if (hd == 64)
-            tree_attention_simple<float, 64><<<grid, kT, 0, s>>>(a);
-        else
-            tree_attention_simple<float, 128><<<grid, kT, 0, s>>>(a);
-    } else {
-        if (hd == 64)
-            tree_attention_simple<uint16_t, 64><<<grid, kT, 0, s>>>(a);
-        else
-            tree_attention_simple<uint16_t, 128><<<grid, kT, 0, s>>>(a);
+        if (hd == 64) return rows <= 16 ? launch<64, 3, 16>(a, max_len, n_sm, s) : launch<64, 3, 32>(a, max_len, n_sm, s);
+        return rows <= 16 ? launch<128, 3, 16>(a, max_len, n_sm, s) : launch<128, 3, 32>(a, max_len, n_sm, s);
     }
-    return cudaGetLastError();
+    if (hd == 64)
+        return rows <= 16   ? launch<64, 1, 16>(a, max_len, n_sm, s)
+               : rows <= 32 ? launch<64, 1, 32>(a, max_len, n_sm, s)
+                            : launch<64, 1, 64>(a, max_len, n_sm, s);
+    return rows <= 16   ? launch<128, 1, 16>(a, max_len, n_sm, s)
+           : rows <= 32 ? launch<128, 1, 32>(a, max_len, n_sm, s)
+                        : launch<128, 1, 64>(a, max_len, n_sm, s);
 }
 
 cudaError_t tree_masks_launch(const int32_t *parents, const int32_t *counts, int B, int T, uint64_t *masks,
