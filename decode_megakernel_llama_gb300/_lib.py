@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_build", "libmk.so")
@@ -72,7 +73,14 @@ class mk_tree_args(ctypes.Structure):
                 + [(n, ctypes.c_int64) for n in ("q_batch_stride", "q_token_stride", "out_batch_stride",
                                                  "out_token_stride")]
                 + [(n, ctypes.c_void_p) for n in ("q", "out", "k_cache", "v_cache", "lengths", "counts", "slot_of",
-                                                  "masks")])
+                                                  "masks", "workspace")]
+                + [("workspace_bytes", ctypes.c_int64), ("status", ctypes.c_void_p)])
+
+
+# The same two as one packed record each (native layout): filling a ctypes
+# structure field by field costs more than the launch it is for.
+_ROPE_ARGS = struct.Struct("@9i2f2q10P")
+_TREE_ARGS = struct.Struct("@9if4q9PqP")
 
 
 _lib = None
@@ -122,9 +130,11 @@ def load(path: str | None = None):
     L.mk_twell_ffn.argtypes = [_VP, _VP, _VP, _I32, _I32, _VP, _VP, _VP, _VP]
     L.mk_prefill.argtypes = [_VP, _VP, _I32, _I32, _VP, _VP, _VP]
     L.mk_tc_gemm.argtypes = [_VP, _I32, _I32, _VP, _VP, _I32, _VP, _VP, _VP, _VP]
-    L.mk_rope_append.argtypes = [ctypes.POINTER(mk_rope_args), _VP]
+    L.mk_rope_append.argtypes = [_VP, _VP]  # a packed record, or byref of the structure
     L.mk_rope_frequencies.argtypes = [_I32, _I32] + [ctypes.c_double] * 5 + [_VP, ctypes.POINTER(ctypes.c_float)]
-    L.mk_tree_attention.argtypes = [ctypes.POINTER(mk_tree_args), _VP]
+    L.mk_tree_attention.argtypes = [_VP, _VP]
+    L.mk_tree_attention_workspace.argtypes = [_VP]
+    L.mk_tree_attention_workspace.restype = ctypes.c_int64
     L.mk_tree_masks.argtypes = [_VP, _VP, _I32, _I32, _VP, _VP, _VP]
     L.mk_tree_accept.argtypes = [_VP, _VP, _VP, _I32, _VP]
     L.mk_kv_compact.argtypes = [_VP, _VP] + [_I32] * 6 + [_VP] * 4
@@ -288,36 +298,38 @@ def _bad(msg: str):
     raise MKError(MK_ERR_INVALID_ARG, msg)
 
 
-def _need(t, what: str, dtype, shape, dev, dense: bool = True):
-    """Device pointer of tensor t after its type, shape (None: any extent), device and layout are checked."""
+def _need(t, what: str, dtype, shape, like, dense: bool = True) -> None:
+    """Raises unless tensor t has this type, shape (a tuple) and layout and is on the device of `like`."""
     if t.dtype != dtype:
         _bad(f"{what} must be {dtype}, not {t.dtype}")
-    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        _bad(f"{what} has shape {tuple(t.shape)}, not {shape}")
-    if t.device != dev:
-        _bad(f"{what} is on {t.device}, not {dev}")
+    if t.shape != shape:
+        _bad(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.device != like.device:
+        _bad(f"{what} is on {t.device}, not {like.device}")
     if dense and not t.is_contiguous():
         _bad(f"{what} must be contiguous")
-    return t.data_ptr()
 
 
-def _run_on(dev, stream, call) -> None:
-    """call(stream pointer) with `dev` current; without a stream, on dev's current one."""
+def _run_on(t, stream, fn, *args) -> None:
+    """fn(*args, stream pointer) with t's device current; without a stream, on that device's current one."""
     import torch
-    if dev.type != "cuda":
-        _bad(f"tensors must be on a CUDA device, not {dev}")
-    if torch.cuda.current_device() == dev.index:
-        check(call((stream or torch.cuda.current_stream()).cuda_stream))
+    d = t.get_device()
+    if d < 0:
+        _bad(f"tensors must be on a CUDA device, not {t.device}")
+    if d == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(dev):
-            check(call((stream or torch.cuda.current_stream()).cuda_stream))
+        with torch.cuda.device(d):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream)
+    if rc < 0:
+        check(rc)
 
 
 def _io_dtype(t, what: str) -> int:
     import torch
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return MK_F32
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return MK_BF16
     _bad(f"{what} must be float32 or bfloat16, not {t.dtype}")
 
@@ -344,77 +356,115 @@ def rope_append(qkv, q_out, k_cache, v_cache, positions, rows, inv_freq, slots=N
     q_out [n][Hq][hd] of the same type (token stride free), k_cache / v_cache bfloat16 [B][Hkv][max_seq][hd]
     (one layer), positions / rows / slots int32 [n], inv_freq float64 [rot / 2], q_norm / k_norm bfloat16 [hd]."""
     import torch
-    dev, dt = qkv.device, _io_dtype(qkv, "qkv")
+    bf, i32, dt = torch.bfloat16, torch.int32, _io_dtype(qkv, "qkv")
     if k_cache.dim() != 4 or q_out.dim() != 3 or qkv.dim() != 2 or inv_freq.dim() != 1:
         _bad("qkv, q_out, k_cache, inv_freq must have 2, 3, 4, 1 dimensions")
     B, Hkv, S, hd = k_cache.shape
     n, Hq, _ = q_out.shape
-    half = inv_freq.shape[0]
-    bf, i32 = torch.bfloat16, torch.int32
-    a = mk_rope_args(n, Hq, Hkv, hd, 2 * half, 1 if interleaved else 0, dt, B, S, eps, mscale, qkv.stride(0),
-                     q_out.stride(0), _need(qkv, "qkv", qkv.dtype, (n, (Hq + 2 * Hkv) * hd), dev, False),
-                     _need(q_out, "q_out", qkv.dtype, (n, Hq, hd), dev, False),
-                     _need(k_cache, "k_cache", bf, (B, Hkv, S, hd), dev),
-                     _need(v_cache, "v_cache", bf, (B, Hkv, S, hd), dev),
-                     _need(positions, "positions", i32, (n,), dev), _need(rows, "rows", i32, (n,), dev),
-                     None if slots is None else _need(slots, "slots", i32, (n,), dev),
-                     _need(inv_freq, "inv_freq", torch.float64, (half,), dev),
-                     None if q_norm is None else _need(q_norm, "q_norm", bf, (hd,), dev),
-                     None if k_norm is None else _need(k_norm, "k_norm", bf, (hd,), dev))
+    half, d, per_token = inv_freq.shape[0], qkv.get_device(), (n,)
+    if not (qkv.shape == (n, (Hq + 2 * Hkv) * hd) and q_out.shape == (n, Hq, hd) and q_out.dtype is qkv.dtype
+            and k_cache.dtype is bf and v_cache.dtype is bf and v_cache.shape == k_cache.shape
+            and positions.dtype is i32 and rows.dtype is i32 and positions.shape == per_token
+            and rows.shape == per_token and inv_freq.dtype is torch.float64
+            and q_out.get_device() == k_cache.get_device() == v_cache.get_device() == positions.get_device()
+            == rows.get_device() == inv_freq.get_device() == d and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and positions.is_contiguous() and rows.is_contiguous()
+            and inv_freq.is_contiguous()):
+        for t, what, dtype, shape, dense in (
+                (qkv, "qkv", qkv.dtype, (n, (Hq + 2 * Hkv) * hd), False), (q_out, "q_out", qkv.dtype, (n, Hq, hd), False),
+                (k_cache, "k_cache", bf, (B, Hkv, S, hd), True), (v_cache, "v_cache", bf, (B, Hkv, S, hd), True),
+                (positions, "positions", i32, per_token, True), (rows, "rows", i32, per_token, True),
+                (inv_freq, "inv_freq", torch.float64, (half,), True)):
+            _need(t, what, dtype, shape, qkv, dense)
+    for t, what, dtype, shape in ((slots, "slots", i32, per_token), (q_norm, "q_norm", bf, (hd,)),
+                                  (k_norm, "k_norm", bf, (hd,))):
+        if t is not None:
+            _need(t, what, dtype, shape, qkv)
     if n == 0:
         return
-    if qkv.stride(1) != 1 or q_out.stride(2) != 1 or q_out.stride(1) != hd:
+    ts, qs = qkv.stride(), q_out.stride()
+    if ts[1] != 1 or qs[2] != 1 or (Hq > 1 and qs[1] != hd):
         _bad("the heads of a token must be contiguous in qkv and q_out")
-    L = load()
-    _run_on(dev, stream, lambda s: L.mk_rope_append(ctypes.byref(a), s))
+    width = (Hq + 2 * Hkv) * hd
+    rec = _ROPE_ARGS.pack(n, Hq, Hkv, hd, 2 * half, 1 if interleaved else 0, dt, B, S, eps, mscale,
+                          ts[0] if n > 1 else width, qs[0] if n > 1 else Hq * hd, qkv.data_ptr(), q_out.data_ptr(),
+                          k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(), rows.data_ptr(),
+                          0 if slots is None else slots.data_ptr(), inv_freq.data_ptr(),
+                          0 if q_norm is None else q_norm.data_ptr(), 0 if k_norm is None else k_norm.data_ptr())
+    _run_on(qkv, stream, load().mk_rope_append, rec)
 
 
 def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None = None, counts=None, slots=None,
-                   max_len: int = 0, stream=None) -> None:
+                   max_len: int = 0, status=None, stream=None) -> None:
     """mk_tree_attention on CUDA tensors: q and out [B][T][Hq][hd] float32 or bfloat16 (batch and node strides
     free), k_cache / v_cache bfloat16 [slots][Hkv][max_seq][hd] (one layer), lengths / counts / slots int32 [B],
-    masks int64 [B][T] (the 64 bits of the ancestor mask). scale defaults to 1 / sqrt(hd)."""
+    masks int64 [B][T] (the 64 bits of the ancestor mask). scale defaults to 1 / sqrt(hd). status: int32 [1]
+    (zeroed by the caller) that becomes 1 if a bounded in-kernel wait ran out. The workspace of long caches comes
+    from torch's allocator, on the call's stream."""
     import torch
-    dev, dt = q.device, _io_dtype(q, "q")
+    bf, i32, i64, dt = torch.bfloat16, torch.int32, torch.int64, _io_dtype(q, "q")
     if q.dim() != 4 or k_cache.dim() != 4:
         _bad("q and k_cache must have 4 dimensions")
     B, T, Hq, hd = q.shape
     n_slots, Hkv, S, _ = k_cache.shape
-    bf, i32 = torch.bfloat16, torch.int32
-    qs, os = q.stride(), out.stride()
-    a = mk_tree_args(B, T, Hq, Hkv, hd, dt, n_slots, S, int(max_len), hd ** -0.5 if scale is None else scale,
-                     qs[0] if B > 1 else 0, qs[1] if T > 1 else Hq * hd, os[0] if B > 1 else 0,
-                     os[1] if T > 1 else Hq * hd, _need(q, "q", q.dtype, (B, T, Hq, hd), dev, False),
-                     _need(out, "out", q.dtype, (B, T, Hq, hd), dev, False),
-                     _need(k_cache, "k_cache", bf, (n_slots, Hkv, S, hd), dev),
-                     _need(v_cache, "v_cache", bf, (n_slots, Hkv, S, hd), dev),
-                     _need(lengths, "lengths", i32, (B,), dev),
-                     None if counts is None else _need(counts, "counts", i32, (B,), dev),
-                     None if slots is None else _need(slots, "slots", i32, (B,), dev),
-                     _need(masks, "masks", torch.int64, (B, T), dev))
+    d, per_seq = q.get_device(), (B,)
+    if not (out.dtype is q.dtype and out.shape == q.shape and k_cache.dtype is bf and v_cache.dtype is bf
+            and k_cache.shape[3] == hd and v_cache.shape == k_cache.shape and lengths.dtype is i32
+            and lengths.shape == per_seq and masks.dtype is i64 and masks.shape == (B, T)
+            and out.get_device() == k_cache.get_device() == v_cache.get_device() == lengths.get_device()
+            == masks.get_device() == d and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and lengths.is_contiguous() and masks.is_contiguous()):
+        for t, what, dtype, shape, dense in (
+                (out, "out", q.dtype, (B, T, Hq, hd), False), (k_cache, "k_cache", bf, (n_slots, Hkv, S, hd), True),
+                (v_cache, "v_cache", bf, (n_slots, Hkv, S, hd), True), (lengths, "lengths", i32, per_seq, True),
+                (masks, "masks", i64, (B, T), True)):
+            _need(t, what, dtype, shape, q, dense)
+    for t, what, shape in ((counts, "counts", per_seq), (slots, "slots", per_seq), (status, "status", (1,))):
+        if t is not None:
+            _need(t, what, i32, shape, q)
     if slots is None and B > n_slots:
         _bad(f"{B} sequences for {n_slots} cache slots")
     if B == 0:
         return
+    qs, os = q.stride(), out.stride()
     if qs[3] != 1 or os[3] != 1 or (Hq > 1 and (qs[2] != hd or os[2] != hd)):
         _bad("the heads of a node must be contiguous in q and out")
-    L = load()
-    _run_on(dev, stream, lambda s: L.mk_tree_attention(ctypes.byref(a), s))
+    row = Hq * hd
+    rec = [B, T, Hq, Hkv, hd, dt, n_slots, S, max_len, hd ** -0.5 if scale is None else scale, qs[0] if B > 1 else 0,
+           qs[1] if T > 1 else row, os[0] if B > 1 else 0, os[1] if T > 1 else row, q.data_ptr(), out.data_ptr(),
+           k_cache.data_ptr(), v_cache.data_ptr(), lengths.data_ptr(), 0 if counts is None else counts.data_ptr(),
+           0 if slots is None else slots.data_ptr(), masks.data_ptr(), 0, 0,
+           0 if status is None else status.data_ptr()]
+    L, work = load(), None
+    if (max_len or S) >= 4096 and d >= 0:  # shorter caches are never split over more than a cluster
+        with torch.cuda.device(d):
+            n = L.mk_tree_attention_workspace(_TREE_ARGS.pack(*rec))
+            if n < 0:
+                check(n)
+            if n > 0:
+                if stream is None:
+                    work = torch.empty(n, dtype=torch.uint8, device=q.device)
+                else:
+                    with torch.cuda.stream(stream):
+                        work = torch.empty(n, dtype=torch.uint8, device=q.device)
+                rec[22], rec[23] = work.data_ptr(), n
+    _run_on(q, stream, L.mk_tree_attention, _TREE_ARGS.pack(*rec))
 
 
 def tree_masks(parents, masks, depths=None, counts=None, stream=None) -> None:
     """mk_tree_masks on CUDA tensors: parents int32 [B][T] -> masks int64 [B][T], depths int32 [B][T] or None."""
     import torch
-    dev, i32 = parents.device, torch.int32
     if parents.dim() != 2:
         _bad("parents must have 2 dimensions")
     B, T = parents.shape
-    p = (_need(parents, "parents", i32, (B, T), dev),
-         None if counts is None else _need(counts, "counts", i32, (B,), dev), B, T,
-         _need(masks, "masks", torch.int64, (B, T), dev),
-         None if depths is None else _need(depths, "depths", i32, (B, T), dev))
-    L = load()
-    _run_on(dev, stream, lambda s: L.mk_tree_masks(*p, s))
+    _need(parents, "parents", torch.int32, (B, T), parents)
+    _need(masks, "masks", torch.int64, (B, T), parents)
+    if depths is not None:
+        _need(depths, "depths", torch.int32, (B, T), parents)
+    if counts is not None:
+        _need(counts, "counts", torch.int32, (B,), parents)
+    _run_on(parents, stream, load().mk_tree_masks, parents.data_ptr(), None if counts is None else counts.data_ptr(), B,
+            T, masks.data_ptr(), None if depths is None else depths.data_ptr())
 
 
 def tree_accept(tokens, parents, draws):
@@ -429,34 +479,40 @@ def tree_accept(tokens, parents, draws):
     return list(path[:c])
 
 
-def _caches(k, v):
+def _cache_shape(k, v):
+    """(L, B, Hkv, max_seq, hd) of two whole caches."""
     import torch
     if k.dim() != 5:
         _bad("the caches must have 5 dimensions")
-    shape = tuple(k.shape)
-    return (_need(k, "k", torch.bfloat16, shape, k.device), _need(v, "v", torch.bfloat16, shape, k.device), *shape)
+    shape = k.shape
+    if not (k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and v.shape == shape
+            and k.get_device() == v.get_device() and k.is_contiguous() and v.is_contiguous()):
+        _need(k, "k", torch.bfloat16, shape, k)
+        _need(v, "v", torch.bfloat16, shape, k)
+    return shape
 
 
 def kv_compact(k, v, starts, nodes, counts, stream=None) -> None:
     """mk_kv_compact on CUDA tensors: k / v bfloat16 [L][B][Hkv][max_seq][hd], starts / counts int32 [B], nodes
     int32 [B][n]: rows starts[b] + nodes[b][i] move to starts[b] + i."""
     import torch
-    c, dev, i32 = _caches(k, v), k.device, torch.int32
-    B, n = k.shape[1], nodes.shape[-1]
-    p = (_need(starts, "starts", i32, (B,), dev), _need(nodes, "nodes", i32, (B, n), dev),
-         _need(counts, "counts", i32, (B,), dev))
-    L = load()
-    _run_on(dev, stream, lambda s: L.mk_kv_compact(*c, n, *p, s))
+    L, B, Hkv, S, hd = _cache_shape(k, v)
+    n = nodes.shape[-1] if nodes.dim() == 2 else 0
+    for t, what, shape in ((starts, "starts", (B,)), (nodes, "nodes", (B, n)), (counts, "counts", (B,))):
+        _need(t, what, torch.int32, shape, k)
+    _run_on(k, stream, load().mk_kv_compact, k.data_ptr(), v.data_ptr(), L, B, Hkv, S, hd, n, starts.data_ptr(),
+            nodes.data_ptr(), counts.data_ptr())
 
 
 def kv_reorder(k, v, sources, lengths, stream=None) -> None:
     """mk_kv_reorder on CUDA tensors: k / v bfloat16 [L][B][Hkv][max_seq][hd], sources / lengths int32 [B]: rows
     [0, lengths[b]) of slot b become slot sources[b]'s."""
     import torch
-    c, dev, i32 = _caches(k, v), k.device, torch.int32
-    p = (_need(sources, "sources", i32, (k.shape[1],), dev), _need(lengths, "lengths", i32, (k.shape[1],), dev))
-    L = load()
-    _run_on(dev, stream, lambda s: L.mk_kv_reorder(*c, *p, s))
+    L, B, Hkv, S, hd = _cache_shape(k, v)
+    _need(sources, "sources", torch.int32, (B,), k)
+    _need(lengths, "lengths", torch.int32, (B,), k)
+    _run_on(k, stream, load().mk_kv_reorder, k.data_ptr(), v.data_ptr(), L, B, Hkv, S, hd, sources.data_ptr(),
+            lengths.data_ptr())
 
 
 class Megakernel:

@@ -50,10 +50,17 @@ struct TreeArgs {
     const uint16_t *kc, *vc;
     const int32_t *lengths, *counts, *slot_of;
     const uint64_t *masks;
-    int *err;  // set to 1 if a bounded wait runs out (nullable)
+    int *err;     // set to 1 if a bounded wait runs out (nullable)
+    float *part;  // the splits' partial results (set by the launch from work)
+    float *work;  // the caller's workspace (nullable)
+    int64_t work_floats;
 };
 
 cudaError_t tree_attention_launch(const TreeArgs &a, int hd, bool f32, int max_len, int n_sm, cudaStream_t s);
+
+// Floats of workspace (TreeArgs::work) with which a call splits long caches
+// over more than a cluster's CTAs; 0: it would not use any.
+cudaError_t tree_attention_work_floats(const TreeArgs &a, int hd, bool f32, int max_len, int n_sm, int64_t *floats);
 
 cudaError_t tree_masks_launch(const int32_t *parents, const int32_t *counts, int B, int T, uint64_t *masks,
                               int32_t *depths, cudaStream_t s);

@@ -14,6 +14,7 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "mk_internal.h"
 #include "mk_ops.h"
@@ -84,51 +85,135 @@ bool cache_map(CUtensorMap *map, const void *cache, int planes, int max_seq, int
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How a call splits the cache rows of its (row tile, sequence, kv head) units:
+// S CTAs of one cluster, or (ws) S CTAs whose partial results go through the
+// workspace.
+struct Plan {
+    int S;
+    bool ws;
+};
+
 template <int HD, int TERMS, int NR>
-cudaError_t launch(const TreeArgs &a, int max_len, int n_sm, cudaStream_t s) {
+cudaError_t configure() {
+    // (function attributes are per device: set once for each)
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(tree_attention<HD, TERMS, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             AttnShape<HD, TERMS, NR>::kSmem);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
+}
+
+void launch_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 grid, int smem, int cluster,
+                   cudaStream_t s) {
+    cfg = cudaLaunchConfig_t{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+}
+
+// Clusters of 2^k CTAs that the device holds at once (asked of the runtime once).
+template <int HD, int TERMS, int NR>
+int active_clusters(int k, int n_sm) {
     using C = AttnShape<HD, TERMS, NR>;
+    static std::atomic<int> known[4];
+    int n = known[k].load(std::memory_order_relaxed);
+    if (n) return n;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    launch_config(cfg, attr, dim3(1 << k, n_sm * 4), C::kSmem, 1 << k, nullptr);
+    if (cudaOccupancyMaxActiveClusters(&n, tree_attention<HD, TERMS, NR>, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        n = 1;
+    }
+    known[k].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// The split with the least estimated time: waves of resident CTAs x (tiles of
+// a split + a fixed part), in microseconds.
+template <int HD, int TERMS, int NR>
+Plan plan(const TreeArgs &a, int max_len, int n_sm, bool ws) {
+    const int row_tiles = (a.T * (a.Hq / a.Hkv) + NR - 1) / NR;
+    const int64_t units = (int64_t)a.B * a.Hkv * row_tiles;
+    const int tiles = (std::min((int64_t)max_len + a.T, (int64_t)a.max_seq) + kTile - 1) / kTile;
+    const double tile = NR >= 64 ? 0.9 : 0.5, fixed = 3.0;
+    Plan best{1, false};
+    double least = 1e30;
+    for (int k = 0; k < 4 && (1 << k) <= tiles; ++k) {
+        const int S = 1 << k, at_once = active_clusters<HD, TERMS, NR>(k, n_sm);
+        const double cost = (double)((units + at_once - 1) / at_once) * (((tiles + S - 1) / S) * tile + fixed) + 0.2 * k;
+        if (cost < least) least = cost, best = Plan{S, false};
+    }
+    if (ws) {
+        const int64_t room = active_clusters<HD, TERMS, NR>(0, n_sm) / std::max<int64_t>(units, 1);
+        const int S = (int)std::min<int64_t>(std::min<int64_t>(room, kMaxSplits), tiles / 2);
+        if (S > 1 && ((tiles + S - 1) / S) * tile + fixed + 4.0 < least) best = Plan{S, true};
+    }
+    return best;
+}
+
+template <int HD, int TERMS, int NR>
+cudaError_t launch(TreeArgs a, int max_len, int n_sm, cudaStream_t s, int64_t *want) {
+    using C = AttnShape<HD, TERMS, NR>;
+    const int row_tiles = (a.T * (a.Hq / a.Hkv) + NR - 1) / NR;
+    cudaError_t e = configure<HD, TERMS, NR>();
+    if (e != cudaSuccess) return e;
+    Plan p = plan<HD, TERMS, NR>(a, max_len, n_sm, want || a.work);
+    const int64_t need = p.ws ? (int64_t)a.B * a.Hkv * row_tiles * p.S * part_floats(NR, HD) : 0;
+    if (want) {
+        *want = need;
+        return cudaSuccess;
+    }
+    if (need > a.work_floats) p = plan<HD, TERMS, NR>(a, max_len, n_sm, false);
+    a.part = p.ws ? a.work : nullptr;
     CUtensorMap kmap, vmap;
     if (!cache_map(&kmap, a.kc, a.slots * a.Hkv, a.max_seq, HD) ||
         !cache_map(&vmap, a.vc, a.slots * a.Hkv, a.max_seq, HD))
         return cudaErrorInvalidValue;
-    const auto kernel = tree_attention<HD, TERMS, NR>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    const int row_tiles = (a.T * (a.Hq / a.Hkv) + NR - 1) / NR;
-    const int64_t units = (int64_t)a.B * a.Hkv * row_tiles;
-    const int tiles = (std::min(max_len + a.T, a.max_seq) + kTile - 1) / kTile;
-    int S = 1;
-    while (S < 16 && units * S * 2 <= n_sm * (HD == 64 ? 2 : 1) && S * 2 <= tiles) S *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(S, a.B * a.Hkv, row_tiles);
-    cfg.blockDim = dim3(kAttnThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = s;
+    cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = S;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, kmap, vmap, a);
+    launch_config(cfg, attr, dim3(p.S, a.B * a.Hkv, row_tiles), C::kSmem, p.ws ? 1 : p.S, s);
+    e = cudaLaunchKernelEx(&cfg, tree_attention<HD, TERMS, NR>, kmap, vmap, a);
+    if (e != cudaSuccess || !p.ws) return e;
+    tree_join<HD, TERMS, NR><<<dim3(row_tiles, a.B * a.Hkv, (NR * HD / 4 + 255) / 256), 256, 0, s>>>(a, p.S);
+    return cudaGetLastError();
+}
+
+// The rows of a CTA: the fewest of 16, 32 (64 with one term) that hold the
+// tree's, else the most (fewer passes over the cache).
+cudaError_t dispatch(const TreeArgs &a, int hd, bool f32, int max_len, int n_sm, cudaStream_t s, int64_t *want) {
+    const int rows = a.T * (a.Hq / a.Hkv);
+    if (f32) {
+        if (hd == 64)
+            return rows <= 16 ? launch<64, 3, 16>(a, max_len, n_sm, s, want) : launch<64, 3, 32>(a, max_len, n_sm, s, want);
+        return rows <= 16 ? launch<128, 3, 16>(a, max_len, n_sm, s, want) : launch<128, 3, 32>(a, max_len, n_sm, s, want);
+    }
+    if (hd == 64)
+        return rows <= 16   ? launch<64, 1, 16>(a, max_len, n_sm, s, want)
+               : rows <= 32 ? launch<64, 1, 32>(a, max_len, n_sm, s, want)
+                            : launch<64, 1, 64>(a, max_len, n_sm, s, want);
+    return rows <= 16   ? launch<128, 1, 16>(a, max_len, n_sm, s, want)
+           : rows <= 32 ? launch<128, 1, 32>(a, max_len, n_sm, s, want)
+                        : launch<128, 1, 64>(a, max_len, n_sm, s, want);
 }
 
 }  // namespace
 
 cudaError_t tree_attention_launch(const TreeArgs &a, int hd, bool f32, int max_len, int n_sm, cudaStream_t s) {
-    const int rows = a.T * (a.Hq / a.Hkv);
-    if (f32) {
-        if (hd == 64) return rows <= 16 ? launch<64, 3, 16>(a, max_len, n_sm, s) : launch<64, 3, 32>(a, max_len, n_sm, s);
-        return rows <= 16 ? launch<128, 3, 16>(a, max_len, n_sm, s) : launch<128, 3, 32>(a, max_len, n_sm, s);
-    }
-    if (hd == 64)
-        return rows <= 16   ? launch<64, 1, 16>(a, max_len, n_sm, s)
-               : rows <= 32 ? launch<64, 1, 32>(a, max_len, n_sm, s)
-                            : launch<64, 1, 64>(a, max_len, n_sm, s);
-    return rows <= 16   ? launch<128, 1, 16>(a, max_len, n_sm, s)
-           : rows <= 32 ? launch<128, 1, 32>(a, max_len, n_sm, s)
-                        : launch<128, 1, 64>(a, max_len, n_sm, s);
+    return dispatch(a, hd, f32, max_len, n_sm, s, nullptr);
+}
+
+cudaError_t tree_attention_work_floats(const TreeArgs &a, int hd, bool f32, int max_len, int n_sm, int64_t *floats) {
+    return dispatch(a, hd, f32, max_len, n_sm, nullptr, floats);
 }
 
 cudaError_t tree_masks_launch(const int32_t *parents, const int32_t *counts, int B, int T, uint64_t *masks,
@@ -139,7 +224,9 @@ cudaError_t tree_masks_launch(const int32_t *parents, const int32_t *counts, int
 
 }  // namespace mkops
 
-extern "C" int mk_tree_attention(const mk_tree_args *a, void *stream) {
+namespace {
+
+int check_tree(const mk_tree_args *a) {
     using mkint::set_error;
     if (!a || !a->q || !a->out || !a->k_cache || !a->v_cache || !a->lengths || !a->masks)
         return set_error(MK_ERR_INVALID_ARG, "mk_tree_attention: a required pointer is NULL");
@@ -168,11 +255,12 @@ extern "C" int mk_tree_attention(const mk_tree_args *a, void *stream) {
          reinterpret_cast<uintptr_t>(a->k_cache) | reinterpret_cast<uintptr_t>(a->v_cache)) & 15u ||
         reinterpret_cast<uintptr_t>(a->masks) & 7u)
         return set_error(MK_ERR_INVALID_ARG, "mk_tree_attention: a pointer is not aligned");
-    int dev = 0, n_sm = 0;
-    if (a->batch == 0) return MK_OK;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return mkops::cuda_error(e, "mk_tree_attention");
+    if (a->workspace_bytes < 0 || (a->workspace && (reinterpret_cast<uintptr_t>(a->workspace) & 15u)))
+        return set_error(MK_ERR_INVALID_ARG, "mk_tree_attention: bad workspace");
+    return MK_OK;
+}
+
+mkops::TreeArgs tree_of(const mk_tree_args *a) {
     mkops::TreeArgs t{};
     t.B = a->batch, t.T = a->nodes, t.Hq = a->n_heads, t.Hkv = a->n_kv_heads, t.slots = a->slots;
     t.max_seq = a->max_seq, t.scale = a->scale;
@@ -181,9 +269,41 @@ extern "C" int mk_tree_attention(const mk_tree_args *a, void *stream) {
     t.q = a->q, t.out = a->out;
     t.kc = static_cast<const uint16_t *>(a->k_cache), t.vc = static_cast<const uint16_t *>(a->v_cache);
     t.lengths = a->lengths, t.counts = a->counts, t.slot_of = a->slot_of, t.masks = a->masks;
-    e = mkops::tree_attention_launch(t, a->head_dim, a->dtype == MK_F32, a->max_len ? a->max_len : a->max_seq, n_sm,
-                                     static_cast<cudaStream_t>(stream));
+    t.work = static_cast<float *>(a->workspace);
+    t.work_floats = a->workspace ? a->workspace_bytes / 4 : 0;
+    t.err = a->status;
+    return t;
+}
+
+cudaError_t device_sms(int *n_sm) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e == cudaSuccess ? cudaDeviceGetAttribute(n_sm, cudaDevAttrMultiProcessorCount, dev) : e;
+}
+
+}  // namespace
+
+extern "C" int mk_tree_attention(const mk_tree_args *a, void *stream) {
+    const int rc = check_tree(a);
+    if (rc || a->batch == 0) return rc;
+    int n_sm = 0;
+    cudaError_t e = device_sms(&n_sm);
+    if (e == cudaSuccess)
+        e = mkops::tree_attention_launch(tree_of(a), a->head_dim, a->dtype == MK_F32,
+                                         a->max_len ? a->max_len : a->max_seq, n_sm, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MK_OK : mkops::cuda_error(e, "mk_tree_attention");
+}
+
+extern "C" int64_t mk_tree_attention_workspace(const mk_tree_args *a) {
+    const int rc = check_tree(a);
+    if (rc || a->batch == 0) return rc;
+    int n_sm = 0;
+    int64_t floats = 0;
+    cudaError_t e = device_sms(&n_sm);
+    if (e == cudaSuccess)
+        e = mkops::tree_attention_work_floats(tree_of(a), a->head_dim, a->dtype == MK_F32,
+                                              a->max_len ? a->max_len : a->max_seq, n_sm, &floats);
+    return e == cudaSuccess ? floats * 4 : mkops::cuda_error(e, "mk_tree_attention_workspace");
 }
 
 extern "C" int mk_tree_masks(const int32_t *d_parents, const int32_t *d_counts, int32_t batch, int32_t nodes,

@@ -405,9 +405,9 @@ int mk_twell_ffn(const void *d_w_gate, const void *d_w_up, const void *d_w_down_
  * move up behind the committed ones (mk_kv_compact); mk_kv_reorder copies,
  * forks and exchanges whole sequences. They work on one layer's (or, the
  * last two, all layers') cache in mk_kv_cache's layout, on the current
- * device, with no handle and no workspace: one launch each, asynchronous on
- * `stream`, safe in several streams at once and in captured graphs as long as
- * the calls touch different memory. Device arrays are read when the kernel
+ * device, with no handle, asynchronous on `stream`, safe in several streams at
+ * once and in captured graphs as long as the calls touch different memory
+ * (the library keeps none for them). Device arrays are read when the kernel
  * runs; what they hold is checked there, and a sequence, row or slot that
  * lies outside the cache is left alone, never followed.
  * The pages name no such operators; each declaration states its formula. */
@@ -491,7 +491,12 @@ int mk_rope_frequencies(int32_t kind, int32_t rot, double theta, double factor, 
  * used only to choose the launch; results are right if a length exceeds it.
  * lengths outside [0, max_seq] and counts past the nodes or the cache's end
  * are cut to them. out must not overlap q or the cache. Pointers 16-byte
- * aligned, strides multiples of 8 elements. */
+ * aligned, strides multiples of 8 elements.
+ * workspace (device, workspace_bytes, NULL or 16-byte aligned): scratch of
+ * this call alone, in use until it is done on the stream; with less than
+ * mk_tree_attention_workspace() asks for, the call does without. status
+ * (device int32, zeroed by the caller, or NULL) becomes 1 if a bounded
+ * in-kernel wait ran out; the rows concerned are then NaN. */
 typedef struct mk_tree_args {
     int32_t batch, nodes, n_heads, n_kv_heads, head_dim, dtype, slots, max_seq, max_len;
     float scale;
@@ -501,8 +506,17 @@ typedef struct mk_tree_args {
     const void *k_cache, *v_cache;
     const int32_t *lengths, *counts, *slot_of;
     const uint64_t *masks;
+    void *workspace;
+    int64_t workspace_bytes;
+    int32_t *status;
 } mk_tree_args;
 int mk_tree_attention(const mk_tree_args *args, void *stream);
+
+/* Bytes of workspace that make mk_tree_attention split these sequences' rows
+ * over more CTAs than one cluster holds (long caches, few sequences); 0 where
+ * it would not use any. Reads the sizes and max_len, follows no pointer.
+ * Returns a negative mk_status for arguments that mk_tree_attention refuses. */
+int64_t mk_tree_attention_workspace(const mk_tree_args *args);
 
 /* masks[b][t] (bit i: node i is t or an ancestor of t) and, if depths is not
  * NULL, depths[b][t] (0 for a root) of the trees d_parents (device int32

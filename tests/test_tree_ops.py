@@ -64,15 +64,26 @@ def tree_args(**kw):
     (dict(q_token_stride=516), -1), (dict(out_token_stride=504), -1), (dict(q_batch_stride=-8), -1),
     (dict(out_batch_stride=4), -1), (dict(q=FAKE + 8), -1), (dict(out=FAKE + 8), -1), (dict(k_cache=FAKE + 2), -1),
     (dict(v_cache=FAKE + 8), -1), (dict(masks=FAKE + 4), -1), (dict(batch=40000), -4),
+    (dict(workspace=FAKE + 4), -1), (dict(workspace_bytes=-1), -1),
 ])
 def test_tree_attention_refuses(lib, bad, code):
+    assert lib.mk_tree_attention_workspace(ctypes.byref(tree_args(**bad))) == code
     assert lib.mk_tree_attention(ctypes.byref(tree_args(**bad)), None) == code
     assert b"mk_tree_attention" in lib.mk_last_error()
 
 
 def test_tree_attention_of_no_sequences_does_nothing(lib):
     assert lib.mk_tree_attention(ctypes.byref(tree_args(batch=0)), None) == 0
-    assert lib.mk_tree_attention(None, None) == -1
+    assert lib.mk_tree_attention_workspace(ctypes.byref(tree_args(batch=0))) == 0
+    assert lib.mk_tree_attention(None, None) == -1 and lib.mk_tree_attention_workspace(None) == -1
+
+
+def test_packed_records_have_the_structures_layout():
+    for packed, cls in ((_lib._ROPE_ARGS, _lib.mk_rope_args), (_lib._TREE_ARGS, _lib.mk_tree_args)):
+        assert packed.size == ctypes.sizeof(cls)
+        values = list(range(1, 1 + len(cls._fields_)))
+        got = cls.from_buffer_copy(packed.pack(*values))
+        assert [getattr(got, f) for f, _ in cls._fields_] == values
 
 
 def test_cache_moves_refuse(lib):
