@@ -93,15 +93,31 @@ struct Plan {
     bool ws;
 };
 
-template <int HD, int TERMS, int NR>
+// The two kernels by what their launch needs.
+template <int HD_, int TERMS_, int NR_>
+struct Few {
+    static constexpr int HD = HD_, TERMS = TERMS_, NR = NR_, kSmem = AttnShape<HD, TERMS, NR>::kSmem;
+    static constexpr double kTileUs = NR >= 64 ? 0.9 : 0.5;
+    static auto fn() { return tree_attention<HD, TERMS, NR>; }
+};
+template <int HD_, int TERMS_>
+struct Many {
+    static constexpr int HD = HD_, TERMS = TERMS_, NR = kRows, kSmem = RowShape<HD, TERMS>::kSmem;
+    static constexpr double kTileUs = TERMS == 1 ? 0.8 : 1.5;
+    static auto fn() { return tree_attention_rows<HD, TERMS>; }
+};
+
+template <class K>
 cudaError_t configure() {
     // (function attributes are per device: set once for each)
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1))) return e;
-    e = cudaFuncSetAttribute(tree_attention<HD, TERMS, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             AttnShape<HD, TERMS, NR>::kSmem);
+    e = cudaFuncSetAttribute(K::fn(), cudaFuncAttributeMaxDynamicSharedMemorySize, K::kSmem);
+    // (two CTAs an SM need the whole carveout as shared memory)
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(K::fn(), cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
     return e;
 }
@@ -120,90 +136,93 @@ void launch_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 grid
     cfg.numAttrs = 1;
 }
 
-// Clusters of 2^k CTAs that the device holds at once (asked of the runtime once).
-template <int HD, int TERMS, int NR>
+// Clusters of 2^k CTAs that the device holds at once (asked of the runtime
+// once; its count of clusters is for one CTA an SM).
+template <class K>
 int active_clusters(int k, int n_sm) {
-    using C = AttnShape<HD, TERMS, NR>;
     static std::atomic<int> known[4];
     int n = known[k].load(std::memory_order_relaxed);
     if (n) return n;
+    int per_sm = 1;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
-    launch_config(cfg, attr, dim3(1 << k, n_sm * 4), C::kSmem, 1 << k, nullptr);
-    if (cudaOccupancyMaxActiveClusters(&n, tree_attention<HD, TERMS, NR>, &cfg) != cudaSuccess || n < 1) {
+    launch_config(cfg, attr, dim3(1 << k, n_sm * 4), K::kSmem, 1 << k, nullptr);
+    if (cudaOccupancyMaxActiveClusters(&n, K::fn(), &cfg) != cudaSuccess || n < 1 ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, K::fn(), kAttnThreads, K::kSmem) != cudaSuccess) {
         (void)cudaGetLastError();
         n = 1;
     }
+    n *= std::max(1, per_sm);
     known[k].store(n, std::memory_order_relaxed);
     return n;
 }
 
 // The split with the least estimated time: waves of resident CTAs x (tiles of
 // a split + a fixed part), in microseconds.
-template <int HD, int TERMS, int NR>
+template <class K>
 Plan plan(const TreeArgs &a, int max_len, int n_sm, bool ws) {
-    const int row_tiles = (a.T * (a.Hq / a.Hkv) + NR - 1) / NR;
+    const int row_tiles = (a.T * (a.Hq / a.Hkv) + K::NR - 1) / K::NR;
     const int64_t units = (int64_t)a.B * a.Hkv * row_tiles;
     const int tiles = (std::min((int64_t)max_len + a.T, (int64_t)a.max_seq) + kTile - 1) / kTile;
-    const double tile = NR >= 64 ? 0.9 : 0.5, fixed = 3.0;
+    const double fixed = 3.0;
     Plan best{1, false};
     double least = 1e30;
     for (int k = 0; k < 4 && (1 << k) <= tiles; ++k) {
-        const int S = 1 << k, at_once = active_clusters<HD, TERMS, NR>(k, n_sm);
-        const double cost = (double)((units + at_once - 1) / at_once) * (((tiles + S - 1) / S) * tile + fixed) + 0.2 * k;
+        const int S = 1 << k, at_once = active_clusters<K>(k, n_sm);
+        const double cost =
+            (double)((units + at_once - 1) / at_once) * (((tiles + S - 1) / S) * K::kTileUs + fixed) + 0.2 * k;
         if (cost < least) least = cost, best = Plan{S, false};
     }
     if (ws) {
-        const int64_t room = active_clusters<HD, TERMS, NR>(0, n_sm) / std::max<int64_t>(units, 1);
-        const int S = (int)std::min<int64_t>(std::min<int64_t>(room, kMaxSplits), tiles / 2);
-        if (S > 1 && ((tiles + S - 1) / S) * tile + fixed + 4.0 < least) best = Plan{S, true};
+        const int64_t room = active_clusters<K>(0, n_sm) / std::max<int64_t>(units, 1);
+        const int S = (int)std::min<int64_t>(std::min<int64_t>(room, max_splits(K::NR)), tiles / 2);
+        if (S > 1 && ((tiles + S - 1) / S) * K::kTileUs + fixed + 4.0 < least) best = Plan{S, true};
     }
     return best;
 }
 
-template <int HD, int TERMS, int NR>
+template <class K>
 cudaError_t launch(TreeArgs a, int max_len, int n_sm, cudaStream_t s, int64_t *want) {
-    using C = AttnShape<HD, TERMS, NR>;
-    const int row_tiles = (a.T * (a.Hq / a.Hkv) + NR - 1) / NR;
-    cudaError_t e = configure<HD, TERMS, NR>();
+    const int row_tiles = (a.T * (a.Hq / a.Hkv) + K::NR - 1) / K::NR;
+    cudaError_t e = configure<K>();
     if (e != cudaSuccess) return e;
-    Plan p = plan<HD, TERMS, NR>(a, max_len, n_sm, want || a.work);
-    const int64_t need = p.ws ? (int64_t)a.B * a.Hkv * row_tiles * p.S * part_floats(NR, HD) : 0;
+    Plan p = plan<K>(a, max_len, n_sm, want || a.work);
+    const int64_t need = p.ws ? (int64_t)a.B * a.Hkv * row_tiles * p.S * part_floats(K::NR, K::HD) : 0;
     if (want) {
         *want = need;
         return cudaSuccess;
     }
-    if (need > a.work_floats) p = plan<HD, TERMS, NR>(a, max_len, n_sm, false);
+    if (need > a.work_floats) p = plan<K>(a, max_len, n_sm, false);
     a.part = p.ws ? a.work : nullptr;
     CUtensorMap kmap, vmap;
-    if (!cache_map(&kmap, a.kc, a.slots * a.Hkv, a.max_seq, HD) ||
-        !cache_map(&vmap, a.vc, a.slots * a.Hkv, a.max_seq, HD))
+    if (!cache_map(&kmap, a.kc, a.slots * a.Hkv, a.max_seq, K::HD) ||
+        !cache_map(&vmap, a.vc, a.slots * a.Hkv, a.max_seq, K::HD))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
-    launch_config(cfg, attr, dim3(p.S, a.B * a.Hkv, row_tiles), C::kSmem, p.ws ? 1 : p.S, s);
-    e = cudaLaunchKernelEx(&cfg, tree_attention<HD, TERMS, NR>, kmap, vmap, a);
+    launch_config(cfg, attr, dim3(p.S, a.B * a.Hkv, row_tiles), K::kSmem, p.ws ? 1 : p.S, s);
+    e = cudaLaunchKernelEx(&cfg, K::fn(), kmap, vmap, a);
     if (e != cudaSuccess || !p.ws) return e;
-    tree_join<HD, TERMS, NR><<<dim3(row_tiles, a.B * a.Hkv, (NR * HD / 4 + 255) / 256), 256, 0, s>>>(a, p.S);
+    tree_join<K::HD, K::TERMS, K::NR>
+        <<<dim3(row_tiles, a.B * a.Hkv, (K::NR * K::HD / 4 + 255) / 256), 256, 0, s>>>(a, p.S);
     return cudaGetLastError();
 }
 
-// The rows of a CTA: the fewest of 16, 32 (64 with one term) that hold the
-// tree's, else the most (fewer passes over the cache).
-cudaError_t dispatch(const TreeArgs &a, int hd, bool f32, int max_len, int n_sm, cudaStream_t s, int64_t *want) {
+// The kernel by the tree's rows of a kv head: the fewest columns of 16, 32 (64
+// with one term) that hold them, or the kernel of 128 rows.
+template <int HD, int TERMS>
+cudaError_t dispatch(const TreeArgs &a, int max_len, int n_sm, cudaStream_t s, int64_t *want) {
     const int rows = a.T * (a.Hq / a.Hkv);
-    if (f32) {
-        if (hd == 64)
-            return rows <= 16 ? launch<64, 3, 16>(a, max_len, n_sm, s, want) : launch<64, 3, 32>(a, max_len, n_sm, s, want);
-        return rows <= 16 ? launch<128, 3, 16>(a, max_len, n_sm, s, want) : launch<128, 3, 32>(a, max_len, n_sm, s, want);
-    }
-    if (hd == 64)
-        return rows <= 16   ? launch<64, 1, 16>(a, max_len, n_sm, s, want)
-               : rows <= 32 ? launch<64, 1, 32>(a, max_len, n_sm, s, want)
-                            : launch<64, 1, 64>(a, max_len, n_sm, s, want);
-    return rows <= 16   ? launch<128, 1, 16>(a, max_len, n_sm, s, want)
-           : rows <= 32 ? launch<128, 1, 32>(a, max_len, n_sm, s, want)
-                        : launch<128, 1, 64>(a, max_len, n_sm, s, want);
+    if (rows <= 16) return launch<Few<HD, TERMS, 16>>(a, max_len, n_sm, s, want);
+    if (rows <= 32) return launch<Few<HD, TERMS, 32>>(a, max_len, n_sm, s, want);
+    if constexpr (TERMS == 1)
+        if (rows <= 64) return launch<Few<HD, TERMS, 64>>(a, max_len, n_sm, s, want);
+    return launch<Many<HD, TERMS>>(a, max_len, n_sm, s, want);
+}
+
+cudaError_t dispatch(const TreeArgs &a, int hd, bool f32, int max_len, int n_sm, cudaStream_t s, int64_t *want) {
+    if (f32) return hd == 64 ? dispatch<64, 3>(a, max_len, n_sm, s, want) : dispatch<128, 3>(a, max_len, n_sm, s, want);
+    return hd == 64 ? dispatch<64, 1>(a, max_len, n_sm, s, want) : dispatch<128, 1>(a, max_len, n_sm, s, want);
 }
 
 }  // namespace
