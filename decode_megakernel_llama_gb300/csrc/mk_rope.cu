@@ -15,9 +15,11 @@
 // What bounds it: memory. Each element is read once and written once; the
 // arithmetic is a few operations an element. A CTA takes one token: its first
 // rot/2 threads form the token's sines and cosines once for all heads
-// (shared memory) while every warp's loads are already in flight; a head is
-// held by hd/4 lanes of a warp, four elements a lane, so the norm is a
-// shuffle sum and the partner of a pair is a shuffle away.
+// (shared memory) while every warp's loads of four heads (eight of 64) are
+// already in flight; a head is held by hd/4 lanes of a warp, four elements a
+// lane, so the norm is a shuffle sum and the partner of a pair a shuffle away
+// (or in shared memory, where rot/2 is no multiple of four). A few tokens are
+// spread over several CTAs each, so that no warp takes more than one round.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -62,87 +64,124 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t *p, float4 v) {
 // The value of element e of this lane's head, from the head's staged row.
 __device__ __forceinline__ float part(const float4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-template <typename T, int HD>
+// TPB tokens a CTA (1 or 4), kW / TPB warps each.
+template <typename T, int HD, int TPB>
 __global__ void __launch_bounds__(kT) rope_append(const RopeArgs a) {
     constexpr int LPH = HD / 4;    // lanes of a head
     constexpr int HPW = 32 / LPH;  // heads of a warp
-    __shared__ float2 cs[kMaxHalf];
-    __shared__ float4 stage[kT];  // a head's row, for pairs that are not whole lanes apart
+    constexpr int B = 4;           // a warp's heads in flight, HPW each
+    constexpr int WPT = kW / TPB;  // warps of a token
+    __shared__ float2 turn[TPB][kMaxHalf];
+    __shared__ float4 stage[kT];  // a head's row, for pairs that are not in one lane
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int sub = lane / LPH, j = lane % LPH;  // head of the warp, lane of the head
-    const int t = blockIdx.x, half = a.rot / 2;
-    const T *in = static_cast<const T *>(a.qkv) + (int64_t)t * a.qkv_stride;
-    T *qo = static_cast<T *>(a.q_out) + (int64_t)t * a.q_stride;
-    const int n_rows = a.Hq + 2 * a.Hkv;
-    const int slot = a.slot_of ? a.slot_of[t] : 0, row = a.rows[t];
-    const bool keep = slot >= 0 && slot < a.slots && row >= 0 && row < a.max_seq;
-    if (tid < half) {
-        // radians to turns in 64 bits; the fraction of a turn fits 32
-        const double turns = (double)a.positions[t] * a.inv_freq[tid] * 0.15915494309189533577;
-        float s, c;
-        sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-        cs[tid] = make_float2(c * a.mscale, s * a.mscale);
-    }
-    __syncthreads();
-    for (int h0 = blockIdx.y * kW * HPW + warp * HPW; h0 < n_rows; h0 += gridDim.y * kW * HPW) {
-        const int h = h0 + sub;
-        const bool live = h < n_rows;
-        float4 v = live ? load4<T>(in + h * HD + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
-        const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
-        const uint16_t *gain = is_q ? a.q_norm : (is_k ? a.k_norm : nullptr);
-        float ss = v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
+    const int t = blockIdx.x * TPB + warp / WPT, half = a.rot / 2, n_rows = a.Hq + 2 * a.Hkv;
+    const bool here = t < a.n;
+    const float2 *cs = turn[warp / WPT];
+    const T *in = static_cast<const T *>(a.qkv) + (int64_t)t * a.qkv_stride + 4 * j;
+    T *qo = static_cast<T *>(a.q_out) + (int64_t)t * a.q_stride + 4 * j;
+    const int row = here ? a.rows[t] : -1, slot = here && a.slot_of ? a.slot_of[t] : 0;
+    const int first = (blockIdx.y * WPT + warp % WPT) * HPW + sub, step = gridDim.y * WPT * HPW;
+    float4 x[B];
+    auto load = [&](int h0) {
 #pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        if (gain) {
-            const float r = 1.0f / sqrtf(ss * (1.0f / HD) + a.eps);
-            const float4 g = load4<uint16_t>(gain + 4 * j);
-            v = make_float4(v.x * r * g.x, v.y * r * g.y, v.z * r * g.z, v.w * r * g.w);
+        for (int u = 0; u < B; ++u) {
+            const int h = h0 + u * step;
+            x[u] = here && h < n_rows ? load4<T>(in + (int64_t)h * HD) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        float4 y = v;
-        if (a.interleaved) {
-            if (is_q || is_k) {
-                if (2 * j < half) {
-                    const float2 c = cs[2 * j];
-                    y.x = v.x * c.x - v.y * c.y;
-                    y.y = v.y * c.x + v.x * c.y;
-                }
-                if (2 * j + 1 < half) {
-                    const float2 c = cs[2 * j + 1];
-                    y.z = v.z * c.x - v.w * c.y;
-                    y.w = v.w * c.x + v.z * c.y;
+    };
+    load(first);
+    for (int i = tid; i < TPB * kMaxHalf; i += kT) {
+        const int tt = blockIdx.x * TPB + i / kMaxHalf, e = i % kMaxHalf;
+        if (e < half && tt < a.n) {
+            // radians to turns in 64 bits; the fraction of a turn fits 32
+            const double turns = (double)a.positions[tt] * a.inv_freq[e] * 0.15915494309189533577;
+            float s, c;
+            sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+            turn[i / kMaxHalf][e] = make_float2(c * a.mscale, s * a.mscale);
+        }
+    }
+    const bool keep = slot >= 0 && slot < a.slots && row >= 0 && row < a.max_seq;
+    __syncthreads();
+    // (a warp's loop is as long as its first head's: h - sub is the same in all lanes)
+    for (int h0 = first; here && h0 - sub < n_rows; h0 += B * step) {
+        if (h0 != first) load(h0);
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+            const int h = h0 + u * step;
+            if (h - sub >= n_rows) break;
+            float4 v = x[u];
+            const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
+            const uint16_t *gain = is_q ? a.q_norm : (is_k ? a.k_norm : nullptr);
+            if (a.q_norm || a.k_norm) {
+                float ss = v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
+#pragma unroll
+                for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+                if (gain) {
+                    const float r = 1.0f / sqrtf(ss * (1.0f / HD) + a.eps);
+                    const float4 g = load4<uint16_t>(gain + 4 * j);
+                    v = make_float4(v.x * r * g.x, v.y * r * g.y, v.z * r * g.z, v.w * r * g.w);
                 }
             }
-        } else {
-            __syncwarp();
-            stage[tid] = v;
-            __syncwarp();
-            if (is_q || is_k) {
-                const float *mine = reinterpret_cast<const float *>(stage + tid - j);
-                float o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = 4 * j + i;
-                    const float x = part(v, i);
-                    if (e < half) {
-                        const float2 c = cs[e];
-                        o[i] = x * c.x - mine[e + half] * c.y;
-                    } else if (e < a.rot) {
-                        const float2 c = cs[e - half];
-                        o[i] = x * c.x + mine[e - half] * c.y;
-                    } else {
-                        o[i] = x;
+            float4 y = v;
+            if (a.interleaved) {
+                if (is_q || is_k) {
+                    if (2 * j < half) {
+                        const float2 c = cs[2 * j];
+                        y.x = v.x * c.x - v.y * c.y;
+                        y.y = v.y * c.x + v.x * c.y;
+                    }
+                    if (2 * j + 1 < half) {
+                        const float2 c = cs[2 * j + 1];
+                        y.z = v.z * c.x - v.w * c.y;
+                        y.w = v.w * c.x + v.z * c.y;
                     }
                 }
-                y = make_float4(o[0], o[1], o[2], o[3]);
+            } else if (half % 4 == 0) {
+                // an element's partner is the same element of the lane half / 4 away
+                const int d = half / 4, from = j < d ? lane + d : lane - d;
+                const float4 o = make_float4(__shfl_sync(0xFFFFFFFFu, v.x, from), __shfl_sync(0xFFFFFFFFu, v.y, from),
+                                             __shfl_sync(0xFFFFFFFFu, v.z, from), __shfl_sync(0xFFFFFFFFu, v.w, from));
+                if ((is_q || is_k) && j < 2 * d) {
+                    const float2 *c = cs + 4 * (j < d ? j : j - d);
+                    const float sg = j < d ? -1.f : 1.f;
+                    y.x = v.x * c[0].x + sg * (o.x * c[0].y);
+                    y.y = v.y * c[1].x + sg * (o.y * c[1].y);
+                    y.z = v.z * c[2].x + sg * (o.z * c[2].y);
+                    y.w = v.w * c[3].x + sg * (o.w * c[3].y);
+                }
+            } else {
+                __syncwarp();
+                stage[tid] = v;
+                __syncwarp();
+                if (is_q || is_k) {
+                    const float *mine = reinterpret_cast<const float *>(stage + tid - j);
+                    float o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int e = 4 * j + i;
+                        const float z = part(v, i);
+                        if (e < half) {
+                            const float2 c = cs[e];
+                            o[i] = z * c.x - mine[e + half] * c.y;
+                        } else if (e < a.rot) {
+                            const float2 c = cs[e - half];
+                            o[i] = z * c.x + mine[e - half] * c.y;
+                        } else {
+                            o[i] = z;
+                        }
+                    }
+                    y = make_float4(o[0], o[1], o[2], o[3]);
+                }
             }
-        }
-        if (!live) continue;
-        if (is_q) {
-            store4<T>(qo + h * HD + 4 * j, y);
-        } else if (keep) {
-            const int kvh = is_k ? h - a.Hq : h - a.Hq - a.Hkv;
-            uint16_t *c = is_k ? a.kc : a.vc;
-            store4<uint16_t>(c + (((int64_t)slot * a.Hkv + kvh) * a.max_seq + row) * HD + 4 * j, y);
+            if (h >= n_rows) continue;
+            if (is_q) {
+                store4<T>(qo + (int64_t)h * HD, y);
+            } else if (keep) {
+                const int kvh = is_k ? h - a.Hq : h - a.Hq - a.Hkv;
+                uint16_t *c = is_k ? a.kc : a.vc;
+                store4<uint16_t>(c + (((int64_t)slot * a.Hkv + kvh) * a.max_seq + row) * HD + 4 * j, y);
+            }
         }
     }
 }
@@ -150,17 +189,23 @@ __global__ void __launch_bounds__(kT) rope_append(const RopeArgs a) {
 }  // namespace
 
 cudaError_t rope_append_launch(const RopeArgs &a, int hd, bool f32, cudaStream_t s) {
-    const dim3 grid(a.n, 1);
+    // Many tokens: four a CTA, so that their angles are formed side by side and each
+    // warp has several rounds of loads (8,192 tokens of 48 heads of 64 in fp32: 48.9
+    // us with one token a CTA). A few: one round a warp, a token over several CTAs.
+    const int per_cta = kW * (hd == 64 ? 2 : 1), rounds = (a.Hq + 2 * a.Hkv + per_cta - 1) / per_cta;
+    const bool many = a.n >= 1024;
+    const dim3 grid(many ? (a.n + 3) / 4 : a.n, a.n <= 64 ? std::min(rounds, 8) : 1);
+    auto go = [&](auto kernel) { kernel<<<grid, kT, 0, s>>>(a); };
     if (f32) {
         if (hd == 64)
-            rope_append<float, 64><<<grid, kT, 0, s>>>(a);
+            many ? go(rope_append<float, 64, 4>) : go(rope_append<float, 64, 1>);
         else
-            rope_append<float, 128><<<grid, kT, 0, s>>>(a);
+            many ? go(rope_append<float, 128, 4>) : go(rope_append<float, 128, 1>);
     } else {
         if (hd == 64)
-            rope_append<uint16_t, 64><<<grid, kT, 0, s>>>(a);
+            many ? go(rope_append<uint16_t, 64, 4>) : go(rope_append<uint16_t, 64, 1>);
         else
-            rope_append<uint16_t, 128><<<grid, kT, 0, s>>>(a);
+            many ? go(rope_append<uint16_t, 128, 4>) : go(rope_append<uint16_t, 128, 1>);
     }
     return cudaGetLastError();
 }

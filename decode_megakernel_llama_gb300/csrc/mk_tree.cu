@@ -91,19 +91,20 @@ bool cache_map(CUtensorMap *map, const void *cache, int planes, int max_seq, int
 struct Plan {
     int S;
     bool ws;
+    double us;  // its estimated time
 };
 
 // The two kernels by what their launch needs.
 template <int HD_, int TERMS_, int NR_>
 struct Few {
     static constexpr int HD = HD_, TERMS = TERMS_, NR = NR_, kSmem = AttnShape<HD, TERMS, NR>::kSmem;
-    static constexpr double kTileUs = NR >= 64 ? 0.9 : 0.5;
+    static constexpr double kTileUs = HD == 64 ? 0.6 : TERMS == 1 ? 0.75 : 1.0, kFixedUs = 5.0, kJoinUs = 4.5;
     static auto fn() { return tree_attention<HD, TERMS, NR>; }
 };
 template <int HD_, int TERMS_>
 struct Many {
     static constexpr int HD = HD_, TERMS = TERMS_, NR = kRows, kSmem = RowShape<HD, TERMS>::kSmem;
-    static constexpr double kTileUs = TERMS == 1 ? 0.8 : 1.5;
+    static constexpr double kTileUs = TERMS == 3 ? 1.2 : HD == 64 ? 0.7 : 1.0, kFixedUs = 6.5, kJoinUs = 7.0;
     static auto fn() { return tree_attention_rows<HD, TERMS>; }
 };
 
@@ -147,36 +148,41 @@ int active_clusters(int k, int n_sm) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     launch_config(cfg, attr, dim3(1 << k, n_sm * 4), K::kSmem, 1 << k, nullptr);
-    if (cudaOccupancyMaxActiveClusters(&n, K::fn(), &cfg) != cudaSuccess || n < 1 ||
+    if (configure<K>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, K::fn(), &cfg) != cudaSuccess || n < 1 ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, K::fn(), kAttnThreads, K::kSmem) != cudaSuccess) {
         (void)cudaGetLastError();
-        n = 1;
+        return n_sm >> k;  // (not kept: the next call asks again)
     }
     n *= std::max(1, per_sm);
     known[k].store(n, std::memory_order_relaxed);
     return n;
 }
 
-// The split with the least estimated time: waves of resident CTAs x (tiles of
-// a split + a fixed part), in microseconds.
+// The split with the least estimated time, in microseconds: waves of resident
+// CTAs x (the tiles of a split x K::kTileUs + a fixed part). The tile times are
+// those of one split over a long cache (S = 1: 44.2 us for 65 tiles of 32 fp32 rows
+// with heads of 64, 49.4 for 128 bf16 rows, 22.5 for 17 tiles of 32 fp32 rows with
+// heads of 128, each with K::kFixedUs of launch, set-up and end); more than a
+// cluster's splits cost K::kJoinUs: a second launch and the partial results'
+// way through memory.
 template <class K>
 Plan plan(const TreeArgs &a, int max_len, int n_sm, bool ws) {
     const int row_tiles = (a.T * (a.Hq / a.Hkv) + K::NR - 1) / K::NR;
     const int64_t units = (int64_t)a.B * a.Hkv * row_tiles;
     const int tiles = (std::min((int64_t)max_len + a.T, (int64_t)a.max_seq) + kTile - 1) / kTile;
-    const double fixed = 3.0;
-    Plan best{1, false};
-    double least = 1e30;
+    Plan best{1, false, 1e30};
     for (int k = 0; k < 4 && (1 << k) <= tiles; ++k) {
         const int S = 1 << k, at_once = active_clusters<K>(k, n_sm);
-        const double cost =
-            (double)((units + at_once - 1) / at_once) * (((tiles + S - 1) / S) * K::kTileUs + fixed) + 0.2 * k;
-        if (cost < least) least = cost, best = Plan{S, false};
+        const double us =
+            (double)((units + at_once - 1) / at_once) * (((tiles + S - 1) / S) * K::kTileUs + K::kFixedUs) +
+            (k ? 0.8 + 0.2 * k : 0.0);  // (the cluster's join)
+        if (us < best.us) best = Plan{S, false, us};
     }
     if (ws) {
-        const int64_t room = active_clusters<K>(0, n_sm) / std::max<int64_t>(units, 1);
+        const int64_t room = active_clusters<K>(0, n_sm) / units;
         const int S = (int)std::min<int64_t>(std::min<int64_t>(room, max_splits(K::NR)), tiles / 2);
-        if (S > 1 && ((tiles + S - 1) / S) * K::kTileUs + fixed + 4.0 < least) best = Plan{S, true};
+        const double us = ((tiles + S - 1) / std::max(S, 1)) * K::kTileUs + K::kFixedUs + K::kJoinUs;
+        if (S > 1 && us < best.us) best = Plan{S, true, us};
     }
     return best;
 }
@@ -208,16 +214,22 @@ cudaError_t launch(TreeArgs a, int max_len, int n_sm, cudaStream_t s, int64_t *w
     return cudaGetLastError();
 }
 
-// The kernel by the tree's rows of a kv head: the fewest columns of 16, 32 (64
-// with one term) that hold them, or the kernel of 128 rows.
+// The kernel of 16 or 32 columns that holds the tree's rows of a kv head; for more
+// rows, several CTAs of 32 or the kernel of 128 rows, whichever plan is shorter.
+// (Measured, 64 fp32 rows over 8,208 cache rows: 14.4 us with 32 columns, 18.7 with
+// 128 rows; 244 bf16 rows and 64 (sequence, kv head) pairs: 99 and 47 us.)
 template <int HD, int TERMS>
 cudaError_t dispatch(const TreeArgs &a, int max_len, int n_sm, cudaStream_t s, int64_t *want) {
     const int rows = a.T * (a.Hq / a.Hkv);
     if (rows <= 16) return launch<Few<HD, TERMS, 16>>(a, max_len, n_sm, s, want);
-    if (rows <= 32) return launch<Few<HD, TERMS, 32>>(a, max_len, n_sm, s, want);
-    if constexpr (TERMS == 1)
-        if (rows <= 64) return launch<Few<HD, TERMS, 64>>(a, max_len, n_sm, s, want);
-    return launch<Many<HD, TERMS>>(a, max_len, n_sm, s, want);
+    // (three terms of a head of 128 and two O of 128 columns exceed tensor memory)
+    if constexpr (!(HD == 128 && TERMS == 3))
+        if (rows > 32) {
+            const bool ws = want || a.work;
+            if (plan<Many<HD, TERMS>>(a, max_len, n_sm, ws).us < plan<Few<HD, TERMS, 32>>(a, max_len, n_sm, ws).us)
+                return launch<Many<HD, TERMS>>(a, max_len, n_sm, s, want);
+        }
+    return launch<Few<HD, TERMS, 32>>(a, max_len, n_sm, s, want);
 }
 
 cudaError_t dispatch(const TreeArgs &a, int hd, bool f32, int max_len, int n_sm, cudaStream_t s, int64_t *want) {

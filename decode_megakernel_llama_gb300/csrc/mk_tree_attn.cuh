@@ -31,13 +31,15 @@
 // come out of the second product where its A operand has room: for HD = 64 the
 // instruction's rows 64 .. 127 are a constant block whose first row is ones, so
 // lane 64 of O^T is sum p; for HD = 128 they stay per thread until the end. In the
-// second kernel a row's statistics are its two threads' own.
+// second kernel a row's statistics are one thread's own.
 //
 // Overlap (one CTA an SM): one warp fills a ring of K and V tiles by TMA, one
-// issues the MMAs, eight do the softmax, two threads for each lane of tensor
-// memory. S is double buffered and so is P: S(i + 2) is issued behind PV(i), so
-// neither product's latency stands in the softmax warps' way, and the order of
-// the MMAs alone makes both buffers free in time.
+// issues the MMAs, and two groups of four softmax warps take the tiles in turn,
+// each with its own buffers of S and P, its own maxima, sums and O (joined at the
+// end like two splits), so neither a product's latency nor a group's votes stand
+// in the other's way. S(i + 2) is issued behind PV(i): the order of the MMAs alone
+// makes the buffers free in time. A commit of a product serves both who waits for
+// its result and the ring's next copy.
 //
 // Up to 8 splits of a sequence's cache rows form a thread-block cluster: each
 // CTA leaves its partial O, sums and maxima in its shared memory, and the
@@ -78,9 +80,12 @@ __device__ __forceinline__ Seq sequence(const TreeArgs &a, int b) {
 
 constexpr int kTile = 128;      // cache rows of a tile
 constexpr int kCluster = 8;     // most splits joined in a cluster
-constexpr int kSoft = 256;      // softmax threads: two for each of the 128 lanes of tensor memory
-constexpr int kSoftWarps = kSoft / 32, kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-constexpr int kAttnThreads = kSoft + 64;
+constexpr int kGroup = 128;     // softmax threads of a group: one for each lane of tensor memory
+constexpr int kSoft = 2 * kGroup;
+// Warps: 0 issues the MMAs, 1 and 2 the copies of K and of V, 3 rests (a group's
+// warps w have w & 3 as their quarter of tensor memory), 4 .. 11 do the softmax.
+constexpr int kMmaWarp = 0, kKWarp = 1, kVWarp = 2, kFirstSoft = 4, kSoftWarps = kSoft / 32;
+constexpr int kAttnThreads = kSoft + 32 * kFirstSoft;
 constexpr int kHalfTile = kTile * 128;  // bytes of 128 rows x 64 dims
 constexpr int kSmemMost = 232448;       // shared memory of a CTA
 constexpr float kNone = -1e30f;         // the maximum of a row that has seen nothing
@@ -99,32 +104,26 @@ __device__ __forceinline__ float max_warp(float x) {
     return y;
 }
 
+// Barriers of both groups, and of group g: a plain one, and a vote.
 __device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ bool soft_any(bool x) {
+__device__ __forceinline__ void group_sync(int g) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + g) : "memory"); }
+__device__ __forceinline__ bool group_any(int g, bool x) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)x)
+        : "r"((uint32_t)x), "r"(2 + g)
         : "memory");
     return r != 0;
 }
 
-// The same between the two warps that share the rows of a lane quarter.
-__device__ __forceinline__ bool pair_any(int quarter, bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)x), "r"(2 + quarter)
-        : "memory");
-    return r != 0;
+// (x, y) * c - m: two fp32 in one instruction.
+__device__ __forceinline__ void fma2(float &x, float &y, float c, float mx, float my) {
+    const float2 r = __ffma2_rn(make_float2(x, y), make_float2(c, c), make_float2(-mx, -my));
+    x = r.x, y = r.y;
 }
 
 // Values of a tensor-memory load, used only behind its wait.
@@ -238,60 +237,102 @@ __device__ __noinline__ void add_taken_out(const TreeArgs &a, int b, int kvh, in
     }
 }
 
-// Barriers and words of a CTA, at the front of its fixed shared memory. The
-// ring's unit 2i is tile i's K, unit 2i + 1 its V; U units.
-template <int U>
+// Barriers and words of a CTA. The ring holds KU tiles of K, then VU of V.
+template <int KU, int VU>
 struct Sync {
-    uint64_t full[U], free[U];
-    // (two of each by the tile's parity: warps of the softmax may be a tile ahead of
-    // others, and a wait must never be two phases behind)
-    uint64_t s_full[2], p_full[2], o_done[2];
+    // full: the copies have landed; done: the product that reads them is (for K the
+    // scores are there, for V the tile is in O)
+    uint64_t k_full[KU], k_done[KU], v_full[VU], v_done[VU];
+    uint64_t s_read[2], p_full[2];  // a group has read its scores, has written its weights
     uint32_t tmem;
-    int err, issued;   // a wait ran out; units whose copies went out
-    uint32_t bad[2];   // drafted rows taken out of the second product
+    int err, k_issued, v_issued;  // a wait ran out; tiles whose copies went out
+    uint32_t bad[2];              // drafted rows taken out of the second product
 };
 
-template <int U>
-__device__ __forceinline__ void init_sync(Sync<U> *y) {
-    for (int u = 0; u < U; ++u) {
-        mbar_init(&y->full[u], 1);
-        mbar_init(&y->free[u], 1);
+template <int KU, int VU>
+__device__ __forceinline__ void init_sync(Sync<KU, VU> *y) {
+    for (int u = 0; u < KU; ++u) {
+        mbar_init(&y->k_full[u], 1);
+        mbar_init(&y->k_done[u], 1);
     }
-    mbar_init(&y->s_full[0], 1);
-    mbar_init(&y->s_full[1], 1);
-    mbar_init(&y->p_full[0], kSoftWarps);
-    mbar_init(&y->p_full[1], kSoftWarps);
-    mbar_init(&y->o_done[0], 1);
-    mbar_init(&y->o_done[1], 1);
-    y->err = y->issued = 0;
+    for (int u = 0; u < VU; ++u) {
+        mbar_init(&y->v_full[u], 1);
+        mbar_init(&y->v_done[u], 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+        mbar_init(&y->s_read[g], kSoftWarps / 2);
+        mbar_init(&y->p_full[g], kSoftWarps / 2);
+    }
+    y->err = y->k_issued = y->v_issued = 0;
     y->bad[0] = y->bad[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     async_fence();
 }
 
-// The copies of unit u into its place in the ring.
-template <int HD, int U>
-__device__ __forceinline__ void load_unit(Sync<U> *y, uint8_t *ring, const CUtensorMap *kmap, const CUtensorMap *vmap,
-                                          int u, int t0, int plane) {
-    uint64_t *bar = &y->full[u % U];
-    uint8_t *at = ring + (u % U) * (kHalfTile * (HD / 64));
+// Waits for tile i's copies, or for its product. A waiter must not be two phases
+// of a place in the ring behind: the tile before it in its place (2 or more
+// before) has to be known to be done. The MMA and copy warps see every tile. A
+// softmax group that awaits S(i) has seen S(i - 2), and with it every product
+// issued before; one that awaits PV(i - 2) has awaited PV(i - 4), or knows it done by
+// S(i - 2), which was issued behind it. Of the last tile's PV that holds for the
+// group of that tile; the other may pass early: what it reads comes behind a
+// barrier with the first.
+template <int KU, int VU>
+__device__ __forceinline__ bool k_full(Sync<KU, VU> *y, int i) {
+    return mbar_wait(&y->k_full[i % KU], (i / KU) & 1, &y->err);
+}
+template <int KU, int VU>
+__device__ __forceinline__ bool v_full(Sync<KU, VU> *y, int i) {
+    return mbar_wait(&y->v_full[i % VU], (i / VU) & 1, &y->err);
+}
+template <int KU, int VU>
+__device__ __forceinline__ bool s_done(Sync<KU, VU> *y, int i) {
+    return mbar_wait(&y->k_done[i % KU], (i / KU) & 1, &y->err);
+}
+template <int KU, int VU>
+__device__ __forceinline__ bool pv_done(Sync<KU, VU> *y, int i) {
+    return mbar_wait(&y->v_done[i % VU], (i / VU) & 1, &y->err);
+}
+
+// The copies of a K (or V) tile into its place in the ring.
+template <int HD>
+__device__ __forceinline__ void load_tile(uint8_t *at, const CUtensorMap *map, int row, int plane, uint64_t *bar) {
     mbar_expect_tx(bar, kHalfTile * (HD / 64));
 #pragma unroll
-    for (int h = 0; h < HD / 64; ++h)
-        tma_load_3d(at + h * kHalfTile, (u & 1) ? vmap : kmap, h * 64, (t0 + u / 2) * kTile, plane, bar);
-    *(volatile int *)&y->issued = u + 1;
+    for (int h = 0; h < HD / 64; ++h) tma_load_3d(at + h * kHalfTile, map, h * 64, row, plane, bar);
+}
+
+// One lane's work: all of a split's K (or V) tiles, into the ring.
+template <int HD, int KU, int VU>
+__device__ __forceinline__ void load_all(Sync<KU, VU> *y, uint8_t *ring, const CUtensorMap *map, bool is_k, int from,
+                                         int to, int t0, int plane) {
+    constexpr int kKv = kHalfTile * (HD / 64);
+    for (int i = from; i < to; ++i) {
+        if (is_k) {
+            if (i >= KU && !s_done(y, i - KU)) break;
+            load_tile<HD>(ring + (i % KU) * kKv, map, (t0 + i) * kTile, plane, &y->k_full[i % KU]);
+            *(volatile int *)&y->k_issued = i + 1;
+        } else {
+            if (i >= VU && !pv_done(y, i - VU)) break;
+            load_tile<HD>(ring + (KU + i % VU) * kKv, map, (t0 + i) * kTile, plane, &y->v_full[i % VU]);
+            *(volatile int *)&y->v_issued = i + 1;
+        }
+    }
 }
 
 // After a wait ran out: the copies that were issued land before the shared
 // memory goes.
-template <int U>
-__device__ __noinline__ void drain(Sync<U> *y, int *status) {
-    const int n = *(volatile int *)&y->issued;
-    for (int u = max(0, n - U); u < n; ++u) {
-        const uint64_t from = gtimer();
-        while (!mbar_try(&y->full[u % U], (u / U) & 1))
-            if (gtimer() - from > kWaitNs) break;
-    }
+template <int KU, int VU>
+__device__ __noinline__ void drain(Sync<KU, VU> *y, int *status) {
+    auto land = [](uint64_t *bar, int units, int n) {
+        for (int i = max(0, n - units); i < n; ++i) {
+            const uint64_t from = gtimer();
+            while (!mbar_try(bar + i % units, (i / units) & 1))
+                if (gtimer() - from > kWaitNs) break;
+        }
+    };
+    land(y->k_full, KU, *(volatile int *)&y->k_issued);
+    land(y->v_full, VU, *(volatile int *)&y->v_issued);
     if (status) atomicExch(status, 1);
 }
 
@@ -379,33 +420,38 @@ struct AttnShape {
     static constexpr int kKv = kHalfTile * (HD / 64);    // bytes of a K (or V) tile
     static constexpr int kP = ((N + 63) / 64) * kHalfTile;  // of a tile's weights; two of them
     static constexpr int kQ = N * HD * 2;
-    static constexpr int kCols = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 3 * N <= 256 ? 256 : 512;
+    static constexpr int kCols = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;
     static constexpr int kOnes = HD == 64 ? 2048 : 0;  // 16 cache rows x 64: ones in the first column
-    static constexpr int kMisc = 512 + 8 * NR + 8 * MK_MAX_TREE + 4 * NR * (3 + 4);
+    static constexpr int kMisc = 512 + 8 * MK_MAX_TREE + 4 * NR * (2 + 2 + 1 + 8);
     static constexpr int kRoom = (kSmemMost - 1024 - 2 * kP - kQ - kOnes - kMisc) / kKv;
-    static constexpr int U = kRoom > 8 ? 8 : kRoom;
-    static constexpr int kOffP = U * kKv, kOffQ = kOffP + 2 * kP, kOffOnes = kOffQ + kQ, kOffMisc = kOffOnes + kOnes;
+    static constexpr int KU = (kRoom + 1) / 2 > 6 ? 6 : (kRoom + 1) / 2, VU = kRoom / 2 > 6 ? 6 : kRoom / 2;
+    // With room for it S runs three tiles ahead of PV and starts as soon as the group
+    // has read the scores before; else it follows PV(i), two tiles ahead.
+    static constexpr bool kEarly = VU >= 4;
+    static constexpr int kAhead = kEarly ? 3 : 2;
+    static constexpr int kOffP = (KU + VU) * kKv, kOffQ = kOffP + 2 * kP, kOffOnes = kOffQ + kQ, kOffMisc = kOffOnes + kOnes;
     static constexpr int kSmem = 1024 + kOffMisc + kMisc;
-    static_assert(N % 16 == 0 && N <= 256 && 3 * N <= 512 && U >= 4, "the instruction's N, tensor and shared memory");
-    static_assert(NR * HD * 4 + 3 * kCluster * NR * 4 <= U * kKv, "the partial result fits the ring");
+    static_assert(N % 16 == 0 && N <= 256 && 4 * N <= 512 && VU >= 2, "the instruction's N, tensor and shared memory");
+    static_assert(NR * HD * 4 + 3 * kCluster * NR * 4 <= (KU + VU) * kKv, "the partial result fits the ring");
 };
 
 template <int HD, int TERMS, int NR>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     tree_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const TreeArgs a) {
     using C = AttnShape<HD, TERMS, NR>;
-    constexpr int N = C::N, U = C::U, HR = NR / 2;  // HR: query rows of a softmax thread
+    constexpr int N = C::N, KU = C::KU, VU = C::VU;
     constexpr bool kScaled = TERMS > 1;             // the queries carry the scale already
     constexpr bool kOnes = HD == 64;                // the sums come out of the second product
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *Ps = sm + C::kOffP, *Qs = sm + C::kOffQ;
-    Sync<U> *y = reinterpret_cast<Sync<U> *>(sm + C::kOffMisc);
-    static_assert(sizeof(Sync<U>) <= 512, "");
+    Sync<KU, VU> *y = reinterpret_cast<Sync<KU, VU> *>(sm + C::kOffMisc);
+    static_assert(sizeof(Sync<KU, VU>) <= 512, "");
     volatile int *err = &y->err;
     uint64_t *seen = reinterpret_cast<uint64_t *>(sm + C::kOffMisc + 512);  // [MK_MAX_TREE] bit r: row r sees it
-    float *mref = reinterpret_cast<float *>(seen + MK_MAX_TREE), *corr = mref + NR, *lsum = corr + NR;
-    float *wtmp = lsum + NR;                    // [4][NR]
+    float *mref = reinterpret_cast<float *>(seen + MK_MAX_TREE), *corr = mref + 2 * NR;  // [2][NR] of the groups
+    float *lsum = corr + 2 * NR;                // [NR]
+    float *wtmp = lsum + NR;                    // [2][4][NR]
     float *Os = reinterpret_cast<float *>(sm);  // [NR][HD], in the ring when the tiles are done
     float *join = Os + NR * HD;                 // [3][kCluster][NR] behind it
 
@@ -415,11 +461,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int row0 = blockIdx.z * NR;
     const float c = a.scale * 1.44269504088896340736f;  // scores in powers of two
     const Seq sq = sequence(a, b);
-    const uint64_t word = tid < NR && row0 + tid < a.T * G ? a.masks[(int64_t)b * a.T + (row0 + tid) / G] : 0;
-    if (warp < kSoftWarps) {
+    const int first = threadIdx.x - kFirstSoft * 32;
+    const uint64_t word =
+        first >= 0 && first < NR && row0 + first < a.T * G ? a.masks[(int64_t)b * a.T + (row0 + first) / G] : 0;
+    if (warp >= kFirstSoft) {
         // The queries as the B operand: row term * NR + r, 128-byte swizzled. (Rows
         // of nodes behind the sequence's last one are columns nobody reads.)
-        for (int i = tid; i < NR * (HD / 8); i += kSoft) {
+        for (int i = first; i < NR * (HD / 8); i += kSoft) {
             const int r = i / (HD / 8), ch = i % (HD / 8);
             uint4 t[TERMS];
             load_query8<HD, TERMS>(a, b, kvh, G, row0 + r, ch, c, t);
@@ -435,11 +483,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int total = sq.len + sq.n, tiles = (total + kTile - 1) / kTile;
     const int t0 = (int)((int64_t)split * tiles / S), nt = (int)((int64_t)(split + 1) * tiles / S) - t0;
     const int plane = sq.slot * a.Hkv + kvh;
-    if (warp == kTmaWarp) {
+    if (warp == kKWarp) {
         if (elect()) {
             init_sync(y);
             // the first copies need nobody else
-            for (int u = 0; u < min(2 * nt, U); ++u) load_unit<HD>(y, sm, &kmap, &vmap, u, t0, plane);
+            load_all<HD>(y, sm, &kmap, true, 0, min(nt, KU), t0, plane);
+            load_all<HD>(y, sm, &vmap, false, 0, min(nt, VU), t0, plane);
         }
     } else if (warp == kMmaWarp) {
         tmem_alloc(&y->tmem, C::kCols);
@@ -447,14 +496,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int i = lane; i < C::kOnes / 16; i += 32)  // chunk 0 of row i / 8 sits at chunk (row & 7)
                 *reinterpret_cast<uint4 *>(sm + C::kOffOnes + i * 16) =
                     make_uint4(i % 8 == ((i / 8) & 7) ? 0x3F80u : 0u, 0u, 0u, 0u);
-    } else {
-        if (tid < NR) {
-            mref[tid] = kNone;
-            lsum[tid] = 0.f;
-        }
-        if ((t0 + nt) * kTile > sq.len && warp * 32 < NR) {  // a split with drafted rows: the masks by drafted row
-            const uint64_t mine = tid < rows ? word : 0;
-            uint32_t *out = reinterpret_cast<uint32_t *>(seen) + warp;
+    } else if (warp >= kFirstSoft) {
+        if (first < 2 * NR) mref[first] = kNone;
+        if ((t0 + nt) * kTile > sq.len && first < ((NR + 31) & ~31)) {  // a split with drafted rows: their masks
+            const uint64_t mine = first < rows ? word : 0;
+            uint32_t *out = reinterpret_cast<uint32_t *>(seen) + first / 32;
             for (int j = 0; j < sq.n; ++j) {
                 const uint32_t w = __ballot_sync(0xFFFFFFFFu, (mine >> j) & 1);
                 if (lane == 0) out[2 * j] = w;
@@ -466,158 +512,159 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncwarp();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tS = uniform(y->tmem), tO = tS + 2 * N;
+    const uint32_t tS = uniform(y->tmem), tO = tS + 2 * N;  // S and O of group g: + g * N
 
-    if (warp == kTmaWarp) {
-        for (int u = U; u < 2 * nt; ++u) {
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&y->free[u % U], ((u / U) - 1) & 1, err))) break;
-            if (elect()) load_unit<HD>(y, sm, &kmap, &vmap, u, t0, plane);
-            __syncwarp();
-        }
+    if (warp == kKWarp) {
+        if (elect()) load_all<HD>(y, sm, &kmap, true, KU, nt, t0, plane);
+    } else if (warp == kVWarp) {
+        if (elect()) load_all<HD>(y, sm, &vmap, false, VU, nt, t0, plane);
     } else if (warp == kMmaWarp) {
         constexpr uint32_t idS = idesc_bf16(N, false, false), idO = idesc_bf16(N, true, true);
         const uint64_t q = sw128_desc(saddr(Qs), 16);
         const uint32_t ring = saddr(sm), ones = saddr(sm + C::kOffOnes), p0 = saddr(Ps);
         auto scores = [&](int i) {
-            const int u = 2 * i;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&y->full[u % U], (u / U) & 1, err))) return false;
-            tc_fence_after();
-            const uint64_t k = sw128_desc(ring + (u % U) * C::kKv, 16);
-            if (elect()) {
+            const uint64_t k = sw128_desc(ring + (i % KU) * C::kKv, 16);
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk)
-                    umma_bf16(tS + (i & 1) * N, k + (((kk / 4) * kHalfTile + (kk % 4) * 32) >> 4),
-                              q + (((kk / 4) * (N * 128) + (kk % 4) * 32) >> 4), idS, kk != 0);
-                umma_commit(&y->free[u % U]);
-                umma_commit(&y->s_full[i & 1]);
-            }
-            __syncwarp();
-            return true;
+            for (int kk = 0; kk < HD / 16; ++kk)
+                umma_bf16(tS + (i & 1) * N, k + (((kk / 4) * kHalfTile + (kk % 4) * 32) >> 4),
+                          q + (((kk / 4) * (N * 128) + (kk % 4) * 32) >> 4), idS, kk != 0);
+            umma_commit(&y->k_done[i % KU]);
         };
-        bool ok = nt > 0 && scores(0) && (nt < 2 || scores(1));
-        for (int i = 0; i < nt && ok; ++i) {
-            const int u = 2 * i + 1;
-            ok = mbar_wait(&y->p_full[i & 1], (i >> 1) & 1, err) && mbar_wait(&y->full[u % U], (u / U) & 1, err);
-            if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
-            tc_fence_after();
-            // (the k-th product's first atom moves on by 2048 bytes, so the constant
-            // block behind it comes nearer)
-            const uint32_t va = ring + (u % U) * C::kKv;
-            const uint64_t v = sw128_desc(va, kOnes ? ones - va : kHalfTile);
-            const uint64_t p = sw128_desc(p0 + (i & 1) * C::kP, kHalfTile);
-            if (elect()) {
+        if (elect()) {
+            bool ok = true;
+            // the scores of tile i (early: once the group has read those of i - 2)
+            for (int i = 0; i < min(nt, C::kAhead) && ok; ++i) {
+                ok = k_full(y, i) && (i < 2 || mbar_wait(&y->s_read[i & 1], ((i >> 1) - 1) & 1, err));
+                tc_fence_after();
+                scores(i);
+            }
+            for (int i = 0; i < nt && ok; ++i) {
+                const int j = i + C::kAhead;
+                if (C::kEarly && j < nt) {
+                    ok = k_full(y, j) && mbar_wait(&y->s_read[j & 1], ((j >> 1) - 1) & 1, err);
+                    tc_fence_after();
+                    scores(j);
+                }
+                // (the k-th product's first atom moves on by 2048 bytes, so the constant
+                // block behind it comes nearer)
+                const uint32_t va = ring + (KU + i % VU) * C::kKv;
+                const uint64_t v = sw128_desc(va, kOnes ? ones - va : kHalfTile);
+                const uint64_t p = sw128_desc(p0 + (i & 1) * C::kP, kHalfTile);
+                if (!(ok = ok && v_full(y, i) && mbar_wait(&y->p_full[i & 1], (i >> 1) & 1, err))) break;
+                tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
-                    umma_bf16(tO, v + ((kk * 2048) >> 4) - (kOnes ? (uint64_t)((kk * 2048) >> 4) << 16 : 0),
-                              p + ((kk * 2048) >> 4), idO, (i | kk) != 0);
-                umma_commit(&y->free[u % U]);
-                umma_commit(&y->o_done[i & 1]);
-            }
-            __syncwarp();
-            if (i + 2 < nt) ok = scores(i + 2);
-        }
-    } else {
-        // thread: cache row `row` of the tile, query rows h0 .. h0 + HR - 1
-        const int row = tid & (kTile - 1), h0 = (tid / kTile) * HR, quarter = warp & 3;
-        const uint32_t mylane = (uint32_t)(quarter * 32) << 16;
-        const float4 *m4 = reinterpret_cast<const float4 *>(mref + h0);
-        float l[kOnes ? 1 : HR];
-        if constexpr (!kOnes)
-#pragma unroll
-            for (int r = 0; r < HR; ++r) l[r] = 0.f;
-        bool ok = true;
-        for (int i = 0; i < nt; ++i) {
-            // (a wait that ran out: the loop goes on, its barriers matched, and
-            // the result becomes NaN)
-            ok &= mbar_wait(&y->s_full[i & 1], (i >> 1) & 1, err);
-            tc_fence_after();
-            float s[TERMS * HR];
-            const uint32_t ts = tS + (i & 1) * N + mylane + h0;
-#pragma unroll
-            for (int k = 0; k < TERMS; ++k) {
-                if constexpr (HR == 8) {
-                    tmem_ld8(ts + k * NR, s + k * HR);
-                } else {
-#pragma unroll
-                    for (int r0 = 0; r0 < HR; r0 += 16) tmem_ld16(ts + k * NR + r0, s + k * HR + r0);
+                    umma_bf16(tO + (i & 1) * N, v + ((kk * 2048) >> 4) - (kOnes ? (uint64_t)((kk * 2048) >> 4) << 16 : 0),
+                              p + ((kk * 2048) >> 4), idO, i >= 2 || kk != 0);
+                umma_commit(&y->v_done[i % VU]);
+                if (!C::kEarly && j < nt) {
+                    ok = k_full(y, j);
+                    tc_fence_after();
+                    scores(j);
                 }
             }
+        }
+    } else if (warp >= kFirstSoft) {
+        // group g takes every other tile; thread: cache row `row` of it, all query rows
+        const int g = (warp - kFirstSoft) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t mylane = (uint32_t)(quarter * 32) << 16;
+        const uint32_t ts = tS + g * N + mylane, to = tO + g * N + mylane;
+        float *gref = mref + g * NR, *gcorr = corr + g * NR, *gtmp = wtmp + g * 4 * NR;
+        const float4 *m4 = reinterpret_cast<const float4 *>(gref);
+        float l[kOnes ? 1 : NR];
+        if constexpr (!kOnes)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) l[r] = 0.f;
+        bool ok = true;
+        for (int i = g; i < nt; i += 2) {
+            // (a wait that ran out: the loop goes on, its barriers matched, and
+            // the result becomes NaN)
+            ok &= s_done(y, i);
+            tc_fence_after();
+            float s[TERMS * NR];
+#pragma unroll
+            for (int n = 0; n < N; n += 16) tmem_ld16(ts + n, s + n);
             tmem_ld_wait();
-            pin<TERMS * HR>(s);
+            pin<N>(s);
+            if (C::kEarly) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&y->s_read[g]);
+            }
 #pragma unroll
-            for (int r = 0; r < HR; ++r)
+            for (int r = 0; r < NR; ++r)
 #pragma unroll
-                for (int k = 1; k < TERMS; ++k) s[r] += s[k * HR + r];
+                for (int k = 1; k < TERMS; ++k) s[r] += s[k * NR + r];
             const int at = (t0 + i) * kTile;
             const bool tail = at + kTile > sq.len;  // drafted rows, or the end
             const int node = at + row - sq.len;
             if (tail && node >= 0) {
-                const uint64_t w = node < sq.n ? seen[node] >> h0 : 0;
+                const uint64_t w = node < sq.n ? seen[node] : 0;
 #pragma unroll
-                for (int r = 0; r < HR; ++r)
+                for (int r = 0; r < NR; ++r)
                     if (!((w >> r) & 1)) s[r] = -INFINITY;
             }
             // x = s - m in powers of two, and the largest of them
-            float x[HR];
+            float x[NR];
             auto shift = [&]() {
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int r = 0; r < HR; r += 4) {
+                for (int r = 0; r < NR; r += 4) {
                     const float4 m = m4[r / 4];
-                    x[r] = kScaled ? s[r] - m.x : fmaf(s[r], c, -m.x);
-                    x[r + 1] = kScaled ? s[r + 1] - m.y : fmaf(s[r + 1], c, -m.y);
-                    x[r + 2] = kScaled ? s[r + 2] - m.z : fmaf(s[r + 2], c, -m.z);
-                    x[r + 3] = kScaled ? s[r + 3] - m.w : fmaf(s[r + 3], c, -m.w);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[r + e] = s[r + e];
+                    fma2(x[r], x[r + 1], kScaled ? 1.f : c, m.x, m.y);
+                    fma2(x[r + 2], x[r + 3], kScaled ? 1.f : c, m.z, m.w);
                     top[(r / 4) & 3] = fmaxf(fmaxf(fmaxf(x[r], x[r + 1]), fmaxf(x[r + 2], x[r + 3])), top[(r / 4) & 3]);
                 }
                 return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             };
-            if (soft_any(shift() > kRaise)) {
+            const bool raise = group_any(g, shift() > kRaise);
+            // PV(i - 2) is done: P and O are this group's again (not early: S(i) was issued after it)
+            if (C::kEarly && i >= 2) ok &= pv_done(y, i - 2);
+            if (raise) {
                 // raise the maxima to those of all cache rows so far
 #pragma unroll
-                for (int r = 0; r < HR; ++r) {
+                for (int r = 0; r < NR; ++r) {
                     const float w = max_warp(kScaled ? s[r] : s[r] * c);
-                    if (lane == (r & 31)) wtmp[quarter * NR + h0 + r] = w;
+                    if (lane == (r & 31)) gtmp[quarter * NR + r] = w;
                 }
-                soft_sync();
-                if (tid < NR) {
-                    const float old = mref[tid];
-                    const float m = fmaxf(fmaxf(fmaxf(wtmp[tid], wtmp[NR + tid]),
-                                                fmaxf(wtmp[2 * NR + tid], wtmp[3 * NR + tid])), old);
-                    corr[tid] = ex2(old - m);
-                    mref[tid] = m;
+                group_sync(g);
+                if (row < NR) {
+                    const float old = gref[row];
+                    const float m = fmaxf(fmaxf(fmaxf(gtmp[row], gtmp[NR + row]),
+                                                fmaxf(gtmp[2 * NR + row], gtmp[3 * NR + row])), old);
+                    gcorr[row] = ex2(old - m);
+                    gref[row] = m;
                 }
-                soft_sync();
+                group_sync(g);
                 shift();
                 if constexpr (!kOnes)
 #pragma unroll
-                    for (int r = 0; r < HR; ++r) l[r] *= corr[h0 + r];
-                if (i > 0) {
-                    ok &= mbar_wait(&y->o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, err);
+                    for (int r = 0; r < NR; ++r) l[r] *= gcorr[r];
+                if (i >= 2) {
                     tc_fence_after();
 #pragma unroll 1
-                    for (int n0 = tid < kTile ? 0 : 16; n0 < N; n0 += 32) {
+                    for (int n0 = 0; n0 < N; n0 += 16) {
                         float o[16];
-                        tmem_ld16(tO + mylane + n0, o);
+                        tmem_ld16(to + n0, o);
                         tmem_ld_wait();
                         pin<16>(o);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] *= corr[n0 % NR + e];
-                        tmem_st16(tO + mylane + n0, o);
+                        for (int e = 0; e < 16; ++e) o[e] *= gcorr[n0 % NR + e];
+                        tmem_st16(to + n0, o);
                     }
                     tmem_st_wait();
                 }
             }
-            if (tail && tid < kTile) {
-                const int u = 2 * i + 1;
-                ok &= mbar_wait(&y->full[u % U], (u / U) & 1, err);
-                if (node >= 0) mend_v<HD>(sm + (u % U) * C::kKv, row, node, sq.n, y->bad);
+            if (tail) {
+                ok &= v_full(y, i);
+                if (node >= 0) mend_v<HD>(sm + (KU + i % VU) * C::kKv, row, node, sq.n, y->bad);
             }
             // the weights as the B operand: row = cache row, column = term * NR + r
-            // (PV(i - 2), which read this buffer, is behind: S(i) was issued after it)
-            uint8_t *p = Ps + (i & 1) * C::kP + row * 128;
+            uint8_t *p = Ps + g * C::kP + row * 128;
 #pragma unroll
-            for (int r0 = 0; r0 < HR; r0 += 8) {
+            for (int r0 = 0; r0 < NR; r0 += 8) {
                 float w[8];
                 uint4 t[TERMS];
 #pragma unroll
@@ -628,48 +675,62 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 split8<TERMS>(w, t);
 #pragma unroll
                 for (int k = 0; k < TERMS; ++k) {
-                    const int ch = (k * NR + h0 + r0) / 8;
+                    const int ch = (k * NR + r0) / 8;
                     *reinterpret_cast<uint4 *>(p + (ch / 8) * kHalfTile + (((ch % 8) ^ (row & 7)) << 4)) = t[k];
                 }
             }
             async_fence();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&y->p_full[i & 1]);
+            if (lane == 0) mbar_arrive(&y->p_full[g]);
         }
-        if (nt > 0) ok &= mbar_wait(&y->o_done[(nt - 1) & 1], ((nt - 1) >> 1) & 1, err);
+        if (nt > 0) ok &= pv_done(y, nt - 1);  // (and with it every product)
         tc_fence_after();
-        const bool all = !soft_any(!ok);
+        if (!ok) *err = 1;
         if constexpr (!kOnes) {
             // the sums of the 128 cache rows, warp by warp
 #pragma unroll
-            for (int r = 0; r < HR; ++r) {
+            for (int r = 0; r < NR; ++r) {
                 float w = l[r];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
-                if (lane == (r & 31)) wtmp[quarter * NR + h0 + r] = w;
+                if (lane == (r & 31)) gtmp[quarter * NR + r] = w;
             }
         }
+        soft_sync();
+        // the groups' factors to the larger maximum, which both keep
+        float f0 = 0.f, f1 = 0.f;
+        if (first < NR) {
+            const float m = fmaxf(mref[first], mref[NR + first]);
+            f0 = corr[first] = nt > 0 ? ex2(mref[first] - m) : 0.f;
+            f1 = corr[NR + first] = nt > 1 ? ex2(mref[NR + first] - m) : 0.f;
+            mref[first] = m;
+            if constexpr (!kOnes)
+                lsum[first] = f0 * ((wtmp[first] + wtmp[NR + first]) + (wtmp[2 * NR + first] + wtmp[3 * NR + first])) +
+                            f1 * ((wtmp[4 * NR + first] + wtmp[5 * NR + first]) + (wtmp[6 * NR + first] + wtmp[7 * NR + first]));
+        }
+        soft_sync();
         // O^T: lane = head dim (lane 64 of a head of 64: the sums), column = term * NR + r
         if (quarter * 32 < HD || (kOnes && quarter == 2)) {
 #pragma unroll 1
-            for (int r0 = tid < kTile ? 0 : 16; r0 < NR; r0 += 32) {
+            for (int r0 = 16 * g; r0 < NR; r0 += 32) {
                 float o[16];
-                if (nt > 0) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = 0.f;
+#pragma unroll 1
+                for (int h = 0; h < min(nt, 2); ++h) {
                     float w[16 * TERMS];
 #pragma unroll
-                    for (int k = 0; k < TERMS; ++k) tmem_ld16(tO + mylane + k * NR + r0, w + 16 * k);
+                    for (int k = 0; k < TERMS; ++k) tmem_ld16(tO + h * N + mylane + k * NR + r0, w + 16 * k);
                     tmem_ld_wait();
                     pin<16 * TERMS>(w);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        o[e] = w[16 * (TERMS - 1) + e];
+                        float z = w[16 * (TERMS - 1) + e];
 #pragma unroll
-                        for (int k = TERMS - 2; k >= 0; --k) o[e] += w[16 * k + e];
+                        for (int k = TERMS - 2; k >= 0; --k) z += w[16 * k + e];
+                        o[e] = fmaf(corr[h * NR + r0 + e], z, o[e]);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = 0.f;
                 }
                 if (quarter * 32 < HD) {
 #pragma unroll
@@ -681,11 +742,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         }
         soft_sync();
-        if constexpr (!kOnes)
-            if (tid < NR) lsum[tid] = (wtmp[tid] + wtmp[NR + tid]) + (wtmp[2 * NR + tid] + wtmp[3 * NR + tid]);
-        if (!all)
-            if (tid < NR) lsum[tid] = __uint_as_float(0x7FC00000u);  // a wait ran out: NaN
-        if (y->bad[0] | y->bad[1]) add_taken_out<HD, TERMS, false>(a, b, kvh, G, row0, rows, sq, y->bad, mref, Os, tid);
+        if (*err && first < NR) lsum[first] = __uint_as_float(0x7FC00000u);  // a wait ran out: NaN
+        if (y->bad[0] | y->bad[1]) add_taken_out<HD, TERMS, false>(a, b, kvh, G, row0, rows, sq, y->bad, mref, Os, first);
     }
     __syncwarp();
     __syncthreads();
@@ -711,18 +769,20 @@ template <int HD, int TERMS>
 struct RowShape {
     static constexpr int kKv = kHalfTile * (HD / 64);
     static constexpr int kQ = TERMS * kKv;  // 128 rows x HD a term
-    // Tensor memory: two buffers of scores, whose 64 columns of a half tile
-    // become the half's weights (32 columns each of the first two terms), two of
-    // the third term, and O.
-    static constexpr int kThird = TERMS > 2 ? kTile / 2 : 0;
+    // Tensor memory, for each group: a tile's scores, its weights, and O. Where the
+    // weights have columns of their own (kApart), the scores can be followed by the
+    // next ones as soon as they are read; else the scores' 128 columns become the
+    // weights (64 columns each of the first two terms) beside a third term.
+    static constexpr bool kApart = TERMS == 1 && HD == 64;
+    static constexpr int kThird = kApart || TERMS > 2 ? kTile / 2 : 0;
     static constexpr int kCols = 512;
     static constexpr int kMisc = 512 + 2 * 4 * kRows;
     static constexpr int kRoom = (kSmemMost - 1024 - kQ - kMisc) / kKv;
-    static constexpr int U = kRoom > 8 ? 8 : kRoom;
-    static constexpr int kOffQ = U * kKv, kOffMisc = kOffQ + kQ;
+    static constexpr int KU = (kRoom + 1) / 2 > 6 ? 6 : (kRoom + 1) / 2, VU = kRoom / 2 > 6 ? 6 : kRoom / 2;
+    static constexpr int kOffQ = (KU + VU) * kKv, kOffMisc = kOffQ + kQ;
     static constexpr int kSmem = 1024 + kOffMisc + kMisc;
-    static_assert(2 * kTile + 2 * kThird + HD <= kCols && U >= 4, "tensor and shared memory of an SM");
-    static_assert(kRows * HD * 4 + (3 * kCluster + 2) * kRows * 4 <= U * kKv, "the partial result fits the ring");
+    static_assert(2 * (kTile + kThird + HD) <= kCols && VU >= 2, "tensor and shared memory of an SM");
+    static_assert(kRows * HD * 4 + (3 * kCluster + 2) * kRows * 4 <= (KU + VU) * kKv, "the partial result fits the ring");
 };
 
 template <int HD, int TERMS>
@@ -730,17 +790,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tree_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const TreeArgs a) {
     using C = RowShape<HD, TERMS>;
-    constexpr int U = C::U;
+    constexpr int KU = C::KU, VU = C::VU;
     constexpr bool kScaled = TERMS > 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *Qs = sm + C::kOffQ;
-    Sync<U> *y = reinterpret_cast<Sync<U> *>(sm + C::kOffMisc);
-    static_assert(sizeof(Sync<U>) <= 512, "");
+    Sync<KU, VU> *y = reinterpret_cast<Sync<KU, VU> *>(sm + C::kOffMisc);
+    static_assert(sizeof(Sync<KU, VU>) <= 512, "");
     volatile int *err = &y->err;
-    float *tops = reinterpret_cast<float *>(sm + C::kOffMisc + 512);  // [2][128] the halves' maxima
-    float *Os = reinterpret_cast<float *>(sm);                        // in the ring when the tiles are done,
-    float *join = Os + kRows * HD;                                    // and behind it
+    float *gm = reinterpret_cast<float *>(sm + C::kOffMisc + 512);  // [2][128] the groups' maxima
+    float *Os = reinterpret_cast<float *>(sm);                      // in the ring when the tiles are done,
+    float *join = Os + kRows * HD;                                  // and behind it
     float *mref = join + 3 * kCluster * kRows, *lsum = mref + kRows;
 
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
@@ -749,11 +809,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int row0 = blockIdx.z * kRows;
     const float c = a.scale * 1.44269504088896340736f;
     const Seq sq = sequence(a, b);
-    const int row = tid & (kRows - 1), half = (tid / kRows) & 1;  // a softmax thread's query row and half of a tile
+    const int row = (warp & 3) * 32 + lane;  // a softmax thread's query row
     uint64_t word = row0 + row < a.T * G ? a.masks[(int64_t)b * a.T + (row0 + row) / G] : 0;
-    if (warp < kSoftWarps) {
+    const int st = tid - kFirstSoft * 32;  // a softmax thread's index
+    if (warp >= kFirstSoft) {
         // the queries as the A operand: term k, 128-byte swizzled rows of 64 dims
-        for (int i = tid; i < kRows * (HD / 8); i += kSoft) {
+        for (int i = st; i < kRows * (HD / 8); i += kSoft) {
             const int r = i / (HD / 8), ch = i % (HD / 8);
             uint4 t[TERMS];
             load_query8<HD, TERMS>(a, b, kvh, G, row0 + r, ch, c, t);
@@ -768,10 +829,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int total = sq.len + sq.n, tiles = (total + kTile - 1) / kTile;
     const int t0 = (int)((int64_t)split * tiles / S), nt = (int)((int64_t)(split + 1) * tiles / S) - t0;
     const int plane = sq.slot * a.Hkv + kvh;
-    if (warp == kTmaWarp) {
+    if (warp == kKWarp) {
         if (elect()) {
             init_sync(y);
-            for (int u = 0; u < min(2 * nt, U); ++u) load_unit<HD>(y, sm, &kmap, &vmap, u, t0, plane);
+            // the first copies need nobody else
+            load_all<HD>(y, sm, &kmap, true, 0, min(nt, KU), t0, plane);
+            load_all<HD>(y, sm, &vmap, false, 0, min(nt, VU), t0, plane);
         }
     } else if (warp == kMmaWarp) {
         tmem_alloc(&y->tmem, C::kCols);
@@ -781,130 +844,133 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncwarp();
     __syncthreads();
     tc_fence_after();
+    // scores, third terms and O of group g: + g * 128, + g * kThird, + g * HD
     const uint32_t tS = uniform(y->tmem), tT = tS + 2 * kTile, tO = tT + 2 * C::kThird;
 
-    if (warp == kTmaWarp) {
-        for (int u = U; u < 2 * nt; ++u) {
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&y->free[u % U], ((u / U) - 1) & 1, err))) break;
-            if (elect()) load_unit<HD>(y, sm, &kmap, &vmap, u, t0, plane);
-            __syncwarp();
-        }
+    if (warp == kKWarp) {
+        if (elect()) load_all<HD>(y, sm, &kmap, true, KU, nt, t0, plane);
+    } else if (warp == kVWarp) {
+        if (elect()) load_all<HD>(y, sm, &vmap, false, VU, nt, t0, plane);
     } else if (warp == kMmaWarp) {
         constexpr uint32_t idS = idesc_bf16(kTile, false, false), idO = idesc_bf16(HD, false, true);
         const uint64_t q = sw128_desc(saddr(Qs), 16);
         const uint32_t ring = saddr(sm);
         auto scores = [&](int i) {
-            const int u = 2 * i;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&y->full[u % U], (u / U) & 1, err))) return false;
-            tc_fence_after();
-            const uint64_t k = sw128_desc(ring + (u % U) * C::kKv, 16);
-            if (elect()) {
+            const uint64_t k = sw128_desc(ring + (i % KU) * C::kKv, 16);
 #pragma unroll
-                for (int t = 0; t < TERMS; ++t)
+            for (int t = 0; t < TERMS; ++t)
 #pragma unroll
-                    for (int kk = 0; kk < HD / 16; ++kk) {
-                        const uint32_t at = (kk / 4) * kHalfTile + (kk % 4) * 32;
-                        umma_bf16(tS + (i & 1) * kTile, q + ((t * C::kKv + at) >> 4), k + (at >> 4), idS, (t | kk) != 0);
-                    }
-                umma_commit(&y->free[u % U]);
-                umma_commit(&y->s_full[i & 1]);
-            }
-            __syncwarp();
-            return true;
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                    const uint32_t at = (kk / 4) * kHalfTile + (kk % 4) * 32;
+                    umma_bf16(tS + (i & 1) * kTile, q + ((t * C::kKv + at) >> 4), k + (at >> 4), idS, (t | kk) != 0);
+                }
+            umma_commit(&y->k_done[i % KU]);
         };
-        bool ok = nt > 0 && scores(0) && (nt < 2 || scores(1));
-        for (int i = 0; i < nt && ok; ++i) {
-            const int u = 2 * i + 1;
-            ok = mbar_wait(&y->p_full[i & 1], (i >> 1) & 1, err) && mbar_wait(&y->full[u % U], (u / U) & 1, err);
-            if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
-            tc_fence_after();
-            const uint64_t v = sw128_desc(ring + (u % U) * C::kKv, kHalfTile);
-            if (elect()) {
+        if (elect()) {
+            bool ok = true;
+            for (int i = 0; i < min(nt, C::kApart ? 3 : 2) && ok; ++i) {
+                ok = k_full(y, i) && (i < 2 || mbar_wait(&y->s_read[i & 1], ((i >> 1) - 1) & 1, err));
+                tc_fence_after();
+                scores(i);
+            }
+            for (int i = 0; i < nt && ok; ++i) {
+                const int j = i + (C::kApart ? 3 : 2);
+                if (C::kApart && j < nt) {
+                    ok = k_full(y, j) && mbar_wait(&y->s_read[j & 1], ((j >> 1) - 1) & 1, err);
+                    tc_fence_after();
+                    scores(j);
+                }
+                const uint64_t v = sw128_desc(ring + (KU + i % VU) * C::kKv, kHalfTile);
+                if (!(ok = ok && v_full(y, i) && mbar_wait(&y->p_full[i & 1], (i >> 1) & 1, err))) break;
+                tc_fence_after();
 #pragma unroll
                 for (int t = 0; t < TERMS; ++t)
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk) {
-                        const uint32_t p = t < 2 ? tS + (i & 1) * kTile + (kk / 4) * 64 + t * 32 + (kk % 4) * 8
-                                                 : tT + (i & 1) * C::kThird + kk * 8;
-                        umma_bf16_ta(tO, p, v + ((kk * 2048) >> 4), idO, (i | t | kk) != 0);
+                        const uint32_t p = t < 2 && !C::kApart ? tS + (i & 1) * kTile + t * 64 + kk * 8
+                                                               : tT + (i & 1) * C::kThird + kk * 8;
+                        umma_bf16_ta(tO + (i & 1) * HD, p, v + ((kk * 2048) >> 4), idO, i >= 2 || (t | kk) != 0);
                     }
-                umma_commit(&y->free[u % U]);
-                umma_commit(&y->o_done[i & 1]);
+                umma_commit(&y->v_done[i % VU]);
+                if (!C::kApart && j < nt) {
+                    ok = k_full(y, j);
+                    tc_fence_after();
+                    scores(j);
+                }
             }
-            __syncwarp();
-            if (i + 2 < nt) ok = scores(i + 2);
         }
-    } else {
-        const int quarter = warp & 3, half0 = half * (kTile / 2);
+    } else if (warp >= kFirstSoft) {
+        // group g takes every other tile, a thread one query row of it
+        const int g = (warp - kFirstSoft) >> 2, quarter = warp & 3;
         const uint32_t mylane = (uint32_t)(quarter * 32) << 16;
+        const uint32_t ts = tS + g * kTile + mylane, tt = tT + g * C::kThird + mylane, to = tO + g * HD + mylane;
         const bool live = quarter * 32 < rows;  // (rows behind the last: the warp only keeps the barriers)
         if (sq.n < 64) word &= (1ull << sq.n) - 1;
         float m = kNone, l = 0.f;
         bool ok = true;
-        for (int i = 0; i < nt; ++i) {
-            ok &= mbar_wait(&y->s_full[i & 1], (i >> 1) & 1, err);
+        for (int i = g; i < nt; i += 2) {
+            ok &= s_done(y, i);
             tc_fence_after();
             const int at = (t0 + i) * kTile;
             const bool tail = at + kTile > sq.len;
             if (live) {
-                const uint32_t ts = tS + (i & 1) * kTile + half0 + mylane;
-                float x[64];
-                auto read = [&]() {
+                float x[kTile];
 #pragma unroll
-                    for (int e = 0; e < 64; e += 16) tmem_ld16(ts + e, x + e);
-                    tmem_ld_wait();
-                    pin<64>(x);
-                    if (tail) {
+                for (int e = 0; e < kTile; e += 16) tmem_ld16(ts + e, x + e);
+                tmem_ld_wait();
+                pin<kTile>(x);
+                if (C::kApart) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&y->s_read[g]);
+                }
+                if (tail) {
 #pragma unroll
-                        for (int w = 0; w < 64; w += 32) {
-                            const uint32_t see = seen32(word, at + half0 + w - sq.len);
+                    for (int w = 0; w < kTile; w += 32) {
+                        const uint32_t see = seen32(word, at + w - sq.len);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((see >> e) & 1)) x[w + e] = -INFINITY;
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!((see >> e) & 1)) x[w + e] = -INFINITY;
                     }
-                };
-                auto largest = [&]() {
-                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                }
+                float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int e = 0; e < 64; e += 8)
+                for (int e = 0; e < kTile; e += 8)
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) t4[w] = fmaxf(fmaxf(t4[w], x[e + 2 * w]), x[e + 2 * w + 1]);
-                    return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-                };
-                read();
-                const float top = kScaled ? largest() : largest() * c;  // (the scale is positive)
-                if (pair_any(quarter, top > m + kRaise)) {
-                    // raise the maxima of these rows to those so far; scale O and the sums
-                    tops[half * kRows + row] = top;
-                    pair_any(quarter, false);
-                    const float best = fmaxf(fmaxf(m, top), tops[(half ^ 1) * kRows + row]);
-                    const float scale = ex2(m - best);
+                    for (int w = 0; w < 4; ++w) t4[w] = fmaxf(fmaxf(t4[w], x[e + 2 * w]), x[e + 2 * w + 1]);
+                float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                if (!kScaled) top *= c;  // (the scale is positive)
+                // PV(i - 2) is done: P and O are this group's again (not apart: S(i) was issued after it)
+                if (C::kApart && i >= 2) ok &= pv_done(y, i - 2);
+                tc_fence_after();
+                if (__any_sync(0xFFFFFFFFu, top > m + kRaise)) {
+                    // raise the warp's maxima to those of the rows so far; scale O and the sums
+                    const float best = fmaxf(m, top), scale = ex2(m - best);
                     m = best;
                     l *= scale;
-                    if (i > 0) {
-                        ok &= mbar_wait(&y->o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, err);
-                        tc_fence_after();
+                    if (i >= 2) {
 #pragma unroll 1
-                        for (int d = half * (HD / 2); d < (half + 1) * (HD / 2); d += 16) {
+                        for (int d = 0; d < HD; d += 16) {
                             float o[16];
-                            tmem_ld16(tO + mylane + d, o);
+                            tmem_ld16(to + d, o);
                             tmem_ld_wait();
                             pin<16>(o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] *= scale;
-                            tmem_st16(tO + mylane + d, o);
+                            tmem_st16(to + d, o);
                         }
                     }
-                    pair_any(quarter, false);  // (tops is read before it is written again)
                 }
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int w0 = 0; w0 < 64; w0 += 32) {
+                for (int w0 = 0; w0 < kTile; w0 += 32) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        x[w0 + e] = ex2(kScaled ? x[w0 + e] - m : fmaf(x[w0 + e], c, -m));
-                        sum[e & 3] += x[w0 + e];
+                    for (int e = 0; e < 32; e += 2) {
+                        float &x0 = x[w0 + e], &x1 = x[w0 + e + 1];
+                        fma2(x0, x1, kScaled ? 1.f : c, m, m);
+                        x0 = ex2(x0);
+                        x1 = ex2(x1);
+                        sum[(e >> 1) & 1] = __ffma2_rn(make_float2(x0, x1), make_float2(1.f, 1.f), sum[(e >> 1) & 1]);
                     }
 #pragma unroll
                     for (int t = 0; t < TERMS; ++t) {
@@ -918,53 +984,66 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 x1 -= bf_hi(w[e]);
                             }
                         }
-                        tmem_st16((t < 2 ? ts + t * 32 : tT + (i & 1) * C::kThird + half * 32 + mylane) + w0 / 2, w);
+                        tmem_st16((t < 2 && !C::kApart ? ts + t * 64 : tt) + w0 / 2, w);
                     }
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_st_wait();
+            } else if (C::kApart) {
+                if (lane == 0) mbar_arrive(&y->s_read[g]);
+                if (i >= 2) ok &= pv_done(y, i - 2);
             }
             tc_fence_before();
-            if (tail && half == 0) {
-                const int u = 2 * i + 1, node = at + row - sq.len;
-                ok &= mbar_wait(&y->full[u % U], (u / U) & 1, err);
-                if (node >= 0) mend_v<HD>(sm + (u % U) * C::kKv, row, node, sq.n, y->bad);
+            if (tail) {
+                const int node = at + row - sq.len;
+                ok &= v_full(y, i);
+                if (node >= 0) mend_v<HD>(sm + (KU + i % VU) * C::kKv, row, node, sq.n, y->bad);
                 async_fence();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&y->p_full[i & 1]);
+            if (lane == 0) mbar_arrive(&y->p_full[g]);
         }
-        if (nt > 0) ok &= mbar_wait(&y->o_done[(nt - 1) & 1], ((nt - 1) >> 1) & 1, err);
+        if (nt > 0) ok &= pv_done(y, nt - 1);  // (and with it every product: the ring is free)
         tc_fence_after();
-        const bool all = !soft_any(!ok);  // (and every copy has landed: the ring is free)
-        if (half == 1) tops[row] = l;
-        if (live) {
-#pragma unroll 1
-            for (int d = half * (HD / 2); d < (half + 1) * (HD / 2); d += 16) {
-                float o[16];
-                if (nt > 0) {
-                    tmem_ld16(tO + mylane + d, o);
-                    tmem_ld_wait();
-                    pin<16>(o);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = 0.f;
-                }
-#pragma unroll
-                for (int e = 0; e < 16; e += 4)
-                    *reinterpret_cast<float4 *>(Os + o_at<HD, true>(row, d + e)) =
-                        make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            }
-        }
+        if (!ok) *err = 1;
+        gm[g * kRows + row] = m;
         soft_sync();
-        if (half == 0) {
-            mref[row] = m;
-            lsum[row] = all ? l + tops[row] : __uint_as_float(0x7FC00000u);  // a wait ran out: NaN
-        }
-        if (y->bad[0] | y->bad[1]) {
+        // the groups' O to the larger maximum: group 0 writes, group 1 adds
+        const float best = fmaxf(m, gm[(g ^ 1) * kRows + row]), scale = g < nt ? ex2(m - best) : 0.f;
+        l *= scale;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            if (g == h) {
+                if (live) {
+#pragma unroll 1
+                    for (int d = 0; d < HD; d += 16) {
+                        float o[16];
+                        if (g < nt) {
+                            tmem_ld16(to + d, o);
+                            tmem_ld_wait();
+                            pin<16>(o);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            float4 *z = reinterpret_cast<float4 *>(Os + o_at<HD, true>(row, d + e));
+                            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (h) w = *z;
+                            w.x = fmaf(scale, o[e], w.x), w.y = fmaf(scale, o[e + 1], w.y);
+                            w.z = fmaf(scale, o[e + 2], w.z), w.w = fmaf(scale, o[e + 3], w.w);
+                            *z = w;
+                        }
+                    }
+                }
+                lsum[row] = h ? lsum[row] + l : l;
+                mref[row] = best;
+            }
             soft_sync();
-            add_taken_out<HD, TERMS, true>(a, b, kvh, G, row0, rows, sq, y->bad, mref, Os, tid);
         }
+        if (*err && g == 0) lsum[row] = __uint_as_float(0x7FC00000u);  // a wait ran out: NaN
+        if (y->bad[0] | y->bad[1]) add_taken_out<HD, TERMS, true>(a, b, kvh, G, row0, rows, sq, y->bad, mref, Os, st);
     }
     __syncwarp();
     __syncthreads();
