@@ -129,6 +129,7 @@ def load(path: str | None = None):
     L.mk_twell_down.argtypes = [_VP, _I32, _I32, _VP, _VP, _VP]
     L.mk_twell_ffn.argtypes = [_VP, _VP, _VP, _I32, _I32, _VP, _VP, _VP, _VP]
     L.mk_prefill.argtypes = [_VP, _VP, _I32, _I32, _VP, _VP, _VP]
+    L.mk_verify.argtypes = [_VP, _VP, _VP, _I32, _I32, _VP, _VP, _VP]
     L.mk_tc_gemm.argtypes = [_VP, _I32, _I32, _VP, _VP, _I32, _VP, _VP, _VP, _VP]
     L.mk_rope_append.argtypes = [_VP, _VP]  # a packed record, or byref of the structure
     L.mk_rope_frequencies.argtypes = [_I32, _I32] + [ctypes.c_double] * 5 + [_VP, ctypes.POINTER(ctypes.c_float)]
@@ -563,6 +564,35 @@ class Megakernel:
         check(load().mk_prefill(self.h, d_tokens.data_ptr(), int(d_tokens.numel()), int(start_pos),
                                 logits.data_ptr() if logits is not None else None, out_token.data_ptr(),
                                 _stream_ptr(stream)))
+
+    def verify(self, d_tokens, d_parents, start_pos: int, out_tokens, logits=None, stream=None) -> None:
+        """mk_verify: the n nodes of a drafted tree (int32 CUDA tensors [n]) behind the committed positions
+        [0, start_pos) of slot 0; out_tokens int32 CUDA tensor [n], logits float32 CUDA tensor [n][vocab] or None."""
+        n = int(d_tokens.numel())
+        if int(d_parents.numel()) != n or int(out_tokens.numel()) < n:
+            _bad("d_parents and out_tokens must have as many entries as d_tokens")
+        check(load().mk_verify(self.h, d_tokens.data_ptr(), d_parents.data_ptr(), n, int(start_pos),
+                               logits.data_ptr() if logits is not None else None, out_tokens.data_ptr(),
+                               _stream_ptr(stream)))
+
+    def accept(self, tokens, parents, draws, start_pos: int, stream=None):
+        """The path of a verified tree that its draws accept (host whole numbers, as given to and returned by
+        verify): its cache rows move up to start_pos .., and the nodes come back as a list. Decoding goes on at
+        start_pos + len(path) with token draws[path[-1]]."""
+        import torch
+        path = tree_accept(tokens, parents, draws)
+        if path[-1] != len(path) - 1:  # else every row is in its place
+            _, k, v = self._keep
+            B = self.max_batch
+            host = torch.zeros(2 + len(path), B, dtype=torch.int32)
+            host[0, 0], host[1, 0] = int(start_pos), len(path)
+            host[2:, 0] = torch.tensor(path, dtype=torch.int32)
+            s = stream or torch.cuda.current_stream(k.device)
+            with torch.cuda.stream(s):
+                dev = host.to(k.device)
+                nodes = dev[2:].T.contiguous()
+                kv_compact(k, v, dev[0], nodes, dev[1], stream=s)
+        return path
 
     def step_unfused(self, token: int, pos: int, out_token, logits=None, stream=None) -> None:
         check(load().mk_decode_step_unfused(self.h, int(token), int(pos),

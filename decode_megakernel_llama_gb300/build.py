@@ -12,8 +12,11 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmk.so")
 LIB_CHECKED = os.path.join(BUILD, "libmk_checked.so")
 SOURCES = ["mk_kernel_hd64.cu", "mk_kernel_hd128.cu", "mk_kernel.cu", "mk_host.cpp", "mk_noalloc.cu", "mk_w2a8.cu",
-           "mk_prefill.cu", "mk_twell.cu", "mk_rope.cu", "mk_tree.cu", "mk_kv.cu"]
-DEPS = SOURCES + ["mk_kernel.cuh", "mk_plan.h", "mk_internal.h", "mk_prefill.h", "mk_ops.h", "mk_tc.cuh", "mk_tree_attn.cuh"]
+           "mk_prefill.cu", "mk_twell.cu"]
+DEPS = SOURCES + ["mk_kernel.cuh", "mk_plan.h", "mk_internal.h", "mk_prefill.h"]
+# the standalone operators: units of their own beside the megakernel's
+OP_SOURCES = ["mk_rope.cu", "mk_tree.cu", "mk_kv.cu"]
+OP_DEPS = OP_SOURCES + ["mk_ops.h", "mk_tc.cuh", "mk_tree_attn.cuh"]
 
 
 def nvcc() -> str:
@@ -32,7 +35,7 @@ def _stale(lib: str) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, s) for s in DEPS] + [os.path.join(ROOT, "include", "mk.h")]
+    deps = [os.path.join(CSRC, s) for s in DEPS + OP_DEPS] + [os.path.join(ROOT, "include", "mk.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -46,7 +49,7 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
     nv = nvcc()
     procs, objs = [], []
     tag = ".chk" if checked else ""
-    for s in SOURCES:
+    for s in SOURCES + OP_SOURCES:
         obj = os.path.join(BUILD, s + tag + ".o")
         extra = ["-Xptxas", "-v"] if (verbose and s.endswith(".cu")) else []
         if checked:

@@ -20,6 +20,7 @@
 
 #include "../../include/mk.h"
 #include "mk_plan.h"
+#include "mk_ops.h"
 #include "mk_prefill.h"
 
 extern "C" cudaError_t mk_kernel_configure(void);
@@ -31,10 +32,12 @@ extern "C" cudaError_t mk_convert_bf16_f16(const void *src, void *dst, size_t n,
 extern "C" size_t mk_filter_lists_keys(int B, int V);
 extern "C" cudaError_t mk_filtered_draw_batch(const float *logits, int B, int V, int K, float top_p, float inv_temp,
                                               const int32_t *positions, int pos0, int slot0, uint64_t seed,
-                                              unsigned long long *lists, int32_t *out_tokens, cudaStream_t stream);
+                                              unsigned long long *lists, int32_t *out_tokens, cudaStream_t stream,
+                                              int slot_step = 1);
 extern "C" cudaError_t mk_sampled_draw_batch(const float *logits, int B, int V, float inv_temp,
                                              const int32_t *positions, int pos0, uint64_t seed,
-                                             unsigned long long *keys, int32_t *out_tokens, cudaStream_t stream);
+                                             unsigned long long *keys, int32_t *out_tokens, cudaStream_t stream,
+                                             int slot_step = 1);
 extern "C" cudaError_t mk_batch_final_norm(const float *x, int B, int d, const uint16_t *gain, float eps, uint16_t *hi,
                                            uint16_t *lo, cudaStream_t stream);
 extern "C" cudaError_t mk_noise_launch(int n, int pos, int slot, uint64_t seed, const uint32_t *words,
@@ -705,6 +708,16 @@ struct mk_handle {
     // caller asks for none) and the candidate lists / slice keys
     float *pd_logits = nullptr;
     unsigned long long *pd_lists = nullptr;
+    // verification of drafted trees (mk_verify), made on its first call: the RoPE
+    // frequencies, the tree's arrays, and logits and draw lists of MK_MAX_TREE
+    // nodes; the attention's workspace, grown as needed
+    void *vf_mem = nullptr;
+    mkpf::Tree vf;
+    float *vf_logits = nullptr;
+    unsigned long long *vf_lists = nullptr;
+    CUtensorMap vf_embed;
+    void *vf_work = nullptr;
+    int64_t vf_work_bytes = 0;
 };
 
 namespace {
@@ -754,6 +767,86 @@ int launch(mk_handle *h, int32_t token, const int32_t *d_token, int32_t position
     e = mk_filtered_draw_batch(logits, 1, h->cfg.vocab, K, h->top_p, h->inv_temp, d_pos, d_pos ? 0 : position, bslot,
                                h->seed, h->pd_lists, out_token, stream);
     if (e != cudaSuccess) return cuda_fail(e, "filtered draw");
+    return MK_OK;
+}
+
+// Tensor maps of the weights (the first call) and scratch for n prompt tokens.
+int prefill_ready(mk_handle *h, int n) {
+    cudaError_t e = cudaSuccess;
+    const mk_config &c = h->cfg;
+    const int d = c.d_model, hd = c.head_dim, qd = c.n_heads * hd, kvd = c.n_kv_heads * hd, F = c.ffn_dim;
+    if (!h->pf_ready) {
+        mkpf::Model &m = h->pf_model;
+        m.L = c.n_layers; m.d = d; m.Hq = c.n_heads; m.Hkv = c.n_kv_heads; m.hd = hd; m.F = F; m.V = c.vocab;
+        m.max_seq = c.max_seq; m.n_sm = h->im.n_sm; m.eps = c.rms_eps;
+        m.embed = h->base.embed;
+        m.final_norm = h->base.final_norm;
+        m.rope = h->base.rope;
+        m.kc = h->base.kc;
+        m.vc = h->base.vc;
+        m.kv_layer_stride = (size_t)c.max_batch * c.n_kv_heads * c.max_seq * hd;
+        m.maps.resize(c.n_layers);
+        m.attn_norm.resize(c.n_layers);
+        m.mlp_norm.resize(c.n_layers);
+        for (int l = 0; l < c.n_layers; ++l) {
+            const mk::LayerW &lw = h->im.lws[l];
+            mkpf::LayerMaps &lm = m.maps[l];
+            m.attn_norm[l] = lw.attn_norm;
+            m.mlp_norm[l] = lw.mlp_norm;
+            if (!mkpf::encode_weight_map(&lm.wq, lw.wq, qd, d) || !mkpf::encode_weight_map(&lm.wk, lw.wk, kvd, d) ||
+                !mkpf::encode_weight_map(&lm.wv, lw.wv, kvd, d) || !mkpf::encode_weight_map(&lm.wo, lw.wo, d, qd) ||
+                !mkpf::encode_gated_map(&lm.wg, lw.w_gate, F, d) || !mkpf::encode_gated_map(&lm.wu, lw.w_up, F, d) ||
+                !mkpf::encode_weight_map(&lm.wd, lw.w_down, d, F))
+                return fail(MK_ERR_UNSUPPORTED, "could not encode the weights' tensor maps");
+        }
+        h->pf_ready = true;
+    }
+    if (h->pf.cap < n) {
+        // scratch for n tokens: residual and q|k|v (fp32), the hi/lo bf16
+        // input of the projections from d or Hq hd columns, and that of the
+        // down projection (h = silu(g) * u)
+        const size_t kmax = std::max(d, qd), qkv = qd + 2 * kvd;
+        // K-split partials: the largest the q/k/v, O and down projections
+        // use (gate/up runs in one pass)
+        const int nsm = h->im.n_sm;
+        const int qkv_rows[3] = {qd, kvd, kvd};
+        const size_t work = std::max(std::max(mkpf::gemm_workspace_floats(d, n, qd, nsm, true),
+                                              mkpf::gemm_workspace_floats(d, n, F, nsm, true)),
+                                     mkpf::gemm_multi_workspace_floats(3, qkv_rows, n, d, nsm));
+        // (+ 256 bytes of alignment for each of the 8 pieces)
+        const size_t bytes = 4 * (size_t)n * (d + qkv) + 2 * 2 * (size_t)n * (kmax + F) +
+                             8 * (size_t)2 * h->im.n_sm + 4 * work + 4 * 512;
+        int32_t err_keep = 0;
+        if (h->pf.err) cudaMemcpy(&err_keep, h->pf.err, sizeof err_keep, cudaMemcpyDeviceToHost);
+        void *mem = nullptr;
+        e = cudaMalloc(&mem, bytes);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(prefill scratch)");
+        if (h->pf_mem) {
+            cudaDeviceSynchronize();
+            cudaFree(h->pf_mem);
+        }
+        h->pf_mem = mem;
+        char *b = static_cast<char *>(mem);
+        auto take = [&](size_t nbytes) {
+            char *at = b;
+            b += (nbytes + 255) & ~size_t(255);
+            return at;
+        };
+        mkpf::Scratch &sc = h->pf;
+        sc.cap = n;
+        sc.X = reinterpret_cast<float *>(take(4 * (size_t)n * d));
+        sc.QKV = reinterpret_cast<float *>(take(4 * (size_t)n * qkv));
+        sc.Hhi = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * F));
+        sc.Hlo = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * F));
+        sc.Ahi = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * kmax));
+        sc.Alo = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * kmax));
+        sc.keys = reinterpret_cast<unsigned long long *>(take(8 * (size_t)2 * h->im.n_sm));
+        sc.work = reinterpret_cast<float *>(take(4 * work));
+        sc.work_floats = work;
+        sc.err = reinterpret_cast<int *>(take(4));
+        e = cudaMemcpy(sc.err, &err_keep, sizeof err_keep, cudaMemcpyHostToDevice);
+        if (e != cudaSuccess) return cuda_fail(e, "prefill status");
+    }
     return MK_OK;
 }
 
@@ -1082,80 +1175,8 @@ int mk_prefill(mk_handle *h, const int32_t *d_tokens, int32_t n, int32_t start_p
         return fail(MK_ERR_INVALID_ARG, "prompt positions outside [0, max_seq)");
     cudaError_t e = cudaSetDevice(h->device);
     if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
-    const mk_config &c = h->cfg;
-    const int d = c.d_model, hd = c.head_dim, qd = c.n_heads * hd, kvd = c.n_kv_heads * hd, F = c.ffn_dim;
-    if (!h->pf_ready) {
-        mkpf::Model &m = h->pf_model;
-        m.L = c.n_layers; m.d = d; m.Hq = c.n_heads; m.Hkv = c.n_kv_heads; m.hd = hd; m.F = F; m.V = c.vocab;
-        m.max_seq = c.max_seq; m.n_sm = h->im.n_sm; m.eps = c.rms_eps;
-        m.embed = h->base.embed;
-        m.final_norm = h->base.final_norm;
-        m.rope = h->base.rope;
-        m.kc = h->base.kc;
-        m.vc = h->base.vc;
-        m.kv_layer_stride = (size_t)c.max_batch * c.n_kv_heads * c.max_seq * hd;
-        m.maps.resize(c.n_layers);
-        m.attn_norm.resize(c.n_layers);
-        m.mlp_norm.resize(c.n_layers);
-        for (int l = 0; l < c.n_layers; ++l) {
-            const mk::LayerW &lw = h->im.lws[l];
-            mkpf::LayerMaps &lm = m.maps[l];
-            m.attn_norm[l] = lw.attn_norm;
-            m.mlp_norm[l] = lw.mlp_norm;
-            if (!mkpf::encode_weight_map(&lm.wq, lw.wq, qd, d) || !mkpf::encode_weight_map(&lm.wk, lw.wk, kvd, d) ||
-                !mkpf::encode_weight_map(&lm.wv, lw.wv, kvd, d) || !mkpf::encode_weight_map(&lm.wo, lw.wo, d, qd) ||
-                !mkpf::encode_gated_map(&lm.wg, lw.w_gate, F, d) || !mkpf::encode_gated_map(&lm.wu, lw.w_up, F, d) ||
-                !mkpf::encode_weight_map(&lm.wd, lw.w_down, d, F))
-                return fail(MK_ERR_UNSUPPORTED, "could not encode the weights' tensor maps");
-        }
-        h->pf_ready = true;
-    }
-    if (h->pf.cap < n) {
-        // scratch for n tokens: residual and q|k|v (fp32), the hi/lo bf16
-        // input of the projections from d or Hq hd columns, and that of the
-        // down projection (h = silu(g) * u)
-        const size_t kmax = std::max(d, qd), qkv = qd + 2 * kvd;
-        // K-split partials: the largest the q/k/v, O and down projections
-        // use (gate/up runs in one pass)
-        const int nsm = h->im.n_sm;
-        const int qkv_rows[3] = {qd, kvd, kvd};
-        const size_t work = std::max(std::max(mkpf::gemm_workspace_floats(d, n, qd, nsm, true),
-                                              mkpf::gemm_workspace_floats(d, n, F, nsm, true)),
-                                     mkpf::gemm_multi_workspace_floats(3, qkv_rows, n, d, nsm));
-        // (+ 256 bytes of alignment for each of the 8 pieces)
-        const size_t bytes = 4 * (size_t)n * (d + qkv) + 2 * 2 * (size_t)n * (kmax + F) +
-                             8 * (size_t)2 * h->im.n_sm + 4 * work + 4 * 512;
-        int32_t err_keep = 0;
-        if (h->pf.err) cudaMemcpy(&err_keep, h->pf.err, sizeof err_keep, cudaMemcpyDeviceToHost);
-        void *mem = nullptr;
-        e = cudaMalloc(&mem, bytes);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(prefill scratch)");
-        if (h->pf_mem) {
-            cudaDeviceSynchronize();
-            cudaFree(h->pf_mem);
-        }
-        h->pf_mem = mem;
-        char *b = static_cast<char *>(mem);
-        auto take = [&](size_t nbytes) {
-            char *at = b;
-            b += (nbytes + 255) & ~size_t(255);
-            return at;
-        };
-        mkpf::Scratch &sc = h->pf;
-        sc.cap = n;
-        sc.X = reinterpret_cast<float *>(take(4 * (size_t)n * d));
-        sc.QKV = reinterpret_cast<float *>(take(4 * (size_t)n * qkv));
-        sc.Hhi = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * F));
-        sc.Hlo = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * F));
-        sc.Ahi = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * kmax));
-        sc.Alo = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * kmax));
-        sc.keys = reinterpret_cast<unsigned long long *>(take(8 * (size_t)2 * h->im.n_sm));
-        sc.work = reinterpret_cast<float *>(take(4 * work));
-        sc.work_floats = work;
-        sc.err = reinterpret_cast<int *>(take(4));
-        e = cudaMemcpy(sc.err, &err_keep, sizeof err_keep, cudaMemcpyHostToDevice);
-        if (e != cudaSuccess) return cuda_fail(e, "prefill status");
-    }
+    const int rc = prefill_ready(h, n);
+    if (rc) return rc;
     // with sampling on, the token of the last position is drawn as the decode
     // step at that position would draw it (same noise, same filter)
     const bool sampled = h->inv_temp > 0.f;
@@ -1184,6 +1205,77 @@ int mk_prefill(mk_handle *h, const int32_t *d_tokens, int32_t n, int32_t start_p
                                       out_token, (cudaStream_t)stream);
         if (e != cudaSuccess) return cuda_fail(e, "prefill draw");
     }
+    return MK_OK;
+}
+
+int mk_verify(mk_handle *h, const int32_t *d_tokens, const int32_t *d_parents, int32_t n, int32_t start_pos,
+              float *out_logits, int32_t *out_tokens, void *stream) {
+    if (!h || !d_tokens || !d_parents || !out_tokens)
+        return fail(MK_ERR_INVALID_ARG, "handle, d_tokens, d_parents or out_tokens is NULL");
+    if (n < 1 || n > MK_MAX_TREE) return fail(MK_ERR_INVALID_ARG, "n outside [1, MK_MAX_TREE]");
+    if (start_pos < 0 || (int64_t)start_pos + n > h->cfg.max_seq)
+        return fail(MK_ERR_INVALID_ARG, "tree rows outside [0, max_seq)");
+    cudaError_t e = cudaSetDevice(h->device);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+    // (scratch for a whole tree at once: a later, larger one allocates nothing)
+    const int rc = prefill_ready(h, std::max(h->pf.cap, std::min(MK_MAX_TREE, h->cfg.max_seq)));
+    if (rc) return rc;
+    const mk_config &c = h->cfg;
+    if (!h->vf_mem) {
+        if (!mkpf::encode_weight_map(&h->vf_embed, h->base.embed, c.vocab, c.d_model))
+            return fail(MK_ERR_UNSUPPORTED, "could not encode the embedding's tensor map");
+        const int half = c.head_dim / 2, T = MK_MAX_TREE;
+        std::vector<double> freq(half);
+        float mscale;
+        const int frc = mk_rope_frequencies(MK_ROPE_PLAIN, c.head_dim, c.rope_theta, 1.0, 1.0, 1.0, 2.0, freq.data(),
+                                            &mscale);
+        if (frc) return frc;
+        const size_t o_mask = 8 * (size_t)half, o_pos = o_mask + 8 * T, o_row = o_pos + 4 * T, o_len = o_row + 4 * T,
+                     o_list = (o_len + 4 + 255) & ~size_t(255),
+                     o_log = (o_list + 8 * mk_filter_lists_keys(T, c.vocab) + 255) & ~size_t(255),
+                     bytes = o_log + 4 * (size_t)T * c.vocab;
+        char *m = nullptr;
+        e = cudaMalloc(&m, bytes);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(tree scratch)");
+        e = cudaMemcpy(m, freq.data(), 8 * (size_t)half, cudaMemcpyHostToDevice);
+        if (e != cudaSuccess) {
+            cudaFree(m);
+            return cuda_fail(e, "RoPE frequencies");
+        }
+        h->vf_mem = m;
+        h->vf.inv_freq = reinterpret_cast<double *>(m);
+        h->vf.masks = reinterpret_cast<uint64_t *>(m + o_mask);
+        h->vf.positions = reinterpret_cast<int32_t *>(m + o_pos);
+        h->vf.rows = reinterpret_cast<int32_t *>(m + o_row);
+        h->vf.length = reinterpret_cast<int32_t *>(m + o_len);
+        h->vf_lists = reinterpret_cast<unsigned long long *>(m + o_list);
+        h->vf_logits = reinterpret_cast<float *>(m + o_log);
+    }
+    mkpf::Tree t = h->vf;
+    const int64_t need = mkpf::tree_work_bytes(h->pf_model, n, start_pos);
+    if (need > h->vf_work_bytes) {
+        void *m = nullptr;
+        e = cudaMalloc(&m, need);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(tree attention workspace)");
+        if (h->vf_work) {
+            cudaDeviceSynchronize();
+            cudaFree(h->vf_work);
+        }
+        h->vf_work = m;
+        h->vf_work_bytes = need;
+    }
+    t.work = static_cast<float *>(h->vf_work);
+    t.work_floats = h->vf_work_bytes / 4;
+    float *logits = out_logits ? out_logits : h->vf_logits;
+    const cudaStream_t s = (cudaStream_t)stream;
+    e = mkpf::run_tree(h->pf_model, h->pf, t, h->vf_embed, d_tokens, d_parents, n, start_pos, logits, s);
+    if (e != cudaSuccess) return cuda_fail(e, "tree launch");
+    const bool filtered = h->inv_temp > 0.f && (h->top_k > 0 || h->top_p < 1.f);
+    e = filtered ? mk_filtered_draw_batch(logits, n, c.vocab, h->top_k > 0 ? h->top_k : mk::kMaxTopK, h->top_p,
+                                          h->inv_temp, t.positions, 0, 0, h->seed, h->vf_lists, out_tokens, s, 0)
+                 : mk_sampled_draw_batch(logits, n, c.vocab, h->inv_temp, t.positions, 0, h->seed, h->vf_lists,
+                                         out_tokens, s, 0);
+    if (e != cudaSuccess) return cuda_fail(e, "tree draw");
     return MK_OK;
 }
 
@@ -1348,6 +1440,8 @@ void mk_destroy(mk_handle *h) {
     if (h->blm_mem) cudaFree(h->blm_mem);  // holds bf_logits and bf_lists
     if (h->pd_logits) cudaFree(h->pd_logits);
     if (h->pd_lists) cudaFree(h->pd_lists);
+    if (h->vf_mem) cudaFree(h->vf_mem);
+    if (h->vf_work) cudaFree(h->vf_work);
     delete h;
 }
 

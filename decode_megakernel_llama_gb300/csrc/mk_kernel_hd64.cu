@@ -54,7 +54,8 @@ extern "C" cudaError_t mk_noise_launch(int n, int pos, int slot, uint64_t seed, 
 // Draws from logits [B][V] already in memory, for a fused batched step with a
 // top-k / top-p filter (its LM head writes every sequence's logits) and for a
 // prefill's last position: sequence b draws with KV slot b's noise at
-// position positions[b] (positions NULL: pos0). Filtered:
+// position positions[b] (positions NULL: pos0); with slot_step 0 (the nodes of
+// a drafted tree, all in one sequence) every row draws with one slot's. Filtered:
 //   filter_lists: CTA (slice j, sequence b) keys entries [1024 j, 1024 j +
 //     1024) of sequence b's logits and publishes its top_k best, in order, as
 //     list j of sequence b;
@@ -84,22 +85,22 @@ __global__ void __launch_bounds__(mk::kConsumerThreads) filter_lists(const float
 __global__ void __launch_bounds__(mk::kConsumerThreads) filter_draw(const unsigned long long *lists, int nl, int K,
                                                                     float top_p, float inv_temp,
                                                                     const int32_t *positions, int pos0, int slot0,
-                                                                    uint32_t seed_lo, uint32_t seed_hi,
-                                                                    int32_t *out_tokens) {
+                                                                    int slot_step, uint32_t seed_lo,
+                                                                    uint32_t seed_hi, int32_t *out_tokens) {
     extern __shared__ unsigned long long g[];  // max(nl * K, 64) keys
     __shared__ int gcount;
     const int b = blockIdx.x;
     const int pos = positions ? positions[b] : pos0;
     const int tok = mk::draw_filtered(lists + (size_t)b * nl * mk::kMaxTopK, nl, K, top_p, inv_temp, pos,
-                                      slot0 + b, seed_lo, seed_hi, g, &gcount);
+                                      slot0 + b * slot_step, seed_lo, seed_hi, g, &gcount);
     if (threadIdx.x == 0) out_tokens[b] = tok;
 }
 
 // inv_temp > 0: the key of logit * inv_temp + noise; otherwise of the logit
 // itself (the greedy choice, lowest index on ties).
 __global__ void __launch_bounds__(256) sample_slices(const float *logits, int V, float inv_temp,
-                                                     const int32_t *positions, int pos0, uint32_t seed_lo,
-                                                     uint32_t seed_hi, unsigned long long *keys) {
+                                                     const int32_t *positions, int pos0, int slot_step,
+                                                     uint32_t seed_lo, uint32_t seed_hi, unsigned long long *keys) {
     __shared__ unsigned long long best8[8];
     const int b = blockIdx.y, j = blockIdx.x, base = j * kFilterSlice;
     const int pos = positions ? positions[b] : pos0;
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(256) sample_slices(const float *logits, int V,
     for (int i = threadIdx.x; i < kFilterSlice; i += blockDim.x) {
         const int e = base + i;
         if (e < V) {
-            const float z = inv_temp > 0.f ? lg[e] * inv_temp + mk::gumbel_noise((uint32_t)e, pos, b, seed_lo, seed_hi)
+            const float z = inv_temp > 0.f ? lg[e] * inv_temp + mk::gumbel_noise((uint32_t)e, pos, b * slot_step, seed_lo, seed_hi)
                                            : lg[e];
             const unsigned long long k = mk::argmax_key(z, (uint32_t)e);
             best = k > best ? k : best;
@@ -167,7 +168,8 @@ extern "C" size_t mk_filter_lists_keys(int B, int V) {
 
 extern "C" cudaError_t mk_filtered_draw_batch(const float *logits, int B, int V, int K, float top_p, float inv_temp,
                                               const int32_t *positions, int pos0, int slot0, uint64_t seed,
-                                              unsigned long long *lists, int32_t *out_tokens, cudaStream_t stream) {
+                                              unsigned long long *lists, int32_t *out_tokens, cudaStream_t stream,
+                                              int slot_step) {
     if (B < 1 || V < 1 || K < 1 || K > mk::kMaxTopK) return cudaErrorInvalidValue;
     const int nl = (V + kFilterSlice - 1) / kFilterSlice;
     const size_t smem = (size_t)(nl * K > 64 ? nl * K : 64) * sizeof(unsigned long long);
@@ -178,7 +180,7 @@ extern "C" cudaError_t mk_filtered_draw_batch(const float *logits, int B, int V,
         configured = smem;
     }
     filter_lists<<<dim3(nl, B), mk::kConsumerThreads, 0, stream>>>(logits, V, K, lists);
-    filter_draw<<<B, mk::kConsumerThreads, smem, stream>>>(lists, nl, K, top_p, inv_temp, positions, pos0, slot0,
+    filter_draw<<<B, mk::kConsumerThreads, smem, stream>>>(lists, nl, K, top_p, inv_temp, positions, pos0, slot0, slot_step,
                                                            (uint32_t)(seed & 0xFFFFFFFFu), (uint32_t)(seed >> 32),
                                                            out_tokens);
     return cudaGetLastError();
@@ -188,11 +190,12 @@ extern "C" cudaError_t mk_filtered_draw_batch(const float *logits, int B, int V,
 // of B sequences from their logits; keys: B * ceil(V / 1024) slots of scratch.
 extern "C" cudaError_t mk_sampled_draw_batch(const float *logits, int B, int V, float inv_temp,
                                              const int32_t *positions, int pos0, uint64_t seed,
-                                             unsigned long long *keys, int32_t *out_tokens, cudaStream_t stream) {
+                                             unsigned long long *keys, int32_t *out_tokens, cudaStream_t stream,
+                                             int slot_step) {
     if (B < 1 || V < 1 || !(inv_temp >= 0.f)) return cudaErrorInvalidValue;
     const int ns = (V + kFilterSlice - 1) / kFilterSlice;
-    sample_slices<<<dim3(ns, B), 256, 0, stream>>>(logits, V, inv_temp, positions, pos0, (uint32_t)(seed & 0xFFFFFFFFu),
-                                                   (uint32_t)(seed >> 32), keys);
+    sample_slices<<<dim3(ns, B), 256, 0, stream>>>(logits, V, inv_temp, positions, pos0, slot_step,
+                                                   (uint32_t)(seed & 0xFFFFFFFFu), (uint32_t)(seed >> 32), keys);
     sample_reduce<<<B, 32, 0, stream>>>(keys, ns, out_tokens);
     return cudaGetLastError();
 }

@@ -65,4 +65,9 @@ cudaError_t tree_attention_work_floats(const TreeArgs &a, int hd, bool f32, int 
 cudaError_t tree_masks_launch(const int32_t *parents, const int32_t *counts, int B, int T, uint64_t *masks,
                               int32_t *depths, cudaStream_t s);
 
+// One tree behind `start` committed rows: masks, positions (start + depth), rows
+// (start + index) of its n nodes, and *length = start.
+cudaError_t tree_plan_launch(const int32_t *parents, int n, int start, uint64_t *masks, int32_t *positions,
+                             int32_t *rows, int32_t *length, cudaStream_t s);
+
 }  // namespace mkops

@@ -38,6 +38,7 @@
 // memory, and returns.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
 
@@ -45,6 +46,7 @@
 #include <mutex>
 #include <vector>
 
+#include "mk_ops.h"
 #include "mk_prefill.h"
 
 namespace mkpf {
@@ -1206,6 +1208,76 @@ cudaError_t run(const Model &m, const Scratch &sc, const int32_t *d_tokens, int 
                        m.final_norm, m.eps, m.embed, m.V, d, out_logits, sc.keys)))
         return e;
     ok(launch_pdl(argmax_keys, dim3(1), dim3(256), 0, s, sc.keys, blocks, out_token));
+    return e;
+}
+
+namespace {
+
+mkops::TreeArgs tree_args(const Model &m, int n) {
+    mkops::TreeArgs a{};
+    a.B = 1, a.T = n, a.Hq = m.Hq, a.Hkv = m.Hkv, a.slots = 1, a.max_seq = m.max_seq;
+    a.scale = 1.0f / sqrtf((float)m.hd);
+    a.q_token = (m.Hq + 2 * m.Hkv) * (int64_t)m.hd, a.o_token = m.Hq * (int64_t)m.hd;
+    return a;
+}
+
+}  // namespace
+
+int64_t tree_work_bytes(const Model &m, int n, int pos0) {
+    mkops::TreeArgs a = tree_args(m, n);
+    int64_t floats = 0;
+    if (mkops::tree_attention_work_floats(a, m.hd, true, pos0, m.n_sm, &floats) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;  // the attention does without
+    }
+    return floats * 4;
+}
+
+cudaError_t run_tree(const Model &m, const Scratch &sc, const Tree &t, const CUtensorMap &embed_map,
+                     const int32_t *d_tokens, const int32_t *d_parents, int n, int pos0, float *logits,
+                     cudaStream_t s) {
+    const int d = m.d, hd = m.hd, F = m.F, qd = m.Hq * hd, kvd = m.Hkv * hd, qkv = qd + 2 * kvd;
+    cudaError_t e = cudaSuccess;
+    auto ok = [&](cudaError_t x) {
+        if (e == cudaSuccess) e = x;
+        return e == cudaSuccess;
+    };
+    ok(mkops::tree_plan_launch(d_parents, n, pos0, t.masks, t.positions, t.rows, t.length, s));
+    ok(launch_pdl(embed_rows, dim3(n), dim3(256), 0, s, m.embed, d_tokens, n, d, m.V, sc.X, sc.err));
+    ok(launch_pdl(norm_split, dim3(n), dim3(256), 0, s, sc.X, d, m.attn_norm[0], m.eps, sc.Ahi, sc.Alo));
+    for (int l = 0; l < m.L && e == cudaSuccess; ++l) {
+        const LayerMaps &lm = m.maps[l];
+        const size_t kv_off = (size_t)l * m.kv_layer_stride;
+        const CUtensorMap *maps[3] = {&lm.wq, &lm.wk, &lm.wv};
+        const int Ms[3] = {qd, kvd, kvd}, lds[3] = {qkv, qkv, qkv};
+        float *Ys[3] = {sc.QKV, sc.QKV + qd, sc.QKV + qd + kvd};
+        int Sq = 1;
+        ok(gemm_multi(3, maps, Ms, Ys, lds, sc.Ahi, sc.Alo, n, d, sc.err, m.n_sm, s, sc.work, sc.work_floats, &Sq));
+        if (Sq > 1)
+            ok(launch_pdl(sum_splits, dim3(256), dim3(256), 0, s, sc.work, Sq, n, qkv, sc.QKV, qkv,
+                          static_cast<const float *>(nullptr)));
+        // rotated by the nodes' depths, appended to consecutive rows
+        mkops::RopeArgs r{};
+        r.n = n, r.Hq = m.Hq, r.Hkv = m.Hkv, r.rot = hd, r.slots = 1, r.max_seq = m.max_seq, r.mscale = 1.f;
+        r.qkv_stride = r.q_stride = qkv;
+        r.qkv = r.q_out = sc.QKV;
+        r.kc = m.kc + kv_off, r.vc = m.vc + kv_off;
+        r.positions = t.positions, r.rows = t.rows, r.inv_freq = t.inv_freq;
+        ok(mkops::rope_append_launch(r, hd, true, s));
+        // every node over the committed rows and its ancestors, written as hi / lo terms
+        mkops::TreeArgs a = tree_args(m, n);
+        a.q = sc.QKV, a.out = sc.X, a.hi = sc.Ahi, a.lo = sc.Alo;
+        a.kc = r.kc, a.vc = r.vc, a.lengths = t.length, a.masks = t.masks, a.err = sc.err;
+        a.work = t.work, a.work_floats = t.work_floats;
+        ok(mkops::tree_attention_launch(a, hd, true, pos0, m.n_sm, s));
+        // as the prefill: O-projection, the gated MLP, the next norm (at last the final one)
+        ok(gemm(lm.wo, sc.Ahi, sc.Alo, d, n, qd, sc.X, d, sc.X, sc.work, sc.work_floats, sc.err, m.n_sm, s,
+                NormOut{m.mlp_norm[l], m.eps, sc.Ahi, sc.Alo}));
+        ok(gemm_gated(lm.wg, lm.wu, F, sc.Ahi, sc.Alo, n, d, sc.Hhi, sc.Hlo, sc.err, m.n_sm, s));
+        ok(gemm(lm.wd, sc.Hhi, sc.Hlo, d, n, F, sc.X, d, sc.X, sc.work, sc.work_floats, sc.err, m.n_sm, s,
+                NormOut{l + 1 < m.L ? m.attn_norm[l + 1] : m.final_norm, m.eps, sc.Ahi, sc.Alo}));
+    }
+    ok(gemm(embed_map, sc.Ahi, sc.Alo, m.V, n, d, logits, m.V, nullptr, nullptr, 0, sc.err, m.n_sm, s, NormOut{}));
     return e;
 }
 

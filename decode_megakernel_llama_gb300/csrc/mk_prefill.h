@@ -78,4 +78,24 @@ size_t gemm_multi_workspace_floats(int nseg, const int *M, int N, int K, int n_s
 cudaError_t run(const Model &m, const Scratch &sc, const int32_t *d_tokens, int n, int pos0, float *out_logits,
                 int32_t *out_token, cudaStream_t s);
 
+// A drafted tree's arrays on the device, of MK_MAX_TREE nodes, and the RoPE
+// frequencies and attention workspace its pass uses.
+struct Tree {
+    double *inv_freq = nullptr;  // [hd/2] radians per position
+    uint64_t *masks = nullptr;
+    int32_t *positions = nullptr, *rows = nullptr, *length = nullptr;
+    float *work = nullptr;
+    int64_t work_floats = 0;
+};
+
+// Bytes of workspace the tree's attention can use for n nodes behind pos0 rows.
+int64_t tree_work_bytes(const Model &m, int n, int pos0);
+
+// The n nodes d_tokens, d_parents of a drafted tree through every layer, behind
+// the cache's rows [0, pos0): node t's K/V row at pos0 + t, its position pos0 +
+// its depth (t.positions), the logits of every node into logits [n][V].
+cudaError_t run_tree(const Model &m, const Scratch &sc, const Tree &t, const CUtensorMap &embed_map,
+                     const int32_t *d_tokens, const int32_t *d_parents, int n, int pos0, float *logits,
+                     cudaStream_t s);
+
 }  // namespace mkpf

@@ -23,10 +23,11 @@
 namespace mkops {
 namespace {
 
-// One warp per sequence; lane l walks up from nodes l and l + 32.
+// One warp per sequence; lane l walks up from nodes l and l + 32. (rows and
+// length, of a single sequence, are the pass through a model's.)
 __global__ void __launch_bounds__(32) tree_masks(const int32_t *__restrict__ parents,
-                                                 const int32_t *__restrict__ counts, int T, uint64_t *masks,
-                                                 int32_t *depths) {
+                                                 const int32_t *__restrict__ counts, int T, int start,
+                                                 uint64_t *masks, int32_t *depths, int32_t *rows, int32_t *length) {
     __shared__ int32_t up[MK_MAX_TREE];
     const int b = blockIdx.x, n = counts ? min(max(counts[b], 0), T) : T;
     for (int t = threadIdx.x; t < n; t += 32) {
@@ -42,8 +43,10 @@ __global__ void __launch_bounds__(32) tree_masks(const int32_t *__restrict__ par
             ++depth;
         }
         masks[(int64_t)b * T + t] = m;
-        if (depths) depths[(int64_t)b * T + t] = depth;
+        if (depths) depths[(int64_t)b * T + t] = start + depth;
+        if (rows) rows[t] = start + t;
     }
+    if (length && threadIdx.x == 0) *length = start;
 }
 
 }  // namespace
@@ -249,7 +252,13 @@ cudaError_t tree_attention_work_floats(const TreeArgs &a, int hd, bool f32, int 
 
 cudaError_t tree_masks_launch(const int32_t *parents, const int32_t *counts, int B, int T, uint64_t *masks,
                               int32_t *depths, cudaStream_t s) {
-    tree_masks<<<B, 32, 0, s>>>(parents, counts, T, masks, depths);
+    tree_masks<<<B, 32, 0, s>>>(parents, counts, T, 0, masks, depths, nullptr, nullptr);
+    return cudaGetLastError();
+}
+
+cudaError_t tree_plan_launch(const int32_t *parents, int n, int start, uint64_t *masks, int32_t *positions,
+                             int32_t *rows, int32_t *length, cudaStream_t s) {
+    tree_masks<<<1, 32, 0, s>>>(parents, nullptr, n, start, masks, positions, rows, length);
     return cudaGetLastError();
 }
 

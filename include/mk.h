@@ -194,6 +194,29 @@ int mk_decode_step_batch(mk_handle *h, const int32_t *d_tokens, const int32_t *d
 int mk_prefill(mk_handle *h, const int32_t *d_tokens, int32_t n, int32_t start_pos, float *out_logits,
                int32_t *out_token, void *stream);
 
+/* Verification of a drafted tree behind batch slot 0's committed rows [0,
+ * start_pos): runs the n <= MK_MAX_TREE nodes d_tokens[0 .. n) (device int32)
+ * through the model in one pass and gives the model's token after each. Node
+ * t's parent is d_parents[t] < t (device int32; anything else makes it a root,
+ * a child of the last committed token); its position is start_pos + its depth;
+ * it attends over the committed rows, its ancestors and itself. Its key/value
+ * row goes to cache row start_pos + t, so start_pos + n must not exceed max_seq;
+ * the accepted path's rows then move up with mk_kv_compact (starts = start_pos,
+ * nodes = the path of mk_tree_accept), and decoding goes on at start_pos + the
+ * path's length. out_logits (device float [n][vocab], nullable) and
+ * out_tokens (device int32 [n]): per node what mk_decode_step would give after
+ * the same tokens (to rounding: greedy, or drawn with this handle's sampling and
+ * filter and the noise of the node's position). The projections run as in
+ * mk_prefill, rotation and append as mk_rope_append, attention as
+ * mk_tree_attention. The first call, and one whose attention wants more
+ * workspace than any before, allocates (on the handle's device, owned by it):
+ * not inside a captured graph. Errors as mk_prefill; one call in flight per
+ * handle.
+ * Source: as mk_prefill; checking drafted tokens in one pass follows
+ * Leviathan, Kalman, Matias (ICML 2023), with a tree instead of a chain. */
+int mk_verify(mk_handle *h, const int32_t *d_tokens, const int32_t *d_parents, int32_t n, int32_t start_pos,
+              float *out_logits, int32_t *out_tokens, void *stream);
+
 /* The prefill's tensor-core contraction on its own:
  * d_y[n][m] = sum_k W[m][k] (Bhi[n][k] + Blo[n][k]) (+ d_r[n][m] if d_r is
  * not NULL; d_r may equal d_y) for m < M, n < N, with W = d_w bf16 [M][K],
