@@ -311,12 +311,10 @@ def _need(t, what: str, dtype, shape, like, dense: bool = True) -> None:
         _bad(f"{what} must be contiguous")
 
 
-def _run_on(t, stream, fn, *args) -> None:
-    """fn(*args, stream pointer) with t's device current; without a stream, on that device's current one."""
-    import torch
-    d = t.get_device()
+def _run_on(torch, d: int, stream, fn, *args) -> None:
+    """fn(*args, stream pointer) with CUDA device d current; without a stream, on that device's current one."""
     if d < 0:
-        _bad(f"tensors must be on a CUDA device, not {t.device}")
+        _bad("tensors must be on a CUDA device")
     if d == torch._C._cuda_getDevice():
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream)
     else:
@@ -326,8 +324,7 @@ def _run_on(t, stream, fn, *args) -> None:
         check(rc)
 
 
-def _io_dtype(t, what: str) -> int:
-    import torch
+def _io_dtype(torch, t, what: str) -> int:
     if t.dtype is torch.float32:
         return MK_F32
     if t.dtype is torch.bfloat16:
@@ -357,7 +354,7 @@ def rope_append(qkv, q_out, k_cache, v_cache, positions, rows, inv_freq, slots=N
     q_out [n][Hq][hd] of the same type (token stride free), k_cache / v_cache bfloat16 [B][Hkv][max_seq][hd]
     (one layer), positions / rows / slots int32 [n], inv_freq float64 [rot / 2], q_norm / k_norm bfloat16 [hd]."""
     import torch
-    bf, i32, dt = torch.bfloat16, torch.int32, _io_dtype(qkv, "qkv")
+    bf, i32, dt = torch.bfloat16, torch.int32, _io_dtype(torch, qkv, "qkv")
     if k_cache.dim() != 4 or q_out.dim() != 3 or qkv.dim() != 2 or inv_freq.dim() != 1:
         _bad("qkv, q_out, k_cache, inv_freq must have 2, 3, 4, 1 dimensions")
     B, Hkv, S, hd = k_cache.shape
@@ -392,7 +389,7 @@ def rope_append(qkv, q_out, k_cache, v_cache, positions, rows, inv_freq, slots=N
                           k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(), rows.data_ptr(),
                           0 if slots is None else slots.data_ptr(), inv_freq.data_ptr(),
                           0 if q_norm is None else q_norm.data_ptr(), 0 if k_norm is None else k_norm.data_ptr())
-    _run_on(qkv, stream, load().mk_rope_append, rec)
+    _run_on(torch, d, stream, load().mk_rope_append, rec)
 
 
 def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None = None, counts=None, slots=None,
@@ -403,7 +400,7 @@ def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None
     (zeroed by the caller) that becomes 1 if a bounded in-kernel wait ran out. The workspace of long caches comes
     from torch's allocator, on the call's stream."""
     import torch
-    bf, i32, i64, dt = torch.bfloat16, torch.int32, torch.int64, _io_dtype(q, "q")
+    bf, i32, i64, dt = torch.bfloat16, torch.int32, torch.int64, _io_dtype(torch, q, "q")
     if q.dim() != 4 or k_cache.dim() != 4:
         _bad("q and k_cache must have 4 dimensions")
     B, T, Hq, hd = q.shape
@@ -449,7 +446,7 @@ def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None
                     with torch.cuda.stream(stream):
                         work = torch.empty(n, dtype=torch.uint8, device=q.device)
                 rec[22], rec[23] = work.data_ptr(), n
-    _run_on(q, stream, L.mk_tree_attention, _TREE_ARGS.pack(*rec))
+    _run_on(torch, d, stream, L.mk_tree_attention, _TREE_ARGS.pack(*rec))
 
 
 def tree_masks(parents, masks, depths=None, counts=None, stream=None) -> None:
@@ -464,7 +461,7 @@ def tree_masks(parents, masks, depths=None, counts=None, stream=None) -> None:
         _need(depths, "depths", torch.int32, (B, T), parents)
     if counts is not None:
         _need(counts, "counts", torch.int32, (B,), parents)
-    _run_on(parents, stream, load().mk_tree_masks, parents.data_ptr(), None if counts is None else counts.data_ptr(), B,
+    _run_on(torch, parents.get_device(), stream, load().mk_tree_masks, parents.data_ptr(), None if counts is None else counts.data_ptr(), B,
             T, masks.data_ptr(), None if depths is None else depths.data_ptr())
 
 
@@ -480,40 +477,43 @@ def tree_accept(tokens, parents, draws):
     return list(path[:c])
 
 
-def _cache_shape(k, v):
-    """(L, B, Hkv, max_seq, hd) of two whole caches."""
-    import torch
-    if k.dim() != 5:
-        _bad("the caches must have 5 dimensions")
-    shape = k.shape
-    if not (k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and v.shape == shape
-            and k.get_device() == v.get_device() and k.is_contiguous() and v.is_contiguous()):
+def _check_caches(torch, k, v, shape, small) -> None:
+    """k, v: the whole caches, of `shape`; small: the int32 arrays that go with them, (tensor, name, shape)."""
+    d = k.get_device()
+    if not (k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and v.shape == shape and v.get_device() == d
+            and k.is_contiguous() and v.is_contiguous()):
         _need(k, "k", torch.bfloat16, shape, k)
         _need(v, "v", torch.bfloat16, shape, k)
-    return shape
+    for t, what, dims in small:
+        if not (t.dtype is torch.int32 and t.shape == dims and t.get_device() == d and t.is_contiguous()):
+            _need(t, what, torch.int32, dims, k)
 
 
 def kv_compact(k, v, starts, nodes, counts, stream=None) -> None:
     """mk_kv_compact on CUDA tensors: k / v bfloat16 [L][B][Hkv][max_seq][hd], starts / counts int32 [B], nodes
     int32 [B][n]: rows starts[b] + nodes[b][i] move to starts[b] + i."""
     import torch
-    L, B, Hkv, S, hd = _cache_shape(k, v)
-    n = nodes.shape[-1] if nodes.dim() == 2 else 0
-    for t, what, shape in ((starts, "starts", (B,)), (nodes, "nodes", (B, n)), (counts, "counts", (B,))):
-        _need(t, what, torch.int32, shape, k)
-    _run_on(k, stream, load().mk_kv_compact, k.data_ptr(), v.data_ptr(), L, B, Hkv, S, hd, n, starts.data_ptr(),
-            nodes.data_ptr(), counts.data_ptr())
+    if k.dim() != 5 or nodes.dim() != 2:
+        _bad("the caches must have 5 dimensions, nodes 2")
+    shape = k.shape
+    L, B, Hkv, S, hd = shape
+    n = nodes.shape[1]
+    _check_caches(torch, k, v, shape, ((starts, "starts", (B,)), (nodes, "nodes", (B, n)), (counts, "counts", (B,))))
+    _run_on(torch, k.get_device(), stream, load().mk_kv_compact, k.data_ptr(), v.data_ptr(), L, B, Hkv, S, hd, n,
+            starts.data_ptr(), nodes.data_ptr(), counts.data_ptr())
 
 
 def kv_reorder(k, v, sources, lengths, stream=None) -> None:
     """mk_kv_reorder on CUDA tensors: k / v bfloat16 [L][B][Hkv][max_seq][hd], sources / lengths int32 [B]: rows
     [0, lengths[b]) of slot b become slot sources[b]'s."""
     import torch
-    L, B, Hkv, S, hd = _cache_shape(k, v)
-    _need(sources, "sources", torch.int32, (B,), k)
-    _need(lengths, "lengths", torch.int32, (B,), k)
-    _run_on(k, stream, load().mk_kv_reorder, k.data_ptr(), v.data_ptr(), L, B, Hkv, S, hd, sources.data_ptr(),
-            lengths.data_ptr())
+    if k.dim() != 5:
+        _bad("the caches must have 5 dimensions")
+    shape = k.shape
+    L, B, Hkv, S, hd = shape
+    _check_caches(torch, k, v, shape, ((sources, "sources", (B,)), (lengths, "lengths", (B,))))
+    _run_on(torch, k.get_device(), stream, load().mk_kv_reorder, k.data_ptr(), v.data_ptr(), L, B, Hkv, S, hd,
+            sources.data_ptr(), lengths.data_ptr())
 
 
 class Megakernel:

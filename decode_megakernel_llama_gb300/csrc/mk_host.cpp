@@ -708,16 +708,16 @@ struct mk_handle {
     // caller asks for none) and the candidate lists / slice keys
     float *pd_logits = nullptr;
     unsigned long long *pd_lists = nullptr;
-    // verification of drafted trees (mk_verify), made on its first call: the RoPE
-    // frequencies, the tree's arrays, and logits and draw lists of MK_MAX_TREE
-    // nodes; the attention's workspace, grown as needed
+    // verification of drafted trees (mk_verify), made on its first call: scratch of
+    // its pass, the RoPE frequencies, the tree's arrays, logits and draw lists of
+    // MK_MAX_TREE nodes, and the attention's workspace
+    mkpf::Scratch vf_sc;
+    void *vf_sc_mem = nullptr;
     void *vf_mem = nullptr;
     mkpf::Tree vf;
     float *vf_logits = nullptr;
     unsigned long long *vf_lists = nullptr;
     CUtensorMap vf_embed;
-    void *vf_work = nullptr;
-    int64_t vf_work_bytes = 0;
 };
 
 namespace {
@@ -770,9 +770,8 @@ int launch(mk_handle *h, int32_t token, const int32_t *d_token, int32_t position
     return MK_OK;
 }
 
-// Tensor maps of the weights (the first call) and scratch for n prompt tokens.
-int prefill_ready(mk_handle *h, int n) {
-    cudaError_t e = cudaSuccess;
+// Tensor maps of the weights, made on the first call.
+int prefill_maps(mk_handle *h) {
     const mk_config &c = h->cfg;
     const int d = c.d_model, hd = c.head_dim, qd = c.n_heads * hd, kvd = c.n_kv_heads * hd, F = c.ffn_dim;
     if (!h->pf_ready) {
@@ -801,52 +800,59 @@ int prefill_ready(mk_handle *h, int n) {
         }
         h->pf_ready = true;
     }
-    if (h->pf.cap < n) {
-        // scratch for n tokens: residual and q|k|v (fp32), the hi/lo bf16
-        // input of the projections from d or Hq hd columns, and that of the
-        // down projection (h = silu(g) * u)
-        const size_t kmax = std::max(d, qd), qkv = qd + 2 * kvd;
-        // K-split partials: the largest the q/k/v, O and down projections
-        // use (gate/up runs in one pass)
-        const int nsm = h->im.n_sm;
-        const int qkv_rows[3] = {qd, kvd, kvd};
-        const size_t work = std::max(std::max(mkpf::gemm_workspace_floats(d, n, qd, nsm, true),
-                                              mkpf::gemm_workspace_floats(d, n, F, nsm, true)),
-                                     mkpf::gemm_multi_workspace_floats(3, qkv_rows, n, d, nsm));
-        // (+ 256 bytes of alignment for each of the 8 pieces)
-        const size_t bytes = 4 * (size_t)n * (d + qkv) + 2 * 2 * (size_t)n * (kmax + F) +
-                             8 * (size_t)2 * h->im.n_sm + 4 * work + 4 * 512;
-        int32_t err_keep = 0;
-        if (h->pf.err) cudaMemcpy(&err_keep, h->pf.err, sizeof err_keep, cudaMemcpyDeviceToHost);
-        void *mem = nullptr;
-        e = cudaMalloc(&mem, bytes);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(prefill scratch)");
-        if (h->pf_mem) {
-            cudaDeviceSynchronize();
-            cudaFree(h->pf_mem);
-        }
-        h->pf_mem = mem;
-        char *b = static_cast<char *>(mem);
-        auto take = [&](size_t nbytes) {
-            char *at = b;
-            b += (nbytes + 255) & ~size_t(255);
-            return at;
-        };
-        mkpf::Scratch &sc = h->pf;
-        sc.cap = n;
-        sc.X = reinterpret_cast<float *>(take(4 * (size_t)n * d));
-        sc.QKV = reinterpret_cast<float *>(take(4 * (size_t)n * qkv));
-        sc.Hhi = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * F));
-        sc.Hlo = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * F));
-        sc.Ahi = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * kmax));
-        sc.Alo = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * kmax));
-        sc.keys = reinterpret_cast<unsigned long long *>(take(8 * (size_t)2 * h->im.n_sm));
-        sc.work = reinterpret_cast<float *>(take(4 * work));
-        sc.work_floats = work;
-        sc.err = reinterpret_cast<int *>(take(4));
-        e = cudaMemcpy(sc.err, &err_keep, sizeof err_keep, cudaMemcpyHostToDevice);
-        if (e != cudaSuccess) return cuda_fail(e, "prefill status");
+    return MK_OK;
+}
+
+// Scratch for a pass over n tokens (any_up_to: or any fewer), owned by *owned.
+int prefill_scratch(mk_handle *h, int n, bool any_up_to, mkpf::Scratch &sc, void **owned) {
+    const mk_config &c = h->cfg;
+    const int d = c.d_model, hd = c.head_dim, qd = c.n_heads * hd, kvd = c.n_kv_heads * hd, F = c.ffn_dim;
+    cudaError_t e;
+    // scratch for n tokens: residual and q|k|v (fp32), the hi/lo bf16
+    // input of the projections from d or Hq hd columns, and that of the
+    // down projection (h = silu(g) * u)
+    const size_t kmax = std::max(d, qd), qkv = qd + 2 * kvd;
+    // K-split partials: the largest the q/k/v, O and down projections
+    // use (gate/up runs in one pass)
+    const int nsm = h->im.n_sm;
+    const int qkv_rows[3] = {qd, kvd, kvd};
+    size_t work = 0;
+    for (int m = any_up_to ? 1 : n; m <= n; ++m)
+        work = std::max({work, mkpf::gemm_workspace_floats(d, m, qd, nsm, true),
+                         mkpf::gemm_workspace_floats(d, m, F, nsm, true),
+                         mkpf::gemm_multi_workspace_floats(3, qkv_rows, m, d, nsm)});
+    // (+ 256 bytes of alignment for each of the 8 pieces)
+    const size_t bytes = 4 * (size_t)n * (d + qkv) + 2 * 2 * (size_t)n * (kmax + F) +
+                         8 * (size_t)2 * h->im.n_sm + 4 * work + 4 * 512;
+    int32_t err_keep = 0;
+    if (sc.err) cudaMemcpy(&err_keep, sc.err, sizeof err_keep, cudaMemcpyDeviceToHost);
+    void *mem = nullptr;
+    e = cudaMalloc(&mem, bytes);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(prefill scratch)");
+    if (*owned) {
+        cudaDeviceSynchronize();
+        cudaFree(*owned);
     }
+    *owned = mem;
+    char *b = static_cast<char *>(mem);
+    auto take = [&](size_t nbytes) {
+        char *at = b;
+        b += (nbytes + 255) & ~size_t(255);
+        return at;
+    };
+    sc.cap = n;
+    sc.X = reinterpret_cast<float *>(take(4 * (size_t)n * d));
+    sc.QKV = reinterpret_cast<float *>(take(4 * (size_t)n * qkv));
+    sc.Hhi = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * F));
+    sc.Hlo = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * F));
+    sc.Ahi = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * kmax));
+    sc.Alo = reinterpret_cast<uint16_t *>(take(2 * (size_t)n * kmax));
+    sc.keys = reinterpret_cast<unsigned long long *>(take(8 * (size_t)2 * h->im.n_sm));
+    sc.work = reinterpret_cast<float *>(take(4 * work));
+    sc.work_floats = work;
+    sc.err = reinterpret_cast<int *>(take(4));
+    e = cudaMemcpy(sc.err, &err_keep, sizeof err_keep, cudaMemcpyHostToDevice);
+    if (e != cudaSuccess) return cuda_fail(e, "prefill status");
     return MK_OK;
 }
 
@@ -1139,16 +1145,23 @@ int mk_get_status(mk_handle *h) {
     cudaError_t e = cudaSetDevice(h->device);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-    int32_t st = 0, bst = 0, pst = 0, lst = 0;
+    int32_t st = 0, bst = 0, pst = 0, lst = 0, vst = 0;
     e = cudaMemcpy(&st, h->base.status, sizeof st, cudaMemcpyDeviceToHost);
     if (e == cudaSuccess && h->has_batch) e = cudaMemcpy(&bst, h->bbase.status, sizeof bst, cudaMemcpyDeviceToHost);
     if (e == cudaSuccess && h->pf.err) e = cudaMemcpy(&pst, h->pf.err, sizeof pst, cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess && h->vf_sc.err) e = cudaMemcpy(&vst, h->vf_sc.err, sizeof vst, cudaMemcpyDeviceToHost);
     if (e == cudaSuccess && h->blm_err) e = cudaMemcpy(&lst, h->blm_err, sizeof lst, cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(e, "status read");
     if (lst != 0) {
         e = cudaMemset(h->blm_err, 0, sizeof(int));
         if (e != cudaSuccess) return cuda_fail(e, "status reset");
         return fail(MK_ERR_TIMEOUT, "a bounded wait of the batched LM head expired");
+    }
+    if (vst != 0) {
+        e = cudaMemset(h->vf_sc.err, 0, sizeof(int));
+        if (e != cudaSuccess) return cuda_fail(e, "status reset");
+        if (vst == 2) return fail(MK_ERR_INVALID_ARG, "tree token outside [0, vocab)");
+        return fail(MK_ERR_TIMEOUT, "a bounded wait of the tree's pass expired");
     }
     if (pst != 0) {
         e = cudaMemset(h->pf.err, 0, sizeof(int));
@@ -1175,7 +1188,8 @@ int mk_prefill(mk_handle *h, const int32_t *d_tokens, int32_t n, int32_t start_p
         return fail(MK_ERR_INVALID_ARG, "prompt positions outside [0, max_seq)");
     cudaError_t e = cudaSetDevice(h->device);
     if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
-    const int rc = prefill_ready(h, n);
+    int rc = prefill_maps(h);
+    if (!rc && h->pf.cap < n) rc = prefill_scratch(h, n, false, h->pf, &h->pf_mem);
     if (rc) return rc;
     // with sampling on, the token of the last position is drawn as the decode
     // step at that position would draw it (same noise, same filter)
@@ -1217,27 +1231,33 @@ int mk_verify(mk_handle *h, const int32_t *d_tokens, const int32_t *d_parents, i
         return fail(MK_ERR_INVALID_ARG, "tree rows outside [0, max_seq)");
     cudaError_t e = cudaSetDevice(h->device);
     if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
-    // (scratch for a whole tree at once: a later, larger one allocates nothing)
-    const int rc = prefill_ready(h, std::max(h->pf.cap, std::min(MK_MAX_TREE, h->cfg.max_seq)));
+    // (everything for the largest tree at the largest position at once, apart from
+    // the prefill's: no later call moves what a captured graph uses)
+    int rc = prefill_maps(h);
+    if (!rc && !h->vf_sc.cap) rc = prefill_scratch(h, MK_MAX_TREE, true, h->vf_sc, &h->vf_sc_mem);
     if (rc) return rc;
     const mk_config &c = h->cfg;
     if (!h->vf_mem) {
         if (!mkpf::encode_weight_map(&h->vf_embed, h->base.embed, c.vocab, c.d_model))
             return fail(MK_ERR_UNSUPPORTED, "could not encode the embedding's tensor map");
         const int half = c.head_dim / 2, T = MK_MAX_TREE;
-        std::vector<double> freq(half);
+        double freq[64];  // head_dim is 64 or 128
         float mscale;
-        const int frc = mk_rope_frequencies(MK_ROPE_PLAIN, c.head_dim, c.rope_theta, 1.0, 1.0, 1.0, 2.0, freq.data(),
+        const int frc = mk_rope_frequencies(MK_ROPE_PLAIN, c.head_dim, c.rope_theta, 1.0, 1.0, 1.0, 2.0, freq,
                                             &mscale);
         if (frc) return frc;
         const size_t o_mask = 8 * (size_t)half, o_pos = o_mask + 8 * T, o_row = o_pos + 4 * T, o_len = o_row + 4 * T,
                      o_list = (o_len + 4 + 255) & ~size_t(255),
                      o_log = (o_list + 8 * mk_filter_lists_keys(T, c.vocab) + 255) & ~size_t(255),
-                     bytes = o_log + 4 * (size_t)T * c.vocab;
+                     o_work = (o_log + 4 * (size_t)T * c.vocab + 255) & ~size_t(255);
+        int64_t work = 0;
+        for (int m = 1; m <= T; ++m)
+            for (int64_t pos = 0; pos < c.max_seq; pos += 128)
+                work = std::max(work, mkpf::tree_work_bytes(h->pf_model, m, (int)pos));
         char *m = nullptr;
-        e = cudaMalloc(&m, bytes);
+        e = cudaMalloc(&m, o_work + work);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(tree scratch)");
-        e = cudaMemcpy(m, freq.data(), 8 * (size_t)half, cudaMemcpyHostToDevice);
+        e = cudaMemcpy(m, freq, 8 * (size_t)half, cudaMemcpyHostToDevice);
         if (e != cudaSuccess) {
             cudaFree(m);
             return cuda_fail(e, "RoPE frequencies");
@@ -1250,25 +1270,13 @@ int mk_verify(mk_handle *h, const int32_t *d_tokens, const int32_t *d_parents, i
         h->vf.length = reinterpret_cast<int32_t *>(m + o_len);
         h->vf_lists = reinterpret_cast<unsigned long long *>(m + o_list);
         h->vf_logits = reinterpret_cast<float *>(m + o_log);
+        h->vf.work = reinterpret_cast<float *>(m + o_work);
+        h->vf.work_floats = work / 4;
     }
-    mkpf::Tree t = h->vf;
-    const int64_t need = mkpf::tree_work_bytes(h->pf_model, n, start_pos);
-    if (need > h->vf_work_bytes) {
-        void *m = nullptr;
-        e = cudaMalloc(&m, need);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(tree attention workspace)");
-        if (h->vf_work) {
-            cudaDeviceSynchronize();
-            cudaFree(h->vf_work);
-        }
-        h->vf_work = m;
-        h->vf_work_bytes = need;
-    }
-    t.work = static_cast<float *>(h->vf_work);
-    t.work_floats = h->vf_work_bytes / 4;
+    const mkpf::Tree &t = h->vf;
     float *logits = out_logits ? out_logits : h->vf_logits;
     const cudaStream_t s = (cudaStream_t)stream;
-    e = mkpf::run_tree(h->pf_model, h->pf, t, h->vf_embed, d_tokens, d_parents, n, start_pos, logits, s);
+    e = mkpf::run_tree(h->pf_model, h->vf_sc, t, h->vf_embed, d_tokens, d_parents, n, start_pos, logits, s);
     if (e != cudaSuccess) return cuda_fail(e, "tree launch");
     const bool filtered = h->inv_temp > 0.f && (h->top_k > 0 || h->top_p < 1.f);
     e = filtered ? mk_filtered_draw_batch(logits, n, c.vocab, h->top_k > 0 ? h->top_k : mk::kMaxTopK, h->top_p,
@@ -1441,7 +1449,7 @@ void mk_destroy(mk_handle *h) {
     if (h->pd_logits) cudaFree(h->pd_logits);
     if (h->pd_lists) cudaFree(h->pd_lists);
     if (h->vf_mem) cudaFree(h->vf_mem);
-    if (h->vf_work) cudaFree(h->vf_work);
+    if (h->vf_sc_mem) cudaFree(h->vf_sc_mem);
     delete h;
 }
 

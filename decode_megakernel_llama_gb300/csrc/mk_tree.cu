@@ -291,6 +291,10 @@ int check_tree(const mk_tree_args *a) {
     if (a->q_token_stride < row || a->out_token_stride < row || a->q_batch_stride < 0 || a->out_batch_stride < 0 ||
         (a->q_token_stride | a->out_token_stride | a->q_batch_stride | a->out_batch_stride) % 8)
         return set_error(MK_ERR_INVALID_ARG, "mk_tree_attention: a stride is too small or not a multiple of 8 elements");
+    // the rows of out must not meet: whole sequences behind one another, or whole nodes
+    if (a->batch > 1 && a->out_batch_stride < (a->nodes - 1) * a->out_token_stride + row &&
+        (a->out_batch_stride < row || a->out_token_stride < (a->batch - 1) * a->out_batch_stride + row))
+        return set_error(MK_ERR_INVALID_ARG, "mk_tree_attention: the rows of out overlap");
     if ((reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(a->out) |
          reinterpret_cast<uintptr_t>(a->k_cache) | reinterpret_cast<uintptr_t>(a->v_cache)) & 15u ||
         reinterpret_cast<uintptr_t>(a->masks) & 7u)

@@ -88,7 +88,7 @@ constexpr int kMmaWarp = 0, kKWarp = 1, kVWarp = 2, kFirstSoft = 4, kSoftWarps =
 constexpr int kAttnThreads = kSoft + 32 * kFirstSoft;
 constexpr int kHalfTile = kTile * 128;  // bytes of 128 rows x 64 dims
 constexpr int kSmemMost = 232448;       // shared memory of a CTA
-constexpr float kNone = -1e30f;         // the maximum of a row that has seen nothing
+constexpr float kNone = -3e38f;         // the maximum of a row that has seen nothing
 constexpr float kRaise = 8.f;           // a score this far above m (in powers of two) raises m
 
 // Most splits joined through the workspace (tree_join keeps their statistics).

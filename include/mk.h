@@ -208,10 +208,10 @@ int mk_prefill(mk_handle *h, const int32_t *d_tokens, int32_t n, int32_t start_p
  * the same tokens (to rounding: greedy, or drawn with this handle's sampling and
  * filter and the noise of the node's position). The projections run as in
  * mk_prefill, rotation and append as mk_rope_append, attention as
- * mk_tree_attention. The first call, and one whose attention wants more
- * workspace than any before, allocates (on the handle's device, owned by it):
- * not inside a captured graph. Errors as mk_prefill; one call in flight per
- * handle.
+ * mk_tree_attention. The first call allocates what any later one uses (on the
+ * handle's device, owned by it): it comes before a graph's capture. A tree
+ * token outside [0, vocab) or an expired in-kernel wait is reported by
+ * mk_get_status. One call in flight per handle.
  * Source: as mk_prefill; checking drafted tokens in one pass follows
  * Leviathan, Kalman, Matias (ICML 2023), with a tree instead of a chain. */
 int mk_verify(mk_handle *h, const int32_t *d_tokens, const int32_t *d_parents, int32_t n, int32_t start_pos,
@@ -513,7 +513,8 @@ int mk_rope_frequencies(int32_t kind, int32_t rot, double theta, double factor, 
  * they are. max_len: a bound on lengths[b] known to the host (0: max_seq),
  * used only to choose the launch; results are right if a length exceeds it.
  * lengths outside [0, max_seq] and counts past the nodes or the cache's end
- * are cut to them. out must not overlap q or the cache. Pointers 16-byte
+ * are cut to them. out must not overlap q, the cache or itself (the rows of
+ * its nodes: refused). Pointers 16-byte
  * aligned, strides multiples of 8 elements.
  * workspace (device, workspace_bytes, NULL or 16-byte aligned): scratch of
  * this call alone, in use until it is done on the stream; with less than

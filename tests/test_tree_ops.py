@@ -64,12 +64,22 @@ def tree_args(**kw):
     (dict(q_token_stride=516), -1), (dict(out_token_stride=504), -1), (dict(q_batch_stride=-8), -1),
     (dict(out_batch_stride=4), -1), (dict(q=FAKE + 8), -1), (dict(out=FAKE + 8), -1), (dict(k_cache=FAKE + 2), -1),
     (dict(v_cache=FAKE + 8), -1), (dict(masks=FAKE + 4), -1), (dict(batch=40000), -4),
-    (dict(workspace=FAKE + 4), -1), (dict(workspace_bytes=-1), -1),
+    (dict(workspace=FAKE + 4), -1), (dict(workspace_bytes=-1), -1), (dict(out_batch_stride=0), -1),
+    (dict(out_batch_stride=512 * 7), -1), (dict(out_batch_stride=504, out_token_stride=4096), -1),
 ])
 def test_tree_attention_refuses(lib, bad, code):
     assert lib.mk_tree_attention_workspace(ctypes.byref(tree_args(**bad))) == code
     assert lib.mk_tree_attention(ctypes.byref(tree_args(**bad)), None) == code
     assert b"mk_tree_attention" in lib.mk_last_error()
+
+
+def test_tree_attention_takes_either_order_of_out(lib):
+    """Sequences behind one another or nodes behind one another pass the check of overlap (one kv head too many
+    for the next check tells)."""
+    for b, t in ((4096, 512), (512, 1024), (512, 2048), (8192, 1024)):
+        a = tree_args(out_batch_stride=b, out_token_stride=t, q=FAKE + 8)
+        assert lib.mk_tree_attention(ctypes.byref(a), None) == -1
+        assert b"aligned" in lib.mk_last_error()
 
 
 def test_tree_attention_of_no_sequences_does_nothing(lib):

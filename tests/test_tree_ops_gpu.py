@@ -310,6 +310,50 @@ def test_tree_attention_is_repeatable_in_streams_and_graphs(dev):
         c.check()
 
 
+@pytest.mark.parametrize("hd,T,Hq,Hkv,dtype", [(64, 12, 8, 2, torch.float32), (64, 40, 8, 2, BF), (128, 20, 6, 2, BF),
+                                               (128, 3, 2, 1, torch.float32)])
+def test_tree_attention_long_caches_in_streams_and_graphs(dev, hd, T, Hq, Hkv, dtype):
+    """Caches split through the workspace: repeated, in two streams at once, and in two graphs replayed side by side."""
+    cases = [Case(dev, [6000], T, Hq, Hkv, hd, dtype, seed=s) for s in (1, 2)]
+    for c in cases:
+        c.run(max_len=6000)
+        c.check()
+    want = [c.out.clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    graphs = []
+    for c in cases:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            c.run(max_len=6000)
+        graphs.append(gr)
+    for rep in range(6):
+        for c in cases:
+            c.out.fill_(99.0)
+        torch.cuda.synchronize()
+        for c, s, gr in zip(cases, streams, graphs):
+            if rep % 2:
+                with torch.cuda.stream(s):
+                    gr.replay()
+            else:
+                c.run(max_len=6000, stream=s)
+        torch.cuda.synchronize()
+        for c, w in zip(cases, want):
+            assert torch.equal(c.out, w)
+
+
+def test_tree_attention_far_scores_and_status(dev):
+    """Scores below -1e30 are scores all the same; the status word stays 0."""
+    c = Case(dev, [70], 3, 2, 1, 64, torch.float32)
+    c.q = torch.full_like(c.q, 3e18)
+    c.k = -torch.full_like(c.k, 3e15)
+    c.k[0, 0, 5] *= 0.5  # the largest score by far: its value comes back
+    st = torch.zeros(1, dtype=I32, device=dev)
+    c.run(status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    assert torch.equal(c.out, c.v[0, 0, 5].float().expand_as(c.out))
+
+
 # ---------------------------------------------------------------- tree_masks
 @pytest.mark.parametrize("T", [1, 2, 31, 33, 64])
 def test_tree_masks_of_random_trees(dev, T):

@@ -240,6 +240,10 @@ def test_verify_in_a_graph(cuda_dev):
         pair.mk.verify(tk, pr, 3, out, lg)
     b = draft(TINY.vocab, 15, g)
     tk.copy_(torch.tensor(b[0])), pr.copy_(torch.tensor(b[1]))
+    # a larger tree and a prefill in between move nothing that the graph uses
+    big = draft(TINY.vocab, 30, g)
+    verify(pair, *big, 3)
+    pair.mk.prefill(synth.prompt_tokens(TINY.vocab, 3).to(dev), 0, torch.zeros(1, dtype=I32, device=dev))
     graph.replay()
     torch.cuda.synchronize()
     assert pair.mk.status() == 0
