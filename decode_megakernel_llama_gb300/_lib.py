@@ -84,6 +84,7 @@ _TREE_ARGS = struct.Struct("@9if4q9PqP")
 
 
 _lib = None
+_quick = None  # the extension module of the drafted-tree operators (csrc/mk_torch.cpp)
 _VP = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _PI32 = ctypes.POINTER(ctypes.c_int32)
@@ -143,7 +144,25 @@ def load(path: str | None = None):
     L.mk_destroy.argtypes = [_VP]
     L.mk_destroy.restype = None
     _lib = L
+    _bind_quick(L)
     return L
+
+
+def _bind_quick(L) -> None:
+    """Loads mk_torch.so beside libmk.so and gives it the library's entry points."""
+    global _quick
+    import importlib.util
+
+    import torch  # noqa: F401  (the module needs its libraries)
+    path = os.path.join(PKG, "_build", "mk_torch.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: run decode_megakernel_llama_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("mk_torch", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.mk_rope_append, L.mk_tree_attention, L.mk_tree_attention_workspace, L.mk_kv_compact, L.mk_kv_reorder)))
+    _quick = mod
 
 
 def declared_symbols(header: str = HEADER) -> list[str]:
@@ -353,6 +372,14 @@ def rope_append(qkv, q_out, k_cache, v_cache, positions, rows, inv_freq, slots=N
     """mk_rope_append on CUDA tensors: qkv [n][(Hq + 2 Hkv) hd] float32 or bfloat16 (rows may be strided),
     q_out [n][Hq][hd] of the same type (token stride free), k_cache / v_cache bfloat16 [B][Hkv][max_seq][hd]
     (one layer), positions / rows / slots int32 [n], inv_freq float64 [rot / 2], q_norm / k_norm bfloat16 [hd]."""
+    q = _quick or (load() and _quick)
+    rc = q.rope_append(qkv, q_out, k_cache, v_cache, positions, rows, inv_freq, slots, q_norm, k_norm, eps, mscale,
+                       interleaved, stream)
+    if rc == MK_OK:
+        return
+    if rc < 0:
+        check(rc)
+    # not done: something is wrong, or the call is for another stream or device
     import torch
     bf, i32, dt = torch.bfloat16, torch.int32, _io_dtype(torch, qkv, "qkv")
     if k_cache.dim() != 4 or q_out.dim() != 3 or qkv.dim() != 2 or inv_freq.dim() != 1:
@@ -399,6 +426,14 @@ def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None
     masks int64 [B][T] (the 64 bits of the ancestor mask). scale defaults to 1 / sqrt(hd). status: int32 [1]
     (zeroed by the caller) that becomes 1 if a bounded in-kernel wait ran out. The workspace of long caches comes
     from torch's allocator, on the call's stream."""
+    quick = _quick or (load() and _quick)
+    rc = quick.tree_attention(q, k_cache, v_cache, lengths, masks, out,
+                              q.shape[-1] ** -0.5 if scale is None else scale, counts, slots, max_len, status, stream)
+    if rc == MK_OK:
+        return
+    if rc < 0:
+        check(rc)
+    # not done: something is wrong, or the call is for another stream or device
     import torch
     bf, i32, i64, dt = torch.bfloat16, torch.int32, torch.int64, _io_dtype(torch, q, "q")
     if q.dim() != 4 or k_cache.dim() != 4:
@@ -492,6 +527,11 @@ def _check_caches(torch, k, v, shape, small) -> None:
 def kv_compact(k, v, starts, nodes, counts, stream=None) -> None:
     """mk_kv_compact on CUDA tensors: k / v bfloat16 [L][B][Hkv][max_seq][hd], starts / counts int32 [B], nodes
     int32 [B][n]: rows starts[b] + nodes[b][i] move to starts[b] + i."""
+    rc = (_quick or (load() and _quick)).kv_compact(k, v, starts, nodes, counts, stream)
+    if rc == MK_OK:
+        return
+    if rc < 0:
+        check(rc)
     import torch
     if k.dim() != 5 or nodes.dim() != 2:
         _bad("the caches must have 5 dimensions, nodes 2")
@@ -506,6 +546,11 @@ def kv_compact(k, v, starts, nodes, counts, stream=None) -> None:
 def kv_reorder(k, v, sources, lengths, stream=None) -> None:
     """mk_kv_reorder on CUDA tensors: k / v bfloat16 [L][B][Hkv][max_seq][hd], sources / lengths int32 [B]: rows
     [0, lengths[b]) of slot b become slot sources[b]'s."""
+    rc = (_quick or (load() and _quick)).kv_reorder(k, v, sources, lengths, stream)
+    if rc == MK_OK:
+        return
+    if rc < 0:
+        check(rc)
     import torch
     if k.dim() != 5:
         _bad("the caches must have 5 dimensions")

@@ -1,4 +1,4 @@
-"""Builds libmk.so (the megakernel and its C ABI) in-tree for sm_103a."""
+"""Builds libmk.so (the megakernel and its C ABI) in-tree for sm_103a, and mk_torch.so, the binding's extension module."""
 from __future__ import annotations
 
 import os
@@ -14,9 +14,12 @@ LIB_CHECKED = os.path.join(BUILD, "libmk_checked.so")
 SOURCES = ["mk_kernel_hd64.cu", "mk_kernel_hd128.cu", "mk_kernel.cu", "mk_host.cpp", "mk_noalloc.cu", "mk_w2a8.cu",
            "mk_prefill.cu", "mk_twell.cu"]
 DEPS = SOURCES + ["mk_kernel.cuh", "mk_plan.h", "mk_internal.h", "mk_prefill.h"]
-# the standalone operators: units of their own beside the megakernel's
+# the standalone operators: units of their own beside the megakernel's, and the
+# extension module through which the binding calls them with torch's tensors
 OP_SOURCES = ["mk_rope.cu", "mk_tree.cu", "mk_kv.cu"]
 OP_DEPS = OP_SOURCES + ["mk_ops.h", "mk_tc.cuh", "mk_tree_attn.cuh"]
+TORCH_SOURCE = "mk_torch.cpp"
+LIB_TORCH = os.path.join(BUILD, "mk_torch.so")
 
 
 def nvcc() -> str:
@@ -31,6 +34,25 @@ def flags() -> list[str]:
             "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", f"-I{os.path.join(ROOT, 'include')}"]
 
 
+def torch_command(out: str) -> list[str]:
+    """The compiler's command for mk_torch.so, against the torch and Python that run this."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in inc],
+            os.path.join(CSRC, TORCH_SOURCE), "-o", out, f"-L{os.path.join(root, 'lib')}", "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def _torch_stale() -> bool:
+    deps = [os.path.join(CSRC, TORCH_SOURCE), os.path.join(ROOT, "include", "mk.h")]
+    return not os.path.exists(LIB_TORCH) or any(os.path.getmtime(d) > os.path.getmtime(LIB_TORCH) for d in deps)
+
+
 def _stale(lib: str) -> bool:
     if not os.path.exists(lib):
         return True
@@ -43,9 +65,24 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
     """checked=True builds libmk_checked.so: every device-side access is
     validated against the registered buffers (slow; for diagnosing faults)."""
     lib = LIB_CHECKED if checked else LIB
-    if not force and not _stale(lib):
-        return lib
     os.makedirs(BUILD, exist_ok=True)
+    ext = None
+    if force or _torch_stale():
+        ext_tmp = LIB_TORCH + f".tmp{os.getpid()}"
+        ext_cmd = torch_command(ext_tmp)
+        ext = subprocess.Popen(ext_cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if force or _stale(lib):
+        _build_lib(lib, verbose, checked)
+    if ext is not None:
+        out, _ = ext.communicate()
+        if ext.returncode:
+            print(out.decode(errors="replace"))
+            raise RuntimeError(f"compile failed: {' '.join(ext_cmd)}")
+        os.replace(ext_tmp, LIB_TORCH)
+    return lib
+
+
+def _build_lib(lib: str, verbose: bool, checked: bool) -> None:
     nv = nvcc()
     procs, objs = [], []
     tag = ".chk" if checked else ""
@@ -67,7 +104,6 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
     subprocess.run([nv, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", "-o", tmp, *objs],
                    check=True)
     os.replace(tmp, lib)
-    return lib
 
 
 if __name__ == "__main__":

@@ -6,7 +6,7 @@
 // read once and written once. The one thing to get right is that sources and
 // targets overlap, so every thread has all its loads behind it before the
 // first store that could touch another's source:
-//   compact: one CTA holds all moved rows of one (layer, K or V, slot, head)
+//   compact: one CTA holds all moved rows of one (layer, slot, head), K and V,
 //     in registers, a barrier between its loads and its stores (no other CTA
 //     touches those rows);
 //   reorder: a thread owns one 16-byte column of a cache row in ALL slots;
@@ -24,7 +24,8 @@ namespace {
 constexpr int kMaxNodes = 64;
 constexpr int kT = 256;
 
-// grid (2 * L * Hkv, B): CTA of (layer, K or V, head) and slot.
+// grid (L * Hkv, B): CTA of (layer, head) and slot; K and V, so that twice the
+// loads are in flight.
 template <int HD>
 __global__ void __launch_bounds__(kT) kv_compact(uint16_t *kc, uint16_t *vc, int L, int B, int Hkv, int max_seq, int T,
                                                  const int32_t *__restrict__ starts, const int32_t *__restrict__ nodes,
@@ -32,12 +33,12 @@ __global__ void __launch_bounds__(kT) kv_compact(uint16_t *kc, uint16_t *vc, int
     constexpr int CPR = HD / 8;                   // 16-byte chunks of a row
     constexpr int NC = kMaxNodes * CPR / kT;      // chunks of a thread
     const int b = blockIdx.y, tid = threadIdx.x;
-    const int plane = blockIdx.x % (L * Hkv), l = plane / Hkv, h = plane % Hkv;
-    uint16_t *cache = blockIdx.x < L * Hkv ? kc : vc;
+    const int l = blockIdx.x / Hkv, h = blockIdx.x % Hkv;
     const int start = starts[b], n = min(counts[b], T);
     if (start < 0 || n <= 0) return;
-    uint4 *rows = reinterpret_cast<uint4 *>(cache + (((int64_t)l * B + b) * Hkv + h) * max_seq * HD);
-    uint4 v[NC];
+    const int64_t at = (((int64_t)l * B + b) * Hkv + h) * max_seq * HD;
+    uint4 *krows = reinterpret_cast<uint4 *>(kc + at), *vrows = reinterpret_cast<uint4 *>(vc + at);
+    uint4 k[NC], v[NC];
     bool move[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -47,14 +48,20 @@ __global__ void __launch_bounds__(kT) kv_compact(uint16_t *kc, uint16_t *vc, int
             const int node = nodes[(int64_t)b * T + i];
             const int64_t src = (int64_t)start + node, dst = (int64_t)start + i;
             move[c] = node >= 0 && node != i && src < max_seq && dst < max_seq;
-            if (move[c]) v[c] = rows[src * CPR + part];
+            if (move[c]) {
+                k[c] = krows[src * CPR + part];
+                v[c] = vrows[src * CPR + part];
+            }
         }
     }
     __syncthreads();
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int i = (tid + c * kT) / CPR, part = tid % CPR;
-        if (move[c]) rows[((int64_t)start + i) * CPR + part] = v[c];
+        const int64_t to = ((int64_t)start + (tid + c * kT) / CPR) * CPR + tid % CPR;
+        if (move[c]) {
+            krows[to] = k[c];
+            vrows[to] = v[c];
+        }
     }
 }
 
@@ -119,7 +126,7 @@ extern "C" int mk_kv_compact(void *k, void *v, int32_t n_layers, int32_t slots, 
         return set_error(MK_ERR_INVALID_ARG, "mk_kv_compact: a required pointer is NULL");
     if (nodes_per_slot < 1 || nodes_per_slot > mkops::kMaxNodes)
         return set_error(MK_ERR_INVALID_ARG, "mk_kv_compact: nodes_per_slot outside [1, MK_MAX_TREE]");
-    const dim3 grid(2 * n_layers * n_kv_heads, slots);
+    const dim3 grid(n_layers * n_kv_heads, slots);
     uint16_t *kc = static_cast<uint16_t *>(k), *vc = static_cast<uint16_t *>(v);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (head_dim == 64)

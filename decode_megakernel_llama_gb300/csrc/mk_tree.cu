@@ -212,9 +212,15 @@ cudaError_t launch(TreeArgs a, int max_len, int n_sm, cudaStream_t s, int64_t *w
     launch_config(cfg, attr, dim3(p.S, a.B * a.Hkv, row_tiles), K::kSmem, p.ws ? 1 : p.S, s);
     e = cudaLaunchKernelEx(&cfg, K::fn(), kmap, vmap, a);
     if (e != cudaSuccess || !p.ws) return e;
-    tree_join<K::HD, K::TERMS, K::NR>
-        <<<dim3(row_tiles, a.B * a.Hkv, (K::NR * K::HD / 4 + 255) / 256), 256, 0, s>>>(a, p.S);
-    return cudaGetLastError();
+    cudaLaunchConfig_t jc = {};
+    jc.gridDim = dim3(row_tiles, a.B * a.Hkv, (K::NR * K::HD / 4 + 255) / 256);
+    jc.blockDim = dim3(256);
+    jc.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    jc.attrs = attr;
+    jc.numAttrs = 1;
+    return cudaLaunchKernelEx(&jc, tree_join<K::HD, K::TERMS, K::NR>, a, p.S);
 }
 
 // The kernel of 16 or 32 columns that holds the tree's rows of a kv head; for more

@@ -345,6 +345,8 @@ __device__ __forceinline__ void finish(const TreeArgs &a, int b, int kvh, int G,
     namespace cg = cooperative_groups;
     const int tid = threadIdx.x;
     if (a.part) {
+        // (tree_join may be brought in; it waits for this grid's end before it reads)
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         const int64_t unit = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
         float *p = a.part + (unit * S + split) * part_floats(NR, HD);
         for (int i = tid; i < rows * (HD / 4); i += kAttnThreads) {
@@ -1067,6 +1069,7 @@ __global__ void __launch_bounds__(256) tree_join(const TreeArgs a, int S) {
     if (rows <= 0) return;
     const int64_t unit = (int64_t)blockIdx.x * gridDim.y + blockIdx.y;
     const float *p = a.part + unit * S * PF;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the splits' partial results
     for (int i = threadIdx.x; i < S * NR; i += 256) {
         const bool in = i % NR < rows;
         ms[i] = in ? p[(i / NR) * PF + NR * HD + i % NR] : kNone;

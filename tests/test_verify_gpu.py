@@ -8,7 +8,7 @@ import torch
 import tree_reference as ref
 from decode_megakernel_llama_gb300 import _lib, synth
 from decode_megakernel_llama_gb300.configs import LLAMA_1B, LLAMA_3B, TINY, ModelShape
-from gpu_helpers import MARGIN, Pair, compare, teacher_forced
+from gpu_helpers import MARGIN, MAX_ABS, Pair, compare, teacher_forced
 
 pytestmark = pytest.mark.gpu
 I32 = torch.int32
@@ -252,7 +252,8 @@ def test_verify_in_a_graph(cuda_dev):
 
 
 def test_a_slot_forked_over_a_batch(cuda_dev):
-    """One sequence's cache forked to the other slots: a batched step of the same token gives each the same logits."""
+    """One sequence's cache forked to the other slots: a batched step of the same token gives each the same logits,
+    to the parity bar (the batched step's warps add into shared accumulators in no fixed order)."""
     B, n = 4, 10
     dev = torch.device("cuda:0")
     w = synth.make_weights(TINY, dev, 0)
@@ -266,6 +267,6 @@ def test_a_slot_forked_over_a_batch(cuda_dev):
     torch.cuda.synchronize()
     assert mk.status() == 0
     for b in range(1, B):
-        assert torch.equal(k[:, b, :, : n + 1], k[:, 0, :, : n + 1])
-        assert torch.equal(lg[b], lg[0])
+        assert torch.equal(k[:, b, :, :n], k[:, 0, :, :n]) and torch.equal(v[:, b, :, :n], v[:, 0, :, :n])
+        assert (lg[b] - lg[0]).abs().max() <= MAX_ABS
     mk.close()
