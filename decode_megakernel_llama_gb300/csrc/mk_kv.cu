@@ -33,6 +33,7 @@ __global__ void __launch_bounds__(kT) kv_compact(uint16_t *kc, uint16_t *vc, int
     constexpr int CPR = HD / 8;                   // 16-byte chunks of a row
     constexpr int NC = kMaxNodes * CPR / kT;      // chunks of a thread
     const int b = blockIdx.y, tid = threadIdx.x;
+    pdl_begin();
     const int l = blockIdx.x / Hkv, h = blockIdx.x % Hkv;
     const int start = starts[b], n = min(counts[b], T);
     if (start < 0 || n <= 0) return;
@@ -74,6 +75,7 @@ __global__ void __launch_bounds__(kT) kv_reorder(V *kc, V *vc, int L, int B, int
     __shared__ int most;
     const int tid = threadIdx.x;
     if (tid == 0) most = 0;
+    pdl_begin();
     __syncthreads();
     if (tid < NB) {
         int s = tid < B ? sources[tid] : tid;
@@ -129,13 +131,11 @@ extern "C" int mk_kv_compact(void *k, void *v, int32_t n_layers, int32_t slots, 
     const dim3 grid(n_layers * n_kv_heads, slots);
     uint16_t *kc = static_cast<uint16_t *>(k), *vc = static_cast<uint16_t *>(v);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (head_dim == 64)
-        mkops::kv_compact<64><<<grid, mkops::kT, 0, s>>>(kc, vc, n_layers, slots, n_kv_heads, max_seq, nodes_per_slot,
-                                                         d_starts, d_nodes, d_counts);
-    else
-        mkops::kv_compact<128><<<grid, mkops::kT, 0, s>>>(kc, vc, n_layers, slots, n_kv_heads, max_seq, nodes_per_slot,
-                                                          d_starts, d_nodes, d_counts);
-    const cudaError_t e = cudaGetLastError();
+    auto go = [&](auto kernel) {
+        return mkops::launch_op(kernel, grid, mkops::kT, 0, 0, s, kc, vc, n_layers, slots, n_kv_heads, max_seq,
+                                nodes_per_slot, d_starts, d_nodes, d_counts);
+    };
+    const cudaError_t e = head_dim == 64 ? go(mkops::kv_compact<64>) : go(mkops::kv_compact<128>);
     return e == cudaSuccess ? MK_OK : mkops::cuda_error(e, "mk_kv_compact");
 }
 
@@ -157,19 +157,15 @@ extern "C" int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, 
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int cpr = head_dim / 8;
     auto go = [&](auto kernel, auto *kc, auto *vc, int c) {
-        kernel<<<grid, mkops::kT, 0, s>>>(kc, vc, n_layers, slots, n_kv_heads, max_seq, c, d_sources, d_lengths);
+        return mkops::launch_op(kernel, grid, mkops::kT, 0, 0, s, kc, vc, n_layers, slots, n_kv_heads, max_seq, c,
+                                d_sources, d_lengths);
     };
     uint4 *k4 = static_cast<uint4 *>(k), *v4 = static_cast<uint4 *>(v);
-    if (slots <= 4)
-        go(mkops::kv_reorder<uint4, 4>, k4, v4, cpr);
-    else if (slots <= 8)
-        go(mkops::kv_reorder<uint4, 8>, k4, v4, cpr);
-    else if (slots <= 16)
-        go(mkops::kv_reorder<uint4, 16>, k4, v4, cpr);
-    else if (slots <= 32)
-        go(mkops::kv_reorder<uint4, 32>, k4, v4, cpr);
-    else
-        go(mkops::kv_reorder<uint2, 64>, static_cast<uint2 *>(k), static_cast<uint2 *>(v), 2 * cpr);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = slots <= 4    ? go(mkops::kv_reorder<uint4, 4>, k4, v4, cpr)
+                          : slots <= 8  ? go(mkops::kv_reorder<uint4, 8>, k4, v4, cpr)
+                          : slots <= 16 ? go(mkops::kv_reorder<uint4, 16>, k4, v4, cpr)
+                          : slots <= 32 ? go(mkops::kv_reorder<uint4, 32>, k4, v4, cpr)
+                                        : go(mkops::kv_reorder<uint2, 64>, static_cast<uint2 *>(k),
+                                             static_cast<uint2 *>(v), 2 * cpr);
     return e == cudaSuccess ? MK_OK : mkops::cuda_error(e, "mk_kv_reorder");
 }

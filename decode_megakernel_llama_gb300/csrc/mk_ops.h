@@ -13,6 +13,17 @@ namespace mkops {
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
+// Programmatic dependent launch: the operators are launched so that they may be
+// brought in while the kernel before them in the stream runs; they touch memory
+// only behind pdl_wait, which waits for that kernel's end. pdl_trigger lets the
+// next one be brought in. Without the launch attribute both do nothing.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_begin() {
+    pdl_wait();
+    pdl_trigger();
+}
+
 // Two fp32 rounded to nearest even as bf16, `lo` in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t u;
@@ -20,6 +31,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return u;
 }
 #endif
+
+// Launches a kernel that begins with pdl_begin, in clusters of `cluster` CTAs
+// along x (0: none). Measured in a stream of calls from the host: a rope token
+// 4.1 us without the attribute, 3.1 with it; a token's attention 8.2 and 6.0.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_op(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, int cluster, cudaStream_t s,
+                             Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
 
 // Sets the calling thread's error text from a CUDA error; returns MK_ERR_CUDA.
 int cuda_error(cudaError_t e, const char *what);

@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(32) tree_masks(const int32_t *__restrict__ par
                                                  const int32_t *__restrict__ counts, int T, int start,
                                                  uint64_t *masks, int32_t *depths, int32_t *rows, int32_t *length) {
     __shared__ int32_t up[MK_MAX_TREE];
+    pdl_begin();
     const int b = blockIdx.x, n = counts ? min(max(counts[b], 0), T) : T;
     for (int t = threadIdx.x; t < n; t += 32) {
         const int p = parents[(int64_t)b * T + t];
@@ -126,20 +127,6 @@ cudaError_t configure() {
     return e;
 }
 
-void launch_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 grid, int smem, int cluster,
-                   cudaStream_t s) {
-    cfg = cudaLaunchConfig_t{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kAttnThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-}
-
 // Clusters of 2^k CTAs that the device holds at once (asked of the runtime
 // once; its count of clusters is for one CTA an SM).
 template <class K>
@@ -148,9 +135,16 @@ int active_clusters(int k, int n_sm) {
     int n = known[k].load(std::memory_order_relaxed);
     if (n) return n;
     int per_sm = 1;
-    cudaLaunchConfig_t cfg;
+    cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    launch_config(cfg, attr, dim3(1 << k, n_sm * 4), K::kSmem, 1 << k, nullptr);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1 << k;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(1 << k, n_sm * 4);
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = K::kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     if (configure<K>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, K::fn(), &cfg) != cudaSuccess || n < 1 ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, K::fn(), kAttnThreads, K::kSmem) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -207,20 +201,10 @@ cudaError_t launch(TreeArgs a, int max_len, int n_sm, cudaStream_t s, int64_t *w
     if (!cache_map(&kmap, a.kc, a.slots * a.Hkv, a.max_seq, K::HD) ||
         !cache_map(&vmap, a.vc, a.slots * a.Hkv, a.max_seq, K::HD))
         return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[1];
-    launch_config(cfg, attr, dim3(p.S, a.B * a.Hkv, row_tiles), K::kSmem, p.ws ? 1 : p.S, s);
-    e = cudaLaunchKernelEx(&cfg, K::fn(), kmap, vmap, a);
+    e = launch_op(K::fn(), dim3(p.S, a.B * a.Hkv, row_tiles), kAttnThreads, K::kSmem, p.ws ? 1 : p.S, s, kmap, vmap, a);
     if (e != cudaSuccess || !p.ws) return e;
-    cudaLaunchConfig_t jc = {};
-    jc.gridDim = dim3(row_tiles, a.B * a.Hkv, (K::NR * K::HD / 4 + 255) / 256);
-    jc.blockDim = dim3(256);
-    jc.stream = s;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    jc.attrs = attr;
-    jc.numAttrs = 1;
-    return cudaLaunchKernelEx(&jc, tree_join<K::HD, K::TERMS, K::NR>, a, p.S);
+    return launch_op(tree_join<K::HD, K::TERMS, K::NR>,
+                     dim3(row_tiles, a.B * a.Hkv, (K::NR * K::HD / 4 + 255) / 256), 256, 0, 0, s, a, p.S);
 }
 
 // The kernel of 16 or 32 columns that holds the tree's rows of a kv head; for more
@@ -258,14 +242,12 @@ cudaError_t tree_attention_work_floats(const TreeArgs &a, int hd, bool f32, int 
 
 cudaError_t tree_masks_launch(const int32_t *parents, const int32_t *counts, int B, int T, uint64_t *masks,
                               int32_t *depths, cudaStream_t s) {
-    tree_masks<<<B, 32, 0, s>>>(parents, counts, T, 0, masks, depths, nullptr, nullptr);
-    return cudaGetLastError();
+    return launch_op(tree_masks, dim3(B), 32, 0, 0, s, parents, counts, T, 0, masks, depths, nullptr, nullptr);
 }
 
 cudaError_t tree_plan_launch(const int32_t *parents, int n, int start, uint64_t *masks, int32_t *positions,
                              int32_t *rows, int32_t *length, cudaStream_t s) {
-    tree_masks<<<1, 32, 0, s>>>(parents, nullptr, n, start, masks, positions, rows, length);
-    return cudaGetLastError();
+    return launch_op(tree_masks, dim3(1), 32, 0, 0, s, parents, nullptr, n, start, masks, positions, rows, length);
 }
 
 }  // namespace mkops
