@@ -2,21 +2,31 @@
 //
 // Two tcgen05 kernels share everything but which operand the queries are.
 //
-// tree_attention (few query rows, up to 64 a CTA): the CACHE is the A operand,
-// so a tile's 128 cache rows (then 64 or 128 head dims) fill the instruction's
-// 128 rows whatever the number of queries, and all softmax threads have work
-// even for one query row:
+// tree_attention (few query rows, 16 or 32 a CTA): the CACHE is the A operand, so
+// a tile's 128 cache rows (then 64 or 128 head dims) fill the instruction's 128
+// rows whatever the number of queries, and all softmax threads have work even for
+// one query row:
 //   S^T [128 cache rows][N] = K [128][HD] . Q^T    (both K-major)
 //   O^T [HD][N]            += V^T [HD][128] . P^T   (both MN-major: V as TMA wrote
 //                                                    it, P as the threads write it)
 // tree_attention_rows (many): 128 query rows are the A operand,
 //   S [128 rows][128 cache rows] = Q . K^T, O [128 rows][HD] += P . V,
-// P from tensor memory, where it overwrites the scores it came from.
+// P from tensor memory (for fp32 queries where the scores were).
 // Measured (MMAs back to back): an instruction of M = 128 costs the larger of
 // 44 cycles, its share of shared-memory reads (4 KB of A and 32 N bytes of B at
 // 128 B a cycle) and N / 2 cycles, and a chain of 8 is seen complete ~340
-// cycles after its last issue. So the first form pays 48 cycles an instruction
-// for N = 64 and the second 64 for twice the scores (and none for P).
+// cycles after its last issue. So the first form pays 56 cycles an instruction
+// for 32 fp32 rows (N = 96) and the second 64 for 128 rows, and none of its P
+// passes through shared memory.
+//
+// What bounds them: the first, for a long cache, memory (131,079 rows of 8 kv heads
+// of 128: 86.0 us = 6.24 TB/s, 0.93 of the measured copy rate); for a short one
+// latency (one token over 191 rows: 5.8 us, of which the launch, the first copies
+// and the join of two splits are all but 2). The second the softmax warps' time
+// a tile, ~1,250 cycles against 616 of its MMAs and 512 of its exponentials (8
+// ragged sequences of up to 8,253 rows, 244 query rows, 64 dims: 49.3 us, of which
+// the longest sequence's 65 tiles are 44): barriers and exponentials share
+// the warps' memory queue.
 //
 // fp32 queries and weights enter as three bf16 terms each (24 bits: x = t0 + t1 +
 // t2 to half a step of fp32): side by side in the first kernel's B operand, N =
@@ -33,13 +43,15 @@
 // lane 64 of O^T is sum p; for HD = 128 they stay per thread until the end. In the
 // second kernel a row's statistics are one thread's own.
 //
-// Overlap (one CTA an SM): one warp fills a ring of K and V tiles by TMA, one
-// issues the MMAs, and two groups of four softmax warps take the tiles in turn,
-// each with its own buffers of S and P, its own maxima, sums and O (joined at the
-// end like two splits), so neither a product's latency nor a group's votes stand
-// in the other's way. S(i + 2) is issued behind PV(i): the order of the MMAs alone
-// makes the buffers free in time. A commit of a product serves both who waits for
-// its result and the ring's next copy.
+// Overlap (one CTA an SM): two warps fill rings of K and V tiles by TMA, one issues
+// the MMAs, and two groups of four softmax warps take the tiles in turn, each
+// with its own buffers of S and P, its own maxima, sums and O (joined at the end
+// like two splits), so neither a product's latency nor a group's votes stand in
+// the other's way. With rings of four tiles or more and P apart from S, S runs
+// three tiles ahead of PV and starts as soon as the scores before are read
+// (64 fp32 rows over 8,208: 52.6 -> 44.2 us for one split); else S(i + 2) is issued
+// behind PV(i), and the order of the MMAs alone makes the buffers free in time. A
+// commit of a product serves both who waits for its result and the ring's next copy.
 //
 // Up to 8 splits of a sequence's cache rows form a thread-block cluster: each
 // CTA leaves its partial O, sums and maxima in its shared memory, and the

@@ -9,7 +9,7 @@ import torch
 
 U = 2.0 ** -24
 BF = 2.0 ** -8
-HI_LO = 2.0 ** -16  # what two bf16 terms leave of a value: half a step of the second
+TERMS = 2.0 ** -24  # what three bf16 terms leave of a value: half a step of the third (2^-8 of a rest of a rest)
 
 
 def rope(qkv, Hq, Hkv, hd, positions, inv_freq, q_norm, k_norm, eps, mscale, interleaved):
@@ -47,11 +47,12 @@ def attention(q, k, v, lengths, masks, counts, slots, scale):
 
     With p the normalised weights and A = sum p |v| the kernel's error is at most A times
       2 d    the scores' error d (the larger of the row's) moves every weight by at most e^(2d) - 1;
-             d = scale sum |q k| (e_q + 2 hd u): e_q = HI_LO for fp32 queries (0 for bf16), fp32 sums of 2 hd terms;
-             and the scaled difference from the maximum rounded: u (|s| + |m|) <= 2 u max|s|
-      e_p    the weights' own rounding: HI_LO (fp32) or BF (bf16), and exp within 2^-20
-      (n/16 + 80) 2^-23   the running sums of weights and products over the n rows, 16 rows at a time, tens of
-             rescalings and joins, one step each
+             d = scale sum |q k| (e_q + 3 hd u): e_q = TERMS + u for fp32 queries, scaled before they are split (0 for
+             bf16), fp32 sums of 3 hd terms; and the scaled difference from the maximum rounded: u (|s| + |m|) <= 2 u
+             max|s|
+      e_p    the weights' own rounding: TERMS (fp32) or BF (bf16), and exp2 within 2^-20
+      (3 n/16 + 80) 2^-23   the running sums of weights and products over the n rows, 16 rows and a term at a time,
+             tens of rescalings and joins, one step each (a tensor core's sum may cut instead of rounding)
     plus the rounding of a bf16 result."""
     f32 = q.dtype == torch.float32
     B, T, Hq, hd = q.shape
@@ -78,9 +79,9 @@ def attention(q, k, v, lengths, masks, counts, slots, scale):
                 s = scale * qt @ kt.T
                 p = torch.softmax(s, -1)
                 a = p @ vt.abs()
-                d = scale * (qt.abs() @ kt.abs().T) * ((HI_LO if f32 else 0.0) + 2 * hd * U) + 2 * U * s.abs().amax()
-                rel = 2 * d.amax(-1, keepdim=True) + (HI_LO if f32 else BF) + 2.0 ** -20
-                rel = rel + (len(on) / 16 + 80) * 2.0 ** -23
+                d = scale * (qt.abs() @ kt.abs().T) * ((TERMS + U if f32 else 0.0) + 3 * hd * U) + 2 * U * s.abs().amax()
+                rel = 2 * d.amax(-1, keepdim=True) + (TERMS if f32 else BF) + 2.0 ** -20
+                rel = rel + (3 * len(on) / 16 + 80) * 2.0 ** -23
                 o = p @ vt
                 out[b, t, h * G:(h + 1) * G] = o
                 tol[b, t, h * G:(h + 1) * G] = a * rel + (0.0 if f32 else BF) * (o.abs() + a * rel) + 1e-30
