@@ -496,8 +496,11 @@ def tree_masks(parents, masks, depths=None, counts=None, stream=None) -> None:
         _need(depths, "depths", torch.int32, (B, T), parents)
     if counts is not None:
         _need(counts, "counts", torch.int32, (B,), parents)
-    _run_on(torch, parents.get_device(), stream, load().mk_tree_masks, parents.data_ptr(), None if counts is None else counts.data_ptr(), B,
-            T, masks.data_ptr(), None if depths is None else depths.data_ptr())
+    if B == 0:
+        return
+    _run_on(torch, parents.get_device(), stream, load().mk_tree_masks, parents.data_ptr(),
+            None if counts is None else counts.data_ptr(), B, T, masks.data_ptr(),
+            None if depths is None else depths.data_ptr())
 
 
 def tree_accept(tokens, parents, draws):
@@ -613,9 +616,16 @@ class Megakernel:
     def verify(self, d_tokens, d_parents, start_pos: int, out_tokens, logits=None, stream=None) -> None:
         """mk_verify: the n nodes of a drafted tree (int32 CUDA tensors [n]) behind the committed positions
         [0, start_pos) of slot 0; out_tokens int32 CUDA tensor [n], logits float32 CUDA tensor [n][vocab] or None."""
-        n = int(d_tokens.numel())
+        import torch
+        n, i32, dev = int(d_tokens.numel()), torch.int32, self._keep[1].device
         if int(d_parents.numel()) != n or int(out_tokens.numel()) < n:
             _bad("d_parents and out_tokens must have as many entries as d_tokens")
+        for t, what in ((d_tokens, "d_tokens"), (d_parents, "d_parents"), (out_tokens, "out_tokens")):
+            if t.dtype is not i32 or t.device != dev or not t.is_contiguous():
+                _bad(f"{what} must be a contiguous int32 tensor on {dev}")
+        if logits is not None and (logits.dtype is not torch.float32 or logits.device != dev
+                                   or not logits.is_contiguous() or logits.numel() < n * self.shape.vocab):
+            _bad(f"logits must be a contiguous float32 tensor of {n} x {self.shape.vocab} on {dev}")
         check(load().mk_verify(self.h, d_tokens.data_ptr(), d_parents.data_ptr(), n, int(start_pos),
                                logits.data_ptr() if logits is not None else None, out_tokens.data_ptr(),
                                _stream_ptr(stream)))
@@ -625,6 +635,8 @@ class Megakernel:
         verify): its cache rows move up to start_pos .., and the nodes come back as a list. Decoding goes on at
         start_pos + len(path) with token draws[path[-1]]."""
         import torch
+        if not 0 <= int(start_pos) <= self.max_seq - len(tokens):
+            _bad("tree rows outside [0, max_seq)")
         path = tree_accept(tokens, parents, draws)
         if path[-1] != len(path) - 1:  # else every row is in its place
             _, k, v = self._keep

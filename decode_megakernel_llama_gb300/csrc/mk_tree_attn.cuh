@@ -713,6 +713,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         }
         soft_sync();
+        tc_fence_after();  // (a group that passed early reads O behind the barrier, too)
         // the groups' factors to the larger maximum, which both keep
         float f0 = 0.f, f1 = 0.f;
         if (first < NR) {
@@ -760,6 +761,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (*err && first < NR) lsum[first] = __uint_as_float(0x7FC00000u);  // a wait ran out: NaN
         if (y->bad[0] | y->bad[1]) add_taken_out<HD, TERMS, false>(a, b, kvh, G, row0, rows, sq, y->bad, mref, Os, first);
     }
+    tc_fence_before();
     __syncwarp();
     __syncthreads();
     if (*err && tid == 0) drain(y, a.err);
@@ -1025,6 +1027,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (!ok) *err = 1;
         gm[g * kRows + row] = m;
         soft_sync();
+        tc_fence_after();  // (a group that passed early reads O behind the barrier, too)
         // the groups' O to the larger maximum: group 0 writes, group 1 adds
         const float best = fmaxf(m, gm[(g ^ 1) * kRows + row]), scale = g < nt ? ex2(m - best) : 0.f;
         l *= scale;
@@ -1062,6 +1065,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (*err && g == 0) lsum[row] = __uint_as_float(0x7FC00000u);  // a wait ran out: NaN
         if (y->bad[0] | y->bad[1]) add_taken_out<HD, TERMS, true>(a, b, kvh, G, row0, rows, sq, y->bad, mref, Os, st);
     }
+    tc_fence_before();
     __syncwarp();
     __syncthreads();
     if (*err && tid == 0) drain(y, a.err);

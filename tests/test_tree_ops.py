@@ -122,6 +122,14 @@ def test_tree_masks_refuses(lib):
     assert lib.mk_tree_masks(FAKE, None, 0, 4, FAKE, None, None) == 0
 
 
+def test_binding_of_an_empty_batch_does_nothing():
+    import torch
+    empty, m = torch.zeros(0, 5, dtype=torch.int32), torch.zeros(0, 5, dtype=torch.int64)
+    _lib.tree_masks(empty, m, depths=empty.clone(), counts=empty[:, 0].contiguous())
+    k, q = torch.zeros(2, 2, 32, 64, dtype=torch.bfloat16), torch.zeros(0, 5, 4, 64)
+    _lib.tree_attention(q, k, k.clone(), torch.zeros(0, dtype=torch.int32), m, q.clone())
+
+
 def test_binding_refuses_before_any_launch():
     import torch
     bf, i32 = torch.bfloat16, torch.int32

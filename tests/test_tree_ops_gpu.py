@@ -462,3 +462,129 @@ def test_cache_moves_in_a_graph(dev):
         gr.replay()
         k0, v0 = (ref.compact(ref.reorder(x, src, ln), starts, nodes, counts) for x in (k0, v0))
     assert torch.equal(k, k0) and torch.equal(v, v0)
+
+
+# ---------------------------------------------------------------- together
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("hd,T,Hq,Hkv", [(64, 5, 4, 2), (64, 21, 8, 2), (128, 13, 6, 2)])
+def test_a_step_of_trees_in_one_graph(dev, dtype, hd, T, Hq, Hkv):
+    """Masks and depths, rotation and append by depth, attention, compaction of a path: a padded batch in slots out of
+    order, captured on a stream of its own, replayed on other trees."""
+    B, n_slots, S = 3, 4, 320
+    g = torch.Generator().manual_seed(hd + T)
+    width = (Hq + 2 * Hkv) * hd
+    qkv = torch.zeros(B, T, width, dtype=dtype, device=dev)
+    out = torch.zeros(B, T, Hq, hd, dtype=dtype, device=dev)
+    k, v = (torch.zeros(1, n_slots, Hkv, S, hd, dtype=BF, device=dev) for _ in range(2))
+    ints = {n: torch.zeros(*s, dtype=I32, device=dev) for n, s in
+            dict(parents=(B, T), depths=(B, T), counts=(B,), lengths=(B,), positions=(B * T,), rows=(B * T,),
+                 token_slots=(B * T,), slots=(B,), starts=(n_slots,), moved=(n_slots,), nodes=(n_slots, T)).items()}
+    masks = torch.zeros(B, T, dtype=torch.int64, device=dev)
+    freq = _lib.rope_frequencies(hd, 1e4)[0].to(dev)
+    q = qkv.view(B, T, -1, hd)[:, :, :Hq]
+    i, step = ints, torch.arange(T, dtype=I32, device=dev)
+
+    def run():
+        _lib.tree_masks(i["parents"], masks, depths=i["depths"], counts=i["counts"])
+        i["positions"].copy_((i["lengths"][:, None] + i["depths"]).view(-1))
+        i["rows"].copy_(torch.where(step < i["counts"][:, None], i["lengths"][:, None] + step, -1).view(-1))
+        flat = qkv.view(B * T, width)
+        _lib.rope_append(flat, flat[:, :Hq * hd].view(B * T, Hq, hd), k[0], v[0], i["positions"], i["rows"], freq,
+                         slots=i["token_slots"])
+        _lib.tree_attention(q, k[0], v[0], i["lengths"], masks, out, counts=i["counts"], slots=i["slots"])
+        _lib.kv_compact(k, v, i["starts"], i["nodes"], i["moved"])
+
+    def fill(seed):
+        """New contents of every array; what run() has to make of them, from the 64-bit forms."""
+        g.manual_seed(seed)
+        lengths, counts, slots = [130, 3, 250], [T, T - 3, 2], [2, 0, 3] if seed % 2 else [1, 3, 2]
+        parents = torch.full((B, T), -1, dtype=I32)
+        for b in range(B):
+            parents[b, :counts[b]] = torch.tensor(ref.random_parents(counts[b], g), dtype=I32)
+        i["parents"].copy_(parents)
+        for name, x in (("lengths", lengths), ("counts", counts), ("slots", slots)):
+            i[name].copy_(torch.tensor(x, dtype=I32))
+        i["token_slots"].copy_(torch.tensor(slots, dtype=I32).repeat_interleave(T))
+        paths = []
+        for b in range(B):
+            at, path = counts[b] - 1, []
+            while at >= 0:
+                path.insert(0, at)
+                at = int(parents[b, at])
+            paths.append(path)
+        starts, moved, nodes = torch.zeros(n_slots, dtype=I32), torch.zeros(n_slots, dtype=I32), torch.zeros(n_slots, T, dtype=I32)
+        for b in range(B):
+            starts[slots[b]], moved[slots[b]] = lengths[b], len(paths[b])
+            nodes[slots[b], :len(paths[b])] = torch.tensor(paths[b], dtype=I32)
+        for name, x in (("starts", starts), ("moved", moved), ("nodes", nodes)):
+            i[name].copy_(x)
+        qkv.copy_(normal(g, B, T, width, dtype=dtype))
+        k.copy_(normal(g, *k.shape, dtype=BF))
+        v.copy_(normal(g, *v.shape, dtype=BF))
+        out.fill_(99.0)
+        masks.fill_(-1)
+        i["depths"].fill_(0)
+        return lengths, counts, slots, parents, paths, qkv.clone(), k.clone(), v.clone()
+
+    def check(lengths, counts, slots, parents, paths, qkv0, k0, v0):
+        words = torch.full((B, T), -1, dtype=torch.int64)
+        for b in range(B):
+            w = ref.mask_words(parents[b, :counts[b]].tolist())
+            words[b, :counts[b]] = torch.tensor([ref.signed(x) for x in w])
+            depth = torch.tensor([bin(x).count("1") - 1 for x in w], dtype=I32, device=dev)
+            assert torch.equal(i["depths"][b, :counts[b]], depth)
+            (q_ref, q_mag), (k_ref, k_mag), v_ref = ref.rope(qkv0[b, :counts[b]], Hq, Hkv, hd, lengths[b] + depth, freq,
+                                                             None, None, 0.0, 1.0, False)
+            tol = ref.ROPE_TOL * q_mag
+            half = 0.0 if dtype == torch.float32 else ref.BF
+            got = q[b, :counts[b]].double()
+            assert ((got - q_ref).abs() <= tol + half * (q_ref.abs() + tol)).all()
+            # the cache as it was, with the path's rows (all of them, unmoved, behind)
+            kb, vb = k0[0, slots[b]], v0[0, slots[b]]
+            rows = slice(lengths[b], lengths[b] + counts[b])
+            vb[:, rows] = v_ref.to(BF).transpose(0, 1)
+            tol = ref.ROPE_TOL * k_mag
+            tol = tol + ref.BF * (k_ref.abs() + tol)
+            bound = torch.zeros(Hkv, S, hd, dtype=torch.float64, device=dev)
+            want = kb.double()
+            want[:, rows], bound[:, rows] = k_ref.transpose(0, 1), tol.transpose(0, 1)
+            for to, node in enumerate(paths[b]):  # a path's nodes only move down: in order is as if at once
+                for x in (want, bound, vb):
+                    x[:, lengths[b] + to] = x[:, lengths[b] + node]
+            assert torch.equal(v[0, slots[b]], vb)
+            assert ((k[0, slots[b]].double() - want).abs() <= bound).all()
+        assert torch.equal(masks.cpu(), words)
+        return words
+
+    def attended(lengths, counts, slots, words, kk, vv):
+        cn, sl = torch.tensor(counts), torch.tensor(slots)
+        o, tol = ref.attention(q, kk[0], vv[0], lengths, words, cn, sl, hd ** -0.5)
+        on = ~o.isnan()
+        assert ((out.double() - o).abs()[on] <= tol[on]).all()
+        for b in range(B):
+            assert (out[b, counts[b]:] == 99.0).all()
+
+    side = torch.cuda.Stream()
+    fill(0)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run()
+    for seed in (1, 2):
+        made = fill(seed)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.cuda.synchronize()
+        words = check(*made)
+        # attention read the appended rows before the path moved: what the moves did not touch lies there still,
+        # and the moved rows' first copies are redone here
+        kk, vv = made[6].clone(), made[7].clone()
+        again = made[5].view(B * T, width).clone()
+        _lib.rope_append(again, torch.empty(B * T, Hq, hd, dtype=dtype, device=dev), kk[0], vv[0], i["positions"],
+                         i["rows"], freq, slots=i["token_slots"])
+        torch.cuda.synchronize()
+        attended(*made[:3], words, kk, vv)

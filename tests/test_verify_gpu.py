@@ -212,8 +212,14 @@ def test_verify_refuses_and_reports(cuda_dev):
         assert e.value.code == _lib.MK_ERR_INVALID_ARG
     with pytest.raises(_lib.MKError):
         pair.mk.verify(tk[:4], pr[:3], 0, out)
-    with pytest.raises(_lib.MKError):
-        pair.mk.verify(tk[:4], pr[:4], 0, out[:3])
+    lg = torch.empty(3, TINY.vocab, device=dev)
+    for bad in (dict(out_tokens=out[:3]), dict(d_tokens=tk[:4].long()), dict(d_parents=pr[:8:2]),
+                dict(out_tokens=out.cpu()), dict(logits=lg), dict(logits=torch.empty(4, TINY.vocab).half().to(dev))):
+        with pytest.raises(_lib.MKError):
+            pair.mk.verify(**{**dict(d_tokens=tk[:4], d_parents=pr[:4], start_pos=0, out_tokens=out), **bad})
+    for start in (-1, 15):  # two nodes do not fit behind 15 rows of 16
+        with pytest.raises(_lib.MKError):
+            pair.mk.accept([1, 2], [-1, 0], [2, 3], start)
     bad = torch.tensor([1, TINY.vocab, 2], dtype=I32, device=dev)
     pair.mk.verify(bad, torch.tensor([-1, 0, 1], dtype=I32, device=dev), 0, out)
     assert pair.mk.status() == _lib.MK_ERR_INVALID_ARG
