@@ -80,6 +80,50 @@ def test_rope_append_large_prompt(dev):
     rope_case(dev, 3000, 8, 2, 64, 64, torch.float32, True, False, slots=2, S=1600)
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,hd,rot,dtype,kw", [
+    (1024, 4, 4, 64, 64, torch.float32, dict(norm=True)), (1025, 32, 8, 64, 64, torch.float32, dict(norm=True)),
+    (1300, 24, 8, 128, 32, BF, dict(norm=True, inter=True)), (2500, 9, 3, 64, 38, torch.float32, dict(pad=4)),
+    (1100, 5, 1, 128, 126, BF, dict(pad=8)), (2999, 2, 1, 64, 2, BF, dict(inter=True, in_place=True)),
+    (1500, 8, 2, 128, 128, torch.float32, dict(norm=True, in_place=True)),
+    (1700, 3, 2, 64, 48, BF, dict(norm=True, pad=4)),              # rows that start at 8 bytes of 16
+    (1030, 40, 8, 128, 64, torch.float32, dict(norm=True)),        # rows of 28 KB
+])
+def test_rope_append_long_prompts(dev, n, Hq, Hkv, hd, rot, dtype, kw):
+    rope_case(dev, n, Hq, Hkv, hd, rot, dtype, **{"norm": False, "inter": False, **kw}, slots=2, S=n, base=100000)
+
+
+def test_rope_append_long_prompts_in_streams_and_graphs(dev):
+    g = torch.Generator().manual_seed(9)
+    n, Hq, Hkv, hd = 1600, 6, 2, 64
+    freq = _lib.rope_frequencies(hd, 1e4)[0].to(dev)
+    rows = torch.arange(n, dtype=I32, device=dev)
+    rows[5], rows[1400] = -1, n
+    sides = []
+    for _ in range(2):
+        x = normal(g, n, (Hq + 2 * Hkv) * hd)
+        q, k, v = torch.empty(n, Hq, hd, device=dev), *(torch.zeros(1, Hkv, n, hd, dtype=BF, device=dev) for _ in "kv")
+        sides.append((x, q, k, v, torch.cuda.Stream(), torch.cuda.CUDAGraph()))
+    torch.cuda.synchronize()
+    for x, q, k, v, s, gr in sides:
+        _lib.rope_append(x, q, k, v, rows, rows, freq, stream=s)
+    torch.cuda.synchronize()
+    for x, q, k, v, s, gr in sides:
+        with torch.cuda.graph(gr):
+            _lib.rope_append(x, q, k, v, rows, rows, freq)
+        x.mul_(-2)
+    want = [(-2 * q, -2 * k, -2 * v) for x, q, k, v, s, gr in sides]  # (exact: signs and a power of two)
+    torch.cuda.synchronize()
+    for x, q, k, v, s, gr in sides:
+        with torch.cuda.stream(s):
+            gr.replay()
+    torch.cuda.synchronize()
+    for (x, q, k, v, s, gr), w in zip(sides, want):
+        (q_ref, mag), _, _ = ref.rope(x, Hq, Hkv, hd, rows, freq, None, None, 0, 1.0, False)
+        assert ((q.double() - q_ref).abs() <= ref.ROPE_TOL * mag).all()
+        assert torch.equal(q, w[0]) and torch.equal(k, w[1]) and torch.equal(v, w[2])
+        assert (k[:, :, 5] == 0).all() and (v[:, :, 1400] == 0).all()
+
+
 def test_rope_append_rows_outside_the_cache_are_not_written(dev):
     g = torch.Generator().manual_seed(5)
     n, Hq, Hkv, hd, S = 8, 2, 1, 64, 16
@@ -339,6 +383,114 @@ def test_tree_attention_long_caches_in_streams_and_graphs(dev, hd, T, Hq, Hkv, d
         torch.cuda.synchronize()
         for c, w in zip(cases, want):
             assert torch.equal(c.out, w)
+
+
+# Large trees (128 rows and more) of ragged batches, in caches far longer than the sequences.
+LARGE = [(64, torch.float32), (64, BF), (128, torch.float32), (128, BF)]
+FAR = 16400
+
+
+@pytest.mark.parametrize("hd,dtype", LARGE)
+def test_tree_attention_large_trees_ragged(dev, hd, dtype):
+    c = Case(dev, [700, 0, 129, 1, 64, 3000, 127, 128], 40, 8, 2, hd, dtype, counts=[40, 1, 0, 13, 7, 40, 33, 32],
+             slots=[4, 6, 0, 2, 5, 7, 1, 8], n_slots=9, S=FAR, roots=3)
+    c.run()
+    c.check()
+    c.out.fill_(99.0)
+    c.slots[3], c.lengths[6], c.counts[7] = 9, FAR, -1  # outside the caches, no room, no node
+    c.run()
+    torch.cuda.synchronize()
+    assert (c.out[[3, 6, 7]] == 99.0).all()
+    c.slots[3], c.lengths[6] = 3, 0  # (for the plain form: the same, said in bounds)
+    c.counts[3] = c.counts[6] = c.counts[7] = 0
+    c.check()
+    c.counts.fill_(0)  # no work at all
+    c.out.fill_(99.0)
+    c.run()
+    torch.cuda.synchronize()
+    assert (c.out == 99.0).all()
+
+
+@pytest.mark.parametrize("hd,dtype", LARGE)
+def test_tree_attention_large_trees_of_many_short_sequences(dev, hd, dtype):
+    B = 33
+    c = Case(dev, [(7 * b) % 150 for b in range(B)], 17, 32, 4, hd, dtype, S=4400, counts=[1 + (5 * b) % 17 for b in range(B)])
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("hd,dtype", LARGE)
+def test_tree_attention_large_trees_junk(dev, hd, dtype):
+    T = 40
+    c = Case(dev, [0, 150, 600, 90, 255, 256, 1000, 5], T, 8, 2, hd, dtype, counts=[T, 5, T, T, T, T, T, T], S=FAR)
+    c.masks[0, 2] = 0
+    c.masks[0, 3] = 1 << 45  # a bit behind the tree
+    c.masks[2, 35] = -1      # every bit: the T nodes
+    nan, inf = float("nan"), float("inf")
+    for x in (c.k, c.v):
+        x[:, :, 1100:] = nan
+        x[0, :, T:] = inf
+        x[1, :, 155:] = nan
+    c.run()
+    c.check()
+    assert (c.out[0, 2:4] == 0).all()
+    # keys and values of nodes that nobody but themselves sees; two tiles of one sequence, and other sequences
+    hit = [(1, 154 - 150), (3, 20), (3, 39), (4, 0), (6, 30)]
+    for b, t in hit:
+        c.masks[b] &= ~(1 << t)
+        c.masks[b, t] |= 1 << t
+    c.run()
+    torch.cuda.synchronize()
+    keep = c.out.clone()
+    for b, t in hit:
+        at = int(c.lengths[b]) + t
+        c.v[b, :, at] = inf
+        c.k[b, 0, at] = nan
+        c.v[b, 1, at, 3] = nan
+    c.run()
+    torch.cuda.synchronize()
+    for b in range(8):
+        for t in range(T):
+            if (b, t) in hit:
+                assert not c.out[b, t].isfinite().all()
+            else:
+                assert torch.equal(c.out[b, t], keep[b, t]), (b, t)
+
+
+@pytest.mark.parametrize("hd,dtype", LARGE)
+def test_tree_attention_large_trees_in_streams_and_graphs(dev, hd, dtype):
+    cases = [Case(dev, [3000, 100, 2047, 900, 31, 4000, 500, 1], 40, 8, 2, hd, dtype, S=FAR, seed=s) for s in (1, 2)]
+    for c in cases:
+        c.run()
+        c.check()
+    want = [c.out.clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    graphs = []
+    for c in cases:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            c.run()
+        graphs.append(gr)
+    for rep in range(6):
+        for c in cases:
+            c.out.fill_(99.0)
+        torch.cuda.synchronize()
+        for c, s, gr in zip(cases, streams, graphs):
+            if rep % 2:
+                with torch.cuda.stream(s):
+                    gr.replay()
+            else:
+                c.run(stream=s)
+        torch.cuda.synchronize()
+        for c, w in zip(cases, want):
+            assert torch.equal(c.out, w)
+    for c in cases:  # other lengths in the same graph
+        c.lengths.copy_(c.lengths.flip(0))
+        c.out.fill_(99.0)
+    graphs[0].replay()
+    graphs[1].replay()
+    for c in cases:
+        c.check()
 
 
 def test_tree_attention_far_scores_and_status(dev):

@@ -35,9 +35,10 @@ def rope(qkv, Hq, Hkv, hd, positions, inv_freq, q_norm, k_norm, eps, mscale, int
 
 
 # The norm: a sum of squares over 4 + log2(32) adds and a product (9 u, halved
-# by the root), root, division and eps (3 u), two products (2 u): 10 u. The
-# angle: the fraction of a turn rounded to fp32 (3.2 u of a radian), sine and
-# cosine within 2 u, times mscale (1 u), a product and an add (2 u): 8.2 u.
+# by the root), the reciprocal root within two steps (4 u) and eps (1 u), two
+# products (2 u): 12 u. The angle: the fraction of a turn rounded to fp32 (3.2 u
+# of a radian), sine and cosine within 2 u, times mscale (1 u), a product and an
+# add (2 u): 8.2 u.
 # A position below 2^17 adds 2^17 * 2^-53 turns: nothing. Rounded up to 24 u.
 ROPE_TOL = 24 * U
 
