@@ -23,10 +23,10 @@
 // of 128: 86.0 us = 6.24 TB/s, 0.93 of the measured copy rate); for a short one
 // latency (one token over 191 rows: 5.8 us, of which the launch, the first copies
 // and the join of two splits are all but 2). The second the softmax warps' time
-// a tile, ~1,250 cycles against 616 of its MMAs and 512 of its exponentials (8
-// ragged sequences of up to 8,253 rows, 244 query rows, 64 dims: 49.3 us, of which
-// the longest sequence's 65 tiles are 44): barriers and exponentials share
-// the warps' memory queue.
+// a tile, ~1,130 cycles against 616 of its MMAs and 530 of its exponentials at 31 a
+// cycle (8 ragged sequences of up to 8,253 rows, 244 query rows, 64 dims: 44.3 us, of
+// which the longest sequence's 65 tiles are 39): a warp's loads, maximum, weights
+// and stores come one behind the other, and only two warps share a scheduler.
 //
 // fp32 queries and weights enter as three bf16 terms each (24 bits: x = t0 + t1 +
 // t2 to half a step of fp32): side by side in the first kernel's B operand, N =
@@ -49,9 +49,9 @@
 // like two splits), so neither a product's latency nor a group's votes stand in
 // the other's way. With rings of four tiles or more and P apart from S, S runs
 // three tiles ahead of PV and starts as soon as the scores before are read
-// (64 fp32 rows over 8,208: 52.6 -> 44.2 us for one split); else S(i + 2) is issued
-// behind PV(i), and the order of the MMAs alone makes the buffers free in time. A
-// commit of a product serves both who waits for its result and the ring's next copy.
+// (64 fp32 rows over 8,208: 52.6 -> 44.2 us for one split); else S(i + 2), in the
+// second kernel S(i + NB), is issued behind PV(i), and the order of the MMAs alone
+// makes the buffers free in time. A commit of a product serves both who waits for its result and the ring's next copy.
 //
 // Up to 8 splits of a sequence's cache rows form a thread-block cluster: each
 // CTA leaves its partial O, sums and maxima in its shared memory, and the
@@ -255,7 +255,9 @@ struct Sync {
     // full: the copies have landed; done: the product that reads them is (for K the
     // scores are there, for V the tile is in O)
     uint64_t k_full[KU], k_done[KU], v_full[VU], v_done[VU];
-    uint64_t s_read[2], p_full[2];  // a group has read its scores, has written its weights
+    // A group has read its scores, has written its weights (of a tile i: place i % 4, so
+    // that a warp or the products, a tile of the group behind, are never two phases late)
+    uint64_t s_read[2], p_full[4];
     uint32_t tmem;
     int err, k_issued, v_issued;  // a wait ran out; tiles whose copies went out
     uint32_t bad[2];              // drafted rows taken out of the second product
@@ -274,6 +276,7 @@ __device__ __forceinline__ void init_sync(Sync<KU, VU> *y) {
     for (int g = 0; g < 2; ++g) {
         mbar_init(&y->s_read[g], kSoftWarps / 2);
         mbar_init(&y->p_full[g], kSoftWarps / 2);
+        mbar_init(&y->p_full[g + 2], kSoftWarps / 2);
     }
     y->err = y->k_issued = y->v_issued = 0;
     y->bad[0] = y->bad[1] = 0;
@@ -286,9 +289,9 @@ __device__ __forceinline__ void init_sync(Sync<KU, VU> *y) {
 // before) has to be known to be done. The MMA and copy warps see every tile. A
 // softmax group that awaits S(i) has seen S(i - 2), and with it every product
 // issued before; one that awaits PV(i - 2) has awaited PV(i - 4), or knows it done by
-// S(i - 2), which was issued behind it. Of the last tile's PV that holds for the
-// group of that tile; the other may pass early: what it reads comes behind a
-// barrier with the first.
+// S(i - 2), or with three buffers by S(i), which was issued behind PV(i - 3). Of the
+// last tile's PV that holds for the group of that tile; the other may pass early:
+// what it reads comes behind a barrier with the first.
 template <int KU, int VU>
 __device__ __forceinline__ bool k_full(Sync<KU, VU> *y, int i) {
     return mbar_wait(&y->k_full[i % KU], (i / KU) & 1, &y->err);
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const uint32_t va = ring + (KU + i % VU) * C::kKv;
                 const uint64_t v = sw128_desc(va, kOnes ? ones - va : kHalfTile);
                 const uint64_t p = sw128_desc(p0 + (i & 1) * C::kP, kHalfTile);
-                if (!(ok = ok && v_full(y, i) && mbar_wait(&y->p_full[i & 1], (i >> 1) & 1, err))) break;
+                if (!(ok = ok && v_full(y, i) && mbar_wait(&y->p_full[i & 3], (i >> 2) & 1, err))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
@@ -697,7 +700,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             async_fence();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&y->p_full[g]);
+            if (lane == 0) mbar_arrive(&y->p_full[i & 3]);
         }
         if (nt > 0) ok &= pv_done(y, nt - 1);  // (and with it every product)
         tc_fence_after();
@@ -786,19 +789,18 @@ template <int HD, int TERMS>
 struct RowShape {
     static constexpr int kKv = kHalfTile * (HD / 64);
     static constexpr int kQ = TERMS * kKv;  // 128 rows x HD a term
-    // Tensor memory, for each group: a tile's scores, its weights, and O. Where the
-    // weights have columns of their own (kApart), the scores can be followed by the
-    // next ones as soon as they are read; else the scores' 128 columns become the
-    // weights (64 columns each of the first two terms) beside a third term.
-    static constexpr bool kApart = TERMS == 1 && HD == 64;
-    static constexpr int kThird = kApart || TERMS > 2 ? kTile / 2 : 0;
-    static constexpr int kCols = 512;
+    // Tensor memory: an O for each group, and NB buffers in which a tile's scores (128
+    // columns) become its weights (64 columns each of the first two terms) beside a
+    // third term. With three a group's next scores wait for the other group's last
+    // second product, not for its own (8 ragged sequences: 49.1 -> 44.3 us).
+    static constexpr int kThird = TERMS > 2 ? kTile / 2 : 0, kCols = 512;
+    static constexpr int NB = (kCols - 2 * HD) / (kTile + kThird) > 2 ? 3 : 2;
     static constexpr int kMisc = 512 + 2 * 4 * kRows;
     static constexpr int kRoom = (kSmemMost - 1024 - kQ - kMisc) / kKv;
     static constexpr int KU = (kRoom + 1) / 2 > 6 ? 6 : (kRoom + 1) / 2, VU = kRoom / 2 > 6 ? 6 : kRoom / 2;
     static constexpr int kOffQ = (KU + VU) * kKv, kOffMisc = kOffQ + kQ;
     static constexpr int kSmem = 1024 + kOffMisc + kMisc;
-    static_assert(2 * (kTile + kThird + HD) <= kCols && VU >= 2, "tensor and shared memory of an SM");
+    static_assert(NB * (kTile + kThird) + 2 * HD <= kCols && VU >= NB && KU >= NB, "tensor and shared memory of an SM");
     static_assert(kRows * HD * 4 + (3 * kCluster + 2) * kRows * 4 <= (KU + VU) * kKv, "the partial result fits the ring");
 };
 
@@ -807,7 +809,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tree_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const TreeArgs a) {
     using C = RowShape<HD, TERMS>;
-    constexpr int KU = C::KU, VU = C::VU;
+    constexpr int KU = C::KU, VU = C::VU, NB = C::NB;
     constexpr bool kScaled = TERMS > 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -863,8 +865,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncwarp();
     __syncthreads();
     tc_fence_after();
-    // scores, third terms and O of group g: + g * 128, + g * kThird, + g * HD
-    const uint32_t tS = uniform(y->tmem), tT = tS + 2 * kTile, tO = tT + 2 * C::kThird;
+    // scores and third terms of tile i: + i % NB * 128, + i % NB * kThird; O of group g: + g * HD
+    const uint32_t tS = uniform(y->tmem), tT = tS + NB * kTile, tO = tT + NB * C::kThird;
 
     if (warp == kKWarp) {
         if (elect()) load_all<HD>(y, sm, &kmap, true, KU, nt, t0, plane);
@@ -881,37 +883,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
                     const uint32_t at = (kk / 4) * kHalfTile + (kk % 4) * 32;
-                    umma_bf16(tS + (i & 1) * kTile, q + ((t * C::kKv + at) >> 4), k + (at >> 4), idS, (t | kk) != 0);
+                    umma_bf16(tS + (i % NB) * kTile, q + ((t * C::kKv + at) >> 4), k + (at >> 4), idS, (t | kk) != 0);
                 }
             umma_commit(&y->k_done[i % KU]);
         };
         if (elect()) {
             bool ok = true;
-            for (int i = 0; i < min(nt, C::kApart ? 3 : 2) && ok; ++i) {
-                ok = k_full(y, i) && (i < 2 || mbar_wait(&y->s_read[i & 1], ((i >> 1) - 1) & 1, err));
+            for (int i = 0; i < min(nt, NB) && (ok = k_full(y, i)); ++i) {
                 tc_fence_after();
                 scores(i);
             }
             for (int i = 0; i < nt && ok; ++i) {
-                const int j = i + (C::kApart ? 3 : 2);
-                if (C::kApart && j < nt) {
-                    ok = k_full(y, j) && mbar_wait(&y->s_read[j & 1], ((j >> 1) - 1) & 1, err);
-                    tc_fence_after();
-                    scores(j);
-                }
+                const int j = i + NB;
                 const uint64_t v = sw128_desc(ring + (KU + i % VU) * C::kKv, kHalfTile);
-                if (!(ok = ok && v_full(y, i) && mbar_wait(&y->p_full[i & 1], (i >> 1) & 1, err))) break;
+                if (!(ok = ok && v_full(y, i) && mbar_wait(&y->p_full[i & 3], (i >> 2) & 1, err))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int t = 0; t < TERMS; ++t)
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk) {
-                        const uint32_t p = t < 2 && !C::kApart ? tS + (i & 1) * kTile + t * 64 + kk * 8
-                                                               : tT + (i & 1) * C::kThird + kk * 8;
+                        const uint32_t p = t < 2 ? tS + (i % NB) * kTile + t * 64 + kk * 8
+                                                 : tT + (i % NB) * C::kThird + kk * 8;
                         umma_bf16_ta(tO + (i & 1) * HD, p, v + ((kk * 2048) >> 4), idO, i >= 2 || (t | kk) != 0);
                     }
                 umma_commit(&y->v_done[i % VU]);
-                if (!C::kApart && j < nt) {
+                if (j < nt) {  // (into the buffer of PV(i))
                     ok = k_full(y, j);
                     tc_fence_after();
                     scores(j);
@@ -922,7 +918,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // group g takes every other tile, a thread one query row of it
         const int g = (warp - kFirstSoft) >> 2, quarter = warp & 3;
         const uint32_t mylane = (uint32_t)(quarter * 32) << 16;
-        const uint32_t ts = tS + g * kTile + mylane, tt = tT + g * C::kThird + mylane, to = tO + g * HD + mylane;
+        const uint32_t to = tO + g * HD + mylane;
         const bool live = quarter * 32 < rows;  // (rows behind the last: the warp only keeps the barriers)
         if (sq.n < 64) word &= (1ull << sq.n) - 1;
         float m = kNone, l = 0.f;
@@ -930,6 +926,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int i = g; i < nt; i += 2) {
             ok &= s_done(y, i);
             tc_fence_after();
+            const uint32_t ts = tS + (i % NB) * kTile + mylane, tt = tT + (i % NB) * C::kThird + mylane;
             const int at = (t0 + i) * kTile;
             const bool tail = at + kTile > sq.len;
             if (live) {
@@ -938,11 +935,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 for (int e = 0; e < kTile; e += 16) tmem_ld16(ts + e, x + e);
                 tmem_ld_wait();
                 pin<kTile>(x);
-                if (C::kApart) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&y->s_read[g]);
-                }
                 if (tail) {
 #pragma unroll
                     for (int w = 0; w < kTile; w += 32) {
@@ -959,15 +951,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     for (int w = 0; w < 4; ++w) t4[w] = fmaxf(fmaxf(t4[w], x[e + 2 * w]), x[e + 2 * w + 1]);
                 float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                 if (!kScaled) top *= c;  // (the scale is positive)
-                // PV(i - 2) is done: P and O are this group's again (not apart: S(i) was issued after it)
-                if (C::kApart && i >= 2) ok &= pv_done(y, i - 2);
-                tc_fence_after();
                 if (__any_sync(0xFFFFFFFFu, top > m + kRaise)) {
                     // raise the warp's maxima to those of the rows so far; scale O and the sums
                     const float best = fmaxf(m, top), scale = ex2(m - best);
                     m = best;
                     l *= scale;
                     if (i >= 2) {
+                        if (NB > 2) ok &= pv_done(y, i - 2);  // O is this group's again (NB = 2: S(i) was issued behind it)
+                        tc_fence_after();
 #pragma unroll 1
                         for (int d = 0; d < HD; d += 16) {
                             float o[16];
@@ -1003,14 +994,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 x1 -= bf_hi(w[e]);
                             }
                         }
-                        tmem_st16((t < 2 && !C::kApart ? ts + t * 64 : tt) + w0 / 2, w);
+                        tmem_st16((t < 2 ? ts + t * 64 : tt) + w0 / 2, w);
                     }
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_st_wait();
-            } else if (C::kApart) {
-                if (lane == 0) mbar_arrive(&y->s_read[g]);
-                if (i >= 2) ok &= pv_done(y, i - 2);
             }
             tc_fence_before();
             if (tail) {
@@ -1020,7 +1008,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 async_fence();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&y->p_full[g]);
+            if (lane == 0) mbar_arrive(&y->p_full[i & 3]);
         }
         if (nt > 0) ok &= pv_done(y, nt - 1);  // (and with it every product: the ring is free)
         tc_fence_after();
