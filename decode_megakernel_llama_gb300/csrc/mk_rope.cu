@@ -13,13 +13,13 @@
 // is off by at most p * 2^-53 turns.
 //
 // What bounds it: memory. Each element is read once and written once; the
-// arithmetic is a few operations an element. A CTA takes one token: its first
-// rot/2 threads form the token's sines and cosines once for all heads
-// (shared memory) while every warp's loads of four heads (eight of 64) are
-// already in flight; a head is held by hd/4 lanes of a warp, four elements a
-// lane, so the norm is a shuffle sum and the partner of a pair a shuffle away
-// (or in shared memory, where rot/2 is no multiple of four). A few tokens are
-// spread over several CTAs each, so that no warp takes more than one round.
+// arithmetic is a few operations an element. A CTA takes one token (or four): its
+// threads form the token's sines and cosines once for all heads (shared memory)
+// while every warp's first loads are already in flight; a head is held by hd/4
+// lanes of a warp, four elements a lane, or by hd/8, four elements of each half, so
+// the norm is a shuffle sum and the partner of a pair is in the lane itself (the
+// whole head rotated), a shuffle away, or in shared memory (rot/2 no multiple of
+// four, or pairs that lie neither way). A few tokens are spread over several CTAs each.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -35,6 +35,7 @@ namespace {
 constexpr int kT = 256;  // threads per CTA
 constexpr int kW = kT / 32;
 constexpr int kMaxHalf = 64;  // rotated pairs of a head
+constexpr int kSpread = 456;  // CTAs that the GPU holds at once of the form for fewer tokens: three an SM
 
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p);
@@ -61,20 +62,20 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t *p, float4 v) {
     *reinterpret_cast<uint2 *>(p) = pack4(v);
 }
 
-// The value of element e of this lane's head, from the head's staged row.
-__device__ __forceinline__ float part(const float4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
-// TPB tokens a CTA (1 or 4), kW / TPB warps each. (64 registers: with four CTAs an
-// SM instead of three a prompt of 8,192 tokens takes 9 % less; the reciprocal root as
-// one instruction instead of a root and a division, 5 % less.)
-template <typename T, int HD, int TPB>
-__global__ void __launch_bounds__(kT, 4) rope_append(const RopeArgs a) {
-    constexpr int LPH = HD / 4;    // lanes of a head
+// TPB tokens a CTA (1 or 4), kW / TPB warps each; a lane holds E elements of a head:
+// four, or four of each half. (64 registers: with four CTAs an SM instead of three a prompt of 8,192 tokens
+// takes 9 % less. Beside memory the instructions bound a long prompt, 140 for 32 x 4
+// elements when they took 53 % of the issue slots: so eight elements a lane, which
+// share a norm's shuffles, a head's tests and its addresses, and the reciprocal root
+// as one instruction.)
+template <typename T, int HD, int TPB, int E>
+__global__ void __launch_bounds__(kT, TPB == 1 && E == 8 ? 3 : 4) rope_append(const RopeArgs a) {
+    constexpr int LPH = HD / E;    // lanes of a head
     constexpr int HPW = 32 / LPH;  // heads of a warp
-    constexpr int B = 4;           // a warp's heads in flight, HPW each
+    constexpr int B = 16 / E;      // a warp's heads in flight, HPW each
     constexpr int WPT = kW / TPB;  // warps of a token
     __shared__ float2 turn[TPB][kMaxHalf];
-    __shared__ float4 stage[kT];  // a head's row, for pairs that are not in one lane
+    __shared__ float4 stage[kT * E / 4];  // a head's row, for pairs that are not a lane apart
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int sub = lane / LPH, j = lane % LPH;  // head of the warp, lane of the head
     const int t = blockIdx.x * TPB + warp / WPT, half = a.rot / 2, n_rows = a.Hq + 2 * a.Hkv;
@@ -85,18 +86,24 @@ __global__ void __launch_bounds__(kT, 4) rope_append(const RopeArgs a) {
     T *qo = static_cast<T *>(a.q_out) + (int64_t)t * a.q_stride + 4 * j;
     const int row = here ? a.rows[t] : -1, slot = here && a.slot_of ? a.slot_of[t] : 0;
     const int first = (blockIdx.y * WPT + warp % WPT) * HPW + sub, step = gridDim.y * WPT * HPW;
-    float4 x[B];
+    float4 x[B][E / 4];
     auto load = [&](int h0) {
 #pragma unroll
-        for (int u = 0; u < B; ++u) {
-            const int h = h0 + u * step;
-            x[u] = here && h < n_rows ? load4<T>(in + (int64_t)h * HD) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+        for (int u = 0; u < B; ++u)
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e) {
+                const int h = h0 + u * step;
+                x[u][e] = here && h < n_rows ? load4<T>(in + (int64_t)h * HD + 4 * e * LPH) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
     };
     load(first);
-    const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
-    const float4 gq = a.q_norm ? load4<uint16_t>(a.q_norm + 4 * j) : one;
-    const float4 gk = a.k_norm ? load4<uint16_t>(a.k_norm + 4 * j) : one;
+    uint2 gq[E / 4], gk[E / 4];  // the gains, bf16
+#pragma unroll
+    for (int e = 0; e < E / 4; ++e) {
+        const uint2 one = make_uint2(0x3F803F80u, 0x3F803F80u);
+        gq[e] = a.q_norm ? *reinterpret_cast<const uint2 *>(a.q_norm + 4 * (e * LPH + j)) : one;
+        gk[e] = a.k_norm ? *reinterpret_cast<const uint2 *>(a.k_norm + 4 * (e * LPH + j)) : one;
+    }
     for (int i = tid; i < TPB * kMaxHalf; i += kT) {
         const int tt = blockIdx.x * TPB + i / kMaxHalf, e = i % kMaxHalf;
         if (e < half && tt < a.n) {
@@ -115,7 +122,14 @@ __global__ void __launch_bounds__(kT, 4) rope_append(const RopeArgs a) {
         float ss[B];  // the batch's sums of squares side by side
         if (a.q_norm || a.k_norm) {
 #pragma unroll
-            for (int u = 0; u < B; ++u) ss[u] = x[u].x * x[u].x + x[u].y * x[u].y + x[u].z * x[u].z + x[u].w * x[u].w;
+            for (int u = 0; u < B; ++u) {
+                ss[u] = 0.f;
+#pragma unroll
+                for (int e = 0; e < E / 4; ++e) {
+                    const float4 v = x[u][e];
+                    ss[u] += v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
+                }
+            }
 #pragma unroll
             for (int o = LPH / 2; o > 0; o >>= 1)
 #pragma unroll
@@ -125,32 +139,69 @@ __global__ void __launch_bounds__(kT, 4) rope_append(const RopeArgs a) {
         for (int u = 0; u < B; ++u) {
             const int h = h0 + u * step;
             if (h - sub >= n_rows) break;
-            float4 v = x[u];
             const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
             if (is_q ? a.q_norm != nullptr : is_k && a.k_norm != nullptr) {
                 const float r = rsqrtf(ss[u] * (1.0f / HD) + a.eps);
-                const float4 g = is_q ? gq : gk;
-                v = make_float4(v.x * r * g.x, v.y * r * g.y, v.z * r * g.z, v.w * r * g.w);
-            }
-            float4 y = v;
-            if (a.interleaved) {
-                if (is_q || is_k) {
-                    if (2 * j < half) {
-                        const float2 c = cs[2 * j];
-                        y.x = v.x * c.x - v.y * c.y;
-                        y.y = v.y * c.x + v.x * c.y;
-                    }
-                    if (2 * j + 1 < half) {
-                        const float2 c = cs[2 * j + 1];
-                        y.z = v.z * c.x - v.w * c.y;
-                        y.w = v.w * c.x + v.z * c.y;
-                    }
+#pragma unroll
+                for (int e = 0; e < E / 4; ++e) {
+                    const uint2 g = is_q ? gq[e] : gk[e];
+                    float4 &v = x[u][e];
+                    v = make_float4(v.x * r * bf_lo(g.x), v.y * r * bf_hi(g.x), v.z * r * bf_lo(g.y), v.w * r * bf_hi(g.y));
                 }
-            } else if (half % 4 == 0) {
-                // an element's partner is the same element of the lane half / 4 away
+            }
+            T *to = qo + (int64_t)h * HD;
+            uint16_t *cache = nullptr;
+            if (!is_q && keep && h < n_rows) {
+                const int kvh = is_k ? h - a.Hq : h - a.Hq - a.Hkv;
+                cache = (is_k ? a.kc : a.vc) + (((int64_t)slot * a.Hkv + kvh) * a.max_seq + row) * HD + 4 * j;
+            }
+            auto store = [&](int e, float4 y) {
+                if (is_q && h < n_rows)
+                    store4<T>(to + 4 * e * LPH, y);
+                else if (cache)
+                    store4<uint16_t>(cache + 4 * e * LPH, y);
+            };
+            if (a.interleaved) {
+#pragma unroll
+                for (int e = 0; e < E / 4; ++e) {
+                    const float4 v = x[u][e];
+                    const int pair = 2 * (e * LPH + j);
+                    float4 y = v;
+                    if (is_q || is_k) {
+                        if (pair < half) {
+                            const float2 c = cs[pair];
+                            y.x = v.x * c.x - v.y * c.y;
+                            y.y = v.y * c.x + v.x * c.y;
+                        }
+                        if (pair + 1 < half) {
+                            const float2 c = cs[pair + 1];
+                            y.z = v.z * c.x - v.w * c.y;
+                            y.w = v.w * c.x + v.z * c.y;
+                        }
+                    }
+                    store(e, y);
+                }
+            } else if (E == 8 && half == HD / 2) {
+                // an element's partner is in the lane's other four
+                float4 v = x[u][0], w = x[u][E / 4 - 1];
+                if (is_q || is_k) {
+                    const float2 *c = cs + 4 * j;
+                    const float2 c0 = c[0], c1 = c[1], c2 = c[2], c3 = c[3];
+                    const float4 o = v;
+                    v = make_float4(v.x * c0.x - w.x * c0.y, v.y * c1.x - w.y * c1.y, v.z * c2.x - w.z * c2.y,
+                                    v.w * c3.x - w.w * c3.y);
+                    w = make_float4(w.x * c0.x + o.x * c0.y, w.y * c1.x + o.y * c1.y, w.z * c2.x + o.z * c2.y,
+                                    w.w * c3.x + o.w * c3.y);
+                }
+                store(0, v);
+                store(E / 4 - 1, w);
+            } else if (half % 4 == 0 && half / 2 <= LPH) {
+                // it is the same element of the lane half / 4 away, of the lane's first four
                 const int d = half / 4, from = j < d ? lane + d : lane - d;
+                const float4 v = x[u][0];
                 const float4 o = make_float4(__shfl_sync(0xFFFFFFFFu, v.x, from), __shfl_sync(0xFFFFFFFFu, v.y, from),
                                              __shfl_sync(0xFFFFFFFFu, v.z, from), __shfl_sync(0xFFFFFFFFu, v.w, from));
+                float4 y = v;
                 if ((is_q || is_k) && j < 2 * d) {
                     const float2 *c = cs + 4 * (j < d ? j : j - d);
                     const float sg = j < d ? -1.f : 1.f;
@@ -159,37 +210,32 @@ __global__ void __launch_bounds__(kT, 4) rope_append(const RopeArgs a) {
                     y.z = v.z * c[2].x + sg * (o.z * c[2].y);
                     y.w = v.w * c[3].x + sg * (o.w * c[3].y);
                 }
+                store(0, y);
+                if (E == 8) store(E / 4 - 1, x[u][E / 4 - 1]);
             } else {
                 __syncwarp();
-                stage[tid] = v;
+#pragma unroll
+                for (int e = 0; e < E / 4; ++e) stage[(tid - j) * (E / 4) + e * LPH + j] = x[u][e];
                 __syncwarp();
-                if (is_q || is_k) {
-                    const float *mine = reinterpret_cast<const float *>(stage + tid - j);
+                const float *mine = reinterpret_cast<const float *>(stage + (tid - j) * (E / 4));
+#pragma unroll
+                for (int q = 0; q < E / 4; ++q) {
+                    const float z[4] = {x[u][q].x, x[u][q].y, x[u][q].z, x[u][q].w};
                     float o[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int e = 4 * j + i;
-                        const float z = part(v, i);
-                        if (e < half) {
+                        const int e = 4 * (q * LPH + j) + i;
+                        o[i] = z[i];
+                        if ((is_q || is_k) && e < half) {
                             const float2 c = cs[e];
-                            o[i] = z * c.x - mine[e + half] * c.y;
-                        } else if (e < a.rot) {
+                            o[i] = z[i] * c.x - mine[e + half] * c.y;
+                        } else if ((is_q || is_k) && e < a.rot) {
                             const float2 c = cs[e - half];
-                            o[i] = z * c.x + mine[e - half] * c.y;
-                        } else {
-                            o[i] = z;
+                            o[i] = z[i] * c.x + mine[e - half] * c.y;
                         }
                     }
-                    y = make_float4(o[0], o[1], o[2], o[3]);
+                    store(q, make_float4(o[0], o[1], o[2], o[3]));
                 }
-            }
-            if (h >= n_rows) continue;
-            if (is_q) {
-                store4<T>(qo + (int64_t)h * HD, y);
-            } else if (keep) {
-                const int kvh = is_k ? h - a.Hq : h - a.Hq - a.Hkv;
-                uint16_t *c = is_k ? a.kc : a.vc;
-                store4<uint16_t>(c + (((int64_t)slot * a.Hkv + kvh) * a.max_seq + row) * HD + 4 * j, y);
             }
         }
     }
@@ -199,19 +245,24 @@ __global__ void __launch_bounds__(kT, 4) rope_append(const RopeArgs a) {
 
 cudaError_t rope_append_launch(const RopeArgs &a, int hd, bool f32, cudaStream_t s) {
     // Many tokens: four a CTA, two warps each, so that their angles are formed side
-    // by side and a warp has several rounds of loads (8,192 tokens of 48 heads of 64
-    // in fp32, normed: 38.8 us = 4.75 TB/s, a sixth less than one token a CTA). A few: one
-    // round a warp, a token over several CTAs (one token: 1.7 us, 3.7 in one CTA).
+    // by side and a warp has several rounds of loads (8,192 tokens of 48 heads of 64 in
+    // fp32, normed: 32.7 us = 5.6 TB/s, 38.8 with four elements a lane). Fewer: a token
+    // over as many CTAs as the GPU holds, up to one for each round (216 tokens: 2.9 us, 3.3
+    // with one CTA each, 4.2 with four elements a lane; 800 tokens of 40 heads of 128:
+    // 6.5 us, 7.8 as many, and 1,000, more than two waves, 8.6 and 7.8). A few, where
+    // latency counts: four elements a lane (one token: 1.75 us, 1.9 with eight).
     const int per_cta = kW * (hd == 64 ? 2 : 1), rounds = (a.Hq + 2 * a.Hkv + per_cta - 1) / per_cta;
-    const bool many = a.n >= 1024;
-    const dim3 grid(many ? (a.n + 3) / 4 : a.n, a.n <= 64 ? std::min(rounds, 8) : 1);
+    const bool many = a.n > 2 * kSpread, few = a.n <= 32;
+    const int spread = std::max(1, std::min({rounds, 8, kSpread / a.n}));
+    const dim3 grid(many ? (a.n + 3) / 4 : a.n, many ? 1 : spread);
     auto go = [&](auto kernel) { return launch_op(kernel, grid, kT, 0, 0, s, a); };
-    if (f32) {
-        if (hd == 64) return many ? go(rope_append<float, 64, 4>) : go(rope_append<float, 64, 1>);
-        return many ? go(rope_append<float, 128, 4>) : go(rope_append<float, 128, 1>);
-    }
-    if (hd == 64) return many ? go(rope_append<uint16_t, 64, 4>) : go(rope_append<uint16_t, 64, 1>);
-    return many ? go(rope_append<uint16_t, 128, 4>) : go(rope_append<uint16_t, 128, 1>);
+    auto pick = [&](auto four, auto one, auto one4) { return many ? go(four) : few ? go(one4) : go(one); };
+    if (f32)
+        return hd == 64 ? pick(rope_append<float, 64, 4, 8>, rope_append<float, 64, 1, 8>, rope_append<float, 64, 1, 4>)
+                        : pick(rope_append<float, 128, 4, 8>, rope_append<float, 128, 1, 8>, rope_append<float, 128, 1, 4>);
+    return hd == 64
+               ? pick(rope_append<uint16_t, 64, 4, 8>, rope_append<uint16_t, 64, 1, 8>, rope_append<uint16_t, 64, 1, 4>)
+               : pick(rope_append<uint16_t, 128, 4, 8>, rope_append<uint16_t, 128, 1, 8>, rope_append<uint16_t, 128, 1, 4>);
 }
 
 }  // namespace mkops

@@ -87,6 +87,11 @@ def test_rope_append_large_prompt(dev):
     (1500, 8, 2, 128, 128, torch.float32, dict(norm=True, in_place=True)),
     (1700, 3, 2, 64, 48, BF, dict(norm=True, pad=4)),              # rows that start at 8 bytes of 16
     (1030, 40, 8, 128, 64, torch.float32, dict(norm=True)),        # rows of 28 KB
+    (32, 24, 8, 128, 128, BF, dict(norm=True)), (33, 7, 1, 64, 64, torch.float32, dict(norm=True)),
+    (216, 24, 8, 128, 96, BF, dict(norm=True)), (300, 4, 2, 64, 32, torch.float32, dict()),
+    (457, 5, 3, 128, 24, BF, dict(inter=True, norm=True)), (912, 3, 1, 64, 40, BF, dict(norm=True, in_place=True)),
+    (913, 3, 1, 128, 112, torch.float32, dict(norm=True)), (940, 12, 4, 128, 128, BF, dict(inter=True)),
+    (1000, 6, 2, 128, 64, BF, dict(norm=True, pad=4)), (1200, 6, 2, 64, 56, torch.float32, dict(norm=True)),
 ])
 def test_rope_append_long_prompts(dev, n, Hq, Hkv, hd, rot, dtype, kw):
     rope_case(dev, n, Hq, Hkv, hd, rot, dtype, **{"norm": False, "inter": False, **kw}, slots=2, S=n, base=100000)
