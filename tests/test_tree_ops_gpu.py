@@ -498,6 +498,18 @@ def test_tree_attention_large_trees_in_streams_and_graphs(dev, hd, dtype):
         c.check()
 
 
+@pytest.mark.parametrize("T,lengths", [(16, [16000, 16000]), (40, [9000, 15000]), (33, [16000] * 4)])
+def test_tree_attention_partly_filled_row_tiles_over_long_caches(dev, T, lengths):
+    """Row tiles with warps that have no row, and caches from memory: warps and products drift apart; no wait runs out."""
+    c = Case(dev, lengths, T, 32, 8, 64, BF, S=FAR)
+    status = torch.zeros(1, dtype=I32, device=dev)
+    for _ in range(5):
+        c.out.fill_(99.0)
+        c.run(max_len=max(lengths), status=status)
+    c.check()
+    assert int(status) == 0
+
+
 def test_tree_attention_far_scores_and_status(dev):
     """Scores below -1e30 are scores all the same; the status word stays 0."""
     c = Case(dev, [70], 3, 2, 1, 64, torch.float32)
