@@ -102,13 +102,13 @@ struct Plan {
 template <int HD_, int TERMS_, int NR_>
 struct Few {
     static constexpr int HD = HD_, TERMS = TERMS_, NR = NR_, kSmem = AttnShape<HD, TERMS, NR>::kSmem;
-    static constexpr double kTileUs = HD == 64 ? 0.6 : TERMS == 1 ? 0.75 : 1.0, kFixedUs = 5.0, kJoinUs = 4.5;
+    static constexpr double kTileUs = (HD == 64 ? 0.6 : 1.0) - (TERMS == 1 ? HD / 64 * 0.1 : 0.0), kFixedUs = 5.0, kJoinUs = 4.5;
     static auto fn() { return tree_attention<HD, TERMS, NR>; }
 };
 template <int HD_, int TERMS_>
 struct Many {
     static constexpr int HD = HD_, TERMS = TERMS_, NR = kRows, kSmem = RowShape<HD, TERMS>::kSmem;
-    static constexpr double kTileUs = TERMS == 3 ? 1.2 : HD == 64 ? 0.6 : 1.0, kFixedUs = 6.5, kJoinUs = 7.0;
+    static constexpr double kTileUs = HD == 64 && TERMS == 1 ? 0.8 : 1.2, kFixedUs = 6.5, kJoinUs = 7.0;
     static auto fn() { return tree_attention_rows<HD, TERMS>; }
 };
 
@@ -157,9 +157,10 @@ int active_clusters(int k, int n_sm) {
 
 // The split with the least estimated time, in microseconds: waves of resident
 // CTAs x (the tiles of a split x K::kTileUs + a fixed part). The tile times are
-// those of one split over a long cache (S = 1: 44.2 us for 65 tiles of 32 fp32 rows
-// with heads of 64, 44.3 for 128 bf16 rows, 22.5 for 17 tiles of 32 fp32 rows with
-// heads of 128, each with K::kFixedUs of launch, set-up and end); more than a
+// those of one split over a cache (S = 1: 65 tiles of 32 fp32 rows with heads of 64
+// 43.1 us, of 32 bf16 rows 36.1, of 128 bf16 rows 58.2; 17 tiles with heads of 128 of
+// 32 fp32 rows 21.4 us, of 32 bf16 rows 20.7, of 128 bf16 rows 26.6; each
+// with K::kFixedUs of launch, set-up and end); more than a
 // cluster's splits cost K::kJoinUs: a second launch and the partial results'
 // way through memory.
 template <class K>
@@ -209,8 +210,9 @@ cudaError_t launch(TreeArgs a, int max_len, int n_sm, cudaStream_t s, int64_t *w
 
 // The kernel of 16 or 32 columns that holds the tree's rows of a kv head; for more
 // rows, several CTAs of 32 or the kernel of 128 rows, whichever plan is shorter.
-// (Measured, 64 fp32 rows over 8,208 cache rows: 14.4 us with 32 columns, 18.7 with
-// 128 rows; 244 bf16 rows and 64 (sequence, kv head) pairs: 99 and 44 us.)
+// (Measured, 64 bf16 rows over 8,208 cache rows: 13.0 us with 32 columns, 16.1 with
+// 128 rows; 244 bf16 rows and 64 (sequence, kv head) pairs: 58.2 us with 128 rows, four
+// waves of 36 with 32 columns.)
 template <int HD, int TERMS>
 cudaError_t dispatch(const TreeArgs &a, int max_len, int n_sm, cudaStream_t s, int64_t *want) {
     const int rows = a.T * (a.Hq / a.Hkv);

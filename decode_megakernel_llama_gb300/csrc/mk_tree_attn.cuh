@@ -23,16 +23,19 @@
 // of 128: 86.0 us = 6.24 TB/s, 0.93 of the measured copy rate); for a short one
 // latency (one token over 191 rows: 5.8 us, of which the launch, the first copies
 // and the join of two splits are all but 2). The second the softmax warps' time
-// a tile, ~1,130 cycles against 616 of its MMAs and 530 of its exponentials at 31 a
-// cycle (8 ragged sequences of up to 8,253 rows, 244 query rows, 64 dims: 44.3 us, of
-// which the longest sequence's 65 tiles are 39): a warp's loads, maximum, weights
-// and stores come one behind the other, and only two warps share a scheduler.
+// a tile, ~1,550 cycles against 960 of its MMAs and 530 of its exponentials at 31 a
+// cycle (8 ragged sequences of up to 8,253 rows, 244 query rows, 64 dims: 58.2 us, of
+// which the longest sequence's 65 tiles are 52): a warp's loads, maximum, weights
+// and stores come one behind the other, and only two warps share a scheduler. The
+// weights' second term costs a third of it (44.3 us with one).
 //
 // fp32 queries and weights enter as three bf16 terms each (24 bits: x = t0 + t1 +
 // t2 to half a step of fp32): side by side in the first kernel's B operand, N =
-// TERMS * NR, added in registers (S) and once at the end (O); as more instructions
-// into the same accumulator in the second. bf16 queries are one term, their
-// weights are rounded to one bf16 (the result's own type).
+// terms * NR, added in registers (S) and once at the end (O); as more instructions
+// into the same accumulator in the second. bf16 queries are one term, exactly, and
+// their weights two (16 bits, 2^-8 of half a step of the bf16 result). With one the
+// weights' own rounding was as large as the result's: 0.0023 of the result's norm off
+// against 0.0017, which is the rounding of the result alone.
 //
 // Softmax, in one pass with a reference maximum m that is raised only when a
 // score exceeds it by 2^8 (the first tile, and hardly ever after): exp2(s - m)
@@ -90,6 +93,9 @@ __device__ __forceinline__ Seq sequence(const TreeArgs &a, int b) {
     return s;
 }
 
+// bf16 terms of a softmax weight, of queries of `terms`.
+__host__ __device__ constexpr int weight_terms(int terms) { return terms == 1 ? 2 : terms; }
+
 constexpr int kTile = 128;      // cache rows of a tile
 constexpr int kCluster = 8;     // most splits joined in a cluster
 constexpr int kGroup = 128;     // softmax threads of a group: one for each lane of tensor memory
@@ -138,6 +144,12 @@ __device__ __forceinline__ void fma2(float &x, float &y, float c, float mx, floa
     x = r.x, y = r.y;
 }
 
+// (x, y) less the bf16 pair w: exact, one instruction for both.
+__device__ __forceinline__ void less2(float &x, float &y, uint32_t w) {
+    const float2 r = __ffma2_rn(make_float2(bf_lo(w), bf_hi(w)), make_float2(-1.f, -1.f), make_float2(x, y));
+    x = r.x, y = r.y;
+}
+
 // Values of a tensor-memory load, used only behind its wait.
 template <int K>
 __device__ __forceinline__ void pin(float *v) {
@@ -154,10 +166,7 @@ __device__ __forceinline__ void split8(float (&x)[8], uint4 (&t)[TERMS]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-            if (k + 1 < TERMS) {
-                x[2 * i] -= bf_lo(w[i]);
-                x[2 * i + 1] -= bf_hi(w[i]);
-            }
+            if (k + 1 < TERMS) less2(x[2 * i], x[2 * i + 1], w[i]);
         }
         t[k] = make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -432,11 +441,11 @@ __device__ __forceinline__ void load_query8(const TreeArgs &a, int b, int kvh, i
 
 template <int HD, int TERMS, int NR>
 struct AttnShape {
-    static constexpr int N = TERMS * NR;
+    static constexpr int N = TERMS * NR, PN = weight_terms(TERMS) * NR;  // columns of S and of O
     static constexpr int kKv = kHalfTile * (HD / 64);    // bytes of a K (or V) tile
-    static constexpr int kP = ((N + 63) / 64) * kHalfTile;  // of a tile's weights; two of them
+    static constexpr int kP = ((PN + 63) / 64) * kHalfTile;  // of a tile's weights; two of them
     static constexpr int kQ = N * HD * 2;
-    static constexpr int kCols = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;
+    static constexpr int kUsed = 2 * (N + PN), kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     static constexpr int kOnes = HD == 64 ? 2048 : 0;  // 16 cache rows x 64: ones in the first column
     static constexpr int kMisc = 512 + 8 * MK_MAX_TREE + 4 * NR * (2 + 2 + 1 + 8);
     static constexpr int kRoom = (kSmemMost - 1024 - 2 * kP - kQ - kOnes - kMisc) / kKv;
@@ -447,7 +456,8 @@ struct AttnShape {
     static constexpr int kAhead = kEarly ? 3 : 2;
     static constexpr int kOffP = (KU + VU) * kKv, kOffQ = kOffP + 2 * kP, kOffOnes = kOffQ + kQ, kOffMisc = kOffOnes + kOnes;
     static constexpr int kSmem = 1024 + kOffMisc + kMisc;
-    static_assert(N % 16 == 0 && N <= 256 && 4 * N <= 512 && VU >= 2, "the instruction's N, tensor and shared memory");
+    static_assert(N % 16 == 0 && PN % 16 == 0 && PN <= 256 && kUsed <= 512 && VU >= 2,
+                  "the instruction's N, tensor and shared memory");
     static_assert(NR * HD * 4 + 3 * kCluster * NR * 4 <= (KU + VU) * kKv, "the partial result fits the ring");
 };
 
@@ -455,7 +465,7 @@ template <int HD, int TERMS, int NR>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     tree_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const TreeArgs a) {
     using C = AttnShape<HD, TERMS, NR>;
-    constexpr int N = C::N, KU = C::KU, VU = C::VU;
+    constexpr int N = C::N, PT = weight_terms(TERMS), PN = C::PN, KU = C::KU, VU = C::VU;
     constexpr bool kScaled = TERMS > 1;             // the queries carry the scale already
     constexpr bool kOnes = HD == 64;                // the sums come out of the second product
     extern __shared__ uint8_t smem_raw[];
@@ -530,14 +540,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncwarp();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tS = uniform(y->tmem), tO = tS + 2 * N;  // S and O of group g: + g * N
+    const uint32_t tS = uniform(y->tmem), tO = tS + 2 * N;  // S and O of group g: + g * N, + g * PN
 
     if (warp == kKWarp) {
         if (elect()) load_all<HD>(y, sm, &kmap, true, KU, nt, t0, plane);
     } else if (warp == kVWarp) {
         if (elect()) load_all<HD>(y, sm, &vmap, false, VU, nt, t0, plane);
     } else if (warp == kMmaWarp) {
-        constexpr uint32_t idS = idesc_bf16(N, false, false), idO = idesc_bf16(N, true, true);
+        constexpr uint32_t idS = idesc_bf16(N, false, false), idO = idesc_bf16(PN, true, true);
         const uint64_t q = sw128_desc(saddr(Qs), 16);
         const uint32_t ring = saddr(sm), ones = saddr(sm + C::kOffOnes), p0 = saddr(Ps);
         auto scores = [&](int i) {
@@ -572,7 +582,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
-                    umma_bf16(tO + (i & 1) * N, v + ((kk * 2048) >> 4) - (kOnes ? (uint64_t)((kk * 2048) >> 4) << 16 : 0),
+                    umma_bf16(tO + (i & 1) * PN, v + ((kk * 2048) >> 4) - (kOnes ? (uint64_t)((kk * 2048) >> 4) << 16 : 0),
                               p + ((kk * 2048) >> 4), idO, i >= 2 || kk != 0);
                 umma_commit(&y->v_done[i % VU]);
                 if (!C::kEarly && j < nt) {
@@ -586,7 +596,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // group g takes every other tile; thread: cache row `row` of it, all query rows
         const int g = (warp - kFirstSoft) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t mylane = (uint32_t)(quarter * 32) << 16;
-        const uint32_t ts = tS + g * N + mylane, to = tO + g * N + mylane;
+        const uint32_t ts = tS + g * N + mylane, to = tO + g * PN + mylane;
         float *gref = mref + g * NR, *gcorr = corr + g * NR, *gtmp = wtmp + g * 4 * NR;
         const float4 *m4 = reinterpret_cast<const float4 *>(gref);
         float l[kOnes ? 1 : NR];
@@ -663,7 +673,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (i >= 2) {
                     tc_fence_after();
 #pragma unroll 1
-                    for (int n0 = 0; n0 < N; n0 += 16) {
+                    for (int n0 = 0; n0 < PN; n0 += 16) {
                         float o[16];
                         tmem_ld16(to + n0, o);
                         tmem_ld_wait();
@@ -684,15 +694,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
             for (int r0 = 0; r0 < NR; r0 += 8) {
                 float w[8];
-                uint4 t[TERMS];
+                uint4 t[PT];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     w[e] = ex2(x[r0 + e]);
                     if constexpr (!kOnes) l[r0 + e] += w[e];
                 }
-                split8<TERMS>(w, t);
+                split8<PT>(w, t);
 #pragma unroll
-                for (int k = 0; k < TERMS; ++k) {
+                for (int k = 0; k < PT; ++k) {
                     const int ch = (k * NR + r0) / 8;
                     *reinterpret_cast<uint4 *>(p + (ch / 8) * kHalfTile + (((ch % 8) ^ (row & 7)) << 4)) = t[k];
                 }
@@ -738,16 +748,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 for (int e = 0; e < 16; ++e) o[e] = 0.f;
 #pragma unroll 1
                 for (int h = 0; h < min(nt, 2); ++h) {
-                    float w[16 * TERMS];
+                    float w[16 * PT];
 #pragma unroll
-                    for (int k = 0; k < TERMS; ++k) tmem_ld16(tO + h * N + mylane + k * NR + r0, w + 16 * k);
+                    for (int k = 0; k < PT; ++k) tmem_ld16(tO + h * PN + mylane + k * NR + r0, w + 16 * k);
                     tmem_ld_wait();
-                    pin<16 * TERMS>(w);
+                    pin<16 * PT>(w);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        float z = w[16 * (TERMS - 1) + e];
+                        float z = w[16 * (PT - 1) + e];
 #pragma unroll
-                        for (int k = TERMS - 2; k >= 0; --k) z += w[16 * k + e];
+                        for (int k = PT - 2; k >= 0; --k) z += w[16 * k + e];
                         o[e] = fmaf(corr[h * NR + r0 + e], z, o[e]);
                     }
                 }
@@ -791,8 +801,9 @@ struct RowShape {
     static constexpr int kQ = TERMS * kKv;  // 128 rows x HD a term
     // Tensor memory: an O for each group, and NB buffers in which a tile's scores (128
     // columns) become its weights (64 columns each of the first two terms) beside a
-    // third term. With three a group's next scores wait for the other group's last
-    // second product, not for its own (8 ragged sequences: 49.1 -> 44.3 us).
+    // third term of fp32. With three a group's next scores wait for the other group's last
+    // second product, not for its own (8 ragged sequences, weights of one term: 49.1 ->
+    // 44.3 us).
     static constexpr int kThird = TERMS > 2 ? kTile / 2 : 0, kCols = 512;
     static constexpr int NB = (kCols - 2 * HD) / (kTile + kThird) > 2 ? 3 : 2;
     static constexpr int kMisc = 512 + 2 * 4 * kRows;
@@ -809,7 +820,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tree_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const TreeArgs a) {
     using C = RowShape<HD, TERMS>;
-    constexpr int KU = C::KU, VU = C::VU, NB = C::NB;
+    constexpr int KU = C::KU, VU = C::VU, NB = C::NB, PT = weight_terms(TERMS);
     constexpr bool kScaled = TERMS > 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -899,7 +910,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!(ok = ok && v_full(y, i) && mbar_wait(&y->p_full[i & 3], (i >> 2) & 1, err))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int t = 0; t < TERMS; ++t)
+                for (int t = 0; t < PT; ++t)
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk) {
                         const uint32_t p = t < 2 ? tS + (i % NB) * kTile + t * 64 + kk * 8
@@ -983,16 +994,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         sum[(e >> 1) & 1] = __ffma2_rn(make_float2(x0, x1), make_float2(1.f, 1.f), sum[(e >> 1) & 1]);
                     }
 #pragma unroll
-                    for (int t = 0; t < TERMS; ++t) {
+                    for (int t = 0; t < PT; ++t) {
                         uint32_t w[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float &x0 = x[w0 + 2 * e], &x1 = x[w0 + 2 * e + 1];
                             w[e] = pack_bf16(x0, x1);
-                            if (t + 1 < TERMS) {
-                                x0 -= bf_lo(w[e]);
-                                x1 -= bf_hi(w[e]);
-                            }
+                            if (t + 1 < PT) less2(x0, x1, w[e]);
                         }
                         tmem_st16((t < 2 ? ts + t * 64 : tt) + w0 / 2, w);
                     }

@@ -510,7 +510,7 @@ int mk_rope_frequencies(int32_t kind, int32_t rot, double theta, double factor, 
  * [n_kv_heads][max_seq][head_dim], one layer; head_dim 64 or 128. Sums and
  * statistics are fp32; fp32 queries and the probabilities with them enter the
  * products as three bf16 terms each (24 bits of the value); bf16 queries enter
- * as they are, their probabilities rounded to bf16. max_len: a bound on
+ * as they are, their probabilities as two (16 bits). max_len: a bound on
  * lengths[b] known to the host (0: max_seq), used only to choose the launch;
  * results are right if a length exceeds it.
  * lengths outside [0, max_seq] and counts past the nodes or the cache's end
