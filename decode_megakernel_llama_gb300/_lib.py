@@ -74,13 +74,13 @@ class mk_tree_args(ctypes.Structure):
                                                  "out_token_stride")]
                 + [(n, ctypes.c_void_p) for n in ("q", "out", "k_cache", "v_cache", "lengths", "counts", "slot_of",
                                                   "masks", "workspace")]
-                + [("workspace_bytes", ctypes.c_int64), ("status", ctypes.c_void_p)])
+                + [("workspace_bytes", ctypes.c_int64), ("status", ctypes.c_void_p), ("wait_ns", ctypes.c_int64)])
 
 
 # The same two as one packed record each (native layout): filling a ctypes
 # structure field by field costs more than the launch it is for.
 _ROPE_ARGS = struct.Struct("@9i2f2q10P")
-_TREE_ARGS = struct.Struct("@9if4q9PqP")
+_TREE_ARGS = struct.Struct("@9if4q9PqPq")
 
 
 _lib = None
@@ -420,15 +420,16 @@ def rope_append(qkv, q_out, k_cache, v_cache, positions, rows, inv_freq, slots=N
 
 
 def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None = None, counts=None, slots=None,
-                   max_len: int = 0, status=None, stream=None) -> None:
+                   max_len: int = 0, status=None, stream=None, wait_ns: int = 0) -> None:
     """mk_tree_attention on CUDA tensors: q and out [B][T][Hq][hd] float32 or bfloat16 (batch and node strides
     free), k_cache / v_cache bfloat16 [slots][Hkv][max_seq][hd] (one layer), lengths / counts / slots int32 [B],
     masks int64 [B][T] (the 64 bits of the ancestor mask). scale defaults to 1 / sqrt(hd). status: int32 [1]
-    (zeroed by the caller) that becomes 1 if a bounded in-kernel wait ran out. The workspace of long caches comes
-    from torch's allocator, on the call's stream."""
+    (zeroed by the caller) that becomes 1 if a bounded in-kernel wait ran out, after wait_ns nanoseconds (0: 2e9); the
+    rows concerned are then NaN. The workspace of long caches comes from torch's allocator, on the call's stream."""
     quick = _quick or (load() and _quick)
     rc = quick.tree_attention(q, k_cache, v_cache, lengths, masks, out,
-                              q.shape[-1] ** -0.5 if scale is None else scale, counts, slots, max_len, status, stream)
+                              q.shape[-1] ** -0.5 if scale is None else scale, counts, slots, max_len, status, stream,
+                              wait_ns)
     if rc == MK_OK:
         return
     if rc < 0:
@@ -467,7 +468,7 @@ def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None
            qs[1] if T > 1 else row, os[0] if B > 1 else 0, os[1] if T > 1 else row, q.data_ptr(), out.data_ptr(),
            k_cache.data_ptr(), v_cache.data_ptr(), lengths.data_ptr(), 0 if counts is None else counts.data_ptr(),
            0 if slots is None else slots.data_ptr(), masks.data_ptr(), 0, 0,
-           0 if status is None else status.data_ptr()]
+           0 if status is None else status.data_ptr(), wait_ns]
     L, work = load(), None
     if (max_len or S) >= 4096 and d >= 0:  # shorter caches are never split over more than a cluster
         with torch.cuda.device(d):

@@ -1273,6 +1273,7 @@ int mk_verify(mk_handle *h, const int32_t *d_tokens, const int32_t *d_parents, i
         h->vf.work = reinterpret_cast<float *>(m + o_work);
         h->vf.work_floats = work / 4;
     }
+    h->vf.wait_ns = h->timeout_ns;
     const mkpf::Tree &t = h->vf;
     float *logits = out_logits ? out_logits : h->vf_logits;
     const cudaStream_t s = (cudaStream_t)stream;

@@ -84,6 +84,8 @@ struct TreeArgs {
     const int32_t *lengths, *counts, *slot_of;
     const uint64_t *masks;
     int *err;     // set to 1 if a bounded wait runs out (nullable)
+    uint64_t wait_ns;    // limit of a wait, and how long a thread sleeps in it (set by the launch)
+    uint32_t wait_sleep;
     float *part;  // the splits' partial results (set by the launch from work)
     float *work;  // the caller's workspace (nullable)
     int64_t work_floats;

@@ -1268,7 +1268,7 @@ cudaError_t run_tree(const Model &m, const Scratch &sc, const Tree &t, const CUt
         mkops::TreeArgs a = tree_args(m, n);
         a.q = sc.QKV, a.out = sc.X, a.hi = sc.Ahi, a.lo = sc.Alo;
         a.kc = r.kc, a.vc = r.vc, a.lengths = t.length, a.masks = t.masks, a.err = sc.err;
-        a.work = t.work, a.work_floats = t.work_floats;
+        a.work = t.work, a.work_floats = t.work_floats, a.wait_ns = t.wait_ns;
         ok(mkops::tree_attention_launch(a, hd, true, pos0, m.n_sm, s));
         // as the prefill: O-projection, the gated MLP, the next norm (at last the final one)
         ok(gemm(lm.wo, sc.Ahi, sc.Alo, d, n, qd, sc.X, d, sc.X, sc.work, sc.work_floats, sc.err, m.n_sm, s,

@@ -86,6 +86,7 @@ struct Tree {
     int32_t *positions = nullptr, *rows = nullptr, *length = nullptr;
     float *work = nullptr;
     int64_t work_floats = 0;
+    uint64_t wait_ns = 0;  // limit of the attention's waits
 };
 
 // Bytes of workspace the tree's attention can use for n nodes behind pos0 rows.

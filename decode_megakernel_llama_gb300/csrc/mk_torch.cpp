@@ -99,9 +99,9 @@ long rope_append(PyObject *const *o, Py_ssize_t n_args) {
     return mk.rope(&a, s);
 }
 
-// q, k_cache, v_cache, lengths, masks, out, scale (0: 1 / sqrt(hd)), counts, slots, max_len, status, stream
+// q, k_cache, v_cache, lengths, masks, out, scale (0: 1 / sqrt(hd)), counts, slots, max_len, status, stream, wait_ns
 long tree_attention(PyObject *const *o, Py_ssize_t n_args) {
-    if (n_args != 12) return kNotHere;
+    if (n_args != 13) return kNotHere;
     const at::Tensor *q = tensor(o[0]), *k = tensor(o[1]), *v = tensor(o[2]), *out = tensor(o[5]);
     if (!q || !k || !v || !out || !q->is_cuda() || !out->is_cuda() || q->dim() != 4 || k->dim() != 4) return kNotHere;
     const int d = q->get_device(), type = io_type(*q);
@@ -120,13 +120,14 @@ long tree_attention(PyObject *const *o, Py_ssize_t n_args) {
     mk_tree_args a{};
     const double scale = PyFloat_AsDouble(o[6]);
     const long max_len = PyLong_AsLong(o[9]);
+    const long long wait_ns = PyLong_AsLongLong(o[12]);
     if (PyErr_Occurred() || max_len < 0 || max_len > INT32_MAX) {
         PyErr_Clear();
         return kNotHere;
     }
     a.batch = B, a.nodes = T, a.n_heads = Hq, a.n_kv_heads = k->size(1), a.head_dim = hd, a.dtype = type;
     a.slots = k->size(0), a.max_seq = S, a.max_len = max_len;
-    a.scale = scale;
+    a.scale = scale, a.wait_ns = wait_ns;
     a.q_batch_stride = B > 1 ? q->stride(0) : 0, a.q_token_stride = T > 1 ? q->stride(1) : row;
     a.out_batch_stride = B > 1 ? out->stride(0) : 0, a.out_token_stride = T > 1 ? out->stride(1) : row;
     a.q = address(q), a.out = out->data_ptr(), a.k_cache = address(k), a.v_cache = address(v);

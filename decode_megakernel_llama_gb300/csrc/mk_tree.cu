@@ -198,6 +198,8 @@ cudaError_t launch(TreeArgs a, int max_len, int n_sm, cudaStream_t s, int64_t *w
     }
     if (need > a.work_floats) p = plan<K>(a, max_len, n_sm, false);
     a.part = p.ws ? a.work : nullptr;
+    if (a.wait_ns == 0) a.wait_ns = kWaitNs;
+    a.wait_sleep = (uint32_t)std::min<uint64_t>(a.wait_ns, kSleepNs);
     CUtensorMap kmap, vmap;
     if (!cache_map(&kmap, a.kc, a.slots * a.Hkv, a.max_seq, K::HD) ||
         !cache_map(&vmap, a.vc, a.slots * a.Hkv, a.max_seq, K::HD))
@@ -291,6 +293,7 @@ int check_tree(const mk_tree_args *a) {
         return set_error(MK_ERR_INVALID_ARG, "mk_tree_attention: a pointer is not aligned");
     if (a->workspace_bytes < 0 || (a->workspace && (reinterpret_cast<uintptr_t>(a->workspace) & 15u)))
         return set_error(MK_ERR_INVALID_ARG, "mk_tree_attention: bad workspace");
+    if (a->wait_ns < 0) return set_error(MK_ERR_INVALID_ARG, "mk_tree_attention: wait_ns is negative");
     return MK_OK;
 }
 
@@ -306,6 +309,7 @@ mkops::TreeArgs tree_of(const mk_tree_args *a) {
     t.work = static_cast<float *>(a->workspace);
     t.work_floats = a->workspace ? a->workspace_bytes / 4 : 0;
     t.err = a->status;
+    t.wait_ns = (uint64_t)a->wait_ns;
     return t;
 }
 

@@ -267,6 +267,7 @@ struct Sync {
     // A group has read its scores, has written its weights (of a tile i: place i % 4, so
     // that a warp or the products, a tile of the group behind, are never two phases late)
     uint64_t s_read[2], p_full[4];
+    uint64_t quiet;  // after a wait that ran out: every product that was issued is done
     uint32_t tmem;
     int err, k_issued, v_issued;  // a wait ran out; tiles whose copies went out
     uint32_t bad[2];              // drafted rows taken out of the second product
@@ -287,6 +288,7 @@ __device__ __forceinline__ void init_sync(Sync<KU, VU> *y) {
         mbar_init(&y->p_full[g], kSoftWarps / 2);
         mbar_init(&y->p_full[g + 2], kSoftWarps / 2);
     }
+    mbar_init(&y->quiet, 1);
     y->err = y->k_issued = y->v_issued = 0;
     y->bad[0] = y->bad[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -302,20 +304,20 @@ __device__ __forceinline__ void init_sync(Sync<KU, VU> *y) {
 // last tile's PV that holds for the group of that tile; the other may pass early:
 // what it reads comes behind a barrier with the first.
 template <int KU, int VU>
-__device__ __forceinline__ bool k_full(Sync<KU, VU> *y, int i) {
-    return mbar_wait(&y->k_full[i % KU], (i / KU) & 1, &y->err);
+__device__ __forceinline__ bool k_full(Sync<KU, VU> *y, int i, const Wait &w) {
+    return mbar_wait(&y->k_full[i % KU], (i / KU) & 1, w);
 }
 template <int KU, int VU>
-__device__ __forceinline__ bool v_full(Sync<KU, VU> *y, int i) {
-    return mbar_wait(&y->v_full[i % VU], (i / VU) & 1, &y->err);
+__device__ __forceinline__ bool v_full(Sync<KU, VU> *y, int i, const Wait &w) {
+    return mbar_wait(&y->v_full[i % VU], (i / VU) & 1, w);
 }
 template <int KU, int VU>
-__device__ __forceinline__ bool s_done(Sync<KU, VU> *y, int i) {
-    return mbar_wait(&y->k_done[i % KU], (i / KU) & 1, &y->err);
+__device__ __forceinline__ bool s_done(Sync<KU, VU> *y, int i, const Wait &w) {
+    return mbar_wait(&y->k_done[i % KU], (i / KU) & 1, w);
 }
 template <int KU, int VU>
-__device__ __forceinline__ bool pv_done(Sync<KU, VU> *y, int i) {
-    return mbar_wait(&y->v_done[i % VU], (i / VU) & 1, &y->err);
+__device__ __forceinline__ bool pv_done(Sync<KU, VU> *y, int i, const Wait &w) {
+    return mbar_wait(&y->v_done[i % VU], (i / VU) & 1, w);
 }
 
 // The copies of a K (or V) tile into its place in the ring.
@@ -329,35 +331,46 @@ __device__ __forceinline__ void load_tile(uint8_t *at, const CUtensorMap *map, i
 // One lane's work: all of a split's K (or V) tiles, into the ring.
 template <int HD, int KU, int VU>
 __device__ __forceinline__ void load_all(Sync<KU, VU> *y, uint8_t *ring, const CUtensorMap *map, bool is_k, int from,
-                                         int to, int t0, int plane) {
+                                         int to, int t0, int plane, const Wait &w) {
     constexpr int kKv = kHalfTile * (HD / 64);
     for (int i = from; i < to; ++i) {
         if (is_k) {
-            if (i >= KU && !s_done(y, i - KU)) break;
+            if (i >= KU && !s_done(y, i - KU, w)) break;
             load_tile<HD>(ring + (i % KU) * kKv, map, (t0 + i) * kTile, plane, &y->k_full[i % KU]);
             *(volatile int *)&y->k_issued = i + 1;
         } else {
-            if (i >= VU && !pv_done(y, i - VU)) break;
+            if (i >= VU && !pv_done(y, i - VU, w)) break;
             load_tile<HD>(ring + (KU + i % VU) * kKv, map, (t0 + i) * kTile, plane, &y->v_full[i % VU]);
             *(volatile int *)&y->v_issued = i + 1;
         }
     }
 }
 
-// After a wait ran out: the copies that were issued land before the shared
-// memory goes.
+// After a wait that ran out, by the whole CTA behind a barrier: the products and copies
+// that were issued (no thread issues more) are done before their shared and tensor
+// memory goes, and before anything that the caller writes behind this. The products
+// read no barrier and the copies wait for nobody, so both end by themselves; their
+// own limit is the default one, however short the call's.
 template <int KU, int VU>
-__device__ __noinline__ void drain(Sync<KU, VU> *y, int *status) {
+__device__ __noinline__ void settle(Sync<KU, VU> *y, int *status) {
     auto land = [](uint64_t *bar, int units, int n) {
-        for (int i = max(0, n - units); i < n; ++i) {
-            const uint64_t from = gtimer();
-            while (!mbar_try(bar + i % units, (i / units) & 1))
-                if (gtimer() - from > kWaitNs) break;
-        }
+        for (int i = max(0, n - units); i < n; ++i) mbar_await(bar + i % units, (i / units) & 1);
     };
-    land(y->k_full, KU, *(volatile int *)&y->k_issued);
-    land(y->v_full, VU, *(volatile int *)&y->v_issued);
-    if (status) atomicExch(status, 1);
+    const int warp = warp_index();
+    if (warp == kMmaWarp) {
+        if (elect()) {  // (the lane that issued them)
+            umma_commit(&y->quiet);
+            mbar_await(&y->quiet, 0);
+        }
+    } else if (warp == kKWarp) {
+        if (elect()) {
+            land(y->k_full, KU, *(volatile int *)&y->k_issued);
+            land(y->v_full, VU, *(volatile int *)&y->v_issued);
+            if (status) atomicExch(status, 1);
+        }
+    }
+    __syncwarp();
+    __syncthreads();
 }
 
 // What a CTA does with its partial result (O in Os, maxima, sums): leaves it
@@ -474,6 +487,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     Sync<KU, VU> *y = reinterpret_cast<Sync<KU, VU> *>(sm + C::kOffMisc);
     static_assert(sizeof(Sync<KU, VU>) <= 512, "");
     volatile int *err = &y->err;
+    const Wait wt{err, a.wait_ns, a.wait_sleep};
     uint64_t *seen = reinterpret_cast<uint64_t *>(sm + C::kOffMisc + 512);  // [MK_MAX_TREE] bit r: row r sees it
     float *mref = reinterpret_cast<float *>(seen + MK_MAX_TREE), *corr = mref + 2 * NR;  // [2][NR] of the groups
     float *lsum = corr + 2 * NR;                // [NR]
@@ -515,8 +529,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (elect()) {
             init_sync(y);
             // the first copies need nobody else
-            load_all<HD>(y, sm, &kmap, true, 0, min(nt, KU), t0, plane);
-            load_all<HD>(y, sm, &vmap, false, 0, min(nt, VU), t0, plane);
+            load_all<HD>(y, sm, &kmap, true, 0, min(nt, KU), t0, plane, wt);
+            load_all<HD>(y, sm, &vmap, false, 0, min(nt, VU), t0, plane, wt);
         }
     } else if (warp == kMmaWarp) {
         tmem_alloc(&y->tmem, C::kCols);
@@ -543,9 +557,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t tS = uniform(y->tmem), tO = tS + 2 * N;  // S and O of group g: + g * N, + g * PN
 
     if (warp == kKWarp) {
-        if (elect()) load_all<HD>(y, sm, &kmap, true, KU, nt, t0, plane);
+        if (elect()) load_all<HD>(y, sm, &kmap, true, KU, nt, t0, plane, wt);
     } else if (warp == kVWarp) {
-        if (elect()) load_all<HD>(y, sm, &vmap, false, VU, nt, t0, plane);
+        if (elect()) load_all<HD>(y, sm, &vmap, false, VU, nt, t0, plane, wt);
     } else if (warp == kMmaWarp) {
         constexpr uint32_t idS = idesc_bf16(N, false, false), idO = idesc_bf16(PN, true, true);
         const uint64_t q = sw128_desc(saddr(Qs), 16);
@@ -562,23 +576,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bool ok = true;
             // the scores of tile i (early: once the group has read those of i - 2)
             for (int i = 0; i < min(nt, C::kAhead) && ok; ++i) {
-                ok = k_full(y, i) && (i < 2 || mbar_wait(&y->s_read[i & 1], ((i >> 1) - 1) & 1, err));
+                ok = k_full(y, i, wt) && (i < 2 || mbar_wait(&y->s_read[i & 1], ((i >> 1) - 1) & 1, wt));
                 tc_fence_after();
-                scores(i);
+                if (ok) scores(i);
             }
             for (int i = 0; i < nt && ok; ++i) {
                 const int j = i + C::kAhead;
                 if (C::kEarly && j < nt) {
-                    ok = k_full(y, j) && mbar_wait(&y->s_read[j & 1], ((j >> 1) - 1) & 1, err);
+                    ok = k_full(y, j, wt) && mbar_wait(&y->s_read[j & 1], ((j >> 1) - 1) & 1, wt);
                     tc_fence_after();
-                    scores(j);
+                    if (ok) scores(j);
                 }
                 // (the k-th product's first atom moves on by 2048 bytes, so the constant
                 // block behind it comes nearer)
                 const uint32_t va = ring + (KU + i % VU) * C::kKv;
                 const uint64_t v = sw128_desc(va, kOnes ? ones - va : kHalfTile);
                 const uint64_t p = sw128_desc(p0 + (i & 1) * C::kP, kHalfTile);
-                if (!(ok = ok && v_full(y, i) && mbar_wait(&y->p_full[i & 3], (i >> 2) & 1, err))) break;
+                if (!(ok = ok && v_full(y, i, wt) && mbar_wait(&y->p_full[i & 3], (i >> 2) & 1, wt))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
@@ -586,9 +600,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                               p + ((kk * 2048) >> 4), idO, i >= 2 || kk != 0);
                 umma_commit(&y->v_done[i % VU]);
                 if (!C::kEarly && j < nt) {
-                    ok = k_full(y, j);
+                    ok = k_full(y, j, wt);
                     tc_fence_after();
-                    scores(j);
+                    if (ok) scores(j);
                 }
             }
         }
@@ -605,9 +619,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int r = 0; r < NR; ++r) l[r] = 0.f;
         bool ok = true;
         for (int i = g; i < nt; i += 2) {
-            // (a wait that ran out: the loop goes on, its barriers matched, and
-            // the result becomes NaN)
-            ok &= s_done(y, i);
+            // (a wait that ran out: the loop goes on, its barriers matched, without
+            // another wait, and the result becomes NaN)
+            ok = ok && s_done(y, i, wt);
             tc_fence_after();
             float s[TERMS * NR];
 #pragma unroll
@@ -649,7 +663,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             };
             const bool raise = group_any(g, shift() > kRaise);
             // PV(i - 2) is done: P and O are this group's again (not early: S(i) was issued after it)
-            if (C::kEarly && i >= 2) ok &= pv_done(y, i - 2);
+            if (C::kEarly && i >= 2) ok = ok && pv_done(y, i - 2, wt);
             if (raise) {
                 // raise the maxima to those of all cache rows so far
 #pragma unroll
@@ -686,7 +700,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             if (tail) {
-                ok &= v_full(y, i);
+                ok = ok && v_full(y, i, wt);
                 if (node >= 0) mend_v<HD>(sm + (KU + i % VU) * C::kKv, row, node, sq.n, y->bad);
             }
             // the weights as the B operand: row = cache row, column = term * NR + r
@@ -712,9 +726,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&y->p_full[i & 3]);
         }
-        if (nt > 0) ok &= pv_done(y, nt - 1);  // (and with it every product)
+        if (nt > 0) ok = ok && pv_done(y, nt - 1, wt);  // (and with it every product)
         tc_fence_after();
-        if (!ok) *err = 1;
         if constexpr (!kOnes) {
             // the sums of the 128 cache rows, warp by warp
 #pragma unroll
@@ -771,13 +784,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         }
         soft_sync();
-        if (*err && first < NR) lsum[first] = __uint_as_float(0x7FC00000u);  // a wait ran out: NaN
         if (y->bad[0] | y->bad[1]) add_taken_out<HD, TERMS, false>(a, b, kvh, G, row0, rows, sq, y->bad, mref, Os, first);
     }
     tc_fence_before();
     __syncwarp();
     __syncthreads();
-    if (*err && tid == 0) drain(y, a.err);
+    if (*err) {  // a wait ran out (nobody waits any more: the same for all threads): the rows are NaN
+        settle(y, a.err);
+        if (tid < NR) lsum[tid] = __uint_as_float(0x7FC00000u);
+        __syncthreads();
+    }
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_free(tS, C::kCols);
@@ -812,7 +828,7 @@ struct RowShape {
     static constexpr int kOffQ = (KU + VU) * kKv, kOffMisc = kOffQ + kQ;
     static constexpr int kSmem = 1024 + kOffMisc + kMisc;
     static_assert(NB * (kTile + kThird) + 2 * HD <= kCols && VU >= NB && KU >= NB, "tensor and shared memory of an SM");
-    static_assert(kRows * HD * 4 + (3 * kCluster + 2) * kRows * 4 <= (KU + VU) * kKv, "the partial result fits the ring");
+    static_assert(kRows * HD * 4 + 3 * kCluster * kRows * 4 <= (KU + VU) * kKv, "the partial result fits the ring");
 };
 
 template <int HD, int TERMS>
@@ -828,10 +844,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     Sync<KU, VU> *y = reinterpret_cast<Sync<KU, VU> *>(sm + C::kOffMisc);
     static_assert(sizeof(Sync<KU, VU>) <= 512, "");
     volatile int *err = &y->err;
-    float *gm = reinterpret_cast<float *>(sm + C::kOffMisc + 512);  // [2][128] the groups' maxima
+    const Wait wt{err, a.wait_ns, a.wait_sleep};
+    // [2][128]: the groups' maxima, then the rows' maxima and sums, each written by the thread that read what was there
+    float *gm = reinterpret_cast<float *>(sm + C::kOffMisc + 512), *mref = gm, *lsum = gm + kRows;
     float *Os = reinterpret_cast<float *>(sm);                      // in the ring when the tiles are done,
     float *join = Os + kRows * HD;                                  // and behind it
-    float *mref = join + 3 * kCluster * kRows, *lsum = mref + kRows;
 
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int split = blockIdx.x, S = gridDim.x;
@@ -865,8 +882,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (elect()) {
             init_sync(y);
             // the first copies need nobody else
-            load_all<HD>(y, sm, &kmap, true, 0, min(nt, KU), t0, plane);
-            load_all<HD>(y, sm, &vmap, false, 0, min(nt, VU), t0, plane);
+            load_all<HD>(y, sm, &kmap, true, 0, min(nt, KU), t0, plane, wt);
+            load_all<HD>(y, sm, &vmap, false, 0, min(nt, VU), t0, plane, wt);
         }
     } else if (warp == kMmaWarp) {
         tmem_alloc(&y->tmem, C::kCols);
@@ -880,9 +897,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t tS = uniform(y->tmem), tT = tS + NB * kTile, tO = tT + NB * C::kThird;
 
     if (warp == kKWarp) {
-        if (elect()) load_all<HD>(y, sm, &kmap, true, KU, nt, t0, plane);
+        if (elect()) load_all<HD>(y, sm, &kmap, true, KU, nt, t0, plane, wt);
     } else if (warp == kVWarp) {
-        if (elect()) load_all<HD>(y, sm, &vmap, false, VU, nt, t0, plane);
+        if (elect()) load_all<HD>(y, sm, &vmap, false, VU, nt, t0, plane, wt);
     } else if (warp == kMmaWarp) {
         constexpr uint32_t idS = idesc_bf16(kTile, false, false), idO = idesc_bf16(HD, false, true);
         const uint64_t q = sw128_desc(saddr(Qs), 16);
@@ -900,14 +917,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         };
         if (elect()) {
             bool ok = true;
-            for (int i = 0; i < min(nt, NB) && (ok = k_full(y, i)); ++i) {
+            for (int i = 0; i < min(nt, NB) && (ok = k_full(y, i, wt)); ++i) {
                 tc_fence_after();
                 scores(i);
             }
             for (int i = 0; i < nt && ok; ++i) {
                 const int j = i + NB;
                 const uint64_t v = sw128_desc(ring + (KU + i % VU) * C::kKv, kHalfTile);
-                if (!(ok = ok && v_full(y, i) && mbar_wait(&y->p_full[i & 3], (i >> 2) & 1, err))) break;
+                if (!(ok = ok && v_full(y, i, wt) && mbar_wait(&y->p_full[i & 3], (i >> 2) & 1, wt))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int t = 0; t < PT; ++t)
@@ -919,9 +936,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                 umma_commit(&y->v_done[i % VU]);
                 if (j < nt) {  // (into the buffer of PV(i))
-                    ok = k_full(y, j);
+                    ok = k_full(y, j, wt);
                     tc_fence_after();
-                    scores(j);
+                    if (ok) scores(j);
                 }
             }
         }
@@ -935,7 +952,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         float m = kNone, l = 0.f;
         bool ok = true;
         for (int i = g; i < nt; i += 2) {
-            ok &= s_done(y, i);
+            ok = ok && s_done(y, i, wt);
             tc_fence_after();
             const uint32_t ts = tS + (i % NB) * kTile + mylane, tt = tT + (i % NB) * C::kThird + mylane;
             const int at = (t0 + i) * kTile;
@@ -968,7 +985,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     m = best;
                     l *= scale;
                     if (i >= 2) {
-                        if (NB > 2) ok &= pv_done(y, i - 2);  // O is this group's again (NB = 2: S(i) was issued behind it)
+                        if (NB > 2) ok = ok && pv_done(y, i - 2, wt);  // O is this group's again (NB = 2: S(i) was issued behind it)
                         tc_fence_after();
 #pragma unroll 1
                         for (int d = 0; d < HD; d += 16) {
@@ -1011,16 +1028,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tc_fence_before();
             if (tail) {
                 const int node = at + row - sq.len;
-                ok &= v_full(y, i);
+                ok = ok && v_full(y, i, wt);
                 if (node >= 0) mend_v<HD>(sm + (KU + i % VU) * C::kKv, row, node, sq.n, y->bad);
                 async_fence();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&y->p_full[i & 3]);
         }
-        if (nt > 0) ok &= pv_done(y, nt - 1);  // (and with it every product: the ring is free)
+        if (nt > 0) ok = ok && pv_done(y, nt - 1, wt);  // (and with it every product: the ring is free)
         tc_fence_after();
-        if (!ok) *err = 1;
         gm[g * kRows + row] = m;
         soft_sync();
         tc_fence_after();  // (a group that passed early reads O behind the barrier, too)
@@ -1054,17 +1070,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                 }
                 lsum[row] = h ? lsum[row] + l : l;
-                mref[row] = best;
+                if (h) mref[row] = best;
             }
             soft_sync();
         }
-        if (*err && g == 0) lsum[row] = __uint_as_float(0x7FC00000u);  // a wait ran out: NaN
         if (y->bad[0] | y->bad[1]) add_taken_out<HD, TERMS, true>(a, b, kvh, G, row0, rows, sq, y->bad, mref, Os, st);
     }
     tc_fence_before();
     __syncwarp();
     __syncthreads();
-    if (*err && tid == 0) drain(y, a.err);
+    if (*err) {  // a wait ran out (nobody waits any more: the same for all threads): the rows are NaN
+        settle(y, a.err);
+        if (tid < kRows) lsum[tid] = __uint_as_float(0x7FC00000u);
+        __syncthreads();
+    }
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_free(tS, C::kCols);

@@ -280,7 +280,8 @@ int mk_decode_step_noalloc(const mk_config *config, const mk_weights *weights,
 int mk_get_status(mk_handle *h);
 
 /* Bounded-wait limit for in-kernel dependency waits, in nanoseconds
- * (default 2e9). Host-only setting, takes effect on the next step.
+ * (default 2e9): those of the decode steps and of mk_verify's attention.
+ * Host-only setting, takes effect on the next step or tree.
  * Source: as mk_get_status (the synchronisation paragraph's in-kernel
  * waits); the limit itself is this library's convention. */
 int mk_set_wait_timeout(mk_handle *h, uint64_t timeout_ns);
@@ -521,7 +522,8 @@ int mk_rope_frequencies(int32_t kind, int32_t rot, double theta, double factor, 
  * this call alone, in use until it is done on the stream; with less than
  * mk_tree_attention_workspace() asks for, the call does without. status
  * (device int32, zeroed by the caller, or NULL) becomes 1 if a bounded
- * in-kernel wait ran out; the rows concerned are then NaN. */
+ * in-kernel wait ran out, each after wait_ns nanoseconds (0: 2e9); the rows
+ * concerned are then NaN. */
 typedef struct mk_tree_args {
     int32_t batch, nodes, n_heads, n_kv_heads, head_dim, dtype, slots, max_seq, max_len;
     float scale;
@@ -534,6 +536,7 @@ typedef struct mk_tree_args {
     void *workspace;
     int64_t workspace_bytes;
     int32_t *status;
+    int64_t wait_ns;
 } mk_tree_args;
 int mk_tree_attention(const mk_tree_args *args, void *stream);
 

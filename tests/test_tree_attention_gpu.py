@@ -1,5 +1,5 @@
-"""tree_attention where its general bounds are too wide to see a fault: the
-weights of bf16 queries."""
+"""tree_attention where its general bounds and ordinary calls see no fault: the
+weights of bf16 queries, waits that run out."""
 import pytest
 import torch
 
@@ -61,3 +61,63 @@ def test_bf16_results_are_rounded_once(dev, hd, T, Hq, Hkv, lengths, counts):
     on = ~want.isnan()
     err = (c.out.double() - want).abs()[on]
     assert (err <= tol[on]).all(), (int((err > tol[on]).sum()), err.numel(), float((err / tol[on]).max()))
+
+
+WAITS = [  # heads, type, nodes and query rows, lengths, max_len: 16 and 32 columns and 128 rows; one CTA, a cluster, many CTAs
+    (64, torch.float32, 4, 4, 1, [9000], 1), (64, BF, 8, 4, 1, [9000, 4000], 9000), (64, torch.float32, 8, 32, 8, [9000], 9000),
+    (128, torch.float32, 8, 4, 1, [9000], 1), (128, BF, 4, 4, 1, [9000], 9000), (128, BF, 8, 8, 2, [30000], 30000),
+    (64, torch.float32, 61, 32, 8, [3000, 5000, 900, 2000] * 2, 5000), (64, BF, 61, 32, 8, [3000, 5000, 900, 2000] * 2, 5000),
+    (128, BF, 61, 32, 8, [3000, 5000, 900, 2000] * 2, 5000), (64, BF, 61, 8, 1, [60000], 60000), (128, BF, 61, 8, 1, [60000], 60000),
+]
+
+
+@pytest.mark.parametrize("hd,dtype,T,Hq,Hkv,lengths,max_len", WAITS)
+def test_a_wait_that_runs_out(dev, hd, dtype, T, Hq, Hkv, lengths, max_len):
+    """A limit of a nanosecond, which copies from memory exceed: the status word says so, a row is NaN or right, and the
+    next call, which waits as long as it has to, is right."""
+    c = Case(dev, lengths, T, Hq, Hkv, hd, dtype)
+    c.run(max_len=max_len)
+    want, st = c.out.clone(), torch.zeros(1, dtype=I32, device=dev)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=dev)
+    lost = 0
+    for rep in range(20):
+        c.out.fill_(99.0)
+        st.zero_()
+        flush.zero_()  # the cache's rows come from memory
+        c.run(max_len=max_len, wait_ns=1, status=st)
+        nan = c.out.isnan()
+        assert int(st) == int(nan.any())
+        assert torch.equal(nan.all(-1), nan.any(-1))
+        assert torch.equal(c.out[~nan], want[~nan])
+        lost += int(nan.sum())
+    assert lost > 0
+    st.zero_()
+    c.out.fill_(99.0)
+    c.run(max_len=max_len, status=st)
+    assert int(st) == 0 and torch.equal(c.out, want)
+
+
+def test_a_wait_that_runs_out_in_a_model(cuda_dev):
+    """mk_set_wait_timeout reaches the attention of mk_verify; its status is reported once and the handle works again."""
+    from decode_megakernel_llama_gb300 import _lib, synth
+    from decode_megakernel_llama_gb300.configs import TINY
+    build()
+    dev = torch.device("cuda:0")
+    k, v = synth.kv_cache(TINY, 600, 1, dev)
+    synth.prefill_cache(k, v, 500)
+    mk = _lib.Megakernel(TINY, synth.make_weights(TINY, dev, 0), k, v)
+    tk = torch.tensor([3, 5, 7], dtype=I32, device=dev)
+    pr = torch.tensor([-1, 0, 0], dtype=I32, device=dev)
+    out, lg = torch.zeros(3, dtype=I32, device=dev), torch.zeros(3, TINY.vocab, device=dev)
+    mk.verify(tk, pr, 500, out, lg)
+    assert mk.status() == 0
+    want = out.tolist(), lg.clone()
+    mk.set_wait_timeout(1)
+    mk.verify(tk, pr, 500, out, lg)
+    assert mk.status() == _lib.MK_ERR_TIMEOUT
+    assert lg.isnan().all()
+    mk.set_wait_timeout(2_000_000_000)
+    mk.verify(tk, pr, 500, out, lg)
+    assert mk.status() == 0
+    assert out.tolist() == want[0] and torch.equal(lg, want[1])
+    mk.close()
