@@ -1,5 +1,5 @@
 """tree_attention where its general bounds and ordinary calls see no fault: the
-weights of bf16 queries, waits that run out."""
+weights of bf16 queries, waits that run out, splits through the workspace."""
 import pytest
 import torch
 
@@ -121,3 +121,120 @@ def test_a_wait_that_runs_out_in_a_model(cuda_dev):
     assert mk.status() == 0
     assert out.tolist() == want[0] and torch.equal(lg, want[1])
     mk.close()
+
+
+# Caches so long that their rows are split over more CTAs than a cluster holds, the parts joined by a second kernel out
+# of a workspace: 16 and 32 columns and 128 rows (the last number), one sequence and several.
+SPLIT = [
+    (64, torch.float32, 4, 8, 2, [20000], 16), (128, BF, 4, 8, 2, [20000], 16), (64, BF, 1, 16, 1, [70000], 16),
+    (64, BF, 8, 8, 2, [24000], 32), (128, torch.float32, 8, 8, 2, [24000], 32), (128, torch.float32, 33, 4, 2, [16000], 32),
+    (64, torch.float32, 40, 16, 2, [40000], 128), (64, BF, 61, 8, 1, [60000], 128), (128, BF, 61, 8, 1, [60000], 128),
+    (64, torch.float32, 5, 6, 2, [30000, 5, 17000], 16), (64, BF, 40, 16, 2, [9000, 40000], 128),
+]
+
+
+def split_args(c, max_len, **kw):
+    """The C call's arguments for a Case, without a workspace."""
+    from decode_megakernel_llama_gb300 import _lib
+    B, T, Hq, hd = c.q.shape
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    return _lib.mk_tree_args(**{**dict(
+        batch=B, nodes=T, n_heads=Hq, n_kv_heads=c.k.shape[1], head_dim=hd, dtype=int(c.q.dtype == BF),
+        slots=c.k.shape[0], max_seq=c.k.shape[2], max_len=max_len, scale=c.scale, q_batch_stride=T * Hq * hd,
+        q_token_stride=Hq * hd, out_batch_stride=T * Hq * hd, out_token_stride=Hq * hd, q=ptr(c.q), out=ptr(c.out),
+        k_cache=ptr(c.k), v_cache=ptr(c.v), lengths=ptr(c.lengths), counts=ptr(c.counts), slot_of=ptr(c.slots),
+        masks=ptr(c.masks)), **kw})
+
+
+def work_bytes(c, max_len, rows):
+    """The workspace asked for, which has to be whole parts of the kernel of so many rows."""
+    import ctypes
+
+    from decode_megakernel_llama_gb300 import _lib
+    n = _lib.load().mk_tree_attention_workspace(ctypes.byref(split_args(c, max_len)))
+    B, T, Hq, hd = c.q.shape
+    tiles = -(-T * (Hq // c.k.shape[1]) // rows)
+    part = 4 * rows * (hd + 2) * B * c.k.shape[1] * tiles
+    assert n > part and n % part == 0, (n, part)
+    return n
+
+
+@pytest.mark.parametrize("hd,dtype,T,Hq,Hkv,lengths,rows", SPLIT)
+def test_splits_through_the_workspace(dev, hd, dtype, T, Hq, Hkv, lengths, rows):
+    """Against the plain form; equal bits again, in two streams at once and in two graphs replayed side by side."""
+    longest = max(lengths)
+    cases = [Case(dev, lengths, T, Hq, Hkv, hd, dtype, seed=s) for s in (1, 2)]
+    for c in cases:
+        work_bytes(c, longest, rows)
+        c.run(max_len=longest)
+        c.check()
+    want = [c.out.clone() for c in cases]
+    streams, graphs = [torch.cuda.Stream() for _ in cases], []
+    for c in cases:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.run(max_len=longest)
+    for rep in range(6):
+        for c in cases:
+            c.out.fill_(99.0)
+        torch.cuda.synchronize()
+        for c, s, gr in zip(cases, streams, graphs):
+            if rep % 2:
+                with torch.cuda.stream(s):
+                    gr.replay()
+            else:
+                c.run(max_len=longest, stream=s)
+        torch.cuda.synchronize()
+        for c, w in zip(cases, want):
+            assert torch.equal(c.out, w)
+
+
+@pytest.mark.parametrize("hd,dtype,T,Hq,Hkv,lengths,rows", SPLIT)
+def test_a_workspace_of_the_size_asked_for_too_small_or_none(dev, hd, dtype, T, Hq, Hkv, lengths, rows):
+    """With less than it asks for a call does without; it never writes outside what it was given."""
+    import ctypes
+
+    from decode_megakernel_llama_gb300 import _lib
+    longest = max(lengths)
+    c = Case(dev, lengths, T, Hq, Hkv, hd, dtype)
+    n = work_bytes(c, longest, rows)
+    stream = torch.cuda.current_stream().cuda_stream
+    for given in (n, n - 4, n // 2, 16, 0, None):
+        room = torch.full((n + 4096,), 77, dtype=torch.uint8, device=dev)
+        kw = {} if given is None else dict(workspace=room.data_ptr(), workspace_bytes=given)
+        c.out.fill_(99.0)
+        _lib.check(_lib.load().mk_tree_attention(ctypes.byref(split_args(c, longest, **kw)), stream))
+        c.check()
+        assert (room[(n if given == n else 0):] == 77).all(), given
+        assert given != n or not (room[:n] == 77).all()
+
+
+@pytest.mark.parametrize("hd,dtype,T,Hq,Hkv,rows", [(64, torch.float32, 5, 6, 2, 16), (128, BF, 8, 8, 2, 32),
+                                                    (64, BF, 40, 16, 2, 128)])
+def test_split_sequences_of_no_node_no_slot_and_junk(dev, hd, dtype, T, Hq, Hkv, rows):
+    c = Case(dev, [30000, 6, 20000, 50], T, Hq, Hkv, hd, dtype, counts=[T, 0, 2, T], slots=[2, 0, 3, 4], n_slots=5,
+             S=30100)
+    work_bytes(c, 30000, rows)
+    c.k[:, :, 30000 + T:] = float("nan")
+    c.v[:, :, 30000 + T:] = float("inf")
+    c.k[3, :, 20002:], c.v[3, :, 20002:] = float("inf"), float("nan")
+    c.masks[0, 1] = -(1 << 63)  # a bit behind the tree
+    c.run(max_len=30000)
+    c.check()
+    c.slots[3] = 5  # outside the cache: its rows are left alone
+    keep = c.out.clone()
+    c.out.fill_(99.0)
+    c.run(max_len=30000)
+    torch.cuda.synchronize()
+    assert (c.out[3] == 99.0).all() and torch.equal(c.out[:3], keep[:3])
+    # a drafted row that is not finite reaches those that see it, and no other
+    c.masks[0, :3] = torch.tensor([1, 2, 4], device=dev)
+    c.masks[0, 3:] &= ~2
+    c.run(max_len=30000)
+    keep = c.out.clone()
+    c.v[2, :, 30001, 3] = float("inf")
+    c.run(max_len=30000)
+    torch.cuda.synchronize()
+    assert (c.out[0, 1, :, 3] == float("inf")).all()
+    c.out[0, 1] = keep[0, 1]
+    assert torch.equal(c.out, keep)
