@@ -470,7 +470,7 @@ def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None
            0 if slots is None else slots.data_ptr(), masks.data_ptr(), 0, 0,
            0 if status is None else status.data_ptr(), wait_ns]
     L, work = load(), None
-    if (max_len or S) >= 4096 and d >= 0:  # shorter caches are never split over more than a cluster
+    if d >= 0:
         with torch.cuda.device(d):
             n = L.mk_tree_attention_workspace(_TREE_ARGS.pack(*rec))
             if n < 0:

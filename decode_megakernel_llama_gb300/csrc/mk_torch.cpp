@@ -137,8 +137,7 @@ long tree_attention(PyObject *const *o, Py_ssize_t n_args) {
     a.slot_of = static_cast<const int32_t *>(address(slots));
     a.status = status ? static_cast<int32_t *>(status->data_ptr()) : nullptr;
     at::Tensor work;
-    // (shorter caches are never split over more than a cluster)
-    const int64_t bytes = (max_len ? max_len : S) >= 4096 ? mk.tree_work(&a) : 0;
+    const int64_t bytes = mk.tree_work(&a);
     if (bytes < 0) return bytes;
     if (bytes > 0) {
         work = at::empty({bytes}, k->options().dtype(at::kByte));

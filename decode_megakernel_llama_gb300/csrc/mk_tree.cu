@@ -162,7 +162,9 @@ int active_clusters(int k, int n_sm) {
 // 32 fp32 rows 21.4 us, of 32 bf16 rows 20.7, of 128 bf16 rows 26.6; each
 // with K::kFixedUs of launch, set-up and end); more than a
 // cluster's splits cost K::kJoinUs: a second launch and the partial results'
-// way through memory.
+// way through memory. (That pays from about 3,000 rows on where whole waves of clusters
+// leave SMs free: two trees of 38 nodes, 16 heads of 128 a kv head, fp32, 3,875 rows
+// 16.9 us, in clusters 21.4.)
 template <class K>
 Plan plan(const TreeArgs &a, int max_len, int n_sm, bool ws) {
     const int row_tiles = (a.T * (a.Hq / a.Hkv) + K::NR - 1) / K::NR;

@@ -238,3 +238,29 @@ def test_split_sequences_of_no_node_no_slot_and_junk(dev, hd, dtype, T, Hq, Hkv,
     assert (c.out[0, 1, :, 3] == float("inf")).all()
     c.out[0, 1] = keep[0, 1]
     assert torch.equal(c.out, keep)
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,hd,dtype", [(3, 64, 8, 1, 128, torch.float32), (1, 64, 16, 1, 64, BF), (2, 33, 8, 2, 64, BF),
+                                                 (1, 1, 8, 8, 128, torch.float32)])
+def test_the_binding_and_the_c_call_split_alike(dev, B, T, Hq, Hkv, hd, dtype):
+    """The workspace is asked for whatever the length: equal bits on either way, and with a stream given."""
+    import ctypes
+
+    from decode_megakernel_llama_gb300 import _lib
+    for n in (3400, 4030, 4095, 9000):
+        c = Case(dev, [n] * B, T, Hq, Hkv, hd, dtype)
+        size = _lib.load().mk_tree_attention_workspace(ctypes.byref(split_args(c, n)))
+        assert size > 0 if B == 3 else size >= 0  # (for the first shape all of these lengths pay)
+        work = torch.empty(size, dtype=torch.uint8, device=dev)
+        a = split_args(c, n, workspace=work.data_ptr() if size else None, workspace_bytes=size)
+        _lib.check(_lib.load().mk_tree_attention(ctypes.byref(a), torch.cuda.current_stream().cuda_stream))
+        want = c.out.clone()
+        for kw in ({}, dict(stream=torch.cuda.Stream())):
+            torch.cuda.synchronize()
+            c.out.fill_(99.0)
+            torch.cuda.synchronize()
+            c.run(max_len=n, **kw)
+            torch.cuda.synchronize()
+            assert torch.equal(c.out, want), n
+        if n == 4030:
+            c.check()
