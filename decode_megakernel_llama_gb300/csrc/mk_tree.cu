@@ -120,21 +120,19 @@ cudaError_t configure() {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1))) return e;
     e = cudaFuncSetAttribute(K::fn(), cudaFuncAttributeMaxDynamicSharedMemorySize, K::kSmem);
-    // (two CTAs an SM need the whole carveout as shared memory)
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(K::fn(), cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
     return e;
 }
 
-// Clusters of 2^k CTAs that the device holds at once (asked of the runtime
-// once; its count of clusters is for one CTA an SM).
+// Clusters of 2^k CTAs, one an SM, that the current device holds at once (asked of
+// the runtime once for each device).
 template <class K>
 int active_clusters(int k, int n_sm) {
-    static std::atomic<int> known[4];
-    int n = known[k].load(std::memory_order_relaxed);
+    static_assert(2 * K::kSmem > kSmemMost, "one CTA an SM");
+    static std::atomic<int> known[64][4];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) n = known[dev][k].load(std::memory_order_relaxed);
     if (n) return n;
-    int per_sm = 1;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -145,13 +143,11 @@ int active_clusters(int k, int n_sm) {
     cfg.dynamicSmemBytes = K::kSmem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (configure<K>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, K::fn(), &cfg) != cudaSuccess || n < 1 ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, K::fn(), kAttnThreads, K::kSmem) != cudaSuccess) {
+    if (configure<K>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, K::fn(), &cfg) != cudaSuccess || n < 1) {
         (void)cudaGetLastError();
         return n_sm >> k;  // (not kept: the next call asks again)
     }
-    n *= std::max(1, per_sm);
-    known[k].store(n, std::memory_order_relaxed);
+    if (dev < 64) known[dev][k].store(n, std::memory_order_relaxed);
     return n;
 }
 
