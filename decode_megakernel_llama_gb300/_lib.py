@@ -10,6 +10,7 @@ import ctypes
 import os
 import re
 import struct
+import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_build", "libmk.so")
@@ -85,6 +86,7 @@ _TREE_ARGS = struct.Struct("@9if4q9PqPq")
 
 _lib = None
 _quick = None  # the extension module of the drafted-tree operators (csrc/mk_torch.cpp)
+_loading = threading.RLock()
 _VP = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _PI32 = ctypes.POINTER(ctypes.c_int32)
@@ -95,8 +97,14 @@ def load(path: str | None = None):
     environment variable MK_LIB selects another build of the same library
     (e.g. the address-checked one)."""
     global _lib
-    if _lib is not None:
-        return _lib
+    if _lib is None:
+        with _loading:
+            if _lib is None:
+                _lib = _load(path)
+    return _lib
+
+
+def _load(path: str | None):
     path = path or os.environ.get("MK_LIB") or LIB_PATH
     if not os.path.exists(path):
         raise ImportError(f"{path} is missing: run decode_megakernel_llama_gb300.build.build() "
@@ -143,26 +151,29 @@ def load(path: str | None = None):
     L.mk_kv_reorder.argtypes = [_VP, _VP] + [_I32] * 5 + [_VP] * 3
     L.mk_destroy.argtypes = [_VP]
     L.mk_destroy.restype = None
-    _lib = L
-    _bind_quick(L)
     return L
 
 
-def _bind_quick(L) -> None:
-    """Loads mk_torch.so beside libmk.so and gives it the library's entry points."""
+def load_extension():
+    """Loads the extension module of the drafted-tree operators (rope_append, tree_attention, kv_compact, kv_reorder),
+    which their first call does otherwise, and gives it the library's entry points. Nothing else needs it."""
     global _quick
-    import importlib.util
+    with _loading:
+        if _quick is None:
+            import importlib.util
 
-    import torch  # noqa: F401  (the module needs its libraries)
-    path = os.path.join(PKG, "_build", "mk_torch.so")
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: run decode_megakernel_llama_gb300.build.build()")
-    spec = importlib.util.spec_from_file_location("mk_torch", path)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
-    mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        L.mk_rope_append, L.mk_tree_attention, L.mk_tree_attention_workspace, L.mk_kv_compact, L.mk_kv_reorder)))
-    _quick = mod
+            from .build import extension_path
+            L, path = load(), extension_path()  # (imports torch, whose libraries the module needs)
+            if not os.path.exists(path):
+                raise ImportError(f"{path} is missing: run decode_megakernel_llama_gb300.build.build()")
+            spec = importlib.util.spec_from_file_location("mk_torch", path)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                L.mk_rope_append, L.mk_tree_attention, L.mk_tree_attention_workspace, L.mk_kv_compact,
+                L.mk_kv_reorder)))
+            _quick = mod
+    return _quick
 
 
 def declared_symbols(header: str = HEADER) -> list[str]:
@@ -372,7 +383,7 @@ def rope_append(qkv, q_out, k_cache, v_cache, positions, rows, inv_freq, slots=N
     """mk_rope_append on CUDA tensors: qkv [n][(Hq + 2 Hkv) hd] float32 or bfloat16 (rows may be strided),
     q_out [n][Hq][hd] of the same type (token stride free), k_cache / v_cache bfloat16 [B][Hkv][max_seq][hd]
     (one layer), positions / rows / slots int32 [n], inv_freq float64 [rot / 2], q_norm / k_norm bfloat16 [hd]."""
-    q = _quick or (load() and _quick)
+    q = _quick or load_extension()
     rc = q.rope_append(qkv, q_out, k_cache, v_cache, positions, rows, inv_freq, slots, q_norm, k_norm, eps, mscale,
                        interleaved, stream)
     if rc == MK_OK:
@@ -426,7 +437,7 @@ def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None
     masks int64 [B][T] (the 64 bits of the ancestor mask). scale defaults to 1 / sqrt(hd). status: int32 [1]
     (zeroed by the caller) that becomes 1 if a bounded in-kernel wait ran out, after wait_ns nanoseconds (0: 2e9); the
     rows concerned are then NaN. The workspace of long caches comes from torch's allocator, on the call's stream."""
-    quick = _quick or (load() and _quick)
+    quick = _quick or load_extension()
     rc = quick.tree_attention(q, k_cache, v_cache, lengths, masks, out,
                               q.shape[-1] ** -0.5 if scale is None else scale, counts, slots, max_len, status, stream,
                               wait_ns)
@@ -531,7 +542,7 @@ def _check_caches(torch, k, v, shape, small) -> None:
 def kv_compact(k, v, starts, nodes, counts, stream=None) -> None:
     """mk_kv_compact on CUDA tensors: k / v bfloat16 [L][B][Hkv][max_seq][hd], starts / counts int32 [B], nodes
     int32 [B][n]: rows starts[b] + nodes[b][i] move to starts[b] + i."""
-    rc = (_quick or (load() and _quick)).kv_compact(k, v, starts, nodes, counts, stream)
+    rc = (_quick or load_extension()).kv_compact(k, v, starts, nodes, counts, stream)
     if rc == MK_OK:
         return
     if rc < 0:
@@ -550,7 +561,7 @@ def kv_compact(k, v, starts, nodes, counts, stream=None) -> None:
 def kv_reorder(k, v, sources, lengths, stream=None) -> None:
     """mk_kv_reorder on CUDA tensors: k / v bfloat16 [L][B][Hkv][max_seq][hd], sources / lengths int32 [B]: rows
     [0, lengths[b]) of slot b become slot sources[b]'s."""
-    rc = (_quick or (load() and _quick)).kv_reorder(k, v, sources, lengths, stream)
+    rc = (_quick or load_extension()).kv_reorder(k, v, sources, lengths, stream)
     if rc == MK_OK:
         return
     if rc < 0:

@@ -1,4 +1,4 @@
-"""Builds libmk.so (the megakernel and its C ABI) in-tree for sm_103a, and mk_torch.so, the binding's extension module."""
+"""Builds libmk.so (the megakernel and its C ABI) in-tree for sm_103a, and mk_torch, the binding's extension module."""
 from __future__ import annotations
 
 import os
@@ -19,7 +19,6 @@ DEPS = SOURCES + ["mk_kernel.cuh", "mk_plan.h", "mk_internal.h", "mk_prefill.h"]
 OP_SOURCES = ["mk_rope.cu", "mk_tree.cu", "mk_kv.cu"]
 OP_DEPS = OP_SOURCES + ["mk_ops.h", "mk_tc.cuh", "mk_tree_attn.cuh"]
 TORCH_SOURCE = "mk_torch.cpp"
-LIB_TORCH = os.path.join(BUILD, "mk_torch.so")
 
 
 def nvcc() -> str:
@@ -34,8 +33,18 @@ def flags() -> list[str]:
             "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", f"-I{os.path.join(ROOT, 'include')}"]
 
 
+def extension_path() -> str:
+    """The extension module for the torch and Python that run this: it unpacks torch's objects, so another torch's
+    or Python's is another file."""
+    import sys
+
+    import torch
+    return os.path.join(BUILD, f"mk_torch.{sys.implementation.cache_tag}.torch-{torch.__version__}."
+                               f"abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}.so")
+
+
 def torch_command(out: str) -> list[str]:
-    """The compiler's command for mk_torch.so, against the torch and Python that run this."""
+    """The compiler's command for the extension module, against the torch and Python that run this."""
     import sysconfig
 
     import torch
@@ -48,37 +57,43 @@ def torch_command(out: str) -> list[str]:
             "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
-def _torch_stale() -> bool:
-    deps = [os.path.join(CSRC, TORCH_SOURCE), os.path.join(ROOT, "include", "mk.h")]
-    return not os.path.exists(LIB_TORCH) or any(os.path.getmtime(d) > os.path.getmtime(LIB_TORCH) for d in deps)
-
-
-def _stale(lib: str) -> bool:
+def _stale(lib: str, sources: list[str]) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, s) for s in DEPS + OP_DEPS] + [os.path.join(ROOT, "include", "mk.h")]
+    deps = [os.path.join(CSRC, s) for s in sources] + [os.path.join(ROOT, "include", "mk.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
     """checked=True builds libmk_checked.so: every device-side access is
-    validated against the registered buffers (slow; for diagnosing faults)."""
+    validated against the registered buffers (slow; for diagnosing faults).
+
+    The library needs neither torch nor Python's headers: without torch it is built
+    alone, and where the extension module does not compile it is there before that is
+    raised."""
     lib = LIB_CHECKED if checked else LIB
     os.makedirs(BUILD, exist_ok=True)
-    ext = None
-    if force or _torch_stale():
-        ext_tmp = LIB_TORCH + f".tmp{os.getpid()}"
+    try:
+        ext = extension_path()
+    except ImportError:
+        ext = None  # (no torch: nothing that the extension module could serve)
+    ext_proc = None
+    if ext and (force or _stale(ext, [TORCH_SOURCE])):
+        ext_tmp = ext + f".tmp{os.getpid()}"
         ext_cmd = torch_command(ext_tmp)
-        ext = subprocess.Popen(ext_cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if force or _stale(lib):
-        _build_lib(lib, verbose, checked)
-    if ext is not None:
-        out, _ = ext.communicate()
-        if ext.returncode:
+        ext_proc = subprocess.Popen(ext_cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    try:
+        if force or _stale(lib, DEPS + OP_DEPS):
+            _build_lib(lib, verbose, checked)
+    finally:
+        if ext_proc is not None:
+            out, _ = ext_proc.communicate()
+    if ext_proc is not None:
+        if ext_proc.returncode:
             print(out.decode(errors="replace"))
             raise RuntimeError(f"compile failed: {' '.join(ext_cmd)}")
-        os.replace(ext_tmp, LIB_TORCH)
+        os.replace(ext_tmp, ext)
     return lib
 
 

@@ -8,7 +8,8 @@
 // not as it should be, or the call wants another device or a stream of its own
 // for its workspace, it does nothing and returns 1, and the Python function says
 // what is wrong or goes the long way. The C ABI's addresses come from the library
-// that _lib.py loaded (bind).
+// that _lib.py loaded (bind). Its file is named after the torch and Python it was
+// compiled against (build.py).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

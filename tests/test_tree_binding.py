@@ -1,12 +1,18 @@
 """The drafted-tree operators' binding and library on the host: refusals and
 loading beside those of test_tree_ops.py."""
 import ctypes
+import os
+import subprocess
+import sys
+import textwrap
 
 import pytest
 
 from decode_megakernel_llama_gb300 import _lib
 from decode_megakernel_llama_gb300.build import build
 from test_tree_ops import tree_args
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -25,3 +31,95 @@ def test_the_binding_has_the_headers_numbers():
     text = open(_lib.HEADER).read()
     for name in ("MK_MAX_TREE", "MK_F32", "MK_BF16"):
         assert f"#define {name} {getattr(_lib, name)}" in text, name
+
+
+def run_fresh(code):
+    """Code in an interpreter of its own, from the repository's root; what it printed."""
+    r = subprocess.run([sys.executable, "-c", textwrap.dedent(code)], cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-3000:]
+    return r.stdout.split()
+
+
+def test_the_library_loads_without_torch_and_without_the_extension(lib):
+    out = run_fresh("""
+        import sys
+        sys.modules["torch"] = None  # (an import of it fails)
+        from decode_megakernel_llama_gb300 import _lib, build
+        for _ in range(2):
+            assert _lib.load().mk_plan_inspect is not None
+        print(build.build() == build.LIB, sys.modules["torch"])
+        for _ in range(2):
+            try:
+                _lib.kv_reorder(None, None, None, None)
+            except ImportError:
+                print("refused")
+    """)
+    assert out == ["True", "None", "refused", "refused"]
+    out = run_fresh("""
+        from decode_megakernel_llama_gb300 import _lib, build
+        build.extension_path = lambda: "/nowhere/mk_torch.so"
+        assert _lib.load().mk_plan_inspect is not None
+        import torch
+        x = torch.zeros(1, 1, 1, 4, 64, dtype=torch.bfloat16)
+        i = torch.zeros(1, dtype=torch.int32)
+        for _ in range(2):
+            try:
+                _lib.kv_reorder(x, x, i, i)
+            except ImportError as e:
+                print("/nowhere" in str(e))
+        print(_lib._quick, _lib.rope_frequencies(64, 1e4)[1])
+    """)
+    assert out == ["True", "True", "None", "1.0"]
+
+
+def test_threads_that_load_at_once(lib):
+    """Sixteen first calls while the module is being loaded: each is answered as a call of CPU tensors is."""
+    out = run_fresh("""
+        import importlib.util, threading, time
+        import torch
+        from decode_megakernel_llama_gb300 import _lib
+        made = importlib.util.module_from_spec
+        def slow(spec):
+            time.sleep(0.3)
+            return made(spec)
+        importlib.util.module_from_spec = slow
+        x = torch.zeros(1, 1, 1, 4, 64, dtype=torch.bfloat16)
+        i = torch.zeros(1, dtype=torch.int32)
+        gate, seen = threading.Barrier(16), []
+        def first():
+            gate.wait()
+            try:
+                _lib.kv_reorder(x, x, i, i)
+            except Exception as e:
+                seen.append(type(e).__name__ + ("CUDA" in str(e)) * "!")
+        threads = [threading.Thread(target=first) for _ in range(16)]
+        [t.start() for t in threads], [t.join() for t in threads]
+        print(*seen)
+    """)
+    assert out == ["MKError!"] * 16
+
+
+def test_the_extension_belongs_to_one_torch_and_python(lib, monkeypatch):
+    import torch
+
+    from decode_megakernel_llama_gb300 import build as mkbuild
+    here = mkbuild.extension_path()
+    assert os.path.exists(here) and not mkbuild._stale(here, [mkbuild.TORCH_SOURCE])
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    other = mkbuild.extension_path()
+    assert other != here and mkbuild._stale(other, [mkbuild.TORCH_SOURCE])
+    monkeypatch.undo()
+    assert mkbuild.extension_path() == here
+
+
+def test_an_extension_that_does_not_compile_leaves_the_library(lib, monkeypatch, tmp_path):
+    """The library is there (and up to date) before the failure is raised, and no half-made file beside it."""
+    from decode_megakernel_llama_gb300 import build as mkbuild
+    done = []
+    monkeypatch.setattr(mkbuild, "extension_path", lambda: str(tmp_path / "x.so"))
+    monkeypatch.setattr(mkbuild, "torch_command", lambda out: ["false"])
+    monkeypatch.setattr(mkbuild, "_build_lib", lambda *a: done.append(a))
+    monkeypatch.setattr(mkbuild, "LIB", str(tmp_path / "libmk.so"))
+    with pytest.raises(RuntimeError, match="compile failed"):
+        mkbuild.build()
+    assert len(done) == 1 and not list(tmp_path.iterdir())
