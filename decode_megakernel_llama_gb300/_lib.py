@@ -438,8 +438,7 @@ def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None
     (zeroed by the caller) that becomes 1 if a bounded in-kernel wait ran out, after wait_ns nanoseconds (0: 2e9); the
     rows concerned are then NaN. The workspace of long caches comes from torch's allocator, on the call's stream."""
     quick = _quick or load_extension()
-    rc = quick.tree_attention(q, k_cache, v_cache, lengths, masks, out,
-                              q.shape[-1] ** -0.5 if scale is None else scale, counts, slots, max_len, status, stream,
+    rc = quick.tree_attention(q, k_cache, v_cache, lengths, masks, out, scale, counts, slots, max_len, status, stream,
                               wait_ns)
     if rc == MK_OK:
         return
@@ -452,6 +451,8 @@ def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None
         _bad("q and k_cache must have 4 dimensions")
     B, T, Hq, hd = q.shape
     n_slots, Hkv, S, _ = k_cache.shape
+    if scale is None:
+        scale = max(hd, 1) ** -0.5
     d, per_seq = q.get_device(), (B,)
     if not (out.dtype is q.dtype and out.shape == q.shape and k_cache.dtype is bf and v_cache.dtype is bf
             and k_cache.shape[3] == hd and v_cache.shape == k_cache.shape and lengths.dtype is i32
@@ -475,7 +476,7 @@ def tree_attention(q, k_cache, v_cache, lengths, masks, out, scale: float | None
     if qs[3] != 1 or os[3] != 1 or (Hq > 1 and (qs[2] != hd or os[2] != hd)):
         _bad("the heads of a node must be contiguous in q and out")
     row = Hq * hd
-    rec = [B, T, Hq, Hkv, hd, dt, n_slots, S, max_len, hd ** -0.5 if scale is None else scale, qs[0] if B > 1 else 0,
+    rec = [B, T, Hq, Hkv, hd, dt, n_slots, S, max_len, scale, qs[0] if B > 1 else 0,
            qs[1] if T > 1 else row, os[0] if B > 1 else 0, os[1] if T > 1 else row, q.data_ptr(), out.data_ptr(),
            k_cache.data_ptr(), v_cache.data_ptr(), lengths.data_ptr(), 0 if counts is None else counts.data_ptr(),
            0 if slots is None else slots.data_ptr(), masks.data_ptr(), 0, 0,

@@ -13,6 +13,8 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <cmath>
+
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -100,7 +102,7 @@ long rope_append(PyObject *const *o, Py_ssize_t n_args) {
     return mk.rope(&a, s);
 }
 
-// q, k_cache, v_cache, lengths, masks, out, scale (0: 1 / sqrt(hd)), counts, slots, max_len, status, stream, wait_ns
+// q, k_cache, v_cache, lengths, masks, out, scale (None: 1 / sqrt(hd)), counts, slots, max_len, status, stream, wait_ns
 long tree_attention(PyObject *const *o, Py_ssize_t n_args) {
     if (n_args != 13) return kNotHere;
     const at::Tensor *q = tensor(o[0]), *k = tensor(o[1]), *v = tensor(o[2]), *out = tensor(o[5]);
@@ -119,7 +121,7 @@ long tree_attention(PyObject *const *o, Py_ssize_t n_args) {
         k->size(1) > INT32_MAX || S > INT32_MAX || !stream_of(d, o[11], &s))
         return kNotHere;
     mk_tree_args a{};
-    const double scale = PyFloat_AsDouble(o[6]);
+    const double scale = o[6] == Py_None ? 1.0 / std::sqrt((double)hd) : PyFloat_AsDouble(o[6]);
     const long max_len = PyLong_AsLong(o[9]);
     const long long wait_ns = PyLong_AsLongLong(o[12]);
     if (PyErr_Occurred() || max_len < 0 || max_len > INT32_MAX) {

@@ -123,3 +123,11 @@ def test_an_extension_that_does_not_compile_leaves_the_library(lib, monkeypatch,
     with pytest.raises(RuntimeError, match="compile failed"):
         mkbuild.build()
     assert len(done) == 1 and not list(tmp_path.iterdir())
+
+
+def test_heads_of_no_elements_are_refused():
+    import torch
+    q, k = torch.zeros(1, 1, 2, 0), torch.zeros(1, 1, 8, 0, dtype=torch.bfloat16)
+    n, m = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int64)
+    with pytest.raises(_lib.MKError):
+        _lib.tree_attention(q, k, k.clone(), n, m, q.clone())
