@@ -114,6 +114,12 @@ int check_cache(const char *who, const void *k, const void *v, int L, int B, int
     return MK_OK;
 }
 
+// (kv_reorder's CTAs take K or V: a shared row would move twice)
+bool caches_meet(const void *k, const void *v, int L, int B, int Hkv, int max_seq, int hd) {
+    const int64_t bytes = 2 * (int64_t)L * B * Hkv * max_seq * hd;
+    return meet(k, bytes, v, bytes);
+}
+
 }  // namespace
 }  // namespace mkops
 
@@ -128,6 +134,8 @@ extern "C" int mk_kv_compact(void *k, void *v, int32_t n_layers, int32_t slots, 
         return set_error(MK_ERR_INVALID_ARG, "mk_kv_compact: a required pointer is NULL");
     if (nodes_per_slot < 1 || nodes_per_slot > mkops::kMaxNodes)
         return set_error(MK_ERR_INVALID_ARG, "mk_kv_compact: nodes_per_slot outside [1, MK_MAX_TREE]");
+    if (mkops::caches_meet(k, v, n_layers, slots, n_kv_heads, max_seq, head_dim))
+        return set_error(MK_ERR_INVALID_ARG, "mk_kv_compact: k and v overlap");
     const dim3 grid(n_layers * n_kv_heads, slots);
     uint16_t *kc = static_cast<uint16_t *>(k), *vc = static_cast<uint16_t *>(v);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -148,6 +156,8 @@ extern "C" int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, 
     if (!d_sources || !d_lengths)
         return set_error(MK_ERR_INVALID_ARG, "mk_kv_reorder: a required pointer is NULL");
     if (slots > 64) return set_error(MK_ERR_UNSUPPORTED, "mk_kv_reorder: more than 64 slots");
+    if (mkops::caches_meet(k, v, n_layers, slots, n_kv_heads, max_seq, head_dim))
+        return set_error(MK_ERR_INVALID_ARG, "mk_kv_reorder: k and v overlap");
     const int planes = 2 * n_layers * n_kv_heads;
     const int64_t chunks = (int64_t)max_seq * head_dim / 8;
     int64_t per = (chunks + mkops::kT - 1) / mkops::kT;

@@ -54,6 +54,12 @@ inline cudaError_t launch_op(void (*kernel)(KArgs...), dim3 grid, int threads, i
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// Whether two ranges of bytes share one.
+inline bool meet(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y ? y - x < (uint64_t)a_bytes : x - y < (uint64_t)b_bytes;
+}
+
 // Sets the calling thread's error text from a CUDA error; returns MK_ERR_CUDA.
 int cuda_error(cudaError_t e, const char *what);
 

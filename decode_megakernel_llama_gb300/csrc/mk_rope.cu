@@ -291,6 +291,25 @@ extern "C" int mk_rope_append(const mk_rope_args *a, void *stream) {
     if ((io & 15u) || (cache & 7u) || (reinterpret_cast<uintptr_t>(a->inv_freq) & 7u))
         return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: a pointer is not aligned");
     if (a->n == 0) return MK_OK;
+    // What one CTA writes no other may read or write: the caches apart from everything,
+    // q_out from qkv but for the same rows in place, or rows in the gaps between qkv's.
+    const int64_t e = a->dtype == MK_F32 ? 4 : 2, q_bytes = ((a->n - 1) * a->q_stride + q) * e,
+                  qkv_bytes = ((a->n - 1) * a->qkv_stride + qkv) * e,
+                  cache_bytes = 2 * (int64_t)a->slots * a->n_kv_heads * a->max_seq * a->head_dim;
+    using mkops::meet;
+    if (meet(a->k_cache, cache_bytes, a->v_cache, cache_bytes) || meet(a->k_cache, cache_bytes, a->q_out, q_bytes) ||
+        meet(a->v_cache, cache_bytes, a->q_out, q_bytes) || meet(a->k_cache, cache_bytes, a->qkv, qkv_bytes) ||
+        meet(a->v_cache, cache_bytes, a->qkv, qkv_bytes))
+        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: a cache overlaps the other, qkv or q_out");
+    if (meet(a->q_out, q_bytes, a->qkv, qkv_bytes)) {
+        const int64_t step = a->qkv_stride * e;
+        int64_t off = (int64_t)(reinterpret_cast<uintptr_t>(a->q_out) - reinterpret_cast<uintptr_t>(a->qkv));
+        const bool same_rows = a->n == 1 || a->q_stride == a->qkv_stride;
+        const bool in_place = off == 0 && same_rows;
+        off = (off % step + step) % step;
+        if (!in_place && !(same_rows && a->n > 1 && off >= qkv * e && off + q * e <= step))
+            return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: q_out overlaps qkv other than row by row in place");
+    }
     mkops::RopeArgs r{};
     r.n = a->n, r.Hq = a->n_heads, r.Hkv = a->n_kv_heads, r.rot = a->rot, r.interleaved = a->interleaved;
     r.slots = a->slots, r.max_seq = a->max_seq, r.eps = a->eps, r.mscale = a->mscale;
@@ -299,9 +318,9 @@ extern "C" int mk_rope_append(const mk_rope_args *a, void *stream) {
     r.kc = static_cast<uint16_t *>(a->k_cache), r.vc = static_cast<uint16_t *>(a->v_cache);
     r.positions = a->positions, r.rows = a->rows, r.slot_of = a->slot_of, r.inv_freq = a->inv_freq;
     r.q_norm = static_cast<const uint16_t *>(a->q_norm), r.k_norm = static_cast<const uint16_t *>(a->k_norm);
-    const cudaError_t e =
+    const cudaError_t err =
         mkops::rope_append_launch(r, a->head_dim, a->dtype == MK_F32, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? MK_OK : mkops::cuda_error(e, "mk_rope_append");
+    return err == cudaSuccess ? MK_OK : mkops::cuda_error(err, "mk_rope_append");
 }
 
 extern "C" int mk_rope_frequencies(int32_t kind, int32_t rot, double theta, double factor, double original_len,

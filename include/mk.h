@@ -450,7 +450,8 @@ int mk_twell_ffn(const void *d_w_gate, const void *d_w_up, const void *d_w_down_
  * over the pairs (x'_i, x'_{i + rot/2}), or with `interleaved` (x'_{2i},
  * x'_{2i+1}), of the first rot elements; the others pass through. Rotated
  * queries go to q_out (dtype, [n][n_heads][head_dim], token stride q_stride;
- * it may be qkv itself with the same stride), rotated keys and the values,
+ * it may be qkv itself with the same stride, or lie in the gaps between its
+ * rows; any other overlap, and one of the caches, is refused), rotated keys and the values,
  * rounded to nearest bf16, to cache row rows[t] of slot slot_of[t] (0 with
  * slot_of NULL). A row outside [0, max_seq) or slot outside [0, slots) is
  * not written (its query still is); two tokens of one call must not name
@@ -566,7 +567,7 @@ int mk_tree_accept(const int32_t *tokens, const int32_t *parents, const int32_t 
  * nodes[b][i] (keys and values) moves to row starts[b] + i, all as if at
  * once. k, v: bf16 [n_layers][slots][n_kv_heads][max_seq][head_dim]; d_starts,
  * d_counts device int32 [slots], d_nodes device int32 [slots][nodes_per_slot],
- * nodes_per_slot <= MK_MAX_TREE. A negative node, or one that leads out of
+ * nodes_per_slot <= MK_MAX_TREE. k and v must not overlap. A negative node, or one that leads out of
  * the cache, moves nothing; a slot with count 0 is left as it is. */
 int mk_kv_compact(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_kv_heads, int32_t max_seq,
                   int32_t head_dim, int32_t nodes_per_slot, const int32_t *d_starts, const int32_t *d_nodes,
@@ -576,7 +577,8 @@ int mk_kv_compact(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_k
  * what slot d_sources[b] held before the call, all slots as if at once, so
  * slots can be forked, exchanged and rotated in place (beams, parallel
  * samples). A slot whose source is itself or outside [0, slots), and rows
- * from d_lengths[b] on, are left as they are. At most 64 slots. */
+ * from d_lengths[b] on, are left as they are. At most 64 slots; k and v must not
+ * overlap. */
 int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_kv_heads, int32_t max_seq,
                   int32_t head_dim, const int32_t *d_sources, const int32_t *d_lengths, void *stream);
 

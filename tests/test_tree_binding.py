@@ -125,6 +125,34 @@ def test_an_extension_that_does_not_compile_leaves_the_library(lib, monkeypatch,
     assert len(done) == 1 and not list(tmp_path.iterdir())
 
 
+K, V, X, Q = (1 << n for n in (30, 31, 32, 33))  # aligned addresses far from one another, that nothing may follow
+
+
+@pytest.mark.parametrize("bad", [
+    dict(v_cache=K), dict(v_cache=K + 2 * 16 * 2 * 64 - 16), dict(k_cache=V + 1024), dict(q_out=K + 64), dict(q_out=V - 16),
+    dict(qkv=K), dict(k_cache=X + 3 * 2048), dict(q_out=X, q_stride=256), dict(q_out=X + 16, q_stride=512),
+    dict(q_out=X + 2048, q_stride=512), dict(q_out=X - 2048, q_stride=512), dict(q_out=X + 2048 - 16, q_stride=512),
+    dict(q_out=X + 2048, qkv_stride=800, q_stride=804), dict(q_out=X + 2048, qkv_stride=764, q_stride=764),
+    dict(q_out=X + 2032, qkv_stride=800, q_stride=800), dict(q_out=X - 1008, qkv_stride=800, q_stride=800),
+    dict(n=1, q_out=X + 16), dict(n=1, q_out=X - 16),
+])
+def test_rope_append_refuses_what_overlaps(lib, bad):
+    """Four tokens of 4 + 2 + 2 heads of 64 in fp32: rows of qkv of 2,048 bytes, of q_out of 1,024."""
+    from test_tree_ops import rope_args
+    a = rope_args(**{**dict(k_cache=K, v_cache=V, qkv=X, q_out=Q), **bad})
+    assert lib.mk_rope_append(ctypes.byref(a), None) == _lib.MK_ERR_INVALID_ARG
+    assert b"overlap" in lib.mk_last_error()
+
+
+def test_cache_moves_refuse_caches_that_overlap(lib):
+    size = 2 * 2 * 2 * 2 * 64 * 64  # bytes of [2][2][2][64][64]
+    for v in (K, K + 16, K + size - 16, K - size + 16):
+        assert lib.mk_kv_compact(K, v, 2, 2, 2, 64, 64, 8, X, X, X, None) == _lib.MK_ERR_INVALID_ARG
+        assert b"overlap" in lib.mk_last_error()
+        assert lib.mk_kv_reorder(K, v, 2, 2, 2, 64, 64, X, X, None) == _lib.MK_ERR_INVALID_ARG
+        assert b"overlap" in lib.mk_last_error()
+
+
 def test_heads_of_no_elements_are_refused():
     import torch
     q, k = torch.zeros(1, 1, 2, 0), torch.zeros(1, 1, 8, 0, dtype=torch.bfloat16)
