@@ -161,7 +161,7 @@ extern "C" int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, 
     const int planes = 2 * n_layers * n_kv_heads;
     const int64_t chunks = (int64_t)max_seq * head_dim / 8;
     int64_t per = (chunks + mkops::kT - 1) / mkops::kT;
-    const int64_t want = (152 * 16 + planes - 1) / planes;
+    const int64_t want = (mkops::sm_count() * 16 + planes - 1) / planes;
     if (per > want) per = want;
     const dim3 grid((unsigned)per, planes);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

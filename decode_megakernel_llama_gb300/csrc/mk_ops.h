@@ -60,6 +60,9 @@ inline bool meet(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
     return x < y ? y - x < (uint64_t)a_bytes : x - y < (uint64_t)b_bytes;
 }
 
+// SMs of the GPU (of the device that is current at the first call: a machine's are alike).
+int sm_count();
+
 // Sets the calling thread's error text from a CUDA error; returns MK_ERR_CUDA.
 int cuda_error(cudaError_t e, const char *what);
 

@@ -35,7 +35,7 @@ namespace {
 constexpr int kT = 256;  // threads per CTA
 constexpr int kW = kT / 32;
 constexpr int kMaxHalf = 64;  // rotated pairs of a head
-constexpr int kSpread = 456;  // CTAs that the GPU holds at once of the form for fewer tokens: three an SM
+constexpr int kPerSm = 3;     // CTAs of the form for fewer tokens that an SM holds
 
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p);
@@ -69,7 +69,7 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t *p, float4 v) {
 // share a norm's shuffles, a head's tests and its addresses, and the reciprocal root
 // as one instruction.)
 template <typename T, int HD, int TPB, int E>
-__global__ void __launch_bounds__(kT, TPB == 1 && E == 8 ? 3 : 4) rope_append(const RopeArgs a) {
+__global__ void __launch_bounds__(kT, TPB == 1 && E == 8 ? kPerSm : 4) rope_append(const RopeArgs a) {
     constexpr int LPH = HD / E;    // lanes of a head
     constexpr int HPW = 32 / LPH;  // heads of a warp
     constexpr int B = 16 / E;      // a warp's heads in flight, HPW each
@@ -252,8 +252,9 @@ cudaError_t rope_append_launch(const RopeArgs &a, int hd, bool f32, cudaStream_t
     // 6.5 us, 7.8 as many, and 1,000, more than two waves, 8.6 and 7.8). A few, where
     // latency counts: four elements a lane (one token: 1.75 us, 1.9 with eight).
     const int per_cta = kW * (hd == 64 ? 2 : 1), rounds = (a.Hq + 2 * a.Hkv + per_cta - 1) / per_cta;
-    const bool many = a.n > 2 * kSpread, few = a.n <= 32;
-    const int spread = std::max(1, std::min({rounds, 8, kSpread / a.n}));
+    const int at_once = kPerSm * sm_count();
+    const bool many = a.n > 2 * at_once, few = a.n <= 32;
+    const int spread = std::max(1, std::min({rounds, 8, at_once / a.n}));
     const dim3 grid(many ? (a.n + 3) / 4 : a.n, many ? 1 : spread);
     auto go = [&](auto kernel) { return launch_op(kernel, grid, kT, 0, 0, s, a); };
     auto pick = [&](auto four, auto one, auto one4) { return many ? go(four) : few ? go(one4) : go(one); };

@@ -8,9 +8,8 @@
 
 namespace mktc {
 
-// One lane of a converged warp. (Inside its branch ptxas keeps the operands of
-// TMA and MMA instructions in uniform registers; behind `lane == 0` it moves
-// each of them there first, and a chain of 8 MMAs took ~960 cycles to issue.)
+// One lane of a converged warp, the same one at every call. (A chain of 8 MMAs took
+// ~360 cycles behind it, ~960 behind `lane == 0`.)
 __device__ __forceinline__ bool elect() {
     uint32_t p;
     asm volatile(

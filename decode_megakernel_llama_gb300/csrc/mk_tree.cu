@@ -52,6 +52,19 @@ __global__ void __launch_bounds__(32) tree_masks(const int32_t *__restrict__ par
 
 }  // namespace
 
+int sm_count() {
+    static const int n = [] {
+        int dev = 0, sms = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+            (void)cudaGetLastError();
+            sms = 152;
+        }
+        return sms;
+    }();
+    return n;
+}
+
 int cuda_error(cudaError_t e, const char *what) {
     char text[256];
     snprintf(text, sizeof text, "%s: %s", what, cudaGetErrorString(e));
@@ -311,34 +324,24 @@ mkops::TreeArgs tree_of(const mk_tree_args *a) {
     return t;
 }
 
-cudaError_t device_sms(int *n_sm) {
-    int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    return e == cudaSuccess ? cudaDeviceGetAttribute(n_sm, cudaDevAttrMultiProcessorCount, dev) : e;
-}
-
 }  // namespace
 
 extern "C" int mk_tree_attention(const mk_tree_args *a, void *stream) {
     const int rc = check_tree(a);
     if (rc || a->batch == 0) return rc;
-    int n_sm = 0;
-    cudaError_t e = device_sms(&n_sm);
-    if (e == cudaSuccess)
-        e = mkops::tree_attention_launch(tree_of(a), a->head_dim, a->dtype == MK_F32,
-                                         a->max_len ? a->max_len : a->max_seq, n_sm, static_cast<cudaStream_t>(stream));
+    const cudaError_t e =
+        mkops::tree_attention_launch(tree_of(a), a->head_dim, a->dtype == MK_F32, a->max_len ? a->max_len : a->max_seq,
+                                     mkops::sm_count(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MK_OK : mkops::cuda_error(e, "mk_tree_attention");
 }
 
 extern "C" int64_t mk_tree_attention_workspace(const mk_tree_args *a) {
     const int rc = check_tree(a);
     if (rc || a->batch == 0) return rc;
-    int n_sm = 0;
     int64_t floats = 0;
-    cudaError_t e = device_sms(&n_sm);
-    if (e == cudaSuccess)
-        e = mkops::tree_attention_work_floats(tree_of(a), a->head_dim, a->dtype == MK_F32,
-                                              a->max_len ? a->max_len : a->max_seq, n_sm, &floats);
+    const cudaError_t e =
+        mkops::tree_attention_work_floats(tree_of(a), a->head_dim, a->dtype == MK_F32,
+                                          a->max_len ? a->max_len : a->max_seq, mkops::sm_count(), &floats);
     return e == cudaSuccess ? floats * 4 : mkops::cuda_error(e, "mk_tree_attention_workspace");
 }
 
