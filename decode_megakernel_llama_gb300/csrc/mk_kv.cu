@@ -2,8 +2,10 @@
 // path of a drafted tree, behind the committed rows) and mk_kv_reorder (slots
 // copied, forked and exchanged).
 //
-// Both are pure copies: what bounds them is the memory's rate, each moved row
-// read once and written once. The one thing to get right is that sources and
+// Both are pure copies: their floor is the memory's rate, each moved row read once
+// and written once (reorder: 2,000 rows of 6 of 8 slots, 16 layers, 620 MB, 101 us =
+// 6.1 TB/s; compact, whose rows are few and mostly in L2, is bound by three dependent
+// loads: 8 x 40 rows of 28 layers, 73 MB, 13.7 us). The one thing to get right is that sources and
 // targets overlap, so every thread has all its loads behind it before the
 // first store that could touch another's source:
 //   compact: one CTA holds all moved rows of one (layer, slot, head), K and V,

@@ -12,8 +12,11 @@
 // cosine are taken in 32, so a far position loses nothing: a turn's fraction
 // is off by at most p * 2^-53 turns.
 //
-// What bounds it: memory. Each element is read once and written once; the
-// arithmetic is a few operations an element. A CTA takes one token (or four): its
+// What bounds it: the floor is memory, as each element is read once and written once and
+// the arithmetic is a few operations an element; a long prompt takes 1.18 times its
+// bytes' time (8,192 tokens of 48 heads of 64, fp32, normed: 32.7 us, DRAM 53 % and issue
+// slots 40 % busy, 43 % of the warps: the latency of the loads), a few tokens the time of
+// their dependent round trips. A CTA takes one token (or four): its
 // threads form the token's sines and cosines once for all heads (shared memory)
 // while every warp's first loads are already in flight; a head is held by hd/4
 // lanes of a warp, four elements a lane, or by hd/8, four elements of each half, so
