@@ -281,7 +281,8 @@ int mk_get_status(mk_handle *h);
 
 /* Bounded-wait limit for in-kernel dependency waits, in nanoseconds
  * (default 2e9): those of the decode steps and of mk_verify's attention.
- * Host-only setting, takes effect on the next step or tree.
+ * Host-only setting, takes effect on the next step or tree; a captured graph
+ * keeps the limit of its capture.
  * Source: as mk_get_status (the synchronisation paragraph's in-kernel
  * waits); the limit itself is this library's convention. */
 int mk_set_wait_timeout(mk_handle *h, uint64_t timeout_ns);
@@ -451,7 +452,8 @@ int mk_twell_ffn(const void *d_w_gate, const void *d_w_up, const void *d_w_down_
  * x'_{2i+1}), of the first rot elements; the others pass through. Rotated
  * queries go to q_out (dtype, [n][n_heads][head_dim], token stride q_stride;
  * it may be qkv itself with the same stride, or lie in the gaps between its
- * rows; any other overlap, and one of the caches, is refused), rotated keys and the values,
+ * rows; any other overlap, and one of the caches, is refused), rotated keys and
+ * the values,
  * rounded to nearest bf16, to cache row rows[t] of slot slot_of[t] (0 with
  * slot_of NULL). A row outside [0, max_seq) or slot outside [0, slots) is
  * not written (its query still is); two tokens of one call must not name
@@ -567,7 +569,8 @@ int mk_tree_accept(const int32_t *tokens, const int32_t *parents, const int32_t 
  * nodes[b][i] (keys and values) moves to row starts[b] + i, all as if at
  * once. k, v: bf16 [n_layers][slots][n_kv_heads][max_seq][head_dim]; d_starts,
  * d_counts device int32 [slots], d_nodes device int32 [slots][nodes_per_slot],
- * nodes_per_slot <= MK_MAX_TREE. k and v must not overlap. A negative node, or one that leads out of
+ * nodes_per_slot <= MK_MAX_TREE. k and v must not overlap. A negative node, or
+ * one that leads out of
  * the cache, moves nothing; a slot with count 0 is left as it is. */
 int mk_kv_compact(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_kv_heads, int32_t max_seq,
                   int32_t head_dim, int32_t nodes_per_slot, const int32_t *d_starts, const int32_t *d_nodes,
