@@ -24,7 +24,7 @@ MK_ERR_UNSUPPORTED = -4
 MK_ERR_TIMEOUT = -5
 MK_ERR_NOMEM = -6
 MK_INSTR_WORDS = 16
-MK_F32, MK_BF16 = 0, 1
+MK_F32, MK_BF16, MK_E4M3 = 0, 1, 2
 MK_MAX_TREE = 64
 ROPE_KINDS = {"none": 0, "linear": 1, "base": 2, "wavelength": 3, "yarn": 4}
 
@@ -78,10 +78,29 @@ class mk_tree_args(ctypes.Structure):
                 + [("workspace_bytes", ctypes.c_int64), ("status", ctypes.c_void_p), ("wait_ns", ctypes.c_int64)])
 
 
-# The same two as one packed record each (native layout): filling a ctypes
+class mk_paged_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_tokens", "batch", "max_pages", "n_heads", "n_kv_heads", "head_dim",
+                                               "dtype", "cache_dtype", "n_pages", "page_size", "max_new", "max_len",
+                                               "window", "sinks")]
+                + [("scale", ctypes.c_float), ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+                + [(n, ctypes.c_void_p) for n in ("q", "out", "k_pages", "v_pages", "k_scales", "v_scales", "table",
+                                                  "starts", "lengths", "workspace")]
+                + [("workspace_bytes", ctypes.c_int64), ("status", ctypes.c_void_p), ("wait_ns", ctypes.c_int64)])
+
+
+class mk_pages_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_layers", "slots", "n_kv_heads", "max_seq", "head_dim", "n_pages",
+                                               "page_size", "cache_dtype", "batch", "max_pages")]
+                + [(n, ctypes.c_void_p) for n in ("k", "v", "k_pages", "v_pages", "k_scales", "v_scales", "table",
+                                                  "lengths", "first", "slot_of")])
+
+
+# The same as one packed record each (native layout): filling a ctypes
 # structure field by field costs more than the launch it is for.
 _ROPE_ARGS = struct.Struct("@9i2f2q10P")
 _TREE_ARGS = struct.Struct("@9if4q9PqPq")
+_PAGED_ARGS = struct.Struct("@14if2q10PqPq")
+_PAGES_ARGS = struct.Struct("@10i10P")
 
 
 _lib = None
@@ -149,6 +168,12 @@ def _load(path: str | None):
     L.mk_tree_accept.argtypes = [_VP, _VP, _VP, _I32, _VP]
     L.mk_kv_compact.argtypes = [_VP, _VP] + [_I32] * 6 + [_VP] * 4
     L.mk_kv_reorder.argtypes = [_VP, _VP] + [_I32] * 5 + [_VP] * 3
+    L.mk_paged_attention.argtypes = [_VP, _VP]
+    L.mk_paged_attention_workspace.argtypes = [_VP]
+    L.mk_paged_attention_workspace.restype = ctypes.c_int64
+    L.mk_rope_append_e4m3.argtypes = [_VP] * 4
+    L.mk_kv_write_pages.argtypes = [_VP, _VP]
+    L.mk_kv_read_pages.argtypes = [_VP, _VP]
     L.mk_destroy.argtypes = [_VP]
     L.mk_destroy.restype = None
     return L
@@ -575,6 +600,160 @@ def kv_reorder(k, v, sources, lengths, stream=None) -> None:
     _check_caches(torch, k, v, shape, ((sources, "sources", (B,)), (lengths, "lengths", (B,))))
     _run_on(torch, k.get_device(), stream, load().mk_kv_reorder, k.data_ptr(), v.data_ptr(), L, B, Hkv, S, hd,
             sources.data_ptr(), lengths.data_ptr())
+
+
+def _pool(torch, k_pages, v_pages, k_scales, v_scales, lead: int) -> int:
+    """Checks a pool of pages ([pages][Hkv][rows][hd] behind `lead` dimensions) and its scales; its type."""
+    e4m3 = torch.float8_e4m3fn
+    if k_pages.dim() != 4 + lead:
+        _bad(f"k_pages must have {4 + lead} dimensions")
+    if k_pages.dtype not in (torch.bfloat16, e4m3):
+        _bad(f"k_pages must be bfloat16 or float8_e4m3fn, not {k_pages.dtype}")
+    q8 = k_pages.dtype is e4m3
+    _need(k_pages, "k_pages", k_pages.dtype, k_pages.shape, k_pages)
+    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape, k_pages)
+    if (k_scales is not None) != q8 or (v_scales is not None) != q8:
+        _bad("float8_e4m3fn pages need k_scales and v_scales, bfloat16 pages none")
+    if q8:
+        shape = (*k_pages.shape[:-1], k_pages.shape[-1] // 32)
+        _need(k_scales, "k_scales", torch.uint8, shape, k_pages)
+        _need(v_scales, "v_scales", torch.uint8, shape, k_pages)
+    return MK_E4M3 if q8 else MK_BF16
+
+
+def _at(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def paged_attention(q, k_pages, v_pages, table, starts, lengths, out, scale: float | None = None, window: int = 0,
+                    sinks: int = 0, k_scales=None, v_scales=None, max_new: int = 0, max_len: int = 0, status=None,
+                    stream=None, wait_ns: int = 0) -> None:
+    """mk_paged_attention on CUDA tensors: q and out [n][Hq][hd] float32 or bfloat16 (token strides free), k_pages /
+    v_pages bfloat16 [pages][Hkv][rows][hd] (one layer), or float8_e4m3fn with k_scales / v_scales uint8
+    [pages][Hkv][rows][hd / 32]; table int32 [B][pages of a sequence], starts int32 [B + 1] (sequence b has tokens
+    starts[b] .. starts[b + 1] - 1 of q), lengths int32 [B] (its rows, the new tokens' own among them). A token sees
+    the rows up to its own, with a window the last `window` of them and the first `sinks`. scale defaults to
+    1 / sqrt(hd). max_new, max_len: bounds on a sequence's tokens and rows, for the choice of the launch alone.
+    status, wait_ns and the workspace: as in tree_attention."""
+    import torch
+    i32, dt = torch.int32, _io_dtype(torch, q, "q")
+    if q.dim() != 3 or table.dim() != 2:
+        _bad("q must have 3 dimensions, table 2")
+    cache = _pool(torch, k_pages, v_pages, k_scales, v_scales, 0)
+    n, Hq, hd = q.shape
+    P, Hkv, ps, kd = k_pages.shape
+    B, M = table.shape
+    if kd != hd:
+        _bad(f"pages of heads of {kd}, queries of {hd}")
+    _need(out, "out", q.dtype, (n, Hq, hd), q, False)
+    _need(k_pages, "k_pages", k_pages.dtype, k_pages.shape, q)
+    _need(table, "table", i32, (B, M), q)
+    _need(starts, "starts", i32, (B + 1,), q)
+    _need(lengths, "lengths", i32, (B,), q)
+    if status is not None:
+        _need(status, "status", i32, (1,), q)
+    if scale is None:
+        scale = max(hd, 1) ** -0.5
+    if n == 0 or B == 0:
+        return
+    qs, os = q.stride(), out.stride()
+    if qs[2] != 1 or os[2] != 1 or (Hq > 1 and (qs[1] != hd or os[1] != hd)):
+        _bad("the heads of a token must be contiguous in q and out")
+    row, d = Hq * hd, q.get_device()
+    if not all(0 <= x < 1 << 31 for x in (window, sinks, max_new, max_len)):
+        _bad("window, sinks, max_new or max_len outside [0, 2^31)")
+    rec = [n, B, M, Hq, Hkv, hd, dt, cache, P, ps, max_new, max_len, window, sinks, scale, qs[0] if n > 1 else row,
+           os[0] if n > 1 else row, q.data_ptr(), out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _at(k_scales),
+           _at(v_scales), table.data_ptr(), starts.data_ptr(), lengths.data_ptr(), 0, 0, _at(status), wait_ns]
+    L, work = load(), None
+    if d >= 0:
+        with torch.cuda.device(d):
+            size = L.mk_paged_attention_workspace(_PAGED_ARGS.pack(*rec))
+            if size < 0:
+                check(size)
+            if size > 0:
+                with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(d)):
+                    work = torch.empty(size, dtype=torch.uint8, device=q.device)
+                rec[26], rec[27] = work.data_ptr(), size
+    _run_on(torch, d, stream, L.mk_paged_attention, _PAGED_ARGS.pack(*rec))
+
+
+def rope_append_e4m3(qkv, q_out, k_pages, v_pages, k_scales, v_scales, positions, rows, inv_freq, slots=None,
+                     q_norm=None, k_norm=None, eps: float = 1e-5, mscale: float = 1.0, interleaved: bool = False,
+                     stream=None) -> None:
+    """mk_rope_append_e4m3 on CUDA tensors: rope_append with 8-bit caches, k_pages / v_pages float8_e4m3fn
+    [slots][Hkv][rows][hd] with k_scales / v_scales uint8 [slots][Hkv][rows][hd / 32]. With a pool of pages slots are
+    the tokens' pages, rows their rows in them."""
+    import torch
+    bf, i32, dt = torch.bfloat16, torch.int32, _io_dtype(torch, qkv, "qkv")
+    if k_pages.dim() != 4 or q_out.dim() != 3 or qkv.dim() != 2 or inv_freq.dim() != 1:
+        _bad("qkv, q_out, k_pages, inv_freq must have 2, 3, 4, 1 dimensions")
+    if k_pages.dtype is not torch.float8_e4m3fn:
+        _bad(f"k_pages must be float8_e4m3fn, not {k_pages.dtype} (rope_append takes bfloat16)")
+    _pool(torch, k_pages, v_pages, k_scales, v_scales, 0)
+    B, Hkv, S, hd = k_pages.shape
+    n, Hq, _ = q_out.shape
+    half = inv_freq.shape[0]
+    for t, what, dtype, shape, dense in (
+            (qkv, "qkv", qkv.dtype, (n, (Hq + 2 * Hkv) * hd), False), (q_out, "q_out", qkv.dtype, (n, Hq, hd), False),
+            (k_pages, "k_pages", k_pages.dtype, (B, Hkv, S, hd), True), (positions, "positions", i32, (n,), True),
+            (rows, "rows", i32, (n,), True), (inv_freq, "inv_freq", torch.float64, (half,), True)):
+        _need(t, what, dtype, shape, qkv, dense)
+    for t, what, dtype, shape in ((slots, "slots", i32, (n,)), (q_norm, "q_norm", bf, (hd,)), (k_norm, "k_norm", bf, (hd,))):
+        if t is not None:
+            _need(t, what, dtype, shape, qkv)
+    if n == 0:
+        return
+    ts, qs = qkv.stride(), q_out.stride()
+    if ts[1] != 1 or qs[2] != 1 or (Hq > 1 and qs[1] != hd):
+        _bad("the heads of a token must be contiguous in qkv and q_out")
+    width = (Hq + 2 * Hkv) * hd
+    rec = _ROPE_ARGS.pack(n, Hq, Hkv, hd, 2 * half, 1 if interleaved else 0, dt, B, S, eps, mscale,
+                          ts[0] if n > 1 else width, qs[0] if n > 1 else Hq * hd, qkv.data_ptr(), q_out.data_ptr(),
+                          k_pages.data_ptr(), v_pages.data_ptr(), positions.data_ptr(), rows.data_ptr(), _at(slots),
+                          inv_freq.data_ptr(), _at(q_norm), _at(k_norm))
+    _run_on(torch, qkv.get_device(), stream, load().mk_rope_append_e4m3, rec, k_scales.data_ptr(), v_scales.data_ptr())
+
+
+def _move_pages(fn, k, v, k_pages, v_pages, table, lengths, slots, first, k_scales, v_scales, stream) -> None:
+    import torch
+    bf, i32 = torch.bfloat16, torch.int32
+    if k.dim() != 5 or table.dim() != 2:
+        _bad("the caches must have 5 dimensions, table 2")
+    cache = _pool(torch, k_pages, v_pages, k_scales, v_scales, 1)
+    L, slots_n, Hkv, S, hd = k.shape
+    _, P, _, ps, _ = k_pages.shape
+    B, M = table.shape
+    _need(k, "k", bf, k.shape, k)
+    _need(v, "v", bf, k.shape, k)
+    _need(k_pages, "k_pages", k_pages.dtype, (L, P, Hkv, ps, hd), k)
+    _need(table, "table", i32, (B, M), k)
+    for t, what in ((lengths, "lengths"), (slots, "slots"), (first, "first")):
+        if t is not None or what == "lengths":
+            _need(t, what, i32, (B,), k)
+    if slots is None and B > slots_n:
+        _bad(f"{B} sequences for {slots_n} cache slots")
+    if B == 0:
+        return
+    rec = _PAGES_ARGS.pack(L, slots_n, Hkv, S, hd, P, ps, cache, B, M, k.data_ptr(), v.data_ptr(), k_pages.data_ptr(),
+                           v_pages.data_ptr(), _at(k_scales), _at(v_scales), table.data_ptr(), lengths.data_ptr(),
+                           _at(first), _at(slots))
+    _run_on(torch, k.get_device(), stream, fn, rec)
+
+
+def kv_write_pages(k, v, k_pages, v_pages, table, lengths, slots=None, first=None, k_scales=None, v_scales=None,
+                   stream=None) -> None:
+    """mk_kv_write_pages on CUDA tensors: rows first[b] (0) .. lengths[b] - 1 of cache slot slots[b] (b) of k / v
+    bfloat16 [L][B][Hkv][max_seq][hd] to the pages table[b] of k_pages / v_pages [L][pages][Hkv][rows][hd], bfloat16 or
+    float8_e4m3fn with k_scales / v_scales uint8 [L][pages][Hkv][rows][hd / 32]."""
+    _move_pages(load().mk_kv_write_pages, k, v, k_pages, v_pages, table, lengths, slots, first, k_scales, v_scales, stream)
+
+
+def kv_read_pages(k_pages, v_pages, k, v, table, lengths, slots=None, first=None, k_scales=None, v_scales=None,
+                  stream=None) -> None:
+    """mk_kv_read_pages on CUDA tensors: the way back of kv_write_pages; 8-bit rows become the bfloat16 values that
+    they stand for, exactly."""
+    _move_pages(load().mk_kv_read_pages, k, v, k_pages, v_pages, table, lengths, slots, first, k_scales, v_scales, stream)
 
 
 class Megakernel:

@@ -30,6 +30,42 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
     return u;
 }
+
+// ---- rows in 8 bits: e4m3 codes with a power of two 2^(s - 127) for each 32 elements.
+constexpr uint32_t kNoScale = 255;  // the block holds no numbers
+
+// The byte s of a block from its largest magnitude: 448 = 1.75 * 2^8, so the
+// exponent is that of `most` less 8, one more where its mantissa exceeds 1.75.
+__device__ __forceinline__ uint32_t e4m3_scale(float most) {
+    const uint32_t bits = __float_as_uint(most);
+    if (bits >= 0x7F800000u) return kNoScale;
+    const int s = (int)(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u);
+    return (uint32_t)min(max(s, 127 - 100), 127 + 7);
+}
+
+// Four values as codes: x * 2^(127 - s) is exact, and rounded once.
+__device__ __forceinline__ uint32_t e4m3_codes(float4 x, uint32_t s) {
+    const float up = __uint_as_float((254u - s) << 23);
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x.y * up), "f"(x.x * up));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x.w * up), "f"(x.z * up));
+    return s == kNoScale ? 0u : (uint32_t)lo | (uint32_t)hi << 16;
+}
+
+// The factor of e4m3_values, twice: a code's bits put at bf16's place are its value
+// * 2^-120, denormals too, and 2^(s - 7) is a bf16 number up to s = 134.
+__device__ __forceinline__ uint32_t e4m3_factor(uint32_t s) { return s > 134 ? 0x7FFF7FFFu : (s + 120) * 0x00800080u; }
+
+// Four codes as bf16 (exact for s >= 10).
+__device__ __forceinline__ uint2 e4m3_values(uint32_t codes, uint32_t factor) {
+    uint2 y;
+    uint32_t u = __byte_perm(codes, 0, 0x1404), v = __byte_perm(codes, 0, 0x3424);
+    u = (u & 0x80008000u) | ((u >> 4) & 0x07F007F0u);
+    v = (v & 0x80008000u) | ((v >> 4) & 0x07F007F0u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y.x) : "r"(u), "r"(factor));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y.y) : "r"(v), "r"(factor));
+    return y;
+}
 #endif
 
 // Launches a kernel that begins with pdl_begin, in clusters of `cluster` CTAs
@@ -72,7 +108,8 @@ struct RopeArgs {
     int64_t qkv_stride, q_stride;  // elements from one token to the next
     const void *qkv;
     void *q_out;
-    uint16_t *kc, *vc;
+    uint16_t *kc, *vc;  // bf16, or with ks set e4m3 codes
+    uint8_t *ks, *vs;
     const int32_t *positions, *rows, *slot_of;
     const double *inv_freq;
     const uint16_t *q_norm, *k_norm;
@@ -105,6 +142,31 @@ cudaError_t tree_attention_launch(const TreeArgs &a, int hd, bool f32, int max_l
 // Floats of workspace (TreeArgs::work) with which a call splits long caches
 // over more than a cluster's CTAs; 0: it would not use any.
 cudaError_t tree_attention_work_floats(const TreeArgs &a, int hd, bool f32, int max_len, int n_sm, int64_t *floats);
+
+// log2 of a pool's page size, 31 with one page a sequence; false for a size that is not allowed.
+bool page_shift(int page_size, int max_pages, int *shift);
+
+// Attention of ragged new tokens over a cache in pages.
+struct PagedArgs {
+    int n, B, max_pages, Hq, Hkv, n_pages, ps, shift;  // ps = 1 << shift, or one page a sequence (shift 31)
+    int cap, window, sinks;                            // most rows of a sequence; window 0: none
+    float scale;
+    int64_t q_stride, o_stride;
+    const void *q;
+    void *out;
+    const void *kc, *vc;
+    const uint8_t *ks, *vs;  // of e4m3 pages, else NULL
+    const int32_t *table, *starts, *lengths;
+    int *err;  // as in TreeArgs, and the following
+    uint64_t wait_ns;
+    uint32_t wait_sleep;
+    float *part;
+    float *work;
+    int64_t work_floats;
+};
+
+cudaError_t paged_attention_launch(const PagedArgs &a, int hd, bool f32, int max_new, int max_len, int n_sm,
+                                   cudaStream_t s);
 
 cudaError_t tree_masks_launch(const int32_t *parents, const int32_t *counts, int B, int T, uint64_t *masks,
                               int32_t *depths, cudaStream_t s);

@@ -26,8 +26,10 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <stdio.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "mk_internal.h"
 #include "mk_ops.h"
@@ -71,7 +73,8 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t *p, float4 v) {
 // elements when they took 53 % of the issue slots: so eight elements a lane, which
 // share a norm's shuffles, a head's tests and its addresses, and the reciprocal root
 // as one instruction.)
-template <typename T, int HD, int TPB, int E>
+// Q8: the cache in e4m3. A block of 32 elements is the four of eight lanes.
+template <typename T, int HD, int TPB, int E, bool Q8>
 __global__ void __launch_bounds__(kT, TPB == 1 && E == 8 ? kPerSm : 4) rope_append(const RopeArgs a) {
     constexpr int LPH = HD / E;    // lanes of a head
     constexpr int HPW = 32 / LPH;  // heads of a warp
@@ -154,11 +157,29 @@ __global__ void __launch_bounds__(kT, TPB == 1 && E == 8 ? kPerSm : 4) rope_appe
             }
             T *to = qo + (int64_t)h * HD;
             uint16_t *cache = nullptr;
+            uint8_t *codes = nullptr, *scale = nullptr;
             if (!is_q && keep && h < n_rows) {
                 const int kvh = is_k ? h - a.Hq : h - a.Hq - a.Hkv;
-                cache = (is_k ? a.kc : a.vc) + (((int64_t)slot * a.Hkv + kvh) * a.max_seq + row) * HD + 4 * j;
+                const int64_t at = ((int64_t)slot * a.Hkv + kvh) * a.max_seq + row;
+                if constexpr (Q8) {
+                    codes = reinterpret_cast<uint8_t *>(is_k ? a.kc : a.vc) + at * HD + 4 * j;
+                    scale = (is_k ? a.ks : a.vs) + at * (HD / 32) + j / 8;
+                } else {
+                    cache = (is_k ? a.kc : a.vc) + at * HD + 4 * j;
+                }
             }
             auto store = [&](int e, float4 y) {
+                if constexpr (Q8) {  // (every lane comes here: the block's largest is found by shuffles)
+                    float most = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
+                    if (!(y.x - y.x == 0.f && y.y - y.y == 0.f && y.z - y.z == 0.f && y.w - y.w == 0.f)) most = INFINITY;
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+                    if (codes) {
+                        const uint32_t s = e4m3_scale(most);
+                        *reinterpret_cast<uint32_t *>(codes + 4 * e * LPH) = e4m3_codes(y, s);
+                        if ((j & 7) == 0) scale[e * LPH / 8] = (uint8_t)s;
+                    }
+                }
                 if (is_q && h < n_rows)
                     store4<T>(to + 4 * e * LPH, y);
                 else if (cache)
@@ -261,50 +282,70 @@ cudaError_t rope_append_launch(const RopeArgs &a, int hd, bool f32, cudaStream_t
     const dim3 grid(many ? (a.n + 3) / 4 : a.n, many ? 1 : spread);
     auto go = [&](auto kernel) { return launch_op(kernel, grid, kT, 0, 0, s, a); };
     auto pick = [&](auto four, auto one, auto one4) { return many ? go(four) : few ? go(one4) : go(one); };
-    if (f32)
-        return hd == 64 ? pick(rope_append<float, 64, 4, 8>, rope_append<float, 64, 1, 8>, rope_append<float, 64, 1, 4>)
-                        : pick(rope_append<float, 128, 4, 8>, rope_append<float, 128, 1, 8>, rope_append<float, 128, 1, 4>);
-    return hd == 64
-               ? pick(rope_append<uint16_t, 64, 4, 8>, rope_append<uint16_t, 64, 1, 8>, rope_append<uint16_t, 64, 1, 4>)
-               : pick(rope_append<uint16_t, 128, 4, 8>, rope_append<uint16_t, 128, 1, 8>, rope_append<uint16_t, 128, 1, 4>);
+    auto of = [&](auto type, auto q8) {
+        using T = decltype(type);
+        constexpr bool Q8 = decltype(q8)::value;
+        return hd == 64 ? pick(rope_append<T, 64, 4, 8, Q8>, rope_append<T, 64, 1, 8, Q8>, rope_append<T, 64, 1, 4, Q8>)
+                        : pick(rope_append<T, 128, 4, 8, Q8>, rope_append<T, 128, 1, 8, Q8>,
+                               rope_append<T, 128, 1, 4, Q8>);
+    };
+    const bool q8 = a.ks != nullptr;
+    if (f32) return q8 ? of(float{}, std::true_type{}) : of(float{}, std::false_type{});
+    return q8 ? of(uint16_t{}, std::true_type{}) : of(uint16_t{}, std::false_type{});
 }
 
 }  // namespace mkops
 
-extern "C" int mk_rope_append(const mk_rope_args *a, void *stream) {
-    using mkint::set_error;
-    if (!a || !a->qkv || !a->q_out || !a->k_cache || !a->v_cache || !a->positions || !a->rows || !a->inv_freq)
-        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: a required pointer is NULL");
+namespace {
+
+// Checks and launches mk_rope_append, or with scales mk_rope_append_e4m3.
+int rope(const char *who, const mk_rope_args *a, bool q8, uint8_t *ks, uint8_t *vs, void *stream) {
+    auto bad = [&](int code, const char *what) {
+        char text[192];
+        snprintf(text, sizeof text, "%s: %s", who, what);
+        return mkint::set_error(code, text);
+    };
+    if (!a || !a->qkv || !a->q_out || !a->k_cache || !a->v_cache || !a->positions || !a->rows || !a->inv_freq ||
+        (q8 && (!ks || !vs)))
+        return bad(MK_ERR_INVALID_ARG, "a required pointer is NULL");
     if (a->dtype != MK_F32 && a->dtype != MK_BF16)
-        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: dtype is neither MK_F32 nor MK_BF16");
+        return bad(MK_ERR_INVALID_ARG, "dtype is neither MK_F32 nor MK_BF16");
     if (a->head_dim != 64 && a->head_dim != 128)
-        return set_error(MK_ERR_UNSUPPORTED, "mk_rope_append: head_dim must be 64 or 128");
+        return bad(MK_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
     if (a->n < 0 || a->n_heads < 1 || a->n_kv_heads < 1 || a->slots < 1 || a->max_seq < 1)
-        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: bad size");
+        return bad(MK_ERR_INVALID_ARG, "bad size");
     if (a->rot < 2 || a->rot > a->head_dim || a->rot % 2)
-        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: rot must be even, 2 .. head_dim");
+        return bad(MK_ERR_INVALID_ARG, "rot must be even, 2 .. head_dim");
     if (!(a->eps >= 0.f) || !isfinite(a->eps) || !isfinite(a->mscale))
-        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: eps or mscale is not a finite number");
+        return bad(MK_ERR_INVALID_ARG, "eps or mscale is not a finite number");
     const int64_t q = (int64_t)a->n_heads * a->head_dim, qkv = q + 2 * (int64_t)a->n_kv_heads * a->head_dim;
-    if (qkv > INT32_MAX) return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: too many heads");
+    if (qkv > INT32_MAX) return bad(MK_ERR_INVALID_ARG, "too many heads");
     if (a->qkv_stride < qkv || a->q_stride < q || a->qkv_stride % 4 || a->q_stride % 4)
-        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: a stride is too small or not a multiple of 4 elements");
+        return bad(MK_ERR_INVALID_ARG, "a stride is too small or not a multiple of 4 elements");
     const uintptr_t io = reinterpret_cast<uintptr_t>(a->qkv) | reinterpret_cast<uintptr_t>(a->q_out);
+    const uintptr_t both = reinterpret_cast<uintptr_t>(a->k_cache) | reinterpret_cast<uintptr_t>(a->v_cache);
     const uintptr_t cache = reinterpret_cast<uintptr_t>(a->k_cache) | reinterpret_cast<uintptr_t>(a->v_cache) |
                             reinterpret_cast<uintptr_t>(a->q_norm) | reinterpret_cast<uintptr_t>(a->k_norm);
-    if ((io & 15u) || (cache & 7u) || (reinterpret_cast<uintptr_t>(a->inv_freq) & 7u))
-        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: a pointer is not aligned");
+    if ((io & 15u) || (cache & 7u) || (q8 && (both & 15u)) || (reinterpret_cast<uintptr_t>(a->inv_freq) & 7u))
+        return bad(MK_ERR_INVALID_ARG, "a pointer is not aligned");
     if (a->n == 0) return MK_OK;
     // What one CTA writes no other may read or write: the caches apart from everything,
     // q_out from qkv but for the same rows in place, or rows in the gaps between qkv's.
     const int64_t e = a->dtype == MK_F32 ? 4 : 2, q_bytes = ((a->n - 1) * a->q_stride + q) * e,
                   qkv_bytes = ((a->n - 1) * a->qkv_stride + qkv) * e,
-                  cache_bytes = 2 * (int64_t)a->slots * a->n_kv_heads * a->max_seq * a->head_dim;
+                  rows = (int64_t)a->slots * a->n_kv_heads * a->max_seq, cache_bytes = rows * a->head_dim * (q8 ? 1 : 2);
     using mkops::meet;
-    if (meet(a->k_cache, cache_bytes, a->v_cache, cache_bytes) || meet(a->k_cache, cache_bytes, a->q_out, q_bytes) ||
-        meet(a->v_cache, cache_bytes, a->q_out, q_bytes) || meet(a->k_cache, cache_bytes, a->qkv, qkv_bytes) ||
-        meet(a->v_cache, cache_bytes, a->qkv, qkv_bytes))
-        return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: a cache overlaps the other, qkv or q_out");
+    const struct {
+        const void *at;
+        int64_t bytes;
+    } written[] = {{a->k_cache, cache_bytes}, {a->v_cache, cache_bytes}, {ks, rows * (a->head_dim / 32)},
+                   {vs, rows * (a->head_dim / 32)}};
+    for (int i = 0; i < (q8 ? 4 : 2); ++i) {
+        bool met = meet(written[i].at, written[i].bytes, a->q_out, q_bytes) ||
+                   meet(written[i].at, written[i].bytes, a->qkv, qkv_bytes);
+        for (int k = 0; k < i; ++k) met = met || meet(written[i].at, written[i].bytes, written[k].at, written[k].bytes);
+        if (met) return bad(MK_ERR_INVALID_ARG, "a cache overlaps the other, qkv or q_out");
+    }
     if (meet(a->q_out, q_bytes, a->qkv, qkv_bytes)) {
         const int64_t step = a->qkv_stride * e;
         int64_t off = (int64_t)(reinterpret_cast<uintptr_t>(a->q_out) - reinterpret_cast<uintptr_t>(a->qkv));
@@ -312,19 +353,30 @@ extern "C" int mk_rope_append(const mk_rope_args *a, void *stream) {
         const bool in_place = off == 0 && same_rows;
         off = (off % step + step) % step;
         if (!in_place && !(same_rows && a->n > 1 && off >= qkv * e && off + q * e <= step))
-            return set_error(MK_ERR_INVALID_ARG, "mk_rope_append: q_out overlaps qkv other than row by row in place");
+            return bad(MK_ERR_INVALID_ARG, "q_out overlaps qkv other than row by row in place");
     }
     mkops::RopeArgs r{};
     r.n = a->n, r.Hq = a->n_heads, r.Hkv = a->n_kv_heads, r.rot = a->rot, r.interleaved = a->interleaved;
     r.slots = a->slots, r.max_seq = a->max_seq, r.eps = a->eps, r.mscale = a->mscale;
     r.qkv_stride = a->qkv_stride, r.q_stride = a->q_stride;
     r.qkv = a->qkv, r.q_out = a->q_out;
+    r.ks = ks, r.vs = vs;
     r.kc = static_cast<uint16_t *>(a->k_cache), r.vc = static_cast<uint16_t *>(a->v_cache);
     r.positions = a->positions, r.rows = a->rows, r.slot_of = a->slot_of, r.inv_freq = a->inv_freq;
     r.q_norm = static_cast<const uint16_t *>(a->q_norm), r.k_norm = static_cast<const uint16_t *>(a->k_norm);
     const cudaError_t err =
         mkops::rope_append_launch(r, a->head_dim, a->dtype == MK_F32, static_cast<cudaStream_t>(stream));
-    return err == cudaSuccess ? MK_OK : mkops::cuda_error(err, "mk_rope_append");
+    return err == cudaSuccess ? MK_OK : mkops::cuda_error(err, who);
+}
+
+}  // namespace
+
+extern "C" int mk_rope_append(const mk_rope_args *a, void *stream) {
+    return rope("mk_rope_append", a, false, nullptr, nullptr, stream);
+}
+
+extern "C" int mk_rope_append_e4m3(const mk_rope_args *a, uint8_t *k_scales, uint8_t *v_scales, void *stream) {
+    return rope("mk_rope_append_e4m3", a, true, k_scales, v_scales, stream);
 }
 
 extern "C" int mk_rope_frequencies(int32_t kind, int32_t rot, double theta, double factor, double original_len,

@@ -585,6 +585,100 @@ int mk_kv_compact(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_k
 int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_kv_heads, int32_t max_seq,
                   int32_t head_dim, const int32_t *d_sources, const int32_t *d_lengths, void *stream);
 
+/* ---- Operators of a cache in pages ----------------------------------------
+ * A pool holds the KV rows of many sequences in pages of page_size rows: bf16
+ * or e4m3 [n_pages][n_kv_heads][page_size][head_dim], keys and values apart
+ * (mk_kv_cache's layout with pages for slots, so mk_rope_append writes bf16
+ * pages as they are: the page as the slot, the row in the page as the row).
+ * Row j of a sequence lies in row j % page_size of page table[j / page_size].
+ * page_size is a power of two from 8 on; a table of one page a sequence takes
+ * any page_size from 8 on, and a contiguous cache is such a pool.
+ *
+ * An e4m3 row (MK_E4M3) is head_dim codes (sign, 4 exponent bits, 3 bits; code
+ * 0x7F and 0xFF do not occur) and, in k_scales / v_scales [n_pages]
+ * [n_kv_heads][page_size][head_dim / 32], a byte s for each 32 of them: the
+ * value is code * 2^(s - 127), and not a number with s = 255. Rows are quantised to
+ * the smallest e = s - 127 in [-100, 7] with max|x| <= 448 * 2^e, codes rounded to
+ * nearest even (beyond 57344 to that); a block with a value that is not finite
+ * gets s = 255. Every such value is a bf16 value.
+ * Like the operators above these calls keep nothing, work on the current
+ * device, asynchronous on `stream`, and check what device arrays hold on the
+ * device. The pages name no such operators. */
+#define MK_E4M3 2
+
+/* Attention of the new tokens of each sequence over its rows in pages. Sequence
+ * b < batch has the tokens starts[b] <= t < starts[b + 1] of q and out, n_b of them,
+ * and lengths[b] rows in the cache, the last n_b its new tokens' own: token i
+ * stands at position p = lengths[b] - n_b + i and sees the rows j <= p with
+ *   window = 0, or j > p - window, or j < sinks.
+ * out = sum_j p_j v_j / sum_j p_j, p_j = exp(scale * q . k_j - max). What rows
+ * hold that a token does not see, NaN and infinities too, does not matter; a
+ * token that sees none (p < 0) gets zeros; tokens outside every sequence are
+ * not written. Sequences must not share tokens (starts must not fall); they may
+ * share pages. A page number outside [0, n_pages) is not followed: its rows count as
+ * zeros. lengths are cut to [0, max_pages * page_size], starts to [0, n_tokens].
+ * q, out: dtype (fp32 or bf16) [n_tokens][n_heads][head_dim], tokens q_stride /
+ * out_stride elements apart, 16-byte aligned, strides multiples of 8; out must
+ * overlap nothing. n_heads a multiple of n_kv_heads, at most MK_MAX_GROUP times it;
+ * head_dim 64 or 128. table: int32 [batch][max_pages]; starts: int32 [batch + 1];
+ * lengths: int32 [batch]. cache_dtype MK_BF16, or MK_E4M3 with both scales.
+ * Sums and statistics are fp32; fp32 queries and their probabilities enter the
+ * products as three bf16 terms each (24 bits), bf16 queries as they are, their
+ * probabilities as two (16 bits).
+ * max_new: a bound on n_b, max_len: on lengths[b], known to the host (0:
+ * n_tokens, max_pages * page_size); used only to choose the launch, results are right
+ * if they are exceeded.
+ * workspace, status, wait_ns: as in mk_tree_args, with
+ * mk_paged_attention_workspace(). */
+typedef struct mk_paged_args {
+    int32_t n_tokens, batch, max_pages, n_heads, n_kv_heads, head_dim, dtype, cache_dtype, n_pages, page_size;
+    int32_t max_new, max_len, window, sinks;
+    float scale;
+    int64_t q_stride, out_stride;
+    const void *q;
+    void *out;
+    const void *k_pages, *v_pages;
+    const uint8_t *k_scales, *v_scales;
+    const int32_t *table, *starts, *lengths;
+    void *workspace;
+    int64_t workspace_bytes;
+    int32_t *status;
+    int64_t wait_ns;
+} mk_paged_args;
+int mk_paged_attention(const mk_paged_args *args, void *stream);
+
+/* Bytes of workspace with which mk_paged_attention splits these calls' rows over
+ * more CTAs than one cluster holds; 0 where it would not use any. Follows no
+ * pointer. A negative mk_status for arguments that mk_paged_attention refuses. */
+int64_t mk_paged_attention_workspace(const mk_paged_args *args);
+
+/* mk_rope_append with e4m3 caches: k_cache and v_cache hold codes [slots]
+ * [n_kv_heads][max_seq][head_dim] (bytes), k_scales and v_scales the exponents
+ * [slots][n_kv_heads][max_seq][head_dim / 32]. With a pool of pages slots is
+ * n_pages, max_seq page_size, slot_of a token's page and rows the row in it.
+ * Keys are quantised from their rotated fp32 values, values from their own.
+ * Caches 16-byte aligned; caches and scales overlap nothing. */
+int mk_rope_append_e4m3(const mk_rope_args *args, uint8_t *k_scales, uint8_t *v_scales, void *stream);
+
+/* Rows between a contiguous cache (bf16 [n_layers][slots][n_kv_heads][max_seq]
+ * [head_dim]) and a pool ([n_layers][n_pages]...; bf16 or e4m3 with scales): for
+ * every layer, sequence b < batch and row first[b] <= j < lengths[b] (first NULL:
+ * 0), row j of slot slot_of[b] (b with slot_of NULL) and row j of sequence b.
+ * mk_kv_write_pages copies to the pages, quantising where they are e4m3;
+ * mk_kv_read_pages from them (exactly: every 8-bit value is a bf16 value).
+ * Rows beyond max_seq or max_pages * page_size, on pages outside
+ * [0, n_pages), and of slots outside the cache are left as they are. Two sequences
+ * of one call must not name the same row to be written. Caches and pools
+ * 16-byte aligned, nothing that is written overlaps anything else; head_dim 64 or 128. */
+typedef struct mk_pages_args {
+    int32_t n_layers, slots, n_kv_heads, max_seq, head_dim, n_pages, page_size, cache_dtype, batch, max_pages;
+    void *k, *v, *k_pages, *v_pages;
+    uint8_t *k_scales, *v_scales;
+    const int32_t *table, *lengths, *first, *slot_of;
+} mk_pages_args;
+int mk_kv_write_pages(const mk_pages_args *args, void *stream);
+int mk_kv_read_pages(const mk_pages_args *args, void *stream);
+
 /* Optional per-instruction timing: when `enable` is non-zero, every step
  * records %globaltimer stamps per instruction into a device buffer that
  * mk_read_trace copies out (see mk_read_trace).
