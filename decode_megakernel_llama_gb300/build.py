@@ -17,7 +17,7 @@ DEPS = SOURCES + ["mk_kernel.cuh", "mk_plan.h", "mk_internal.h", "mk_prefill.h"]
 # the standalone operators: units of their own beside the megakernel's, and the
 # extension module through which the binding calls them with torch's tensors
 OP_SOURCES = ["mk_rope.cu", "mk_tree.cu", "mk_kv.cu", "mk_pages.cu", "mk_paged.cu"]
-OP_DEPS = OP_SOURCES + ["mk_ops.h", "mk_tc.cuh", "mk_tree_attn.cuh"]
+OP_DEPS = OP_SOURCES + ["mk_ops.h", "mk_tc.cuh", "mk_tree_attn.cuh", "mk_paged_attn.cuh"]
 TORCH_SOURCE = "mk_torch.cpp"
 
 

@@ -150,6 +150,7 @@ bool page_shift(int page_size, int max_pages, int *shift);
 struct PagedArgs {
     int n, B, max_pages, Hq, Hkv, n_pages, ps, shift;  // ps = 1 << shift, or one page a sequence (shift 31)
     int cap, window, sinks;                            // most rows of a sequence; window 0: none
+    int units;                                         // tiles of query rows in the grid (set by the launch)
     float scale;
     int64_t q_stride, o_stride;
     const void *q;
@@ -164,9 +165,6 @@ struct PagedArgs {
     float *work;
     int64_t work_floats;
 };
-
-cudaError_t paged_attention_launch(const PagedArgs &a, int hd, bool f32, int max_new, int max_len, int n_sm,
-                                   cudaStream_t s);
 
 cudaError_t tree_masks_launch(const int32_t *parents, const int32_t *counts, int B, int T, uint64_t *masks,
                               int32_t *depths, cudaStream_t s);

@@ -17,92 +17,127 @@
 
 #include "mk_internal.h"
 #include "mk_ops.h"
+#include "mk_paged_attn.cuh"
 
 namespace mkops {
 namespace {
 
-// Where row j of a sequence lies in the pool, in rows; -1 on a page outside it.
-__device__ __forceinline__ int64_t pool_row(const PagedArgs &a, int b, int kvh, int j) {
-    const int p = j >> a.shift, page = a.table[(int64_t)b * a.max_pages + p];
-    if (page < 0 || page >= a.n_pages) return -1;
-    return ((int64_t)page * a.Hkv + kvh) * a.ps + (j - (p << a.shift));
+// The two kernels by what their launch needs. kTileUs: a tile of one CTA; kFixedUs:
+// launch, set-up and end; kJoinUs: the workspace's second launch.
+template <int HD_, int TERMS_, int NR_, bool Q8_>
+struct PagedFew {
+    static constexpr int kThreads = paged_threads(Q8_), HD = HD_, TERMS = TERMS_, NR = NR_,
+                         kSmem = AttnShape<HD, TERMS, NR>::kSmem;
+    static constexpr bool Q8 = Q8_;
+    static constexpr double kTileUs = (HD == 64 ? 0.6 : 1.0) - (TERMS == 1 ? HD / 64 * 0.1 : 0.0), kFixedUs = 5.0, kJoinUs = 4.5;
+    static auto fn() { return paged_attention<HD, TERMS, NR, Q8>; }
+};
+template <int HD_, int TERMS_, bool Q8_>
+struct PagedMany {
+    static constexpr int kThreads = paged_threads(Q8_), HD = HD_, TERMS = TERMS_, NR = kRows,
+                         kSmem = RowShape<HD, TERMS, 4 * kBadWords>::kSmem;
+    static constexpr bool Q8 = Q8_;
+    static constexpr double kTileUs = HD == 64 && TERMS == 1 ? 0.8 : 1.2, kFixedUs = 6.5, kJoinUs = 7.0;
+    static auto fn() { return paged_attention_rows<HD, TERMS, Q8>; }
+};
+
+struct Plan {
+    int S, U;  // splits of a unit's tiles; tiles of query rows, over all sequences
+    bool ws;
+    double us;  // its estimated time
+};
+
+// What a call's host knows: bounds on a sequence's tokens and rows.
+struct Bounds {
+    int max_new, max_len, n_sm;
+};
+
+// The split with the least estimated time. Units (tiles of query rows x kv heads)
+// that do not fit the GPU at once follow one another, so more than a wave of them
+// cost their mean, less the longest. The mean of a prompt's tiles is about half of
+// the longest's.
+template <class K>
+Plan plan(const PagedArgs &a, const Bounds &h, bool ws) {
+    const int G = a.Hq / a.Hkv;
+    const int U = (int)(((int64_t)a.n * G + (int64_t)std::min(a.B, a.n) * (K::NR - 1)) / K::NR);
+    const int64_t real = std::min<int64_t>(U, (int64_t)a.B * (((int64_t)h.max_new * G + K::NR - 1) / K::NR));
+    const int64_t units = real * a.Hkv;
+    double rows = h.max_len, mean = h.max_len - 0.5 * std::min(h.max_new, h.max_len);
+    if (a.window) {
+        const double seen = (double)a.window + a.sinks + kTile + K::NR / G;
+        rows = std::min(rows, seen), mean = std::min(mean, seen);
+    }
+    const int tiles = std::max(1, (int)((rows + kTile - 1) / kTile));
+    const double mean_tiles = std::max(1.0, mean / kTile);
+    Plan best{1, U, false, 1e30};
+    for (int k = 0; k < 4 && (1 << k) <= tiles; ++k) {
+        const int S = 1 << k, at_once = active_clusters<K>(k, h.n_sm);
+        const int64_t waves = (units + at_once - 1) / at_once;
+        const double each = waves > 1 ? mean_tiles / S + 0.5 : (tiles + S - 1) / S;
+        const double us = (double)waves * (each * K::kTileUs + K::kFixedUs) + (k ? 0.8 + 0.2 * k : 0.0);
+        if (us < best.us) best = Plan{S, U, false, us};
+    }
+    if (ws) {
+        const int64_t room = active_clusters<K>(0, h.n_sm) / units;
+        const int S = (int)std::min<int64_t>(std::min<int64_t>(room, max_splits(K::NR)), tiles / 2);
+        const double us = ((tiles + S - 1) / std::max(S, 1)) * K::kTileUs + K::kFixedUs + K::kJoinUs;
+        if (S > 1 && us < best.us) best = Plan{S, U, true, us};
+    }
+    return best;
 }
 
-// Element d of a row of the pool, in fp32.
-template <int HD, bool Q8>
-__device__ __forceinline__ float pool_value(const void *pool, const uint8_t *scales, int64_t row, int d) {
-    if (row < 0) return 0.f;
-    if constexpr (Q8) {
-        const uint32_t code = static_cast<const uint8_t *>(pool)[row * HD + d];
-        return bf_lo(e4m3_values(code, e4m3_factor(scales[row * (HD / 32) + d / 32])).x);
-    } else {
-        return bf_lo(static_cast<const uint16_t *>(pool)[row * HD + d]);
+template <class K>
+cudaError_t launch(PagedArgs a, const Bounds &h, cudaStream_t s, int64_t *want) {
+    cudaError_t e = configure<K>();
+    if (e != cudaSuccess) return e;
+    Plan p = plan<K>(a, h, want || a.work);
+    const int64_t need = p.ws ? (int64_t)p.U * a.Hkv * p.S * part_floats(K::NR, K::HD) : 0;
+    if (want) {
+        *want = need;
+        return cudaSuccess;
     }
+    if (need > a.work_floats) p = plan<K>(a, h, false);
+    a.part = p.ws ? a.work : nullptr;
+    a.units = p.U;
+    if (a.wait_ns == 0) a.wait_ns = kWaitNs;
+    a.wait_sleep = (uint32_t)std::min<uint64_t>(a.wait_ns, kSleepNs);
+    CUtensorMap kmap{}, vmap{};
+    if (!K::Q8) {
+        const int box = a.shift < 31 ? std::min(a.ps, kTile) : kTile;
+        if (!cache_map(&kmap, a.kc, a.n_pages * a.Hkv, a.ps, K::HD, box) ||
+            !cache_map(&vmap, a.vc, a.n_pages * a.Hkv, a.ps, K::HD, box))
+            return cudaErrorInvalidValue;
+    }
+    e = launch_op(K::fn(), dim3(p.S * p.U, a.Hkv), K::kThreads, K::kSmem, p.ws ? 1 : p.S, s, kmap, vmap, a);
+    if (e != cudaSuccess || !p.ws) return e;
+    return launch_op(paged_join<K::HD, K::TERMS, K::NR>, dim3(p.U, a.Hkv, (K::NR * K::HD / 4 + 255) / 256), 256, 0, 0, s, a,
+                     p.S);
 }
 
-// A warp per (token, head): 32 rows at a time, a lane the score of one, then all
-// lanes HD / 32 dims each of the weighted sum.
-template <typename T, int HD, bool Q8>
-__global__ void __launch_bounds__(128) paged_simple(const PagedArgs a) {
-    __shared__ float qs[4][HD];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.x, h = blockIdx.y * 4 + warp;
-    pdl_begin();
-    if (h >= a.Hq) return;
-    int b = 0, n = 0, i = -1;
-    for (; b < a.B; ++b) {
-        const int lo = min(max(a.starts[b], 0), a.n), hi = min(max(a.starts[b + 1], 0), a.n);
-        if (t >= lo && t < hi) {
-            n = hi - lo, i = t - lo;
-            break;
+// The kernel of 16 or 32 columns that holds a sequence's rows of a kv head, or, for
+// more rows, several CTAs of 32 or the kernel of 128 rows, whichever plan is shorter.
+template <int HD, int TERMS, bool Q8>
+cudaError_t dispatch(const PagedArgs &a, const Bounds &h, cudaStream_t s, int64_t *want) {
+    const int64_t rows = (int64_t)h.max_new * (a.Hq / a.Hkv);
+    if (rows <= 16) return launch<PagedFew<HD, TERMS, 16, Q8>>(a, h, s, want);
+    // (three terms of a head of 128 and two O of 128 columns exceed tensor memory)
+    if constexpr (!(HD == 128 && TERMS == 3))
+        if (rows > 32) {
+            const bool ws = want || a.work;
+            if (plan<PagedMany<HD, TERMS, Q8>>(a, h, ws).us < plan<PagedFew<HD, TERMS, 32, Q8>>(a, h, ws).us)
+                return launch<PagedMany<HD, TERMS, Q8>>(a, h, s, want);
         }
-    }
-    if (i < 0) return;
-    const int pos = min(max(a.lengths[b], 0), a.cap) - n + i, kvh = h / (a.Hq / a.Hkv);
-    const T *q = static_cast<const T *>(a.q) + t * a.q_stride + (int64_t)h * HD;
-    for (int d = lane; d < HD; d += 32) {
-        if constexpr (sizeof(T) == 4)
-            qs[warp][d] = q[d];
-        else
-            qs[warp][d] = bf_lo(q[d]);
-    }
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[HD / 32] = {};
-    for (int j0 = 0; j0 <= pos; j0 += 32) {
-        const int j = j0 + lane;
-        const bool sees = j <= pos && (!a.window || j > pos - a.window || j < a.sinks);
-        if (!__any_sync(0xFFFFFFFFu, sees)) continue;
-        float x = -INFINITY;
-        int64_t row = -1;
-        if (sees) {
-            row = pool_row(a, b, kvh, j);
-            x = 0.f;
-            for (int d = 0; d < HD; ++d) x = fmaf(qs[warp][d], pool_value<HD, Q8>(a.kc, a.ks, row, d), x);
-            x *= a.scale;
-        }
-        float top = x;
-        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
-        top = fmaxf(top, m);
-        const float corr = m == top ? 1.f : expf(m - top), w = sees ? expf(x - top) : 0.f;
-        m = top;
-        l = l * corr + w;
-        for (int e = 0; e < HD / 32; ++e) o[e] *= corr;
-        for (int s = 0; s < 32; ++s) {
-            const float ws = __shfl_sync(0xFFFFFFFFu, w, s);
-            const int64_t rs = __shfl_sync(0xFFFFFFFFu, row, s);
-            if (__shfl_sync(0xFFFFFFFFu, (int)sees, s))
-                for (int e = 0; e < HD / 32; ++e)
-                    o[e] = fmaf(ws, pool_value<HD, Q8>(a.vc, a.vs, rs, e * 32 + lane), o[e]);
-        }
-    }
-    for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    T *out = static_cast<T *>(a.out) + t * a.o_stride + (int64_t)h * HD;
-    for (int e = 0; e < HD / 32; ++e) {
-        if constexpr (sizeof(T) == 4)
-            out[e * 32 + lane] = o[e] * inv;
-        else
-            out[e * 32 + lane] = (uint16_t)pack_bf16(o[e] * inv, 0.f);
-    }
+    return launch<PagedFew<HD, TERMS, 32, Q8>>(a, h, s, want);
+}
+
+template <int HD, int TERMS>
+cudaError_t dispatch(const PagedArgs &a, const Bounds &h, cudaStream_t s, int64_t *want) {
+    return a.ks ? dispatch<HD, TERMS, true>(a, h, s, want) : dispatch<HD, TERMS, false>(a, h, s, want);
+}
+
+cudaError_t dispatch(const PagedArgs &a, int hd, bool f32, const Bounds &h, cudaStream_t s, int64_t *want) {
+    if (f32) return hd == 64 ? dispatch<64, 3>(a, h, s, want) : dispatch<128, 3>(a, h, s, want);
+    return hd == 64 ? dispatch<64, 1>(a, h, s, want) : dispatch<128, 1>(a, h, s, want);
 }
 
 }  // namespace
@@ -114,17 +149,6 @@ bool page_shift(int page_size, int max_pages, int *shift) {
     if (page_size & (page_size - 1)) return false;
     for (*shift = 3; (1 << *shift) < page_size;) ++*shift;
     return true;
-}
-
-cudaError_t paged_attention_launch(const PagedArgs &a, int hd, bool f32, int max_new, int max_len, int n_sm,
-                                   cudaStream_t s) {
-    auto go = [&](auto kernel) { return launch_op(kernel, dim3(a.n, (a.Hq + 3) / 4), 128, 0, 0, s, a); };
-    auto of = [&](auto type) {
-        using T = decltype(type);
-        if (a.ks) return hd == 64 ? go(paged_simple<T, 64, true>) : go(paged_simple<T, 128, true>);
-        return hd == 64 ? go(paged_simple<T, 64, false>) : go(paged_simple<T, 128, false>);
-    };
-    return f32 ? of(float{}) : of(uint16_t{});
 }
 
 }  // namespace mkops
@@ -153,22 +177,23 @@ int check_paged(const mk_paged_args *a, mkops::PagedArgs *p) {
     int shift;
     if (!mkops::page_shift(a->page_size, a->max_pages, &shift))
         return bad(MK_ERR_INVALID_ARG, "page_size must be a power of two from 8 on (any from 8 on with max_pages 1)");
+    if (q8 && a->page_size % 8) return bad(MK_ERR_INVALID_ARG, "page_size of e4m3 pages must be a multiple of 8");
     const int64_t cap = (int64_t)a->max_pages * a->page_size;
-    if (cap > (1 << 30)) return bad(MK_ERR_UNSUPPORTED, "max_pages * page_size above 2^30");
+    if (cap > (1 << 29)) return bad(MK_ERR_UNSUPPORTED, "max_pages * page_size above 2^29");
     if (!isfinite(a->scale) || !(a->scale > 0.f)) return bad(MK_ERR_INVALID_ARG, "scale must be finite and > 0");
     if (a->window < 0 || a->sinks < 0) return bad(MK_ERR_INVALID_ARG, "window or sinks is negative");
     if (a->max_new < 0 || a->max_new > a->n_tokens || a->max_len < 0 || a->max_len > cap)
         return bad(MK_ERR_INVALID_ARG, "max_new outside [0, n_tokens] or max_len outside [0, max_pages * page_size]");
     const int64_t row = (int64_t)a->n_heads * a->head_dim;
-    if (a->n_kv_heads > 65535 || (int64_t)a->n_pages * a->n_kv_heads > INT32_MAX ||
-        (int64_t)a->n_tokens * a->n_heads > (1 << 30) || a->batch > (1 << 20))
+    if (a->n_kv_heads > 65535 || ((int64_t)a->n_pages + 1) * a->n_kv_heads > INT32_MAX ||
+        (int64_t)a->n_tokens * a->n_heads > (1 << 29) || a->batch > (1 << 20))
         return bad(MK_ERR_UNSUPPORTED, "too many tokens, heads, pages or sequences");
     if (a->q_stride < row || a->out_stride < row || (a->q_stride | a->out_stride) % 8)
         return bad(MK_ERR_INVALID_ARG, "a stride is too small or not a multiple of 8 elements");
     const uintptr_t all = reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(a->out) |
                           reinterpret_cast<uintptr_t>(a->k_pages) | reinterpret_cast<uintptr_t>(a->v_pages) |
                           reinterpret_cast<uintptr_t>(a->workspace);
-    if ((all & 15u) || (q8 && ((reinterpret_cast<uintptr_t>(a->k_scales) | reinterpret_cast<uintptr_t>(a->v_scales)) & 3u)))
+    if ((all & 15u) || (q8 && ((reinterpret_cast<uintptr_t>(a->k_scales) | reinterpret_cast<uintptr_t>(a->v_scales)) & 7u)))
         return bad(MK_ERR_INVALID_ARG, "a pointer is not aligned");
     if (a->workspace_bytes < 0) return bad(MK_ERR_INVALID_ARG, "bad workspace");
     if (a->wait_ns < 0) return bad(MK_ERR_INVALID_ARG, "wait_ns is negative");
@@ -202,13 +227,18 @@ extern "C" int mk_paged_attention(const mk_paged_args *a, void *stream) {
     mkops::PagedArgs p;
     const int rc = check_paged(a, &p);
     if (rc || a->batch == 0 || a->n_tokens == 0) return rc;
+    const mkops::Bounds h{a->max_new ? a->max_new : a->n_tokens, a->max_len ? a->max_len : p.cap, mkops::sm_count()};
     const cudaError_t e =
-        mkops::paged_attention_launch(p, a->head_dim, a->dtype == MK_F32, a->max_new ? a->max_new : a->n_tokens,
-                                      a->max_len ? a->max_len : p.cap, mkops::sm_count(), static_cast<cudaStream_t>(stream));
+        mkops::dispatch(p, a->head_dim, a->dtype == MK_F32, h, static_cast<cudaStream_t>(stream), nullptr);
     return e == cudaSuccess ? MK_OK : mkops::cuda_error(e, "mk_paged_attention");
 }
 
 extern "C" int64_t mk_paged_attention_workspace(const mk_paged_args *a) {
     mkops::PagedArgs p;
-    return check_paged(a, &p);
+    const int rc = check_paged(a, &p);
+    if (rc || a->batch == 0 || a->n_tokens == 0) return rc;
+    const mkops::Bounds h{a->max_new ? a->max_new : a->n_tokens, a->max_len ? a->max_len : p.cap, mkops::sm_count()};
+    int64_t floats = 0;
+    const cudaError_t e = mkops::dispatch(p, a->head_dim, a->dtype == MK_F32, h, nullptr, &floats);
+    return e == cudaSuccess ? floats * 4 : mkops::cuda_error(e, "mk_paged_attention_workspace");
 }

@@ -1,0 +1,919 @@
+// mk_paged_attn.cuh — the attention kernels over a cache in pages (see mk_paged.cu).
+//
+// The two tcgen05 kernels of a drafted tree (mk_tree_attn.cuh, whose head states the
+// products, the softmax in one pass, the overlap and what a wait that runs out does),
+// with what ragged sequences in pages need instead of a tree in a slot:
+//   - a CTA finds its sequence and rows from `starts` (find_work), so the grid
+//     follows the tokens, not the longest sequence: a batch of one prompt and many
+//     single tokens has no empty CTAs to speak of;
+//   - a tile of 128 rows is one TMA box a page (16 pages of 8 rows at most, a lane
+//     each), the page numbers read a tile ahead; pages that are not there, and what
+//     lies behind the sequence, are boxes outside the map, which read as zeros;
+//   - tiles that no row of the CTA sees (behind the last token, before the window)
+//     are not visited, those that all rows see whole take no mask; the others, five at
+//     most (Span), select scores and clean V;
+//   - 8-bit pages (Q8): four more warps read codes and powers, put the bf16 values,
+//     which are exact, where TMA puts them, and from there on all is as with bf16.
+//     So their products are those of the bf16 kernel and only the bytes are half.
+#pragma once
+#include "mk_tree_attn.cuh"
+
+namespace mkops {
+
+constexpr int kFirstConv = kFirstSoft + kSoftWarps, kConvWarps = 4;
+constexpr int kParts = 5, kBadRows = kParts * kTile, kBadWords = kBadRows / 32;
+
+__host__ __device__ constexpr int paged_threads(bool q8) { return kAttnThreads + (q8 ? 32 * kConvWarps : 0); }
+__device__ __forceinline__ bool is_soft(int warp) { return warp >= kFirstSoft && warp < kFirstSoft + kSoftWarps; }
+
+// A CTA's rows: query rows row0 .. row0 + rows - 1 of sequence b (row = token of the
+// sequence * G + head of the group), whose n tokens begin at tok0 of the call's.
+struct Work {
+    int b, n, len, tok0, row0, rows;
+};
+
+// The u-th tile of NR rows over all sequences, by a whole warp; rows = 0 behind the last.
+__device__ __forceinline__ Work find_work(const PagedArgs &a, int u, int NR, int G, int lane) {
+    Work w{0, 0, 0, 0, 0, 0};
+    int before = 0;  // tiles of the sequences seen so far
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int b = b0 + lane;
+        int lo = 0, n = 0, len = 0;
+        if (b < a.B) {
+            lo = min(max(a.starts[b], 0), a.n);
+            n = max(min(max(a.starts[b + 1], 0), a.n) - lo, 0);
+            len = min(max(a.lengths[b], 0), a.cap);
+        }
+        const int mine = (n * G + NR - 1) / NR;
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        const uint32_t has = __ballot_sync(0xFFFFFFFFu, before + upto > u);
+        if (has) {
+            const int l = __ffs(has) - 1;
+            w.b = b0 + l;
+            w.n = __shfl_sync(0xFFFFFFFFu, n, l);
+            w.len = __shfl_sync(0xFFFFFFFFu, len, l);
+            w.tok0 = __shfl_sync(0xFFFFFFFFu, lo, l);
+            w.row0 = (u - before - __shfl_sync(0xFFFFFFFFu, upto - mine, l)) * NR;
+            w.rows = min(NR, w.n * G - w.row0);
+            return w;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    return w;
+}
+
+// Bits below n of 32.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
+// The cache rows that a CTA's tokens, at positions p0 .. p1 (p1 - p0 < 128), see: its
+// tiles in order are the ns that hold the first `sinks` rows, then those from wt on.
+struct Span {
+    int base, p0, p1, end, window, sinks, ns, wt, tiles, last;  // base: position of token 0; last: of the CTA, + 1
+    __device__ __forceinline__ int tile(int v) const { return v < ns ? v : wt + v - ns; }
+    // Which of the kParts tiles that not all rows see whole; -1: all do. (0: the end of
+    // the first rows; 1, 2: where the windows begin; 3, 4: where the tokens stand.)
+    __device__ __forceinline__ int part(int t) const {
+        const int at = t * kTile;
+        if (window && at <= p1 - window && at + kTile > sinks) return t < wt ? 0 : 1 + t - wt;
+        return at + kTile > p0 + 1 ? 3 + t - max(p0 + 1, 0) / kTile : -1;
+    }
+    __device__ __forceinline__ int tile_of_part(int k) const {
+        return k == 0 ? ns - 1 : k < 3 ? wt + k - 1 : max(p0 + 1, 0) / kTile + k - 3;
+    }
+    __device__ __forceinline__ bool sees(int pos, int j) const {
+        return j <= pos && (!window || j > pos - window || j < sinks);
+    }
+    __device__ __forceinline__ bool somebody(int j) const {
+        return j < end && (!window || j > p0 - window || j < sinks);
+    }
+    // The query rows of the CTA that see cache row j: [lo, hi).
+    __device__ __forceinline__ void columns(int j, int G, int row0, int &lo, int &hi) const {
+        lo = max(j - base, 0) * G - row0;
+        hi = last * G - row0;
+        if (window && j >= sinks) hi = min(max(j - base + window, 0), last) * G - row0;
+    }
+    // Bit e: the token at pos sees row j + e.
+    __device__ __forceinline__ uint32_t sees32(int pos, int j) const {
+        uint32_t m = below(pos + 1 - j);
+        if (window) m &= ~below(pos - window + 1 - j) | below(sinks - j);
+        return m;
+    }
+};
+
+__device__ __forceinline__ Span span_of(const PagedArgs &a, const Work &w, int G) {
+    Span s;
+    s.base = w.len - w.n;
+    s.last = (w.row0 + w.rows - 1) / G + 1;
+    s.p0 = s.base + w.row0 / G;
+    s.p1 = s.base + s.last - 1;
+    s.end = max(s.p1 + 1, 0);
+    s.window = a.window, s.sinks = a.sinks;
+    s.wt = a.window ? max(s.p0 - a.window + 1, 0) / kTile : 0;
+    s.ns = a.window ? min((min(a.sinks, s.end) + kTile - 1) / kTile, s.wt) : 0;
+    s.tiles = s.ns + max((s.end + kTile - 1) / kTile - s.wt, 0);
+    return s;
+}
+
+// The sequence's queries and results as those of one tree.
+template <int TERMS>
+__device__ __forceinline__ TreeArgs tree_args(const PagedArgs &a, const Work &w) {
+    constexpr int kBytes = TERMS == 1 ? 2 : 4;
+    TreeArgs t{};
+    t.T = w.n, t.Hq = a.Hq, t.Hkv = a.Hkv, t.scale = a.scale, t.part = a.part;
+    t.q_token = a.q_stride, t.o_token = a.o_stride;
+    t.q = static_cast<const uint8_t *>(a.q) + w.tok0 * a.q_stride * kBytes;
+    t.out = static_cast<uint8_t *>(a.out) + w.tok0 * a.o_stride * kBytes;
+    return t;
+}
+
+// Row j of sequence b in the pool, counted in rows; -1 on a page that is not there.
+__device__ __forceinline__ int64_t pool_row(const PagedArgs &a, int b, int kvh, int j) {
+    const int p = j >> a.shift, page = a.table[(int64_t)b * a.max_pages + p];
+    if (page < 0 || page >= a.n_pages) return -1;
+    return ((int64_t)page * a.Hkv + kvh) * a.ps + (j - (int)((int64_t)p << a.shift));
+}
+
+// Element d of a row of the pool, in fp32.
+template <int HD, bool Q8>
+__device__ __forceinline__ float pool_value(const void *pool, const uint8_t *scales, int64_t row, int d) {
+    if (row < 0) return 0.f;
+    if constexpr (Q8) {
+        const uint32_t code = static_cast<const uint8_t *>(pool)[row * HD + d];
+        return bf_lo(e4m3_values(code, e4m3_factor(scales[row * (HD / 32) + d / 32])).x);
+    } else {
+        return bf_lo(static_cast<const uint16_t *>(pool)[row * HD + d]);
+    }
+}
+
+template <bool Q8, int KU, int VU>
+__device__ __forceinline__ void init_paged(Sync<KU, VU> *y, uint32_t *bad) {
+    for (int i = 0; i < kBadWords; ++i) bad[i] = 0;
+    init_sync(y, Q8 ? kConvWarps / 2 : 1);
+}
+
+__device__ __forceinline__ bool any_bad(const uint32_t *bad) {
+    uint32_t x = 0;
+#pragma unroll
+    for (int i = 0; i < kBadWords; ++i) x |= bad[i];
+    return x != 0;
+}
+
+// A warp's work: tiles from .. to - 1 of a split's K (or V), a box of a page a lane.
+template <int HD, int KU, int VU>
+__device__ __forceinline__ void load_pages(Sync<KU, VU> *y, uint8_t *ring, const CUtensorMap *map, bool is_k,
+                                           const PagedArgs &a, int b, int kvh, const Span &sp, int t0, int from, int to,
+                                           int lane, const Wait &w) {
+    constexpr int kKv = kHalfTile * (HD / 64), kHalves = HD / 64;
+    const int parts = max(kTile >> a.shift, 1), rows = kTile / parts;
+    const int part = lane / kHalves, half = lane % kHalves;
+    const bool mine = lane < parts * kHalves;
+    const int32_t *table = a.table + (int64_t)b * a.max_pages;
+    int at_row = 0, page = a.n_pages;  // of this lane's box
+    auto look = [&](int i) {
+        const int j = sp.tile(t0 + i) * kTile + part * rows;
+        page = a.n_pages;
+        if (mine && j < sp.end) page = table[j >> a.shift];
+        at_row = a.shift < 31 ? j & (a.ps - 1) : j;
+    };
+    if (from < to) look(from);
+    for (int i = from; i < to; ++i) {
+        const bool there = page >= 0 && page < a.n_pages;
+        const int plane = (there ? page : a.n_pages) * a.Hkv + kvh, row = at_row;
+        if (i + 1 < to) look(i + 1);
+        const int u = is_k ? i % KU : i % VU;
+        bool ok = true;
+        if (is_k ? i >= KU : i >= VU) ok = is_k ? s_done(y, i - KU, w) : pv_done(y, i - VU, w);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        uint64_t *bar = is_k ? &y->k_full[u] : &y->v_full[u];
+        if (lane == 0) {
+            mbar_expect_tx(bar, kKv);
+            *(volatile int *)(is_k ? &y->k_issued : &y->v_issued) = i + 1;
+        }
+        __syncwarp();
+        if (mine)
+            tma_load_3d(ring + (is_k ? u : KU + u) * kKv + half * kHalfTile + part * rows * 128, map, half * 64, row,
+                        plane, bar);
+    }
+}
+
+// One of four warps (two for K, two for V, each 64 rows of every tile): codes and
+// powers from the pool, a tile (heads of 64: two) ahead in registers, their bf16 values
+// into the ring, 128-byte swizzled as TMA writes it.
+template <int HD, int KU, int VU>
+__device__ __forceinline__ void convert_pages(Sync<KU, VU> *y, uint8_t *ring, const PagedArgs &a, int b, int kvh,
+                                              const Span &sp, int t0, int nt, int who, int lane, const Wait &w) {
+    constexpr int kKv = kHalfTile * (HD / 64);
+    constexpr int LPR = HD / 16, RPI = 32 / LPR, NI = 64 / RPI, D = 16 / NI;  // lanes a row, rows a load, loads a tile
+    const bool is_k = who < 2;
+    const int half = who & 1, sub = lane / LPR, dim = lane % LPR;
+    const uint8_t *codes = static_cast<const uint8_t *>(is_k ? a.kc : a.vc), *scales = is_k ? a.ks : a.vs;
+    const int32_t *table = a.table + (int64_t)b * a.max_pages;
+    uint4 r[D][NI];
+    uint32_t sc[D][HD / 64];  // the powers of rows 2 * lane and 2 * lane + 1 (a word of both, or one each)
+    // Lane l: where rows 8 (l & 7) .. of its half of tile i lie in the pool; -1: not there.
+    auto look = [&](int i) -> int64_t {
+        const int j = sp.tile(t0 + i) * kTile + half * 64 + (lane & 7) * 8;
+        if (j >= sp.end) return -1;
+        const int p = j >> a.shift, page = table[p];
+        if (page < 0 || page >= a.n_pages) return -1;
+        return ((int64_t)page * a.Hkv + kvh) * a.ps + (j - (int)((int64_t)p << a.shift));
+    };
+    auto fetch = [&](uint4 &x, int64_t group, int k) {
+        const int row = k * RPI + sub;
+        const int64_t at = __shfl_sync(0xFFFFFFFFu, group, row >> 3);
+        x = make_uint4(0, 0, 0, 0);
+        if (at >= 0) x = __ldcs(reinterpret_cast<const uint4 *>(codes + (at + (row & 7)) * HD + dim * 16));
+    };
+    auto fetch_scales = [&](uint32_t (&s)[HD / 64], int64_t group) {
+        const int64_t at = __shfl_sync(0xFFFFFFFFu, group, lane >> 2);
+        const uint8_t *from = scales + (at + 2 * (lane & 3)) * (HD / 32);
+        if constexpr (HD == 64) {
+            s[0] = at >= 0 ? *reinterpret_cast<const uint32_t *>(from) : 0u;
+        } else {
+            const uint2 z = at >= 0 ? *reinterpret_cast<const uint2 *>(from) : make_uint2(0u, 0u);
+            s[0] = z.x, s[1] = z.y;
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (d < nt) {
+            const int64_t group = look(d);
+            fetch_scales(sc[d], group);
+#pragma unroll
+            for (int k = 0; k < NI; ++k) fetch(r[d][k], group, k);
+        }
+    int64_t next = D < nt ? look(D) : -1;
+    for (int i0 = 0; i0 < nt; i0 += D)
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const int i = i0 + d;
+            if (i >= nt) return;
+            const int64_t group = next;  // of tile i + D
+            next = i + D + 1 < nt ? look(i + D + 1) : -1;
+            const int u = is_k ? i % KU : i % VU;
+            bool ok = true;
+            if (is_k ? i >= KU : i >= VU) ok = is_k ? s_done(y, i - KU, w) : pv_done(y, i - VU, w);
+            if (!__all_sync(0xFFFFFFFFu, ok)) return;
+            uint8_t *to = ring + (is_k ? u : KU + u) * kKv + (dim >> 2) * kHalfTile;
+            uint32_t s[HD / 64];
+#pragma unroll
+            for (int e = 0; e < HD / 64; ++e) s[e] = sc[d][e];
+            if (i + D < nt) fetch_scales(sc[d], group);
+#pragma unroll
+            for (int k = 0; k < NI; ++k) {
+                const int row = k * RPI + sub, R = half * 64 + row;
+                uint32_t f;
+                if constexpr (HD == 64) {
+                    f = __shfl_sync(0xFFFFFFFFu, s[0], row >> 1) >> (16 * (row & 1) + 8 * (dim >> 1));
+                } else {
+                    const uint32_t f0 = __shfl_sync(0xFFFFFFFFu, s[0], row >> 1),
+                                   f1 = __shfl_sync(0xFFFFFFFFu, s[HD / 64 - 1], row >> 1);
+                    f = (row & 1 ? f1 : f0) >> (8 * (dim >> 1));
+                }
+                f = e4m3_factor(f & 0xFFu);
+                const uint4 x = r[d][k];
+                const uint2 v0 = e4m3_values(x.x, f), v1 = e4m3_values(x.y, f), v2 = e4m3_values(x.z, f),
+                            v3 = e4m3_values(x.w, f);
+                const uint4 lo = make_uint4(v0.x, v0.y, v1.x, v1.y), hi = make_uint4(v2.x, v2.y, v3.x, v3.y);
+                // (the lanes of a row's second 64 dims, in the same banks, store their halves in the other order)
+                const int ch = 2 * (dim & 3), o = dim >> 2;
+                *reinterpret_cast<uint4 *>(to + R * 128 + (((ch + o) ^ (R & 7)) << 4)) = o ? hi : lo;
+                *reinterpret_cast<uint4 *>(to + R * 128 + (((ch + 1 - o) ^ (R & 7)) << 4)) = o ? lo : hi;
+                if (i + D < nt) fetch(r[d][k], group, k);
+            }
+            async_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(is_k ? &y->k_full[u] : &y->v_full[u]);
+        }
+}
+
+// The products of the V rows that were taken out of their tiles (a value that is no
+// number), element by element for the query rows that see them; a rare case.
+template <int HD, int TERMS, bool SWZ, bool Q8>
+__device__ __noinline__ void add_hidden_rows(const PagedArgs &a, const TreeArgs &t, const Work &wk, const Span &sp, int kvh,
+                                             int G, const uint32_t *bad, const float *mref, float *Os, int tid) {
+    const float c = a.scale * 1.44269504088896340736f;
+    for (int i = tid; i < wk.rows * HD; i += kSoft) {
+        const int r = i / HD, d = i % HD, rg = wk.row0 + r, pos = sp.base + rg / G;
+        const int64_t qat = (rg / G) * t.q_token + (int64_t)(kvh * G + rg % G) * HD;
+        for (int word = 0; word < kBadWords; ++word)
+            for (uint32_t w = bad[word]; w; w &= w - 1) {
+                const int j = sp.tile_of_part(word / 4) * kTile + word % 4 * 32 + __ffs(w) - 1;
+                if (!sp.sees(pos, j)) continue;
+                const int64_t at = pool_row(a, wk.b, kvh, j);
+                float x = 0.f;
+                for (int e = 0; e < HD; ++e) {
+                    float qv;
+                    if constexpr (TERMS == 1)
+                        qv = bf_lo(static_cast<const uint16_t *>(t.q)[qat + e]);
+                    else
+                        qv = static_cast<const float *>(t.q)[qat + e];
+                    x = fmaf(qv, pool_value<HD, Q8>(a.kc, a.ks, at, e), x);
+                }
+                float *o = Os + o_at<HD, SWZ>(r, d);
+                *o = fmaf(ex2(fmaf(x, c, -mref[r])), pool_value<HD, Q8>(a.vc, a.vs, at, d), *o);
+            }
+    }
+}
+
+template <int HD, int TERMS, int NR, bool Q8>
+__global__ void __launch_bounds__(paged_threads(Q8), 1)
+    paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PagedArgs a) {
+    using C = AttnShape<HD, TERMS, NR>;
+    constexpr int kThreads = paged_threads(Q8);
+    constexpr int N = C::N, PT = weight_terms(TERMS), PN = C::PN, KU = C::KU, VU = C::VU;
+    constexpr bool kScaled = TERMS > 1;             // the queries carry the scale already
+    constexpr bool kOnes = HD == 64;                // the sums come out of the second product
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *Ps = sm + C::kOffP, *Qs = sm + C::kOffQ;
+    Sync<KU, VU> *y = reinterpret_cast<Sync<KU, VU> *>(sm + C::kOffMisc);
+    static_assert(sizeof(Sync<KU, VU>) <= 512, "");
+    volatile int *err = &y->err;
+    const Wait wt{err, a.wait_ns, a.wait_sleep};
+    uint32_t *bad = reinterpret_cast<uint32_t *>(sm + C::kOffMisc + 512);  // [kBadWords]
+    float *mref = reinterpret_cast<float *>(bad + kBadWords), *corr = mref + 2 * NR;  // [2][NR] of the groups
+    float *lsum = corr + 2 * NR;                // [NR]
+    float *wtmp = lsum + NR;                    // [2][4][NR]
+    float *Os = reinterpret_cast<float *>(sm);  // [NR][HD], in the ring when the tiles are done
+    float *join = Os + NR * HD;                 // [3][kCluster][NR] behind it
+
+    const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
+    const int S = gridDim.x / a.units, split = blockIdx.x % S, kvh = blockIdx.y, G = a.Hq / a.Hkv;
+    const int turn = a.units - 1 - blockIdx.x / S;  // (a prompt's last rows, the longest, first)
+    const float c = a.scale * 1.44269504088896340736f;  // scores in powers of two
+    pdl_wait();
+    if (!a.part) pdl_trigger();
+    const Work wk = find_work(a, turn, NR, G, lane);
+    const int row0 = wk.row0, rows = wk.rows;
+    const TreeArgs t = tree_args<TERMS>(a, wk);
+    const int first = threadIdx.x - kFirstSoft * 32;
+    if (is_soft(warp)) {
+        // The queries as the B operand: row term * NR + r, 128-byte swizzled. (Rows
+        // behind the sequence's last token are zeros, and columns nobody reads.)
+        for (int i = first; i < NR * (HD / 8); i += kSoft) {
+            const int r = i / (HD / 8), ch = i % (HD / 8);
+            uint4 q[TERMS];
+            load_query8<HD, TERMS>(t, 0, kvh, G, row0 + r, ch, c, q);
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k) {
+                const int n = k * NR + r;
+                *reinterpret_cast<uint4 *>(Qs + (ch / 8) * (N * 128) + n * 128 + (((ch % 8) ^ (n & 7)) << 4)) = q[k];
+            }
+        }
+    }
+    if (rows <= 0) return;  // the whole cluster
+    const Span sp = span_of(a, wk, G);
+    const int t0 = (int)((int64_t)split * sp.tiles / S), nt = (int)((int64_t)(split + 1) * sp.tiles / S) - t0;
+    if (warp == kKWarp) {
+        if (lane == 0) init_paged<Q8>(y, bad);
+        __syncwarp();
+        if constexpr (!Q8) {  // the first copies need nobody else
+            load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 0, min(nt, KU), lane, wt);
+            load_pages<HD>(y, sm, &vmap, false, a, wk.b, kvh, sp, t0, 0, min(nt, VU), lane, wt);
+        }
+    } else if (warp == kMmaWarp) {
+        tmem_alloc(&y->tmem, C::kCols);
+        if constexpr (kOnes)
+            for (int i = lane; i < C::kOnes / 16; i += 32)  // chunk 0 of row i / 8 sits at chunk (row & 7)
+                *reinterpret_cast<uint4 *>(sm + C::kOffOnes + i * 16) =
+                    make_uint4(i % 8 == ((i / 8) & 7) ? 0x3F80u : 0u, 0u, 0u, 0u);
+    } else if (is_soft(warp)) {
+        if (first < 2 * NR) mref[first] = kNone;
+    }
+    async_fence();
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tS = uniform(y->tmem), tO = tS + 2 * N;  // S and O of group g: + g * N, + g * PN
+
+    if (warp >= kFirstConv) {
+        if constexpr (Q8) convert_pages<HD, KU, VU>(y, sm, a, wk.b, kvh, sp, t0, nt, warp - kFirstConv, lane, wt);
+    } else if (!Q8 && warp == kKWarp) {
+        load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, KU, nt, lane, wt);
+    } else if (!Q8 && warp == kVWarp) {
+        load_pages<HD>(y, sm, &vmap, false, a, wk.b, kvh, sp, t0, VU, nt, lane, wt);
+    } else if (warp == kMmaWarp) {
+        constexpr uint32_t idS = idesc_bf16(N, false, false), idO = idesc_bf16(PN, true, true);
+        const uint64_t q = sw128_desc(saddr(Qs), 16);
+        const uint32_t ring = saddr(sm), ones = saddr(sm + C::kOffOnes), p0 = saddr(Ps);
+        auto scores = [&](int i) {
+            const uint64_t k = sw128_desc(ring + (i % KU) * C::kKv, 16);
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk)
+                umma_bf16(tS + (i & 1) * N, k + (((kk / 4) * kHalfTile + (kk % 4) * 32) >> 4),
+                          q + (((kk / 4) * (N * 128) + (kk % 4) * 32) >> 4), idS, kk != 0);
+            umma_commit(&y->k_done[i % KU]);
+        };
+        if (elect()) {
+            bool ok = true;
+            // the scores of tile i (early: once the group has read those of i - 2)
+            for (int i = 0; i < min(nt, C::kAhead) && ok; ++i) {
+                ok = k_full(y, i, wt) && (i < 2 || mbar_wait(&y->s_read[i & 1], ((i >> 1) - 1) & 1, wt));
+                tc_fence_after();
+                if (ok) scores(i);
+            }
+            for (int i = 0; i < nt && ok; ++i) {
+                const int j = i + C::kAhead;
+                if (C::kEarly && j < nt) {
+                    ok = k_full(y, j, wt) && mbar_wait(&y->s_read[j & 1], ((j >> 1) - 1) & 1, wt);
+                    tc_fence_after();
+                    if (ok) scores(j);
+                }
+                // (the k-th product's first atom moves on by 2048 bytes, so the constant
+                // block behind it comes nearer)
+                const uint32_t va = ring + (KU + i % VU) * C::kKv;
+                const uint64_t v = sw128_desc(va, kOnes ? ones - va : kHalfTile);
+                const uint64_t p = sw128_desc(p0 + (i & 1) * C::kP, kHalfTile);
+                if (!(ok = ok && v_full(y, i, wt) && mbar_wait(&y->p_full[i & 3], (i >> 2) & 1, wt))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    umma_bf16(tO + (i & 1) * PN, v + ((kk * 2048) >> 4) - (kOnes ? (uint64_t)((kk * 2048) >> 4) << 16 : 0),
+                              p + ((kk * 2048) >> 4), idO, i >= 2 || kk != 0);
+                umma_commit(&y->v_done[i % VU]);
+                if (!C::kEarly && j < nt) {
+                    ok = k_full(y, j, wt);
+                    tc_fence_after();
+                    if (ok) scores(j);
+                }
+            }
+        }
+    } else if (is_soft(warp)) {
+        // group g takes every other tile; thread: cache row `row` of it, all query rows
+        const int g = (warp - kFirstSoft) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t mylane = (uint32_t)(quarter * 32) << 16;
+        const uint32_t ts = tS + g * N + mylane, to = tO + g * PN + mylane;
+        float *gref = mref + g * NR, *gcorr = corr + g * NR, *gtmp = wtmp + g * 4 * NR;
+        const float4 *m4 = reinterpret_cast<const float4 *>(gref);
+        float l[kOnes ? 1 : NR];
+        if constexpr (!kOnes)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) l[r] = 0.f;
+        bool ok = true;
+        for (int i = g; i < nt; i += 2) {
+            // (a wait that ran out: the loop goes on, its barriers matched, without
+            // another wait, and the result becomes NaN)
+            ok = ok && s_done(y, i, wt);
+            tc_fence_after();
+            float s[TERMS * NR];
+#pragma unroll
+            for (int n = 0; n < N; n += 16) tmem_ld16(ts + n, s + n);
+            tmem_ld_wait();
+            pin<N>(s);
+            if (C::kEarly) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&y->s_read[g]);
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int k = 1; k < TERMS; ++k) s[r] += s[k * NR + r];
+            const int tile = sp.tile(t0 + i), j = tile * kTile + row, part = sp.part(tile);
+            if (part >= 0) {  // not all rows see all of it: columns [lo, hi) see this one
+                int lo, hi;
+                sp.columns(j, G, row0, lo, hi);
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+                    if (r < lo || r >= hi) s[r] = -INFINITY;
+            }
+            // x = s - m in powers of two, and the largest of them
+            float x[NR];
+            auto shift = [&]() {
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int r = 0; r < NR; r += 4) {
+                    const float4 m = m4[r / 4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[r + e] = s[r + e];
+                    fma2(x[r], x[r + 1], kScaled ? 1.f : c, m.x, m.y);
+                    fma2(x[r + 2], x[r + 3], kScaled ? 1.f : c, m.z, m.w);
+                    top[(r / 4) & 3] = fmaxf(fmaxf(fmaxf(x[r], x[r + 1]), fmaxf(x[r + 2], x[r + 3])), top[(r / 4) & 3]);
+                }
+                return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            };
+            const bool raise = group_any(g, shift() > kRaise);
+            // PV(i - 2) is done: P and O are this group's again (not early: S(i) was issued after it)
+            if (C::kEarly && i >= 2) ok = ok && pv_done(y, i - 2, wt);
+            if (raise) {
+                // raise the maxima to those of all cache rows so far
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const float w = max_warp(kScaled ? s[r] : s[r] * c);
+                    if (lane == (r & 31)) gtmp[quarter * NR + r] = w;
+                }
+                group_sync(g);
+                if (row < NR) {
+                    const float old = gref[row];
+                    const float m = fmaxf(fmaxf(fmaxf(gtmp[row], gtmp[NR + row]),
+                                                fmaxf(gtmp[2 * NR + row], gtmp[3 * NR + row])), old);
+                    gcorr[row] = ex2(old - m);
+                    gref[row] = m;
+                }
+                group_sync(g);
+                shift();
+                if constexpr (!kOnes)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) l[r] *= gcorr[r];
+                if (i >= 2) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int n0 = 0; n0 < PN; n0 += 16) {
+                        float o[16];
+                        tmem_ld16(to + n0, o);
+                        tmem_ld_wait();
+                        pin<16>(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= gcorr[n0 % NR + e];
+                        tmem_st16(to + n0, o);
+                    }
+                    tmem_st_wait();
+                }
+            }
+            if (part >= 0) {
+                ok = ok && v_full(y, i, wt);
+                mend_v<HD>(sm + (KU + i % VU) * C::kKv, row, sp.somebody(j) ? part * kTile + row : kBadRows, kBadRows, bad);
+            }
+            // the weights as the B operand: row = cache row, column = term * NR + r
+            uint8_t *p = Ps + g * C::kP + row * 128;
+#pragma unroll
+            for (int r0 = 0; r0 < NR; r0 += 8) {
+                float w[8];
+                uint4 u[PT];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    w[e] = ex2(x[r0 + e]);
+                    if constexpr (!kOnes) l[r0 + e] += w[e];
+                }
+                split8<PT>(w, u);
+#pragma unroll
+                for (int k = 0; k < PT; ++k) {
+                    const int ch = (k * NR + r0) / 8;
+                    *reinterpret_cast<uint4 *>(p + (ch / 8) * kHalfTile + (((ch % 8) ^ (row & 7)) << 4)) = u[k];
+                }
+            }
+            async_fence();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&y->p_full[i & 3]);
+        }
+        if (nt > 0) ok = ok && pv_done(y, nt - 1, wt);  // (and with it every product)
+        tc_fence_after();
+        if constexpr (!kOnes) {
+            // the sums of the 128 cache rows, warp by warp
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                float w = l[r];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
+                if (lane == (r & 31)) gtmp[quarter * NR + r] = w;
+            }
+        }
+        soft_sync();
+        tc_fence_after();  // (a group that passed early reads O behind the barrier, too)
+        // the groups' factors to the larger maximum, which both keep
+        float f0 = 0.f, f1 = 0.f;
+        if (first < NR) {
+            const float m = fmaxf(mref[first], mref[NR + first]);
+            f0 = corr[first] = nt > 0 ? ex2(mref[first] - m) : 0.f;
+            f1 = corr[NR + first] = nt > 1 ? ex2(mref[NR + first] - m) : 0.f;
+            mref[first] = m;
+            if constexpr (!kOnes)
+                lsum[first] = f0 * ((wtmp[first] + wtmp[NR + first]) + (wtmp[2 * NR + first] + wtmp[3 * NR + first])) +
+                            f1 * ((wtmp[4 * NR + first] + wtmp[5 * NR + first]) + (wtmp[6 * NR + first] + wtmp[7 * NR + first]));
+        }
+        soft_sync();
+        // O^T: lane = head dim (lane 64 of a head of 64: the sums), column = term * NR + r
+        if (quarter * 32 < HD || (kOnes && quarter == 2)) {
+#pragma unroll 1
+            for (int r0 = 16 * g; r0 < NR; r0 += 32) {
+                float o[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = 0.f;
+#pragma unroll 1
+                for (int h = 0; h < min(nt, 2); ++h) {
+                    float w[16 * PT];
+#pragma unroll
+                    for (int k = 0; k < PT; ++k) tmem_ld16(tO + h * PN + mylane + k * NR + r0, w + 16 * k);
+                    tmem_ld_wait();
+                    pin<16 * PT>(w);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float z = w[16 * (PT - 1) + e];
+#pragma unroll
+                        for (int k = PT - 2; k >= 0; --k) z += w[16 * k + e];
+                        o[e] = fmaf(corr[h * NR + r0 + e], z, o[e]);
+                    }
+                }
+                if (quarter * 32 < HD) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) Os[(r0 + e) * HD + quarter * 32 + lane] = o[e];
+                } else if (lane == 0) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) lsum[r0 + e] = o[e];
+                }
+            }
+        }
+        soft_sync();
+        if (any_bad(bad)) add_hidden_rows<HD, TERMS, false, Q8>(a, t, wk, sp, kvh, G, bad, mref, Os, first);
+    }
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    if (*err) {  // a wait ran out (nobody waits any more: the same for all threads): the rows are NaN
+        settle(y, a.err);
+        if (tid < NR) lsum[tid] = __uint_as_float(0x7FC00000u);
+        __syncthreads();
+    }
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_free(tS, C::kCols);
+    }
+    finish<HD, TERMS, NR, false, kThreads>(t, (int64_t)turn * a.Hkv + kvh, 0, kvh, G, row0, rows, split, S, Os, mref,
+                                   lsum, join);
+}
+
+template <int HD, int TERMS, bool Q8>
+__global__ void __launch_bounds__(paged_threads(Q8), 1)
+    paged_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                         const PagedArgs a) {
+    using C = RowShape<HD, TERMS, 4 * kBadWords>;
+    constexpr int kThreads = paged_threads(Q8);
+    constexpr int KU = C::KU, VU = C::VU, NB = C::NB, PT = weight_terms(TERMS);
+    constexpr bool kScaled = TERMS > 1;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *Qs = sm + C::kOffQ;
+    Sync<KU, VU> *y = reinterpret_cast<Sync<KU, VU> *>(sm + C::kOffMisc);
+    static_assert(sizeof(Sync<KU, VU>) <= 512, "");
+    volatile int *err = &y->err;
+    const Wait wt{err, a.wait_ns, a.wait_sleep};
+    // [2][128]: the groups' maxima, then the rows' maxima and sums, each written by the thread that read what was there
+    uint32_t *bad = reinterpret_cast<uint32_t *>(sm + C::kOffMisc + 512);  // [kBadWords]
+    float *gm = reinterpret_cast<float *>(bad + kBadWords), *mref = gm, *lsum = gm + kRows;
+    float *Os = reinterpret_cast<float *>(sm);                      // in the ring when the tiles are done,
+    float *join = Os + kRows * HD;                                  // and behind it
+
+    const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
+    const int S = gridDim.x / a.units, split = blockIdx.x % S, kvh = blockIdx.y, G = a.Hq / a.Hkv;
+    const int turn = a.units - 1 - blockIdx.x / S;  // (a prompt's last rows, the longest, first)
+    const float c = a.scale * 1.44269504088896340736f;
+    pdl_wait();
+    if (!a.part) pdl_trigger();
+    const Work wk = find_work(a, turn, kRows, G, lane);
+    const int row0 = wk.row0, rows = wk.rows;
+    const TreeArgs t = tree_args<TERMS>(a, wk);
+    const int row = (warp & 3) * 32 + lane;  // a softmax thread's query row
+    const int st = tid - kFirstSoft * 32;  // a softmax thread's index
+    if (is_soft(warp)) {
+        // the queries as the A operand: term k, 128-byte swizzled rows of 64 dims
+        for (int i = st; i < kRows * (HD / 8); i += kSoft) {
+            const int r = i / (HD / 8), ch = i % (HD / 8);
+            uint4 q[TERMS];
+            load_query8<HD, TERMS>(t, 0, kvh, G, row0 + r, ch, c, q);
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k)
+                *reinterpret_cast<uint4 *>(Qs + k * C::kKv + (ch / 8) * kHalfTile + r * 128 +
+                                           (((ch % 8) ^ (r & 7)) << 4)) = q[k];
+        }
+    }
+    if (rows <= 0) return;  // the whole cluster
+    const Span sp = span_of(a, wk, G);
+    const int t0 = (int)((int64_t)split * sp.tiles / S), nt = (int)((int64_t)(split + 1) * sp.tiles / S) - t0;
+    if (warp == kKWarp) {
+        if (lane == 0) init_paged<Q8>(y, bad);
+        __syncwarp();
+        if constexpr (!Q8) {  // the first copies need nobody else
+            load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 0, min(nt, KU), lane, wt);
+            load_pages<HD>(y, sm, &vmap, false, a, wk.b, kvh, sp, t0, 0, min(nt, VU), lane, wt);
+        }
+    } else if (warp == kMmaWarp) {
+        tmem_alloc(&y->tmem, C::kCols);
+    }
+    async_fence();
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    tc_fence_after();
+    // scores and third terms of tile i: + i % NB * 128, + i % NB * kThird; O of group g: + g * HD
+    const uint32_t tS = uniform(y->tmem), tT = tS + NB * kTile, tO = tT + NB * C::kThird;
+
+    if (warp >= kFirstConv) {
+        if constexpr (Q8) convert_pages<HD, KU, VU>(y, sm, a, wk.b, kvh, sp, t0, nt, warp - kFirstConv, lane, wt);
+    } else if (!Q8 && warp == kKWarp) {
+        load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, KU, nt, lane, wt);
+    } else if (!Q8 && warp == kVWarp) {
+        load_pages<HD>(y, sm, &vmap, false, a, wk.b, kvh, sp, t0, VU, nt, lane, wt);
+    } else if (warp == kMmaWarp) {
+        constexpr uint32_t idS = idesc_bf16(kTile, false, false), idO = idesc_bf16(HD, false, true);
+        const uint64_t q = sw128_desc(saddr(Qs), 16);
+        const uint32_t ring = saddr(sm);
+        auto scores = [&](int i) {
+            const uint64_t k = sw128_desc(ring + (i % KU) * C::kKv, 16);
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                    const uint32_t at = (kk / 4) * kHalfTile + (kk % 4) * 32;
+                    umma_bf16(tS + (i % NB) * kTile, q + ((t * C::kKv + at) >> 4), k + (at >> 4), idS, (t | kk) != 0);
+                }
+            umma_commit(&y->k_done[i % KU]);
+        };
+        if (elect()) {
+            bool ok = true;
+            for (int i = 0; i < min(nt, NB) && (ok = k_full(y, i, wt)); ++i) {
+                tc_fence_after();
+                scores(i);
+            }
+            for (int i = 0; i < nt && ok; ++i) {
+                const int j = i + NB;
+                const uint64_t v = sw128_desc(ring + (KU + i % VU) * C::kKv, kHalfTile);
+                if (!(ok = ok && v_full(y, i, wt) && mbar_wait(&y->p_full[i & 3], (i >> 2) & 1, wt))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int t = 0; t < PT; ++t)
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk) {
+                        const uint32_t p = t < 2 ? tS + (i % NB) * kTile + t * 64 + kk * 8
+                                                 : tT + (i % NB) * C::kThird + kk * 8;
+                        umma_bf16_ta(tO + (i & 1) * HD, p, v + ((kk * 2048) >> 4), idO, i >= 2 || (t | kk) != 0);
+                    }
+                umma_commit(&y->v_done[i % VU]);
+                if (j < nt) {  // (into the buffer of PV(i))
+                    ok = k_full(y, j, wt);
+                    tc_fence_after();
+                    if (ok) scores(j);
+                }
+            }
+        }
+    } else if (is_soft(warp)) {
+        // group g takes every other tile, a thread one query row of it
+        const int g = (warp - kFirstSoft) >> 2, quarter = warp & 3;
+        const uint32_t mylane = (uint32_t)(quarter * 32) << 16;
+        const uint32_t to = tO + g * HD + mylane;
+        const bool live = quarter * 32 < rows;  // (rows behind the last: the warp only keeps the barriers)
+        const int pos = sp.base + (row0 + row) / G;  // the row's token
+        float m = kNone, l = 0.f;
+        bool ok = true;
+        for (int i = g; i < nt; i += 2) {
+            ok = ok && s_done(y, i, wt);
+            tc_fence_after();
+            const uint32_t ts = tS + (i % NB) * kTile + mylane, tt = tT + (i % NB) * C::kThird + mylane;
+            const int tile = sp.tile(t0 + i), at = tile * kTile, part = sp.part(tile);
+            if (live) {
+                float x[kTile];
+#pragma unroll
+                for (int e = 0; e < kTile; e += 16) tmem_ld16(ts + e, x + e);
+                tmem_ld_wait();
+                pin<kTile>(x);
+                if (part >= 0) {
+#pragma unroll
+                    for (int w = 0; w < kTile; w += 32) {
+                        const uint32_t see = sp.sees32(pos, at + w);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((see >> e) & 1)) x[w + e] = -INFINITY;
+                    }
+                }
+                float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < kTile; e += 8)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) t4[w] = fmaxf(fmaxf(t4[w], x[e + 2 * w]), x[e + 2 * w + 1]);
+                float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                if (!kScaled) top *= c;  // (the scale is positive)
+                if (__any_sync(0xFFFFFFFFu, top > m + kRaise)) {
+                    // raise the warp's maxima to those of the rows so far; scale O and the sums
+                    const float best = fmaxf(m, top), scale = ex2(m - best);
+                    m = best;
+                    l *= scale;
+                    if (i >= 2) {
+                        if (NB > 2) ok = ok && pv_done(y, i - 2, wt);  // O is this group's again (NB = 2: S(i) was issued behind it)
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int d = 0; d < HD; d += 16) {
+                            float o[16];
+                            tmem_ld16(to + d, o);
+                            tmem_ld_wait();
+                            pin<16>(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= scale;
+                            tmem_st16(to + d, o);
+                        }
+                    }
+                }
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int w0 = 0; w0 < kTile; w0 += 32) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float &x0 = x[w0 + e], &x1 = x[w0 + e + 1];
+                        fma2(x0, x1, kScaled ? 1.f : c, m, m);
+                        x0 = ex2(x0);
+                        x1 = ex2(x1);
+                        sum[(e >> 1) & 1] = __ffma2_rn(make_float2(x0, x1), make_float2(1.f, 1.f), sum[(e >> 1) & 1]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < PT; ++t) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float &x0 = x[w0 + 2 * e], &x1 = x[w0 + 2 * e + 1];
+                            w[e] = pack_bf16(x0, x1);
+                            if (t + 1 < PT) less2(x0, x1, w[e]);
+                        }
+                        tmem_st16((t < 2 ? ts + t * 64 : tt) + w0 / 2, w);
+                    }
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            if (part >= 0) {
+                ok = ok && v_full(y, i, wt);
+                mend_v<HD>(sm + (KU + i % VU) * C::kKv, row, sp.somebody(at + row) ? part * kTile + row : kBadRows, kBadRows,
+                           bad);
+                async_fence();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&y->p_full[i & 3]);
+        }
+        if (nt > 0) ok = ok && pv_done(y, nt - 1, wt);  // (and with it every product: the ring is free)
+        tc_fence_after();
+        gm[g * kRows + row] = m;
+        soft_sync();
+        tc_fence_after();  // (a group that passed early reads O behind the barrier, too)
+        // the groups' O to the larger maximum: group 0 writes, group 1 adds
+        const float best = fmaxf(m, gm[(g ^ 1) * kRows + row]), scale = g < nt ? ex2(m - best) : 0.f;
+        l *= scale;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            if (g == h) {
+                if (live) {
+#pragma unroll 1
+                    for (int d = 0; d < HD; d += 16) {
+                        float o[16];
+                        if (g < nt) {
+                            tmem_ld16(to + d, o);
+                            tmem_ld_wait();
+                            pin<16>(o);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            float4 *z = reinterpret_cast<float4 *>(Os + o_at<HD, true>(row, d + e));
+                            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (h) w = *z;
+                            w.x = fmaf(scale, o[e], w.x), w.y = fmaf(scale, o[e + 1], w.y);
+                            w.z = fmaf(scale, o[e + 2], w.z), w.w = fmaf(scale, o[e + 3], w.w);
+                            *z = w;
+                        }
+                    }
+                }
+                lsum[row] = h ? lsum[row] + l : l;
+                if (h) mref[row] = best;
+            }
+            soft_sync();
+        }
+        if (any_bad(bad)) add_hidden_rows<HD, TERMS, true, Q8>(a, t, wk, sp, kvh, G, bad, mref, Os, st);
+    }
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    if (*err) {  // a wait ran out (nobody waits any more: the same for all threads): the rows are NaN
+        settle(y, a.err);
+        if (tid < kRows) lsum[tid] = __uint_as_float(0x7FC00000u);
+        __syncthreads();
+    }
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_free(tS, C::kCols);
+    }
+    finish<HD, TERMS, kRows, true, kThreads>(t, (int64_t)turn * a.Hkv + kvh, 0, kvh, G, row0, rows, split, S, Os, mref,
+                                   lsum, join);
+}
+
+// Joins the S splits' partial results of every unit: grid (tiles of rows, kv heads, dims).
+template <int HD, int TERMS, int NR>
+__global__ void __launch_bounds__(256) paged_join(const PagedArgs a, int S) {
+    constexpr int64_t PF = part_floats(NR, HD);
+    __shared__ float ms[max_splits(NR) * NR], wg[max_splits(NR) * NR];
+    const int kvh = blockIdx.y, G = a.Hq / a.Hkv;
+    pdl_begin();  // (behind it the splits' partial results are there)
+    const Work wk = find_work(a, blockIdx.x, NR, G, threadIdx.x & 31);
+    if (wk.rows <= 0) return;
+    const TreeArgs t = tree_args<TERMS>(a, wk);
+    join_splits<HD, TERMS, NR>(t, a.part + ((int64_t)blockIdx.x * a.Hkv + kvh) * S * PF, 0, kvh, G, wk.row0, wk.rows, S, ms,
+                               wg);
+}
+
+}  // namespace mkops

@@ -83,7 +83,7 @@ __device__ __forceinline__ bool mbar_try_for(uint64_t *bar, uint32_t parity, uin
 // Bounded wait on an mbarrier phase; false (and the CTA's error word set) on
 // expiry or when another of its threads gave up. (The first look takes no limit of its
 // own: with one, 65 tiles of 16 rows took 33.6 us instead of 31.2.)
-__device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, const Wait w) {
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, const Wait w) {
     const uint64_t from = gtimer();
     while (!mbar_try_for(bar, parity, w.sleep)) {
         if (*w.err) return false;

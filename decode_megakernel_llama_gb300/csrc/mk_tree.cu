@@ -89,18 +89,22 @@ EncodeTiled encoder() {
     return fn;
 }
 
-// The cache of one layer as [planes][max_seq][hd], boxes of 128 rows x 64
+}  // namespace
+
+// The cache of one layer as [planes][max_seq][hd], boxes of `box` rows x 64
 // dims, 128-byte swizzle. Made for each call (it holds the address).
-bool cache_map(CUtensorMap *map, const void *cache, int planes, int max_seq, int hd) {
+bool cache_map(CUtensorMap *map, const void *cache, int planes, int max_seq, int hd, int box_rows) {
     const EncodeTiled enc = encoder();
     if (!enc) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)max_seq, (cuuint64_t)planes};
     const cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)max_seq * hd * 2};
-    const cuuint32_t box[3] = {64, kTile, 1}, one[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(cache), dims, strides, box, one,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // How a call splits the cache rows of its (row tile, sequence, kv head) units:
 // S CTAs of one cluster, or (ws) S CTAs whose partial results go through the
@@ -114,55 +118,16 @@ struct Plan {
 // The two kernels by what their launch needs.
 template <int HD_, int TERMS_, int NR_>
 struct Few {
-    static constexpr int HD = HD_, TERMS = TERMS_, NR = NR_, kSmem = AttnShape<HD, TERMS, NR>::kSmem;
+    static constexpr int kThreads = kAttnThreads, HD = HD_, TERMS = TERMS_, NR = NR_, kSmem = AttnShape<HD, TERMS, NR>::kSmem;
     static constexpr double kTileUs = (HD == 64 ? 0.6 : 1.0) - (TERMS == 1 ? HD / 64 * 0.1 : 0.0), kFixedUs = 5.0, kJoinUs = 4.5;
     static auto fn() { return tree_attention<HD, TERMS, NR>; }
 };
 template <int HD_, int TERMS_>
 struct Many {
-    static constexpr int HD = HD_, TERMS = TERMS_, NR = kRows, kSmem = RowShape<HD, TERMS>::kSmem;
+    static constexpr int kThreads = kAttnThreads, HD = HD_, TERMS = TERMS_, NR = kRows, kSmem = RowShape<HD, TERMS>::kSmem;
     static constexpr double kTileUs = HD == 64 && TERMS == 1 ? 0.8 : 1.2, kFixedUs = 6.5, kJoinUs = 7.0;
     static auto fn() { return tree_attention_rows<HD, TERMS>; }
 };
-
-template <class K>
-cudaError_t configure() {
-    // (function attributes are per device: set once for each)
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1))) return e;
-    e = cudaFuncSetAttribute(K::fn(), cudaFuncAttributeMaxDynamicSharedMemorySize, K::kSmem);
-    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
-    return e;
-}
-
-// Clusters of 2^k CTAs, one an SM, that the current device holds at once (asked of
-// the runtime once for each device).
-template <class K>
-int active_clusters(int k, int n_sm) {
-    static_assert(2 * K::kSmem > kSmemMost, "one CTA an SM");
-    static std::atomic<int> known[64][4];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) n = known[dev][k].load(std::memory_order_relaxed);
-    if (n) return n;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1 << k;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(1 << k, n_sm * 4);
-    cfg.blockDim = dim3(kAttnThreads);
-    cfg.dynamicSmemBytes = K::kSmem;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (configure<K>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, K::fn(), &cfg) != cudaSuccess || n < 1) {
-        (void)cudaGetLastError();
-        return n_sm >> k;  // (not kept: the next call asks again)
-    }
-    if (dev < 64) known[dev][k].store(n, std::memory_order_relaxed);
-    return n;
-}
 
 // The split with the least estimated time, in microseconds: waves of resident
 // CTAs x (the tiles of a split x K::kTileUs + a fixed part). The tile times are
@@ -212,8 +177,8 @@ cudaError_t launch(TreeArgs a, int max_len, int n_sm, cudaStream_t s, int64_t *w
     if (a.wait_ns == 0) a.wait_ns = kWaitNs;
     a.wait_sleep = (uint32_t)std::min<uint64_t>(a.wait_ns, kSleepNs);
     CUtensorMap kmap, vmap;
-    if (!cache_map(&kmap, a.kc, a.slots * a.Hkv, a.max_seq, K::HD) ||
-        !cache_map(&vmap, a.vc, a.slots * a.Hkv, a.max_seq, K::HD))
+    if (!cache_map(&kmap, a.kc, a.slots * a.Hkv, a.max_seq, K::HD, kTile) ||
+        !cache_map(&vmap, a.vc, a.slots * a.Hkv, a.max_seq, K::HD, kTile))
         return cudaErrorInvalidValue;
     e = launch_op(K::fn(), dim3(p.S, a.B * a.Hkv, row_tiles), kAttnThreads, K::kSmem, p.ws ? 1 : p.S, s, kmap, vmap, a);
     if (e != cudaSuccess || !p.ws) return e;

@@ -71,6 +71,8 @@
 #pragma once
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "mk_ops.h"
 #include "mk_tc.cuh"
 
@@ -273,14 +275,15 @@ struct Sync {
     uint32_t bad[2];              // drafted rows taken out of the second product
 };
 
+// (landers: arrivals that make a tile of K, or of V, full)
 template <int KU, int VU>
-__device__ __forceinline__ void init_sync(Sync<KU, VU> *y) {
+__device__ __forceinline__ void init_sync(Sync<KU, VU> *y, int landers = 1) {
     for (int u = 0; u < KU; ++u) {
-        mbar_init(&y->k_full[u], 1);
+        mbar_init(&y->k_full[u], landers);
         mbar_init(&y->k_done[u], 1);
     }
     for (int u = 0; u < VU; ++u) {
-        mbar_init(&y->v_full[u], 1);
+        mbar_init(&y->v_full[u], landers);
         mbar_init(&y->v_done[u], 1);
     }
     for (int g = 0; g < 2; ++g) {
@@ -376,20 +379,20 @@ __device__ __noinline__ void settle(Sync<KU, VU> *y, int *status) {
 // What a CTA does with its partial result (O in Os, maxima, sums): leaves it
 // in the workspace for tree_join, or joins it with the cluster's other splits:
 // first every split's maxima and sums, then the rows, shared out over the CTAs.
-template <int HD, int TERMS, int NR, bool SWZ>
-__device__ __forceinline__ void finish(const TreeArgs &a, int b, int kvh, int G, int row0, int rows, int split, int S,
-                                       float *Os, float *mref, float *lsum, float *join) {
+// (unit: its number in the workspace; NT: the CTA's threads)
+template <int HD, int TERMS, int NR, bool SWZ, int NT = kAttnThreads>
+__device__ __forceinline__ void finish(const TreeArgs &a, int64_t unit, int b, int kvh, int G, int row0, int rows,
+                                       int split, int S, float *Os, float *mref, float *lsum, float *join) {
     namespace cg = cooperative_groups;
     const int tid = threadIdx.x;
     if (a.part) {
         pdl_trigger();  // (brought in earlier, tree_join's CTAs stand in the tiles' way: 86.6 -> 88.7 us at 131k rows)
-        const int64_t unit = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
         float *p = a.part + (unit * S + split) * part_floats(NR, HD);
-        for (int i = tid; i < rows * (HD / 4); i += kAttnThreads) {
+        for (int i = tid; i < rows * (HD / 4); i += NT) {
             const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
             reinterpret_cast<float4 *>(p)[i] = *reinterpret_cast<const float4 *>(Os + o_at<HD, SWZ>(r, d));
         }
-        for (int r = tid; r < rows; r += kAttnThreads) {
+        for (int r = tid; r < rows; r += NT) {
             p[NR * HD + r] = mref[r];
             p[NR * HD + NR + r] = lsum[r];
         }
@@ -398,12 +401,12 @@ __device__ __forceinline__ void finish(const TreeArgs &a, int b, int kvh, int G,
     float *wgt = join, *m8 = wgt + kCluster * NR, *l8 = m8 + kCluster * NR;
     cg::cluster_group cl = cg::this_cluster();
     if (S > 1) cl.sync();
-    for (int i = tid; i < S * NR; i += kAttnThreads) {
+    for (int i = tid; i < S * NR; i += NT) {
         m8[i] = *cl.map_shared_rank(mref + i % NR, i / NR);
         l8[i] = *cl.map_shared_rank(lsum + i % NR, i / NR);
     }
     __syncthreads();
-    for (int r = tid; r < rows; r += kAttnThreads) {
+    for (int r = tid; r < rows; r += NT) {
         float m = kNone, sum = 0.f;
         for (int s = 0; s < S; ++s) m = fmaxf(m, m8[s * NR + r]);
         for (int s = 0; s < S; ++s) sum = fmaf(ex2(m8[s * NR + r] - m), l8[s * NR + r], sum);
@@ -411,7 +414,7 @@ __device__ __forceinline__ void finish(const TreeArgs &a, int b, int kvh, int G,
         for (int s = 0; s < S; ++s) wgt[s * NR + r] = ex2(m8[s * NR + r] - m) * inv;
     }
     __syncthreads();
-    for (int i = split * kAttnThreads + tid; i < rows * (HD / 4); i += S * kAttnThreads) {
+    for (int i = split * NT + tid; i < rows * (HD / 4); i += S * NT) {
         const int r = i / (HD / 4), d = 4 * (i % (HD / 4)), rg = row0 + r;
         float4 o[kCluster];
 #pragma unroll
@@ -798,7 +801,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tc_fence_after();
         tmem_free(tS, C::kCols);
     }
-    finish<HD, TERMS, NR, false>(a, b, kvh, G, row0, rows, split, S, Os, mref, lsum, join);
+    finish<HD, TERMS, NR, false>(a, (int64_t)blockIdx.z * gridDim.y + blockIdx.y, b, kvh, G, row0, rows, split, S, Os, mref,
+                                   lsum, join);
 }
 
 constexpr int kRows = 128;
@@ -811,7 +815,8 @@ __device__ __forceinline__ uint32_t seen32(uint64_t word, int first) {
     return first > -32 ? (uint32_t)(word << -first) | ((1u << -first) - 1u) : 0xFFFFFFFFu;
 }
 
-template <int HD, int TERMS>
+// (EXTRA: bytes of the caller's own behind the barriers)
+template <int HD, int TERMS, int EXTRA = 0>
 struct RowShape {
     static constexpr int kKv = kHalfTile * (HD / 64);
     static constexpr int kQ = TERMS * kKv;  // 128 rows x HD a term
@@ -822,7 +827,7 @@ struct RowShape {
     // 44.3 us).
     static constexpr int kThird = TERMS > 2 ? kTile / 2 : 0, kCols = 512;
     static constexpr int NB = (kCols - 2 * HD) / (kTile + kThird) > 2 ? 3 : 2;
-    static constexpr int kMisc = 512 + 2 * 4 * kRows;
+    static constexpr int kMisc = 512 + EXTRA + 2 * 4 * kRows;
     static constexpr int kRoom = (kSmemMost - 1024 - kQ - kMisc) / kKv;
     static constexpr int KU = (kRoom + 1) / 2 > 6 ? 6 : (kRoom + 1) / 2, VU = kRoom / 2 > 6 ? 6 : kRoom / 2;
     static constexpr int kOffQ = (KU + VU) * kKv, kOffMisc = kOffQ + kQ;
@@ -1088,22 +1093,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tc_fence_after();
         tmem_free(tS, C::kCols);
     }
-    finish<HD, TERMS, kRows, true>(a, b, kvh, G, row0, rows, split, S, Os, mref, lsum, join);
+    finish<HD, TERMS, kRows, true>(a, (int64_t)blockIdx.z * gridDim.y + blockIdx.y, b, kvh, G, row0, rows, split, S, Os, mref,
+                                   lsum, join);
 }
 
-// Joins the S splits' partial results of every (row tile, sequence, kv head):
-// grid (row tiles, batch * Hkv), a thread per four dims of a row.
+// A CTA's share (blockIdx.z of gridDim.z) of joining the S partial results at p of `rows` rows.
 template <int HD, int TERMS, int NR>
-__global__ void __launch_bounds__(256) tree_join(const TreeArgs a, int S) {
+__device__ __forceinline__ void join_splits(const TreeArgs &a, const float *p, int b, int kvh, int G, int row0, int rows,
+                                            int S, float *ms, float *wg) {
     constexpr int64_t PF = part_floats(NR, HD);
-    __shared__ float ms[max_splits(NR) * NR], wg[max_splits(NR) * NR];
-    const int b = blockIdx.y / a.Hkv, kvh = blockIdx.y % a.Hkv, G = a.Hq / a.Hkv, row0 = blockIdx.x * NR;
-    pdl_begin();  // (behind it the splits' partial results are there)
-    const Seq sq = sequence(a, b);
-    const int rows = min(NR, sq.n * G - row0);
-    if (rows <= 0) return;
-    const int64_t unit = (int64_t)blockIdx.x * gridDim.y + blockIdx.y;
-    const float *p = a.part + unit * S * PF;
     for (int i = threadIdx.x; i < S * NR; i += 256) {
         const bool in = i % NR < rows;
         ms[i] = in ? p[(i / NR) * PF + NR * HD + i % NR] : kNone;
@@ -1136,6 +1134,64 @@ __global__ void __launch_bounds__(256) tree_join(const TreeArgs a, int S) {
         }
         put4<TERMS>(a, b * a.o_batch + (rg / G) * a.o_token + (int64_t)(kvh * G + rg % G) * HD + d, y);
     }
+}
+
+// Joins the S splits' partial results of every (row tile, sequence, kv head):
+// grid (row tiles, batch * Hkv), a thread per four dims of a row.
+template <int HD, int TERMS, int NR>
+__global__ void __launch_bounds__(256) tree_join(const TreeArgs a, int S) {
+    constexpr int64_t PF = part_floats(NR, HD);
+    __shared__ float ms[max_splits(NR) * NR], wg[max_splits(NR) * NR];
+    const int b = blockIdx.y / a.Hkv, kvh = blockIdx.y % a.Hkv, G = a.Hq / a.Hkv, row0 = blockIdx.x * NR;
+    pdl_begin();  // (behind it the splits' partial results are there)
+    const Seq sq = sequence(a, b);
+    const int rows = min(NR, sq.n * G - row0);
+    if (rows <= 0) return;
+    const int64_t unit = (int64_t)blockIdx.x * gridDim.y + blockIdx.y;
+    const float *p = a.part + unit * S * PF;
+    join_splits<HD, TERMS, NR>(a, p, b, kvh, G, row0, rows, S, ms, wg);
+}
+
+// ---- host: what the launches of these kernels share. K: a kernel's fn(), kSmem, kThreads.
+bool cache_map(CUtensorMap *map, const void *cache, int planes, int max_seq, int hd, int box_rows);
+
+template <class K>
+cudaError_t configure() {
+    // (function attributes are per device: set once for each)
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(K::fn(), cudaFuncAttributeMaxDynamicSharedMemorySize, K::kSmem);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
+}
+
+// Clusters of 2^k CTAs, one an SM, that the current device holds at once (asked of
+// the runtime once for each device).
+template <class K>
+int active_clusters(int k, int n_sm) {
+    static_assert(2 * K::kSmem > kSmemMost, "one CTA an SM");
+    static std::atomic<int> known[64][4];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) n = known[dev][k].load(std::memory_order_relaxed);
+    if (n) return n;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1 << k;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(1 << k, n_sm * 4);
+    cfg.blockDim = dim3(K::kThreads);
+    cfg.dynamicSmemBytes = K::kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (configure<K>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, K::fn(), &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        return n_sm >> k;  // (not kept: the next call asks again)
+    }
+    if (dev < 64) known[dev][k].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 }  // namespace mkops

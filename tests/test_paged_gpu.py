@@ -74,7 +74,9 @@ class Paged:
         assert bool((self.out[count:] == 7.0).all()), "rows behind the last sequence were written"
         got, want, tol = self.out[:count].double(), want[:count], tol[:count]
         odd = ~torch.isfinite(want)
-        assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got[odd].nan_to_num(9.0), want[odd].nan_to_num(9.0))
+        # (an infinite value that a token sees times a weight's lower terms, zeros or of the other sign, is no number:
+        # the result is not finite where the formula's is not)
+        assert torch.equal(torch.isfinite(got), ~odd)
         bad = ((got - want).abs() > tol) & ~odd
         assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} off, worst {float(((got - want).abs() / tol)[~odd].max())} bounds, {outside.sum()}"
 
@@ -140,7 +142,7 @@ def test_bounds_that_are_exceeded_only_choose_the_launch():
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("new,window", [(5, 0), (5, 40), (150, 0), (150, 60)])
 def test_rows_that_some_tokens_see_may_hold_anything(type, cache, hd, new, window):
-    """A token that does not see a row is not touched by its NaN or infinities, and one that sees it has them."""
+    """A token that does not see a row is not touched by its NaN or infinities; one that sees it is not finite there."""
     p = Paged([400], [new], 4, 2, hd, 16, type, cache, window, 2, seed=6)
     for j in (400 - new + 1, 400 - new // 2, 399, 400 - new - 20):
         page, row = int(p.table[0, j // 16]), j % 16
