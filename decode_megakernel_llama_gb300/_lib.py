@@ -104,7 +104,7 @@ _PAGES_ARGS = struct.Struct("@10i10P")
 
 
 _lib = None
-_quick = None  # the extension module of the drafted-tree operators (csrc/mk_torch.cpp)
+_quick = None  # the extension module of the standalone operators (csrc/mk_torch.cpp)
 _loading = threading.RLock()
 _VP = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -180,8 +180,8 @@ def _load(path: str | None):
 
 
 def load_extension():
-    """Loads the extension module of the drafted-tree operators (rope_append, tree_attention, kv_compact, kv_reorder),
-    which their first call does otherwise, and gives it the library's entry points. Nothing else needs it."""
+    """Loads the extension module of the drafted-tree operators (rope_append, tree_attention, kv_compact, kv_reorder)
+    and of those of pages (paged_attention, rope_append_e4m3, kv_write_pages, kv_read_pages), which their first call does otherwise, and gives it the library's entry points. Nothing else needs it."""
     global _quick
     with _loading:
         if _quick is None:
@@ -196,7 +196,8 @@ def load_extension():
             spec.loader.exec_module(mod)
             mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 L.mk_rope_append, L.mk_tree_attention, L.mk_tree_attention_workspace, L.mk_kv_compact,
-                L.mk_kv_reorder)))
+                L.mk_kv_reorder, L.mk_paged_attention, L.mk_paged_attention_workspace, L.mk_rope_append_e4m3,
+                L.mk_kv_write_pages, L.mk_kv_read_pages)))
             _quick = mod
     return _quick
 
@@ -635,6 +636,14 @@ def paged_attention(q, k_pages, v_pages, table, starts, lengths, out, scale: flo
     the rows up to its own, with a window the last `window` of them and the first `sinks`. scale defaults to
     1 / sqrt(hd). max_new, max_len: bounds on a sequence's tokens and rows, for the choice of the launch alone.
     status, wait_ns and the workspace: as in tree_attention."""
+    rc = (_quick or load_extension()).paged_attention(q, k_pages, v_pages, table, starts, lengths, out, scale, window,
+                                                   sinks, k_scales, v_scales, max_new, max_len, status, stream,
+                                                   wait_ns)
+    if rc == MK_OK:
+        return
+    if rc < 0:
+        check(rc)
+    # not done: something is wrong, or the call is for another stream or device
     import torch
     i32, dt = torch.int32, _io_dtype(torch, q, "q")
     if q.dim() != 3 or table.dim() != 2:
@@ -684,6 +693,14 @@ def rope_append_e4m3(qkv, q_out, k_pages, v_pages, k_scales, v_scales, positions
     """mk_rope_append_e4m3 on CUDA tensors: rope_append with 8-bit caches, k_pages / v_pages float8_e4m3fn
     [slots][Hkv][rows][hd] with k_scales / v_scales uint8 [slots][Hkv][rows][hd / 32]. With a pool of pages slots are
     the tokens' pages, rows their rows in them."""
+    rc = (_quick or load_extension()).rope_append_e4m3(qkv, q_out, k_pages, v_pages, positions, rows, inv_freq, slots,
+                                                    q_norm, k_norm, eps, mscale, interleaved, stream, k_scales,
+                                                    v_scales)
+    if rc == MK_OK:
+        return
+    if rc < 0:
+        check(rc)
+    # not done: something is wrong, or the call is for another stream or device
     import torch
     bf, i32, dt = torch.bfloat16, torch.int32, _io_dtype(torch, qkv, "qkv")
     if k_pages.dim() != 4 or q_out.dim() != 3 or qkv.dim() != 2 or inv_freq.dim() != 1:
@@ -715,7 +732,14 @@ def rope_append_e4m3(qkv, q_out, k_pages, v_pages, k_scales, v_scales, positions
     _run_on(torch, qkv.get_device(), stream, load().mk_rope_append_e4m3, rec, k_scales.data_ptr(), v_scales.data_ptr())
 
 
-def _move_pages(fn, k, v, k_pages, v_pages, table, lengths, slots, first, k_scales, v_scales, stream) -> None:
+def _move_pages(name, k, v, k_pages, v_pages, table, lengths, slots, first, k_scales, v_scales, stream) -> None:
+    rc = getattr(_quick or load_extension(), name)(k, v, k_pages, v_pages, table, lengths, slots, first, k_scales, v_scales,
+                                                   stream)
+    if rc == MK_OK:
+        return
+    if rc < 0:
+        check(rc)
+    # not done: something is wrong, or the call is for another stream or device
     import torch
     bf, i32 = torch.bfloat16, torch.int32
     if k.dim() != 5 or table.dim() != 2:
@@ -738,7 +762,7 @@ def _move_pages(fn, k, v, k_pages, v_pages, table, lengths, slots, first, k_scal
     rec = _PAGES_ARGS.pack(L, slots_n, Hkv, S, hd, P, ps, cache, B, M, k.data_ptr(), v.data_ptr(), k_pages.data_ptr(),
                            v_pages.data_ptr(), _at(k_scales), _at(v_scales), table.data_ptr(), lengths.data_ptr(),
                            _at(first), _at(slots))
-    _run_on(torch, k.get_device(), stream, fn, rec)
+    _run_on(torch, k.get_device(), stream, getattr(load(), "mk_" + name), rec)
 
 
 def kv_write_pages(k, v, k_pages, v_pages, table, lengths, slots=None, first=None, k_scales=None, v_scales=None,
@@ -746,14 +770,14 @@ def kv_write_pages(k, v, k_pages, v_pages, table, lengths, slots=None, first=Non
     """mk_kv_write_pages on CUDA tensors: rows first[b] (0) .. lengths[b] - 1 of cache slot slots[b] (b) of k / v
     bfloat16 [L][B][Hkv][max_seq][hd] to the pages table[b] of k_pages / v_pages [L][pages][Hkv][rows][hd], bfloat16 or
     float8_e4m3fn with k_scales / v_scales uint8 [L][pages][Hkv][rows][hd / 32]."""
-    _move_pages(load().mk_kv_write_pages, k, v, k_pages, v_pages, table, lengths, slots, first, k_scales, v_scales, stream)
+    _move_pages("kv_write_pages", k, v, k_pages, v_pages, table, lengths, slots, first, k_scales, v_scales, stream)
 
 
 def kv_read_pages(k_pages, v_pages, k, v, table, lengths, slots=None, first=None, k_scales=None, v_scales=None,
                   stream=None) -> None:
     """mk_kv_read_pages on CUDA tensors: the way back of kv_write_pages; 8-bit rows become the bfloat16 values that
     they stand for, exactly."""
-    _move_pages(load().mk_kv_read_pages, k, v, k_pages, v_pages, table, lengths, slots, first, k_scales, v_scales, stream)
+    _move_pages("kv_read_pages", k, v, k_pages, v_pages, table, lengths, slots, first, k_scales, v_scales, stream)
 
 
 class Megakernel:

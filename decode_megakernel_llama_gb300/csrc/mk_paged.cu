@@ -26,7 +26,7 @@ namespace {
 // launch, set-up and end; kJoinUs: the workspace's second launch.
 template <int HD_, int TERMS_, int NR_, bool Q8_>
 struct PagedFew {
-    static constexpr int kThreads = paged_threads(Q8_), HD = HD_, TERMS = TERMS_, NR = NR_,
+    static constexpr int kThreads = paged_threads(false, Q8_), HD = HD_, TERMS = TERMS_, NR = NR_,
                          kSmem = AttnShape<HD, TERMS, NR>::kSmem;
     static constexpr bool Q8 = Q8_;
     static constexpr double kTileUs = (HD == 64 ? 0.6 : 1.0) - (TERMS == 1 ? HD / 64 * 0.1 : 0.0), kFixedUs = 5.0, kJoinUs = 4.5;
@@ -34,7 +34,7 @@ struct PagedFew {
 };
 template <int HD_, int TERMS_, bool Q8_>
 struct PagedMany {
-    static constexpr int kThreads = paged_threads(Q8_), HD = HD_, TERMS = TERMS_, NR = kRows,
+    static constexpr int kThreads = paged_threads(true, Q8_), HD = HD_, TERMS = TERMS_, NR = kRows,
                          kSmem = RowShape<HD, TERMS, 4 * kBadWords>::kSmem;
     static constexpr bool Q8 = Q8_;
     static constexpr double kTileUs = HD == 64 && TERMS == 1 ? 0.8 : 1.2, kFixedUs = 6.5, kJoinUs = 7.0;

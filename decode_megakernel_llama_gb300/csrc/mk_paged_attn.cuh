@@ -12,7 +12,7 @@
 //   - tiles that no row of the CTA sees (behind the last token, before the window)
 //     are not visited, those that all rows see whole take no mask; the others, five at
 //     most (Span), select scores and clean V;
-//   - 8-bit pages (Q8): four more warps read codes and powers, put the bf16 values,
+//   - 8-bit pages (Q8): eight more warps read codes and powers, put the bf16 values,
 //     which are exact, where TMA puts them, and from there on all is as with bf16.
 //     So their products are those of the bf16 kernel and only the bytes are half.
 #pragma once
@@ -20,11 +20,21 @@
 
 namespace mkops {
 
-constexpr int kFirstConv = kFirstSoft + kSoftWarps, kConvWarps = 4;
+// Threads: four warps for products and copies, the softmax warps (few rows: two groups of
+// four; many: of eight, two to 32 rows), and for 8-bit pages those that convert them.
+constexpr int kRowSoft = 512;
+__host__ __device__ constexpr int soft_threads(bool many) { return many ? kRowSoft : kSoft; }
+__host__ __device__ constexpr int conv_warps(bool many) { return many ? 4 : 8; }
 constexpr int kParts = 5, kBadRows = kParts * kTile, kBadWords = kBadRows / 32;
 
-__host__ __device__ constexpr int paged_threads(bool q8) { return kAttnThreads + (q8 ? 32 * kConvWarps : 0); }
-__device__ __forceinline__ bool is_soft(int warp) { return warp >= kFirstSoft && warp < kFirstSoft + kSoftWarps; }
+__host__ __device__ constexpr int first_conv(bool many) { return kFirstSoft + soft_threads(many) / 32; }
+__host__ __device__ constexpr int paged_threads(bool many, bool q8) {
+    return 32 * (first_conv(many) + (q8 ? conv_warps(many) : 0));
+}
+template <bool MANY>
+__device__ __forceinline__ bool is_soft(int warp) {
+    return warp >= kFirstSoft && warp < first_conv(MANY);
+}
 
 // A CTA's rows: query rows row0 .. row0 + rows - 1 of sequence b (row = token of the
 // sequence * G + head of the group), whose n tokens begin at tok0 of the call's.
@@ -150,10 +160,10 @@ __device__ __forceinline__ float pool_value(const void *pool, const uint8_t *sca
     }
 }
 
-template <bool Q8, int KU, int VU>
+template <bool MANY, bool Q8, int KU, int VU>
 __device__ __forceinline__ void init_paged(Sync<KU, VU> *y, uint32_t *bad) {
     for (int i = 0; i < kBadWords; ++i) bad[i] = 0;
-    init_sync(y, Q8 ? kConvWarps / 2 : 1);
+    init_sync(y, Q8 ? conv_warps(MANY) / 2 : 1, soft_threads(MANY) / 64);
 }
 
 __device__ __forceinline__ bool any_bad(const uint32_t *bad) {
@@ -201,104 +211,101 @@ __device__ __forceinline__ void load_pages(Sync<KU, VU> *y, uint8_t *ring, const
     }
 }
 
-// One of four warps (two for K, two for V, each 64 rows of every tile): codes and
-// powers from the pool, a tile (heads of 64: two) ahead in registers, their bf16 values
-// into the ring, 128-byte swizzled as TMA writes it.
-template <int HD, int KU, int VU>
+// One of W warps (half of them for K, half for V, each its rows of every tile): codes and
+// powers from the pool, R loads ahead in registers, their bf16 values into the ring,
+// 128-byte swizzled as TMA writes it. A lane has 16 elements of CH consecutive rows.
+template <int HD, int KU, int VU, int W, int R>
 __device__ __forceinline__ void convert_pages(Sync<KU, VU> *y, uint8_t *ring, const PagedArgs &a, int b, int kvh,
                                               const Span &sp, int t0, int nt, int who, int lane, const Wait &w) {
-    constexpr int kKv = kHalfTile * (HD / 64);
-    constexpr int LPR = HD / 16, RPI = 32 / LPR, NI = 64 / RPI, D = 16 / NI;  // lanes a row, rows a load, loads a tile
-    const bool is_k = who < 2;
-    const int half = who & 1, sub = lane / LPR, dim = lane % LPR;
-    const uint8_t *codes = static_cast<const uint8_t *>(is_k ? a.kc : a.vc), *scales = is_k ? a.ks : a.vs;
+    constexpr int kKv = kHalfTile * (HD / 64), kWarpRows = 2 * kTile / W;
+    constexpr int LPR = HD / 16, CH = kWarpRows * LPR / 32;       // lanes of a row, rows of a lane
+    constexpr int BN = R < CH ? (R < 8 ? R : 8) : CH, D = R / BN;  // rows of a batch, batches in flight
+    constexpr int BT = CH / BN, SW = BN * HD / 128;               // batches of a tile, words of a batch's powers
+    static_assert(R % BN == 0 && CH % BN == 0 && BN <= 8 && SW % 2 == 0, "");
+    const bool is_k = who < W / 2;
+    const int sub = lane / LPR, dim = lane % LPR, first = (who & (W / 2 - 1)) * kWarpRows + sub * CH;
+    const uint8_t *codes = static_cast<const uint8_t *>(is_k ? a.kc : a.vc) + dim * 16, *scales = is_k ? a.ks : a.vs;
     const int32_t *table = a.table + (int64_t)b * a.max_pages;
-    uint4 r[D][NI];
-    uint32_t sc[D][HD / 64];  // the powers of rows 2 * lane and 2 * lane + 1 (a word of both, or one each)
-    // Lane l: where rows 8 (l & 7) .. of its half of tile i lie in the pool; -1: not there.
-    auto look = [&](int i) -> int64_t {
-        const int j = sp.tile(t0 + i) * kTile + half * 64 + (lane & 7) * 8;
+    uint64_t *full = is_k ? y->k_full : y->v_full;
+    const int units = is_k ? KU : VU, batches = nt * BT;
+    uint4 r[D][BN];
+    uint32_t sc[D][SW];
+    // Where the lane's rows of batch m lie in the pool; -1: not there. (Pages of 8-bit rows
+    // hold multiples of 8 rows, so the rows of a batch are of one page.)
+    auto look = [&](int m) -> int64_t {
+        if (m >= batches) return -1;
+        const int j = sp.tile(t0 + m / BT) * kTile + first + m % BT * BN;
         if (j >= sp.end) return -1;
         const int p = j >> a.shift, page = table[p];
         if (page < 0 || page >= a.n_pages) return -1;
         return ((int64_t)page * a.Hkv + kvh) * a.ps + (j - (int)((int64_t)p << a.shift));
     };
-    auto fetch = [&](uint4 &x, int64_t group, int k) {
-        const int row = k * RPI + sub;
-        const int64_t at = __shfl_sync(0xFFFFFFFFu, group, row >> 3);
+    auto fetch_scales = [&](uint32_t (&s)[SW], int64_t at) {
+#pragma unroll
+        for (int e = 0; e < SW; e += 2) {
+            uint2 z = make_uint2(0u, 0u);
+            if (at >= 0) z = *reinterpret_cast<const uint2 *>(scales + at * (HD / 32) + 4 * e);
+            s[e] = z.x, s[e + 1] = z.y;
+        }
+    };
+    auto fetch = [&](uint4 &x, int64_t at, int k) {
         x = make_uint4(0, 0, 0, 0);
-        if (at >= 0) x = __ldcs(reinterpret_cast<const uint4 *>(codes + (at + (row & 7)) * HD + dim * 16));
-    };
-    auto fetch_scales = [&](uint32_t (&s)[HD / 64], int64_t group) {
-        const int64_t at = __shfl_sync(0xFFFFFFFFu, group, lane >> 2);
-        const uint8_t *from = scales + (at + 2 * (lane & 3)) * (HD / 32);
-        if constexpr (HD == 64) {
-            s[0] = at >= 0 ? *reinterpret_cast<const uint32_t *>(from) : 0u;
-        } else {
-            const uint2 z = at >= 0 ? *reinterpret_cast<const uint2 *>(from) : make_uint2(0u, 0u);
-            s[0] = z.x, s[1] = z.y;
-        }
+        if (at >= 0) x = __ldcs(reinterpret_cast<const uint4 *>(codes + (at + k) * HD));
     };
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-        if (d < nt) {
-            const int64_t group = look(d);
-            fetch_scales(sc[d], group);
+    for (int d = 0; d < D; ++d) {
+        const int64_t at = look(d);
+        fetch_scales(sc[d], at);
 #pragma unroll
-            for (int k = 0; k < NI; ++k) fetch(r[d][k], group, k);
-        }
-    int64_t next = D < nt ? look(D) : -1;
-    for (int i0 = 0; i0 < nt; i0 += D)
+        for (int k = 0; k < BN; ++k) fetch(r[d][k], at, k);
+    }
+    int64_t next = look(D);
+    for (int m0 = 0; m0 < batches; m0 += D)
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            const int i = i0 + d;
-            if (i >= nt) return;
-            const int64_t group = next;  // of tile i + D
-            next = i + D + 1 < nt ? look(i + D + 1) : -1;
-            const int u = is_k ? i % KU : i % VU;
+            const int m = m0 + d, i = m / BT;
+            if (m >= batches) return;
+            const int64_t at = next;  // of batch m + D
+            next = look(m + D + 1);
+            const int u = i % units;
             bool ok = true;
-            if (is_k ? i >= KU : i >= VU) ok = is_k ? s_done(y, i - KU, w) : pv_done(y, i - VU, w);
+            if (i >= units && m % BT == 0) ok = is_k ? s_done(y, i - KU, w) : pv_done(y, i - VU, w);
             if (!__all_sync(0xFFFFFFFFu, ok)) return;
             uint8_t *to = ring + (is_k ? u : KU + u) * kKv + (dim >> 2) * kHalfTile;
-            uint32_t s[HD / 64];
+            uint32_t s[SW];
 #pragma unroll
-            for (int e = 0; e < HD / 64; ++e) s[e] = sc[d][e];
-            if (i + D < nt) fetch_scales(sc[d], group);
+            for (int e = 0; e < SW; ++e) s[e] = sc[d][e];
+            fetch_scales(sc[d], at);
 #pragma unroll
-            for (int k = 0; k < NI; ++k) {
-                const int row = k * RPI + sub, R = half * 64 + row;
-                uint32_t f;
-                if constexpr (HD == 64) {
-                    f = __shfl_sync(0xFFFFFFFFu, s[0], row >> 1) >> (16 * (row & 1) + 8 * (dim >> 1));
-                } else {
-                    const uint32_t f0 = __shfl_sync(0xFFFFFFFFu, s[0], row >> 1),
-                                   f1 = __shfl_sync(0xFFFFFFFFu, s[HD / 64 - 1], row >> 1);
-                    f = (row & 1 ? f1 : f0) >> (8 * (dim >> 1));
-                }
-                f = e4m3_factor(f & 0xFFu);
+            for (int k = 0; k < BN; ++k) {
+                const int row = first + m % BT * BN + k;
+                const uint32_t f = e4m3_factor((HD == 64 ? s[k / 2] >> (16 * (k & 1) + 8 * (dim >> 1))
+                                                         : s[k % SW] >> (8 * (dim >> 1))) & 0xFFu);
                 const uint4 x = r[d][k];
+                fetch(r[d][k], at, k);
                 const uint2 v0 = e4m3_values(x.x, f), v1 = e4m3_values(x.y, f), v2 = e4m3_values(x.z, f),
                             v3 = e4m3_values(x.w, f);
                 const uint4 lo = make_uint4(v0.x, v0.y, v1.x, v1.y), hi = make_uint4(v2.x, v2.y, v3.x, v3.y);
-                // (the lanes of a row's second 64 dims, in the same banks, store their halves in the other order)
-                const int ch = 2 * (dim & 3), o = dim >> 2;
-                *reinterpret_cast<uint4 *>(to + R * 128 + (((ch + o) ^ (R & 7)) << 4)) = o ? hi : lo;
-                *reinterpret_cast<uint4 *>(to + R * 128 + (((ch + 1 - o) ^ (R & 7)) << 4)) = o ? lo : hi;
-                if (i + D < nt) fetch(r[d][k], group, k);
+                // (of the eight lanes that store at once, four in the other's banks begin with their second half)
+                const int ch = 2 * (dim & 3), o = HD == 64 ? sub & 1 : dim >> 2;
+                *reinterpret_cast<uint4 *>(to + row * 128 + (((ch + o) ^ (row & 7)) << 4)) = o ? hi : lo;
+                *reinterpret_cast<uint4 *>(to + row * 128 + (((ch + 1 - o) ^ (row & 7)) << 4)) = o ? lo : hi;
             }
-            async_fence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(is_k ? &y->k_full[u] : &y->v_full[u]);
+            if (m % BT == BT - 1) {
+                async_fence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + u);
+            }
         }
 }
 
 // The products of the V rows that were taken out of their tiles (a value that is no
 // number), element by element for the query rows that see them; a rare case.
-template <int HD, int TERMS, bool SWZ, bool Q8>
+template <int HD, int TERMS, bool MANY, bool Q8>
 __device__ __noinline__ void add_hidden_rows(const PagedArgs &a, const TreeArgs &t, const Work &wk, const Span &sp, int kvh,
                                              int G, const uint32_t *bad, const float *mref, float *Os, int tid) {
     const float c = a.scale * 1.44269504088896340736f;
-    for (int i = tid; i < wk.rows * HD; i += kSoft) {
+    for (int i = tid; i < wk.rows * HD; i += soft_threads(MANY)) {
         const int r = i / HD, d = i % HD, rg = wk.row0 + r, pos = sp.base + rg / G;
         const int64_t qat = (rg / G) * t.q_token + (int64_t)(kvh * G + rg % G) * HD;
         for (int word = 0; word < kBadWords; ++word)
@@ -315,17 +322,17 @@ __device__ __noinline__ void add_hidden_rows(const PagedArgs &a, const TreeArgs 
                         qv = static_cast<const float *>(t.q)[qat + e];
                     x = fmaf(qv, pool_value<HD, Q8>(a.kc, a.ks, at, e), x);
                 }
-                float *o = Os + o_at<HD, SWZ>(r, d);
+                float *o = Os + o_at<HD, MANY>(r, d);
                 *o = fmaf(ex2(fmaf(x, c, -mref[r])), pool_value<HD, Q8>(a.vc, a.vs, at, d), *o);
             }
     }
 }
 
 template <int HD, int TERMS, int NR, bool Q8>
-__global__ void __launch_bounds__(paged_threads(Q8), 1)
+__global__ void __launch_bounds__(paged_threads(false, Q8), 1)
     paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PagedArgs a) {
     using C = AttnShape<HD, TERMS, NR>;
-    constexpr int kThreads = paged_threads(Q8);
+    constexpr int kThreads = paged_threads(false, Q8);
     constexpr int N = C::N, PT = weight_terms(TERMS), PN = C::PN, KU = C::KU, VU = C::VU;
     constexpr bool kScaled = TERMS > 1;             // the queries carry the scale already
     constexpr bool kOnes = HD == 64;                // the sums come out of the second product
@@ -353,7 +360,7 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
     const int row0 = wk.row0, rows = wk.rows;
     const TreeArgs t = tree_args<TERMS>(a, wk);
     const int first = threadIdx.x - kFirstSoft * 32;
-    if (is_soft(warp)) {
+    if (is_soft<false>(warp)) {
         // The queries as the B operand: row term * NR + r, 128-byte swizzled. (Rows
         // behind the sequence's last token are zeros, and columns nobody reads.)
         for (int i = first; i < NR * (HD / 8); i += kSoft) {
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
     const Span sp = span_of(a, wk, G);
     const int t0 = (int)((int64_t)split * sp.tiles / S), nt = (int)((int64_t)(split + 1) * sp.tiles / S) - t0;
     if (warp == kKWarp) {
-        if (lane == 0) init_paged<Q8>(y, bad);
+        if (lane == 0) init_paged<false, Q8>(y, bad);
         __syncwarp();
         if constexpr (!Q8) {  // the first copies need nobody else
             load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 0, min(nt, KU), lane, wt);
@@ -383,7 +390,7 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
             for (int i = lane; i < C::kOnes / 16; i += 32)  // chunk 0 of row i / 8 sits at chunk (row & 7)
                 *reinterpret_cast<uint4 *>(sm + C::kOffOnes + i * 16) =
                     make_uint4(i % 8 == ((i / 8) & 7) ? 0x3F80u : 0u, 0u, 0u, 0u);
-    } else if (is_soft(warp)) {
+    } else if (is_soft<false>(warp)) {
         if (first < 2 * NR) mref[first] = kNone;
     }
     async_fence();
@@ -393,8 +400,9 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
     tc_fence_after();
     const uint32_t tS = uniform(y->tmem), tO = tS + 2 * N;  // S and O of group g: + g * N, + g * PN
 
-    if (warp >= kFirstConv) {
-        if constexpr (Q8) convert_pages<HD, KU, VU>(y, sm, a, wk.b, kvh, sp, t0, nt, warp - kFirstConv, lane, wt);
+    if (warp >= first_conv(false)) {
+        if constexpr (Q8)
+            convert_pages<HD, KU, VU, conv_warps(false), 8>(y, sm, a, wk.b, kvh, sp, t0, nt, warp - first_conv(false), lane, wt);
     } else if (!Q8 && warp == kKWarp) {
         load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, KU, nt, lane, wt);
     } else if (!Q8 && warp == kVWarp) {
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
                 }
             }
         }
-    } else if (is_soft(warp)) {
+    } else if (is_soft<false>(warp)) {
         // group g takes every other tile; thread: cache row `row` of it, all query rows
         const int g = (warp - kFirstSoft) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t mylane = (uint32_t)(quarter * 32) << 16;
@@ -640,14 +648,31 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
                                    lsum, join);
 }
 
+// Barriers of the softmax threads, and of a pair of their warps: a plain one, and a vote.
+__device__ __forceinline__ void rows_sync() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(id)
+        : "memory");
+    return r != 0;
+}
+
 template <int HD, int TERMS, bool Q8>
-__global__ void __launch_bounds__(paged_threads(Q8), 1)
+__global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     paged_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const PagedArgs a) {
     using C = RowShape<HD, TERMS, 4 * kBadWords>;
-    constexpr int kThreads = paged_threads(Q8);
+    constexpr int kThreads = paged_threads(true, Q8);
     constexpr int KU = C::KU, VU = C::VU, NB = C::NB, PT = weight_terms(TERMS);
     constexpr bool kScaled = TERMS > 1;
+    constexpr int kHalf = kTile / 2;  // a softmax thread's columns of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *Qs = sm + C::kOffQ;
@@ -655,7 +680,7 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
     static_assert(sizeof(Sync<KU, VU>) <= 512, "");
     volatile int *err = &y->err;
     const Wait wt{err, a.wait_ns, a.wait_sleep};
-    // [2][128]: the groups' maxima, then the rows' maxima and sums, each written by the thread that read what was there
+    // [2][128]: the groups' maxima, then the rows' maxima and sums
     uint32_t *bad = reinterpret_cast<uint32_t *>(sm + C::kOffMisc + 512);  // [kBadWords]
     float *gm = reinterpret_cast<float *>(bad + kBadWords), *mref = gm, *lsum = gm + kRows;
     float *Os = reinterpret_cast<float *>(sm);                      // in the ring when the tiles are done,
@@ -672,9 +697,9 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
     const TreeArgs t = tree_args<TERMS>(a, wk);
     const int row = (warp & 3) * 32 + lane;  // a softmax thread's query row
     const int st = tid - kFirstSoft * 32;  // a softmax thread's index
-    if (is_soft(warp)) {
+    if (is_soft<true>(warp)) {
         // the queries as the A operand: term k, 128-byte swizzled rows of 64 dims
-        for (int i = st; i < kRows * (HD / 8); i += kSoft) {
+        for (int i = st; i < kRows * (HD / 8); i += kRowSoft) {
             const int r = i / (HD / 8), ch = i % (HD / 8);
             uint4 q[TERMS];
             load_query8<HD, TERMS>(t, 0, kvh, G, row0 + r, ch, c, q);
@@ -688,7 +713,7 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
     const Span sp = span_of(a, wk, G);
     const int t0 = (int)((int64_t)split * sp.tiles / S), nt = (int)((int64_t)(split + 1) * sp.tiles / S) - t0;
     if (warp == kKWarp) {
-        if (lane == 0) init_paged<Q8>(y, bad);
+        if (lane == 0) init_paged<true, Q8>(y, bad);
         __syncwarp();
         if constexpr (!Q8) {  // the first copies need nobody else
             load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 0, min(nt, KU), lane, wt);
@@ -705,8 +730,9 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
     // scores and third terms of tile i: + i % NB * 128, + i % NB * kThird; O of group g: + g * HD
     const uint32_t tS = uniform(y->tmem), tT = tS + NB * kTile, tO = tT + NB * C::kThird;
 
-    if (warp >= kFirstConv) {
-        if constexpr (Q8) convert_pages<HD, KU, VU>(y, sm, a, wk.b, kvh, sp, t0, nt, warp - kFirstConv, lane, wt);
+    if (warp >= first_conv(true)) {
+        if constexpr (Q8)
+            convert_pages<HD, KU, VU, conv_warps(true), 8>(y, sm, a, wk.b, kvh, sp, t0, nt, warp - first_conv(true), lane, wt);
     } else if (!Q8 && warp == kKWarp) {
         load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, KU, nt, lane, wt);
     } else if (!Q8 && warp == kVWarp) {
@@ -741,7 +767,7 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
                 for (int t = 0; t < PT; ++t)
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk) {
-                        const uint32_t p = t < 2 ? tS + (i % NB) * kTile + t * 64 + kk * 8
+                        const uint32_t p = t < 2 ? tS + (i % NB) * kTile + kk / 2 * 32 + t * 16 + kk % 2 * 8
                                                  : tT + (i % NB) * C::kThird + kk * 8;
                         umma_bf16_ta(tO + (i & 1) * HD, p, v + ((kk * 2048) >> 4), idO, i >= 2 || (t | kk) != 0);
                     }
@@ -753,30 +779,32 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
                 }
             }
         }
-    } else if (is_soft(warp)) {
-        // group g takes every other tile, a thread one query row of it
-        const int g = (warp - kFirstSoft) >> 2, quarter = warp & 3;
+    } else if (is_soft<true>(warp)) {
+        // group g takes every other tile; two warps have a row of it each in their lanes, and
+        // half (h) of its columns: their maximum is one, their sums are added at the end
+        const int sw = warp - kFirstSoft, g = (sw >> 2) & 1, h = sw >> 3, quarter = warp & 3, pair = 2 + g * 4 + quarter;
         const uint32_t mylane = (uint32_t)(quarter * 32) << 16;
-        const uint32_t to = tO + g * HD + mylane;
-        const bool live = quarter * 32 < rows;  // (rows behind the last: the warp only keeps the barriers)
+        const uint32_t to = tO + g * HD + h * (HD / 2) + mylane;
+        const bool live = quarter * 32 < rows;  // (rows behind the last: the warps only keep the barriers)
         const int pos = sp.base + (row0 + row) / G;  // the row's token
         float m = kNone, l = 0.f;
         bool ok = true;
         for (int i = g; i < nt; i += 2) {
             ok = ok && s_done(y, i, wt);
             tc_fence_after();
-            const uint32_t ts = tS + (i % NB) * kTile + mylane, tt = tT + (i % NB) * C::kThird + mylane;
+            const uint32_t ts = tS + (i % NB) * kTile + h * kHalf + mylane;
+            const uint32_t tt = tT + (i % NB) * C::kThird + h * (kHalf / 2) + mylane;
             const int tile = sp.tile(t0 + i), at = tile * kTile, part = sp.part(tile);
             if (live) {
-                float x[kTile];
+                float x[kHalf];
 #pragma unroll
-                for (int e = 0; e < kTile; e += 16) tmem_ld16(ts + e, x + e);
+                for (int e = 0; e < kHalf; e += 16) tmem_ld16(ts + e, x + e);
                 tmem_ld_wait();
-                pin<kTile>(x);
+                pin<kHalf>(x);
                 if (part >= 0) {
 #pragma unroll
-                    for (int w = 0; w < kTile; w += 32) {
-                        const uint32_t see = sp.sees32(pos, at + w);
+                    for (int w = 0; w < kHalf; w += 32) {
+                        const uint32_t see = sp.sees32(pos, at + h * kHalf + w);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (!((see >> e) & 1)) x[w + e] = -INFINITY;
@@ -784,21 +812,26 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
                 }
                 float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < kTile; e += 8)
+                for (int e = 0; e < kHalf; e += 8)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) t4[w] = fmaxf(fmaxf(t4[w], x[e + 2 * w]), x[e + 2 * w + 1]);
                 float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                 if (!kScaled) top *= c;  // (the scale is positive)
-                if (__any_sync(0xFFFFFFFFu, top > m + kRaise)) {
-                    // raise the warp's maxima to those of the rows so far; scale O and the sums
-                    const float best = fmaxf(m, top), scale = ex2(m - best);
+                if (pair_any(pair, top > m + kRaise)) {
+                    // raise the warps' maxima to those of the rows so far; scale O and the sums
+                    float *seen = gm + g * kRows + row;
+                    if (h) *seen = top;
+                    pair_sync(pair);
+                    if (!h) *seen = fmaxf(fmaxf(*seen, top), m);
+                    pair_sync(pair);
+                    const float best = *seen, scale = ex2(m - best);
                     m = best;
                     l *= scale;
                     if (i >= 2) {
                         if (NB > 2) ok = ok && pv_done(y, i - 2, wt);  // O is this group's again (NB = 2: S(i) was issued behind it)
                         tc_fence_after();
 #pragma unroll 1
-                        for (int d = 0; d < HD; d += 16) {
+                        for (int d = 0; d < HD / 2; d += 16) {
                             float o[16];
                             tmem_ld16(to + d, o);
                             tmem_ld_wait();
@@ -811,7 +844,7 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
                 }
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int w0 = 0; w0 < kTile; w0 += 32) {
+                for (int w0 = 0; w0 < kHalf; w0 += 32) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         float &x0 = x[w0 + e], &x1 = x[w0 + e + 1];
@@ -829,7 +862,8 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
                             w[e] = pack_bf16(x0, x1);
                             if (t + 1 < PT) less2(x0, x1, w[e]);
                         }
-                        tmem_st16((t < 2 ? ts + t * 64 : tt) + w0 / 2, w);
+                        // (into the columns that the 32 scores were in)
+                        tmem_st16(t < 2 ? ts + w0 + t * 16 : tt + w0 / 2, w);
                     }
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -838,8 +872,9 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
             tc_fence_before();
             if (part >= 0) {
                 ok = ok && v_full(y, i, wt);
-                mend_v<HD>(sm + (KU + i % VU) * C::kKv, row, sp.somebody(at + row) ? part * kTile + row : kBadRows, kBadRows,
-                           bad);
+                if (!h)
+                    mend_v<HD>(sm + (KU + i % VU) * C::kKv, row, sp.somebody(at + row) ? part * kTile + row : kBadRows,
+                               kBadRows, bad);
                 async_fence();
             }
             __syncwarp();
@@ -847,42 +882,44 @@ __global__ void __launch_bounds__(paged_threads(Q8), 1)
         }
         if (nt > 0) ok = ok && pv_done(y, nt - 1, wt);  // (and with it every product: the ring is free)
         tc_fence_after();
-        gm[g * kRows + row] = m;
-        soft_sync();
+        // (the pair's raises are over: each of its warps has read the last one's before this)
+        if (!h) gm[g * kRows + row] = m;
+        rows_sync();
         tc_fence_after();  // (a group that passed early reads O behind the barrier, too)
         // the groups' O to the larger maximum: group 0 writes, group 1 adds
         const float best = fmaxf(m, gm[(g ^ 1) * kRows + row]), scale = g < nt ? ex2(m - best) : 0.f;
-        l *= scale;
+        float *sums = join + 3 * kCluster * kRows;  // [4][128], in the ring
+        sums[(g * 2 + h) * kRows + row] = l * scale;
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-            if (g == h) {
-                if (live) {
+        for (int u = 0; u < 2; ++u) {
+            if (g == u && live) {
 #pragma unroll 1
-                    for (int d = 0; d < HD; d += 16) {
-                        float o[16];
-                        if (g < nt) {
-                            tmem_ld16(to + d, o);
-                            tmem_ld_wait();
-                            pin<16>(o);
-                        } else {
+                for (int d = 0; d < HD / 2; d += 16) {
+                    float o[16];
+                    if (g < nt) {
+                        tmem_ld16(to + d, o);
+                        tmem_ld_wait();
+                        pin<16>(o);
+                    } else {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = 0.f;
-                        }
+                        for (int e = 0; e < 16; ++e) o[e] = 0.f;
+                    }
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            float4 *z = reinterpret_cast<float4 *>(Os + o_at<HD, true>(row, d + e));
-                            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (h) w = *z;
-                            w.x = fmaf(scale, o[e], w.x), w.y = fmaf(scale, o[e + 1], w.y);
-                            w.z = fmaf(scale, o[e + 2], w.z), w.w = fmaf(scale, o[e + 3], w.w);
-                            *z = w;
-                        }
+                    for (int e = 0; e < 16; e += 4) {
+                        float4 *z = reinterpret_cast<float4 *>(Os + o_at<HD, true>(row, h * (HD / 2) + d + e));
+                        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (u) w = *z;
+                        w.x = fmaf(scale, o[e], w.x), w.y = fmaf(scale, o[e + 1], w.y);
+                        w.z = fmaf(scale, o[e + 2], w.z), w.w = fmaf(scale, o[e + 3], w.w);
+                        *z = w;
                     }
                 }
-                lsum[row] = h ? lsum[row] + l : l;
-                if (h) mref[row] = best;
             }
-            soft_sync();
+            if (u == 1 && st < kRows) {  // (st is the row here; the maxima were read before the last barrier)
+                mref[row] = best;
+                lsum[row] = (sums[row] + sums[kRows + row]) + (sums[2 * kRows + row] + sums[3 * kRows + row]);
+            }
+            rows_sync();
         }
         if (any_bad(bad)) add_hidden_rows<HD, TERMS, true, Q8>(a, t, wk, sp, kvh, G, bad, mref, Os, st);
     }
