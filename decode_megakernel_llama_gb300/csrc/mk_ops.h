@@ -54,7 +54,10 @@ __device__ __forceinline__ uint32_t e4m3_codes(float4 x, uint32_t s) {
 
 // The factor of e4m3_values, twice: a code's bits put at bf16's place are its value
 // * 2^-120, denormals too, and 2^(s - 7) is a bf16 number up to s = 134.
-__device__ __forceinline__ uint32_t e4m3_factor(uint32_t s) { return s > 134 ? 0x7FFF7FFFu : (s + 120) * 0x00800080u; }
+__device__ __forceinline__ uint32_t e4m3_factor2(uint32_t s2) {  // of s in both halves
+    return s2 > 134 * 0x00010001u ? 0x7FFF7FFFu : s2 * 128u + 120 * 0x00800080u;
+}
+__device__ __forceinline__ uint32_t e4m3_factor(uint32_t s) { return e4m3_factor2(s * 0x00010001u); }
 
 // Four codes as bf16 (exact for s >= 10).
 __device__ __forceinline__ uint2 e4m3_values(uint32_t codes, uint32_t factor) {

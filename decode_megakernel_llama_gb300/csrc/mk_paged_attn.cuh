@@ -43,6 +43,7 @@ struct Work {
 };
 
 // The u-th tile of NR rows over all sequences, by a whole warp; rows = 0 behind the last.
+// A sequence's last rows, which see the most, come first.
 __device__ __forceinline__ Work find_work(const PagedArgs &a, int u, int NR, int G, int lane) {
     Work w{0, 0, 0, 0, 0, 0};
     int before = 0;  // tiles of the sequences seen so far
@@ -68,7 +69,7 @@ __device__ __forceinline__ Work find_work(const PagedArgs &a, int u, int NR, int
             w.n = __shfl_sync(0xFFFFFFFFu, n, l);
             w.len = __shfl_sync(0xFFFFFFFFu, len, l);
             w.tok0 = __shfl_sync(0xFFFFFFFFu, lo, l);
-            w.row0 = (u - before - __shfl_sync(0xFFFFFFFFu, upto - mine, l)) * NR;
+            w.row0 = (before + __shfl_sync(0xFFFFFFFFu, upto, l) - 1 - u) * NR;
             w.rows = min(NR, w.n * G - w.row0);
             return w;
         }
@@ -173,6 +174,40 @@ __device__ __forceinline__ bool any_bad(const uint32_t *bad) {
     return x != 0;
 }
 
+// The first copies of a split, K and V, by one warp: all page numbers are asked for at
+// once (one after the other they took 8,400 cycles for 12 tiles), and K and V share them.
+template <int HD, int KU, int VU>
+__device__ __forceinline__ void load_first(Sync<KU, VU> *y, uint8_t *ring, const CUtensorMap *kmap, const CUtensorMap *vmap,
+                                           const PagedArgs &a, int b, int kvh, const Span &sp, int t0, int nt, int lane) {
+    constexpr int kKv = kHalfTile * (HD / 64), kHalves = HD / 64, kMost = KU > VU ? KU : VU;
+    const int parts = max(kTile >> a.shift, 1), rows = kTile / parts;
+    const int part = lane / kHalves, half = lane % kHalves;
+    const bool mine = lane < parts * kHalves;
+    const int32_t *table = a.table + (int64_t)b * a.max_pages;
+    int page[kMost];
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int j = sp.tile(t0 + i) * kTile + part * rows;
+        page[i] = a.n_pages;
+        if (mine && i < nt && j < sp.end) page[i] = table[j >> a.shift];
+    }
+    for (int i = lane; i < KU + VU; i += 32)
+        if (i < KU ? i < nt : i - KU < nt) mbar_expect_tx(i < KU ? &y->k_full[i] : &y->v_full[i - KU], kKv);
+    if (lane == 0) *(volatile int *)&y->k_issued = min(nt, KU), *(volatile int *)&y->v_issued = min(nt, VU);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        if (i >= nt || !mine) break;
+        const int j = sp.tile(t0 + i) * kTile + part * rows;
+        const bool there = page[i] >= 0 && page[i] < a.n_pages;
+        const int plane = (there ? page[i] : a.n_pages) * a.Hkv + kvh, row = a.shift < 31 ? j & (a.ps - 1) : j;
+        const int at = half * kHalfTile + part * rows * 128;
+        if (i < KU) tma_load_3d(ring + i * kKv + at, kmap, half * 64, row, plane, &y->k_full[i]);
+        if (i < VU) tma_load_3d(ring + (KU + i) * kKv + at, vmap, half * 64, row, plane, &y->v_full[i]);
+    }
+    __syncwarp();
+}
+
 // A warp's work: tiles from .. to - 1 of a split's K (or V), a box of a page a lane.
 template <int HD, int KU, int VU>
 __device__ __forceinline__ void load_pages(Sync<KU, VU> *y, uint8_t *ring, const CUtensorMap *map, bool is_k,
@@ -240,26 +275,30 @@ __device__ __forceinline__ void convert_pages(Sync<KU, VU> *y, uint8_t *ring, co
         if (page < 0 || page >= a.n_pages) return -1;
         return ((int64_t)page * a.Hkv + kvh) * a.ps + (j - (int)((int64_t)p << a.shift));
     };
+    // (rows that are not there are read from the pool's first ones, and their factors are 0)
     auto fetch_scales = [&](uint32_t (&s)[SW], int64_t at) {
 #pragma unroll
         for (int e = 0; e < SW; e += 2) {
-            uint2 z = make_uint2(0u, 0u);
-            if (at >= 0) z = *reinterpret_cast<const uint2 *>(scales + at * (HD / 32) + 4 * e);
+            const uint2 z = *reinterpret_cast<const uint2 *>(scales + (at < 0 ? 0 : at) * (HD / 32) + 4 * e);
             s[e] = z.x, s[e + 1] = z.y;
         }
     };
-    auto fetch = [&](uint4 &x, int64_t at, int k) {
-        x = make_uint4(0, 0, 0, 0);
-        if (at >= 0) x = __ldcs(reinterpret_cast<const uint4 *>(codes + (at + k) * HD));
+    auto fetch = [&](uint4 &x, const uint8_t *from, int k) {
+        x = __ldcs(reinterpret_cast<const uint4 *>(from + k * HD));
     };
+    auto place = [&](int64_t at) { return codes + (at < 0 ? 0 : at) * HD; };
+    uint32_t there[D];
 #pragma unroll
     for (int d = 0; d < D; ++d) {
         const int64_t at = look(d);
+        there[d] = at < 0 ? 0u : 0xFFFFFFFFu;
         fetch_scales(sc[d], at);
 #pragma unroll
-        for (int k = 0; k < BN; ++k) fetch(r[d][k], at, k);
+        for (int k = 0; k < BN; ++k) fetch(r[d][k], place(at), k);
     }
     int64_t next = look(D);
+    const int o = HD == 64 ? sub & 1 : dim >> 2;  // this lane stores the second half of its 16 elements first
+    const uint32_t byte = 0x4040u + 0x0101u * (dim >> 1);  // of a row's powers (HD = 64: of two rows'), twice
     for (int m0 = 0; m0 < batches; m0 += D)
 #pragma unroll
         for (int d = 0; d < D; ++d) {
@@ -271,25 +310,27 @@ __device__ __forceinline__ void convert_pages(Sync<KU, VU> *y, uint8_t *ring, co
             bool ok = true;
             if (i >= units && m % BT == 0) ok = is_k ? s_done(y, i - KU, w) : pv_done(y, i - VU, w);
             if (!__all_sync(0xFFFFFFFFu, ok)) return;
-            uint8_t *to = ring + (is_k ? u : KU + u) * kKv + (dim >> 2) * kHalfTile;
+            const int row0 = first + m % BT * BN;
+            uint8_t *to = ring + (is_k ? u : KU + u) * kKv + (dim >> 2) * kHalfTile + row0 * 128;
             uint32_t s[SW];
 #pragma unroll
             for (int e = 0; e < SW; ++e) s[e] = sc[d][e];
+            const uint32_t keep = there[d];
+            there[d] = at < 0 ? 0u : 0xFFFFFFFFu;
             fetch_scales(sc[d], at);
+            const uint8_t *from = place(at);
 #pragma unroll
             for (int k = 0; k < BN; ++k) {
-                const int row = first + m % BT * BN + k;
-                const uint32_t f = e4m3_factor((HD == 64 ? s[k / 2] >> (16 * (k & 1) + 8 * (dim >> 1))
-                                                         : s[k % SW] >> (8 * (dim >> 1))) & 0xFFu);
+                const uint32_t f =
+                    e4m3_factor2(__byte_perm(HD == 64 ? s[k / 2] : s[k % SW], 0, byte + (HD == 64 ? 0x0202u * (k & 1) : 0u))) & keep;
                 const uint4 x = r[d][k];
-                fetch(r[d][k], at, k);
-                const uint2 v0 = e4m3_values(x.x, f), v1 = e4m3_values(x.y, f), v2 = e4m3_values(x.z, f),
-                            v3 = e4m3_values(x.w, f);
-                const uint4 lo = make_uint4(v0.x, v0.y, v1.x, v1.y), hi = make_uint4(v2.x, v2.y, v3.x, v3.y);
-                // (of the eight lanes that store at once, four in the other's banks begin with their second half)
-                const int ch = 2 * (dim & 3), o = HD == 64 ? sub & 1 : dim >> 2;
-                *reinterpret_cast<uint4 *>(to + row * 128 + (((ch + o) ^ (row & 7)) << 4)) = o ? hi : lo;
-                *reinterpret_cast<uint4 *>(to + row * 128 + (((ch + 1 - o) ^ (row & 7)) << 4)) = o ? lo : hi;
+                fetch(r[d][k], from, k);
+                const uint32_t a0 = o ? x.z : x.x, a1 = o ? x.w : x.y, b0 = o ? x.x : x.z, b1 = o ? x.y : x.w;
+                const uint2 v0 = e4m3_values(a0, f), v1 = e4m3_values(a1, f), v2 = e4m3_values(b0, f), v3 = e4m3_values(b1, f);
+                // (so the eight lanes that store at once meet in no bank)
+                const int ch = 2 * (dim & 3) + o, r7 = (row0 + k) & 7;
+                *reinterpret_cast<uint4 *>(to + k * 128 + ((ch ^ r7) << 4)) = make_uint4(v0.x, v0.y, v1.x, v1.y);
+                *reinterpret_cast<uint4 *>(to + k * 128 + ((ch ^ 1 ^ r7) << 4)) = make_uint4(v2.x, v2.y, v3.x, v3.y);
             }
             if (m % BT == BT - 1) {
                 async_fence();
@@ -352,7 +393,7 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
 
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int S = gridDim.x / a.units, split = blockIdx.x % S, kvh = blockIdx.y, G = a.Hq / a.Hkv;
-    const int turn = a.units - 1 - blockIdx.x / S;  // (a prompt's last rows, the longest, first)
+    const int turn = blockIdx.x / S;
     const float c = a.scale * 1.44269504088896340736f;  // scores in powers of two
     pdl_wait();
     if (!a.part) pdl_trigger();
@@ -363,8 +404,10 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
     if (is_soft<false>(warp)) {
         // The queries as the B operand: row term * NR + r, 128-byte swizzled. (Rows
         // behind the sequence's last token are zeros, and columns nobody reads.)
-        for (int i = first; i < NR * (HD / 8); i += kSoft) {
-            const int r = i / (HD / 8), ch = i % (HD / 8);
+#pragma unroll
+        for (int i0 = 0; i0 < NR * (HD / 8); i0 += kSoft) {
+            const int i = i0 + first, r = i / (HD / 8), ch = i % (HD / 8);
+            if (NR * (HD / 8) < kSoft && i >= NR * (HD / 8)) break;
             uint4 q[TERMS];
             load_query8<HD, TERMS>(t, 0, kvh, G, row0 + r, ch, c, q);
 #pragma unroll
@@ -381,8 +424,7 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
         if (lane == 0) init_paged<false, Q8>(y, bad);
         __syncwarp();
         if constexpr (!Q8) {  // the first copies need nobody else
-            load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 0, min(nt, KU), lane, wt);
-            load_pages<HD>(y, sm, &vmap, false, a, wk.b, kvh, sp, t0, 0, min(nt, VU), lane, wt);
+            load_first<HD>(y, sm, &kmap, &vmap, a, wk.b, kvh, sp, t0, nt, lane);
         }
     } else if (warp == kMmaWarp) {
         tmem_alloc(&y->tmem, C::kCols);
@@ -688,7 +730,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
 
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int S = gridDim.x / a.units, split = blockIdx.x % S, kvh = blockIdx.y, G = a.Hq / a.Hkv;
-    const int turn = a.units - 1 - blockIdx.x / S;  // (a prompt's last rows, the longest, first)
+    const int turn = blockIdx.x / S;
     const float c = a.scale * 1.44269504088896340736f;
     pdl_wait();
     if (!a.part) pdl_trigger();
@@ -699,8 +741,9 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     const int st = tid - kFirstSoft * 32;  // a softmax thread's index
     if (is_soft<true>(warp)) {
         // the queries as the A operand: term k, 128-byte swizzled rows of 64 dims
-        for (int i = st; i < kRows * (HD / 8); i += kRowSoft) {
-            const int r = i / (HD / 8), ch = i % (HD / 8);
+#pragma unroll
+        for (int i0 = 0; i0 < kRows * (HD / 8); i0 += kRowSoft) {
+            const int r = (i0 + st) / (HD / 8), ch = (i0 + st) % (HD / 8);
             uint4 q[TERMS];
             load_query8<HD, TERMS>(t, 0, kvh, G, row0 + r, ch, c, q);
 #pragma unroll
@@ -716,8 +759,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
         if (lane == 0) init_paged<true, Q8>(y, bad);
         __syncwarp();
         if constexpr (!Q8) {  // the first copies need nobody else
-            load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 0, min(nt, KU), lane, wt);
-            load_pages<HD>(y, sm, &vmap, false, a, wk.b, kvh, sp, t0, 0, min(nt, VU), lane, wt);
+            load_first<HD>(y, sm, &kmap, &vmap, a, wk.b, kvh, sp, t0, nt, lane);
         }
     } else if (warp == kMmaWarp) {
         tmem_alloc(&y->tmem, C::kCols);
@@ -730,6 +772,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     // scores and third terms of tile i: + i % NB * 128, + i % NB * kThird; O of group g: + g * HD
     const uint32_t tS = uniform(y->tmem), tT = tS + NB * kTile, tO = tT + NB * C::kThird;
 
+    bool direct = false;  // (of the softmax threads: their results are written)
     if (warp >= first_conv(true)) {
         if constexpr (Q8)
             convert_pages<HD, KU, VU, conv_warps(true), 8>(y, sm, a, wk.b, kvh, sp, t0, nt, warp - first_conv(true), lane, wt);
@@ -890,6 +933,38 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
         const float best = fmaxf(m, gm[(g ^ 1) * kRows + row]), scale = g < nt ? ex2(m - best) : 0.f;
         float *sums = join + 3 * kCluster * kRows;  // [4][128], in the ring
         sums[(g * 2 + h) * kRows + row] = l * scale;
+        direct = S == 1 && !a.part && !any_bad(bad);
+        if (direct) {
+            // one split: a row's four threads a quarter of its dims each, from both groups' O
+            float *scales = sums + 4 * kRows;  // [2][128]
+            if (!h) scales[g * kRows + row] = scale;
+            rows_sync();
+            if (live) {  // (whole warps: they load together)
+                const float sum = (sums[row] + sums[kRows + row]) + (sums[2 * kRows + row] + sums[3 * kRows + row]);
+                // (no row seen: zeros; a wait that ran out: NaN)
+                const float inv = *err ? __uint_as_float(0x7FC00000u) : sum == 0.f ? 0.f : 1.f / sum;
+                const float f0 = nt > 0 ? scales[row] * inv : 0.f, f1 = nt > 1 ? scales[kRows + row] * inv : 0.f;
+                const int rg = row0 + row, d0 = (g * 2 + h) * (HD / 4);
+                const int64_t at = (rg / G) * t.o_token + (int64_t)(kvh * G + rg % G) * HD + d0;
+#pragma unroll 1
+                for (int d = 0; d < HD / 4; d += 16) {
+                    float o[16], p[16];
+                    if (nt > 0) tmem_ld16(tO + mylane + d0 + d, o);
+                    if (nt > 1) tmem_ld16(tO + HD + mylane + d0 + d, p);
+                    tmem_ld_wait();
+                    pin<16>(o);
+                    pin<16>(p);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        o[e] = nt > 0 ? f0 * o[e] : *err ? f0 + inv : 0.f;
+                        if (nt > 1) o[e] = fmaf(f1, p[e], o[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        if (row < rows) put4<TERMS>(t, at + d + e, make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                }
+            }
+        } else
 #pragma unroll 1
         for (int u = 0; u < 2; ++u) {
             if (g == u && live) {
@@ -921,7 +996,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
             }
             rows_sync();
         }
-        if (any_bad(bad)) add_hidden_rows<HD, TERMS, true, Q8>(a, t, wk, sp, kvh, G, bad, mref, Os, st);
+        if (!direct && any_bad(bad)) add_hidden_rows<HD, TERMS, true, Q8>(a, t, wk, sp, kvh, G, bad, mref, Os, st);
     }
     tc_fence_before();
     __syncwarp();
@@ -935,6 +1010,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
         tc_fence_after();
         tmem_free(tS, C::kCols);
     }
+    if (S == 1 && !a.part && !any_bad(bad)) return;  // (written, or NaN)
     finish<HD, TERMS, kRows, true, kThreads>(t, (int64_t)turn * a.Hkv + kvh, 0, kvh, G, row0, rows, split, S, Os, mref,
                                    lsum, join);
 }

@@ -398,9 +398,19 @@ __device__ __forceinline__ void finish(const TreeArgs &a, int64_t unit, int b, i
         }
         return;
     }
+    if (S == 1) {  // nothing to join
+        for (int i = tid; i < rows * (HD / 4); i += NT) {
+            const int r = i / (HD / 4), d = 4 * (i % (HD / 4)), rg = row0 + r;
+            const float4 o = *reinterpret_cast<const float4 *>(Os + o_at<HD, SWZ>(r, d));
+            const float w = lsum[r] == 0.f ? 0.f : 1.f / lsum[r];  // no row seen: zeros
+            put4<TERMS>(a, b * a.o_batch + (rg / G) * a.o_token + (int64_t)(kvh * G + rg % G) * HD + d,
+                        make_float4(w * o.x, w * o.y, w * o.z, w * o.w));
+        }
+        return;
+    }
     float *wgt = join, *m8 = wgt + kCluster * NR, *l8 = m8 + kCluster * NR;
     cg::cluster_group cl = cg::this_cluster();
-    if (S > 1) cl.sync();
+    cl.sync();
     for (int i = tid; i < S * NR; i += NT) {
         m8[i] = *cl.map_shared_rank(mref + i % NR, i / NR);
         l8[i] = *cl.map_shared_rank(lsum + i % NR, i / NR);
@@ -430,7 +440,7 @@ __device__ __forceinline__ void finish(const TreeArgs &a, int64_t unit, int b, i
             }
         put4<TERMS>(a, b * a.o_batch + (rg / G) * a.o_token + (int64_t)(kvh * G + rg % G) * HD + d, y);
     }
-    if (S > 1) cl.sync();  // nobody leaves while its memory is read
+    cl.sync();  // nobody leaves while its memory is read
 }
 
 // Eight elements of query row rg (node rg / G, head rg % G of the group) as
