@@ -27,7 +27,7 @@ namespace {
 template <int HD_, int TERMS_, int NR_, bool Q8_>
 struct PagedFew {
     static constexpr int kThreads = paged_threads(false, Q8_), HD = HD_, TERMS = TERMS_, NR = NR_,
-                         kSmem = AttnShape<HD, TERMS, NR>::kSmem;
+                         kSmem = AttnShape<HD, TERMS, NR, less_bytes(HD, Q8_)>::kSmem;
     static constexpr bool Q8 = Q8_;
     static constexpr double kTileUs = (HD == 64 ? 0.6 : 1.0) - (TERMS == 1 ? HD / 64 * 0.1 : 0.0), kFixedUs = 5.0, kJoinUs = 4.5;
     static auto fn() { return paged_attention<HD, TERMS, NR, Q8>; }
@@ -35,7 +35,7 @@ struct PagedFew {
 template <int HD_, int TERMS_, bool Q8_>
 struct PagedMany {
     static constexpr int kThreads = paged_threads(true, Q8_), HD = HD_, TERMS = TERMS_, NR = kRows,
-                         kSmem = RowShape<HD, TERMS, 4 * kBadWords>::kSmem;
+                         kSmem = RowShape<HD, TERMS, kOwnBytes, less_bytes(HD, Q8_)>::kSmem;
     static constexpr bool Q8 = Q8_;
     static constexpr double kTileUs = HD == 64 && TERMS == 1 ? 0.8 : 1.2, kFixedUs = 6.5, kJoinUs = 7.0;
     static auto fn() { return paged_attention_rows<HD, TERMS, Q8>; }
@@ -119,7 +119,9 @@ cudaError_t launch(PagedArgs a, const Bounds &h, cudaStream_t s, int64_t *want) 
 template <int HD, int TERMS, bool Q8>
 cudaError_t dispatch(const PagedArgs &a, const Bounds &h, cudaStream_t s, int64_t *want) {
     const int64_t rows = (int64_t)h.max_new * (a.Hq / a.Hkv);
-    if (rows <= 16) return launch<PagedFew<HD, TERMS, 16, Q8>>(a, h, s, want);
+    // (32 columns of three terms and heads of 128 leave no room for 8-bit pages' stages)
+    constexpr bool kNarrow = HD == 128 && TERMS == 3 && Q8;
+    if (rows <= 16 || kNarrow) return launch<PagedFew<HD, TERMS, 16, Q8>>(a, h, s, want);
     // (three terms of a head of 128 and two O of 128 columns exceed tensor memory)
     if constexpr (!(HD == 128 && TERMS == 3))
         if (rows > 32) {
@@ -127,7 +129,8 @@ cudaError_t dispatch(const PagedArgs &a, const Bounds &h, cudaStream_t s, int64_
             if (plan<PagedMany<HD, TERMS, Q8>>(a, h, ws).us < plan<PagedFew<HD, TERMS, 32, Q8>>(a, h, ws).us)
                 return launch<PagedMany<HD, TERMS, Q8>>(a, h, s, want);
         }
-    return launch<PagedFew<HD, TERMS, 32, Q8>>(a, h, s, want);
+    if constexpr (!kNarrow) return launch<PagedFew<HD, TERMS, 32, Q8>>(a, h, s, want);
+    return cudaErrorInvalidValue;  // (not reached)
 }
 
 template <int HD, int TERMS>
@@ -193,7 +196,7 @@ int check_paged(const mk_paged_args *a, mkops::PagedArgs *p) {
     const uintptr_t all = reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(a->out) |
                           reinterpret_cast<uintptr_t>(a->k_pages) | reinterpret_cast<uintptr_t>(a->v_pages) |
                           reinterpret_cast<uintptr_t>(a->workspace);
-    if ((all & 15u) || (q8 && ((reinterpret_cast<uintptr_t>(a->k_scales) | reinterpret_cast<uintptr_t>(a->v_scales)) & 7u)))
+    if ((all & 15u) || (q8 && ((reinterpret_cast<uintptr_t>(a->k_scales) | reinterpret_cast<uintptr_t>(a->v_scales)) & 15u)))
         return bad(MK_ERR_INVALID_ARG, "a pointer is not aligned");
     if (a->workspace_bytes < 0) return bad(MK_ERR_INVALID_ARG, "bad workspace");
     if (a->wait_ns < 0) return bad(MK_ERR_INVALID_ARG, "wait_ns is negative");

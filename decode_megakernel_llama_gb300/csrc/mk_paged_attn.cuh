@@ -164,7 +164,7 @@ __device__ __forceinline__ float pool_value(const void *pool, const uint8_t *sca
 template <bool MANY, bool Q8, int KU, int VU>
 __device__ __forceinline__ void init_paged(Sync<KU, VU> *y, uint32_t *bad) {
     for (int i = 0; i < kBadWords; ++i) bad[i] = 0;
-    init_sync(y, Q8 ? conv_warps(MANY) / 2 : 1, soft_threads(MANY) / 64);
+    init_sync(y, Q8 ? conv_warps(MANY) : 1, soft_threads(MANY) / 64);
 }
 
 __device__ __forceinline__ bool any_bad(const uint32_t *bad) {
@@ -246,98 +246,140 @@ __device__ __forceinline__ void load_pages(Sync<KU, VU> *y, uint8_t *ring, const
     }
 }
 
-// One of W warps (half of them for K, half for V, each its rows of every tile): codes and
-// powers from the pool, R loads ahead in registers, their bf16 values into the ring,
-// 128-byte swizzled as TMA writes it. A lane has 16 elements of CH consecutive rows.
-template <int HD, int KU, int VU, int W, int R>
-__device__ __forceinline__ void convert_pages(Sync<KU, VU> *y, uint8_t *ring, const PagedArgs &a, int b, int kvh,
-                                              const Span &sp, int t0, int nt, int who, int lane, const Wait &w) {
-    constexpr int kKv = kHalfTile * (HD / 64), kWarpRows = 2 * kTile / W;
-    constexpr int LPR = HD / 16, CH = kWarpRows * LPR / 32;       // lanes of a row, rows of a lane
-    constexpr int BN = R < CH ? (R < 8 ? R : 8) : CH, D = R / BN;  // rows of a batch, batches in flight
-    constexpr int BT = CH / BN, SW = BN * HD / 128;               // batches of a tile, words of a batch's powers
-    static_assert(R % BN == 0 && CH % BN == 0 && BN <= 8 && SW % 2 == 0, "");
-    const bool is_k = who < W / 2;
-    const int sub = lane / LPR, dim = lane % LPR, first = (who & (W / 2 - 1)) * kWarpRows + sub * CH;
-    const uint8_t *codes = static_cast<const uint8_t *>(is_k ? a.kc : a.vc) + dim * 16, *scales = is_k ? a.ks : a.vs;
-    const int32_t *table = a.table + (int64_t)b * a.max_pages;
-    uint64_t *full = is_k ? y->k_full : y->v_full;
-    const int units = is_k ? KU : VU, batches = nt * BT;
-    uint4 r[D][BN];
-    uint32_t sc[D][SW];
-    // Where the lane's rows of batch m lie in the pool; -1: not there. (Pages of 8-bit rows
-    // hold multiples of 8 rows, so the rows of a batch are of one page.)
-    auto look = [&](int m) -> int64_t {
-        if (m >= batches) return -1;
-        const int j = sp.tile(t0 + m / BT) * kTile + first + m % BT * BN;
-        if (j >= sp.end) return -1;
-        const int p = j >> a.shift, page = table[p];
-        if (page < 0 || page >= a.n_pages) return -1;
-        return ((int64_t)page * a.Hkv + kvh) * a.ps + (j - (int)((int64_t)p << a.shift));
-    };
-    // (rows that are not there are read from the pool's first ones, and their factors are 0)
-    auto fetch_scales = [&](uint32_t (&s)[SW], int64_t at) {
-#pragma unroll
-        for (int e = 0; e < SW; e += 2) {
-            const uint2 z = *reinterpret_cast<const uint2 *>(scales + (at < 0 ? 0 : at) * (HD / 32) + 4 * e);
-            s[e] = z.x, s[e + 1] = z.y;
-        }
-    };
-    auto fetch = [&](uint4 &x, const uint8_t *from, int k) {
-        x = __ldcs(reinterpret_cast<const uint4 *>(from + k * HD));
-    };
-    auto place = [&](int64_t at) { return codes + (at < 0 ? 0 : at) * HD; };
-    uint32_t there[D];
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-        const int64_t at = look(d);
-        there[d] = at < 0 ? 0u : 0xFFFFFFFFu;
-        fetch_scales(sc[d], at);
-#pragma unroll
-        for (int k = 0; k < BN; ++k) fetch(r[d][k], place(at), k);
+// ---- 8-bit pages. One warp copies codes and powers as they lie in the pages into a ring
+// of stages (bulk copies: a page of a head is contiguous), the converting warps make
+// bf16 tiles of them in the products' own ring. The tiles go K(0), then K(i + 1), V(i).
+// (Loads into registers, a tile ahead, kept the warps waiting: 1.9 us a tile of heads of 128.)
+__host__ __device__ constexpr int n_stages(int hd) { return hd == 64 ? 4 : 3; }
+__host__ __device__ constexpr int stage_bytes(int hd) { return kTile * hd + kTile * hd / 32; }
+__host__ __device__ constexpr int less_bytes(int hd, bool q8) { return q8 ? n_stages(hd) * stage_bytes(hd) : 0; }
+
+struct Stages {
+    uint64_t full[4], free[4];
+    uint32_t there[4];  // a stage's parts (of a page each) that hold rows of the pool; the others are zeros
+    int issued;
+};
+constexpr int kOwnBytes = 4 * kBadWords + 112;  // of a CTA: bad rows, and this
+static_assert(sizeof(Stages) <= 112 && 4 * kBadWords % 8 == 0, "");
+
+template <int HD>
+__device__ __forceinline__ void init_stages(Stages *g, int readers) {
+    for (int u = 0; u < n_stages(HD); ++u) {
+        mbar_init(&g->full[u], 1);
+        mbar_init(&g->free[u], readers);
     }
-    int64_t next = look(D);
-    const int o = HD == 64 ? sub & 1 : dim >> 2;  // this lane stores the second half of its 16 elements first
-    const uint32_t byte = 0x4040u + 0x0101u * (dim >> 1);  // of a row's powers (HD = 64: of two rows'), twice
-    for (int m0 = 0; m0 < batches; m0 += D)
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const int m = m0 + d, i = m / BT;
-            if (m >= batches) return;
-            const int64_t at = next;  // of batch m + D
-            next = look(m + D + 1);
-            const int u = i % units;
-            bool ok = true;
-            if (i >= units && m % BT == 0) ok = is_k ? s_done(y, i - KU, w) : pv_done(y, i - VU, w);
-            if (!__all_sync(0xFFFFFFFFu, ok)) return;
-            const int row0 = first + m % BT * BN;
-            uint8_t *to = ring + (is_k ? u : KU + u) * kKv + (dim >> 2) * kHalfTile + row0 * 128;
-            uint32_t s[SW];
-#pragma unroll
-            for (int e = 0; e < SW; ++e) s[e] = sc[d][e];
-            const uint32_t keep = there[d];
-            there[d] = at < 0 ? 0u : 0xFFFFFFFFu;
-            fetch_scales(sc[d], at);
-            const uint8_t *from = place(at);
-#pragma unroll
-            for (int k = 0; k < BN; ++k) {
-                const uint32_t f =
-                    e4m3_factor2(__byte_perm(HD == 64 ? s[k / 2] : s[k % SW], 0, byte + (HD == 64 ? 0x0202u * (k & 1) : 0u))) & keep;
-                const uint4 x = r[d][k];
-                fetch(r[d][k], from, k);
-                const uint32_t a0 = o ? x.z : x.x, a1 = o ? x.w : x.y, b0 = o ? x.x : x.z, b1 = o ? x.y : x.w;
-                const uint2 v0 = e4m3_values(a0, f), v1 = e4m3_values(a1, f), v2 = e4m3_values(b0, f), v3 = e4m3_values(b1, f);
-                // (so the eight lanes that store at once meet in no bank)
-                const int ch = 2 * (dim & 3) + o, r7 = (row0 + k) & 7;
-                *reinterpret_cast<uint4 *>(to + k * 128 + ((ch ^ r7) << 4)) = make_uint4(v0.x, v0.y, v1.x, v1.y);
-                *reinterpret_cast<uint4 *>(to + k * 128 + ((ch ^ 1 ^ r7) << 4)) = make_uint4(v2.x, v2.y, v3.x, v3.y);
-            }
-            if (m % BT == BT - 1) {
-                async_fence();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full + u);
-            }
+    g->issued = 0;
+}
+
+// Calls f(is_k, tile) for all tiles of a split in their order, while it returns true.
+template <class F>
+__device__ __forceinline__ void each_tile(int nt, F f) {
+    for (int i = -1; i < nt; ++i) {
+        if (i + 1 < nt && !f(true, i + 1)) return;
+        if (i >= 0 && !f(false, i)) return;
+    }
+}
+
+// The copying warp.
+template <int HD>
+__device__ __forceinline__ void stage_pages(Stages *g, uint8_t *stages, const PagedArgs &a, int b, int kvh, const Span &sp,
+                                            int t0, int nt, int lane, const Wait &w) {
+    constexpr int N = n_stages(HD), kRow = HD + HD / 32;
+    const int parts = max(kTile >> a.shift, 1), rows = kTile / parts;
+    const int32_t *table = a.table + (int64_t)b * a.max_pages;
+    auto row_of = [&](int i) {
+        const int j = sp.tile(t0 + i) * kTile + lane * rows;
+        return lane < parts && i < nt && j < sp.end ? j : -1;
+    };
+    auto ask = [&](int j) { return j < 0 ? -1 : table[j >> a.shift]; };
+    // (K(i + 1) and V(i) come one behind the other: two pages a lane, each asked for a tile ahead)
+    int jk = row_of(0), pk = ask(jk), jv = jk, pv = pk, e = 0;
+    each_tile(nt, [&](bool is_k, int i) __attribute__((always_inline)) {
+        const int j = is_k ? jk : jv, page = is_k ? pk : pv;
+        if (is_k) {
+            jk = row_of(i + 1);
+            pk = ask(jk);
+        } else {
+            jv = row_of(i + 1);
+            pv = ask(jv);
         }
+        const int u = e % N;
+        const bool ok = e < N || mbar_wait(&g->free[u], (e / N - 1) & 1, w);
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+        const bool there = j >= 0 && page >= 0 && page < a.n_pages;
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
+        const int at = a.shift < 31 ? j & (a.ps - 1) : j, n = min(rows, a.ps - at);  // row of the page, rows
+        if (lane == 0) {
+            g->there[u] = mask;
+            mbar_expect_tx(&g->full[u], parts > 1 ? __popc(mask) * rows * kRow : there ? n * kRow : 0);
+            *(volatile int *)&g->issued = e + 1;
+        }
+        __syncwarp();
+        if (there) {
+            uint8_t *to = stages + u * stage_bytes(HD);
+            const int64_t from = ((int64_t)page * a.Hkv + kvh) * a.ps + at;
+            bulk_load(to + lane * rows * HD, static_cast<const uint8_t *>(is_k ? a.kc : a.vc) + from * HD, n * HD,
+                      &g->full[u]);
+            bulk_load(to + kTile * HD + lane * rows * (HD / 32), (is_k ? a.ks : a.vs) + from * (HD / 32), n * (HD / 32),
+                      &g->full[u]);
+        }
+        ++e;
+        return true;
+    });
+}
+
+// One of W converting warps, kTile / W rows of every tile: bf16 values into the ring,
+// 128-byte swizzled as TMA writes it; 16 elements of a row a lane.
+template <int HD, int KU, int VU, int W>
+__device__ __forceinline__ void convert_pages(Sync<KU, VU> *y, uint8_t *ring, Stages *g, const uint8_t *stages,
+                                              const PagedArgs &a, int nt, int who, int lane, const Wait &w) {
+    constexpr int kKv = kHalfTile * (HD / 64), N = n_stages(HD);
+    constexpr int LPR = HD / 16, RPI = 32 / LPR, NI = kTile / W / RPI;  // lanes of a row, rows at once, times
+    const int sub = lane / LPR, dim = lane % LPR, row0 = who * (kTile / W) + sub, part_bits = min(a.shift, 7);
+    const int o = HD == 64 ? 0 : dim >> 2;  // this lane stores the second half of its elements first: no bank twice
+    const int ch = 2 * (dim & 3) + o;
+    int e = 0;
+    each_tile(nt, [&](bool is_k, int i) __attribute__((always_inline)) {
+        const int u = e % N, slot = is_k ? i % KU : i % VU;
+        bool ok = mbar_wait(&g->full[u], (e / N) & 1, w);
+        if (is_k ? i >= KU : i >= VU) ok = ok && (is_k ? s_done(y, i - KU, w) : pv_done(y, i - VU, w));
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+        const uint8_t *codes = stages + u * stage_bytes(HD) + row0 * HD + dim * 16;
+        const uint8_t *scales = stages + u * stage_bytes(HD) + kTile * HD + row0 * (HD / 32) + (dim >> 1);
+        uint8_t *to = ring + (is_k ? slot : KU + slot) * kKv + (dim >> 2) * kHalfTile + row0 * 128;
+        const uint32_t there = g->there[u];
+        uint4 x[NI];
+        uint32_t f[NI];
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            x[k] = *reinterpret_cast<const uint4 *>(codes + k * RPI * HD);
+            f[k] = scales[k * RPI * (HD / 32)];
+        }
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            const uint32_t z = (there >> ((row0 + k * RPI) >> part_bits)) & 1 ? e4m3_factor(f[k]) : 0u;
+            const uint32_t a0 = o ? x[k].z : x[k].x, a1 = o ? x[k].w : x[k].y, b0 = o ? x[k].x : x[k].z, b1 = o ? x[k].y : x[k].w;
+            const uint2 v0 = e4m3_values(a0, z), v1 = e4m3_values(a1, z), v2 = e4m3_values(b0, z), v3 = e4m3_values(b1, z);
+            const int r7 = (row0 + k * RPI) & 7;
+            *reinterpret_cast<uint4 *>(to + k * RPI * 128 + ((ch ^ r7) << 4)) = make_uint4(v0.x, v0.y, v1.x, v1.y);
+            *reinterpret_cast<uint4 *>(to + k * RPI * 128 + ((ch ^ 1 ^ r7) << 4)) = make_uint4(v2.x, v2.y, v3.x, v3.y);
+        }
+        async_fence();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&g->free[u]);
+            mbar_arrive(is_k ? &y->k_full[slot] : &y->v_full[slot]);
+        }
+        ++e;
+        return true;
+    });
+}
+
+// After a wait that ran out: the copies that were issued have landed.
+template <int HD>
+__device__ __noinline__ void settle_stages(Stages *g) {
+    const int n = *(volatile int *)&g->issued;
+    for (int e = max(0, n - n_stages(HD)); e < n; ++e) mbar_await(&g->full[e % n_stages(HD)], (e / n_stages(HD)) & 1);
 }
 
 // The products of the V rows that were taken out of their tiles (a value that is no
@@ -372,7 +414,7 @@ __device__ __noinline__ void add_hidden_rows(const PagedArgs &a, const TreeArgs 
 template <int HD, int TERMS, int NR, bool Q8>
 __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
     paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PagedArgs a) {
-    using C = AttnShape<HD, TERMS, NR>;
+    using C = AttnShape<HD, TERMS, NR, less_bytes(HD, Q8)>;
     constexpr int kThreads = paged_threads(false, Q8);
     constexpr int N = C::N, PT = weight_terms(TERMS), PN = C::PN, KU = C::KU, VU = C::VU;
     constexpr bool kScaled = TERMS > 1;             // the queries carry the scale already
@@ -385,7 +427,10 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
     volatile int *err = &y->err;
     const Wait wt{err, a.wait_ns, a.wait_sleep};
     uint32_t *bad = reinterpret_cast<uint32_t *>(sm + C::kOffMisc + 512);  // [kBadWords]
-    float *mref = reinterpret_cast<float *>(bad + kBadWords), *corr = mref + 2 * NR;  // [2][NR] of the groups
+    Stages *stage = reinterpret_cast<Stages *>(bad + kBadWords);
+    uint8_t *stages = sm + C::kOffMore;
+    static_assert(kOwnBytes <= 8 * MK_MAX_TREE, "");
+    float *mref = reinterpret_cast<float *>(sm + C::kOffMisc + 512 + kOwnBytes), *corr = mref + 2 * NR;  // [2][NR] of the groups
     float *lsum = corr + 2 * NR;                // [NR]
     float *wtmp = lsum + NR;                    // [2][4][NR]
     float *Os = reinterpret_cast<float *>(sm);  // [NR][HD], in the ring when the tiles are done
@@ -421,7 +466,10 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
     const Span sp = span_of(a, wk, G);
     const int t0 = (int)((int64_t)split * sp.tiles / S), nt = (int)((int64_t)(split + 1) * sp.tiles / S) - t0;
     if (warp == kKWarp) {
-        if (lane == 0) init_paged<false, Q8>(y, bad);
+        if (lane == 0) {
+            if constexpr (Q8) init_stages<HD>(stage, conv_warps(false));
+            init_paged<false, Q8>(y, bad);
+        }
         __syncwarp();
         if constexpr (!Q8) {  // the first copies need nobody else
             load_first<HD>(y, sm, &kmap, &vmap, a, wk.b, kvh, sp, t0, nt, lane);
@@ -444,7 +492,9 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
 
     if (warp >= first_conv(false)) {
         if constexpr (Q8)
-            convert_pages<HD, KU, VU, conv_warps(false), 8>(y, sm, a, wk.b, kvh, sp, t0, nt, warp - first_conv(false), lane, wt);
+            convert_pages<HD, KU, VU, conv_warps(false)>(y, sm, stage, stages, a, nt, warp - first_conv(false), lane, wt);
+    } else if (Q8 && warp == kKWarp) {
+        if constexpr (Q8) stage_pages<HD>(stage, stages, a, wk.b, kvh, sp, t0, nt, lane, wt);
     } else if (!Q8 && warp == kKWarp) {
         load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, KU, nt, lane, wt);
     } else if (!Q8 && warp == kVWarp) {
@@ -678,6 +728,8 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
     __syncwarp();
     __syncthreads();
     if (*err) {  // a wait ran out (nobody waits any more: the same for all threads): the rows are NaN
+        if constexpr (Q8)
+            if (warp == kKWarp && elect()) settle_stages<HD>(stage);
         settle(y, a.err);
         if (tid < NR) lsum[tid] = __uint_as_float(0x7FC00000u);
         __syncthreads();
@@ -710,7 +762,7 @@ template <int HD, int TERMS, bool Q8>
 __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     paged_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const PagedArgs a) {
-    using C = RowShape<HD, TERMS, 4 * kBadWords>;
+    using C = RowShape<HD, TERMS, kOwnBytes, less_bytes(HD, Q8)>;
     constexpr int kThreads = paged_threads(true, Q8);
     constexpr int KU = C::KU, VU = C::VU, NB = C::NB, PT = weight_terms(TERMS);
     constexpr bool kScaled = TERMS > 1;
@@ -724,7 +776,9 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     const Wait wt{err, a.wait_ns, a.wait_sleep};
     // [2][128]: the groups' maxima, then the rows' maxima and sums
     uint32_t *bad = reinterpret_cast<uint32_t *>(sm + C::kOffMisc + 512);  // [kBadWords]
-    float *gm = reinterpret_cast<float *>(bad + kBadWords), *mref = gm, *lsum = gm + kRows;
+    Stages *stage = reinterpret_cast<Stages *>(bad + kBadWords);
+    uint8_t *stages = sm + C::kOffMore;
+    float *gm = reinterpret_cast<float *>(sm + C::kOffMisc + 512 + kOwnBytes), *mref = gm, *lsum = gm + kRows;
     float *Os = reinterpret_cast<float *>(sm);                      // in the ring when the tiles are done,
     float *join = Os + kRows * HD;                                  // and behind it
 
@@ -756,7 +810,10 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     const Span sp = span_of(a, wk, G);
     const int t0 = (int)((int64_t)split * sp.tiles / S), nt = (int)((int64_t)(split + 1) * sp.tiles / S) - t0;
     if (warp == kKWarp) {
-        if (lane == 0) init_paged<true, Q8>(y, bad);
+        if (lane == 0) {
+            if constexpr (Q8) init_stages<HD>(stage, conv_warps(true));
+            init_paged<true, Q8>(y, bad);
+        }
         __syncwarp();
         if constexpr (!Q8) {  // the first copies need nobody else
             load_first<HD>(y, sm, &kmap, &vmap, a, wk.b, kvh, sp, t0, nt, lane);
@@ -775,7 +832,9 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     bool direct = false;  // (of the softmax threads: their results are written)
     if (warp >= first_conv(true)) {
         if constexpr (Q8)
-            convert_pages<HD, KU, VU, conv_warps(true), 8>(y, sm, a, wk.b, kvh, sp, t0, nt, warp - first_conv(true), lane, wt);
+            convert_pages<HD, KU, VU, conv_warps(true)>(y, sm, stage, stages, a, nt, warp - first_conv(true), lane, wt);
+    } else if (Q8 && warp == kKWarp) {
+        if constexpr (Q8) stage_pages<HD>(stage, stages, a, wk.b, kvh, sp, t0, nt, lane, wt);
     } else if (!Q8 && warp == kKWarp) {
         load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, KU, nt, lane, wt);
     } else if (!Q8 && warp == kVWarp) {
@@ -1002,6 +1061,8 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     __syncwarp();
     __syncthreads();
     if (*err) {  // a wait ran out (nobody waits any more: the same for all threads): the rows are NaN
+        if constexpr (Q8)
+            if (warp == kKWarp && elect()) settle_stages<HD>(stage);
         settle(y, a.err);
         if (tid < kRows) lsum[tid] = __uint_as_float(0x7FC00000u);
         __syncthreads();

@@ -115,6 +115,13 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
+// `bytes` (a multiple of 16, as the addresses are) of global memory, completing them on bar.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(saddr(dst)),
+                 "l"(src), "r"(bytes), "r"(saddr(bar))
+                 : "memory");
+}
+
 // Shared-memory matrix descriptor of a bf16 tile in the 128-byte swizzle
 // layout (as TMA writes it): rows of 128 bytes, atoms of 8 rows (1024 bytes,
 // `stride` apart), whose 16-byte chunks are XOR-swizzled by the row.

@@ -465,7 +465,8 @@ __device__ __forceinline__ void load_query8(const TreeArgs &a, int b, int kvh, i
     }
 }
 
-template <int HD, int TERMS, int NR>
+// (LESS: bytes of shared memory that the ring leaves to the caller, behind the rest)
+template <int HD, int TERMS, int NR, int LESS = 0>
 struct AttnShape {
     static constexpr int N = TERMS * NR, PN = weight_terms(TERMS) * NR;  // columns of S and of O
     static constexpr int kKv = kHalfTile * (HD / 64);    // bytes of a K (or V) tile
@@ -474,14 +475,14 @@ struct AttnShape {
     static constexpr int kUsed = 2 * (N + PN), kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     static constexpr int kOnes = HD == 64 ? 2048 : 0;  // 16 cache rows x 64: ones in the first column
     static constexpr int kMisc = 512 + 8 * MK_MAX_TREE + 4 * NR * (2 + 2 + 1 + 8);
-    static constexpr int kRoom = (kSmemMost - 1024 - 2 * kP - kQ - kOnes - kMisc) / kKv;
+    static constexpr int kRoom = (kSmemMost - 1024 - 2 * kP - kQ - kOnes - kMisc - LESS) / kKv;
     static constexpr int KU = (kRoom + 1) / 2 > 6 ? 6 : (kRoom + 1) / 2, VU = kRoom / 2 > 6 ? 6 : kRoom / 2;
     // With room for it S runs three tiles ahead of PV and starts as soon as the group
     // has read the scores before; else it follows PV(i), two tiles ahead.
     static constexpr bool kEarly = VU >= 4;
     static constexpr int kAhead = kEarly ? 3 : 2;
     static constexpr int kOffP = (KU + VU) * kKv, kOffQ = kOffP + 2 * kP, kOffOnes = kOffQ + kQ, kOffMisc = kOffOnes + kOnes;
-    static constexpr int kSmem = 1024 + kOffMisc + kMisc;
+    static constexpr int kOffMore = kOffMisc + kMisc, kSmem = 1024 + kOffMore + LESS;
     static_assert(N % 16 == 0 && PN % 16 == 0 && PN <= 256 && kUsed <= 512 && VU >= 2,
                   "the instruction's N, tensor and shared memory");
     static_assert(NR * HD * 4 + 3 * kCluster * NR * 4 <= (KU + VU) * kKv, "the partial result fits the ring");
@@ -825,8 +826,8 @@ __device__ __forceinline__ uint32_t seen32(uint64_t word, int first) {
     return first > -32 ? (uint32_t)(word << -first) | ((1u << -first) - 1u) : 0xFFFFFFFFu;
 }
 
-// (EXTRA: bytes of the caller's own behind the barriers)
-template <int HD, int TERMS, int EXTRA = 0>
+// (EXTRA: bytes of the caller's own behind the barriers; LESS as above)
+template <int HD, int TERMS, int EXTRA = 0, int LESS = 0>
 struct RowShape {
     static constexpr int kKv = kHalfTile * (HD / 64);
     static constexpr int kQ = TERMS * kKv;  // 128 rows x HD a term
@@ -838,10 +839,10 @@ struct RowShape {
     static constexpr int kThird = TERMS > 2 ? kTile / 2 : 0, kCols = 512;
     static constexpr int NB = (kCols - 2 * HD) / (kTile + kThird) > 2 ? 3 : 2;
     static constexpr int kMisc = 512 + EXTRA + 2 * 4 * kRows;
-    static constexpr int kRoom = (kSmemMost - 1024 - kQ - kMisc) / kKv;
+    static constexpr int kRoom = (kSmemMost - 1024 - kQ - kMisc - LESS) / kKv;
     static constexpr int KU = (kRoom + 1) / 2 > 6 ? 6 : (kRoom + 1) / 2, VU = kRoom / 2 > 6 ? 6 : kRoom / 2;
     static constexpr int kOffQ = (KU + VU) * kKv, kOffMisc = kOffQ + kQ;
-    static constexpr int kSmem = 1024 + kOffMisc + kMisc;
+    static constexpr int kOffMore = kOffMisc + kMisc, kSmem = 1024 + kOffMore + LESS;
     static_assert(NB * (kTile + kThird) + 2 * HD <= kCols && VU >= NB && KU >= NB, "tensor and shared memory of an SM");
     static_assert(kRows * HD * 4 + 3 * kCluster * kRows * 4 <= (KU + VU) * kKv, "the partial result fits the ring");
 };
