@@ -161,10 +161,11 @@ __device__ __forceinline__ float pool_value(const void *pool, const uint8_t *sca
     }
 }
 
+// (landers: arrivals that make a tile of 8-bit pages full)
 template <bool MANY, bool Q8, int KU, int VU>
-__device__ __forceinline__ void init_paged(Sync<KU, VU> *y, uint32_t *bad) {
+__device__ __forceinline__ void init_paged(Sync<KU, VU> *y, uint32_t *bad, int landers) {
     for (int i = 0; i < kBadWords; ++i) bad[i] = 0;
-    init_sync(y, Q8 ? conv_warps(MANY) : 1, soft_threads(MANY) / 64);
+    init_sync(y, Q8 ? landers : 1, soft_threads(MANY) / 64);
 }
 
 __device__ __forceinline__ bool any_bad(const uint32_t *bad) {
@@ -246,140 +247,142 @@ __device__ __forceinline__ void load_pages(Sync<KU, VU> *y, uint8_t *ring, const
     }
 }
 
-// ---- 8-bit pages. One warp copies codes and powers as they lie in the pages into a ring
-// of stages (bulk copies: a page of a head is contiguous), the converting warps make
-// bf16 tiles of them in the products' own ring. The tiles go K(0), then K(i + 1), V(i).
-// (Loads into registers, a tile ahead, kept the warps waiting: 1.9 us a tile of heads of 128.)
-__host__ __device__ constexpr int n_stages(int hd) { return hd == 64 ? 4 : 3; }
-__host__ __device__ constexpr int stage_bytes(int hd) { return kTile * hd + kTile * hd / 32; }
-__host__ __device__ constexpr int less_bytes(int hd, bool q8) { return q8 ? n_stages(hd) * stage_bytes(hd) : 0; }
+// ---- 8-bit pages. A warp for K and one for V copy codes and powers as they lie in the
+// pages into rings of three stages (bulk copies: a page of a head is contiguous), and the
+// converting warps, half of them for K, half for V, make bf16 tiles of them in the products'
+// own ring. (Loads into registers a tile ahead kept the warps waiting: 1.9 us a tile of
+// heads of 128; all warps on one ring of K and V in turn 1.45.)
+constexpr int kStages = 3;
+__host__ __device__ constexpr int stage_rows(int hd) { return hd == 64 ? kTile : kTile / 2; }
+__host__ __device__ constexpr int stage_bytes(int hd) { return stage_rows(hd) * (hd + hd / 32); }
+__host__ __device__ constexpr int less_bytes(int hd, bool q8) { return q8 ? 2 * kStages * stage_bytes(hd) : 0; }
 
-struct Stages {
-    uint64_t full[4], free[4];
-    uint32_t there[4];  // a stage's parts (of a page each) that hold rows of the pool; the others are zeros
-    int issued;
+struct Stages {  // [K, V]
+    uint64_t full[2][kStages], free[2][kStages];
+    uint32_t there[2][kStages];  // a stage's parts (of a page each) that hold rows of the pool; the others are zeros
+    int issued[2];
 };
-constexpr int kOwnBytes = 4 * kBadWords + 112;  // of a CTA: bad rows, and this
-static_assert(sizeof(Stages) <= 112 && 4 * kBadWords % 8 == 0, "");
+constexpr int kOwnBytes = 4 * kBadWords + 128;  // of a CTA: bad rows, and this
+static_assert(sizeof(Stages) <= 128 && 4 * kBadWords % 8 == 0, "");
 
-template <int HD>
 __device__ __forceinline__ void init_stages(Stages *g, int readers) {
-    for (int u = 0; u < n_stages(HD); ++u) {
-        mbar_init(&g->full[u], 1);
-        mbar_init(&g->free[u], readers);
-    }
-    g->issued = 0;
-}
-
-// Calls f(is_k, tile) for all tiles of a split in their order, while it returns true.
-template <class F>
-__device__ __forceinline__ void each_tile(int nt, F f) {
-    for (int i = -1; i < nt; ++i) {
-        if (i + 1 < nt && !f(true, i + 1)) return;
-        if (i >= 0 && !f(false, i)) return;
+    for (int o = 0; o < 2; ++o) {
+        for (int u = 0; u < kStages; ++u) {
+            mbar_init(&g->full[o][u], 1);
+            mbar_init(&g->free[o][u], readers);
+        }
+        g->issued[o] = 0;
     }
 }
 
-// The copying warp.
+// A copying warp: all of a split's K (o = 0) or V.
 template <int HD>
-__device__ __forceinline__ void stage_pages(Stages *g, uint8_t *stages, const PagedArgs &a, int b, int kvh, const Span &sp,
-                                            int t0, int nt, int lane, const Wait &w) {
-    constexpr int N = n_stages(HD), kRow = HD + HD / 32;
-    const int parts = max(kTile >> a.shift, 1), rows = kTile / parts;
+__device__ __forceinline__ void stage_pages(Stages *g, uint8_t *stages, int o, const PagedArgs &a, int b, int kvh,
+                                            const Span &sp, int t0, int nt, int lane, const Wait &w) {
+    constexpr int HR = stage_rows(HD), PER = kTile / HR;
+    const int parts = max(HR >> a.shift, 1), rows = HR / parts, n_items = nt * PER;
     const int32_t *table = a.table + (int64_t)b * a.max_pages;
-    auto row_of = [&](int i) {
-        const int j = sp.tile(t0 + i) * kTile + lane * rows;
-        return lane < parts && i < nt && j < sp.end ? j : -1;
+    const uint8_t *codes = static_cast<const uint8_t *>(o ? a.vc : a.kc), *scales = o ? a.vs : a.ks;
+    stages += o * kStages * stage_bytes(HD);
+    auto row_of = [&](int e) {
+        if (lane >= parts || e >= n_items) return -1;
+        const int j = sp.tile(t0 + e / PER) * kTile + e % PER * HR + lane * rows;
+        return j < sp.end ? j : -1;
     };
     auto ask = [&](int j) { return j < 0 ? -1 : table[j >> a.shift]; };
-    // (K(i + 1) and V(i) come one behind the other: two pages a lane, each asked for a tile ahead)
-    int jk = row_of(0), pk = ask(jk), jv = jk, pv = pk, e = 0;
-    each_tile(nt, [&](bool is_k, int i) __attribute__((always_inline)) {
-        const int j = is_k ? jk : jv, page = is_k ? pk : pv;
-        if (is_k) {
-            jk = row_of(i + 1);
-            pk = ask(jk);
-        } else {
-            jv = row_of(i + 1);
-            pv = ask(jv);
-        }
-        const int u = e % N;
-        const bool ok = e < N || mbar_wait(&g->free[u], (e / N - 1) & 1, w);
-        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+    int next = row_of(0), page_next = ask(next);  // (the page is asked for an item before it is used)
+    for (int e = 0; e < n_items; ++e) {
+        const int j = next, page = page_next, u = e % kStages;
+        next = row_of(e + 1);
+        page_next = ask(next);
+        const bool ok = e < kStages || mbar_wait(&g->free[o][u], (e / kStages - 1) & 1, w);
+        if (!__all_sync(0xFFFFFFFFu, ok)) return;
         const bool there = j >= 0 && page >= 0 && page < a.n_pages;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
         const int at = a.shift < 31 ? j & (a.ps - 1) : j, n = min(rows, a.ps - at);  // row of the page, rows
         if (lane == 0) {
-            g->there[u] = mask;
-            mbar_expect_tx(&g->full[u], parts > 1 ? __popc(mask) * rows * kRow : there ? n * kRow : 0);
-            *(volatile int *)&g->issued = e + 1;
+            g->there[o][u] = mask;
+            mbar_expect_tx(&g->full[o][u], (parts > 1 ? __popc(mask) * rows : there ? n : 0) * (HD + HD / 32));
+            *(volatile int *)&g->issued[o] = e + 1;
         }
         __syncwarp();
         if (there) {
             uint8_t *to = stages + u * stage_bytes(HD);
             const int64_t from = ((int64_t)page * a.Hkv + kvh) * a.ps + at;
-            bulk_load(to + lane * rows * HD, static_cast<const uint8_t *>(is_k ? a.kc : a.vc) + from * HD, n * HD,
-                      &g->full[u]);
-            bulk_load(to + kTile * HD + lane * rows * (HD / 32), (is_k ? a.ks : a.vs) + from * (HD / 32), n * (HD / 32),
-                      &g->full[u]);
+            bulk_load(to + lane * rows * HD, codes + from * HD, n * HD, &g->full[o][u]);
+            bulk_load(to + HR * HD + lane * rows * (HD / 32), scales + from * (HD / 32), n * (HD / 32), &g->full[o][u]);
         }
-        ++e;
-        return true;
-    });
+    }
 }
 
-// One of W converting warps, kTile / W rows of every tile: bf16 values into the ring,
-// 128-byte swizzled as TMA writes it; 16 elements of a row a lane.
+// One of W converting warps: its rows of every stage of K (who < W / 2) or V as bf16
+// values into the ring, 128-byte swizzled as TMA writes it. A lane takes 16 elements at a
+// time of every eighth row; of heads of 128 neighbouring rows' lanes take different
+// halves, so that the eight lanes that read or write at once meet in no bank.
 template <int HD, int KU, int VU, int W>
 __device__ __forceinline__ void convert_pages(Sync<KU, VU> *y, uint8_t *ring, Stages *g, const uint8_t *stages,
                                               const PagedArgs &a, int nt, int who, int lane, const Wait &w) {
-    constexpr int kKv = kHalfTile * (HD / 64), N = n_stages(HD);
-    constexpr int LPR = HD / 16, RPI = 32 / LPR, NI = kTile / W / RPI;  // lanes of a row, rows at once, times
-    const int sub = lane / LPR, dim = lane % LPR, row0 = who * (kTile / W) + sub, part_bits = min(a.shift, 7);
-    const int o = HD == 64 ? 0 : dim >> 2;  // this lane stores the second half of its elements first: no bank twice
-    const int ch = 2 * (dim & 3) + o;
-    int e = 0;
-    each_tile(nt, [&](bool is_k, int i) __attribute__((always_inline)) {
-        const int u = e % N, slot = is_k ? i % KU : i % VU;
-        bool ok = mbar_wait(&g->full[u], (e / N) & 1, w);
-        if (is_k ? i >= KU : i >= VU) ok = ok && (is_k ? s_done(y, i - KU, w) : pv_done(y, i - VU, w));
-        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
-        const uint8_t *codes = stages + u * stage_bytes(HD) + row0 * HD + dim * 16;
-        const uint8_t *scales = stages + u * stage_bytes(HD) + kTile * HD + row0 * (HD / 32) + (dim >> 1);
-        uint8_t *to = ring + (is_k ? slot : KU + slot) * kKv + (dim >> 2) * kHalfTile + row0 * 128;
-        const uint32_t there = g->there[u];
-        uint4 x[NI];
-        uint32_t f[NI];
+    constexpr int kKv = kHalfTile * (HD / 64), HR = stage_rows(HD), PER = kTile / HR, ROWS = HR / (W / 2), H = HD / 64;
+    const bool is_k = who < W / 2;
+    const int op = is_k ? 0 : 1, sub = lane >> 2, dim = lane & 3, row0 = who % (W / 2) * ROWS + sub;
+    const int part_bits = a.shift < 31 ? min(a.shift, HR == kTile ? 7 : 6) : 7;
+    const int units = is_k ? KU : VU, h0 = H > 1 ? sub & 1 : 0;
+    const uint8_t *from = stages + op * kStages * stage_bytes(HD);
+    const int to0 = h0 * kHalfTile + row0 * 128 + (((2 * dim) ^ sub) << 4), to1 = to0 ^ 16;  // (row0 & 7 is sub)
+    const uint32_t all = (1u << max(HR >> part_bits, 1)) - 1u;  // (at most 16 parts)
+    int u = 0, slot = 0;
+    uint32_t stage_phase = 0, slot_phase = 1;  // (of a slot: of the products that last read it)
+    for (int e = 0; e < nt * PER; ++e) {
+        bool ok = mbar_wait(&g->full[op][u], stage_phase, w);
+        if (e >= units * PER && e % PER == 0) ok = ok && mbar_wait(is_k ? &y->k_done[slot] : &y->v_done[slot], slot_phase, w);
+        if (!__all_sync(0xFFFFFFFFu, ok)) return;
+        const uint8_t *codes = from + u * stage_bytes(HD) + row0 * HD + h0 * 64 + dim * 16;
+        const uint8_t *scales = from + u * stage_bytes(HD) + HR * HD + row0 * (HD / 32) + h0 * 2 + (dim >> 1);
+        uint8_t *to = ring + (is_k ? slot : KU + slot) * kKv + e % PER * HR * 128;
+        const uint32_t there = g->there[op][u];
 #pragma unroll
-        for (int k = 0; k < NI; ++k) {
-            x[k] = *reinterpret_cast<const uint4 *>(codes + k * RPI * HD);
-            f[k] = scales[k * RPI * (HD / 32)];
-        }
+        for (int r0 = 0; r0 < ROWS; r0 += 32 / H) {
+            constexpr int N = 4;  // loads at once: N / H groups of eight rows
+            uint4 x[N];
+            uint32_t f[N];
 #pragma unroll
-        for (int k = 0; k < NI; ++k) {
-            const uint32_t z = (there >> ((row0 + k * RPI) >> part_bits)) & 1 ? e4m3_factor(f[k]) : 0u;
-            const uint32_t a0 = o ? x[k].z : x[k].x, a1 = o ? x[k].w : x[k].y, b0 = o ? x[k].x : x[k].z, b1 = o ? x[k].y : x[k].w;
-            const uint2 v0 = e4m3_values(a0, z), v1 = e4m3_values(a1, z), v2 = e4m3_values(b0, z), v3 = e4m3_values(b1, z);
-            const int r7 = (row0 + k * RPI) & 7;
-            *reinterpret_cast<uint4 *>(to + k * RPI * 128 + ((ch ^ r7) << 4)) = make_uint4(v0.x, v0.y, v1.x, v1.y);
-            *reinterpret_cast<uint4 *>(to + k * RPI * 128 + ((ch ^ 1 ^ r7) << 4)) = make_uint4(v2.x, v2.y, v3.x, v3.y);
+            for (int k = 0; k < N; ++k) {
+                const int r = r0 + k / H * 8, flip = k % H;  // (the other half: 64 bytes on, or back)
+                x[k] = *reinterpret_cast<const uint4 *>(codes + r * HD + (flip ? 64 - 128 * h0 : 0));
+                f[k] = scales[r * (HD / 32) + (flip ? 2 - 4 * h0 : 0)];
+            }
+            if (there != all) {  // rows that are not there: zeros
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (!((there >> ((row0 + r0 + k / H * 8) >> part_bits)) & 1)) x[k] = make_uint4(0, 0, 0, 0), f[k] = 127;
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const uint32_t z = e4m3_factor(f[k]);
+                const uint2 v0 = e4m3_values(x[k].x, z), v1 = e4m3_values(x[k].y, z), v2 = e4m3_values(x[k].z, z),
+                            v3 = e4m3_values(x[k].w, z);
+                uint8_t *at = to + (r0 + k / H * 8) * 128 + (k % H ? kHalfTile - 2 * kHalfTile * h0 : 0);
+                *reinterpret_cast<uint4 *>(at + to0) = make_uint4(v0.x, v0.y, v1.x, v1.y);
+                *reinterpret_cast<uint4 *>(at + to1) = make_uint4(v2.x, v2.y, v3.x, v3.y);
+            }
         }
         async_fence();
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(&g->free[u]);
+            mbar_arrive(&g->free[op][u]);
             mbar_arrive(is_k ? &y->k_full[slot] : &y->v_full[slot]);
         }
-        ++e;
-        return true;
-    });
+        if (++u == kStages) u = 0, stage_phase ^= 1;
+        if (e % PER == PER - 1 && ++slot == units) slot = 0, slot_phase ^= 1;
+    }
 }
 
 // After a wait that ran out: the copies that were issued have landed.
-template <int HD>
-__device__ __noinline__ void settle_stages(Stages *g) {
-    const int n = *(volatile int *)&g->issued;
-    for (int e = max(0, n - n_stages(HD)); e < n; ++e) mbar_await(&g->full[e % n_stages(HD)], (e / n_stages(HD)) & 1);
+static __device__ __noinline__ void settle_stages(Stages *g) {
+    for (int o = 0; o < 2; ++o) {
+        const int n = *(volatile int *)&g->issued[o];
+        for (int e = max(0, n - kStages); e < n; ++e) mbar_await(&g->full[o][e % kStages], (e / kStages) & 1);
+    }
 }
 
 // The products of the V rows that were taken out of their tiles (a value that is no
@@ -413,7 +416,7 @@ __device__ __noinline__ void add_hidden_rows(const PagedArgs &a, const TreeArgs 
 
 template <int HD, int TERMS, int NR, bool Q8>
 __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
-    paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PagedArgs a) {
+    paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PagedArgs a) {
     using C = AttnShape<HD, TERMS, NR, less_bytes(HD, Q8)>;
     constexpr int kThreads = paged_threads(false, Q8);
     constexpr int N = C::N, PT = weight_terms(TERMS), PN = C::PN, KU = C::KU, VU = C::VU;
@@ -467,8 +470,8 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
     const int t0 = (int)((int64_t)split * sp.tiles / S), nt = (int)((int64_t)(split + 1) * sp.tiles / S) - t0;
     if (warp == kKWarp) {
         if (lane == 0) {
-            if constexpr (Q8) init_stages<HD>(stage, conv_warps(false));
-            init_paged<false, Q8>(y, bad);
+            if constexpr (Q8) init_stages(stage, conv_warps(false) / 2);
+            init_paged<false, Q8>(y, bad, conv_warps(false) / 2 * (kTile / stage_rows(HD)));
         }
         __syncwarp();
         if constexpr (!Q8) {  // the first copies need nobody else
@@ -493,8 +496,8 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
     if (warp >= first_conv(false)) {
         if constexpr (Q8)
             convert_pages<HD, KU, VU, conv_warps(false)>(y, sm, stage, stages, a, nt, warp - first_conv(false), lane, wt);
-    } else if (Q8 && warp == kKWarp) {
-        if constexpr (Q8) stage_pages<HD>(stage, stages, a, wk.b, kvh, sp, t0, nt, lane, wt);
+    } else if (Q8 && (warp == kKWarp || warp == kVWarp)) {
+        if constexpr (Q8) stage_pages<HD>(stage, stages, warp == kVWarp, a, wk.b, kvh, sp, t0, nt, lane, wt);
     } else if (!Q8 && warp == kKWarp) {
         load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, KU, nt, lane, wt);
     } else if (!Q8 && warp == kVWarp) {
@@ -729,7 +732,7 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
     __syncthreads();
     if (*err) {  // a wait ran out (nobody waits any more: the same for all threads): the rows are NaN
         if constexpr (Q8)
-            if (warp == kKWarp && elect()) settle_stages<HD>(stage);
+            if (warp == kKWarp && elect()) settle_stages(stage);
         settle(y, a.err);
         if (tid < NR) lsum[tid] = __uint_as_float(0x7FC00000u);
         __syncthreads();
@@ -761,12 +764,15 @@ __device__ __forceinline__ bool pair_any(int id, bool x) {
 template <int HD, int TERMS, bool Q8>
 __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     paged_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                         const PagedArgs a) {
+                         const __grid_constant__ PagedArgs a) {
     using C = RowShape<HD, TERMS, kOwnBytes, less_bytes(HD, Q8)>;
     constexpr int kThreads = paged_threads(true, Q8);
     constexpr int KU = C::KU, VU = C::VU, NB = C::NB, PT = weight_terms(TERMS);
     constexpr bool kScaled = TERMS > 1;
     constexpr int kHalf = kTile / 2;  // a softmax thread's columns of a tile
+    // Scores that a thread keeps from the maximum to the weights; with 8-bit pages, whose
+    // converting warps leave 80 registers, it reads them again.
+    constexpr int kKeep = Q8 ? 32 : kHalf;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *Qs = sm + C::kOffQ;
@@ -811,8 +817,8 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     const int t0 = (int)((int64_t)split * sp.tiles / S), nt = (int)((int64_t)(split + 1) * sp.tiles / S) - t0;
     if (warp == kKWarp) {
         if (lane == 0) {
-            if constexpr (Q8) init_stages<HD>(stage, conv_warps(true));
-            init_paged<true, Q8>(y, bad);
+            if constexpr (Q8) init_stages(stage, conv_warps(true) / 2);
+            init_paged<true, Q8>(y, bad, conv_warps(true) / 2 * (kTile / stage_rows(HD)));
         }
         __syncwarp();
         if constexpr (!Q8) {  // the first copies need nobody else
@@ -833,8 +839,8 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     if (warp >= first_conv(true)) {
         if constexpr (Q8)
             convert_pages<HD, KU, VU, conv_warps(true)>(y, sm, stage, stages, a, nt, warp - first_conv(true), lane, wt);
-    } else if (Q8 && warp == kKWarp) {
-        if constexpr (Q8) stage_pages<HD>(stage, stages, a, wk.b, kvh, sp, t0, nt, lane, wt);
+    } else if (Q8 && (warp == kKWarp || warp == kVWarp)) {
+        if constexpr (Q8) stage_pages<HD>(stage, stages, warp == kVWarp, a, wk.b, kvh, sp, t0, nt, lane, wt);
     } else if (!Q8 && warp == kKWarp) {
         load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, KU, nt, lane, wt);
     } else if (!Q8 && warp == kVWarp) {
@@ -898,25 +904,32 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
             const uint32_t tt = tT + (i % NB) * C::kThird + h * (kHalf / 2) + mylane;
             const int tile = sp.tile(t0 + i), at = tile * kTile, part = sp.part(tile);
             if (live) {
-                float x[kHalf];
+                float x[kKeep];
+                // The scores of columns w0 .. w0 + kKeep - 1 of the half, hidden ones -inf.
+                auto load = [&](int w0) {
 #pragma unroll
-                for (int e = 0; e < kHalf; e += 16) tmem_ld16(ts + e, x + e);
-                tmem_ld_wait();
-                pin<kHalf>(x);
-                if (part >= 0) {
+                    for (int e = 0; e < kKeep; e += 16) tmem_ld16(ts + w0 + e, x + e);
+                    tmem_ld_wait();
+                    pin<kKeep>(x);
+                    if (part >= 0) {
 #pragma unroll
-                    for (int w = 0; w < kHalf; w += 32) {
-                        const uint32_t see = sp.sees32(pos, at + h * kHalf + w);
+                        for (int w = 0; w < kKeep; w += 32) {
+                            const uint32_t see = sp.sees32(pos, at + h * kHalf + w0 + w);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((see >> e) & 1)) x[w + e] = -INFINITY;
+                            for (int e = 0; e < 32; ++e)
+                                if (!((see >> e) & 1)) x[w + e] = -INFINITY;
+                        }
                     }
-                }
+                };
                 float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < kHalf; e += 8)
+                for (int w0 = 0; w0 < kHalf; w0 += kKeep) {
+                    load(w0);
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) t4[w] = fmaxf(fmaxf(t4[w], x[e + 2 * w]), x[e + 2 * w + 1]);
+                    for (int e = 0; e < kKeep; e += 8)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) t4[w] = fmaxf(fmaxf(t4[w], x[e + 2 * w]), x[e + 2 * w + 1]);
+                }
                 float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                 if (!kScaled) top *= c;  // (the scale is positive)
                 if (pair_any(pair, top > m + kRaise)) {
@@ -947,9 +960,10 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int w0 = 0; w0 < kHalf; w0 += 32) {
+                    if (kKeep < kHalf) load(w0);
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float &x0 = x[w0 + e], &x1 = x[w0 + e + 1];
+                        float &x0 = x[w0 % kKeep + e], &x1 = x[w0 % kKeep + e + 1];
                         fma2(x0, x1, kScaled ? 1.f : c, m, m);
                         x0 = ex2(x0);
                         x1 = ex2(x1);
@@ -960,7 +974,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
                         uint32_t w[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            float &x0 = x[w0 + 2 * e], &x1 = x[w0 + 2 * e + 1];
+                            float &x0 = x[w0 % kKeep + 2 * e], &x1 = x[w0 % kKeep + 2 * e + 1];
                             w[e] = pack_bf16(x0, x1);
                             if (t + 1 < PT) less2(x0, x1, w[e]);
                         }
@@ -1062,7 +1076,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     __syncthreads();
     if (*err) {  // a wait ran out (nobody waits any more: the same for all threads): the rows are NaN
         if constexpr (Q8)
-            if (warp == kKWarp && elect()) settle_stages<HD>(stage);
+            if (warp == kKWarp && elect()) settle_stages(stage);
         settle(y, a.err);
         if (tid < kRows) lsum[tid] = __uint_as_float(0x7FC00000u);
         __syncthreads();
@@ -1078,7 +1092,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
 
 // Joins the S splits' partial results of every unit: grid (tiles of rows, kv heads, dims).
 template <int HD, int TERMS, int NR>
-__global__ void __launch_bounds__(256) paged_join(const PagedArgs a, int S) {
+__global__ void __launch_bounds__(256) paged_join(const __grid_constant__ PagedArgs a, int S) {
     constexpr int64_t PF = part_floats(NR, HD);
     __shared__ float ms[max_splits(NR) * NR], wg[max_splits(NR) * NR];
     const int kvh = blockIdx.y, G = a.Hq / a.Hkv;
