@@ -161,11 +161,24 @@ __device__ __forceinline__ float pool_value(const void *pool, const uint8_t *sca
     }
 }
 
-// (landers: arrivals that make a tile of 8-bit pages full)
-template <bool MANY, bool Q8, int KU, int VU>
-__device__ __forceinline__ void init_paged(Sync<KU, VU> *y, uint32_t *bad, int landers) {
-    for (int i = 0; i < kBadWords; ++i) bad[i] = 0;
-    init_sync(y, Q8 ? landers : 1, soft_threads(MANY) / 64);
+// The CTA's barriers and words, by a whole warp. (landers: arrivals that make a tile of K,
+// or of V, full; warps: of a softmax group)
+template <int KU, int VU>
+__device__ __forceinline__ void init_paged(Sync<KU, VU> *y, uint32_t *bad, int landers, int warps, int lane) {
+    static_assert(KU <= 8 && VU <= 8 && kBadWords <= 32, "");
+    if (lane < KU) mbar_init(&y->k_full[lane], landers), mbar_init(&y->k_done[lane], 1);
+    if (lane < VU) mbar_init(&y->v_full[lane], landers), mbar_init(&y->v_done[lane], 1);
+    if (lane < 2) mbar_init(&y->s_read[lane], warps);
+    if (lane < 4) mbar_init(&y->p_full[lane], warps);
+    if (lane < kBadWords) bad[lane] = 0;
+    if (lane < 2) y->bad[lane] = 0;
+    if (lane == 0) {
+        mbar_init(&y->quiet, 1);
+        y->err = y->k_issued = y->v_issued = 0;
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    async_fence();
+    __syncwarp();
 }
 
 __device__ __forceinline__ bool any_bad(const uint32_t *bad) {
@@ -175,41 +188,9 @@ __device__ __forceinline__ bool any_bad(const uint32_t *bad) {
     return x != 0;
 }
 
-// The first copies of a split, K and V, by one warp: all page numbers are asked for at
-// once (one after the other they took 8,400 cycles for 12 tiles), and K and V share them.
-template <int HD, int KU, int VU>
-__device__ __forceinline__ void load_first(Sync<KU, VU> *y, uint8_t *ring, const CUtensorMap *kmap, const CUtensorMap *vmap,
-                                           const PagedArgs &a, int b, int kvh, const Span &sp, int t0, int nt, int lane) {
-    constexpr int kKv = kHalfTile * (HD / 64), kHalves = HD / 64, kMost = KU > VU ? KU : VU;
-    const int parts = max(kTile >> a.shift, 1), rows = kTile / parts;
-    const int part = lane / kHalves, half = lane % kHalves;
-    const bool mine = lane < parts * kHalves;
-    const int32_t *table = a.table + (int64_t)b * a.max_pages;
-    int page[kMost];
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-        const int j = sp.tile(t0 + i) * kTile + part * rows;
-        page[i] = a.n_pages;
-        if (mine && i < nt && j < sp.end) page[i] = table[j >> a.shift];
-    }
-    for (int i = lane; i < KU + VU; i += 32)
-        if (i < KU ? i < nt : i - KU < nt) mbar_expect_tx(i < KU ? &y->k_full[i] : &y->v_full[i - KU], kKv);
-    if (lane == 0) *(volatile int *)&y->k_issued = min(nt, KU), *(volatile int *)&y->v_issued = min(nt, VU);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-        if (i >= nt || !mine) break;
-        const int j = sp.tile(t0 + i) * kTile + part * rows;
-        const bool there = page[i] >= 0 && page[i] < a.n_pages;
-        const int plane = (there ? page[i] : a.n_pages) * a.Hkv + kvh, row = a.shift < 31 ? j & (a.ps - 1) : j;
-        const int at = half * kHalfTile + part * rows * 128;
-        if (i < KU) tma_load_3d(ring + i * kKv + at, kmap, half * 64, row, plane, &y->k_full[i]);
-        if (i < VU) tma_load_3d(ring + (KU + i) * kKv + at, vmap, half * 64, row, plane, &y->v_full[i]);
-    }
-    __syncwarp();
-}
-
-// A warp's work: tiles from .. to - 1 of a split's K (or V), a box of a page a lane.
+// A warp's work: tiles from .. to - 1 of a split's K (or V), a box of a page a lane. (The
+// lanes' copies go out one behind the other, ~48 cycles each: before the CTA's first
+// barrier only one tile's do; all that the rings hold took 6,000 cycles there.)
 template <int HD, int KU, int VU>
 __device__ __forceinline__ void load_pages(Sync<KU, VU> *y, uint8_t *ring, const CUtensorMap *map, bool is_k,
                                            const PagedArgs &a, int b, int kvh, const Span &sp, int t0, int from, int to,
@@ -265,14 +246,12 @@ struct Stages {  // [K, V]
 constexpr int kOwnBytes = 4 * kBadWords + 128;  // of a CTA: bad rows, and this
 static_assert(sizeof(Stages) <= 128 && 4 * kBadWords % 8 == 0, "");
 
-__device__ __forceinline__ void init_stages(Stages *g, int readers) {
-    for (int o = 0; o < 2; ++o) {
-        for (int u = 0; u < kStages; ++u) {
-            mbar_init(&g->full[o][u], 1);
-            mbar_init(&g->free[o][u], readers);
-        }
-        g->issued[o] = 0;
+__device__ __forceinline__ void init_stages(Stages *g, int readers, int lane) {
+    if (lane < 2 * kStages) {
+        mbar_init(&g->full[0][0] + lane, 1);
+        mbar_init(&g->free[0][0] + lane, readers);
     }
+    if (lane < 2) g->issued[lane] = 0;
 }
 
 // A copying warp: all of a split's K (o = 0) or V.
@@ -443,8 +422,14 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
     const int S = gridDim.x / a.units, split = blockIdx.x % S, kvh = blockIdx.y, G = a.Hq / a.Hkv;
     const int turn = blockIdx.x / S;
     const float c = a.scale * 1.44269504088896340736f;  // scores in powers of two
+    // (what needs nothing of the kernel before comes before its end is awaited)
+    if (warp == kKWarp) {
+        if constexpr (Q8) init_stages(stage, conv_warps(false) / 2, lane);
+        init_paged(y, bad, Q8 ? conv_warps(false) / 2 * (kTile / stage_rows(HD)) : 1, soft_threads(false) / 64, lane);
+    }
     pdl_wait();
     if (!a.part) pdl_trigger();
+    if (warp == kMmaWarp) tmem_alloc(&y->tmem, C::kCols);
     const Work wk = find_work(a, turn, NR, G, lane);
     const int row0 = wk.row0, rows = wk.rows;
     const TreeArgs t = tree_args<TERMS>(a, wk);
@@ -465,20 +450,18 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
             }
         }
     }
-    if (rows <= 0) return;  // the whole cluster
+    if (rows <= 0) {  // the whole cluster
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == kMmaWarp) tmem_free(uniform(y->tmem), C::kCols);
+        return;
+    }
     const Span sp = span_of(a, wk, G);
     const int t0 = (int)((int64_t)split * sp.tiles / S), nt = (int)((int64_t)(split + 1) * sp.tiles / S) - t0;
-    if (warp == kKWarp) {
-        if (lane == 0) {
-            if constexpr (Q8) init_stages(stage, conv_warps(false) / 2);
-            init_paged<false, Q8>(y, bad, conv_warps(false) / 2 * (kTile / stage_rows(HD)));
-        }
-        __syncwarp();
-        if constexpr (!Q8) {  // the first copies need nobody else
-            load_first<HD>(y, sm, &kmap, &vmap, a, wk.b, kvh, sp, t0, nt, lane);
-        }
+    if (!Q8 && warp == kKWarp) {  // the first copy needs nobody else
+        load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 0, min(nt, 1), lane, wt);
     } else if (warp == kMmaWarp) {
-        tmem_alloc(&y->tmem, C::kCols);
         if constexpr (kOnes)
             for (int i = lane; i < C::kOnes / 16; i += 32)  // chunk 0 of row i / 8 sits at chunk (row & 7)
                 *reinterpret_cast<uint4 *>(sm + C::kOffOnes + i * 16) =
@@ -499,9 +482,9 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), 1)
     } else if (Q8 && (warp == kKWarp || warp == kVWarp)) {
         if constexpr (Q8) stage_pages<HD>(stage, stages, warp == kVWarp, a, wk.b, kvh, sp, t0, nt, lane, wt);
     } else if (!Q8 && warp == kKWarp) {
-        load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, KU, nt, lane, wt);
+        load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 1, nt, lane, wt);
     } else if (!Q8 && warp == kVWarp) {
-        load_pages<HD>(y, sm, &vmap, false, a, wk.b, kvh, sp, t0, VU, nt, lane, wt);
+        load_pages<HD>(y, sm, &vmap, false, a, wk.b, kvh, sp, t0, 0, nt, lane, wt);
     } else if (warp == kMmaWarp) {
         constexpr uint32_t idS = idesc_bf16(N, false, false), idO = idesc_bf16(PN, true, true);
         const uint64_t q = sw128_desc(saddr(Qs), 16);
@@ -761,6 +744,23 @@ __device__ __forceinline__ bool pair_any(int id, bool x) {
     return r != 0;
 }
 
+// A thread's N consecutive dims of a result.
+template <int TERMS, int N>
+__device__ __forceinline__ void put_row(const TreeArgs &t, int64_t at, const float (&o)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; e += 8) {
+        if constexpr (TERMS == 1) {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(t.out) + at + e) =
+                make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]), pack_bf16(o[e + 4], o[e + 5]),
+                           pack_bf16(o[e + 6], o[e + 7]));
+        } else {
+            float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(t.out) + at + e);
+            to[0] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            to[1] = make_float4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
+        }
+    }
+}
+
 template <int HD, int TERMS, bool Q8>
 __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     paged_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -792,8 +792,14 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     const int S = gridDim.x / a.units, split = blockIdx.x % S, kvh = blockIdx.y, G = a.Hq / a.Hkv;
     const int turn = blockIdx.x / S;
     const float c = a.scale * 1.44269504088896340736f;
+    // (what needs nothing of the kernel before comes before its end is awaited)
+    if (warp == kKWarp) {
+        if constexpr (Q8) init_stages(stage, conv_warps(true) / 2, lane);
+        init_paged(y, bad, Q8 ? conv_warps(true) / 2 * (kTile / stage_rows(HD)) : 1, soft_threads(true) / 64, lane);
+    }
     pdl_wait();
     if (!a.part) pdl_trigger();
+    if (warp == kMmaWarp) tmem_alloc(&y->tmem, C::kCols);
     const Work wk = find_work(a, turn, kRows, G, lane);
     const int row0 = wk.row0, rows = wk.rows;
     const TreeArgs t = tree_args<TERMS>(a, wk);
@@ -812,20 +818,17 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
                                            (((ch % 8) ^ (r & 7)) << 4)) = q[k];
         }
     }
-    if (rows <= 0) return;  // the whole cluster
+    if (rows <= 0) {  // the whole cluster
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == kMmaWarp) tmem_free(uniform(y->tmem), C::kCols);
+        return;
+    }
     const Span sp = span_of(a, wk, G);
     const int t0 = (int)((int64_t)split * sp.tiles / S), nt = (int)((int64_t)(split + 1) * sp.tiles / S) - t0;
-    if (warp == kKWarp) {
-        if (lane == 0) {
-            if constexpr (Q8) init_stages(stage, conv_warps(true) / 2);
-            init_paged<true, Q8>(y, bad, conv_warps(true) / 2 * (kTile / stage_rows(HD)));
-        }
-        __syncwarp();
-        if constexpr (!Q8) {  // the first copies need nobody else
-            load_first<HD>(y, sm, &kmap, &vmap, a, wk.b, kvh, sp, t0, nt, lane);
-        }
-    } else if (warp == kMmaWarp) {
-        tmem_alloc(&y->tmem, C::kCols);
+    if (!Q8 && warp == kKWarp) {  // the first copy needs nobody else
+        load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 0, min(nt, 1), lane, wt);
     }
     async_fence();
     tc_fence_before();
@@ -842,9 +845,9 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     } else if (Q8 && (warp == kKWarp || warp == kVWarp)) {
         if constexpr (Q8) stage_pages<HD>(stage, stages, warp == kVWarp, a, wk.b, kvh, sp, t0, nt, lane, wt);
     } else if (!Q8 && warp == kKWarp) {
-        load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, KU, nt, lane, wt);
+        load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 1, nt, lane, wt);
     } else if (!Q8 && warp == kVWarp) {
-        load_pages<HD>(y, sm, &vmap, false, a, wk.b, kvh, sp, t0, VU, nt, lane, wt);
+        load_pages<HD>(y, sm, &vmap, false, a, wk.b, kvh, sp, t0, 0, nt, lane, wt);
     } else if (warp == kMmaWarp) {
         constexpr uint32_t idS = idesc_bf16(kTile, false, false), idO = idesc_bf16(HD, false, true);
         const uint64_t q = sw128_desc(saddr(Qs), 16);
@@ -1016,26 +1019,24 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
                 const float sum = (sums[row] + sums[kRows + row]) + (sums[2 * kRows + row] + sums[3 * kRows + row]);
                 // (no row seen: zeros; a wait that ran out: NaN)
                 const float inv = *err ? __uint_as_float(0x7FC00000u) : sum == 0.f ? 0.f : 1.f / sum;
-                const float f0 = nt > 0 ? scales[row] * inv : 0.f, f1 = nt > 1 ? scales[kRows + row] * inv : 0.f;
+                const float f0 = scales[row] * inv, f1 = scales[kRows + row] * inv;
                 const int rg = row0 + row, d0 = (g * 2 + h) * (HD / 4);
                 const int64_t at = (rg / G) * t.o_token + (int64_t)(kvh * G + rg % G) * HD + d0;
-#pragma unroll 1
+                float o[HD / 4], p[HD / 4];
+#pragma unroll
                 for (int d = 0; d < HD / 4; d += 16) {
-                    float o[16], p[16];
-                    if (nt > 0) tmem_ld16(tO + mylane + d0 + d, o);
-                    if (nt > 1) tmem_ld16(tO + HD + mylane + d0 + d, p);
-                    tmem_ld_wait();
-                    pin<16>(o);
-                    pin<16>(p);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        o[e] = nt > 0 ? f0 * o[e] : *err ? f0 + inv : 0.f;
-                        if (nt > 1) o[e] = fmaf(f1, p[e], o[e]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        if (row < rows) put4<TERMS>(t, at + d + e, make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                    if (nt > 0) tmem_ld16(tO + mylane + d0 + d, o + d);
+                    if (nt > 1) tmem_ld16(tO + HD + mylane + d0 + d, p + d);
                 }
+                tmem_ld_wait();
+                pin<HD / 4>(o);
+                pin<HD / 4>(p);
+#pragma unroll
+                for (int e = 0; e < HD / 4; ++e) {
+                    o[e] = nt > 0 ? f0 * o[e] : inv;  // (no tile: 0, or NaN)
+                    if (nt > 1) o[e] = fmaf(f1, p[e], o[e]);
+                }
+                if (row < rows) put_row<TERMS, HD / 4>(t, at, o);
             }
         } else
 #pragma unroll 1

@@ -275,21 +275,20 @@ struct Sync {
     uint32_t bad[2];              // drafted rows taken out of the second product
 };
 
-// (landers: arrivals that make a tile of K, or of V, full; warps: of a group)
 template <int KU, int VU>
-__device__ __forceinline__ void init_sync(Sync<KU, VU> *y, int landers = 1, int warps = kSoftWarps / 2) {
+__device__ __forceinline__ void init_sync(Sync<KU, VU> *y) {
     for (int u = 0; u < KU; ++u) {
-        mbar_init(&y->k_full[u], landers);
+        mbar_init(&y->k_full[u], 1);
         mbar_init(&y->k_done[u], 1);
     }
     for (int u = 0; u < VU; ++u) {
-        mbar_init(&y->v_full[u], landers);
+        mbar_init(&y->v_full[u], 1);
         mbar_init(&y->v_done[u], 1);
     }
     for (int g = 0; g < 2; ++g) {
-        mbar_init(&y->s_read[g], warps);
-        mbar_init(&y->p_full[g], warps);
-        mbar_init(&y->p_full[g + 2], warps);
+        mbar_init(&y->s_read[g], kSoftWarps / 2);
+        mbar_init(&y->p_full[g], kSoftWarps / 2);
+        mbar_init(&y->p_full[g + 2], kSoftWarps / 2);
     }
     mbar_init(&y->quiet, 1);
     y->err = y->k_issued = y->v_issued = 0;
