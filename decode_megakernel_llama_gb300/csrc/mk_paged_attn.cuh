@@ -393,10 +393,10 @@ __device__ __noinline__ void add_hidden_rows(const PagedArgs &a, const TreeArgs 
     }
 }
 
-template <int HD, int TERMS, int NR, bool Q8>
-__global__ void __launch_bounds__(paged_threads(false, Q8), 1)
+template <int HD, int TERMS, int NR, bool Q8, int PER>
+__global__ void __launch_bounds__(paged_threads(false, Q8), PER)
     paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PagedArgs a) {
-    using C = AttnShape<HD, TERMS, NR, less_bytes(HD, Q8)>;
+    using C = AttnShape<HD, TERMS, NR, less_bytes(HD, Q8), PER>;
     constexpr int kThreads = paged_threads(false, Q8);
     constexpr int N = C::N, PT = weight_terms(TERMS), PN = C::PN, KU = C::KU, VU = C::VU;
     constexpr bool kScaled = TERMS > 1;             // the queries carry the scale already

@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kT, TPB == 1 && E == 8 ? kPerSm : 4) rope_appe
                 }
             }
             auto store = [&](int e, float4 y) {
-                if constexpr (Q8) {  // (every lane comes here: the block's largest is found by shuffles)
+                // (whole warps: a block's largest is found by shuffles; not where all heads are queries)
+                if (Q8 && h - sub + HPW > a.Hq) {
                     float most = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
                     if (!(y.x - y.x == 0.f && y.y - y.y == 0.f && y.z - y.z == 0.f && y.w - y.w == 0.f)) most = INFINITY;
 #pragma unroll

@@ -107,7 +107,8 @@ constexpr int kSoft = 2 * kGroup;
 constexpr int kMmaWarp = 0, kKWarp = 1, kVWarp = 2, kFirstSoft = 4, kSoftWarps = kSoft / 32;
 constexpr int kAttnThreads = kSoft + 32 * kFirstSoft;
 constexpr int kHalfTile = kTile * 128;  // bytes of 128 rows x 64 dims
-constexpr int kSmemMost = 232448;       // shared memory of a CTA
+constexpr int kSmemMost = 232448;       // shared memory of a CTA, and of one of two on an SM
+constexpr int kSmemHalf = 115712;
 constexpr float kNone = -3e38f;         // the maximum of a row that has seen nothing
 constexpr float kRaise = 8.f;           // a score this far above m (in powers of two) raises m
 
@@ -464,8 +465,8 @@ __device__ __forceinline__ void load_query8(const TreeArgs &a, int b, int kvh, i
     }
 }
 
-// (LESS: bytes of shared memory that the ring leaves to the caller, behind the rest)
-template <int HD, int TERMS, int NR, int LESS = 0>
+// (LESS: bytes of shared memory that the ring leaves to the caller, behind the rest; PER: CTAs an SM)
+template <int HD, int TERMS, int NR, int LESS = 0, int PER = 1>
 struct AttnShape {
     static constexpr int N = TERMS * NR, PN = weight_terms(TERMS) * NR;  // columns of S and of O
     static constexpr int kKv = kHalfTile * (HD / 64);    // bytes of a K (or V) tile
@@ -474,7 +475,7 @@ struct AttnShape {
     static constexpr int kUsed = 2 * (N + PN), kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     static constexpr int kOnes = HD == 64 ? 2048 : 0;  // 16 cache rows x 64: ones in the first column
     static constexpr int kMisc = 512 + 8 * MK_MAX_TREE + 4 * NR * (2 + 2 + 1 + 8);
-    static constexpr int kRoom = (kSmemMost - 1024 - 2 * kP - kQ - kOnes - kMisc - LESS) / kKv;
+    static constexpr int kRoom = ((PER == 1 ? kSmemMost : kSmemHalf) - 1024 - 2 * kP - kQ - kOnes - kMisc - LESS) / kKv;
     static constexpr int KU = (kRoom + 1) / 2 > 6 ? 6 : (kRoom + 1) / 2, VU = kRoom / 2 > 6 ? 6 : kRoom / 2;
     // With room for it S runs three tiles ahead of PV and starts as soon as the group
     // has read the scores before; else it follows PV(i), two tiles ahead.
@@ -1181,7 +1182,6 @@ cudaError_t configure() {
 // the runtime once for each device).
 template <class K>
 int active_clusters(int k, int n_sm) {
-    static_assert(2 * K::kSmem > kSmemMost, "one CTA an SM");
     static std::atomic<int> known[64][4];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) n = known[dev][k].load(std::memory_order_relaxed);
