@@ -416,7 +416,6 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
     float *lsum = corr + 2 * NR;                // [NR]
     float *wtmp = lsum + NR;                    // [2][4][NR]
     float *Os = reinterpret_cast<float *>(sm);  // [NR][HD], in the ring when the tiles are done
-    float *join = Os + NR * HD;                 // [3][kCluster][NR] behind it
 
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int S = gridDim.x / a.units, split = blockIdx.x % S, kvh = blockIdx.y, G = a.Hq / a.Hkv;
@@ -725,7 +724,7 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
         tmem_free(tS, C::kCols);
     }
     finish<HD, TERMS, NR, false, kThreads>(t, (int64_t)turn * a.Hkv + kvh, 0, kvh, G, row0, rows, split, S, Os, mref,
-                                   lsum, join);
+                                   lsum);
 }
 
 // Barriers of the softmax threads, and of a pair of their warps: a plain one, and a vote.
@@ -838,7 +837,6 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     // scores and third terms of tile i: + i % NB * 128, + i % NB * kThird; O of group g: + g * HD
     const uint32_t tS = uniform(y->tmem), tT = tS + NB * kTile, tO = tT + NB * C::kThird;
 
-    bool direct = false;  // (of the softmax threads: their results are written)
     if (warp >= first_conv(true)) {
         if constexpr (Q8)
             convert_pages<HD, KU, VU, conv_warps(true)>(y, sm, stage, stages, a, nt, warp - first_conv(true), lane, wt);
@@ -1005,69 +1003,45 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
         if (!h) gm[g * kRows + row] = m;
         rows_sync();
         tc_fence_after();  // (a group that passed early reads O behind the barrier, too)
-        // the groups' O to the larger maximum: group 0 writes, group 1 adds
+        // the groups' O and sums to the larger maximum; a row's four threads take a quarter of
+        // its dims each, from both groups' O
         const float best = fmaxf(m, gm[(g ^ 1) * kRows + row]), scale = g < nt ? ex2(m - best) : 0.f;
-        float *sums = join + 3 * kCluster * kRows;  // [4][128], in the ring
+        float *sums = join, *scales = sums + 4 * kRows;  // [4][128], [2][128], in the ring
         sums[(g * 2 + h) * kRows + row] = l * scale;
-        direct = S == 1 && !a.part && !any_bad(bad);
-        if (direct) {
-            // one split: a row's four threads a quarter of its dims each, from both groups' O
-            float *scales = sums + 4 * kRows;  // [2][128]
-            if (!h) scales[g * kRows + row] = scale;
-            rows_sync();
-            if (live) {  // (whole warps: they load together)
-                const float sum = (sums[row] + sums[kRows + row]) + (sums[2 * kRows + row] + sums[3 * kRows + row]);
-                // (no row seen: zeros; a wait that ran out: NaN)
-                const float inv = *err ? __uint_as_float(0x7FC00000u) : sum == 0.f ? 0.f : 1.f / sum;
-                const float f0 = scales[row] * inv, f1 = scales[kRows + row] * inv;
-                const int rg = row0 + row, d0 = (g * 2 + h) * (HD / 4);
-                const int64_t at = (rg / G) * t.o_token + (int64_t)(kvh * G + rg % G) * HD + d0;
-                float o[HD / 4], p[HD / 4];
+        if (!h) scales[g * kRows + row] = scale;
+        const bool direct = S == 1 && !a.part && !any_bad(bad);
+        rows_sync();
+        const float sum = (sums[row] + sums[kRows + row]) + (sums[2 * kRows + row] + sums[3 * kRows + row]);
+        if (live) {  // (whole warps: they load together)
+            // one split: the result (no row seen: zeros; a wait that ran out: NaN); else its part of it
+            const float inv = !direct ? 1.f : *err ? __uint_as_float(0x7FC00000u) : sum == 0.f ? 0.f : 1.f / sum;
+            const float f0 = scales[row] * inv, f1 = scales[kRows + row] * inv;
+            const int d0 = (g * 2 + h) * (HD / 4);
+            float o[HD / 4], p[HD / 4];
 #pragma unroll
-                for (int d = 0; d < HD / 4; d += 16) {
-                    if (nt > 0) tmem_ld16(tO + mylane + d0 + d, o + d);
-                    if (nt > 1) tmem_ld16(tO + HD + mylane + d0 + d, p + d);
-                }
-                tmem_ld_wait();
-                pin<HD / 4>(o);
-                pin<HD / 4>(p);
-#pragma unroll
-                for (int e = 0; e < HD / 4; ++e) {
-                    o[e] = nt > 0 ? f0 * o[e] : inv;  // (no tile: 0, or NaN)
-                    if (nt > 1) o[e] = fmaf(f1, p[e], o[e]);
-                }
-                if (row < rows) put_row<TERMS, HD / 4>(t, at, o);
+            for (int d = 0; d < HD / 4; d += 16) {
+                if (nt > 0) tmem_ld16(tO + mylane + d0 + d, o + d);
+                if (nt > 1) tmem_ld16(tO + HD + mylane + d0 + d, p + d);
             }
-        } else
-#pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-            if (g == u && live) {
-#pragma unroll 1
-                for (int d = 0; d < HD / 2; d += 16) {
-                    float o[16];
-                    if (g < nt) {
-                        tmem_ld16(to + d, o);
-                        tmem_ld_wait();
-                        pin<16>(o);
-                    } else {
+            tmem_ld_wait();
+            pin<HD / 4>(o);
+            pin<HD / 4>(p);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = 0.f;
-                    }
+            for (int e = 0; e < HD / 4; ++e) {
+                o[e] = nt > 0 ? f0 * o[e] : direct ? inv : 0.f;  // (no tile: 0, or NaN)
+                if (nt > 1) o[e] = fmaf(f1, p[e], o[e]);
+            }
+            if (!direct) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        float4 *z = reinterpret_cast<float4 *>(Os + o_at<HD, true>(row, h * (HD / 2) + d + e));
-                        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (u) w = *z;
-                        w.x = fmaf(scale, o[e], w.x), w.y = fmaf(scale, o[e + 1], w.y);
-                        w.z = fmaf(scale, o[e + 2], w.z), w.w = fmaf(scale, o[e + 3], w.w);
-                        *z = w;
-                    }
-                }
+                for (int e = 0; e < HD / 4; e += 4)
+                    *reinterpret_cast<float4 *>(Os + o_at<HD, true>(row, d0 + e)) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            } else if (row < rows) {
+                const int rg = row0 + row;
+                put_row<TERMS, HD / 4>(t, (rg / G) * t.o_token + (int64_t)(kvh * G + rg % G) * HD + d0, o);
             }
-            if (u == 1 && st < kRows) {  // (st is the row here; the maxima were read before the last barrier)
-                mref[row] = best;
-                lsum[row] = (sums[row] + sums[kRows + row]) + (sums[2 * kRows + row] + sums[3 * kRows + row]);
-            }
+        }
+        if (!direct) {
+            if (st < kRows) mref[row] = best, lsum[row] = sum;  // (st is the row here; the maxima have been read)
             rows_sync();
         }
         if (!direct && any_bad(bad)) add_hidden_rows<HD, TERMS, true, Q8>(a, t, wk, sp, kvh, G, bad, mref, Os, st);
@@ -1088,7 +1062,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     }
     if (S == 1 && !a.part && !any_bad(bad)) return;  // (written, or NaN)
     finish<HD, TERMS, kRows, true, kThreads>(t, (int64_t)turn * a.Hkv + kvh, 0, kvh, G, row0, rows, split, S, Os, mref,
-                                   lsum, join);
+                                   lsum);
 }
 
 // Joins the S splits' partial results of every unit: grid (tiles of rows, kv heads, dims).

@@ -382,7 +382,7 @@ __device__ __noinline__ void settle(Sync<KU, VU> *y, int *status) {
 // (unit: its number in the workspace; NT: the CTA's threads)
 template <int HD, int TERMS, int NR, bool SWZ, int NT = kAttnThreads>
 __device__ __forceinline__ void finish(const TreeArgs &a, int64_t unit, int b, int kvh, int G, int row0, int rows,
-                                       int split, int S, float *Os, float *mref, float *lsum, float *join) {
+                                       int split, int S, float *Os, float *mref, float *lsum) {
     namespace cg = cooperative_groups;
     const int tid = threadIdx.x;
     if (a.part) {
@@ -408,33 +408,37 @@ __device__ __forceinline__ void finish(const TreeArgs &a, int64_t unit, int b, i
         }
         return;
     }
-    float *wgt = join, *m8 = wgt + kCluster * NR, *l8 = m8 + kCluster * NR;
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();
-    for (int i = tid; i < S * NR; i += NT) {
-        m8[i] = *cl.map_shared_rank(mref + i % NR, i / NR);
-        l8[i] = *cl.map_shared_rank(lsum + i % NR, i / NR);
-    }
-    __syncthreads();
-    for (int r = tid; r < rows; r += NT) {
-        float m = kNone, sum = 0.f;
-        for (int s = 0; s < S; ++s) m = fmaxf(m, m8[s * NR + r]);
-        for (int s = 0; s < S; ++s) sum = fmaf(ex2(m8[s * NR + r] - m), l8[s * NR + r], sum);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no row seen: zeros
-        for (int s = 0; s < S; ++s) wgt[s * NR + r] = ex2(m8[s * NR + r] - m) * inv;
-    }
-    __syncthreads();
     for (int i = split * NT + tid; i < rows * (HD / 4); i += S * NT) {
         const int r = i / (HD / 4), d = 4 * (i % (HD / 4)), rg = row0 + r;
+        // (all that a thread needs is asked for at once; gathered for the CTA first, the
+        // maxima and sums cost two more round trips)
         float4 o[kCluster];
+        float ms[kCluster], ls[kCluster];
 #pragma unroll
         for (int s = 0; s < kCluster; ++s)
-            if (s < S) o[s] = *reinterpret_cast<const float4 *>(cl.map_shared_rank(Os + o_at<HD, SWZ>(r, d), s));
+            if (s < S) {
+                o[s] = *reinterpret_cast<const float4 *>(cl.map_shared_rank(Os + o_at<HD, SWZ>(r, d), s));
+                ms[s] = *cl.map_shared_rank(mref + r, s);
+                ls[s] = *cl.map_shared_rank(lsum + r, s);
+            }
+        float m = kNone, sum = 0.f;
+#pragma unroll
+        for (int s = 0; s < kCluster; ++s)
+            if (s < S) m = fmaxf(m, ms[s]);
+#pragma unroll
+        for (int s = 0; s < kCluster; ++s)
+            if (s < S) {
+                ms[s] = ex2(ms[s] - m);
+                sum = fmaf(ms[s], ls[s], sum);
+            }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no row seen: zeros
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int s = 0; s < kCluster; ++s)
             if (s < S) {
-                const float w = wgt[s * NR + r];
+                const float w = ms[s] * inv;
                 y.x = fmaf(w, o[s].x, y.x), y.y = fmaf(w, o[s].y, y.y);
                 y.z = fmaf(w, o[s].z, y.z), y.w = fmaf(w, o[s].w, y.w);
             }
@@ -507,7 +511,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     float *lsum = corr + 2 * NR;                // [NR]
     float *wtmp = lsum + NR;                    // [2][4][NR]
     float *Os = reinterpret_cast<float *>(sm);  // [NR][HD], in the ring when the tiles are done
-    float *join = Os + NR * HD;                 // [3][kCluster][NR] behind it
 
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int split = blockIdx.x, S = gridDim.x;
@@ -813,7 +816,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tmem_free(tS, C::kCols);
     }
     finish<HD, TERMS, NR, false>(a, (int64_t)blockIdx.z * gridDim.y + blockIdx.y, b, kvh, G, row0, rows, split, S, Os, mref,
-                                   lsum, join);
+                                   lsum);
 }
 
 constexpr int kRows = 128;
@@ -864,7 +867,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // [2][128]: the groups' maxima, then the rows' maxima and sums, each written by the thread that read what was there
     float *gm = reinterpret_cast<float *>(sm + C::kOffMisc + 512), *mref = gm, *lsum = gm + kRows;
     float *Os = reinterpret_cast<float *>(sm);                      // in the ring when the tiles are done,
-    float *join = Os + kRows * HD;                                  // and behind it
 
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int split = blockIdx.x, S = gridDim.x;
@@ -1105,7 +1107,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tmem_free(tS, C::kCols);
     }
     finish<HD, TERMS, kRows, true>(a, (int64_t)blockIdx.z * gridDim.y + blockIdx.y, b, kvh, G, row0, rows, split, S, Os, mref,
-                                   lsum, join);
+                                   lsum);
 }
 
 // A CTA's share (blockIdx.z of gridDim.z) of joining the S partial results at p of `rows` rows.
