@@ -229,40 +229,54 @@ __device__ __forceinline__ void load_pages(Sync<KU, VU> *y, uint8_t *ring, const
 }
 
 // ---- 8-bit pages. A warp for K and one for V copy codes and powers as they lie in the
-// pages into rings of three stages (bulk copies: a page of a head is contiguous), and the
+// pages into rings of stages (bulk copies: a page of a head is contiguous), and the
 // converting warps, half of them for K, half for V, make bf16 tiles of them in the products'
-// own ring. (Loads into registers a tile ahead kept the warps waiting: 1.9 us a tile of
-// heads of 128; all warps on one ring of K and V in turn 1.45.)
-constexpr int kStages = 3;
-__host__ __device__ constexpr int stage_rows(int hd) { return hd == 64 ? kTile : kTile / 2; }
-__host__ __device__ constexpr int stage_bytes(int hd) { return stage_rows(hd) * (hd + hd / 32); }
-__host__ __device__ constexpr int less_bytes(int hd, bool q8) { return q8 ? 2 * kStages * stage_bytes(hd) : 0; }
-
-struct Stages {  // [K, V]
-    uint64_t full[2][kStages], free[2][kStages];
-    uint32_t there[2][kStages];  // a stage's parts (of a page each) that hold rows of the pool; the others are zeros
-    int issued[2];
+// own ring. With `split` the two halves of a tile have rings and warps of their own, so
+// that a warp waits, reads and hands over once a tile.
+// Measured, a token a sequence, heads of 64 and 128, us a tile: loads into registers a
+// tile ahead 1.06, 1.75; one ring of K and V in turn 1.05, 1.45; rings for each, whole
+// tiles 0.75 and (halves, for want of room) 1.43; split rings 0.92, 1.23; each warp's own
+// copies, bulk 1.20, 1.53, cp.async 0.92, 1.64.
+struct Form {  // of an instance
+    int rows, stages;  // of a stage; of a ring
+    bool split;
 };
-constexpr int kOwnBytes = 4 * kBadWords + 128;  // of a CTA: bad rows, and this
-static_assert(sizeof(Stages) <= 128 && 4 * kBadWords % 8 == 0, "");
+constexpr int kMostStages = 3;
+__host__ __device__ constexpr Form form_of(bool many, int hd, int pn) {
+    // (heads of 128 have room for split rings beside packed weights only)
+    return hd == 64 ? Form{128, 3, false} : !many && pn <= 32 ? Form{64, 2, true} : Form{64, 3, false};
+}
+__host__ __device__ constexpr int stage_bytes(Form f, int hd) { return f.rows * (hd + hd / 32); }
+__host__ __device__ constexpr int less_bytes(bool q8, Form f, int hd) {
+    return q8 ? 2 * (f.split ? 2 : 1) * f.stages * stage_bytes(f, hd) : 0;
+}
+
+struct Stages {  // [K, V][half]
+    uint64_t full[2][2][kMostStages], free[2][2][kMostStages];
+    uint32_t there[2][2][kMostStages];  // a stage's parts (of a page each) that hold rows of the pool; the others are zeros
+    int issued[2][2];
+};
+constexpr int kOwnBytes = 4 * kBadWords + 256;  // of a CTA: bad rows, and this
+static_assert(sizeof(Stages) <= 256 && 4 * kBadWords % 8 == 0, "");
 
 __device__ __forceinline__ void init_stages(Stages *g, int readers, int lane) {
-    if (lane < 2 * kStages) {
-        mbar_init(&g->full[0][0] + lane, 1);
-        mbar_init(&g->free[0][0] + lane, readers);
+    if (lane < 4 * kMostStages) {
+        mbar_init(&g->full[0][0][0] + lane, 1);
+        mbar_init(&g->free[0][0][0] + lane, readers);
     }
-    if (lane < 2) g->issued[lane] = 0;
+    if (lane < 4) (&g->issued[0][0])[lane] = 0;
 }
 
 // A copying warp: all of a split's K (o = 0) or V.
-template <int HD>
+template <int HD, int HR, int N, bool SPLIT>
 __device__ __forceinline__ void stage_pages(Stages *g, uint8_t *stages, int o, const PagedArgs &a, int b, int kvh,
                                             const Span &sp, int t0, int nt, int lane, const Wait &w) {
-    constexpr int HR = stage_rows(HD), PER = kTile / HR;
-    const int parts = max(HR >> a.shift, 1), rows = HR / parts, n_items = nt * PER;
+    constexpr int PER = kTile / HR, kBytes = HR * (HD + HD / 32);
+    static_assert(!SPLIT || PER == 2, "");
+    const int parts = max(HR >> a.shift, 1), rows = HR / parts, n_items = PER * nt;
     const int32_t *table = a.table + (int64_t)b * a.max_pages;
     const uint8_t *codes = static_cast<const uint8_t *>(o ? a.vc : a.kc), *scales = o ? a.vs : a.ks;
-    stages += o * kStages * stage_bytes(HD);
+    stages += o * (SPLIT ? 2 : 1) * N * kBytes;
     auto row_of = [&](int e) {
         if (lane >= parts || e >= n_items) return -1;
         const int j = sp.tile(t0 + e / PER) * kTile + e % PER * HR + lane * rows;
@@ -270,77 +284,91 @@ __device__ __forceinline__ void stage_pages(Stages *g, uint8_t *stages, int o, c
     };
     auto ask = [&](int j) { return j < 0 ? -1 : table[j >> a.shift]; };
     int next = row_of(0), page_next = ask(next);  // (the page is asked for an item before it is used)
+    int u = 0;                                    // stage, and whether its last reader is waited for
+    uint32_t phase = 0;
+    bool used = false;
     for (int e = 0; e < n_items; ++e) {
-        const int j = next, page = page_next, u = e % kStages;
+        const int j = next, page = page_next, half = SPLIT ? e & 1 : 0;
         next = row_of(e + 1);
         page_next = ask(next);
-        const bool ok = e < kStages || mbar_wait(&g->free[o][u], (e / kStages - 1) & 1, w);
+        const bool ok = !used || mbar_wait(&g->free[o][half][u], phase, w);
         if (!__all_sync(0xFFFFFFFFu, ok)) return;
         const bool there = j >= 0 && page >= 0 && page < a.n_pages;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
         const int at = a.shift < 31 ? j & (a.ps - 1) : j, n = min(rows, a.ps - at);  // row of the page, rows
+        uint64_t *full = &g->full[o][half][u];
         if (lane == 0) {
-            g->there[o][u] = mask;
-            mbar_expect_tx(&g->full[o][u], (parts > 1 ? __popc(mask) * rows : there ? n : 0) * (HD + HD / 32));
-            *(volatile int *)&g->issued[o] = e + 1;
+            g->there[o][half][u] = mask;
+            mbar_expect_tx(full, (parts > 1 ? __popc(mask) * rows : there ? n : 0) * (HD + HD / 32));
+            *(volatile int *)&g->issued[o][half] = (SPLIT ? e / 2 : e) + 1;
         }
         __syncwarp();
         if (there) {
-            uint8_t *to = stages + u * stage_bytes(HD);
+            uint8_t *to = stages + (half * N + u) * kBytes;
             const int64_t from = ((int64_t)page * a.Hkv + kvh) * a.ps + at;
-            bulk_load(to + lane * rows * HD, codes + from * HD, n * HD, &g->full[o][u]);
-            bulk_load(to + HR * HD + lane * rows * (HD / 32), scales + from * (HD / 32), n * (HD / 32), &g->full[o][u]);
+            bulk_load(to + lane * rows * HD, codes + from * HD, n * HD, full);
+            bulk_load(to + HR * HD + lane * rows * (HD / 32), scales + from * (HD / 32), n * (HD / 32), full);
+        }
+        if ((!SPLIT || half == 1) && ++u == N) {
+            u = 0;
+            if (used) phase ^= 1;
+            used = true;
         }
     }
 }
 
-// One of W converting warps: its rows of every stage of K (who < W / 2) or V as bf16
+// One of W converting warps: its rows of every tile of K (who < W / 2) or V as bf16
 // values into the ring, 128-byte swizzled as TMA writes it. A lane takes 16 elements at a
 // time of every eighth row; of heads of 128 neighbouring rows' lanes take different
 // halves, so that the eight lanes that read or write at once meet in no bank.
-template <int HD, int KU, int VU, int W>
+// (The next stage's codes read before these are widened: 0.83 for 0.75 us a tile.)
+template <int HD, int KU, int VU, int W, int HR, int NS, bool SPLIT>
 __device__ __forceinline__ void convert_pages(Sync<KU, VU> *y, uint8_t *ring, Stages *g, const uint8_t *stages,
                                               const PagedArgs &a, int nt, int who, int lane, const Wait &w) {
-    constexpr int kKv = kHalfTile * (HD / 64), HR = stage_rows(HD), PER = kTile / HR, ROWS = HR / (W / 2), H = HD / 64;
+    constexpr int kKv = kHalfTile * (HD / 64), PER = SPLIT ? 1 : kTile / HR, H = HD / 64,
+                  kBytes = HR * (HD + HD / 32);
+    constexpr int ROWS = HR / (W / 2) * (SPLIT ? 2 : 1), N = ROWS / 8 * H;  // a warp's rows of a stage, a lane's loads
+    constexpr int B = N < 4 ? N : 4, NB = N / B;  // loads of a batch, batches of a stage
     const bool is_k = who < W / 2;
-    const int op = is_k ? 0 : 1, sub = lane >> 2, dim = lane & 3, row0 = who % (W / 2) * ROWS + sub;
-    const int part_bits = a.shift < 31 ? min(a.shift, HR == kTile ? 7 : 6) : 7;
-    const int units = is_k ? KU : VU, h0 = H > 1 ? sub & 1 : 0;
-    const uint8_t *from = stages + op * kStages * stage_bytes(HD);
+    const int op = is_k ? 0 : 1, q = who % (W / 2), half = SPLIT ? q / (W / 4) : 0;
+    const int sub = lane >> 2, dim = lane & 3, row0 = (SPLIT ? q % (W / 4) : q) * ROWS + sub;
+    const int part_bits = min(a.shift, HR == 128 ? 7 : 6), units = is_k ? KU : VU, h0 = H > 1 ? sub & 1 : 0;
+    const uint8_t *from = stages + (op * (SPLIT ? 2 : 1) + half) * NS * kBytes;
     const int to0 = h0 * kHalfTile + row0 * 128 + (((2 * dim) ^ sub) << 4), to1 = to0 ^ 16;  // (row0 & 7 is sub)
-    const uint32_t all = (1u << max(HR >> part_bits, 1)) - 1u;  // (at most 16 parts)
-    int u = 0, slot = 0;
+    const uint32_t all = (1u << (HR >> part_bits)) - 1u;  // (at most 16 parts)
+    uint64_t *full = g->full[op][half], *done = is_k ? y->k_done : y->v_done, *ready = is_k ? y->k_full : y->v_full;
+    const int items = nt * PER;
+    int u = 0, slot = 0;  // the stage, the place in the ring
     uint32_t stage_phase = 0, slot_phase = 1;  // (of a slot: of the products that last read it)
-    for (int e = 0; e < nt * PER; ++e) {
-        bool ok = mbar_wait(&g->full[op][u], stage_phase, w);
-        if (e >= units * PER && e % PER == 0) ok = ok && mbar_wait(is_k ? &y->k_done[slot] : &y->v_done[slot], slot_phase, w);
+    for (int e = 0; e < items; ++e) {
+        bool ok = mbar_wait(full + u, stage_phase, w);
+        if (e >= units * PER && e % PER == 0) ok = ok && mbar_wait(done + slot, slot_phase, w);
         if (!__all_sync(0xFFFFFFFFu, ok)) return;
-        const uint8_t *codes = from + u * stage_bytes(HD) + row0 * HD + h0 * 64 + dim * 16;
-        const uint8_t *scales = from + u * stage_bytes(HD) + HR * HD + row0 * (HD / 32) + h0 * 2 + (dim >> 1);
-        uint8_t *to = ring + (is_k ? slot : KU + slot) * kKv + e % PER * HR * 128;
-        const uint32_t there = g->there[op][u];
+        const uint8_t *codes = from + u * kBytes + row0 * HD + h0 * 64 + dim * 16;
+        const uint8_t *scales = from + u * kBytes + HR * HD + row0 * (HD / 32) + h0 * 2 + (dim >> 1);
+        uint8_t *to = ring + (is_k ? slot : KU + slot) * kKv + (SPLIT ? half : e % PER) * HR * 128;
+        const uint32_t there = g->there[op][half][u];
 #pragma unroll
-        for (int r0 = 0; r0 < ROWS; r0 += 32 / H) {
-            constexpr int N = 4;  // loads at once: N / H groups of eight rows
-            uint4 x[N];
-            uint32_t f[N];
+        for (int b = 0; b < NB; ++b) {
+            uint4 x[B];
+            uint32_t f[B];
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const int r = r0 + k / H * 8, flip = k % H;  // (the other half: 64 bytes on, or back)
+            for (int k = 0; k < B; ++k) {
+                const int r = (b * B + k) / H * 8, flip = k % H;  // (the other half of the dims: 64 bytes on, or back)
                 x[k] = *reinterpret_cast<const uint4 *>(codes + r * HD + (flip ? 64 - 128 * h0 : 0));
                 f[k] = scales[r * (HD / 32) + (flip ? 2 - 4 * h0 : 0)];
             }
             if (there != all) {  // rows that are not there: zeros
 #pragma unroll
-                for (int k = 0; k < N; ++k)
-                    if (!((there >> ((row0 + r0 + k / H * 8) >> part_bits)) & 1)) x[k] = make_uint4(0, 0, 0, 0), f[k] = 127;
+                for (int k = 0; k < B; ++k)
+                    if (!((there >> ((row0 + (b * B + k) / H * 8) >> part_bits)) & 1)) x[k] = make_uint4(0, 0, 0, 0), f[k] = 127;
             }
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const uint32_t z = e4m3_factor(f[k]);
-                const uint2 v0 = e4m3_values(x[k].x, z), v1 = e4m3_values(x[k].y, z), v2 = e4m3_values(x[k].z, z),
-                            v3 = e4m3_values(x[k].w, z);
-                uint8_t *at = to + (r0 + k / H * 8) * 128 + (k % H ? kHalfTile - 2 * kHalfTile * h0 : 0);
+            for (int k = 0; k < B; ++k) {
+                const uint32_t s = e4m3_factor(f[k]);
+                const uint2 v0 = e4m3_values(x[k].x, s), v1 = e4m3_values(x[k].y, s), v2 = e4m3_values(x[k].z, s),
+                            v3 = e4m3_values(x[k].w, s);
+                uint8_t *at = to + (b * B + k) / H * 8 * 128 + (k % H ? kHalfTile - 2 * kHalfTile * h0 : 0);
                 *reinterpret_cast<uint4 *>(at + to0) = make_uint4(v0.x, v0.y, v1.x, v1.y);
                 *reinterpret_cast<uint4 *>(at + to1) = make_uint4(v2.x, v2.y, v3.x, v3.y);
             }
@@ -348,19 +376,20 @@ __device__ __forceinline__ void convert_pages(Sync<KU, VU> *y, uint8_t *ring, St
         async_fence();
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(&g->free[op][u]);
-            mbar_arrive(is_k ? &y->k_full[slot] : &y->v_full[slot]);
+            mbar_arrive(&g->free[op][half][u]);
+            mbar_arrive(ready + slot);
         }
-        if (++u == kStages) u = 0, stage_phase ^= 1;
+        if (++u == NS) u = 0, stage_phase ^= 1;
         if (e % PER == PER - 1 && ++slot == units) slot = 0, slot_phase ^= 1;
     }
 }
 
 // After a wait that ran out: the copies that were issued have landed.
-static __device__ __noinline__ void settle_stages(Stages *g) {
-    for (int o = 0; o < 2; ++o) {
-        const int n = *(volatile int *)&g->issued[o];
-        for (int e = max(0, n - kStages); e < n; ++e) mbar_await(&g->full[o][e % kStages], (e / kStages) & 1);
+static __device__ __noinline__ void settle_stages(Stages *g, int stages) {
+    for (int i = 0; i < 4; ++i) {
+        const int n = *(volatile int *)(&g->issued[0][0] + i);
+        for (int e = max(0, n - stages); e < n; ++e)
+            mbar_await(&g->full[0][0][0] + i * kMostStages + e % stages, (e / stages) & 1);
     }
 }
 
@@ -396,7 +425,8 @@ __device__ __noinline__ void add_hidden_rows(const PagedArgs &a, const TreeArgs 
 template <int HD, int TERMS, int NR, bool Q8, int PER>
 __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
     paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PagedArgs a) {
-    using C = AttnShape<HD, TERMS, NR, less_bytes(HD, Q8), PER>;
+    constexpr Form F = form_of(false, HD, weight_terms(TERMS) * NR);
+    using C = AttnShape<HD, TERMS, NR, less_bytes(Q8, F, HD), PER, true>;
     constexpr int kThreads = paged_threads(false, Q8);
     constexpr int N = C::N, PT = weight_terms(TERMS), PN = C::PN, KU = C::KU, VU = C::VU;
     constexpr bool kScaled = TERMS > 1;             // the queries carry the scale already
@@ -423,8 +453,8 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
     const float c = a.scale * 1.44269504088896340736f;  // scores in powers of two
     // (what needs nothing of the kernel before comes before its end is awaited)
     if (warp == kKWarp) {
-        if constexpr (Q8) init_stages(stage, conv_warps(false) / 2, lane);
-        init_paged(y, bad, Q8 ? conv_warps(false) / 2 * (kTile / stage_rows(HD)) : 1, soft_threads(false) / 64, lane);
+        if constexpr (Q8) init_stages(stage, conv_warps(false) / (F.split ? 4 : 2), lane);
+        init_paged(y, bad, Q8 ? conv_warps(false) / 2 * (F.split ? 1 : kTile / F.rows) : 1, soft_threads(false) / 64, lane);
     }
     pdl_wait();
     if (!a.part) pdl_trigger();
@@ -477,9 +507,9 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
 
     if (warp >= first_conv(false)) {
         if constexpr (Q8)
-            convert_pages<HD, KU, VU, conv_warps(false)>(y, sm, stage, stages, a, nt, warp - first_conv(false), lane, wt);
+            convert_pages<HD, KU, VU, conv_warps(false), F.rows, F.stages, F.split>(y, sm, stage, stages, a, nt, warp - first_conv(false), lane, wt);
     } else if (Q8 && (warp == kKWarp || warp == kVWarp)) {
-        if constexpr (Q8) stage_pages<HD>(stage, stages, warp == kVWarp, a, wk.b, kvh, sp, t0, nt, lane, wt);
+        if constexpr (Q8) stage_pages<HD, F.rows, F.stages, F.split>(stage, stages, warp == kVWarp, a, wk.b, kvh, sp, t0, nt, lane, wt);
     } else if (!Q8 && warp == kKWarp) {
         load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 1, nt, lane, wt);
     } else if (!Q8 && warp == kVWarp) {
@@ -515,7 +545,7 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
                 // block behind it comes nearer)
                 const uint32_t va = ring + (KU + i % VU) * C::kKv;
                 const uint64_t v = sw128_desc(va, kOnes ? ones - va : kHalfTile);
-                const uint64_t p = sw128_desc(p0 + (i & 1) * C::kP, kHalfTile);
+                const uint64_t p = sw128_desc(p0 + (i & 1) * C::kP, kHalfTile);  // (packed: 64 bytes into the rows)
                 if (!(ok = ok && v_full(y, i, wt) && mbar_wait(&y->p_full[i & 3], (i >> 2) & 1, wt))) break;
                 tc_fence_after();
 #pragma unroll
@@ -627,7 +657,8 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
                 mend_v<HD>(sm + (KU + i % VU) * C::kKv, row, sp.somebody(j) ? part * kTile + row : kBadRows, kBadRows, bad);
             }
             // the weights as the B operand: row = cache row, column = term * NR + r
-            uint8_t *p = Ps + g * C::kP + row * 128;
+            uint8_t *p = Ps + (C::kPacked ? 0 : g * C::kP) + row * 128;
+            constexpr int kChunks = C::kPacked ? 4 : 0;  // of the row, before group 1's
 #pragma unroll
             for (int r0 = 0; r0 < NR; r0 += 8) {
                 float w[8];
@@ -640,7 +671,7 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
                 split8<PT>(w, u);
 #pragma unroll
                 for (int k = 0; k < PT; ++k) {
-                    const int ch = (k * NR + r0) / 8;
+                    const int ch = (k * NR + r0) / 8 + g * kChunks;
                     *reinterpret_cast<uint4 *>(p + (ch / 8) * kHalfTile + (((ch % 8) ^ (row & 7)) << 4)) = u[k];
                 }
             }
@@ -714,7 +745,7 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
     __syncthreads();
     if (*err) {  // a wait ran out (nobody waits any more: the same for all threads): the rows are NaN
         if constexpr (Q8)
-            if (warp == kKWarp && elect()) settle_stages(stage);
+            if (warp == kKWarp && elect()) settle_stages(stage, F.stages);
         settle(y, a.err);
         if (tid < NR) lsum[tid] = __uint_as_float(0x7FC00000u);
         __syncthreads();
@@ -764,7 +795,8 @@ template <int HD, int TERMS, bool Q8>
 __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     paged_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ PagedArgs a) {
-    using C = RowShape<HD, TERMS, kOwnBytes, less_bytes(HD, Q8)>;
+    constexpr Form F = form_of(true, HD, 0);
+    using C = RowShape<HD, TERMS, kOwnBytes, less_bytes(Q8, F, HD)>;
     constexpr int kThreads = paged_threads(true, Q8);
     constexpr int KU = C::KU, VU = C::VU, NB = C::NB, PT = weight_terms(TERMS);
     constexpr bool kScaled = TERMS > 1;
@@ -793,8 +825,8 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     const float c = a.scale * 1.44269504088896340736f;
     // (what needs nothing of the kernel before comes before its end is awaited)
     if (warp == kKWarp) {
-        if constexpr (Q8) init_stages(stage, conv_warps(true) / 2, lane);
-        init_paged(y, bad, Q8 ? conv_warps(true) / 2 * (kTile / stage_rows(HD)) : 1, soft_threads(true) / 64, lane);
+        if constexpr (Q8) init_stages(stage, conv_warps(true) / (F.split ? 4 : 2), lane);
+        init_paged(y, bad, Q8 ? conv_warps(true) / 2 * (F.split ? 1 : kTile / F.rows) : 1, soft_threads(true) / 64, lane);
     }
     pdl_wait();
     if (!a.part) pdl_trigger();
@@ -839,9 +871,9 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
 
     if (warp >= first_conv(true)) {
         if constexpr (Q8)
-            convert_pages<HD, KU, VU, conv_warps(true)>(y, sm, stage, stages, a, nt, warp - first_conv(true), lane, wt);
+            convert_pages<HD, KU, VU, conv_warps(true), F.rows, F.stages, F.split>(y, sm, stage, stages, a, nt, warp - first_conv(true), lane, wt);
     } else if (Q8 && (warp == kKWarp || warp == kVWarp)) {
-        if constexpr (Q8) stage_pages<HD>(stage, stages, warp == kVWarp, a, wk.b, kvh, sp, t0, nt, lane, wt);
+        if constexpr (Q8) stage_pages<HD, F.rows, F.stages, F.split>(stage, stages, warp == kVWarp, a, wk.b, kvh, sp, t0, nt, lane, wt);
     } else if (!Q8 && warp == kKWarp) {
         load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 1, nt, lane, wt);
     } else if (!Q8 && warp == kVWarp) {
@@ -1051,7 +1083,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     __syncthreads();
     if (*err) {  // a wait ran out (nobody waits any more: the same for all threads): the rows are NaN
         if constexpr (Q8)
-            if (warp == kKWarp && elect()) settle_stages(stage);
+            if (warp == kKWarp && elect()) settle_stages(stage, F.stages);
         settle(y, a.err);
         if (tid < kRows) lsum[tid] = __uint_as_float(0x7FC00000u);
         __syncthreads();

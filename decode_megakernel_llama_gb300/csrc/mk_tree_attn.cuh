@@ -469,23 +469,26 @@ __device__ __forceinline__ void load_query8(const TreeArgs &a, int b, int kvh, i
     }
 }
 
-// (LESS: bytes of shared memory that the ring leaves to the caller, behind the rest; PER: CTAs an SM)
-template <int HD, int TERMS, int NR, int LESS = 0, int PER = 1>
+// (LESS: bytes of shared memory that the ring leaves to the caller, behind the rest; PER: CTAs an SM;
+// PACK: up to 32 columns of weights leave half of their rows of 128 bytes to the other group's)
+template <int HD, int TERMS, int NR, int LESS = 0, int PER = 1, bool PACK = false>
 struct AttnShape {
     static constexpr int N = TERMS * NR, PN = weight_terms(TERMS) * NR;  // columns of S and of O
     static constexpr int kKv = kHalfTile * (HD / 64);    // bytes of a K (or V) tile
-    static constexpr int kP = ((PN + 63) / 64) * kHalfTile;  // of a tile's weights; two of them
+    static constexpr bool kPacked = PACK && PN <= 32;
+    // of a tile's weights, one for each group: all of them, and from one to the other
+    static constexpr int kAllP = (kPacked ? 1 : 2) * ((PN + 63) / 64) * kHalfTile, kP = kPacked ? 64 : kAllP / 2;
     static constexpr int kQ = N * HD * 2;
     static constexpr int kUsed = 2 * (N + PN), kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     static constexpr int kOnes = HD == 64 ? 2048 : 0;  // 16 cache rows x 64: ones in the first column
     static constexpr int kMisc = 512 + 8 * MK_MAX_TREE + 4 * NR * (2 + 2 + 1 + 8);
-    static constexpr int kRoom = ((PER == 1 ? kSmemMost : kSmemHalf) - 1024 - 2 * kP - kQ - kOnes - kMisc - LESS) / kKv;
+    static constexpr int kRoom = ((PER == 1 ? kSmemMost : kSmemHalf) - 1024 - kAllP - kQ - kOnes - kMisc - LESS) / kKv;
     static constexpr int KU = (kRoom + 1) / 2 > 6 ? 6 : (kRoom + 1) / 2, VU = kRoom / 2 > 6 ? 6 : kRoom / 2;
     // With room for it S runs three tiles ahead of PV and starts as soon as the group
     // has read the scores before; else it follows PV(i), two tiles ahead.
     static constexpr bool kEarly = VU >= 4;
     static constexpr int kAhead = kEarly ? 3 : 2;
-    static constexpr int kOffP = (KU + VU) * kKv, kOffQ = kOffP + 2 * kP, kOffOnes = kOffQ + kQ, kOffMisc = kOffOnes + kOnes;
+    static constexpr int kOffP = (KU + VU) * kKv, kOffQ = kOffP + kAllP, kOffOnes = kOffQ + kQ, kOffMisc = kOffOnes + kOnes;
     static constexpr int kOffMore = kOffMisc + kMisc, kSmem = 1024 + kOffMore + LESS;
     static_assert(N % 16 == 0 && PN % 16 == 0 && PN <= 256 && kUsed <= 512 && VU >= 2,
                   "the instruction's N, tensor and shared memory");
