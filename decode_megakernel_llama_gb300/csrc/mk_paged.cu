@@ -30,7 +30,9 @@ struct PagedFew {
                          kSmem = AttnShape<HD, TERMS, NR, less_bytes(Q8_, form_of(false, HD, weight_terms(TERMS) * NR), HD), PER_,
                                            true>::kSmem;
     static constexpr bool Q8 = Q8_;
-    static constexpr double kTileUs = (HD == 64 ? 0.6 : 1.0) - (TERMS == 1 ? HD / 64 * 0.1 : 0.0), kFixedUs = 5.0, kJoinUs = 4.5;
+    static constexpr double kTileUs = Q8_ ? (HD == 64 ? 0.8 : NR_ == 16 && TERMS_ == 1 ? 1.15 : 1.55)
+                                          : (HD == 64 ? 0.6 : 1.0) - (TERMS == 1 ? HD / 64 * 0.1 : 0.0);
+    static constexpr double kFixedUs = 4.5, kJoinUs = 4.5;
     static auto fn() { return paged_attention<HD, TERMS, NR, Q8, PER_>; }
 };
 template <int HD_, int TERMS_, bool Q8_>
@@ -38,7 +40,7 @@ struct PagedMany {
     static constexpr int kThreads = paged_threads(true, Q8_), HD = HD_, TERMS = TERMS_, NR = kRows,
                          kSmem = RowShape<HD, TERMS, kOwnBytes, less_bytes(Q8_, form_of(true, HD, 0), HD)>::kSmem;
     static constexpr bool Q8 = Q8_;
-    static constexpr double kTileUs = HD == 64 && TERMS == 1 ? 0.8 : 1.2, kFixedUs = 6.5, kJoinUs = 7.0;
+    static constexpr double kTileUs = (HD == 64 && TERMS == 1 ? 0.78 : 1.1) * (Q8_ ? 1.75 : 1.0), kFixedUs = 8.0, kJoinUs = 7.0;
     static auto fn() { return paged_attention_rows<HD, TERMS, Q8>; }
 };
 
@@ -55,8 +57,9 @@ struct Bounds {
 
 // The split with the least estimated time. Units (tiles of query rows x kv heads)
 // that do not fit the GPU at once follow one another, so more than a wave of them
-// cost their mean, less the longest. The mean of a prompt's tiles is about half of
-// the longest's.
+// cost their mean, less the longest (the mean of a prompt's tiles is about half of
+// the longest's). A tile takes kTileUs, or its share of the memory's rate when the CTAs
+// at work read more than that (the tiles of a sequence's query rows share what they read).
 template <class K>
 Plan plan(const PagedArgs &a, const Bounds &h, bool ws) {
     const int G = a.Hq / a.Hkv;
@@ -70,19 +73,31 @@ Plan plan(const PagedArgs &a, const Bounds &h, bool ws) {
     }
     const int tiles = std::max(1, (int)((rows + kTile - 1) / kTile));
     const double mean_tiles = std::max(1.0, mean / kTile);
+    constexpr double kRate = 6.5e6;  // bytes a microsecond
+    constexpr double kTileBytes = 2.0 * kTile * K::HD * (K::Q8 ? 1.03 : 2.0);
+    const double sharers = (double)std::max<int64_t>(1, ((int64_t)h.max_new * G + K::NR - 1) / K::NR);
+    auto tile_us = [&](double ctas) { return std::max(K::kTileUs, ctas / sharers * kTileBytes / kRate); };
     Plan best{1, U, false, 1e30};
     for (int k = 0; k < 4 && (1 << k) <= tiles; ++k) {
         const int S = 1 << k, at_once = active_clusters<K>(k, h.n_sm);
         const int64_t waves = (units + at_once - 1) / at_once;
         const double each = waves > 1 ? mean_tiles / S + 0.5 : (tiles + S - 1) / S;
-        const double us = (double)waves * (each * K::kTileUs + K::kFixedUs) + (k ? 0.8 + 0.2 * k : 0.0);
+        const double us = (double)waves * (each * tile_us((double)S * std::min<int64_t>(units, at_once)) + K::kFixedUs) +
+                          (k ? 0.8 + 0.2 * k : 0.0);
         if (us < best.us) best = Plan{S, U, false, us};
     }
-    if (ws) {
-        const int64_t room = active_clusters<K>(0, h.n_sm) / units;
-        const int S = (int)std::min<int64_t>(std::min<int64_t>(room, max_splits(K::NR)), tiles / 2);
-        const double us = ((tiles + S - 1) / std::max(S, 1)) * K::kTileUs + K::kFixedUs + K::kJoinUs;
-        if (S > 1 && us < best.us) best = Plan{S, U, true, us};
+    if (ws && units > 0) {
+        // (any number of splits, in whole waves: 64 units leave 24 of 152 SMs idle in two
+        // splits, and none to speak of in seven: 8 sequences of 32,768 rows of 8 bits, heads of
+        // 128, 154.9 -> 145.9 us)
+        const int at_once = active_clusters<K>(0, h.n_sm), most = std::min(max_splits(K::NR), tiles / 2);
+        for (int S = 2; S <= most; ++S) {
+            const int64_t waves = (units * S + at_once - 1) / at_once;
+            const double us = (double)waves * (((tiles + S - 1) / S) * tile_us((double)std::min<int64_t>(units * S, at_once)) +
+                                               K::kFixedUs) +
+                              K::kJoinUs + 8.0 * units * S * part_floats(K::NR, K::HD) / kRate;
+            if (us < best.us) best = Plan{S, U, true, us};
+        }
     }
     return best;
 }
