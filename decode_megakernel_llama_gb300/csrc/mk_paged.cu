@@ -27,8 +27,7 @@ namespace {
 template <int HD_, int TERMS_, int NR_, bool Q8_, int PER_ = 1>
 struct PagedFew {
     static constexpr int kThreads = paged_threads(false, Q8_), HD = HD_, TERMS = TERMS_, NR = NR_,
-                         kSmem = AttnShape<HD, TERMS, NR, less_bytes(Q8_, form_of(false, HD, weight_terms(TERMS) * NR), HD), PER_,
-                                           true>::kSmem;
+                         kSmem = PagedShape<HD, TERMS, NR, Q8_, PER_>::kSmem;
     static constexpr bool Q8 = Q8_;
     static constexpr double kTileUs = Q8_ ? (HD == 64 ? 0.8 : NR_ == 16 && TERMS_ == 1 ? 1.15 : 1.55)
                                           : (HD == 64 ? 0.6 : 1.0) - (TERMS == 1 ? HD / 64 * 0.1 : 0.0);
@@ -38,7 +37,7 @@ struct PagedFew {
 template <int HD_, int TERMS_, bool Q8_>
 struct PagedMany {
     static constexpr int kThreads = paged_threads(true, Q8_), HD = HD_, TERMS = TERMS_, NR = kRows,
-                         kSmem = RowShape<HD, TERMS, kOwnBytes, less_bytes(Q8_, form_of(true, HD, 0), HD)>::kSmem;
+                         kSmem = PagedRowShape<HD, TERMS, Q8_>::kSmem;
     static constexpr bool Q8 = Q8_;
     static constexpr double kTileUs = (HD == 64 && TERMS == 1 ? 0.78 : 1.1) * (Q8_ ? 1.75 : 1.0), kFixedUs = 8.0, kJoinUs = 7.0;
     static auto fn() { return paged_attention_rows<HD, TERMS, Q8>; }

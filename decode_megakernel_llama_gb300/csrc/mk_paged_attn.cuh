@@ -422,11 +422,18 @@ __device__ __noinline__ void add_hidden_rows(const PagedArgs &a, const TreeArgs 
     }
 }
 
+// The kernels' shared memory, for them and for their launches.
+template <int HD, int TERMS, int NR, bool Q8, int PER>
+using PagedShape =
+    AttnShape<HD, TERMS, NR, less_bytes(Q8, form_of(false, HD, weight_terms(TERMS) * NR), HD), PER, true>;
+template <int HD, int TERMS, bool Q8>
+using PagedRowShape = RowShape<HD, TERMS, kOwnBytes, less_bytes(Q8, form_of(true, HD, 0), HD)>;
+
 template <int HD, int TERMS, int NR, bool Q8, int PER>
 __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
     paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PagedArgs a) {
     constexpr Form F = form_of(false, HD, weight_terms(TERMS) * NR);
-    using C = AttnShape<HD, TERMS, NR, less_bytes(Q8, F, HD), PER, true>;
+    using C = PagedShape<HD, TERMS, NR, Q8, PER>;
     constexpr int kThreads = paged_threads(false, Q8);
     constexpr int N = C::N, PT = weight_terms(TERMS), PN = C::PN, KU = C::KU, VU = C::VU;
     constexpr bool kScaled = TERMS > 1;             // the queries carry the scale already
@@ -796,7 +803,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     paged_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ PagedArgs a) {
     constexpr Form F = form_of(true, HD, 0);
-    using C = RowShape<HD, TERMS, kOwnBytes, less_bytes(Q8, F, HD)>;
+    using C = PagedRowShape<HD, TERMS, Q8>;
     constexpr int kThreads = paged_threads(true, Q8);
     constexpr int KU = C::KU, VU = C::VU, NB = C::NB, PT = weight_terms(TERMS);
     constexpr bool kScaled = TERMS > 1;
