@@ -206,8 +206,7 @@ int check_paged(const mk_paged_args *a, mkops::PagedArgs *p) {
     if (cap > (1 << 29)) return bad(MK_ERR_UNSUPPORTED, "max_pages * page_size above 2^29");
     if (!isfinite(a->scale) || !(a->scale > 0.f)) return bad(MK_ERR_INVALID_ARG, "scale must be finite and > 0");
     if (a->window < 0 || a->sinks < 0) return bad(MK_ERR_INVALID_ARG, "window or sinks is negative");
-    if (a->max_new < 0 || a->max_new > a->n_tokens || a->max_len < 0 || a->max_len > cap)
-        return bad(MK_ERR_INVALID_ARG, "max_new outside [0, n_tokens] or max_len outside [0, max_pages * page_size]");
+    if (a->max_new < 0 || a->max_len < 0) return bad(MK_ERR_INVALID_ARG, "max_new or max_len is negative");
     const int64_t row = (int64_t)a->n_heads * a->head_dim;
     if (a->n_kv_heads > 65535 || ((int64_t)a->n_pages + 1) * a->n_kv_heads > INT32_MAX ||
         (int64_t)a->n_tokens * a->n_heads > (1 << 29) || a->batch > (1 << 20))
@@ -245,13 +244,18 @@ int check_paged(const mk_paged_args *a, mkops::PagedArgs *p) {
     return MK_OK;
 }
 
+mkops::Bounds bounds_of(const mk_paged_args *a, const mkops::PagedArgs &p) {
+    return {a->max_new ? std::min(a->max_new, a->n_tokens) : a->n_tokens, a->max_len ? std::min(a->max_len, p.cap) : p.cap,
+            mkops::sm_count()};
+}
+
 }  // namespace
 
 extern "C" int mk_paged_attention(const mk_paged_args *a, void *stream) {
     mkops::PagedArgs p;
     const int rc = check_paged(a, &p);
     if (rc || a->batch == 0 || a->n_tokens == 0) return rc;
-    const mkops::Bounds h{a->max_new ? a->max_new : a->n_tokens, a->max_len ? a->max_len : p.cap, mkops::sm_count()};
+    const mkops::Bounds h = bounds_of(a, p);
     const cudaError_t e =
         mkops::dispatch(p, a->head_dim, a->dtype == MK_F32, h, static_cast<cudaStream_t>(stream), nullptr);
     return e == cudaSuccess ? MK_OK : mkops::cuda_error(e, "mk_paged_attention");
@@ -261,7 +265,7 @@ extern "C" int64_t mk_paged_attention_workspace(const mk_paged_args *a) {
     mkops::PagedArgs p;
     const int rc = check_paged(a, &p);
     if (rc || a->batch == 0 || a->n_tokens == 0) return rc;
-    const mkops::Bounds h{a->max_new ? a->max_new : a->n_tokens, a->max_len ? a->max_len : p.cap, mkops::sm_count()};
+    const mkops::Bounds h = bounds_of(a, p);
     int64_t floats = 0;
     const cudaError_t e = mkops::dispatch(p, a->head_dim, a->dtype == MK_F32, h, nullptr, &floats);
     return e == cudaSuccess ? floats * 4 : mkops::cuda_error(e, "mk_paged_attention_workspace");

@@ -627,7 +627,7 @@ int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_k
  * probabilities as two (16 bits).
  * max_new: a bound on n_b, max_len: on lengths[b], known to the host (0:
  * n_tokens, max_pages * page_size); used only to choose the launch, results are right
- * if they are exceeded.
+ * if they are exceeded, or far above.
  * workspace, status, wait_ns: as in mk_tree_args, with
  * mk_paged_attention_workspace(). */
 typedef struct mk_paged_args {
