@@ -242,9 +242,10 @@ struct Form {  // of an instance
     bool split;
 };
 constexpr int kMostStages = 3;
-__host__ __device__ constexpr Form form_of(bool many, int hd, int pn) {
+__host__ __device__ constexpr Form form_of(bool many, int hd, int terms, int nr = 0) {
     // (heads of 128 have room for split rings beside packed weights only)
-    return hd == 64 ? Form{128, 3, false} : !many && pn <= 32 ? Form{64, 2, true} : Form{64, 3, false};
+    return hd == 64 ? Form{128, many && terms > 1 ? 2 : 3, false}
+                    : !many && weight_terms(terms) * nr <= 32 ? Form{64, 2, true} : Form{64, 3, false};
 }
 __host__ __device__ constexpr int stage_bytes(Form f, int hd) { return f.rows * (hd + hd / 32); }
 __host__ __device__ constexpr int less_bytes(bool q8, Form f, int hd) {
@@ -425,14 +426,17 @@ __device__ __noinline__ void add_hidden_rows(const PagedArgs &a, const TreeArgs 
 // The kernels' shared memory, for them and for their launches.
 template <int HD, int TERMS, int NR, bool Q8, int PER>
 using PagedShape =
-    AttnShape<HD, TERMS, NR, less_bytes(Q8, form_of(false, HD, weight_terms(TERMS) * NR), HD), PER, true>;
+    AttnShape<HD, TERMS, NR, less_bytes(Q8, form_of(false, HD, TERMS, NR), HD), PER, true>;
+// (sum_bytes: the results of many rows of fp32 queries, summed tile by tile)
+__host__ __device__ constexpr int sum_bytes(int hd, int terms) { return terms > 1 ? 2 * kRows * hd * 4 : 0; }
 template <int HD, int TERMS, bool Q8>
-using PagedRowShape = RowShape<HD, TERMS, kOwnBytes, less_bytes(Q8, form_of(true, HD, 0), HD)>;
+using PagedRowShape =
+    RowShape<HD, TERMS, kOwnBytes, less_bytes(Q8, form_of(true, HD, TERMS), HD) + sum_bytes(HD, TERMS)>;
 
 template <int HD, int TERMS, int NR, bool Q8, int PER>
 __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
     paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PagedArgs a) {
-    constexpr Form F = form_of(false, HD, weight_terms(TERMS) * NR);
+    constexpr Form F = form_of(false, HD, TERMS, NR);
     using C = PagedShape<HD, TERMS, NR, Q8, PER>;
     constexpr int kThreads = paged_threads(false, Q8);
     constexpr int N = C::N, PT = weight_terms(TERMS), PN = C::PN, KU = C::KU, VU = C::VU;
@@ -802,7 +806,7 @@ template <int HD, int TERMS, bool Q8>
 __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     paged_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ PagedArgs a) {
-    constexpr Form F = form_of(true, HD, 0);
+    constexpr Form F = form_of(true, HD, TERMS);
     using C = PagedRowShape<HD, TERMS, Q8>;
     constexpr int kThreads = paged_threads(true, Q8);
     constexpr int KU = C::KU, VU = C::VU, NB = C::NB, PT = weight_terms(TERMS);
@@ -811,6 +815,13 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     // Scores that a thread keeps from the maximum to the weights; with 8-bit pages, whose
     // converting warps leave 80 registers, it reads them again.
     constexpr int kKeep = Q8 ? 32 : kHalf;
+    // A tensor core's sum cuts what it cannot hold, always downwards: over 125 tiles of three
+    // terms the results of fp32 queries were 1.3e-5 of their norm off (the sums of the
+    // weights, rounded, are not cut alike). So theirs are summed by the softmax threads, a
+    // group's two tiles at a time, in shared memory, and no product adds to more (each tile:
+    // 104 us for 80 without, 24 heads of 64 over 6,001 rows, 301 tokens and fewer).
+    constexpr bool kSums = TERMS > 1;
+    static_assert(!kSums || NB == 2, "S(i) is issued behind PV(i - 2)");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *Qs = sm + C::kOffQ;
@@ -822,6 +833,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     uint32_t *bad = reinterpret_cast<uint32_t *>(sm + C::kOffMisc + 512);  // [kBadWords]
     Stages *stage = reinterpret_cast<Stages *>(bad + kBadWords);
     uint8_t *stages = sm + C::kOffMore;
+    float *acc = reinterpret_cast<float *>(stages + less_bytes(Q8, F, HD));  // kSums: [2][128][HD], of the groups
     float *gm = reinterpret_cast<float *>(sm + C::kOffMisc + 512 + kOwnBytes), *mref = gm, *lsum = gm + kRows;
     float *Os = reinterpret_cast<float *>(sm);                      // in the ring when the tiles are done,
     float *join = Os + kRows * HD;                                  // and behind it
@@ -917,7 +929,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
                     for (int kk = 0; kk < kTile / 16; ++kk) {
                         const uint32_t p = t < 2 ? tS + (i % NB) * kTile + kk / 2 * 32 + t * 16 + kk % 2 * 8
                                                  : tT + (i % NB) * C::kThird + kk * 8;
-                        umma_bf16_ta(tO + (i & 1) * HD, p, v + ((kk * 2048) >> 4), idO, i >= 2 || (t | kk) != 0);
+                        umma_bf16_ta(tO + (i & 1) * HD, p, v + ((kk * 2048) >> 4), idO, (kSums ? (i & 2) != 0 : i >= 2) || (t | kk) != 0);
                     }
                 umma_commit(&y->v_done[i % VU]);
                 if (j < nt) {  // (into the buffer of PV(i))
@@ -972,17 +984,20 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
                 }
                 float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                 if (!kScaled) top *= c;  // (the scale is positive)
-                if (pair_any(pair, top > m + kRaise)) {
+                float scale = 1.f;
+                const bool raise = pair_any(pair, top > m + kRaise);
+                if (raise) {
                     // raise the warps' maxima to those of the rows so far; scale O and the sums
                     float *seen = gm + g * kRows + row;
                     if (h) *seen = top;
                     pair_sync(pair);
                     if (!h) *seen = fmaxf(fmaxf(*seen, top), m);
                     pair_sync(pair);
-                    const float best = *seen, scale = ex2(m - best);
+                    const float best = *seen;
+                    scale = ex2(m - best);
                     m = best;
                     l *= scale;
-                    if (i >= 2) {
+                    if (kSums ? (i & 2) != 0 : i >= 2) {
                         if (NB > 2) ok = ok && pv_done(y, i - 2, wt);  // O is this group's again (NB = 2: S(i) was issued behind it)
                         tc_fence_after();
 #pragma unroll 1
@@ -994,6 +1009,25 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] *= scale;
                             tmem_st16(to + d, o);
+                        }
+                    }
+                }
+                // (PV(i - 2) is done: S(i) was issued behind it)
+                if (kSums && i >= 4 && ((i & 2) == 0 || raise)) {
+                    const bool take = (i & 2) == 0;
+#pragma unroll
+                    for (int d = 0; d < HD / 2; d += 16) {
+                        float o[16];
+                        tmem_ld16(to + d, o);
+                        tmem_ld_wait();
+                        pin<16>(o);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            float4 *z = reinterpret_cast<float4 *>(acc + g * kRows * HD + o_at<HD, true>(row, h * (HD / 2) + d + e));
+                            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (i >= 6) w = *z;
+                            if (take) w = make_float4(w.x + o[e], w.y + o[e + 1], w.z + o[e + 2], w.w + o[e + 3]);
+                            *z = make_float4(w.x * scale, w.y * scale, w.z * scale, w.w * scale);
                         }
                     }
                 }
@@ -1065,6 +1099,14 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
             tmem_ld_wait();
             pin<HD / 4>(o);
             pin<HD / 4>(p);
+            if constexpr (kSums) {
+#pragma unroll
+                for (int e = 0; e < HD / 4; ++e) {
+                    const float *z = acc + o_at<HD, true>(row, d0 + e);
+                    if (nt > 4) o[e] += z[0];
+                    if (nt > 5) p[e] += z[kRows * HD];
+                }
+            }
 #pragma unroll
             for (int e = 0; e < HD / 4; ++e) {
                 o[e] = nt > 0 ? f0 * o[e] : direct ? inv : 0.f;  // (no tile: 0, or NaN)

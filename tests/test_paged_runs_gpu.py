@@ -235,3 +235,42 @@ def test_a_models_cache_saved_and_restored():
     _lib.paged_attention(q, k[1], v[1], torch.zeros(1, 1, dtype=I32, device=dev), starts, n, b)
     assert torch.equal(a, b)
     mk.close()
+
+
+@pytest.mark.parametrize("hd,Hkv,new,cache", [(64, 8, 100, "bf16"), (64, 8, 100, "e4m3"), (64, 8, 8, "bf16"), (128, 8, 8, "bf16"),
+                                              (128, 8, 1, "e4m3")])
+def test_sums_over_a_long_cache_are_not_cut(hd, Hkv, new, cache):
+    """fp32 queries, values all positive: a sum that cuts instead of rounding falls behind with every product. At most 48
+    products of 16 rows (heads of 128: 8 * 32 tiles, and the sums of the weights, which are not cut, 62) add to a sum that
+    may cut, 2^-23 of it each; what adds those up, rounds: 2^-24 for each of 235 pairs of tiles and some joins. Beside them
+    the scores' error twice and the weights', as in paged_reference.attention."""
+    L, G = 60000, 4
+    p = Paged([L], [new], Hkv * G, Hkv, hd, 128, "f32", "bf16", seed=9, poison=False, q_scale=0.5)
+    p.v = p.v.abs()
+    if cache == "e4m3":
+        (p.k, p.ks), (p.v, p.vs) = (ref.quantise(x.double()) for x in (p.k, p.v))
+        p.k64, p.v64 = ref.values(p.k, p.ks), ref.values(p.v, p.vs)
+    else:
+        p.k64, p.v64 = p.k.double(), p.v.double()
+    p.run(max_new=new)
+    torch.cuda.synchronize()
+    want, tol = ref.attention(p.q, p.k64, p.v64, p.table.cpu(), p.starts.cpu(), p.lengths.cpu(), hd ** -0.5, 0, 0)
+    n = torch.arange(L - new + 1, L + 1, device="cuda")[:, None, None]
+    loose = (3 * n / 16 + 80) * 2.0 ** -23  # (that bound's share of the sums, of sum p|v| = the result here)
+    cut = 48 if hd == 64 else 8 * 32
+    tight = tol - want * loose + want * ((cut + 62) * 2.0 ** -23 + 300 * 2.0 ** -24)
+    assert bool(((p.out.double() - want).abs() <= tight).all())
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("hd,new", [(64, 300), (128, 300), (64, 3), (128, 8)])
+def test_scores_that_keep_rising(type, hd, new):
+    """Keys that grow along the sequence: maxima are raised in tile after tile."""
+    p = Paged([5000], [new], 4, 1, hd, 64, type, "bf16", seed=10, poison=False)
+    order = p.table[0].long()
+    ramp = torch.linspace(0.1, 8.0, order.numel() * 64, device="cuda").view(-1, 1, 64, 1)
+    p.k[order] = (p.k[order].abs().float() * ramp).to(BF)
+    p.q.copy_(p.q.abs())
+    p.k64 = p.k.double()
+    p.run(max_new=new)
+    p.check()
