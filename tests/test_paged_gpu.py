@@ -287,6 +287,33 @@ def test_append_in_8_bits_leaves_what_is_outside():
     assert bool((c["q"] != 7.0).any())
 
 
+def test_append_in_8_bits_keeps_the_whole_angle():
+    """Heads of ones and zeros come out as cosines and sines. Of each, sincospif is within one unit in the last place,
+    2 u of it, and the correction rounds once, u: 3 u of the value, also where it is next to 0; the angle, 16,000 turns
+    at most after three roundings in 64 bits, is within 16000 * 2 pi * 3 * 2^-53 = 3.4e-11."""
+    n, hd = 500, 64
+    c = _rope_case(n, 1, 1, hd, hd, "f32", False, 5, 40)
+    c["qkv"].view(n, 3, hd)[:] = torch.cat([torch.ones(hd // 2), torch.zeros(hd // 2)]).cuda()
+    _lib.rope_append_e4m3(c["qkv"], c["q"], c["k"], c["v"], c["ks"], c["vs"], c["pos"], c["rows"], c["freq"], slots=c["slots"])
+    angle = c["pos"].double()[:, None] * c["freq"].double()
+    want = torch.cat([angle.cos(), angle.sin()], -1)
+    assert bool(((c["q"][:, 0].double() - want).abs() <= 3 * tree.U * want.abs() + 1e-10).all())
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_append_in_8_bits_norms_an_infinite_key(type):
+    """An infinite mean leaves zeros, and no number where the infinity was: in its block alone."""
+    n, hd = 5, 128
+    c = _rope_case(n, 2, 1, hd, 64, type, True, 3)
+    c["qkv"].view(n, 4, hd)[2, 2, 100] = math.inf
+    _lib.rope_append_e4m3(c["qkv"], c["q"], c["k"], c["v"], c["ks"], c["vs"], c["pos"], c["rows"], c["freq"],
+                          slots=c["slots"], q_norm=c["qn"], k_norm=c["kn"])
+    at = int(c["slots"][2]), 0, int(c["rows"][2])
+    assert c["ks"][at].tolist() == [27, 27, 27, 255]
+    assert bool((c["k"].view(torch.uint8)[at][:96] & 127 == 0).all())
+    assert bool(torch.isfinite(c["q"]).all()) and not bool((c["vs"][at] == 255).any())
+
+
 def _hard_rows(g, *shape):
     """bf16 rows with blocks at the format's edges: zeros, powers over the whole range, values that round to ties or sit
     at 448 and 57344, infinities and NaN."""
