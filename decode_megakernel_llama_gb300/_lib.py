@@ -181,7 +181,8 @@ def _load(path: str | None):
 
 def load_extension():
     """Loads the extension module of the drafted-tree operators (rope_append, tree_attention, kv_compact, kv_reorder)
-    and of those of pages (paged_attention, rope_append_e4m3, kv_write_pages, kv_read_pages), which their first call does otherwise, and gives it the library's entry points. Nothing else needs it."""
+    and of those of pages (paged_attention, rope_append_e4m3, kv_write_pages, kv_read_pages), which their first call
+    does otherwise, and gives it the library's entry points. Nothing else needs it."""
     global _quick
     with _loading:
         if _quick is None:

@@ -39,7 +39,9 @@ struct PagedMany {
     static constexpr int kThreads = paged_threads(true, Q8_), HD = HD_, TERMS = TERMS_, NR = kRows,
                          kSmem = PagedRowShape<HD, TERMS, Q8_>::kSmem;
     static constexpr bool Q8 = Q8_;
-    static constexpr double kTileUs = (HD == 128 ? 1.1 : TERMS == 1 ? 0.78 : 1.4) * (!Q8_ ? 1.0 : TERMS == 1 ? 1.75 : 1.25), kFixedUs = 8.0, kJoinUs = 7.0;
+    static constexpr double kTileUs = (HD == 128 ? 1.1 : TERMS == 1 ? 0.78 : 1.4) *
+                                      (!Q8_ ? 1.0 : TERMS == 1 ? 1.75 : 1.25);
+    static constexpr double kFixedUs = 8.0, kJoinUs = 7.0;
     static auto fn() { return paged_attention_rows<HD, TERMS, Q8>; }
 };
 
@@ -98,9 +100,9 @@ Plan plan(const PagedArgs &a, const Bounds &h, bool ws) {
         const int at_once = active_clusters<K>(0, h.n_sm), most = std::min(max_splits(K::NR), tiles / 2);
         for (int S = std::max(2, std::min(least, most)); S <= most; ++S) {
             const int64_t waves = (units * S + at_once - 1) / at_once;
-            const double us = (double)waves * (((tiles + S - 1) / S) * tile_us((double)std::min<int64_t>(units * S, at_once)) +
-                                               K::kFixedUs) +
-                              K::kJoinUs + 8.0 * units * S * part_floats(K::NR, K::HD) / kRate;
+            const double tile = tile_us((double)std::min<int64_t>(units * S, at_once));
+            const double us = (double)waves * (((tiles + S - 1) / S) * tile + K::kFixedUs) + K::kJoinUs +
+                              8.0 * units * S * part_floats(K::NR, K::HD) / kRate;
             if (us < best.us) best = Plan{S, U, true, us};
         }
     }

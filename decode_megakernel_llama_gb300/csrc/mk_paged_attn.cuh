@@ -362,7 +362,8 @@ __device__ __forceinline__ void convert_pages(Sync<KU, VU> *y, uint8_t *ring, St
             if (there != all) {  // rows that are not there: zeros
 #pragma unroll
                 for (int k = 0; k < B; ++k)
-                    if (!((there >> ((row0 + (b * B + k) / H * 8) >> part_bits)) & 1)) x[k] = make_uint4(0, 0, 0, 0), f[k] = 127;
+                    if (!((there >> ((row0 + (b * B + k) / H * 8) >> part_bits)) & 1))
+                        x[k] = make_uint4(0, 0, 0, 0), f[k] = 127;
             }
 #pragma unroll
             for (int k = 0; k < B; ++k) {
@@ -433,6 +434,11 @@ template <int HD, int TERMS, bool Q8>
 using PagedRowShape =
     RowShape<HD, TERMS, kOwnBytes, less_bytes(Q8, form_of(true, HD, TERMS), HD) + sum_bytes(HD, TERMS)>;
 
+// Few rows: up to 16 or 32 query rows of a kv head a CTA, S = K q^T and O = V^T P. What
+// bounds it: for bf16 pages memory and the longest sequences at the end (32 of 199 to
+// 4,099 rows, 8 kv heads of 64: 35.1 us = 4.0 TB/s over all, DRAM 49 % busy), for 8-bit pages
+// the widening (8 of 27,767 to 32,768 rows, heads of 128: 146.5 us = 3.5 TB/s, issue slots
+// 59 %), for one token over a short context latency (192 rows, fp32: 6.2 us).
 template <int HD, int TERMS, int NR, bool Q8, int PER>
 __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
     paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PagedArgs a) {
@@ -518,9 +524,11 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
 
     if (warp >= first_conv(false)) {
         if constexpr (Q8)
-            convert_pages<HD, KU, VU, conv_warps(false), F.rows, F.stages, F.split>(y, sm, stage, stages, a, nt, warp - first_conv(false), lane, wt);
+            convert_pages<HD, KU, VU, conv_warps(false), F.rows, F.stages, F.split>(y, sm, stage, stages, a, nt,
+                                                                                    warp - first_conv(false), lane, wt);
     } else if (Q8 && (warp == kKWarp || warp == kVWarp)) {
-        if constexpr (Q8) stage_pages<HD, F.rows, F.stages, F.split>(stage, stages, warp == kVWarp, a, wk.b, kvh, sp, t0, nt, lane, wt);
+        if constexpr (Q8)
+            stage_pages<HD, F.rows, F.stages, F.split>(stage, stages, warp == kVWarp, a, wk.b, kvh, sp, t0, nt, lane, wt);
     } else if (!Q8 && warp == kKWarp) {
         load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 1, nt, lane, wt);
     } else if (!Q8 && warp == kVWarp) {
@@ -802,6 +810,15 @@ __device__ __forceinline__ void put_row(const TreeArgs &t, int64_t at, const flo
     }
 }
 
+// Many rows: 128 query rows of a kv head a CTA, S = q K^T and O = P V with P in tensor
+// memory, in place of the scores it comes from. 16 warps for the softmax, two to 32 rows,
+// half of a tile's columns each: with eight 8-bit chunks took 156 us for 125. What bounds it is neither the
+// products (tensor pipe 31 %) nor memory: a prompt of 4,096 tokens, 32 heads of 64, takes 136 us
+// (505 TFLOP/s of the formula's operations), 111 tiles an SM of 0.75 us and the set-up and end
+// of seven CTAs an SM; 4 x 33 tokens, window 4,096, heads of 128, 31.8 us (1.07 a tile); fp32
+// chunks over 6,001 rows of 8 bits 90.5 us (1.74 a tile). With fp32 queries a tensor core's sums,
+// which cut what they cannot hold, are too short: two tiles of a group are summed there, and
+// those sums in shared memory (80 us without, off by up to 1.3e-5 of the norm, 2.1e-6 with).
 template <int HD, int TERMS, bool Q8>
 __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     paged_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -890,9 +907,11 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
 
     if (warp >= first_conv(true)) {
         if constexpr (Q8)
-            convert_pages<HD, KU, VU, conv_warps(true), F.rows, F.stages, F.split>(y, sm, stage, stages, a, nt, warp - first_conv(true), lane, wt);
+            convert_pages<HD, KU, VU, conv_warps(true), F.rows, F.stages, F.split>(y, sm, stage, stages, a, nt,
+                                                                                    warp - first_conv(true), lane, wt);
     } else if (Q8 && (warp == kKWarp || warp == kVWarp)) {
-        if constexpr (Q8) stage_pages<HD, F.rows, F.stages, F.split>(stage, stages, warp == kVWarp, a, wk.b, kvh, sp, t0, nt, lane, wt);
+        if constexpr (Q8)
+            stage_pages<HD, F.rows, F.stages, F.split>(stage, stages, warp == kVWarp, a, wk.b, kvh, sp, t0, nt, lane, wt);
     } else if (!Q8 && warp == kKWarp) {
         load_pages<HD>(y, sm, &kmap, true, a, wk.b, kvh, sp, t0, 1, nt, lane, wt);
     } else if (!Q8 && warp == kVWarp) {
@@ -929,7 +948,8 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
                     for (int kk = 0; kk < kTile / 16; ++kk) {
                         const uint32_t p = t < 2 ? tS + (i % NB) * kTile + kk / 2 * 32 + t * 16 + kk % 2 * 8
                                                  : tT + (i % NB) * C::kThird + kk * 8;
-                        umma_bf16_ta(tO + (i & 1) * HD, p, v + ((kk * 2048) >> 4), idO, (kSums ? (i & 2) != 0 : i >= 2) || (t | kk) != 0);
+                        umma_bf16_ta(tO + (i & 1) * HD, p, v + ((kk * 2048) >> 4), idO,
+                                     (kSums ? (i & 2) != 0 : i >= 2) || (t | kk) != 0);
                     }
                 umma_commit(&y->v_done[i % VU]);
                 if (j < nt) {  // (into the buffer of PV(i))

