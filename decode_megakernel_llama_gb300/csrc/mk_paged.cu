@@ -78,11 +78,6 @@ Plan plan(const PagedArgs &a, const Bounds &h, bool ws) {
     constexpr double kTileBytes = 2.0 * kTile * K::HD * (K::Q8 ? 1.03 : 2.0);
     const double sharers = (double)std::max<int64_t>(1, ((int64_t)h.max_new * G + K::NR - 1) / K::NR);
     auto tile_us = [&](double ctas) { return std::max(K::kTileUs, ctas / sharers * kTileBytes / kRate); };
-    // Sums of tensor cores cut what they cannot hold: with heads of 128 and three terms,
-    // whose weights are summed apart, no more than 32 tiles of them where there is a choice
-    // (16,000 rows in one split were 9.6e-6 of the result's norm off, 4,000 2.5e-6; heads of
-    // 64 have the weights' sums out of the same product).
-    const int least = K::NR < kRows && K::HD == 128 && K::TERMS > 1 ? (tiles + 31) / 32 : 1;
     Plan best{1, U, false, 1e30};
     for (int k = 0; k < 4 && (1 << k) <= tiles; ++k) {
         const int S = 1 << k, at_once = active_clusters<K>(k, h.n_sm);
@@ -92,13 +87,12 @@ Plan plan(const PagedArgs &a, const Bounds &h, bool ws) {
                           (k ? 0.8 + 0.2 * k : 0.0);
         if (us < best.us) best = Plan{S, U, false, us};
     }
-    if (best.S < least) best.us = 1e30;  // (in clusters only where the workspace is wanting)
     if (ws && units > 0) {
         // (any number of splits, in whole waves: 64 units leave 24 of 152 SMs idle in two
         // splits, and none to speak of in seven: 8 sequences of 32,768 rows of 8 bits, heads of
         // 128, 154.9 -> 145.9 us)
         const int at_once = active_clusters<K>(0, h.n_sm), most = std::min(max_splits(K::NR), tiles / 2);
-        for (int S = std::max(2, std::min(least, most)); S <= most; ++S) {
+        for (int S = 2; S <= most; ++S) {
             const int64_t waves = (units * S + at_once - 1) / at_once;
             const double tile = tile_us((double)std::min<int64_t>(units * S, at_once));
             const double us = (double)waves * (((tiles + S - 1) / S) * tile + K::kFixedUs) + K::kJoinUs +

@@ -448,6 +448,16 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
     constexpr int N = C::N, PT = weight_terms(TERMS), PN = C::PN, KU = C::KU, VU = C::VU;
     constexpr bool kScaled = TERMS > 1;             // the queries carry the scale already
     constexpr bool kOnes = HD == 64;                // the sums come out of the second product
+    // A tensor core's sum cuts what it cannot hold, towards zero: 60,000 rows of a CTA left
+    // results 1.5e-4 of their norm short, a million 2.6e-3 (also with heads of 64, whose weights' sums
+    // come out of the same product). So a group's product starts anew every kSumTiles of its tiles,
+    // and what there was is added up, rounded, in tensor memory of its own (F): 60,000 rows 1.7e-6,
+    // however many CTAs share them. (Its instructions: one token over 192 rows 6.46 -> 6.48 us, the
+    // decode batch 35.63 -> 35.85, 8-bit tokens 146.2 -> 146.4, fp32 ones with heads of 128 3 %, which
+    // spill; in a function of its own, or with the raising of the maxima, the batch took 1.2 to 1.5
+    // us more, with columns by eights 0.8.)
+    constexpr int kSumTiles = 8;
+    static_assert(C::kUsed + 2 * NR <= C::kCols, "S, O and F of both groups");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *Ps = sm + C::kOffP, *Qs = sm + C::kOffQ;
@@ -520,7 +530,8 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
     __syncwarp();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tS = uniform(y->tmem), tO = tS + 2 * N;  // S and O of group g: + g * N, + g * PN
+    // S, O and F of group g: + g * N, + g * PN, + g * NR
+    const uint32_t tS = uniform(y->tmem), tO = tS + 2 * N, tF = tO + 2 * PN;
 
     if (warp >= first_conv(false)) {
         if constexpr (Q8)
@@ -570,7 +581,7 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
                     umma_bf16(tO + (i & 1) * PN, v + ((kk * 2048) >> 4) - (kOnes ? (uint64_t)((kk * 2048) >> 4) << 16 : 0),
-                              p + ((kk * 2048) >> 4), idO, i >= 2 || kk != 0);
+                              p + ((kk * 2048) >> 4), idO, (i >> 1) % kSumTiles != 0 || kk != 0);
                 umma_commit(&y->v_done[i % VU]);
                 if (!C::kEarly && j < nt) {
                     ok = k_full(y, j, wt);
@@ -583,7 +594,7 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
         // group g takes every other tile; thread: cache row `row` of it, all query rows
         const int g = (warp - kFirstSoft) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t mylane = (uint32_t)(quarter * 32) << 16;
-        const uint32_t ts = tS + g * N + mylane, to = tO + g * PN + mylane;
+        const uint32_t ts = tS + g * N + mylane, to = tO + g * PN + mylane, tf = tF + g * NR + mylane;
         float *gref = mref + g * NR, *gcorr = corr + g * NR, *gtmp = wtmp + g * 4 * NR;
         const float4 *m4 = reinterpret_cast<const float4 *>(gref);
         float l[kOnes ? 1 : NR];
@@ -658,18 +669,47 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
                     for (int r = 0; r < NR; ++r) l[r] *= gcorr[r];
                 if (i >= 2) {
                     tc_fence_after();
+                    const int n1 = (i >> 1) > kSumTiles ? PN + NR : PN;  // (F behind O, once there is one)
 #pragma unroll 1
-                    for (int n0 = 0; n0 < PN; n0 += 16) {
+                    for (int n0 = 0; n0 < n1; n0 += 16) {
+                        const uint32_t at = n0 < PN ? to + n0 : tf + n0 - PN;
                         float o[16];
-                        tmem_ld16(to + n0, o);
+                        tmem_ld16(at, o);
                         tmem_ld_wait();
                         pin<16>(o);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[e] *= gcorr[n0 % NR + e];
-                        tmem_st16(to + n0, o);
+                        tmem_st16(at, o);
                     }
                     tmem_st_wait();
                 }
+            }
+            if (i >= 2 && (i >> 1) % kSumTiles == 0) {  // O starts anew with this tile
+                tc_fence_after();
+#pragma unroll 1
+                for (int r0 = 0; r0 < NR; r0 += 16) {
+                    float z[16], w[16];
+                    tmem_ld16(to + (PT - 1) * NR + r0, z);
+                    tmem_ld_wait();
+                    pin<16>(z);
+#pragma unroll 1
+                    for (int k = PT - 2; k >= 0; --k) {
+                        tmem_ld16(to + k * NR + r0, w);
+                        tmem_ld_wait();
+                        pin<16>(w);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) z[e] += w[e];
+                    }
+                    if ((i >> 1) > kSumTiles) {
+                        tmem_ld16(tf + r0, w);
+                        tmem_ld_wait();
+                        pin<16>(w);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) z[e] += w[e];
+                    }
+                    tmem_st16(tf + r0, z);
+                }
+                tmem_st_wait();
             }
             if (part >= 0) {
                 ok = ok && v_full(y, i, wt);
@@ -744,8 +784,18 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
                         float z = w[16 * (PT - 1) + e];
 #pragma unroll
                         for (int k = PT - 2; k >= 0; --k) z += w[16 * k + e];
-                        o[e] = fmaf(corr[h * NR + r0 + e], z, o[e]);
+                        w[e] = z;
                     }
+                    if ((nt - h + 1) / 2 > kSumTiles) {
+                        float f[16];
+                        tmem_ld16(tF + h * NR + mylane + r0, f);
+                        tmem_ld_wait();
+                        pin<16>(f);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] += f[e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = fmaf(corr[h * NR + r0 + e], w[e], o[e]);
                 }
                 if (quarter * 32 < HD) {
 #pragma unroll
@@ -832,7 +882,7 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     // Scores that a thread keeps from the maximum to the weights; with 8-bit pages, whose
     // converting warps leave 80 registers, it reads them again.
     constexpr int kKeep = Q8 ? 32 : kHalf;
-    // A tensor core's sum cuts what it cannot hold, always downwards: over 125 tiles of three
+    // A tensor core's sum cuts what it cannot hold, towards zero: over 125 tiles of three
     // terms the results of fp32 queries were 1.3e-5 of their norm off (the sums of the
     // weights, rounded, are not cut alike). So theirs are summed by the softmax threads, a
     // group's two tiles at a time, in shared memory, and no product adds to more (each tile:

@@ -1,0 +1,98 @@
+"""Sums of paged_attention over long caches, whatever bounds and workspace the call is given."""
+import ctypes
+
+import pytest
+import torch
+
+from decode_megakernel_llama_gb300 import _lib
+from decode_megakernel_llama_gb300.build import build
+from tests import paged_reference as ref
+from tests.test_paged_gpu import Paged
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build()
+
+
+def call(p, workspace, **kw):
+    """mk_paged_attention on p through the C ABI, with the workspace that it asks for or none."""
+    row = p.Hq * p.hd
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    rec = dict(n_tokens=p.q.shape[0], batch=p.lengths.numel(), max_pages=p.table.shape[1], n_heads=p.Hq,
+               n_kv_heads=p.k.shape[1], head_dim=p.hd, dtype=0 if p.q.dtype == torch.float32 else 1,
+               cache_dtype=1 if p.ks is None else 2, n_pages=p.k.shape[0], page_size=p.k.shape[2], window=p.window,
+               sinks=p.sinks, scale=p.hd ** -0.5, q_stride=row, out_stride=row, q=at(p.q), out=at(p.out), k_pages=at(p.k),
+               v_pages=at(p.v), k_scales=at(p.ks), v_scales=at(p.vs), table=at(p.table), starts=at(p.starts),
+               lengths=at(p.lengths), status=at(p.status), **kw)
+    lib, work = _lib.load(), None
+    need = lib.mk_paged_attention_workspace(ctypes.byref(_lib.mk_paged_args(**rec)))
+    assert need >= 0
+    if workspace and need:
+        work = torch.empty(need, dtype=torch.uint8, device="cuda")
+        rec.update(workspace=work.data_ptr(), workspace_bytes=need)
+    assert lib.mk_paged_attention(ctypes.byref(_lib.mk_paged_args(**rec)), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert int(p.status) == 0
+
+
+@pytest.mark.parametrize("sign", ["plus", "minus", "by dim"])
+@pytest.mark.parametrize("how", ["bounds", "no workspace", "a bound that is exceeded"])
+@pytest.mark.parametrize("hd,Hkv,new,cache", [(64, 2, 3, "bf16"), (64, 2, 8, "e4m3"), (64, 2, 60, "bf16"), (128, 2, 3, "e4m3"),
+                                              (128, 2, 8, "bf16"), (128, 2, 60, "bf16"), (64, 1, 300, "bf16")])
+def test_sums_do_not_hang_on_bounds_workspace_or_sign(hd, Hkv, new, cache, how, sign):
+    """fp32 queries, values of one sign in a dim, so that a sum that cuts what it cannot hold falls behind with every
+    product. At most 8 tiles of a group (or 2, of many rows) are added up by a tensor core, 8 * 8 * 3 products that cut at most
+    2^-23 each; what adds those up rounds, 2^-24 for each of 30 sums of tiles (or 118) and some joins: 200. Beside them the
+    weights' sums, which one thread adds up over 235 tiles where they are not the product's (2^-24 each, 235 and the warp's 8),
+    the scores' error twice and the weights', as in paged_reference.attention."""
+    L, G = 60000, 4
+    p = Paged([L], [new], Hkv * G, Hkv, hd, 128, "f32", "bf16", seed=9, poison=False, q_scale=0.5)
+    to = {"plus": 1.0, "minus": -1.0, "by dim": torch.where(torch.arange(hd, device="cuda") % 3 == 0, -1.0, 1.0)}[sign]
+    p.v = (p.v.abs() * to).to(BF)
+    if cache == "e4m3":
+        (p.k, p.ks), (p.v, p.vs) = (ref.quantise(x.double()) for x in (p.k, p.v))
+        p.k64, p.v64 = ref.values(p.k, p.ks), ref.values(p.v, p.vs)
+    else:
+        p.k64, p.v64 = p.k.double(), p.v.double()
+    call(p, how != "no workspace", max_new=new, max_len=1 if how == "a bound that is exceeded" else L)
+    want, tol = ref.attention(p.q, p.k64, p.v64, p.table.cpu(), p.starts.cpu(), p.lengths.cpu(), hd ** -0.5, 0, 0)
+    n = torch.arange(L - new + 1, L + 1, device="cuda")[:, None, None]
+    loose = (3 * n / 16 + 80) * 2.0 ** -23  # (that bound's share of the sums, of sum p|v| = |the result| here)
+    tight = tol - want.abs() * loose + want.abs() * (8 * 8 * 3 * 2.0 ** -23 + (200 + 243) * 2.0 ** -24)
+    err = (p.out.double() - want).abs()
+    assert bool((err <= tight).all()), f"worst {float((err / want.abs()).max()):.2e} of a result, {float((err / tight).max())} bounds"
+
+
+@pytest.mark.parametrize("hd,cache", [(64, "bf16"), (128, "bf16"), (64, "e4m3"), (128, "e4m3")])
+def test_bf16_results_of_a_million_rows_are_rounded_once(hd, cache):
+    """One CTA over 2^20 rows (the bound says one). A result is the rounding of a value within `off` of the formula's, so it
+    lies between the roundings of the ends: off is twice the scores' error (3 hd products in fp32 each) and 2^-20, the
+    weights' 2^-16, 8 * 8 * 2 products that cut at most 2^-23, and what adds those up (512 of them) and the weights (4,096 of a
+    thread, 8 over a warp), 2^-24 each. Sums that cut left results 2.6e-3 short."""
+    L, new, G = 1 << 20, 3, 4
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = (0.5 * torch.randn(new, G, hd, generator=g, device="cuda")).to(BF)
+    k, v = (torch.randn(1, 1, L, hd, generator=g, device="cuda").to(BF) for _ in range(2))
+    v = v.abs()
+    ks = vs = None
+    k64, v64 = k, v
+    if cache == "e4m3":  # (one power for all: every value fits)
+        k, v = (x.float().clamp(-7, 7).mul(64).to(ref.E4M3) for x in (k, v))
+        ks = vs = torch.full((1, 1, L, hd // 32), 127 - 6, dtype=torch.uint8, device="cuda")
+        k64, v64 = (x.float() / 64 for x in (k, v))
+    out = torch.zeros_like(q)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    _lib.paged_attention(q, k, v, torch.zeros(1, 1, **i32), torch.tensor([0, new], **i32), torch.tensor([L], **i32), out,
+                         k_scales=ks, v_scales=None if vs is None else vs.clone(), max_new=new, max_len=1)
+    for t in range(new):
+        n = L - new + t + 1
+        kk, vv, qq = k64[0, 0, :n].double(), v64[0, 0, :n].double(), q[t].double()
+        want = torch.softmax(hd ** -0.5 * qq @ kk.T, -1) @ vv
+        d = hd ** -0.5 * (qq.abs() @ kk.abs().T).amax(-1, keepdim=True) * 3 * hd * 2.0 ** -24
+        off = 2 * d + 2.0 ** -20 + 2.0 ** -16 + 128 * 2.0 ** -23 + (512 + 4096 + 8) * 2.0 ** -24
+        low, high = (want * (1 - off)).to(BF), (want * (1 + off)).to(BF)
+        assert bool(((out[t] >= low) & (out[t] <= high)).all()), float((out[t].double() - want).mean() / want.mean())
