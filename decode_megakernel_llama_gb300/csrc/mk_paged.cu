@@ -91,7 +91,11 @@ Plan plan(const PagedArgs &a, const Bounds &h, bool ws) {
         // (any number of splits, in whole waves: 64 units leave 24 of 152 SMs idle in two
         // splits, and none to speak of in seven: 8 sequences of 32,768 rows of 8 bits, heads of
         // 128, 154.9 -> 145.9 us)
-        const int at_once = active_clusters<K>(0, h.n_sm), most = std::min(max_splits(K::NR), tiles / 2);
+        // (At most eight waves of partial results, 81 MB where a CTA has 128 rows of 128 dims: the
+        // workspace has room for all of the call's tokens, not for the bound on a sequence's alone.
+        // Tokens far above that bound, 100,000 for one, had asked for 27 GB.)
+        const int at_once = active_clusters<K>(0, h.n_sm);
+        const int most = (int)std::min<int64_t>(std::min(max_splits(K::NR), tiles / 2), 8ll * at_once / ((int64_t)U * a.Hkv));
         for (int S = 2; S <= most; ++S) {
             const int64_t waves = (units * S + at_once - 1) / at_once;
             const double tile = tile_us((double)std::min<int64_t>(units * S, at_once));

@@ -96,3 +96,34 @@ def test_bf16_results_of_a_million_rows_are_rounded_once(hd, cache):
         off = 2 * d + 2.0 ** -20 + 2.0 ** -16 + 128 * 2.0 ** -23 + (512 + 4096 + 8) * 2.0 ** -24
         low, high = (want * (1 - off)).to(BF), (want * (1 + off)).to(BF)
         assert bool(((out[t] >= low) & (out[t] <= high)).all()), float((out[t].double() - want).mean() / want.mean())
+
+
+def _need(**kw):
+    a = dict(n_tokens=1, batch=1, max_pages=8192, n_heads=32, n_kv_heads=8, head_dim=128, dtype=1, cache_dtype=1,
+             n_pages=20000, page_size=16, scale=0.1, q=1 << 30, out=1 << 50, k_pages=1 << 51, v_pages=1 << 52, table=1 << 53,
+             starts=1 << 53, lengths=1 << 53)
+    a.update(kw)
+    a.update(q_stride=a["n_heads"] * a["head_dim"], out_stride=a["n_heads"] * a["head_dim"])
+    return _lib.load().mk_paged_attention_workspace(ctypes.byref(_lib.mk_paged_args(**a)))
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_the_workspace_stays_small(dtype, hd):
+    """Prompts with no bound on the rows, tokens far above the bound on a sequence's: eight waves of partial results at most,
+    8 * 152 of (128 * 128 + 256) floats; a long context of one sequence still gets one. (The addresses are not followed.)"""
+    most = 8 * 152 * (128 * 128 + 256) * 4
+    for kw in (dict(n_tokens=4096), dict(n_tokens=4096, max_len=32768), dict(n_tokens=100000, max_new=1),
+               dict(n_tokens=8192, batch=8, max_new=1), dict(n_tokens=30000, batch=4, max_new=40, max_len=100000),
+               dict(n_tokens=300), dict(n_tokens=1000, batch=1000, max_new=1)):
+        assert 0 <= _need(dtype=dtype, head_dim=hd, **kw) <= most, kw
+    for kw in (dict(n_tokens=1), dict(n_tokens=40, max_new=40)):
+        assert 0 < _need(dtype=dtype, head_dim=hd, **kw) <= most, kw
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_many_more_tokens_than_the_bound_says(type):
+    """A launch padded to 5,000 tokens, of which two sequences have one each: the right results, the others untouched."""
+    p = Paged([9000, 20000], [1, 1], 8, 2, 128, 64, type, "bf16", pad=4998, seed=12)
+    p.run(max_new=1, max_len=20000)
+    p.check()
