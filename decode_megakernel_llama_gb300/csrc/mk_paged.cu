@@ -46,7 +46,7 @@ struct PagedMany {
 };
 
 struct Plan {
-    int S, U;  // splits of a unit's tiles; tiles of query rows, over all sequences
+    int S, U;  // splits of a unit's tiles; places of tiles of query rows, over all sequences
     bool ws;
     double us;  // its estimated time
 };
@@ -64,7 +64,7 @@ struct Bounds {
 template <class K>
 Plan plan(const PagedArgs &a, const Bounds &h, bool ws) {
     const int G = a.Hq / a.Hkv;
-    const int U = (int)(((int64_t)a.n * G + (int64_t)std::min(a.B, a.n) * (K::NR - 1)) / K::NR);
+    const int U = (int)(((int64_t)a.n * G + K::NR - 1) / K::NR) + std::min(a.B, a.n) - 1;  // (places: find_work)
     const int64_t real = std::min<int64_t>(U, (int64_t)a.B * (((int64_t)h.max_new * G + K::NR - 1) / K::NR));
     const int64_t units = real * a.Hkv;
     double rows = h.max_len, mean = h.max_len - 0.5 * std::min(h.max_new, h.max_len);

@@ -42,39 +42,50 @@ struct Work {
     int b, n, len, tok0, row0, rows;
 };
 
-// The u-th tile of NR rows over all sequences, by a whole warp; rows = 0 behind the last.
-// A sequence's last rows, which see the most, come first.
-__device__ __forceinline__ Work find_work(const PagedArgs &a, int u, int NR, int G, int lane) {
-    Work w{0, 0, 0, 0, 0, 0};
-    int before = 0;  // tiles of the sequences seen so far
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int b = b0 + lane;
-        int lo = 0, n = 0, len = 0;
-        if (b < a.B) {
-            lo = min(max(a.starts[b], 0), a.n);
-            n = max(min(max(a.starts[b + 1], 0), a.n) - lo, 0);
-            len = min(max(a.lengths[b], 0), a.cap);
-        }
-        const int mine = (n * G + NR - 1) / NR;
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-            if (lane >= o) upto += x;
-        }
-        const uint32_t has = __ballot_sync(0xFFFFFFFFu, before + upto > u);
-        if (has) {
-            const int l = __ffs(has) - 1;
-            w.b = b0 + l;
-            w.n = __shfl_sync(0xFFFFFFFFu, n, l);
-            w.len = __shfl_sync(0xFFFFFFFFu, len, l);
-            w.tok0 = __shfl_sync(0xFFFFFFFFu, lo, l);
-            w.row0 = (before + __shfl_sync(0xFFFFFFFFu, upto, l) - 1 - u) * NR;
-            w.rows = min(NR, w.n * G - w.row0);
-            return w;
-        }
-        before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+// The grid's places of tiles of NR rows: sequence b's begin at starts[b] * G / NR + min(b, starts[b]), so
+// that each has room for its tiles, an empty one takes none, and they rise with b.
+__device__ __forceinline__ int place(int b, int start, int NR, int G) { return start * G / NR + min(b, start); }
+
+// (x) the first of y <= 32 sequences that place u is one of's, of more than 32, by a whole warp: a
+// 32nd of them is left each time, so two rounds of loads for 1,024, four for 2^20. (Counting the tiles
+// of all sequences before took 0.3 ms for 1,024 sequences of 20 rows, 40 ms for 16,384; now 0.2 and 2.8.)
+static __device__ __noinline__ int2 narrow(const int32_t *starts, int B, int n, int u, int NR, int G, int lane) {
+    int lo = 0, size = B;
+    while (size > 32) {
+        const int step = (size + 31) / 32, b = lo + lane * step;
+        const bool in = lane * step < size && place(b, min(max(starts[b], 0), n), NR, G) <= u;
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, in);
+        const int skip = m ? (31 - __clz(m)) * step : 0;
+        lo += skip, size = min(step, size - skip);
     }
+    return make_int2(lo, size);
+}
+
+// The tile of NR rows at place u, by a whole warp; rows = 0: an empty place. A sequence's
+// last rows, which see the most, come first.
+__device__ __forceinline__ Work find_work(const PagedArgs &a, int u, int NR, int G, int lane) {
+    Work w;
+    int2 in = make_int2(0, a.B);
+    if (a.B > 32) in = narrow(a.starts, a.B, a.n, u, NR, G, lane);
+    const int b = in.x + lane;
+    int lo = 0, n = 0, len = 0, at = 0;
+    if (lane < in.y) {
+        lo = min(max(a.starts[b], 0), a.n);
+        n = max(min(max(a.starts[b + 1], 0), a.n) - lo, 0);
+        len = min(max(a.lengths[b], 0), a.cap);
+        at = place(b, lo, NR, G);
+    }
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, lane < in.y && at <= u);
+    const int first = __shfl_sync(0xFFFFFFFFu, at, 0), l = m ? 31 - __clz(m) : 0;
+    w.b = in.x + l;
+    w.n = __shfl_sync(0xFFFFFFFFu, n, l);
+    w.len = __shfl_sync(0xFFFFFFFFu, len, l);
+    w.tok0 = __shfl_sync(0xFFFFFFFFu, lo, l);
+    w.row0 = __shfl_sync(0xFFFFFFFFu, (at + (n * G + NR - 1) / NR - 1 - u) * NR, l);  // (behind its tiles: below 0)
+    w.rows = first <= u && w.row0 >= 0 ? min(NR, w.n * G - w.row0) : 0;
+    w.row0 = max(w.row0, 0);  // (an empty place's queries are read, too)
+    // (else the compiler forms them anew in the loops: a chunk of tokens over 8-bit pages 91.1 -> 97.5 us)
+    asm volatile("" : "+r"(w.row0), "+r"(w.rows), "+r"(w.b), "+r"(w.n), "+r"(w.len), "+r"(w.tok0));
     return w;
 }
 
