@@ -96,8 +96,19 @@ inline cudaError_t launch_op(void (*kernel)(KArgs...), dim3 grid, int threads, i
 
 // Whether two ranges of bytes share one.
 inline bool meet(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    if (a_bytes <= 0 || b_bytes <= 0) return false;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y ? y - x < (uint64_t)a_bytes : x - y < (uint64_t)b_bytes;
+}
+
+// The same for n rows of `row` bytes, `step` apart (what lies between them is not theirs).
+inline bool meet_rows(const void *a, int64_t n, int64_t step, int64_t row, const void *b, int64_t b_bytes) {
+    if (n <= 0 || b_bytes <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    if (y <= x) return x - y < (uint64_t)b_bytes;
+    const uint64_t k = (y - x) / (uint64_t)step, at = (y - x) % (uint64_t)step;  // b begins `at` behind row k's start
+    if (k >= (uint64_t)n) return false;
+    return at < (uint64_t)row || (k + 1 < (uint64_t)n && (uint64_t)b_bytes > (uint64_t)step - at);
 }
 
 // SMs of the GPU (of the device that is current at the first call: a machine's are alike).

@@ -236,6 +236,22 @@ int check_paged(const mk_paged_args *a, mkops::PagedArgs *p) {
             meet(a->out, out_bytes, a->v_pages, pool) ||
             (q8 && (meet(a->out, out_bytes, a->k_scales, scales) || meet(a->out, out_bytes, a->v_scales, scales))))
             return bad(MK_ERR_INVALID_ARG, "out overlaps q, the pages or their scales");
+        // what is written apart from everything else: the rows of out, the workspace and the status word
+        const int64_t b = a->batch, work = a->workspace ? a->workspace_bytes : 0, word = a->status ? 4 : 0;
+        const struct {
+            const void *at;
+            int64_t bytes;
+        } read[] = {{a->table, b * a->max_pages * 4}, {a->starts, b ? (b + 1) * 4 : 0}, {a->lengths, b * 4},
+                    {a->q, q_bytes}, {a->k_pages, pool}, {a->v_pages, pool}, {a->k_scales, scales},
+                    {a->v_scales, scales}};
+        auto out_meets = [&](const void *at, int64_t bytes) {
+            return mkops::meet_rows(a->out, a->n_tokens, a->out_stride * e, row * e, at, bytes);
+        };
+        bool met = out_meets(a->workspace, work) || out_meets(a->status, word) || meet(a->workspace, work, a->status, word);
+        for (int i = 0; i < 8; ++i)
+            met = met || (i < 3 && out_meets(read[i].at, read[i].bytes)) ||
+                  meet(a->workspace, work, read[i].at, read[i].bytes) || meet(a->status, word, read[i].at, read[i].bytes);
+        if (met) return bad(MK_ERR_INVALID_ARG, "out, the workspace or status overlaps something else");
     }
     mkops::PagedArgs r{};
     r.n = a->n_tokens, r.B = a->batch, r.max_pages = a->max_pages, r.Hq = a->n_heads, r.Hkv = a->n_kv_heads;

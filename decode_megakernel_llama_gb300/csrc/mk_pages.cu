@@ -176,6 +176,12 @@ int move(const char *who, const mk_pages_args *a, bool write, void *stream) {
             if (meet(part[i].at, part[i].bytes, part[j].at, part[j].bytes))
                 return bad(MK_ERR_INVALID_ARG, "caches, pages and scales must not overlap");
     if (a->batch == 0) return MK_OK;
+    const int64_t each = (int64_t)a->batch * 4;
+    for (int i = write ? 2 : 0; i < (!write ? 2 : q8 ? 6 : 4); ++i)  // (what is written)
+        if (meet(part[i].at, part[i].bytes, a->table, each * a->max_pages) ||
+            meet(part[i].at, part[i].bytes, a->lengths, each) || meet(part[i].at, part[i].bytes, a->first, each) ||
+            meet(part[i].at, part[i].bytes, a->slot_of, each))
+            return bad(MK_ERR_INVALID_ARG, "what is written overlaps table, lengths, first or slot_of");
     MoveArgs m{};
     m.L = a->n_layers, m.slots = a->slots, m.Hkv = a->n_kv_heads, m.max_seq = a->max_seq, m.n_pages = a->n_pages;
     m.ps = a->page_size, m.shift = shift, m.B = a->batch, m.max_pages = a->max_pages;

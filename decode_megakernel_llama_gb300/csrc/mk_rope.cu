@@ -358,6 +358,17 @@ int rope(const char *who, const mk_rope_args *a, bool q8, uint8_t *ks, uint8_t *
         for (int k = 0; k < i; ++k) met = met || meet(written[i].at, written[i].bytes, written[k].at, written[k].bytes);
         if (met) return bad(MK_ERR_INVALID_ARG, "a cache overlaps the other, qkv or q_out");
     }
+    const int64_t each = (int64_t)a->n * 4, gains = (int64_t)a->head_dim * 2;
+    const struct {
+        const void *at;
+        int64_t bytes;
+    } read[] = {{a->positions, each}, {a->rows, each}, {a->slot_of, a->slot_of ? each : 0},
+                {a->inv_freq, (int64_t)a->rot * 4}, {a->q_norm, a->q_norm ? gains : 0}, {a->k_norm, a->k_norm ? gains : 0}};
+    for (const auto &r : read) {
+        bool met = mkops::meet_rows(a->q_out, a->n, a->q_stride * e, q * e, r.at, r.bytes);
+        for (int i = 0; i < (q8 ? 4 : 2); ++i) met = met || meet(written[i].at, written[i].bytes, r.at, r.bytes);
+        if (met) return bad(MK_ERR_INVALID_ARG, "what is written overlaps positions, rows, slot_of, inv_freq or a gain");
+    }
     if (meet(a->q_out, q_bytes, a->qkv, qkv_bytes)) {
         const int64_t step = a->qkv_stride * e;
         int64_t off = (int64_t)(reinterpret_cast<uintptr_t>(a->q_out) - reinterpret_cast<uintptr_t>(a->qkv));

@@ -452,7 +452,7 @@ int mk_twell_ffn(const void *d_w_gate, const void *d_w_up, const void *d_w_down_
  * x'_{2i+1}), of the first rot elements; the others pass through. Rotated
  * queries go to q_out (dtype, [n][n_heads][head_dim], token stride q_stride;
  * it may be qkv itself with the same stride, or lie in the gaps between its
- * rows; any other overlap, and one of the caches, is refused), rotated keys and
+ * rows; any other overlap of what is written is refused), rotated keys and
  * the values,
  * rounded to nearest bf16, to cache row rows[t] of slot slot_of[t] (0 with
  * slot_of NULL). A row outside [0, max_seq) or slot outside [0, slots) is
@@ -619,8 +619,9 @@ int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_k
  * share pages. A page number outside [0, n_pages) is not followed: its rows count as
  * zeros. lengths are cut to [0, max_pages * page_size], starts to [0, n_tokens].
  * q, out: dtype (fp32 or bf16) [n_tokens][n_heads][head_dim], tokens q_stride /
- * out_stride elements apart, 16-byte aligned, strides multiples of 8; out must
- * overlap nothing. n_heads a multiple of n_kv_heads, at most MK_MAX_GROUP times it;
+ * out_stride elements apart, 16-byte aligned, strides multiples of 8. out, the
+ * workspace and status must overlap nothing (refused; with q and the pages out's
+ * gaps between its rows count, too). n_heads a multiple of n_kv_heads, at most MK_MAX_GROUP times it;
  * head_dim 64 or 128. table: int32 [batch][max_pages]; starts: int32 [batch + 1];
  * lengths: int32 [batch]. cache_dtype MK_BF16, or MK_E4M3 with both scales, all
  * pools 16-byte aligned. max_pages * page_size at most 2^29, n_tokens * n_heads too.
@@ -663,7 +664,7 @@ int64_t mk_paged_attention_workspace(const mk_paged_args *args);
  * [slots][n_kv_heads][max_seq][head_dim / 32]. With a pool of pages slots is
  * n_pages, max_seq page_size, slot_of a token's page and rows the row in it.
  * Keys are quantised from their rotated fp32 values, values from their own.
- * Caches 16-byte aligned; caches and scales overlap nothing. */
+ * Caches 16-byte aligned; caches and scales overlap nothing (refused). */
 int mk_rope_append_e4m3(const mk_rope_args *args, uint8_t *k_scales, uint8_t *v_scales, void *stream);
 
 /* Rows between a contiguous cache (bf16 [n_layers][slots][n_kv_heads][max_seq]
@@ -675,7 +676,8 @@ int mk_rope_append_e4m3(const mk_rope_args *args, uint8_t *k_scales, uint8_t *v_
  * Rows beyond max_seq or max_pages * page_size, on pages outside
  * [0, n_pages), and of slots outside the cache are left as they are. Two sequences
  * of one call must not name the same row to be written. Caches and pools
- * 16-byte aligned, nothing that is written overlaps anything else; head_dim 64 or 128. */
+ * 16-byte aligned; k, v, the pools and their scales must not overlap one another,
+ * nor what is written an index array (refused); head_dim 64 or 128. */
 typedef struct mk_pages_args {
     int32_t n_layers, slots, n_kv_heads, max_seq, head_dim, n_pages, page_size, cache_dtype, batch, max_pages;
     void *k, *v, *k_pages, *v_pages;
