@@ -53,13 +53,13 @@ __device__ __forceinline__ uint32_t e4m3_codes(float4 x, uint32_t s) {
 }
 
 // The factor of e4m3_values, twice: a code's bits put at bf16's place are its value
-// * 2^-120, denormals too, and 2^(s - 7) is a bf16 number up to s = 134.
+// * 2^-120, denormals too, and 2^(s - 7) is a bf16 number up to s = 134; above: not a number.
 __device__ __forceinline__ uint32_t e4m3_factor2(uint32_t s2) {  // of s in both halves
     return s2 > 134 * 0x00010001u ? 0x7FFF7FFFu : s2 * 128u + 120 * 0x00800080u;
 }
 __device__ __forceinline__ uint32_t e4m3_factor(uint32_t s) { return e4m3_factor2(s * 0x00010001u); }
 
-// Four codes as bf16 (exact for s >= 10). A code c = 128 sign + m belongs at 2^15 sign +
+// Four codes as bf16 (exact for s >= 3: a code's last bit is 2^-9, bf16's 2^-133). A code c = 128 sign + m belongs at 2^15 sign +
 // 16 m: 16 c + 240 (c & 128), two multiplications (shifts and masks took twice the ALU's time).
 __device__ __forceinline__ uint2 e4m3_values(uint32_t codes, uint32_t factor) {
     uint2 y;

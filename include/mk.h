@@ -598,10 +598,11 @@ int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_k
  * An e4m3 row (MK_E4M3) is head_dim codes (sign, 4 exponent bits, 3 bits; code
  * 0x7F and 0xFF do not occur) and, in k_scales / v_scales [n_pages]
  * [n_kv_heads][page_size][head_dim / 32], a byte s for each 32 of them: the
- * value is code * 2^(s - 127), and not a number with s = 255. Rows are quantised to
+ * value is code * 2^(s - 127) for s up to 134 (rounded to bf16 below s = 3), and not
+ * a number with a larger s: rows from elsewhere must keep to that. Rows are quantised to
  * the smallest e = s - 127 in [-100, 7] with max|x| <= 448 * 2^e, codes rounded to
  * nearest even (beyond 57344 to that); a block with a value that is not finite
- * gets s = 255. Every such value is a bf16 value.
+ * gets s = 255. So s is written from 27 to 134, and 255; every such value is a bf16 value.
  * Like the operators above these calls keep nothing, work on the current
  * device, asynchronous on `stream`, and check what device arrays hold on the
  * device. The pages name no such operators. */
