@@ -120,10 +120,10 @@ __global__ void __launch_bounds__(kT, TPB == 1 && E == 8 ? kPerSm : 4) rope_appe
             // radians to turns in 64 bits; the fraction of a turn fits 32
             const double turns = (double)a.positions[tt] * a.inv_freq[e] * 0.15915494309189533577;
             float s, c;
-            const double part = 2.0 * (turns - rint(turns));
-            sincospif((float)part, &s, &c);
+            const double part = turns - rint(turns);
+            sincospif(2.0f * (float)part, &s, &c);
             if constexpr (Q8) {  // what 32 bits cut off the angle, to first order
-                const float rest = (float)(part - (double)(float)part) * 3.14159265358979f, s0 = s;
+                const float rest = (float)(part - (double)(float)part) * 6.28318530717959f, s0 = s;
                 s = fmaf(rest, c, s), c = fmaf(-rest, s0, c);
             }
             turn[i / kMaxHalf][e] = make_float2(c * a.mscale, s * a.mscale);
