@@ -462,12 +462,13 @@ __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
     // A tensor core's sum cuts what it cannot hold, towards zero: 60,000 rows of a CTA left
     // results 1.5e-4 of their norm short, a million 2.6e-3 (also with heads of 64, whose weights' sums
     // come out of the same product). So a group's product starts anew every kSumTiles of its tiles,
-    // and what there was is added up, rounded, in tensor memory of its own (F): 60,000 rows 1.7e-6,
-    // however many CTAs share them. (Its instructions: one token over 192 rows 6.46 -> 6.48 us, the
-    // decode batch 35.63 -> 35.85, 8-bit tokens 146.2 -> 146.4, fp32 ones with heads of 128 3 %, which
+    // and what there was is added up, rounded, in tensor memory of its own (F), however many CTAs
+    // share the rows. (Eight tiles instead of four cost as much and left up to 1.7 times the
+    // error of fp32 operations. Its instructions: one token over 192 rows 6.46 -> 6.48 us, the decode
+    // batch 35.63 -> 35.85, 8-bit tokens 146.2 -> 146.4, fp32 ones with heads of 128 3 to 5 %, which
     // spill; in a function of its own, or with the raising of the maxima, the batch took 1.2 to 1.5
     // us more, with columns by eights 0.8.)
-    constexpr int kSumTiles = 8;
+    constexpr int kSumTiles = 4;
     static_assert(C::kUsed + 2 * NR <= C::kCols, "S, O and F of both groups");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -984,11 +985,12 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
         auto scores = [&](int i) {
             const uint64_t k = sw128_desc(ring + (i % KU) * C::kKv, 16);
 #pragma unroll
-            for (int t = 0; t < TERMS; ++t)
+            for (int t = TERMS - 1; t >= 0; --t)  // (the small terms first: a sum cuts by its size)
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
                     const uint32_t at = (kk / 4) * kHalfTile + (kk % 4) * 32;
-                    umma_bf16(tS + (i % NB) * kTile, q + ((t * C::kKv + at) >> 4), k + (at >> 4), idS, (t | kk) != 0);
+                    umma_bf16(tS + (i % NB) * kTile, q + ((t * C::kKv + at) >> 4), k + (at >> 4), idS,
+                              t != TERMS - 1 || kk != 0);
                 }
             umma_commit(&y->k_done[i % KU]);
         };
@@ -1004,13 +1006,13 @@ __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
                 if (!(ok = ok && v_full(y, i, wt) && mbar_wait(&y->p_full[i & 3], (i >> 2) & 1, wt))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int t = 0; t < PT; ++t)
+                for (int t = PT - 1; t >= 0; --t)
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk) {
                         const uint32_t p = t < 2 ? tS + (i % NB) * kTile + kk / 2 * 32 + t * 16 + kk % 2 * 8
                                                  : tT + (i % NB) * C::kThird + kk * 8;
                         umma_bf16_ta(tO + (i & 1) * HD, p, v + ((kk * 2048) >> 4), idO,
-                                     (kSums ? (i & 2) != 0 : i >= 2) || (t | kk) != 0);
+                                     (kSums ? (i & 2) != 0 : i >= 2) || t != PT - 1 || kk != 0);
                     }
                 umma_commit(&y->v_done[i % VU]);
                 if (j < nt) {  // (into the buffer of PV(i))

@@ -629,9 +629,10 @@ int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_k
  * Sums and statistics are fp32; fp32 queries and their probabilities enter the
  * products as three bf16 terms each (24 bits), bf16 queries as they are, their
  * probabilities as two (16 bits). A tensor core's sum cuts what it cannot hold,
- * towards zero, so sums begin anew every 2,048 rows at most (fp32 results over
- * 60,000 rows were 1.7e-6 of their norm short, with any bounds and workspace); not so where more than
- * 32 query rows of a kv head are bf16: their results over n rows may be n * 2^-27 short.
+ * towards zero, so sums begin anew every 1,024 rows at most, with any bounds
+ * and workspace (fp32 results were nearer to 64 bits than those of fp32
+ * operations, or at most 1.2 times as far); not so where more than 32 query rows of
+ * a kv head are bf16: their results over n rows may be n * 2^-27 short.
  * max_new: a bound on n_b, max_len: on lengths[b], known to the host (0:
  * n_tokens, max_pages * page_size); used only to choose the launch, results are right
  * if they are exceeded, or far above.
