@@ -400,7 +400,7 @@ __device__ __forceinline__ void finish(const TreeArgs &a, int64_t unit, int b, i
     }
     if (S == 1) {  // nothing to join
         // (a thread with many of the rows' dims takes their reciprocals from shared memory: 8 x 244
-        // rows 59.1 -> 58.4 us; with one or two it forms them, without another barrier: 14 tokens 5.8 -> 5.5)
+        // rows 59.1 -> 58.4 us; with one or two it forms them, without another barrier: 14 tokens 5.8 -> 5.6)
         constexpr bool kOnce = NR * HD / 4 > 2 * NT;
         auto inverse = [&](int r) { return lsum[r] == 0.f ? 0.f : 1.f / lsum[r]; };  // no row seen: zeros
         if constexpr (kOnce) {

@@ -615,7 +615,7 @@ int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_k
  *   window = 0, or j > p - window, or j < sinks.
  * out = sum_j p_j v_j / sum_j p_j, p_j = exp(scale * q . k_j - max). What rows
  * hold that a token does not see, NaN and infinities too, does not matter (those
- * that it sees leave its result infinite or NaN); a token that sees none (p < 0) gets
+ * that it sees leave its result infinite or NaN, by where the row lies); a token that sees none (p < 0) gets
  * zeros; tokens outside every sequence are not written. Sequences must not share tokens (starts must not fall); they may
  * share pages. A page number outside [0, n_pages) is not followed: its rows count as
  * zeros. lengths are cut to [0, max_pages * page_size], starts to [0, n_tokens].

@@ -69,3 +69,28 @@ def test_the_time_does_not_grow_with_the_square_of_the_sequences():
         took.append(min(times))
     print("ms", took)
     assert took[1] < 8 * took[0]
+
+
+def test_as_many_sequences_as_a_call_may_have():
+    """2^20 of one token each, over 64 shared pages. A bf16 result is within 2^-8 of itself and of sum p|v| twice the scores'
+    error, 3 * 64 products' roundings of |q||k| / 8 < 8 (5e-4 at 64 / 8 * 3 * 64 * 2^-24 * 2 * 2.8, the largest seen here), and
+    2^-16 for the weights."""
+    B, pages, ps, hd, Hq = 1 << 20, 64, 16, 64, 2
+    g = torch.Generator(device="cuda").manual_seed(4)
+    k, v = (torch.randn(pages, 1, ps, hd, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(B, Hq, hd, generator=g, device="cuda").bfloat16()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    b = torch.arange(B, **i32)
+    lengths = 1 + (b // pages) % ps
+    out = torch.empty_like(q)
+    status = torch.zeros(1, **i32)
+    _lib.paged_attention(q, k, v, (b % pages)[:, None].contiguous(), torch.arange(B + 1, **i32), lengths, out, max_new=1,
+                         max_len=ps, status=status)
+    assert int(status) == 0
+    for page in range(pages):
+        s = 0.125 * q[page::pages].float() @ k[page, 0].float().T
+        seen = torch.arange(ps, device="cuda")[None, None] < lengths[page::pages, None, None]
+        w = torch.softmax(torch.where(seen, s, -torch.inf), -1)
+        want, most = w @ v[page, 0].float(), w @ v[page, 0].float().abs()
+        err = (out[page::pages].float() - want).abs()
+        assert bool((err <= 2.0 ** -8 * want.abs() + (5e-4 + 2.0 ** -16) * most).all())
