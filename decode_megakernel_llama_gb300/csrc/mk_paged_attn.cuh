@@ -12,8 +12,8 @@
 //   - tiles that no row of the CTA sees (behind the last token, before the window)
 //     are not visited, those that all rows see whole take no mask; the others, five at
 //     most (Span), select scores and clean V;
-//   - 8-bit pages (Q8): eight more warps read codes and powers, put the bf16 values,
-//     which are exact, where TMA puts them, and from there on all is as with bf16.
+//   - 8-bit pages (Q8): more warps (eight, with many rows four) read codes and powers, put the
+//     bf16 values, which are exact, where TMA puts them, and from there on all is as with bf16.
 //     So their products are those of the bf16 kernel and only the bytes are half.
 #pragma once
 #include "mk_tree_attn.cuh"
@@ -447,9 +447,9 @@ using PagedRowShape =
 
 // Few rows: up to 16 or 32 query rows of a kv head a CTA, S = K q^T and O = V^T P. What
 // bounds it: for bf16 pages memory and the longest sequences at the end (32 of 199 to
-// 4,099 rows, 8 kv heads of 64: 35.1 us = 4.0 TB/s over all, DRAM 49 % busy), for 8-bit pages
-// the widening (8 of 27,767 to 32,768 rows, heads of 128: 146.5 us = 3.5 TB/s, issue slots
-// 59 %), for one token over a short context latency (192 rows, fp32: 6.2 us).
+// 4,099 rows, 8 kv heads of 64: 35.6 us = 4.0 TB/s over all, DRAM 46 % busy), for 8-bit pages
+// the widening (8 of 27,767 to 32,768 rows, heads of 128: 147.8 us = 3.5 TB/s, issue slots
+// 60 %), for one token over a short context latency (192 rows, fp32: 6.2 us).
 template <int HD, int TERMS, int NR, bool Q8, int PER>
 __global__ void __launch_bounds__(paged_threads(false, Q8), PER)
     paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PagedArgs a) {
@@ -875,12 +875,12 @@ __device__ __forceinline__ void put_row(const TreeArgs &t, int64_t at, const flo
 // Many rows: 128 query rows of a kv head a CTA, S = q K^T and O = P V with P in tensor
 // memory, in place of the scores it comes from. 16 warps for the softmax, two to 32 rows,
 // half of a tile's columns each: with eight 8-bit chunks took 156 us for 125. What bounds it is neither the
-// products (tensor pipe 31 %) nor memory: a prompt of 4,096 tokens, 32 heads of 64, takes 136 us
-// (505 TFLOP/s of the formula's operations), 111 tiles an SM of 0.75 us and the set-up and end
-// of seven CTAs an SM; 4 x 33 tokens, window 4,096, heads of 128, 31.8 us (1.07 a tile); fp32
-// chunks over 6,001 rows of 8 bits 90.5 us (1.74 a tile). With fp32 queries a tensor core's sums,
+// products (tensor pipe 33 % of the active cycles) nor memory: a prompt of 4,096 tokens, 32 heads of 64, takes
+// 139 us (494 TFLOP/s of the formula's operations), 111 tiles an SM of 0.75 us and the set-up and end
+// of seven CTAs an SM; 4 x 33 tokens, window 4,096, heads of 128, 32.6 us (1.07 a tile, 80 CTAs for
+// 152 SMs); fp32 chunks over 6,001 rows of 8 bits 91.2 us (1.74 a tile). With fp32 queries a tensor core's sums,
 // which cut what they cannot hold, are too short: two tiles of a group are summed there, and
-// those sums in shared memory (80 us without, off by up to 1.3e-5 of the norm, 2.1e-6 with).
+// those sums in shared memory (80 us without, off by up to 1.3e-5 of the norm over 32,000 rows; 1.7e-6 with, over a million).
 template <int HD, int TERMS, bool Q8>
 __global__ void __launch_bounds__(paged_threads(true, Q8), 1)
     paged_attention_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
