@@ -78,8 +78,13 @@ Plan plan(const PagedArgs &a, const Bounds &h, bool ws) {
     constexpr double kTileBytes = 2.0 * kTile * K::HD * (K::Q8 ? 1.03 : 2.0);
     const double sharers = (double)std::max<int64_t>(1, ((int64_t)h.max_new * G + K::NR - 1) / K::NR);
     auto tile_us = [&](double ctas) { return std::max(K::kTileUs, ctas / sharers * kTileBytes / kRate); };
+    // Many rows of bf16 queries have no room to begin a tensor core's sum anew, and it cuts what it
+    // cannot hold, n * 2^-27 over n rows: so at most 262,144 rows a split, half of the result's own
+    // rounding, as far as a cluster's splits go (a million rows in one split were 3.4e-3 short).
+    const int least = K::NR == kRows && K::TERMS == 1 ? std::min((tiles + 2047) / 2048, kCluster) : 1;
     Plan best{1, U, false, 1e30};
     for (int k = 0; k < 4 && (1 << k) <= tiles; ++k) {
+        if ((1 << k) < least && k < 3) continue;
         const int S = 1 << k, at_once = active_clusters<K>(k, h.n_sm);
         const int64_t waves = (units + at_once - 1) / at_once;
         const double each = waves > 1 ? mean_tiles / S + 0.5 : (tiles + S - 1) / S;
@@ -96,7 +101,7 @@ Plan plan(const PagedArgs &a, const Bounds &h, bool ws) {
         // Tokens far above that bound, 100,000 for one, had asked for 27 GB.)
         const int at_once = active_clusters<K>(0, h.n_sm);
         const int most = (int)std::min<int64_t>(std::min(max_splits(K::NR), tiles / 2), 8ll * at_once / ((int64_t)U * a.Hkv));
-        for (int S = 2; S <= most; ++S) {
+        for (int S = std::max(2, least); S <= most; ++S) {
             const int64_t waves = (units * S + at_once - 1) / at_once;
             const double tile = tile_us((double)std::min<int64_t>(units * S, at_once));
             const double us = (double)waves * (((tiles + S - 1) / S) * tile + K::kFixedUs) + K::kJoinUs +

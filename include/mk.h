@@ -632,7 +632,9 @@ int mk_kv_reorder(void *k, void *v, int32_t n_layers, int32_t slots, int32_t n_k
  * towards zero, so sums begin anew every 1,024 rows at most, with any bounds
  * and workspace (fp32 results were nearer to 64 bits than those of fp32
  * operations, or at most 1.2 times as far); not so where more than 32 query rows of
- * a kv head are bf16: their results over n rows may be n * 2^-27 short.
+ * a kv head are bf16: their results over n rows may be n * 2^-27 short, or with
+ * max_len (0: all) not exceeded and up to 2,097,152 rows 2^-9, half of their
+ * own rounding.
  * max_new: a bound on n_b, max_len: on lengths[b], known to the host (0:
  * n_tokens, max_pages * page_size); used only to choose the launch, results are right
  * if they are exceeded, or far above.

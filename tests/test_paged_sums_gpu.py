@@ -155,3 +155,27 @@ def test_fp32_results_are_as_near_as_those_of_fp32_operations(lens, news, Hq, Hk
         plain[lo:lo + n] = o.view(Hkv, n, Hq // Hkv, hd).transpose(0, 1).reshape(n, Hq, hd)
     ours, theirs = (float((x.double() - want).norm() / want.norm()) for x in (p.out, plain))
     assert ours <= 1.5 * theirs, (ours, theirs, ours / theirs)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_many_bf16_rows_over_a_million_are_split(hd):
+    """1,216 tokens of 16 heads, as many tiles of 128 query rows as the GPU has SMs, over 2^20 rows: one split's sums that cut
+    left the results 3.4e-3 short. A split has 2^18 rows at most, half of them a group's, whose 2 * 2^17 / 16 products cut 2^-23
+    each: 2^-9. Beside it the scores' error twice and 2^-20, the weights' 2^-16, and 4,104 roundings of the weights' sums."""
+    L, new, G = 1 << 20, 1216, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = (0.5 * torch.randn(new, G, hd, generator=g, device="cuda")).to(BF)
+    k, v = (torch.randn(1, 1, L, hd, generator=g, device="cuda").to(BF) for _ in range(2))
+    v = (v.abs() * torch.linspace(0.5, 1, hd, device="cuda").to(BF)).to(BF)
+    out = torch.zeros_like(q)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for kw in (dict(), dict(max_new=new, max_len=L)):
+        _lib.paged_attention(q, k, v, torch.zeros(1, 1, **i32), torch.tensor([0, new], **i32), torch.tensor([L], **i32), out, **kw)
+        for t in (0, 600, new - 1):
+            n = L - new + t + 1
+            kk, vv, qq = k[0, 0, :n].double(), v[0, 0, :n].double(), q[t].double()
+            want = torch.softmax(hd ** -0.5 * qq @ kk.T, -1) @ vv
+            d = hd ** -0.5 * (qq.abs() @ kk.abs().T).amax(-1, keepdim=True) * 3 * hd * 2.0 ** -24
+            off = 2 * d + 2.0 ** -20 + 2.0 ** -16 + 2.0 ** -9 + 4104 * 2.0 ** -24
+            low, high = (want * (1 - off)).to(BF), (want * (1 + off)).to(BF)
+            assert bool(((out[t] >= low) & (out[t] <= high)).all()), float(((out[t].double() - want) / want).mean())
